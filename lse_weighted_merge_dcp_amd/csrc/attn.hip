@@ -1,0 +1,568 @@
+// attn.hip -- attention of new tokens over a rank's paged cache, with the
+// partial output and log-sum-exp that the merge takes.
+//
+// attn_rows: 128 query rows of a key head to a workgroup, 32 (or 64) to a
+// wave, tiles of keys and values in LDS shared by the four waves.
+// attn_keys: up to 32 rows (decode of grouped heads); each wave takes its own
+// tiles of keys, and the four are joined in LDS at the end.
+// attn_join: joins the key ranges of one row tile that went to different
+// workgroups.
+#include "attn_tile.hpp"
+
+namespace dcpa {
+
+namespace {
+
+// The address of a cached token's row for one key head, or 0 where the table
+// names no page.
+__device__ __forceinline__ uint64_t page_row(int page, const Batch& m, const char* base, int64_t P, int64_t S,
+                                             int64_t off, uint32_t place) {
+    if ((uint32_t)page >= (uint32_t)m.pages) return 0;
+    return (uint64_t)(base + (int64_t)page * P + (int64_t)place * S + off);
+}
+
+// Writes a wave's finished rows: to the outputs, or as a part for the join.
+template <typename E, int DK, int DV, int RB>
+__device__ __forceinline__ void write_rows(const AttnArgs& p, const Unit& u, const Rows<DK, DV, RB>& w, int hk,
+                                           int unit, int tile_rows, int row0, int wave_row, int nrows) {
+    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+        const int in_tile = wave_row + rb * 32 + r, row = row0 + in_tile;
+        const float l = half_sum(w.l[rb]);
+        float f, lse2;
+        finish(l, w.mc[rb], p.vs, f, lse2);
+        if (row >= nrows) continue;
+        if (u.splits > 1) {
+            const int64_t at = ((int64_t)hk * p.units + unit) * tile_rows + in_tile;
+            float* o = p.ws_o + at * p.Dv;
+            if (h == 0) p.ws_l[at] = lse2;
+#pragma unroll
+            for (int cb = 0; cb < DV / 32; ++cb)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int col = cb * 32 + i * 8 + h * 4;
+                    if (col < p.Dv) {
+                        f32x4 x;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x[k] = l == 0.0f ? 0.0f : w.o[rb][cb][i * 4 + k] * f;
+                        *(f32x4*)(o + col) = x;
+                    }
+                }
+        } else {
+            const int token = (int)fdiv((uint32_t)row, p.m.fG), head = hk * p.m.G + row - token * p.m.G;
+            char* o = p.out + (int64_t)(u.s.first + token) * p.o_T + (int64_t)head * p.o_H;
+            if (h == 0 && p.lse != nullptr)
+                p.lse[(int64_t)(u.s.first + token) * p.l_T + (int64_t)head * p.l_H] = lse2 * p.lmul;
+#pragma unroll
+            for (int cb = 0; cb < DV / 32; ++cb)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int col = cb * 32 + i * 8 + h * 4;
+                    if (col < p.Dv) {
+                        float x[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x[k] = l == 0.0f ? 0.0f : w.o[rb][cb][i * 4 + k] * f;
+                        store4<E>(o + col * 2, x[0], x[1], x[2], x[3]);
+                    }
+                }
+        }
+    }
+}
+
+// Rows [first, end) of the unit one by one, without matrix products: a wave to
+// a row, the columns over its lanes, one key after the other, so that a key is
+// either seen by the row or never touched.  Taken only where attend() asks for
+// it (values that are not finite in a masked tile).
+template <typename E, bool KV8, int DK, int DV>
+__device__ __noinline__ void slow_rows(const AttnArgs& p, const Unit& u, int hk, int unit, int tile_rows, int row0,
+                                       int first, int end, int k0, int k1) {
+    const int lane = threadIdx.x & 63;
+    constexpr int NQ = (DK + 63) / 64, NO = (DV + 63) / 64, ES = KV8 ? 1 : 2;
+    using C = std::conditional_t<KV8, dcp::FP8T, E>;
+    auto one = [](const char* at) {
+        float f;
+        if constexpr (KV8) dcp::Cvt<C, 1>::unpack(dcp::vload<1>(at), &f);
+        else dcp::Cvt<C, 2>::unpack(dcp::vload<2>(at), &f);
+        return f;
+    };
+    const int32_t* table = p.m.table + (int64_t)u.b * p.m.t_B;
+#pragma unroll 1
+    for (int row = first; row < end; ++row) {
+        const int token = (int)fdiv((uint32_t)row, p.m.fG), head = hk * p.m.G + row - token * p.m.G;
+        const int stop = min(k1, visible(p.m, u.s, token));
+        const char* q = p.q + (int64_t)(u.s.first + token) * p.q_T + (int64_t)head * p.q_H;
+        float x[NQ], acc[NO], mc = kNoMax, l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            x[i] = 0.0f;
+            if (lane + 64 * i < p.Dk) dcp::Cvt<E, 2>::unpack(dcp::vload<2>(q + (lane + 64 * i) * 2), &x[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < NO; ++i) acc[i] = 0.0f;
+#pragma unroll 1
+        for (int key = k0; key < stop; ++key) {
+            const uint32_t page = fdiv((uint32_t)key, p.m.fpage);
+            const int id = table[page];
+            if ((uint32_t)id >= (uint32_t)p.m.pages) continue;
+            const int64_t place = key - (int64_t)page * p.m.page_size;
+            const char* kr = p.k + (int64_t)id * p.k_P + place * p.k_S + (int64_t)hk * p.k_H;
+            const char* vr = p.v == nullptr ? kr : p.v + (int64_t)id * p.v_P + place * p.v_S + (int64_t)hk * p.v_H;
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i)
+                if (lane + 64 * i < p.Dk) s += x[i] * one(kr + (lane + 64 * i) * ES);
+#pragma unroll
+            for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d, 64);
+            s *= p.c;
+            const float next = fmaxf(mc, s), f = exp2_fast(mc - next), w = exp2_fast(s - next);
+            mc = next;
+            l = l * f + w;
+#pragma unroll
+            for (int i = 0; i < NO; ++i)
+                if (lane + 64 * i < p.Dv) acc[i] = acc[i] * f + w * one(vr + (lane + 64 * i) * ES);
+        }
+        float f, lse2;
+        finish(l, mc, p.vs, f, lse2);
+        const int64_t at = ((int64_t)hk * p.units + unit) * tile_rows + (row - row0);
+        if (lane == 0) {
+            if (u.splits > 1) p.ws_l[at] = lse2;
+            else if (p.lse != nullptr) p.lse[(int64_t)(u.s.first + token) * p.l_T + (int64_t)head * p.l_H] = lse2 * p.lmul;
+        }
+#pragma unroll
+        for (int i = 0; i < NO; ++i) {
+            const int col = lane + 64 * i;
+            if (col >= p.Dv) continue;
+            const float o = l == 0.0f ? 0.0f : acc[i] * f;
+            if (u.splits > 1) p.ws_o[at * p.Dv + col] = o;
+            else dcp::vstore<2>(p.out + (int64_t)(u.s.first + token) * p.o_T + (int64_t)head * p.o_H + col * 2,
+                                dcp::Cvt<E, 2>::pack(&o));
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// attn_rows
+// ---------------------------------------------------------------------------
+template <typename E, bool KV8, int DK, int DV, bool SHARED, int KT, int RB>
+__global__ __launch_bounds__(256, DK > 256 ? 1 : 2) void attn_rows(AttnArgs p) {
+    constexpr int R = 128 * RB, KC = DK / 8, VC = DV / 8;
+    constexpr int KROW = KC * 16, VROW = SHARED ? KROW : VC * 16;
+    constexpr int KB = KT * KROW, VB = SHARED ? 0 : KT * VROW;
+    constexpr int NK = KT * KC / 256, NV = SHARED ? 0 : KT * VC / 256;   // 16-byte chunks of a thread
+    static_assert(KT * KC % 256 == 0 && (SHARED || KT * VC % 256 == 0), "a tile is whole rounds of the workgroup");
+    __shared__ __attribute__((aligned(1024))) char tile[2][KB + VB];
+    __shared__ uint64_t krow_at[2][KT], vrow_at[2][SHARED ? 1 : KT];
+    __shared__ uint64_t there_at[4];
+
+    const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv), unit = (int)(blockIdx.x / (uint32_t)p.m.Hkv);
+    const Unit u = find_unit<KT>(p.m, R, p.target, unit);
+    if (!u.ok) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = (int)dcp::wave_id(), r = lane & 31, h = lane >> 5;
+    const int nrows = u.s.n * p.m.G, row0 = u.tile * R, wave_row = wave * 32 * RB;
+
+    // the key range of this unit: what the tile's last row sees, cut to the split
+    const int last_row = min(row0 + R, nrows) - 1;
+    const int kend = visible(p.m, u.s, (int)fdiv((uint32_t)last_row, p.m.fG));
+    const int k0 = u.split * u.chunk, k1 = (int)min((int64_t)kend, (int64_t)k0 + u.chunk);
+    if (u.split > 0 && k0 >= k1) return;      // (the join counts the ranges by itself)
+    const int tiles = k1 > k0 ? (k1 - k0 + KT - 1) / KT : 0;
+
+    Rows<DK, DV, RB> w;
+    int vis[RB];
+    int vmin = 0x7fffffff, vmax = 0;
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+        const int row = min(row0 + wave_row + rb * 32 + r, last_row);
+        const int token = (int)fdiv((uint32_t)row, p.m.fG);
+        vis[rb] = visible(p.m, u.s, token) - k0;
+        load_query<DK>(w.q[rb], p.q + (int64_t)(u.s.first + token) * p.q_T +
+                                    (int64_t)(hk * p.m.G + row - token * p.m.G) * p.q_H, p.Dk, h);
+        // rows are in the order of their tokens: the first sees least, the last most
+        vmin = min(vmin, __builtin_amdgcn_readlane(vis[rb], 0));
+        vmax = max(vmax, __builtin_amdgcn_readlane(vis[rb], 31));
+    }
+    clear_rows(w);
+    bool odd = false;
+
+    const int64_t koff = (int64_t)hk * p.k_H, voff = (int64_t)hk * p.v_H;
+    const int32_t* table = p.m.table + (int64_t)u.b * p.m.t_B;
+    // where the rows of tile t lie, by the first wave
+    auto page_of = [&](int t) {
+        const int key = k0 + t * KT + lane;
+        return lane < KT && key < k1 ? table[fdiv((uint32_t)key, p.m.fpage)] : -1;
+    };
+    auto place_rows = [&](int t, int page) {
+        const uint32_t key = (uint32_t)(k0 + t * KT + lane);
+        const uint32_t place = key - fdiv(key, p.m.fpage) * p.m.fpage.d;
+        const uint64_t ka = page_row(page, p.m, p.k, p.k_P, p.k_S, koff, place);
+        if (lane < KT) {
+            krow_at[t & 1][lane] = ka;
+            if constexpr (!SHARED) vrow_at[t & 1][lane] = page_row(page, p.m, p.v, p.v_P, p.v_S, voff, place);
+        }
+        const uint64_t bits = __ballot(lane < KT && ka != 0);
+        if (lane == 0) there_at[t & 3] = bits;
+    };
+    const uint32_t lds0 = lds_addr(&tile[0][0]);
+    u32x2 reg8[KV8 ? NK + NV : 1];
+    // tile t into buffer t & 1: straight into LDS, or into registers to be widened
+    auto fetch = [&](int t) {
+        const uint32_t buf = lds0 + (uint32_t)((t & 1) * (KB + VB));
+#pragma unroll
+        for (int i = 0; i < NK + NV; ++i) {
+            const bool val = i >= NK;
+            const int ch = (val ? i - NK : i) * 256 + tid, cols = val ? VC : KC;
+            const int row = ch / cols, c = (ch % cols) ^ swz(row);
+            const uint64_t base = val ? vrow_at[t & 1][SHARED ? 0 : row] : krow_at[t & 1][row];
+            const bool ok = base != 0 && c * 8 < (val ? p.Dv : p.Dk);
+            if constexpr (KV8) {
+                reg8[i] = u32x2{0, 0};
+                if (ok) reg8[i] = *(const u32x2*)(base + (uint64_t)(c * 8));
+            } else {
+                const char* g = ok ? (const char*)(base + (uint64_t)(c * 16)) : (const char*)kZeros;
+                dma16(g, __builtin_amdgcn_readfirstlane(buf + (uint32_t)((val ? KB : 0) +
+                                                                        ((val ? i - NK : i) * 256 + wave * 64) * 16)));
+            }
+        }
+    };
+    auto widen = [&](int t) {
+        if constexpr (KV8) {
+            const uint32_t buf = lds0 + (uint32_t)((t & 1) * (KB + VB));
+#pragma unroll
+            for (int i = 0; i < NK + NV; ++i) {
+                const bool val = i >= NK;
+                lds_write16(buf + (uint32_t)((val ? KB : 0) + ((val ? i - NK : i) * 256 + tid) * 16), widen8<E>(reg8[i]));
+            }
+        }
+    };
+
+    if (wave == 0) {
+        if (tiles > 0) place_rows(0, page_of(0));
+        if (tiles > 1) place_rows(1, page_of(1));
+    }
+    meet();
+    if (tiles > 0) {
+        fetch(0);
+        widen(0);
+    }
+#pragma unroll 1
+    for (int t = 0; t < tiles; ++t) {
+        if constexpr (!KV8) dma_wait();
+        meet();       // tile t is there, and every wave is done with the buffer of t - 1
+        int page = -1;
+        if (wave == 0 && t + 2 < tiles) page = page_of(t + 2);
+        if (t + 1 < tiles) fetch(t + 1);
+        if (vmax > t * KT) {
+            const uint32_t buf = lds0 + (uint32_t)((t & 1) * (KB + VB));
+            const uint64_t there = there_at[t & 3];
+            const uint64_t whole = KT == 64 ? ~0ull : (1ull << (KT & 63)) - 1;
+            const bool full = there == whole && vmin >= (t + 1) * KT;
+            int lim[RB];
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) lim[rb] = vis[rb] - t * KT;
+            odd |= attend<E, DK, DV, RB, KT, KROW, VROW>(w, buf, SHARED ? buf : buf + KB, there, lim, full, p.c);
+        }
+        if (wave == 0 && t + 2 < tiles) place_rows(t + 2, page);
+        if (t + 1 < tiles) widen(t + 1);
+    }
+    if (odd)
+        slow_rows<E, KV8, DK, DV>(p, u, hk, unit, R, row0, row0 + wave_row,
+                                  min(row0 + wave_row + 32 * RB, nrows), k0, k1);
+    else
+        write_rows<E>(p, u, w, hk, unit, R, row0, wave_row, nrows);
+}
+
+// ---------------------------------------------------------------------------
+// attn_keys
+// ---------------------------------------------------------------------------
+template <typename E, bool KV8, int DK, int DV>
+__global__ __launch_bounds__(256, 1) void attn_keys(AttnArgs p) {
+    constexpr int KT = 32, KC = DK / 8, VC = DV / 8, KROW = KC * 16, VROW = VC * 16;
+    constexpr int KB = KT * KROW, VB = KT * VROW, NK = KT * KC / 64, NV = KT * VC / 64;
+    constexpr int NBUF = (KB + VB) * 8 <= 147456 ? 2 : 1;
+    __shared__ __attribute__((aligned(1024))) char tile[4][NBUF][KB + VB];
+    __shared__ float part_mc[4][32], part_l[4][32];
+    __shared__ int part_odd[4];
+
+    const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv), unit = (int)(blockIdx.x / (uint32_t)p.m.Hkv);
+    const Unit u = find_unit<128>(p.m, 32, p.target, unit);
+    if (!u.ok) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = (int)dcp::wave_id(), r = lane & 31, h = lane >> 5;
+    const int nrows = u.s.n * p.m.G, row0 = u.tile * 32;
+    const int last_row = min(row0 + 32, nrows) - 1;
+    const int kend = visible(p.m, u.s, (int)fdiv((uint32_t)last_row, p.m.fG));
+    const int k0 = u.split * u.chunk, k1 = (int)min((int64_t)kend, (int64_t)k0 + u.chunk);
+    if (u.split > 0 && k0 >= k1) return;
+    const int tiles = k1 > k0 ? (k1 - k0 + KT - 1) / KT : 0;
+
+    Rows<DK, DV, 1> w;
+    const int row = min(row0 + r, last_row), token = (int)fdiv((uint32_t)row, p.m.fG);
+    const int vis = visible(p.m, u.s, token) - k0;
+    const int vmin = __builtin_amdgcn_readlane(vis, 0);
+    load_query<DK>(w.q[0], p.q + (int64_t)(u.s.first + token) * p.q_T +
+                               (int64_t)(hk * p.m.G + row - token * p.m.G) * p.q_H, p.Dk, h);
+    clear_rows(w);
+    bool odd = false;
+
+    const int64_t koff = (int64_t)hk * p.k_H, voff = (int64_t)hk * p.v_H;
+    const int32_t* table = p.m.table + (int64_t)u.b * p.m.t_B;
+    const uint32_t lds0 = lds_addr(&tile[wave][0][0]);
+    // lane j < 32 knows where key j of the tile lies
+    auto page_of = [&](int t) {
+        const int key = k0 + t * KT + r;
+        return t < tiles && key < k1 ? table[fdiv((uint32_t)key, p.m.fpage)] : -1;
+    };
+    u32x2 reg8[KV8 ? NK + NV : 1];
+    auto fetch = [&](int t, int page, uint32_t buf) -> uint32_t {
+        const uint32_t key = (uint32_t)(k0 + t * KT + r);
+        const uint32_t place = key - fdiv(key, p.m.fpage) * p.m.fpage.d;
+        const uint64_t ka = page_row(page, p.m, p.k, p.k_P, p.k_S, koff, place);
+        const uint64_t va = page_row(page, p.m, p.v, p.v_P, p.v_S, voff, place);
+#pragma unroll
+        for (int i = 0; i < NK + NV; ++i) {
+            const bool val = i >= NK;
+            const int ch = (val ? i - NK : i) * 64 + lane, cols = val ? VC : KC;
+            const int from = ch / cols, c = (ch % cols) ^ swz(from);
+            const uint64_t a = val ? va : ka;
+            const uint64_t base = (uint64_t)(uint32_t)__shfl((int)(uint32_t)a, from, 64) |
+                                  (uint64_t)(uint32_t)__shfl((int)(uint32_t)(a >> 32), from, 64) << 32;
+            const bool ok = base != 0 && c * 8 < (val ? p.Dv : p.Dk);
+            if constexpr (KV8) {
+                reg8[i] = u32x2{0, 0};
+                if (ok) reg8[i] = *(const u32x2*)(base + (uint64_t)(c * 8));
+            } else {
+                const char* g = ok ? (const char*)(base + (uint64_t)(c * 16)) : (const char*)kZeros;
+                dma16(g, __builtin_amdgcn_readfirstlane(buf + (uint32_t)((val ? KB : 0) + (val ? i - NK : i) * 1024)));
+            }
+        }
+        return (uint32_t)__ballot(h == 0 && ka != 0);
+    };
+    auto widen = [&](uint32_t buf) {
+        if constexpr (KV8) {
+#pragma unroll
+            for (int i = 0; i < NK + NV; ++i) {
+                const bool val = i >= NK;
+                lds_write16(buf + (uint32_t)((val ? KB : 0) + (val ? i - NK : i) * 1024 + lane * 16), widen8<E>(reg8[i]));
+            }
+        }
+    };
+    uint32_t there = 0;
+    int t = wave;
+    int page = page_of(t + 4);
+    if (t < tiles) {
+        there = fetch(t, page_of(t), lds0);
+        widen(lds0);
+    }
+    int b = 0;
+#pragma unroll 1
+    for (; t < tiles; t += 4) {
+        const uint32_t cur = lds0 + (uint32_t)(b * (KB + VB)), nxt = lds0 + (uint32_t)((NBUF - 1 - b) * (KB + VB));
+        uint32_t there_next = 0;
+        if constexpr (!KV8) dma_wait();
+        if (NBUF == 2 || KV8) {
+            if (t + 4 < tiles) there_next = fetch(t + 4, page, nxt);
+        }
+        const int page_next = page_of(t + 8);
+        const int lim[1] = {vis - t * KT};
+        const bool full = there == 0xffffffffu && vmin >= (t + 1) * KT;
+        odd |= attend<E, DK, DV, 1, KT, KROW, VROW>(w, cur, cur + KB, there, lim, full, p.c);
+        // this wave's LDS accesses stay in order, but loads into LDS do not wait for its reads
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (NBUF == 1 && !KV8) {
+            if (t + 4 < tiles) there_next = fetch(t + 4, page, nxt);
+        }
+        if (t + 4 < tiles) widen(nxt);
+        page = page_next;
+        there = there_next;
+        if (NBUF == 2) b ^= 1;
+    }
+
+    // the four waves' sums and outputs on one scale, through LDS
+    const float l = half_sum(w.l[0]);
+    if (h == 0) {
+        part_mc[wave][r] = w.mc[0];
+        part_l[wave][r] = l;
+    }
+    if (lane == 0) part_odd[wave] = odd;
+    meet();
+    if ((part_odd[0] | part_odd[1] | part_odd[2] | part_odd[3]) != 0) {
+        slow_rows<E, KV8, DK, DV>(p, u, hk, unit, 32, row0, row0 + wave * 8, min(row0 + wave * 8 + 8, nrows), k0, k1);
+        return;
+    }
+    float mc = kNoMax;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mc = fmaxf(mc, part_mc[k][r]);
+    float total = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) total += part_l[k][r] * exp2_fast(part_mc[k][r] - mc);
+    // (mc +infinity, a row that met a score of +infinity: its sums are NaN already)
+    const float f = w.mc[0] == mc ? 1.0f : exp2_fast(w.mc[0] - mc);
+    float* all = (float*)&tile[0][0][0];
+    static_assert(sizeof(tile) >= 4 * 32 * 32 * 4, "room for the parts of 32 columns");
+#pragma unroll
+    for (int cb = 0; cb < DV / 32; ++cb) {
+        meet();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) all[(wave * 16 + i) * 64 + lane] = w.o[0][cb][i] * f;
+        meet();
+        if (wave == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                w.o[0][cb][i] = (all[i * 64 + lane] + all[(16 + i) * 64 + lane]) +
+                                (all[(32 + i) * 64 + lane] + all[(48 + i) * 64 + lane]);
+        }
+    }
+    if (wave != 0) return;
+    w.mc[0] = mc;
+    w.l[0] = h == 0 ? total : 0.0f;
+    write_rows<E>(p, u, w, hk, unit, 32, row0, 0, nrows);
+}
+
+// ---------------------------------------------------------------------------
+// attn_join: one wave to a row; each lane a few columns
+// ---------------------------------------------------------------------------
+template <typename E, int STEP>
+__global__ __launch_bounds__(256) void attn_join(AttnArgs p, int rows) {
+    const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv), id = (int)(blockIdx.x / (uint32_t)p.m.Hkv);
+    const int lane = threadIdx.x & 63, wave = (int)dcp::wave_id();
+    const int chunk = key_chunk<STEP>(p.m, rows, p.target);
+    int base = 0, sbase = 0;
+    for (int b0 = 0; b0 < p.m.B; b0 += 64) {
+        const int b = b0 + lane;
+        int tiles = 0, splits = 0;
+        if (b < p.m.B) {
+            const Seq s = load_seq(p.m, b);
+            tiles = (s.n * p.m.G + rows - 1) / rows;
+            splits = max(1, (s.kv + chunk - 1) / chunk);
+        }
+        const int incl = base + scan_incl(tiles, lane), sincl = sbase + scan_incl(tiles * splits, lane);
+        const uint64_t past = __ballot(incl > id);
+        if (past == 0) {
+            base = __builtin_amdgcn_readlane(incl, 63);
+            sbase = __builtin_amdgcn_readlane(sincl, 63);
+            continue;
+        }
+        const int at = __builtin_ctzll(past);
+        const int nt = __builtin_amdgcn_readlane(tiles, at), ns = __builtin_amdgcn_readlane(splits, at);
+        if (ns == 1) return;                  // written whole
+        const int tile = id - (__builtin_amdgcn_readlane(incl, at) - nt);
+        const int slot = __builtin_amdgcn_readlane(sincl, at) - nt * ns + tile * ns;
+        const Seq s = load_seq(p.m, b0 + at);
+        const int nrows = s.n * p.m.G, row0 = tile * rows;
+        if (tile < 0 || slot < 0 || row0 >= nrows) return;
+        const int last = min(row0 + rows, nrows) - 1;
+        const int kend = visible(p.m, s, (int)fdiv((uint32_t)last, p.m.fG));
+        const int parts = min(max(1, (kend + chunk - 1) / chunk), p.units - slot);
+        for (int row = row0 + wave; row <= last; row += 4) {
+            const int64_t first = ((int64_t)hk * p.units + slot) * rows + (row - row0);
+            float top = -INFINITY;
+            bool bad = false;
+            for (int k = lane; k < parts; k += 64) {
+                const float x = p.ws_l[first + (int64_t)k * rows];
+                bad |= x != x;
+                top = fmaxf(top, x);
+            }
+#pragma unroll
+            for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+            bad = __ballot(bad) != 0;
+            const float ref = top == -INFINITY ? 0.0f : top;
+            const int token = (int)fdiv((uint32_t)row, p.m.fG), head = hk * p.m.G + row - token * p.m.G;
+            char* o = p.out + (int64_t)(s.first + token) * p.o_T + (int64_t)head * p.o_H;
+            for (int c0 = 0; c0 < p.Dv; c0 += 256) {
+                const int col = c0 + lane * 4;
+                float acc[4] = {0, 0, 0, 0}, sum = 0.0f;
+                for (int k = 0; k < parts; ++k) {
+                    const float x = p.ws_l[first + (int64_t)k * rows];
+                    const float f = exp2_fast(x - ref);
+                    sum += f;
+                    if (col < p.Dv && f != 0.0f) {
+                        const f32x4 y = *(const f32x4*)(p.ws_o + (first + (int64_t)k * rows) * p.Dv + col);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[i] += f * y[i];
+                    }
+                }
+                if (bad) sum = NAN;
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                if (col < p.Dv) store4<E>(o + col * 2, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+                if (c0 == 0 && lane == 0 && p.lse != nullptr)
+                    p.lse[(int64_t)(s.first + token) * p.l_T + (int64_t)head * p.l_H] =
+                        (sum == 0.0f ? -INFINITY : ref + __builtin_amdgcn_logf(sum)) * p.lmul;
+            }
+        }
+        return;
+    }
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+AttnPlan plan_attn(const Batch& m, int Dk, int Dv, bool shared) {
+    AttnPlan pl;
+    const int64_t rows = (int64_t)m.T * m.G;
+    // few rows a sequence: 32-row tiles whose waves share out the keys
+    pl.by_keys = !shared && rows <= (int64_t)32 * m.B;
+    pl.rows = pl.by_keys ? 32 : 128;
+    pl.tiles = (int32_t)(rows / pl.rows + m.B);
+    const int64_t busy = (int64_t)pl.tiles * m.Hkv;
+    const int64_t want = pl.by_keys ? 1024 : 512;
+    pl.target = busy >= 4 * want ? 0 : (int32_t)((want + m.Hkv - 1) / m.Hkv);
+    pl.units = pl.tiles + pl.target;
+    pl.ws_bytes = pl.target == 0 ? 0 : (int64_t)pl.units * m.Hkv * pl.rows * (Dv + 1) * 4;
+    (void)Dk;
+    return pl;
+}
+
+namespace {
+
+struct JoinCall {
+    AttnArgs a;
+    int rows;
+};
+
+template <typename E, int STEP>
+hipError_t run_join(const AttnArgs& a, const AttnPlan& pl, hipStream_t stream) {
+    AttnArgs arg = a;
+    int rows = pl.rows;
+    void* args[] = {&arg, &rows};
+    return hipLaunchKernel(reinterpret_cast<const void*>(&attn_join<E, STEP>), dim3((uint32_t)(pl.tiles * a.m.Hkv)),
+                           dim3(256), args, 0, stream);
+}
+
+template <typename E, bool KV8>
+hipError_t run(const AttnArgs& a, const AttnPlan& pl, hipStream_t stream) {
+    const dim3 grid((uint32_t)((int64_t)pl.units * a.m.Hkv)), block(256);
+    hipError_t e;
+    const int d = a.Dk > a.Dv ? a.Dk : a.Dv;
+    if (pl.by_keys) {
+        e = d <= 64    ? launch(attn_keys<E, KV8, 64, 64>, grid, block, stream, a)
+            : d <= 128 ? launch(attn_keys<E, KV8, 128, 128>, grid, block, stream, a)
+                       : launch(attn_keys<E, KV8, 256, 256>, grid, block, stream, a);
+        if (e != hipSuccess || pl.target == 0) return e;
+        return run_join<E, 128>(a, pl, stream);
+    }
+    if (a.v == nullptr) {
+        e = launch(attn_rows<E, KV8, 576, 512, true, 32, 1>, grid, block, stream, a);
+        if (e != hipSuccess || pl.target == 0) return e;
+        return run_join<E, 32>(a, pl, stream);
+    }
+    if (d <= 64) e = launch(attn_rows<E, KV8, 64, 64, false, 64, 1>, grid, block, stream, a);
+    else if (d <= 128) e = launch(attn_rows<E, KV8, 128, 128, false, 64, 1>, grid, block, stream, a);
+    else {
+        e = launch(attn_rows<E, KV8, 256, 256, false, 32, 1>, grid, block, stream, a);
+        if (e != hipSuccess || pl.target == 0) return e;
+        return run_join<E, 32>(a, pl, stream);
+    }
+    if (e != hipSuccess || pl.target == 0) return e;
+    return run_join<E, 64>(a, pl, stream);
+}
+
+}  // namespace
+
+hipError_t launch_attn(const AttnArgs& a, const AttnPlan& pl, bool bf16, bool kv8, hipStream_t stream) {
+    if (bf16) return kv8 ? run<BF16T, true>(a, pl, stream) : run<BF16T, false>(a, pl, stream);
+    return kv8 ? run<F16T, true>(a, pl, stream) : run<F16T, false>(a, pl, stream);
+}
+
+}  // namespace dcpa

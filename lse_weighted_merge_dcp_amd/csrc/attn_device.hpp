@@ -1,0 +1,255 @@
+// attn_device.hpp -- device helpers of the cached-attention kernels: matrix
+// instructions, the LDS layout of a key tile, loads that go straight into
+// LDS, and the mapping of workgroups to sequences.
+#pragma once
+#include <type_traits>
+
+#include "attn_launch.hpp"
+#include "dcp_device.hpp"
+
+namespace dcpa {
+
+using dcp::BF16T;
+using dcp::F16T;
+using dcp::fdiv;
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+#define DCPA_LDS __attribute__((address_space(3)))
+
+// --------------------------------------------------------------------------
+// v_mfma 32x32x16: D[m][n] += sum_k A[m][k] B[k][n].  Lane l holds A[l%32][8h
+// .. 8h+7] and B[8h .. 8h+7][l%32] with h = l / 32, and D[8(i/4) + i%4 +
+// 4h][l%32] in register i of 16.
+// --------------------------------------------------------------------------
+template <typename E> struct Mat;
+template <> struct Mat<BF16T> {
+    static __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
+                                                       c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ uint32_t pack2(float a, float b) {
+        bf16x2 v;
+        v.x = (__bf16)a;
+        v.y = (__bf16)b;
+        return __builtin_bit_cast(uint32_t, v);
+    }
+    static constexpr uint32_t kExp = 0x7f807f80u;   // exponent bits of the two halves
+    // The weights' exponent is free: with the row maximum at 2^0 the smallest
+    // bf16 is far below fp32's resolution of the sum.
+    static constexpr float kTop = 0.0f;
+};
+template <> struct Mat<F16T> {
+    static __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b),
+                                                      c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ uint32_t pack2(float a, float b) {
+        f16x2 v;
+        v.x = (_Float16)a;
+        v.y = (_Float16)b;
+        return __builtin_bit_cast(uint32_t, v);
+    }
+    static constexpr uint32_t kExp = 0x7c007c00u;
+    // fp16 loses relative precision below 2^-14: the row maximum stands at
+    // 2^8, so that weights down to 2^-22 of the largest keep 11 bits.
+    static constexpr float kTop = 8.0f;
+};
+
+// A new row maximum rescales sums and outputs only when it is more than this
+// many powers of two above the old reference: weights reach 2^(kTop + 6) at
+// most (2^14 < 65504 in fp16), and almost no tile rescales.
+constexpr float kLazy = 6.0f;
+constexpr float kNoMax = -3.0e38f;
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The other half-wave's value beside one's own: lanes l and l ^ 32 get the
+// same result.
+__device__ __forceinline__ float half_max(float x) {
+    auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+    auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// --------------------------------------------------------------------------
+// A tile in LDS is [keys][chunks of 16 bytes]; chunk c of key r lies at place
+// c ^ swz(r) (the low three bits of c change).  Reads of one chunk column over
+// eight consecutive keys (the key fragments) then touch eight different
+// 16-byte places of 128 bytes, and transposing reads of 32 bytes of four
+// consecutive keys (the value fragments) four different 32-byte ones.
+// --------------------------------------------------------------------------
+__device__ __forceinline__ int swz(int r) { return ((r & 3) << 1) | ((r >> 2) & 1); }
+
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+    return (uint32_t)(uintptr_t)(const DCPA_LDS char*)p;
+}
+__device__ __forceinline__ u32x4 lds_read16(uint32_t a) { return *(const DCPA_LDS u32x4*)(uintptr_t)a; }
+__device__ __forceinline__ void lds_write16(uint32_t a, u32x4 x) { *(DCPA_LDS u32x4*)(uintptr_t)a = x; }
+// Four 8-byte pieces of 16 lanes are four rows of 16 elements; lane i of the 16
+// gets column i of the four rows.
+__device__ __forceinline__ u32x2 lds_read_tr(uint32_t a) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((DCPA_LDS s16x4*)(uintptr_t)a));
+}
+
+// 16 bytes of every lane from global memory to LDS at base + 16 * lane (base
+// the same for the wave).  Written in asm so that the compiler does not put a
+// wait for it in front of every LDS read; dma_wait() has to run before the
+// data is read.  (m0 is never allocated, so writing it needs no clobber.)
+__device__ __forceinline__ void dma16(const char* g, uint32_t base) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                 :: "v"((uint64_t)g), "s"(base) : "memory");
+}
+__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// All LDS accesses of this wave done, then the workgroup meets.
+__device__ __forceinline__ void meet() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// What absent keys and columns are loaded from.
+__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
+
+// Eight e4m3 values as eight 16-bit ones (exact: both types hold them).
+template <typename E> __device__ __forceinline__ u32x4 widen8(u32x2 x) {
+    u32x4 r;
+    if constexpr (std::is_same_v<E, BF16T>) {
+        r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x.x, 1.0f, false));
+        r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x.x, 1.0f, true));
+        r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x.y, 1.0f, false));
+        r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x.y, 1.0f, true));
+    } else {
+        r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x.x, 1.0f, false));
+        r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x.x, 1.0f, true));
+        r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x.y, 1.0f, false));
+        r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x.y, 1.0f, true));
+    }
+    return r;
+}
+
+// --------------------------------------------------------------------------
+// lengths
+// --------------------------------------------------------------------------
+// Positions below x that lie on this rank.
+__device__ __forceinline__ int owned(const Batch& m, int x) {
+    const uint32_t block = (uint32_t)m.N * (uint32_t)m.inter, u = (uint32_t)max(x, 0);
+    const uint32_t full = u / block, rest = u - full * block;
+    return (int)(full * (uint32_t)m.inter) + min(max((int)rest - m.rank * m.inter, 0), m.inter);
+}
+
+struct Seq {
+    int first, n;   // token rows [first, first + n)
+    int kv;         // cached keys
+    int len;        // whole length
+};
+
+__device__ __forceinline__ Seq load_seq(const Batch& m, int b) {
+    Seq s;
+    s.first = min(max(m.cu[b], 0), m.T);
+    s.n = min(max(m.cu[b + 1], s.first), m.T) - s.first;
+    s.kv = min(max(m.kv[b], 0), m.max_keys);
+    s.len = m.seq != nullptr ? m.seq[b] : 0;
+    return s;
+}
+
+// Keys that token i of the sequence sees.
+__device__ __forceinline__ int visible(const Batch& m, const Seq& s, int i) {
+    if (!m.causal) return s.kv;
+    const int hidden = m.seq == nullptr ? s.n - 1 - i : owned(m, s.len) - owned(m, s.len - s.n + i + 1);
+    return min(max(s.kv - hidden, 0), s.kv);
+}
+
+__device__ __forceinline__ int scan_incl(int x, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int y = __shfl_up(x, d, 64);
+        if (lane >= d) x += y;
+    }
+    return x;
+}
+__device__ __forceinline__ int64_t sum_wave(int64_t x) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) x += __shfl_xor((long long)x, d, 64);
+    return x;
+}
+
+// The share of a batch that one workgroup takes: row tile `tile` of sequence
+// b against the keys [split * chunk, (split + 1) * chunk).  Every wave works
+// it out by itself from the lengths on the device: a first pass over the
+// sequences sums tiles * keys and sets the chunk so that about `target` equal
+// ranges come out, a second finds the unit.  So ragged batches are balanced
+// whatever the width of the page table, and the host needs no lengths.
+struct Unit {
+    Seq s;
+    int b, tile, split, splits, chunk;
+    int slot;       // of the tile's first split
+    bool ok;
+};
+
+template <int STEP>
+__device__ __forceinline__ int key_chunk(const Batch& m, int rows, int target) {
+    if (target <= 0) return 0x40000000;
+    const int lane = threadIdx.x & 63;
+    int64_t work = 0;
+    for (int b0 = 0; b0 < m.B; b0 += 64) {
+        const int b = b0 + lane;
+        if (b < m.B) {
+            const Seq s = load_seq(m, b);
+            work += (int64_t)(rows > 0 ? (s.n * m.G + rows - 1) / rows : 1) * s.kv;
+        }
+    }
+    work = sum_wave(work);
+    const int64_t chunk = (work + target - 1) / target;
+    return (int)min((int64_t)0x40000000, max((int64_t)(4 * STEP), (chunk + STEP - 1) / STEP * STEP));
+}
+
+// rows == 0: one unit column per sequence whatever its rows (the weights).
+template <int STEP>
+__device__ __forceinline__ Unit find_unit(const Batch& m, int rows, int target, int id) {
+    Unit u;
+    u.ok = false;
+    u.chunk = key_chunk<STEP>(m, rows, target);
+    const int lane = threadIdx.x & 63;
+    int base = 0;
+    for (int b0 = 0; b0 < m.B; b0 += 64) {
+        const int b = b0 + lane;
+        int tiles = 0, splits = 0;
+        if (b < m.B) {
+            const Seq s = load_seq(m, b);
+            tiles = rows > 0 ? (s.n * m.G + rows - 1) / rows : (s.n > 0);
+            splits = max(1, (s.kv + u.chunk - 1) / u.chunk);
+        }
+        const int incl = base + scan_incl(tiles * splits, lane);
+        const uint64_t past = __ballot(incl > id);
+        if (past != 0) {
+            const int at = __builtin_ctzll(past);
+            const int t = __builtin_amdgcn_readlane(tiles, at), s = __builtin_amdgcn_readlane(splits, at);
+            const int rest = id - (__builtin_amdgcn_readlane(incl, at) - t * s);
+            u.b = b0 + at;
+            u.s = load_seq(m, u.b);
+            u.splits = s;
+            u.tile = rest / s;
+            u.split = rest - u.tile * s;
+            u.slot = id - u.split;
+            // (lengths that contradict each other could lead outside the tile)
+            u.ok = rest >= 0 && (rows <= 0 || (int64_t)u.tile * rows < (int64_t)u.s.n * m.G);
+            return u;
+        }
+        base = __builtin_amdgcn_readlane(incl, 63);
+    }
+    return u;
+}
+
+}  // namespace dcpa

@@ -1,5 +1,5 @@
-"""Build libdcpmerge.so (and its measurement twin libdcpmerge_bench.so) for
-gfx950 with hipcc (cross-compiles without a GPU).
+"""Build libdcpmerge.so (and its measurement twin libdcpmerge_bench.so) and
+libdcpattn.so for gfx950 with hipcc (cross-compiles without a GPU).
 
     python -m lse_weighted_merge_dcp_amd.csrc.build
 
@@ -9,7 +9,8 @@ binding (lse_weighted_merge_dcp_amd/), where the binding loads them.
 libdcpmerge.so exports exactly the calls of include/dcpmerge.h.
 libdcpmerge_bench.so links the same kernel objects behind the dcpb_* calls of
 csrc/dcpmerge_bench.h (timing events on the kernels' own dispatches) and
-exports nothing else; only measurement code loads it.  A linker version
+exports nothing else; only measurement code loads it.  libdcpattn.so exports
+exactly the calls of include/dcpattn.h.  A linker version
 script fixes each library's exported names.
 """
 from __future__ import annotations
@@ -23,17 +24,22 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 PKG = os.path.dirname(HERE)
 ROOT = os.path.dirname(PKG)
-SOURCES = ["api.cpp", "pack.hip", "combine.hip", "inplace.hip", "bench_api.cpp"]
+SOURCES = ["attn.hip", "attn_mass.hip", "attn_rope.hip", "attn_evict.hip", "attn_api.cpp",
+           "api.cpp", "pack.hip", "combine.hip", "inplace.hip", "bench_api.cpp"]
 LIB = os.path.join(PKG, "libdcpmerge.so")
 BENCH_LIB = os.path.join(PKG, "libdcpmerge_bench.so")
+ATTN_LIB = os.path.join(PKG, "libdcpattn.so")
 # exported names of each library (everything else is local)
 EXPORTS = {
     LIB: ["dcp_lse_pack_dim", "dcp_status_str", "dcp_pack", "dcp_unpack_combine", "dcp_lse_combine_inplace"],
     BENCH_LIB: ["dcpb_pack", "dcpb_unpack_combine", "dcpb_lse_combine_inplace", "dcpb_empty_kernel"],
+    ATTN_LIB: ["dcpa_status_str", "dcpa_qk_norm_rope_append", "dcpa_paged_attn", "dcpa_paged_attn_workspace",
+               "dcpa_attn_mass", "dcpa_attn_mass_workspace", "dcpa_cache_evict"],
 }
 OBJECTS = {
     LIB: ["api", "pack", "combine", "inplace"],
     BENCH_LIB: ["bench_api", "api", "pack", "combine", "inplace"],
+    ATTN_LIB: ["attn_api", "attn", "attn_mass", "attn_rope", "attn_evict"],
 }
 ARCH = "gfx950"
 
@@ -78,14 +84,14 @@ def _link(lib: str, bdir: str, verbose: bool) -> None:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source and link libdcpmerge.so and
-    libdcpmerge_bench.so (always rebuilds).  Returns libdcpmerge.so's path."""
+    """Compile every HIP source and link libdcpmerge.so,
+    libdcpmerge_bench.so and libdcpattn.so (always rebuilds).  Returns libdcpmerge.so's path."""
     bdir = os.path.join(HERE, "_build")
     os.makedirs(bdir, exist_ok=True)
     objs = [os.path.join(bdir, s.rsplit(".", 1)[0] + ".o") for s in SOURCES]
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(5, os.cpu_count() or 1)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         list(ex.map(lambda so: _compile(so[0], so[1], verbose), zip(SOURCES, objs)))
-    for lib in (LIB, BENCH_LIB):
+    for lib in (LIB, BENCH_LIB, ATTN_LIB):
         _link(lib, bdir, verbose)
     return LIB
 

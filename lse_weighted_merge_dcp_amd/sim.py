@@ -19,7 +19,7 @@ from __future__ import annotations
 
 import torch
 
-from . import ops
+from . import attn, ops
 
 
 class StackedInterleaved:
@@ -123,3 +123,111 @@ def reduce_scatter_merge(partial: torch.Tensor, lse: torch.Tensor, out=None, out
         out_lse = torch.empty((T, H), dtype=torch.float32, device=partial.device)
     ops.dcp_lse_combine(partial, lse, is_lse_base_on_e=True, out=out, out_lse=out_lse, timing=timing)
     return out, out_lse
+
+
+class StackedAttention:
+    """One attention layer of N ranks in one GPU's memory: every rank's paged
+    cache [N, pages, page_size, Hkv, D], page tables, cached lengths and
+    accumulated weights, the exchange of the partials simulated by
+    StackedInterleaved.  Pages are handed out from a list per rank on the host."""
+
+    def __init__(self, N: int, Hq: int, Hkv: int, Dk: int, Dv: int, *, page_size: int, pages: int, sequences: int,
+                 max_pages: int, dtype: torch.dtype, device, interleave: int = 1):
+        assert Hq % N == 0
+        self.N, self.Hq, self.Hkv, self.Dk, self.Dv = N, Hq, Hkv, Dk, Dv
+        self.page_size, self.interleave, self.dtype, self.device = page_size, interleave, dtype, device
+        self.k_cache = torch.zeros((N, pages, page_size, Hkv, Dk), dtype=dtype, device=device)
+        self.v_cache = torch.zeros((N, pages, page_size, Hkv, Dv), dtype=dtype, device=device)
+        self.mass = torch.zeros((N, pages, page_size, Hkv), dtype=torch.float32, device=device)
+        self.table = torch.full((N, sequences, max_pages), -1, dtype=torch.int32, device=device)
+        self.kv_len = torch.zeros((N, sequences), dtype=torch.int32, device=device)
+        self.lens = [0] * sequences                              # whole lengths
+        self.held = [[0] * sequences for _ in range(N)]          # cached keys of each rank, as kv_len
+        self.pages = [[[] for _ in range(sequences)] for _ in range(N)]
+        self.free = [list(range(pages)) for _ in range(N)]
+
+    def _hold(self, r: int, b: int, keys: int) -> None:
+        """Pages for `keys` cached keys of sequence b on rank r."""
+        need = -(-keys // self.page_size)
+        assert need <= self.table.shape[2], "sequence longer than its page table"
+        while len(self.pages[r][b]) < need:
+            self.pages[r][b].append(self.free[r].pop())
+        self.table[r, b, :need] = torch.tensor(self.pages[r][b][:need], dtype=torch.int32)
+
+    def step(self, q, k, v, new, q_weight, k_weight, cos_sin, eps: float = 1e-6, weights: bool = True):
+        """One layer step with new[b] tokens of sequence b (q [T,Hq,Dk], k
+        [T,Hkv,Dk], v [T,Hkv,Dv] rows in the order of the sequences): norm,
+        rotation and append, attention on every rank, pack, exchange, merge,
+        and (weights) the accumulated weights.  Returns the merged out
+        [T,Hq,Dv] and log-sum-exp [T,Hq]."""
+        N, T, dev = self.N, q.shape[0], self.device
+        pos = torch.cat([torch.arange(m, m + n) for m, n in zip(self.lens, new)])
+        seq = torch.repeat_interleave(torch.arange(len(new)), torch.tensor(new))
+        owner = pos // self.interleave % N
+        slots = []
+        for r in range(N):
+            at = []
+            for b, n in enumerate(new):
+                first = self.held[r][b]
+                mine = owner[seq == b] == r
+                self.held[r][b] += int(mine.sum())
+                self._hold(r, b, self.held[r][b])
+                # the rank's cache may have been cut, so places count on from what it holds
+                j = first + torch.cumsum(mine.long(), 0) - 1
+                page = torch.tensor(self.pages[r][b] + [0])[(j // self.page_size).clamp(min=0)]
+                at.append(torch.where(mine, page * self.page_size + j % self.page_size, -1))
+            slots.append(torch.cat(at).to(dev))
+        self.lens = [m + n for m, n in zip(self.lens, new)]
+        self.kv_len.copy_(torch.tensor(self.held, dtype=torch.int32))
+        seq_len = torch.tensor(self.lens, dtype=torch.int32, device=dev)
+        cu = torch.tensor([sum(new[:b]) for b in range(len(new) + 1)], dtype=torch.int32, device=dev)
+        pos = pos.to(torch.int32).to(dev)
+        out = torch.empty((N, T, self.Hq, self.Dv), dtype=self.dtype, device=dev)
+        lse = torch.empty((N, T, self.Hq), dtype=torch.float32, device=dev)
+        qr = None
+        for r in range(N):
+            qr = attn.qk_norm_rope_append(q, k, v, q_weight, k_weight, pos, cos_sin, slots[r], self.k_cache[r],
+                                          self.v_cache[r], eps=eps, q_out=qr)
+            attn.dcp_paged_attn(qr, self.k_cache[r], self.v_cache[r], self.table[r], cu, self.kv_len[r],
+                                seq_len=seq_len, rank=r, n_ranks=N, interleave=self.interleave, out=out[r],
+                                out_lse=lse[r])
+        st = StackedInterleaved(N, T, self.Hq, self.Dv, self.dtype, dev)
+        st.pack(out, lse)
+        merged, g = st.combine(is_lse_base_on_e=True)            # [N, T, Hq / N, Dv], [N, T, Hq / N]
+        merged, g = merged.transpose(0, 1).reshape(T, self.Hq, self.Dv), g.transpose(0, 1).reshape(T, self.Hq)
+        if weights:
+            for r in range(N):
+                attn.dcp_attn_mass(qr, self.k_cache[r], g, self.mass[r], self.table[r], cu, self.kv_len[r],
+                                   seq_len=seq_len, rank=r, n_ranks=N, interleave=self.interleave)
+        return merged, g
+
+    def evict(self, budget: int, n_sink: int = 0, n_recent: int = 0) -> None:
+        """Every rank cuts its caches to `budget` keys for each sequence and
+        key head, into fresh pages; the old ones are free again."""
+        new = -(-budget // self.page_size)
+        for r in range(self.N):
+            dst = [[self.free[r].pop() for _ in range(new)] for _ in self.lens]
+            attn.dcp_cache_evict(self.mass[r], self.k_cache[r], self.v_cache[r], self.table[r], self.kv_len[r].clone(),
+                                 torch.tensor(dst, dtype=torch.int32, device=self.device), budget, n_sink=n_sink,
+                                 n_recent=n_recent, new_len=self.kv_len[r])
+            for b, pages in enumerate(dst):
+                self.free[r] += self.pages[r][b]
+                self.pages[r][b] = pages
+                self.held[r][b] = min(self.held[r][b], budget)
+                self.table[r, b] = -1
+                self.table[r, b, :new] = torch.tensor(pages, dtype=torch.int32)
+                # places behind the kept keys start without weight
+        self._clear_unused()
+
+    def _clear_unused(self) -> None:
+        """Weights of free places are zero, as a new key's are."""
+        for r in range(self.N):
+            for b, pages in enumerate(self.pages[r]):
+                full, rest = divmod(self.held[r][b], self.page_size)
+                for i, page in enumerate(pages):
+                    if i > full or (i == full and rest == 0):
+                        self.mass[r, page] = 0
+                    elif i == full:
+                        self.mass[r, page, rest:] = 0
+            if self.free[r]:
+                self.mass[r, self.free[r]] = 0

@@ -1,0 +1,272 @@
+"""Host side of libdcpattn (no GPU, no kernel launch): exported names, the
+argument structs, every refusal (fake, never dereferenced addresses; only
+rejected or empty calls are made), the workspace query, and the Python
+binding's checks."""
+import ctypes
+import os
+import re
+import struct
+import subprocess
+
+import pytest
+import torch
+
+from lse_weighted_merge_dcp_amd import attn
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "dcpattn.h")
+OK, NULL, SHAPE, HEADS, DTYPE, BASE, STRIDE, ALIGN = 0, -1, -2, -3, -4, -5, -6, -7
+WORKSPACE, VALUE = -20, -21
+A = 0x100000
+
+
+def fields(name):
+    """The struct's fields in the header's order: (name, is a double)."""
+    body = re.search(r"typedef struct \{((?:(?!typedef).)*?)\} " + name, open(HEADER).read(), re.S).group(1)
+    body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
+    got = []
+    for decl in body.split(";"):
+        decl = decl.strip()
+        if decl:
+            kind, rest = re.match(r"(const void\*|const float\*|const int32_t\*|const int64_t\*|void\*|float\*|int32_t\*|"
+                                  r"int64_t|double) (.*)", decl, re.S).groups()
+            got += [(n.strip(), kind == "double") for n in rest.split(",")]
+    return got
+
+
+def pack(layout, name, values):
+    f = fields(name)
+    assert layout.format.lstrip("=") == "%dq" % sum(not d for _, d in f) + ("3d" if any(d for _, d in f) else "")
+    assert set(values) <= {n for n, _ in f}
+    return layout.pack(*[values.get(n, 0.0 if d else 0) for n, d in f])
+
+
+ATTN = dict(q=A, q_T=1024, q_H=128, k=A, k_P=8192, k_S=512, k_H=128, v=A, v_P=8192, v_S=512, v_H=128, block_table=A,
+            t_B=4, cu_q=A, kv_len=A, seq_len=A, out=A, o_T=1024, o_H=128, lse=A, l_T=8, l_H=1, workspace=A,
+            workspace_bytes=1 << 40, B=0, T=8, Hq=8, Hkv=4, Dk=128, Dv=128, num_pages=9, page_size=16, max_pages=4,
+            N=2, rank=1, interleave=1, causal=1, dtype=2, cache_dtype=2, lse_base=0, scale=0.1, k_scale=1.0,
+            v_scale=1.0)
+ROPE = dict(q=A, q_T=1024, q_H=128, k=A, k_T=512, k_H=128, v=A, v_T=512, v_H=128, q_weight=A, k_weight=A, positions=A,
+            cos_sin=A, cs_P=128, slots=A, q_out=A, qo_T=1024, qo_H=128, k_cache=A, kc_P=8192, kc_S=512, kc_H=128,
+            v_cache=A, vc_P=8192, vc_S=512, vc_H=128, T=0, Hq=8, Hkv=4, D=128, Dv=128, q_norm=128, k_norm=128,
+            rope_off=0, rot=128, interleaved=0, positions_max=100, num_pages=9, page_size=16, dtype=2, cache_dtype=2,
+            eps=1e-6, k_scale=1.0, v_scale=1.0)
+EVICT = dict(mass=A, m_P=64, m_S=4, m_H=1, k=A, k_P=8192, k_S=512, k_H=128, v=A, v_P=8192, v_S=512, v_H=128,
+             block_table=A, t_B=4, kv_len=A, dst_table=A, d_B=2, new_len=A, kept=A, kp_B=128, kp_H=32, B=0, Hkv=4,
+             Dk=128, Dv=128, esize=2, num_pages=9, page_size=16, max_pages=4, dst_pages=2, budget=32, n_sink=4,
+             n_recent=8)
+
+
+def attn_call(**over):
+    return attn.lib().dcpa_paged_attn(pack(attn.ATTN_ARGS, "dcpa_attn_args", dict(ATTN, **over)), None)
+
+
+def mass_call(m=A, strides=(64, 4, 1), **over):
+    return attn.lib().dcpa_attn_mass(pack(attn.ATTN_ARGS, "dcpa_attn_args", dict(ATTN, **over)), m, *strides, None)
+
+
+def rope_call(**over):
+    return attn.lib().dcpa_qk_norm_rope_append(pack(attn.ROPE_ARGS, "dcpa_rope_args", dict(ROPE, **over)), None)
+
+
+def evict_call(**over):
+    return attn.lib().dcpa_cache_evict(pack(attn.EVICT_ARGS, "dcpa_evict_args", dict(EVICT, **over)), None)
+
+
+def test_library_exports_exactly_the_declared_symbols():
+    text = open(HEADER).read()
+    declared = sorted(set(re.findall(r"^\s*(?:int|int64_t|const char\*)\s+(dcpa_\w+)\s*\(", text, re.M)))
+    out = subprocess.run(["nm", "-D", "--defined-only", attn.ATTN_LIB_PATH], capture_output=True, text=True, check=True)
+    assert sorted(set(re.findall(r" T (\w+)$", out.stdout, re.M))) == declared == sorted(attn.SIGNATURES)
+
+
+def test_header_compiles_as_c(tmp_path):
+    src = tmp_path / "h.c"
+    src.write_text('#include "dcpattn.h"\n_Static_assert(sizeof(dcpa_attn_args) == %d, "");\n'
+                   '_Static_assert(sizeof(dcpa_rope_args) == %d, "");\n_Static_assert(sizeof(dcpa_evict_args) == %d, "");\n'
+                   'int main(void) { return dcpa_paged_attn(0, 0) == DCP_OK; }\n'
+                   % (attn.ATTN_ARGS.size, attn.ROPE_ARGS.size, attn.EVICT_ARGS.size))
+    subprocess.check_call(["gcc", "-std=c11", "-Wall", "-Wextra", "-Werror", "-I" + os.path.join(ROOT, "include"), "-c",
+                           str(src), "-o", str(tmp_path / "h.o")])
+
+
+def test_status_strings():
+    for code, name in attn.STATUS.items():
+        if code != -8:
+            assert attn.lib().dcpa_status_str(code).decode().startswith(name)
+    assert attn.lib().dcpa_status_str(77).decode() == "unknown dcpattn status"
+
+
+COMMON = [
+    (dict(dtype=0), DTYPE), (dict(dtype=3), DTYPE), (dict(cache_dtype=1), DTYPE), (dict(cache_dtype=0), DTYPE),
+    (dict(lse_base=2), BASE), (dict(B=-1), SHAPE), (dict(T=-1), SHAPE), (dict(Hq=0), SHAPE), (dict(Hkv=0), SHAPE),
+    (dict(Hkv=16), SHAPE), (dict(Hkv=3), HEADS), (dict(Dk=0), SHAPE), (dict(Dk=4), SHAPE), (dict(Dk=132), SHAPE),
+    (dict(Dk=584), SHAPE), (dict(T=1 << 31), SHAPE), (dict(T=1 << 28), SHAPE), (dict(B=1 << 21), SHAPE),
+    (dict(num_pages=-1), SHAPE), (dict(page_size=0), SHAPE), (dict(max_pages=-1), SHAPE),
+    (dict(max_pages=1 << 26), SHAPE), (dict(N=0), SHAPE), (dict(rank=2), SHAPE), (dict(rank=-1), SHAPE),
+    (dict(interleave=0), SHAPE), (dict(interleave=1 << 20, N=1 << 11), SHAPE),
+    (dict(scale=0.0), VALUE), (dict(scale=-1.0), VALUE), (dict(scale=float("nan")), VALUE),
+    (dict(scale=float("inf")), VALUE), (dict(k_scale=0.0), VALUE), (dict(v_scale=-1.0), VALUE),
+    (dict(scale=1e30, k_scale=1e30), VALUE), (dict(scale=1e-30, k_scale=1e-30), VALUE),
+    (dict(q_T=-1), STRIDE), (dict(k_P=(1 << 56) + 8), STRIDE), (dict(t_B=-1), STRIDE), (dict(l_T=-1), STRIDE),
+    (dict(k_P=1 << 56), STRIDE),
+]
+
+
+@pytest.mark.parametrize("over,want", COMMON)
+def test_attention_and_weights_refuse(over, want):
+    assert attn_call(**over) == want
+    assert mass_call(**over) == want
+    assert attn.lib().dcpa_paged_attn_workspace(pack(attn.ATTN_ARGS, "dcpa_attn_args", dict(ATTN, **over))) == want
+
+
+@pytest.mark.parametrize("over,want", [
+    (dict(Dv=0), SHAPE), (dict(Dv=12), SHAPE), (dict(Dv=264), SHAPE), (dict(Dk=264, Dv=128), SHAPE),
+    (dict(v=0, Dv=136), SHAPE), (dict(v=0, Dk=576, Dv=520), SHAPE), (dict(v_P=-8), STRIDE), (dict(o_H=-1), STRIDE),
+])
+def test_attention_refuses(over, want):
+    assert attn_call(**over) == want
+
+
+@pytest.mark.parametrize("over,want", [
+    (dict(q=0), NULL), (dict(k=0), NULL), (dict(cu_q=0), NULL), (dict(kv_len=0), NULL), (dict(block_table=0), NULL),
+    (dict(seq_len=0), NULL), (dict(out=0), NULL),
+    (dict(q=A + 8), ALIGN), (dict(q_T=1028), ALIGN), (dict(q_H=12), ALIGN), (dict(k=A + 8), ALIGN), (dict(k_S=516), ALIGN),
+    (dict(v=A + 2), ALIGN), (dict(v_H=132), ALIGN), (dict(out=A + 2), ALIGN), (dict(o_T=1023), ALIGN),
+    (dict(cu_q=A + 2), ALIGN), (dict(kv_len=A + 1), ALIGN), (dict(seq_len=A + 2), ALIGN), (dict(block_table=A + 1), ALIGN),
+    (dict(lse=A + 2), ALIGN), (dict(cache_dtype=3, k=A + 4), ALIGN),
+    (dict(workspace=0), WORKSPACE), (dict(workspace_bytes=0), WORKSPACE), (dict(workspace=A + 8), WORKSPACE),
+])
+def test_attention_refuses_pointers(over, want):
+    assert attn_call(B=3, **over) == want
+
+
+@pytest.mark.parametrize("over,want", [
+    (dict(lse=0), NULL), (dict(m=0), NULL), (dict(m=A + 2), ALIGN), (dict(q=0), NULL), (dict(k=A + 8), ALIGN),
+    (dict(strides=(-1, 4, 1)), STRIDE), (dict(strides=(64, 1 << 57, 1)), STRIDE),
+])
+def test_weights_refuse(over, want):
+    assert mass_call(B=3, **over) == want
+
+
+def test_split_rows_of_the_weights_need_a_workspace():
+    many = dict(B=1, T=512, q_T=1024)
+    need = attn.lib().dcpa_attn_mass_workspace(pack(attn.ATTN_ARGS, "dcpa_attn_args", dict(ATTN, **many)))
+    assert need > 0
+    assert mass_call(workspace_bytes=need - 1, **many) == WORKSPACE
+    assert mass_call(workspace=0, **many) == WORKSPACE
+    assert attn.lib().dcpa_attn_mass_workspace(pack(attn.ATTN_ARGS, "dcpa_attn_args", ATTN)) == 0
+
+
+def test_workspace_grows_with_the_columns_and_is_zero_for_large_batches():
+    q = lambda **o: attn.lib().dcpa_paged_attn_workspace(pack(attn.ATTN_ARGS, "dcpa_attn_args", dict(ATTN, **o)))  # noqa: E731
+    assert q() == 0                                     # B = 0
+    assert 0 < q(B=1, T=1, Dv=64) < q(B=1, T=1)
+    assert q(B=4, T=1 << 15, Hq=32) == 0                # enough row tiles: the keys stay whole
+    assert attn_call(B=1, T=1, workspace_bytes=q(B=1, T=1) - 1) == WORKSPACE
+
+
+def test_empty_calls_are_accepted():
+    assert attn_call() == OK and mass_call() == OK and rope_call() == OK and evict_call() == OK
+    assert attn_call(B=3, T=0) == OK and mass_call(B=3, T=0) == OK
+    for fn in ("dcpa_paged_attn", "dcpa_qk_norm_rope_append", "dcpa_cache_evict"):
+        assert getattr(attn.lib(), fn)(None, None) == NULL
+    assert attn.lib().dcpa_attn_mass(None, None, 0, 0, 0, None) == NULL
+    assert attn.lib().dcpa_paged_attn_workspace(None) == NULL and attn.lib().dcpa_attn_mass_workspace(None) == NULL
+
+
+@pytest.mark.parametrize("over,want", [
+    (dict(dtype=0), DTYPE), (dict(cache_dtype=1), DTYPE), (dict(T=-1), SHAPE), (dict(Hq=0), SHAPE), (dict(Hkv=0), SHAPE),
+    (dict(D=4), SHAPE), (dict(D=1032), SHAPE), (dict(D=100), SHAPE), (dict(Dv=12), SHAPE), (dict(q_norm=136), SHAPE),
+    (dict(k_norm=4), SHAPE), (dict(rot=8), SHAPE), (dict(rot=-16), SHAPE), (dict(rope_off=4), SHAPE),
+    (dict(rope_off=8), SHAPE), (dict(positions_max=0), SHAPE), (dict(page_size=0), SHAPE), (dict(eps=-1.0), VALUE),
+    (dict(eps=float("nan")), VALUE), (dict(k_scale=0.0), VALUE), (dict(v_scale=float("inf")), VALUE),
+    (dict(k_scale=1e-45), VALUE), (dict(q_T=-8), STRIDE), (dict(kc_P=1 << 57), STRIDE),
+    (dict(T=1, q=0), NULL), (dict(T=1, k=0), NULL), (dict(T=1, q_out=0), NULL), (dict(T=1, slots=0), NULL),
+    (dict(T=1, positions=0), NULL), (dict(T=1, cos_sin=0), NULL), (dict(T=1, q_weight=0), NULL),
+    (dict(T=1, k_cache=0), NULL), (dict(T=1, v_cache=0), NULL), (dict(T=1, q=A + 8), ALIGN), (dict(T=1, v_T=4), ALIGN),
+    (dict(T=1, q_out=A + 2), ALIGN), (dict(T=1, cs_P=130), ALIGN), (dict(T=1, kc_S=516), ALIGN),
+    (dict(T=1, slots=A + 4), ALIGN), (dict(T=1, cos_sin=A + 4), ALIGN),
+])
+def test_norm_rope_refuses(over, want):
+    assert rope_call(**over) == want
+
+
+@pytest.mark.parametrize("over,want", [
+    (dict(esize=3), DTYPE), (dict(B=-1), SHAPE), (dict(Hkv=0), SHAPE), (dict(Dk=0), SHAPE), (dict(Dv=0), SHAPE),
+    (dict(page_size=0), SHAPE), (dict(budget=0), VALUE), (dict(budget=33), VALUE), (dict(n_sink=-1), VALUE),
+    (dict(n_recent=-1), VALUE), (dict(n_sink=20, n_recent=13), VALUE), (dict(m_P=-1), STRIDE), (dict(kp_B=-1), STRIDE),
+    (dict(B=1, mass=0), NULL), (dict(B=1, k=0), NULL), (dict(B=1, kv_len=0), NULL), (dict(B=1, dst_table=0), NULL),
+    (dict(B=1, new_len=0), NULL), (dict(B=1, kept=0), NULL), (dict(B=1, block_table=0), NULL),
+    (dict(B=1, k=A + 4), ALIGN), (dict(B=1, Dk=126), ALIGN), (dict(B=1, v_S=510), ALIGN), (dict(B=1, mass=A + 2), ALIGN),
+])
+def test_evict_refuses(over, want):
+    assert evict_call(**over) == want
+
+
+def test_python_binding_rejects_before_any_call(monkeypatch):
+    monkeypatch.setattr(attn, "_on_gpu", lambda *ts: 0)
+    z = torch.zeros
+    q, kc = z(3, 8, 64, dtype=torch.bfloat16), z(4, 16, 2, 64, dtype=torch.bfloat16)
+    table, cu, kv = z(1, 4, dtype=torch.int32), torch.tensor([0, 3], dtype=torch.int32), z(1, dtype=torch.int32)
+    bad = [
+        dict(q=q.float()), dict(q=q[0]), dict(q=q.transpose(1, 2)), dict(k_cache=kc.half()), dict(k_cache=kc[0]),
+        dict(v_cache=kc[..., :32].to(torch.float8_e4m3fn)), dict(v_cache=kc[:3]), dict(v_cache=None),
+        dict(block_table=table.long()), dict(block_table=table[0]), dict(cu_q=cu[:1]), dict(cu_q=cu.long()),
+        dict(kv_len=kv.long()), dict(n_ranks=2), dict(n_ranks=2, seq_len=kv.long()), dict(out=q[:2]),
+        dict(out=q.half()), dict(out_lse=z(3, 8, dtype=torch.float64)), dict(out_lse=z(3, 7)), dict(v_dim=32),
+    ]
+    for over in bad:
+        a = dict(dict(q=q, k_cache=kc, v_cache=kc, block_table=table, cu_q=cu, kv_len=kv), **over)
+        with pytest.raises(ValueError):
+            attn.dcp_paged_attn(**a)
+    mass, lse = z(4, 16, 2), z(3, 8)
+    for over in [dict(lse=z(3, 7)), dict(lse=lse.double()), dict(mass=z(4, 16, 3)), dict(mass=mass.half())]:
+        with pytest.raises(ValueError):
+            attn.dcp_attn_mass(**dict(dict(q=q, k_cache=kc, lse=lse, mass=mass, block_table=table, cu_q=cu, kv_len=kv),
+                                      **over))
+    for over in [dict(mass=z(4, 16, 3)), dict(budget=-1), dict(kv_len=kv.long()), dict(dst_table=table[0]),
+                 dict(kept=z(1, 2, 7, dtype=torch.int32)), dict(new_len=z(2, dtype=torch.int32)),
+                 dict(v_cache=kc.half())]:
+        with pytest.raises(ValueError):
+            attn.dcp_cache_evict(**dict(dict(mass=mass, k_cache=kc, v_cache=kc, block_table=table, kv_len=kv,
+                                             dst_table=table, budget=8), **over))
+    k, w, cs = z(3, 2, 64, dtype=torch.bfloat16), z(64, dtype=torch.bfloat16), z(10, 64)
+    pos, slots = z(3, dtype=torch.int32), z(3, dtype=torch.int64)
+    for over in [dict(q=q.float()), dict(k=k[:2]), dict(v=None), dict(v_cache=None), dict(v=k[:, :1]),
+                 dict(q_weight=w.float()), dict(k_weight=w[::2]), dict(positions=pos.long()), dict(slots=slots.int()),
+                 dict(cos_sin=cs.double()), dict(q_out=q[:2]), dict(k_cache=kc.half())]:
+        a = dict(dict(q=q, k=k, v=k, q_weight=w, k_weight=w, positions=pos, cos_sin=cs, slots=slots, k_cache=kc,
+                      v_cache=kc), **over)
+        with pytest.raises(ValueError):
+            attn.qk_norm_rope_append(**a)
+    with pytest.raises(ValueError):      # CPU tensors are refused
+        monkeypatch.undo()
+        attn.dcp_paged_attn(q, kc, kc, table, cu, kv)
+
+
+def test_cache_slots_follow_the_round_robin():
+    """Every position of two sequences gets a slot on exactly one rank, in the
+    order of its pages."""
+    page, N, inter = 4, 3, 2
+    table = torch.tensor([[7, 2, 5], [1, 8, 3]], dtype=torch.int32)
+    pos = torch.arange(30).repeat(2)
+    seq = torch.arange(2).repeat_interleave(30)
+    got = [attn.cache_slots(pos, seq, table, page, r, N, inter) for r in range(N)]
+    count = [0] * (2 * N)
+    for i in range(60):
+        p, b = int(pos[i]), int(seq[i])
+        owner = p // inter % N
+        for r in range(N):
+            if r != owner:
+                assert int(got[r][i]) == -1
+        j = count[b * N + owner]
+        count[b * N + owner] += 1
+        assert int(got[owner][i]) == int(table[b, j // page]) * page + j % page
+    assert int(attn.cache_slots(torch.tensor([36]), torch.tensor([0]), table, page, 0, N, inter)[0]) == -1
+
+
+def test_struct_fields_are_eight_bytes():
+    for layout in (attn.ATTN_ARGS, attn.ROPE_ARGS, attn.EVICT_ARGS):
+        assert layout.size % 8 == 0 and struct.calcsize("=q") == 8
+    assert ctypes.sizeof(ctypes.c_void_p) == 8
