@@ -7,152 +7,24 @@
 // tiles of keys, and the four are joined in LDS at the end.
 // attn_join: joins the key ranges of one row tile that went to different
 // workgroups.
-#include "attn_tile.hpp"
+#include "attn_common.hpp"
 
 namespace dcpa {
 
 namespace {
 
-// The address of a cached token's row for one key head, or 0 where the table
-// names no page.
-__device__ __forceinline__ uint64_t page_row(int page, const Batch& m, const char* base, int64_t P, int64_t S,
-                                             int64_t off, uint32_t place) {
-    if ((uint32_t)page >= (uint32_t)m.pages) return 0;
-    return (uint64_t)(base + (int64_t)page * P + (int64_t)place * S + off);
-}
-
-// Writes a wave's finished rows: to the outputs, or as a part for the join.
-template <typename E, int DK, int DV, int RB>
-__device__ __forceinline__ void write_rows(const AttnArgs& p, const Unit& u, const Rows<DK, DV, RB>& w, int hk,
-                                           int unit, int tile_rows, int row0, int wave_row, int nrows) {
-    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-        const int in_tile = wave_row + rb * 32 + r, row = row0 + in_tile;
-        const float l = half_sum(w.l[rb]);
-        float f, lse2;
-        finish(l, w.mc[rb], p.vs, f, lse2);
-        if (row >= nrows) continue;
-        if (u.splits > 1) {
-            const int64_t at = ((int64_t)hk * p.units + unit) * tile_rows + in_tile;
-            float* o = p.ws_o + at * p.Dv;
-            if (h == 0) p.ws_l[at] = lse2;
-#pragma unroll
-            for (int cb = 0; cb < DV / 32; ++cb)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int col = cb * 32 + i * 8 + h * 4;
-                    if (col < p.Dv) {
-                        f32x4 x;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) x[k] = l == 0.0f ? 0.0f : w.o[rb][cb][i * 4 + k] * f;
-                        *(f32x4*)(o + col) = x;
-                    }
-                }
-        } else {
-            const int token = (int)fdiv((uint32_t)row, p.m.fG), head = hk * p.m.G + row - token * p.m.G;
-            char* o = p.out + (int64_t)(u.s.first + token) * p.o_T + (int64_t)head * p.o_H;
-            if (h == 0 && p.lse != nullptr)
-                p.lse[(int64_t)(u.s.first + token) * p.l_T + (int64_t)head * p.l_H] = lse2 * p.lmul;
-#pragma unroll
-            for (int cb = 0; cb < DV / 32; ++cb)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int col = cb * 32 + i * 8 + h * 4;
-                    if (col < p.Dv) {
-                        float x[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) x[k] = l == 0.0f ? 0.0f : w.o[rb][cb][i * 4 + k] * f;
-                        store4<E>(o + col * 2, x[0], x[1], x[2], x[3]);
-                    }
-                }
-        }
-    }
-}
-
-// Rows [first, end) of the unit one by one, without matrix products: a wave to
-// a row, the columns over its lanes, one key after the other, so that a key is
-// either seen by the row or never touched.  Taken only where attend() asks for
-// it (values that are not finite in a masked tile).
-template <typename E, bool KV8, int DK, int DV>
-__device__ __noinline__ void slow_rows(const AttnArgs& p, const Unit& u, int hk, int unit, int tile_rows, int row0,
-                                       int first, int end, int k0, int k1) {
-    const int lane = threadIdx.x & 63;
-    constexpr int NQ = (DK + 63) / 64, NO = (DV + 63) / 64, ES = KV8 ? 1 : 2;
-    using C = std::conditional_t<KV8, dcp::FP8T, E>;
-    auto one = [](const char* at) {
-        float f;
-        if constexpr (KV8) dcp::Cvt<C, 1>::unpack(dcp::vload<1>(at), &f);
-        else dcp::Cvt<C, 2>::unpack(dcp::vload<2>(at), &f);
-        return f;
-    };
-    const int32_t* table = p.m.table + (int64_t)u.b * p.m.t_B;
-#pragma unroll 1
-    for (int row = first; row < end; ++row) {
-        const int token = (int)fdiv((uint32_t)row, p.m.fG), head = hk * p.m.G + row - token * p.m.G;
-        const int stop = min(k1, visible(p.m, u.s, token));
-        const char* q = p.q + (int64_t)(u.s.first + token) * p.q_T + (int64_t)head * p.q_H;
-        float x[NQ], acc[NO], mc = kNoMax, l = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-            x[i] = 0.0f;
-            if (lane + 64 * i < p.Dk) dcp::Cvt<E, 2>::unpack(dcp::vload<2>(q + (lane + 64 * i) * 2), &x[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < NO; ++i) acc[i] = 0.0f;
-#pragma unroll 1
-        for (int key = k0; key < stop; ++key) {
-            const uint32_t page = fdiv((uint32_t)key, p.m.fpage);
-            const int id = table[page];
-            if ((uint32_t)id >= (uint32_t)p.m.pages) continue;
-            const int64_t place = key - (int64_t)page * p.m.page_size;
-            const char* kr = p.k + (int64_t)id * p.k_P + place * p.k_S + (int64_t)hk * p.k_H;
-            const char* vr = p.v == nullptr ? kr : p.v + (int64_t)id * p.v_P + place * p.v_S + (int64_t)hk * p.v_H;
-            float s = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NQ; ++i)
-                if (lane + 64 * i < p.Dk) s += x[i] * one(kr + (lane + 64 * i) * ES);
-#pragma unroll
-            for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d, 64);
-            s *= p.c;
-            const float next = fmaxf(mc, s), f = exp2_fast(mc - next), w = exp2_fast(s - next);
-            mc = next;
-            l = l * f + w;
-#pragma unroll
-            for (int i = 0; i < NO; ++i)
-                if (lane + 64 * i < p.Dv) acc[i] = acc[i] * f + w * one(vr + (lane + 64 * i) * ES);
-        }
-        float f, lse2;
-        finish(l, mc, p.vs, f, lse2);
-        const int64_t at = ((int64_t)hk * p.units + unit) * tile_rows + (row - row0);
-        if (lane == 0) {
-            if (u.splits > 1) p.ws_l[at] = lse2;
-            else if (p.lse != nullptr) p.lse[(int64_t)(u.s.first + token) * p.l_T + (int64_t)head * p.l_H] = lse2 * p.lmul;
-        }
-#pragma unroll
-        for (int i = 0; i < NO; ++i) {
-            const int col = lane + 64 * i;
-            if (col >= p.Dv) continue;
-            const float o = l == 0.0f ? 0.0f : acc[i] * f;
-            if (u.splits > 1) p.ws_o[at * p.Dv + col] = o;
-            else dcp::vstore<2>(p.out + (int64_t)(u.s.first + token) * p.o_T + (int64_t)head * p.o_H + col * 2,
-                                dcp::Cvt<E, 2>::pack(&o));
-        }
-    }
-}
-
 // ---------------------------------------------------------------------------
 // attn_rows
 // ---------------------------------------------------------------------------
-template <typename E, bool KV8, int DK, int DV, bool SHARED, int KT, int RB>
-__global__ __launch_bounds__(256, DK > 256 ? 1 : 2) void attn_rows(AttnArgs p) {
+template <typename E, bool KV8, int DK, int DV, int KT, int RB>
+__global__ __launch_bounds__(256, 2) void attn_rows(AttnArgs p) {
     constexpr int R = 128 * RB, KC = DK / 8, VC = DV / 8;
-    constexpr int KROW = KC * 16, VROW = SHARED ? KROW : VC * 16;
-    constexpr int KB = KT * KROW, VB = SHARED ? 0 : KT * VROW;
-    constexpr int NK = KT * KC / 256, NV = SHARED ? 0 : KT * VC / 256;   // 16-byte chunks of a thread
-    static_assert(KT * KC % 256 == 0 && (SHARED || KT * VC % 256 == 0), "a tile is whole rounds of the workgroup");
+    constexpr int KROW = KC * 16, VROW = VC * 16;
+    constexpr int KB = KT * KROW, VB = KT * VROW;
+    constexpr int NK = KT * KC / 256, NV = KT * VC / 256;   // 16-byte chunks of a thread
+    static_assert(KT * KC % 256 == 0 && KT * VC % 256 == 0, "a tile is whole rounds of the workgroup");
     __shared__ __attribute__((aligned(1024))) char tile[2][KB + VB];
-    __shared__ uint64_t krow_at[2][KT], vrow_at[2][SHARED ? 1 : KT];
+    __shared__ uint64_t krow_at[2][KT], vrow_at[2][KT];
     __shared__ uint64_t there_at[4];
 
     const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv), unit = (int)(blockIdx.x / (uint32_t)p.m.Hkv);
@@ -198,9 +70,9 @@ __global__ __launch_bounds__(256, DK > 256 ? 1 : 2) void attn_rows(AttnArgs p) {
         const uint64_t ka = page_row(page, p.m, p.k, p.k_P, p.k_S, koff, place);
         if (lane < KT) {
             krow_at[t & 1][lane] = ka;
-            if constexpr (!SHARED) vrow_at[t & 1][lane] = page_row(page, p.m, p.v, p.v_P, p.v_S, voff, place);
+            vrow_at[t & 1][lane] = page_row(page, p.m, p.v, p.v_P, p.v_S, voff, place);
         }
-        const uint64_t bits = __ballot(lane < KT && ka != 0);
+        const uint64_t bits = __ballot(lane < KT && (uint32_t)page < (uint32_t)p.m.pages);
         if (lane == 0) there_at[t & 3] = bits;
     };
     const uint32_t lds0 = lds_addr(&tile[0][0]);
@@ -213,14 +85,12 @@ __global__ __launch_bounds__(256, DK > 256 ? 1 : 2) void attn_rows(AttnArgs p) {
             const bool val = i >= NK;
             const int ch = (val ? i - NK : i) * 256 + tid, cols = val ? VC : KC;
             const int row = ch / cols, c = (ch % cols) ^ swz(row);
-            const uint64_t base = val ? vrow_at[t & 1][SHARED ? 0 : row] : krow_at[t & 1][row];
-            const bool ok = base != 0 && c * 8 < (val ? p.Dv : p.Dk);
+            const uint64_t base = val ? vrow_at[t & 1][row] : krow_at[t & 1][row];
+            const uint64_t a = at_or_zeros(c * 8 < (val ? p.Dv : p.Dk), base + (uint64_t)(c * (KV8 ? 8 : 16)));
             if constexpr (KV8) {
-                reg8[i] = u32x2{0, 0};
-                if (ok) reg8[i] = *(const u32x2*)(base + (uint64_t)(c * 8));
+                reg8[i] = *(const u32x2*)a;
             } else {
-                const char* g = ok ? (const char*)(base + (uint64_t)(c * 16)) : (const char*)kZeros;
-                dma16(g, __builtin_amdgcn_readfirstlane(buf + (uint32_t)((val ? KB : 0) +
+                dma16((const char*)a, __builtin_amdgcn_readfirstlane(buf + (uint32_t)((val ? KB : 0) +
                                                                         ((val ? i - NK : i) * 256 + wave * 64) * 16)));
             }
         }
@@ -260,7 +130,7 @@ __global__ __launch_bounds__(256, DK > 256 ? 1 : 2) void attn_rows(AttnArgs p) {
             int lim[RB];
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb) lim[rb] = vis[rb] - t * KT;
-            odd |= attend<E, DK, DV, RB, KT, KROW, VROW>(w, buf, SHARED ? buf : buf + KB, there, lim, full, p.c);
+            odd |= attend<E, DK, DV, RB, KT, KROW, VROW>(w, buf, buf + KB, there, lim, full, p.c);
         }
         if (wave == 0 && t + 2 < tiles) place_rows(t + 2, page);
         if (t + 1 < tiles) widen(t + 1);
@@ -323,19 +193,17 @@ __global__ __launch_bounds__(256, 1) void attn_keys(AttnArgs p) {
             const bool val = i >= NK;
             const int ch = (val ? i - NK : i) * 64 + lane, cols = val ? VC : KC;
             const int from = ch / cols, c = (ch % cols) ^ swz(from);
-            const uint64_t a = val ? va : ka;
-            const uint64_t base = (uint64_t)(uint32_t)__shfl((int)(uint32_t)a, from, 64) |
-                                  (uint64_t)(uint32_t)__shfl((int)(uint32_t)(a >> 32), from, 64) << 32;
-            const bool ok = base != 0 && c * 8 < (val ? p.Dv : p.Dk);
+            const uint64_t mine = val ? va : ka;
+            const uint64_t base = (uint64_t)(uint32_t)__shfl((int)(uint32_t)mine, from, 64) |
+                                  (uint64_t)(uint32_t)__shfl((int)(uint32_t)(mine >> 32), from, 64) << 32;
+            const uint64_t a = at_or_zeros(c * 8 < (val ? p.Dv : p.Dk), base + (uint64_t)(c * (KV8 ? 8 : 16)));
             if constexpr (KV8) {
-                reg8[i] = u32x2{0, 0};
-                if (ok) reg8[i] = *(const u32x2*)(base + (uint64_t)(c * 8));
+                reg8[i] = *(const u32x2*)a;
             } else {
-                const char* g = ok ? (const char*)(base + (uint64_t)(c * 16)) : (const char*)kZeros;
-                dma16(g, __builtin_amdgcn_readfirstlane(buf + (uint32_t)((val ? KB : 0) + (val ? i - NK : i) * 1024)));
+                dma16((const char*)a, __builtin_amdgcn_readfirstlane(buf + (uint32_t)((val ? KB : 0) + (val ? i - NK : i) * 1024)));
             }
         }
-        return (uint32_t)__ballot(h == 0 && ka != 0);
+        return (uint32_t)__ballot(h == 0 && (uint32_t)page < (uint32_t)p.m.pages);
     };
     auto widen = [&](uint32_t buf) {
         if constexpr (KV8) {
@@ -498,11 +366,12 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs p, int rows) {
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-AttnPlan plan_attn(const Batch& m, int Dk, int Dv, bool shared) {
+AttnPlan plan_attn(const Batch& m, int Dk, int Dv) {
     AttnPlan pl;
     const int64_t rows = (int64_t)m.T * m.G;
+    pl.latent = Dk > 256 || Dv > 256;
     // few rows a sequence: 32-row tiles whose waves share out the keys
-    pl.by_keys = !shared && rows <= (int64_t)32 * m.B;
+    pl.by_keys = !pl.latent && rows <= (int64_t)32 * m.B;
     pl.rows = pl.by_keys ? 32 : 128;
     pl.tiles = (int32_t)(rows / pl.rows + m.B);
     const int64_t busy = (int64_t)pl.tiles * m.Hkv;
@@ -510,16 +379,10 @@ AttnPlan plan_attn(const Batch& m, int Dk, int Dv, bool shared) {
     pl.target = busy >= 4 * want ? 0 : (int32_t)((want + m.Hkv - 1) / m.Hkv);
     pl.units = pl.tiles + pl.target;
     pl.ws_bytes = pl.target == 0 ? 0 : (int64_t)pl.units * m.Hkv * pl.rows * (Dv + 1) * 4;
-    (void)Dk;
     return pl;
 }
 
 namespace {
-
-struct JoinCall {
-    AttnArgs a;
-    int rows;
-};
 
 template <typename E, int STEP>
 hipError_t run_join(const AttnArgs& a, const AttnPlan& pl, hipStream_t stream) {
@@ -542,15 +405,15 @@ hipError_t run(const AttnArgs& a, const AttnPlan& pl, hipStream_t stream) {
         if (e != hipSuccess || pl.target == 0) return e;
         return run_join<E, 128>(a, pl, stream);
     }
-    if (a.v == nullptr) {
-        e = launch(attn_rows<E, KV8, 576, 512, true, 32, 1>, grid, block, stream, a);
+    if (pl.latent) {
+        e = launch_latent(a, grid, std::is_same_v<E, BF16T>, KV8, stream);
         if (e != hipSuccess || pl.target == 0) return e;
         return run_join<E, 32>(a, pl, stream);
     }
-    if (d <= 64) e = launch(attn_rows<E, KV8, 64, 64, false, 64, 1>, grid, block, stream, a);
-    else if (d <= 128) e = launch(attn_rows<E, KV8, 128, 128, false, 64, 1>, grid, block, stream, a);
+    if (d <= 64) e = launch(attn_rows<E, KV8, 64, 64, 64, 1>, grid, block, stream, a);
+    else if (d <= 128) e = launch(attn_rows<E, KV8, 128, 128, 64, 1>, grid, block, stream, a);
     else {
-        e = launch(attn_rows<E, KV8, 256, 256, false, 32, 1>, grid, block, stream, a);
+        e = launch(attn_rows<E, KV8, 256, 256, 32, 1>, grid, block, stream, a);
         if (e != hipSuccess || pl.target == 0) return e;
         return run_join<E, 32>(a, pl, stream);
     }
@@ -560,7 +423,12 @@ hipError_t run(const AttnArgs& a, const AttnPlan& pl, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_attn(const AttnArgs& a, const AttnPlan& pl, bool bf16, bool kv8, hipStream_t stream) {
+hipError_t launch_attn(const AttnArgs& arg, const AttnPlan& pl, bool bf16, bool kv8, hipStream_t stream) {
+    AttnArgs a = arg;
+    if (!pl.latent && a.v == nullptr) {        // narrow rows: the values are read as columns of their own
+        a.v = a.k;
+        a.v_P = a.k_P; a.v_S = a.k_S; a.v_H = a.k_H;
+    }
     if (bf16) return kv8 ? run<BF16T, true>(a, pl, stream) : run<BF16T, false>(a, pl, stream);
     return kv8 ? run<F16T, true>(a, pl, stream) : run<F16T, false>(a, pl, stream);
 }

@@ -122,7 +122,7 @@ int check_attn(const dcpa_attn_args* a, Batch& m) {
                  esize_of(a->cache_dtype)) ||
         !span_ok({{a->T, a->o_T}, {a->Hq, a->o_H}, {a->Dv, 1}}, 2))
         return DCP_ERR_STRIDE;
-    const AttnPlan pl = plan_attn(m, (int)a->Dk, (int)a->Dv, shared);
+    const AttnPlan pl = plan_attn(m, (int)a->Dk, (int)a->Dv);
     if ((int64_t)pl.units * m.Hkv > kMaxGrid) return DCP_ERR_SHAPE;
     return DCP_OK;
 }
@@ -153,7 +153,7 @@ int64_t dcpa_paged_attn_workspace(const dcpa_attn_args* a) {
     Batch m;
     if (int st = check_attn(a, m)) return st;
     if (a->B == 0 || a->T == 0) return 0;
-    return plan_attn(m, (int)a->Dk, (int)a->Dv, a->v == nullptr).ws_bytes;
+    return plan_attn(m, (int)a->Dk, (int)a->Dv).ws_bytes;
 }
 
 int dcpa_paged_attn(const dcpa_attn_args* a, void* stream) {
@@ -167,7 +167,7 @@ int dcpa_paged_attn(const dcpa_attn_args* a, void* stream) {
     if (!aligned(a->v, 8 * ec) || (a->v && !multiples({a->v_P, a->v_S, a->v_H}, 8)) || !aligned(a->out, 4) ||
         !multiples({a->o_T, a->o_H}, 2))
         return DCP_ERR_ALIGN;
-    const AttnPlan pl = plan_attn(k.m, (int)a->Dk, (int)a->Dv, a->v == nullptr);
+    const AttnPlan pl = plan_attn(k.m, (int)a->Dk, (int)a->Dv);
     if (pl.ws_bytes > 0 && (!a->workspace || a->workspace_bytes < pl.ws_bytes || !aligned(a->workspace, 16)))
         return DCPA_ERR_WORKSPACE;
     k.q = (const char*)a->q;

@@ -119,8 +119,15 @@ __device__ __forceinline__ void meet() {
     asm volatile("" ::: "memory");
 }
 
-// What absent keys and columns are loaded from.
-__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
+// What absent keys and columns are loaded from: a row of the widest cache.
+__device__ __attribute__((aligned(16))) const uint32_t kZeros[288] = {};
+
+// at, or the row of zeros (in bit operations: written as a choice, the compiler
+// branches around the read of `at` for every piece).
+__device__ __forceinline__ uint64_t at_or_zeros(bool ok, uint64_t at) {
+    const uint64_t mask = 0 - (uint64_t)ok;
+    return (at & mask) | ((uint64_t)kZeros & ~mask);
+}
 
 // Eight e4m3 values as eight 16-bit ones (exact: both types hold them).
 template <typename E> __device__ __forceinline__ u32x4 widen8(u32x2 x) {

@@ -1,0 +1,452 @@
+// attn_latent.hip -- attention in the latent layout: many query heads share
+// one key row of up to 576 columns, whose first Dv <= 512 are its value.
+//
+// A workgroup takes 128 query rows, a wave 32 of them against tiles of 32 keys
+// in LDS; keys and values are the same tile, so a key is fetched once for the
+// 2 * (576 + 512) * 128 operations done with it.  A wave's 32 x 512 outputs
+// fill the 256 accumulation registers and its queries 144 of the others, so
+// one wave runs on a SIMD and nothing but its own order of instructions hides a
+// latency: key and value fragments are read from LDS several products ahead,
+// the next tile comes straight into LDS meanwhile.  The products read 70 KB of
+// LDS per wave and tile (4 waves: 2176 clocks at 128 bytes a clock), as long as
+// their 68 matrix instructions take.
+//
+// The compiler would move outputs between the two halves of the register file
+// around every use outside a product, and spill.  So the outputs live in a0 ..
+// a255 by name: every instruction that touches them is written in asm here (the
+// compiler itself takes no accumulation register in this kernel, which a test
+// of the compiled code checks).
+#include "attn_common.hpp"
+
+namespace dcpa {
+
+namespace {
+
+// The scores' products, in ordinary registers.  The compiler does not see that
+// these are matrix instructions, so the waits it would add stand here: two
+// states in front, since a vector instruction may have written an operand just
+// before, and settle() between the last product and the first other use (an
+// 8-pass product's result may be read 11 states later).
+template <typename E> __device__ __forceinline__ void mma_first(f32x16& d, u32x4 a, u32x4 b) {
+    if constexpr (std::is_same_v<E, BF16T>)
+        asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(d) : "v"(a), "v"(b));
+    else
+        asm("s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, 0" : "=&v"(d) : "v"(a), "v"(b));
+}
+template <typename E> __device__ __forceinline__ void mma_next(f32x16& d, u32x4 a, u32x4 b) {
+    if constexpr (std::is_same_v<E, BF16T>)
+        asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(d) : "v"(a), "v"(b));
+    else
+        asm("s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+v"(d) : "v"(a), "v"(b));
+}
+__device__ __forceinline__ void settle(f32x16& d) { asm volatile("s_nop 15\n\ts_nop 3" : "+v"(d)); }
+
+// Output block CB (32 columns) is a[16 CB .. 16 CB + 15].
+template <typename E, int CB> __device__ __forceinline__ void out_mma(u32x4 a, u32x4 b) {
+    if constexpr (std::is_same_v<E, BF16T>)
+        asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 a[%2:%3], %0, %1, a[%2:%3]"
+                     :: "v"(a), "v"(b), "n"(16 * CB), "n"(16 * CB + 15));
+    else
+        asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_f16 a[%2:%3], %0, %1, a[%2:%3]"
+                     :: "v"(a), "v"(b), "n"(16 * CB), "n"(16 * CB + 15));
+}
+template <int I> __device__ __forceinline__ void out_scale4(float f) {
+    float t0, t1, t2, t3;
+    asm volatile("v_accvgpr_read_b32 %0, a[%5]\n\tv_accvgpr_read_b32 %1, a[%6]\n\t"
+                 "v_accvgpr_read_b32 %2, a[%7]\n\tv_accvgpr_read_b32 %3, a[%8]\n\t"
+                 "v_mul_f32 %0, %0, %4\n\tv_mul_f32 %1, %1, %4\n\tv_mul_f32 %2, %2, %4\n\tv_mul_f32 %3, %3, %4\n\t"
+                 "v_accvgpr_write_b32 a[%5], %0\n\tv_accvgpr_write_b32 a[%6], %1\n\t"
+                 "v_accvgpr_write_b32 a[%7], %2\n\tv_accvgpr_write_b32 a[%8], %3"
+                 : "=&v"(t0), "=&v"(t1), "=&v"(t2), "=&v"(t3)
+                 : "v"(f), "n"(I), "n"(I + 1), "n"(I + 2), "n"(I + 3));
+}
+template <int I> __device__ __forceinline__ f32x4 out_read4() {
+    float t0, t1, t2, t3;
+    asm volatile("v_accvgpr_read_b32 %0, a[%4]\n\tv_accvgpr_read_b32 %1, a[%5]\n\t"
+                 "v_accvgpr_read_b32 %2, a[%6]\n\tv_accvgpr_read_b32 %3, a[%7]"
+                 : "=&v"(t0), "=&v"(t1), "=&v"(t2), "=&v"(t3) : "n"(I), "n"(I + 1), "n"(I + 2), "n"(I + 3));
+    return f32x4{t0, t1, t2, t3};
+}
+template <int I> __device__ __forceinline__ void out_zero4() {
+    asm volatile("v_accvgpr_write_b32 a[%0], 0\n\tv_accvgpr_write_b32 a[%1], 0\n\t"
+                 "v_accvgpr_write_b32 a[%2], 0\n\tv_accvgpr_write_b32 a[%3], 0"
+                 :: "n"(I), "n"(I + 1), "n"(I + 2), "n"(I + 3));
+}
+#define DCPA_A8(x) "a" #x "0", "a" #x "1", "a" #x "2", "a" #x "3", "a" #x "4", "a" #x "5", "a" #x "6", "a" #x "7", "a" #x "8", "a" #x "9"
+// Declares the accumulation registers as written: the kernel is given them, and
+// the compiler keeps no value of its own in one of them across this place.  It
+// stands wherever a value could be live for long.
+__device__ __forceinline__ void out_claim() {
+    asm volatile("" ::: DCPA_A8(), DCPA_A8(1), DCPA_A8(2), DCPA_A8(3), DCPA_A8(4), DCPA_A8(5), DCPA_A8(6), DCPA_A8(7),
+                 DCPA_A8(8), DCPA_A8(9), DCPA_A8(10), DCPA_A8(11), DCPA_A8(12), DCPA_A8(13), DCPA_A8(14), DCPA_A8(15),
+                 DCPA_A8(16), DCPA_A8(17), DCPA_A8(18), DCPA_A8(19), DCPA_A8(20), DCPA_A8(21), DCPA_A8(22),
+                 DCPA_A8(23), DCPA_A8(24), "a250", "a251", "a252", "a253", "a254", "a255");
+}
+#undef DCPA_A8
+
+template <int N, typename F> __device__ __forceinline__ void times(F&& f) {
+    [&]<int... I>(std::integer_sequence<int, I...>) { (f(std::integral_constant<int, I>{}), ...); }(
+        std::make_integer_sequence<int, N>{});
+}
+
+constexpr int DK = 576, DV = 512, KT = 32;
+// A tile in LDS: 32 rows of the first 512 columns (1 KB each), then 32 rows of
+// the other 64.  Chunk c of row r lies at c ^ swz(r) of its part.
+constexpr int MAIN = KT * 1024, KB = MAIN + KT * 128;
+
+// 16 bytes at base + off of every lane (base the same for the wave) to LDS.
+__device__ __forceinline__ void dma16_from(uint64_t base, uint32_t off, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :: "v"(off), "s"(base), "s"(to) : "memory");
+}
+__device__ __forceinline__ uint64_t lane64(uint64_t x, int lane) {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, lane) |
+           (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(x >> 32), lane) << 32;
+}
+
+// EXACT: rows of all 576 columns (others are padded with zeros).
+template <typename E, bool KV8, bool EXACT>
+__global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
+    constexpr int R = 128, STEPS = DK / 16, CBS = DV / 32;
+    // Tiles t and t + 1 are read while t + 2 and t + 3 arrive.  8-bit rows arrive as
+    // they lie in the cache and are widened when their turn comes.
+    constexpr int NBUF = KV8 ? 3 : 4, RAW = KV8 ? KT * DK : 0;
+    __shared__ __attribute__((aligned(1024))) char tile[NBUF * KB + 2 * RAW];
+    __shared__ uint8_t there_at[8][4];
+    // page numbers of the keys of 16 tiles, and of the next 16
+    constexpr int GROUP = 16;
+    __shared__ int32_t page_of[2][GROUP * KT];
+
+    const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv), unit = (int)(blockIdx.x / (uint32_t)p.m.Hkv);
+    const Unit u = find_unit<KT>(p.m, R, p.target, unit);
+    if (!u.ok) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = (int)dcp::wave_id(), r = lane & 31, h = lane >> 5;
+    const int nrows = u.s.n * p.m.G, row0 = u.tile * R, wave_row = wave * 32;
+    const int last_row = min(row0 + R, nrows) - 1;
+    const int kend = visible(p.m, u.s, (int)fdiv((uint32_t)last_row, p.m.fG));
+    const int k0 = u.split * u.chunk, k1 = (int)min((int64_t)kend, (int64_t)k0 + u.chunk);
+    if (u.split > 0 && k0 >= k1) return;      // (the join counts the ranges by itself)
+    const int tiles = k1 > k0 ? (k1 - k0 + KT - 1) / KT : 0;
+
+    // --- tiles into LDS: a wave fetches 8 rows, lane l knows where row l / 8 of them lies
+    const int64_t koff = (int64_t)hk * p.k_H;
+    const int32_t* table = p.m.table + (int64_t)u.b * p.m.t_B;
+    const int my_key = k0 + wave * 8 + lane / 8;
+    const uint32_t lds0 = lds_addr(&tile[0]);
+    auto page_at = [&](int key) { return key < k1 ? table[fdiv((uint32_t)key, p.m.fpage)] : -1; };
+    uint64_t row_at = 0;           // of the tile that is fetched next
+    auto place_rows = [&](int t) {
+        const int page = page_of[t / GROUP & 1][t % GROUP * KT + wave * 8 + lane / 8];
+        const uint32_t key = (uint32_t)(my_key + t * KT);
+        const uint32_t place = key - fdiv(key, p.m.fpage) * p.m.fpage.d;
+        row_at = page_row(page, p.m, p.k, p.k_P, p.k_S, koff, place);
+        // one bit for each of the 8 rows
+        const uint64_t bits = __ballot((lane & 7) == 0 && (uint32_t)page < (uint32_t)p.m.pages);
+        if (lane == 0) there_at[t & 7][wave] = (uint8_t)(bits * 0x0102040810204080ull >> 56);
+    };
+    auto buffer = [&](int t) { return lds0 + (uint32_t)(t % NBUF * KB); };
+    // the wave's rows of a tile: of each row the first 512 columns, then what is left of all eight
+    auto fetch_rows = [&](uint32_t buf) {
+        int ln = lane;
+        asm volatile("" : "+v"(ln));        // (keeps nine offsets from being held in registers)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = ln ^ swz(i);
+            const uint32_t to = buf + (uint32_t)((wave * 8 + i) * 1024);
+            if constexpr (EXACT) dma16_from(lane64(row_at, 8 * i), (uint32_t)(c * 16), to);
+            else dma16((const char*)at_or_zeros(c * 8 < p.Dk, lane64(row_at, 8 * i) + (uint64_t)(c * 16)), to);
+        }
+        const int c = 64 + ((ln & 7) ^ swz(ln / 8));
+        dma16((const char*)at_or_zeros(EXACT || c * 8 < p.Dk, row_at + (uint64_t)(c * 16)),
+              buf + (uint32_t)(MAIN + wave * 1024));
+    };
+    // 8-bit: rows as they are (576 bytes each) behind the tiles
+    auto raw = [&](int t) { return lds0 + (uint32_t)(NBUF * KB + (t & 1) * RAW + wave * 8 * DK); };
+    auto fetch_raw = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+            // 288 pieces of 16 bytes: 36 to a row; the last round is half empty and repeats the last piece
+            const int ch = min(i * 64 + lane, 8 * 36 - 1), row = ch / 36, c = ch % 36;
+            const uint64_t base = (uint64_t)(uint32_t)__shfl((int)(uint32_t)row_at, row * 8, 64) |
+                                  (uint64_t)(uint32_t)__shfl((int)(uint32_t)(row_at >> 32), row * 8, 64) << 32;
+            if (i < 4 || lane < 32)
+                dma16((const char*)at_or_zeros(c * 16 + 16 <= p.Dk && (base & 15) == 0, base + (uint64_t)(c * 16)),
+                      __builtin_amdgcn_readfirstlane(raw(t) + (uint32_t)(i * 1024)));
+        }
+    };
+    auto widen = [&](int t, uint64_t rows) {
+        const uint32_t buf = buffer(t);
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+            const int ch = i * 64 + lane;
+            if (ch >= 8 * 36) continue;
+            const int row = ch / 36, c = ch % 36, in_tile = wave * 8 + row;
+            u32x4 x = lds_read16(raw(t) + (uint32_t)(ch * 16));
+            // rows that are only 8-byte aligned, and the half piece at a row's end
+            const uint64_t base = (uint64_t)(uint32_t)__shfl((int)(uint32_t)rows, row * 8, 64) |
+                                  (uint64_t)(uint32_t)__shfl((int)(uint32_t)(rows >> 32), row * 8, 64) << 32;
+            if (c * 16 < p.Dk && ((base & 15) != 0 || c * 16 + 16 > p.Dk)) {
+                const u32x2 lo = *(const u32x2*)(base + (uint64_t)(c * 16));
+                u32x2 hi = {0, 0};
+                if (c * 16 + 16 <= p.Dk) hi = *(const u32x2*)(base + (uint64_t)(c * 16 + 8));
+                x = u32x4{lo.x, lo.y, hi.x, hi.y};
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int d = 2 * c + k;
+                const uint32_t to = d < 64 ? (uint32_t)(in_tile * 1024 + (d ^ swz(row)) * 16)
+                                           : (uint32_t)(MAIN + in_tile * 128 + ((d - 64) ^ swz(row)) * 16);
+                lds_write16(buf + to, widen8<E>(k == 0 ? u32x2{x.x, x.y} : u32x2{x.z, x.w}));
+            }
+        }
+    };
+    // tile t asked for; its rows have been placed
+    auto fetch = [&](int t) {
+        if constexpr (KV8) fetch_raw(t);
+        else fetch_rows(buffer(t));
+    };
+    auto load_pages = [&](int group, int32_t (&x)[2]) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) x[k] = page_at(k0 + group * GROUP * KT + k * 256 + tid);
+    };
+    auto keep_pages = [&](int group, const int32_t (&x)[2]) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) page_of[group & 1][k * 256 + tid] = x[k];
+    };
+
+    out_claim();
+    times<DV / 8>([&](auto i) { out_zero4<i * 4>(); });
+    u32x4 q[STEPS];
+    const int my_row = min(row0 + wave_row + r, last_row), token = (int)fdiv((uint32_t)my_row, p.m.fG);
+    const int vis = visible(p.m, u.s, token) - k0;
+    load_query<DK>(q, p.q + (int64_t)(u.s.first + token) * p.q_T +
+                          (int64_t)(hk * p.m.G + my_row - token * p.m.G) * p.q_H, p.Dk, h);
+    const int vmin = __builtin_amdgcn_readlane(vis, 0), vmax = __builtin_amdgcn_readlane(vis, 31);
+    const bool work = row0 + wave_row < nrows;          // (waves behind the last row only help to fetch)
+    float mc = kNoMax, l = 0.0f;
+    bool odd = false;
+
+    // lane constants of the fragment reads (see attn_tile.hpp)
+    uint32_t ka[4], va[2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ka[j] = (uint32_t)(r * 1024 + ((2 * j + h) ^ swz(r)) * 16);
+    const int g = (lane >> 4) & 1, li = lane & 15;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        va[j] = (uint32_t)((4 * h + li / 4) * 1024 + (li & 1) * 8 +
+                           ((4 * j + 2 * g + (li & 3) / 2) ^ swz(4 * h + li / 4)) * 16);
+    auto key_fragment = [&](uint32_t buf, int st) {
+        return lds_read16(buf + ka[st & 3] + (st < 32 ? (uint32_t)((st >> 2) * 128) : (uint32_t)(MAIN - r * 896)));
+    };
+    auto value_fragment = [&](uint32_t buf, int i) {          // i = 2 * block + half of the keys
+        const uint32_t a = buf + va[(i >> 1) & 1] + (uint32_t)((i >> 2) * 128 + (i & 1) * 16 * 1024);
+        const u32x2 x = lds_read_tr(a), y = lds_read_tr(a + 8 * 1024);
+        return u32x4{x.x, x.y, y.x, y.y};
+    };
+    constexpr int AHEAD = 6, VAHEAD = 4;
+#define DCPA_PIN __builtin_amdgcn_sched_barrier(0)
+
+    // what arrives first: tile 0, then 1 and 2
+    f32x16 s;
+    uint64_t rows1 = 0, rows2 = 0;     // 8-bit: of the two tiles that are still to be widened
+    if (tiles > 0) {
+        int32_t x[2];
+        load_pages(0, x);
+        keep_pages(0, x);
+        meet();
+#pragma unroll
+        for (int t = 0; t < 3; ++t) {
+            if (t < tiles) {
+                place_rows(t);
+                if (KV8 && t == 2) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                fetch(t);
+            }
+            if (KV8 && t == 0) {
+                dma_wait();
+                widen(0, row_at);
+            }
+            if (KV8 && t == 1) rows1 = row_at;
+            if (KV8 && t == 2) rows2 = row_at;
+        }
+        dma_wait();
+        meet();
+        if (work && vmax > 0) {
+            const uint32_t buf = buffer(0);
+            times<STEPS>([&](auto st) {
+                if constexpr (st == 0) mma_first<E>(s, key_fragment(buf, st), q[0]);
+                else mma_next<E>(s, key_fragment(buf, st), q[st]);
+            });
+            settle(s);
+        }
+    }
+    out_claim();
+
+    // One tile's weights and outputs, with the next tile's scores between: the
+    // exponentials run in the shadow of its matrix instructions.
+    auto advance = [&](int t, auto next) {
+        constexpr bool NEXT = decltype(next)::value;
+        const uint32_t buf = buffer(t), nbuf = buffer(t + 1);
+        u32x4 kf[AHEAD], vf[VAHEAD];
+        if constexpr (NEXT) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) kf[i] = key_fragment(nbuf, i);
+        }
+        const uint32_t there = *(const uint32_t*)&there_at[t & 7][0];
+        const bool full = there == 0xffffffffu && vmin >= (t + 1) * KT;
+        if (!full) {
+            const uint32_t bits = there >> (4 * h);
+            const int lim = vis - t * KT - 4 * h;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int j = 8 * (i / 4) + i % 4;
+                s[i] = (bits >> j & 1u) != 0 && j < lim ? s[i] : -INFINITY;
+            }
+        }
+        f32x16 n;
+        auto product = [&](auto st) {
+            if constexpr (NEXT) {
+                if constexpr (st == 0) mma_first<E>(n, kf[0], q[0]);
+                else mma_next<E>(n, kf[st % AHEAD], q[st]);
+                DCPA_PIN;
+                if constexpr (st + AHEAD < STEPS) kf[st % AHEAD] = key_fragment(nbuf, st + AHEAD);
+            }
+        };
+        DCPA_PIN;
+        float top = -INFINITY;
+        times<8>([&](auto st) {
+            product(st);
+            top = fmaxf(top, fmaxf(s[2 * st], s[2 * st + 1]));
+            DCPA_PIN;
+        });
+        top = half_max(top) * p.c;
+        if (__ballot(top > mc + Mat<E>::kTop + kLazy) != 0) {
+            const float next_mc = top > mc + Mat<E>::kTop ? top - Mat<E>::kTop : mc;
+            const float f = exp2_fast(mc - next_mc);
+            mc = next_mc;
+            l *= f;
+            asm volatile("s_nop 15\n\ts_nop 3");
+            times<DV / 8>([&](auto i) { out_scale4<i * 4>(f); });
+        }
+        uint32_t pr[8];
+        float sum = 0.0f;
+        DCPA_PIN;
+        times<28>([&](auto k) {
+            product(std::integral_constant<int, 8 + k>{});
+            if constexpr (k >= 2 && k < 18) {
+                constexpr int i = k - 2;
+                s[i] = exp2_fast(__builtin_fmaf(s[i], p.c, -mc));
+                sum += s[i];
+                if constexpr (i % 2 == 1) pr[i / 2] = Mat<E>::pack2(s[i - 1], s[i]);
+            }
+            if constexpr (k >= 28 - VAHEAD) vf[k - (28 - VAHEAD)] = value_fragment(buf, k - (28 - VAHEAD));
+            DCPA_PIN;
+        });
+        l += sum;
+        const u32x4 p0 = {pr[0], pr[1], pr[2], pr[3]}, p1 = {pr[4], pr[5], pr[6], pr[7]};
+        DCPA_PIN;
+        times<2 * CBS>([&](auto i) {
+            out_mma<E, i / 2>(vf[i % VAHEAD], i % 2 == 0 ? p0 : p1);
+            if constexpr (i + VAHEAD < 2 * CBS) vf[i % VAHEAD] = value_fragment(buf, i + VAHEAD);
+            DCPA_PIN;
+        });
+        out_claim();
+        if (!full) {
+            // (a masked value that is not finite: see attend())
+            uint32_t hit = 0;
+#pragma unroll 1
+            for (int i = lane; i < KT * (DV / 8); i += 64) {
+                const u32x4 x = lds_read16(buf + (uint32_t)(i * 16));
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    hit |= (x[k] & Mat<E>::kExp & 0xffffu) == (Mat<E>::kExp & 0xffffu) ||
+                           (x[k] & Mat<E>::kExp & 0xffff0000u) == (Mat<E>::kExp & 0xffff0000u);
+            }
+            odd |= __ballot(hit != 0) != 0;
+        }
+        if constexpr (NEXT) {
+            settle(n);
+            s = n;
+        }
+    };
+
+#pragma unroll 1
+    for (int t = 0; t < tiles; ++t) {
+        out_claim();
+        // this wave's rows of tile t + 1 are there; the pieces of t + 2 may still be on their way
+        if constexpr (KV8) {
+            asm volatile("s_waitcnt vmcnt(5)" ::: "memory");
+            if (t + 1 < tiles) widen(t + 1, rows1);
+            rows1 = rows2;
+        } else {
+            asm volatile("s_waitcnt vmcnt(9)" ::: "memory");
+        }
+        meet();               // tile t + 1 is there, and every wave is done with tile t - 1
+        if (t % GROUP == 0 && t + GROUP < tiles) {
+            int32_t x[2];
+            load_pages(t / GROUP + 1, x);
+            keep_pages(t / GROUP + 1, x);
+        }
+        if (t + 3 < tiles) {
+            place_rows(t + 3);
+            fetch(t + 3);
+            if constexpr (KV8) rows2 = row_at;
+        } else {
+            dma_wait();       // (nothing follows that the count above could leave out)
+        }
+        out_claim();
+        if (work && vmax > t * KT) {
+            if (t + 1 < tiles && vmax > (t + 1) * KT) advance(t, std::true_type{});
+            else advance(t, std::false_type{});
+        }
+    }
+#undef DCPA_PIN
+
+    if (odd) {
+        slow_rows<E, KV8, DK, DV>(p, u, hk, unit, R, row0, row0 + wave_row, min(row0 + wave_row + 32, nrows), k0, k1);
+        return;
+    }
+    asm volatile("s_nop 15\n\ts_nop 3");
+    out_claim();
+    const float lsum = half_sum(l);
+    float f, lse2;
+    finish(lsum, mc, p.vs, f, lse2);
+    const int in_tile = wave_row + r, row = row0 + in_tile;
+    if (row >= nrows) return;
+    if (u.splits > 1) {
+        const int64_t at = ((int64_t)hk * p.units + unit) * R + in_tile;
+        float* o = p.ws_o + at * p.Dv + h * 4;
+        if (h == 0) p.ws_l[at] = lse2;
+        times<DV / 8>([&](auto i) {
+            f32x4 x = out_read4<i * 4>();
+            const int col = i * 8;
+            if (lsum == 0.0f) x = f32x4{0, 0, 0, 0};
+            if (col + h * 4 < p.Dv) *(f32x4*)(o + col) = x * f;
+        });
+    } else {
+        const int head = hk * p.m.G + my_row - token * p.m.G;
+        char* o = p.out + (int64_t)(u.s.first + token) * p.o_T + (int64_t)head * p.o_H + h * 8;
+        if (h == 0 && p.lse != nullptr) p.lse[(int64_t)(u.s.first + token) * p.l_T + (int64_t)head * p.l_H] = lse2 * p.lmul;
+        times<DV / 8>([&](auto i) {
+            f32x4 x = out_read4<i * 4>();
+            const int col = i * 8;
+            if (lsum == 0.0f) x = f32x4{0, 0, 0, 0};
+            if (col + h * 4 < p.Dv) store4<E>(o + col * 2, x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+        });
+    }
+}
+
+}  // namespace
+
+hipError_t launch_latent(const AttnArgs& a, dim3 grid, bool bf16, bool kv8, hipStream_t stream) {
+    const dim3 block(256);
+    auto run = [&](auto e, auto k) {
+        using E = decltype(e);
+        constexpr bool K8 = decltype(k)::value;
+        return a.Dk == DK ? launch(attn_latent<E, K8, true>, grid, block, stream, a)
+                          : launch(attn_latent<E, K8, false>, grid, block, stream, a);
+    };
+    if (bf16) return kv8 ? run(BF16T{}, std::true_type{}) : run(BF16T{}, std::false_type{});
+    return kv8 ? run(F16T{}, std::true_type{}) : run(F16T{}, std::false_type{});
+}
+
+}  // namespace dcpa

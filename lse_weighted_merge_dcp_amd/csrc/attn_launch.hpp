@@ -53,12 +53,15 @@ struct AttnArgs {
 // and the launch.
 struct AttnPlan {
     int rows;                // rows of a tile
+    bool latent;             // wide rows, the values are columns of the keys
     bool by_keys;            // the waves of a workgroup take different keys (few rows)
     int32_t target, tiles, units;
     int64_t ws_bytes;
 };
-AttnPlan plan_attn(const Batch& m, int Dk, int Dv, bool shared);
+AttnPlan plan_attn(const Batch& m, int Dk, int Dv);
 hipError_t launch_attn(const AttnArgs& a, const AttnPlan& pl, bool bf16, bool kv8, hipStream_t stream);
+
+hipError_t launch_latent(const AttnArgs& a, dim3 grid, bool bf16, bool kv8, hipStream_t stream);
 
 struct MassArgs {
     Batch m;

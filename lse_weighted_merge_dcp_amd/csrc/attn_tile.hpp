@@ -40,10 +40,10 @@ template <int DK, int N>
 __device__ __forceinline__ void load_query(u32x4 (&q)[N], const char* row, int Dk, int h) {
 #pragma unroll
     for (int s = 0; s < DK / 16; ++s) {
+        // (one address for all columns, no branch around a load)
         const int c = 2 * s + h;
-        u32x4 x = {0, 0, 0, 0};
-        if (c * 8 < Dk) x = *(const u32x4*)(row + c * 16);
-        q[s] = x;
+        const u32x4 x = *(const u32x4*)(row + min(c, Dk / 8 - 1) * 16);
+        q[s] = c * 8 < Dk ? x : u32x4{0, 0, 0, 0};
     }
 }
 

@@ -24,7 +24,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 PKG = os.path.dirname(HERE)
 ROOT = os.path.dirname(PKG)
-SOURCES = ["attn.hip", "attn_mass.hip", "attn_rope.hip", "attn_evict.hip", "attn_api.cpp",
+SOURCES = ["attn.hip", "attn_latent.hip", "attn_mass.hip", "attn_rope.hip", "attn_evict.hip", "attn_api.cpp",
            "api.cpp", "pack.hip", "combine.hip", "inplace.hip", "bench_api.cpp"]
 LIB = os.path.join(PKG, "libdcpmerge.so")
 BENCH_LIB = os.path.join(PKG, "libdcpmerge_bench.so")
@@ -39,7 +39,7 @@ EXPORTS = {
 OBJECTS = {
     LIB: ["api", "pack", "combine", "inplace"],
     BENCH_LIB: ["bench_api", "api", "pack", "combine", "inplace"],
-    ATTN_LIB: ["attn_api", "attn", "attn_mass", "attn_rope", "attn_evict"],
+    ATTN_LIB: ["attn_api", "attn", "attn_latent", "attn_mass", "attn_rope", "attn_evict"],
 }
 ARCH = "gfx950"
 
