@@ -28,7 +28,7 @@ __global__ __launch_bounds__(256, 2) void attn_rows(AttnArgs p) {
     __shared__ uint64_t there_at[4];
 
     const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv), unit = (int)(blockIdx.x / (uint32_t)p.m.Hkv);
-    const Unit u = find_unit<KT>(p.m, R, p.target, unit);
+    const Unit u = find_unit<KT>(p.m, R, p.slots, unit);
     if (!u.ok) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = (int)dcp::wave_id(), r = lane & 31, h = lane >> 5;
     const int nrows = u.s.n * p.m.G, row0 = u.tile * R, wave_row = wave * 32 * RB;
@@ -155,7 +155,7 @@ __global__ __launch_bounds__(256, 1) void attn_keys(AttnArgs p) {
     __shared__ int part_odd[4];
 
     const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv), unit = (int)(blockIdx.x / (uint32_t)p.m.Hkv);
-    const Unit u = find_unit<128>(p.m, 32, p.target, unit);
+    const Unit u = find_unit<128>(p.m, 32, p.slots, unit);
     if (!u.ok) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = (int)dcp::wave_id(), r = lane & 31, h = lane >> 5;
     const int nrows = u.s.n * p.m.G, row0 = u.tile * 32;
@@ -287,76 +287,86 @@ __global__ __launch_bounds__(256, 1) void attn_keys(AttnArgs p) {
 }
 
 // ---------------------------------------------------------------------------
-// attn_join: one wave to a row; each lane a few columns
+// attn_join: a wave to a row of a sequence whose keys were split; each lane
+// holds four columns (eight where the rows are wide)
 // ---------------------------------------------------------------------------
-template <typename E, int STEP>
-__global__ __launch_bounds__(256) void attn_join(AttnArgs p, int rows) {
-    const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv), id = (int)(blockIdx.x / (uint32_t)p.m.Hkv);
-    const int lane = threadIdx.x & 63, wave = (int)dcp::wave_id();
-    const int chunk = key_chunk<STEP>(p.m, rows, p.target);
-    int base = 0, sbase = 0;
+template <typename E, int STEP, int NC>
+__global__ __launch_bounds__(256) void attn_join(AttnArgs p) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t id = blockIdx.x * 4 + dcp::wave_id();
+    const int hk = (int)(id % (uint32_t)p.m.Hkv), at_row = (int)(id / (uint32_t)p.m.Hkv);
+    const int t = (int)fdiv((uint32_t)at_row, p.m.fG), head = at_row - t * p.m.G;
+    if (t >= p.m.T) return;
+    const int chunk = key_chunk<STEP>(p.m, p.rows, p.slots);
+    int base = 0;
     for (int b0 = 0; b0 < p.m.B; b0 += 64) {
         const int b = b0 + lane;
-        int tiles = 0, splits = 0;
+        int tiles, kv;
+        tiles_of(p.m, b, p.rows, tiles, kv);
+        const int splits = max(1, (kv + chunk - 1) / chunk);
+        bool here = false;
         if (b < p.m.B) {
             const Seq s = load_seq(p.m, b);
-            tiles = (s.n * p.m.G + rows - 1) / rows;
-            splits = max(1, (s.kv + chunk - 1) / chunk);
+            here = t >= s.first && t < s.first + s.n;
         }
-        const int incl = base + scan_incl(tiles, lane), sincl = sbase + scan_incl(tiles * splits, lane);
-        const uint64_t past = __ballot(incl > id);
-        if (past == 0) {
+        const int incl = base + scan_incl(tiles * splits, lane);
+        const uint64_t found = __ballot(here);
+        if (found == 0) {
             base = __builtin_amdgcn_readlane(incl, 63);
-            sbase = __builtin_amdgcn_readlane(sincl, 63);
             continue;
         }
-        const int at = __builtin_ctzll(past);
+        const int at = __builtin_ctzll(found);
         const int nt = __builtin_amdgcn_readlane(tiles, at), ns = __builtin_amdgcn_readlane(splits, at);
         if (ns == 1) return;                  // written whole
-        const int tile = id - (__builtin_amdgcn_readlane(incl, at) - nt);
-        const int slot = __builtin_amdgcn_readlane(sincl, at) - nt * ns + tile * ns;
         const Seq s = load_seq(p.m, b0 + at);
-        const int nrows = s.n * p.m.G, row0 = tile * rows;
-        if (tile < 0 || slot < 0 || row0 >= nrows) return;
-        const int last = min(row0 + rows, nrows) - 1;
+        const int row = (t - s.first) * p.m.G + head, tile = row / p.rows, in_tile = row - tile * p.rows;
+        const int slot = __builtin_amdgcn_readlane(incl, at) - nt * ns + tile * ns;
+        if (slot < 0) return;
+        // the ranges that the tile's last row has keys in
+        const int last = min((tile + 1) * p.rows, s.n * p.m.G) - 1;
         const int kend = visible(p.m, s, (int)fdiv((uint32_t)last, p.m.fG));
         const int parts = min(max(1, (kend + chunk - 1) / chunk), p.units - slot);
-        for (int row = row0 + wave; row <= last; row += 4) {
-            const int64_t first = ((int64_t)hk * p.units + slot) * rows + (row - row0);
-            float top = -INFINITY;
-            bool bad = false;
-            for (int k = lane; k < parts; k += 64) {
-                const float x = p.ws_l[first + (int64_t)k * rows];
-                bad |= x != x;
-                top = fmaxf(top, x);
-            }
+        const int64_t first = ((int64_t)hk * p.units + slot) * p.rows + in_tile;
+        float top = -INFINITY;
+        bool bad = false;
+        for (int k = lane; k < parts; k += 64) {
+            const float x = p.ws_l[first + (int64_t)k * p.rows];
+            bad |= x != x;
+            top = fmaxf(top, x);
+        }
 #pragma unroll
-            for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-            bad = __ballot(bad) != 0;
-            const float ref = top == -INFINITY ? 0.0f : top;
-            const int token = (int)fdiv((uint32_t)row, p.m.fG), head = hk * p.m.G + row - token * p.m.G;
-            char* o = p.out + (int64_t)(s.first + token) * p.o_T + (int64_t)head * p.o_H;
-            for (int c0 = 0; c0 < p.Dv; c0 += 256) {
-                const int col = c0 + lane * 4;
-                float acc[4] = {0, 0, 0, 0}, sum = 0.0f;
-                for (int k = 0; k < parts; ++k) {
-                    const float x = p.ws_l[first + (int64_t)k * rows];
-                    const float f = exp2_fast(x - ref);
-                    sum += f;
-                    if (col < p.Dv && f != 0.0f) {
-                        const f32x4 y = *(const f32x4*)(p.ws_o + (first + (int64_t)k * rows) * p.Dv + col);
+        for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+        bad = __ballot(bad) != 0;
+        const float ref = top == -INFINITY ? 0.0f : top;
+        float acc[NC * 4], sum = 0.0f;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[i] += f * y[i];
-                    }
+        for (int i = 0; i < NC * 4; ++i) acc[i] = 0.0f;
+#pragma unroll 4
+        for (int k = 0; k < parts; ++k) {
+            const float f = exp2_fast(p.ws_l[first + (int64_t)k * p.rows] - ref);
+            sum += f;
+#pragma unroll
+            for (int j = 0; j < NC; ++j) {
+                const int col = j * 256 + lane * 4;
+                if (col < p.Dv) {
+                    const f32x4 y = *(const f32x4*)(p.ws_o + (first + (int64_t)k * p.rows) * p.Dv + col);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[j * 4 + i] += f * y[i];
                 }
-                if (bad) sum = NAN;
-                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                if (col < p.Dv) store4<E>(o + col * 2, acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
-                if (c0 == 0 && lane == 0 && p.lse != nullptr)
-                    p.lse[(int64_t)(s.first + token) * p.l_T + (int64_t)head * p.l_H] =
-                        (sum == 0.0f ? -INFINITY : ref + __builtin_amdgcn_logf(sum)) * p.lmul;
             }
         }
+        if (bad) sum = NAN;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        char* o = p.out + (int64_t)t * p.o_T + (int64_t)(hk * p.m.G + head) * p.o_H;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            const int col = j * 256 + lane * 4;
+            if (col < p.Dv)
+                store4<E>(o + col * 2, acc[j * 4] * inv, acc[j * 4 + 1] * inv, acc[j * 4 + 2] * inv, acc[j * 4 + 3] * inv);
+        }
+        if (lane == 0 && p.lse != nullptr)
+            p.lse[(int64_t)t * p.l_T + (int64_t)(hk * p.m.G + head) * p.l_H] =
+                (sum == 0.0f ? -INFINITY : ref + __builtin_amdgcn_logf(sum)) * p.lmul;
         return;
     }
 }
@@ -373,24 +383,27 @@ AttnPlan plan_attn(const Batch& m, int Dk, int Dv) {
     // few rows a sequence: 32-row tiles whose waves share out the keys
     pl.by_keys = !pl.latent && rows <= (int64_t)32 * m.B;
     pl.rows = pl.by_keys ? 32 : 128;
-    pl.tiles = (int32_t)(rows / pl.rows + m.B);
+    // row tiles, at most: a tile holds rows of one sequence
+    const int64_t most = rows / pl.rows + m.B, each = (int64_t)m.T * ((m.G + pl.rows - 1) / pl.rows);
+    pl.tiles = (int32_t)(most < each ? most : each);
+    // Workgroups that run at once: one latent workgroup to a CU, two of the others.  Fewer row
+    // tiles than that: the keys are split so that the units fill the chip once; decode of ragged
+    // batches fills it several times over, so that long and short sequences even out.
     const int64_t busy = (int64_t)pl.tiles * m.Hkv;
-    const int64_t want = pl.by_keys ? 1024 : 512;
-    pl.target = busy >= 4 * want ? 0 : (int32_t)((want + m.Hkv - 1) / m.Hkv);
-    pl.units = pl.tiles + pl.target;
-    pl.ws_bytes = pl.target == 0 ? 0 : (int64_t)pl.units * m.Hkv * pl.rows * (Dv + 1) * 4;
+    const int64_t chip = pl.latent ? 256 : pl.by_keys ? 1024 : 512;
+    pl.slots = busy >= (pl.by_keys ? 4 * chip : chip) ? 0 : (int32_t)((chip + m.Hkv - 1) / m.Hkv);
+    pl.units = pl.slots > pl.tiles ? pl.slots : pl.tiles;
+    pl.ws_bytes = pl.slots == 0 ? 0 : (int64_t)pl.units * m.Hkv * pl.rows * (Dv + 1) * 4;
     return pl;
 }
 
 namespace {
 
 template <typename E, int STEP>
-hipError_t run_join(const AttnArgs& a, const AttnPlan& pl, hipStream_t stream) {
-    AttnArgs arg = a;
-    int rows = pl.rows;
-    void* args[] = {&arg, &rows};
-    return hipLaunchKernel(reinterpret_cast<const void*>(&attn_join<E, STEP>), dim3((uint32_t)(pl.tiles * a.m.Hkv)),
-                           dim3(256), args, 0, stream);
+hipError_t run_join(const AttnArgs& a, hipStream_t stream) {
+    const dim3 grid((uint32_t)(((int64_t)a.m.T * a.m.G * a.m.Hkv + 3) / 4)), block(256);
+    return a.Dv <= 256 ? launch(attn_join<E, STEP, 1>, grid, block, stream, a)
+                       : launch(attn_join<E, STEP, 2>, grid, block, stream, a);
 }
 
 template <typename E, bool KV8>
@@ -402,23 +415,23 @@ hipError_t run(const AttnArgs& a, const AttnPlan& pl, hipStream_t stream) {
         e = d <= 64    ? launch(attn_keys<E, KV8, 64, 64>, grid, block, stream, a)
             : d <= 128 ? launch(attn_keys<E, KV8, 128, 128>, grid, block, stream, a)
                        : launch(attn_keys<E, KV8, 256, 256>, grid, block, stream, a);
-        if (e != hipSuccess || pl.target == 0) return e;
-        return run_join<E, 128>(a, pl, stream);
+        if (e != hipSuccess || pl.slots == 0) return e;
+        return run_join<E, 128>(a, stream);
     }
     if (pl.latent) {
         e = launch_latent(a, grid, std::is_same_v<E, BF16T>, KV8, stream);
-        if (e != hipSuccess || pl.target == 0) return e;
-        return run_join<E, 32>(a, pl, stream);
+        if (e != hipSuccess || pl.slots == 0) return e;
+        return run_join<E, 32>(a, stream);
     }
     if (d <= 64) e = launch(attn_rows<E, KV8, 64, 64, 64, 1>, grid, block, stream, a);
     else if (d <= 128) e = launch(attn_rows<E, KV8, 128, 128, 64, 1>, grid, block, stream, a);
     else {
         e = launch(attn_rows<E, KV8, 256, 256, 32, 1>, grid, block, stream, a);
-        if (e != hipSuccess || pl.target == 0) return e;
-        return run_join<E, 32>(a, pl, stream);
+        if (e != hipSuccess || pl.slots == 0) return e;
+        return run_join<E, 32>(a, stream);
     }
-    if (e != hipSuccess || pl.target == 0) return e;
-    return run_join<E, 64>(a, pl, stream);
+    if (e != hipSuccess || pl.slots == 0) return e;
+    return run_join<E, 64>(a, stream);
 }
 
 }  // namespace

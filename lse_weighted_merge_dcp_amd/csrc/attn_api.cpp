@@ -123,7 +123,7 @@ int check_attn(const dcpa_attn_args* a, Batch& m) {
         !span_ok({{a->T, a->o_T}, {a->Hq, a->o_H}, {a->Dv, 1}}, 2))
         return DCP_ERR_STRIDE;
     const AttnPlan pl = plan_attn(m, (int)a->Dk, (int)a->Dv);
-    if ((int64_t)pl.units * m.Hkv > kMaxGrid) return DCP_ERR_SHAPE;
+    if ((int64_t)pl.units * m.Hkv > kMaxGrid || (pl.slots > 0 && a->T * a->Hq / 4 >= kMaxGrid)) return DCP_ERR_SHAPE;
     return DCP_OK;
 }
 
@@ -182,9 +182,9 @@ int dcpa_paged_attn(const dcpa_attn_args* a, void* stream) {
     k.l_T = a->l_T; k.l_H = a->l_H;
     k.Dk = (int32_t)a->Dk;
     k.Dv = (int32_t)a->Dv;
-    k.target = pl.target;
+    k.rows = pl.rows;
+    k.slots = pl.slots;
     k.units = pl.units;
-    k.tiles = pl.tiles;
     k.ws_o = (float*)a->workspace;
     k.ws_l = k.ws_o == nullptr ? nullptr : k.ws_o + (int64_t)pl.units * k.m.Hkv * pl.rows * a->Dv;
     k.c = (float)(a->scale * a->k_scale * 1.4426950408889634);

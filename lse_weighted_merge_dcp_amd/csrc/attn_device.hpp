@@ -194,10 +194,9 @@ __device__ __forceinline__ int64_t sum_wave(int64_t x) {
 
 // The share of a batch that one workgroup takes: row tile `tile` of sequence
 // b against the keys [split * chunk, (split + 1) * chunk).  Every wave works
-// it out by itself from the lengths on the device: a first pass over the
-// sequences sums tiles * keys and sets the chunk so that about `target` equal
-// ranges come out, a second finds the unit.  So ragged batches are balanced
-// whatever the width of the page table, and the host needs no lengths.
+// it out by itself from the lengths on the device, so ragged batches are
+// balanced whatever the width of the page table, and the host needs no
+// lengths.
 struct Unit {
     Seq s;
     int b, tile, split, splits, chunk;
@@ -205,39 +204,64 @@ struct Unit {
     bool ok;
 };
 
-template <int STEP>
-__device__ __forceinline__ int key_chunk(const Batch& m, int rows, int target) {
-    if (target <= 0) return 0x40000000;
-    const int lane = threadIdx.x & 63;
-    int64_t work = 0;
-    for (int b0 = 0; b0 < m.B; b0 += 64) {
-        const int b = b0 + lane;
-        if (b < m.B) {
-            const Seq s = load_seq(m, b);
-            work += (int64_t)(rows > 0 ? (s.n * m.G + rows - 1) / rows : 1) * s.kv;
-        }
+constexpr int kWhole = 0x40000000;     // longer than any cache
+
+// Row tiles and cached keys of sequence b (none behind the last one).
+__device__ __forceinline__ void tiles_of(const Batch& m, int b, int rows, int& tiles, int& kv) {
+    tiles = kv = 0;
+    if (b < m.B) {
+        const Seq s = load_seq(m, b);
+        tiles = (s.n * m.G + rows - 1) / rows;
+        kv = s.kv;
     }
-    work = sum_wave(work);
-    const int64_t chunk = (work + target - 1) / target;
-    return (int)min((int64_t)0x40000000, max((int64_t)(4 * STEP), (chunk + STEP - 1) / STEP * STEP));
 }
 
-// rows == 0: one unit column per sequence whatever its rows (the weights).
+// The length of a key range: the shortest multiple of STEP (to within an
+// eighth of the interval) with which the whole batch needs at most `slots`
+// units; kWhole where the tiles alone need that many.
 template <int STEP>
-__device__ __forceinline__ Unit find_unit(const Batch& m, int rows, int target, int id) {
+__device__ __forceinline__ int key_chunk(const Batch& m, int rows, int slots) {
+    if (slots <= 0) return kWhole;
+    const int lane = threadIdx.x & 63;
+    int64_t work = 0;
+    int all = 0, tiles = 0, kv = 0;
+    for (int b0 = 0; b0 < m.B; b0 += 64) {
+        tiles_of(m, b0 + lane, rows, tiles, kv);
+        work += (int64_t)tiles * kv;
+        all += tiles;
+    }
+    work = sum_wave(work);
+    all = (int)sum_wave((int64_t)all);
+    if (all >= slots) return kWhole;
+    // units <= work / chunk + tiles: `hi` is always enough, `lo` never too long
+    auto steps = [](int64_t x) { return (int)min((int64_t)(kWhole / STEP), max((int64_t)2, (x + STEP - 1) / STEP)); };
+    int lo = steps((work + slots - 1) / slots), hi = max(lo, steps((work + slots - all - 1) / (slots - all)));
+#pragma unroll 1
+    for (int round = 0; round < 3 && lo < hi; ++round) {
+        const int mid = lo + (hi - lo) / 2;
+        int64_t units = 0;
+        for (int b0 = 0; b0 < m.B; b0 += 64) {
+            if (m.B > 64) tiles_of(m, b0 + lane, rows, tiles, kv);
+            units += (int64_t)tiles * max(1, (kv + mid * STEP - 1) / (mid * STEP));
+        }
+        units = sum_wave(units);
+        if (units <= slots) hi = mid;
+        else lo = mid + 1;
+    }
+    return hi * STEP;
+}
+
+template <int STEP>
+__device__ __forceinline__ Unit find_unit(const Batch& m, int rows, int slots, int id) {
     Unit u;
     u.ok = false;
-    u.chunk = key_chunk<STEP>(m, rows, target);
+    u.chunk = key_chunk<STEP>(m, rows, slots);
     const int lane = threadIdx.x & 63;
     int base = 0;
     for (int b0 = 0; b0 < m.B; b0 += 64) {
-        const int b = b0 + lane;
-        int tiles = 0, splits = 0;
-        if (b < m.B) {
-            const Seq s = load_seq(m, b);
-            tiles = rows > 0 ? (s.n * m.G + rows - 1) / rows : (s.n > 0);
-            splits = max(1, (s.kv + u.chunk - 1) / u.chunk);
-        }
+        int tiles, kv;
+        tiles_of(m, b0 + lane, rows, tiles, kv);
+        const int splits = max(1, (kv + u.chunk - 1) / u.chunk);
         const int incl = base + scan_incl(tiles * splits, lane);
         const uint64_t past = __ballot(incl > id);
         if (past != 0) {
@@ -251,7 +275,7 @@ __device__ __forceinline__ Unit find_unit(const Batch& m, int rows, int target, 
             u.split = rest - u.tile * s;
             u.slot = id - u.split;
             // (lengths that contradict each other could lead outside the tile)
-            u.ok = rest >= 0 && (rows <= 0 || (int64_t)u.tile * rows < (int64_t)u.s.n * m.G);
+            u.ok = rest >= 0 && (int64_t)u.tile * rows < (int64_t)u.s.n * m.G;
             return u;
         }
         base = __builtin_amdgcn_readlane(incl, 63);

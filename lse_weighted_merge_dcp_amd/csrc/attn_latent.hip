@@ -118,7 +118,7 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
     __shared__ int32_t page_of[2][GROUP * KT];
 
     const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv), unit = (int)(blockIdx.x / (uint32_t)p.m.Hkv);
-    const Unit u = find_unit<KT>(p.m, R, p.target, unit);
+    const Unit u = find_unit<KT>(p.m, R, p.slots, unit);
     if (!u.ok) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = (int)dcp::wave_id(), r = lane & 31, h = lane >> 5;
     const int nrows = u.s.n * p.m.G, row0 = u.tile * R, wave_row = wave * 32;

@@ -41,9 +41,9 @@ struct AttnArgs {
     float* ws_o;             // [units][rows][Dv]
     float* ws_l;             // [units][rows]
     int32_t Dk, Dv;
-    int32_t target;          // workgroups the keys are split towards (0: not split)
+    int32_t rows;            // of a tile
+    int32_t slots;           // units of one key head that the keys are split into (0: not split)
     int32_t units;           // (row tile, key range) pairs of one key head the launch covers
-    int32_t tiles;           // row tiles of one key head, at most
     float c;                 // scale * k_scale * log2(e): scores in powers of two
     float vs;                // v_scale
     float lmul;              // ln 2, or 1 for base 2
@@ -55,7 +55,7 @@ struct AttnPlan {
     int rows;                // rows of a tile
     bool latent;             // wide rows, the values are columns of the keys
     bool by_keys;            // the waves of a workgroup take different keys (few rows)
-    int32_t target, tiles, units;
+    int32_t slots, tiles, units;
     int64_t ws_bytes;
 };
 AttnPlan plan_attn(const Batch& m, int Dk, int Dv);
