@@ -131,8 +131,8 @@ int dcpa_qk_norm_rope_append(const dcpa_rope_args* a, void* stream);
  *
  * dtype: DCP_F16 or DCP_BF16 (q, out).  Hq a multiple of Hkv.  Dk, Dv
  * multiples of 8, at most 256, or in the latent layout (v == NULL) Dk <= 576,
- * Dv <= 512, Dv <= Dk.  q rows 16-byte aligned, cache rows 8-element aligned,
- * out rows 4-byte aligned.  scale, k_scale and v_scale positive and finite.
+ * Dv <= 512, Dv <= Dk.  q rows 16-byte aligned, caches 16-byte aligned with
+ * rows 8 elements aligned, out rows 4-byte aligned.  scale, k_scale and v_scale positive and finite.
  *
  * Where rows are few, the keys are split over workgroups and joined by a
  * second kernel; the split parts live in `workspace`, whose size

@@ -130,7 +130,14 @@ __global__ __launch_bounds__(256, 2) void attn_rows(AttnArgs p) {
             int lim[RB];
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb) lim[rb] = vis[rb] - t * KT;
-            odd |= attend<E, DK, DV, RB, KT, KROW, VROW>(w, buf, buf + KB, there, lim, full, p.c);
+            f32x16 s[RB][KT / 32];
+            uint32_t pr[RB][KT / 32][8];
+            scores<E, DK, RB, KT, KROW>(s, w.q, buf);
+            weights<E>(w, s, pr, there, lim, full, p.c);
+            ValuePlace<VROW> vp;
+            vp.set(buf + KB, lane);
+            outputs<E, DK, DV, RB, KT>(w, pr, [&](int cb, int ks) { return vp.read(cb, ks); });
+            if (!full) odd |= odd_values<E, false>(buf + KB, VB);
         }
         if (wave == 0 && t + 2 < tiles) place_rows(t + 2, page);
         if (t + 1 < tiles) widen(t + 1);
@@ -144,13 +151,22 @@ __global__ __launch_bounds__(256, 2) void attn_rows(AttnArgs p) {
 
 // ---------------------------------------------------------------------------
 // attn_keys
+//
+// Bound by the cache's bytes: 32 keys of 128 columns are 16 KB and 512 clocks of
+// matrix instructions.  A wave keeps one tile of keys and one of values in LDS and
+// asks for the next keys as soon as its products have read the present ones,
+// for the next values likewise, so one of the two is always on its way; the
+// other waves of the CU (two workgroups) fill the gaps.  8-bit rows lie in LDS
+// as in the cache and are widened as fragments: no two waves read the same.
 // ---------------------------------------------------------------------------
 template <typename E, bool KV8, int DK, int DV>
-__global__ __launch_bounds__(256, 1) void attn_keys(AttnArgs p) {
-    constexpr int KT = 32, KC = DK / 8, VC = DV / 8, KROW = KC * 16, VROW = VC * 16;
-    constexpr int KB = KT * KROW, VB = KT * VROW, NK = KT * KC / 64, NV = KT * VC / 64;
-    constexpr int NBUF = (KB + VB) * 8 <= 147456 ? 2 : 1;
-    __shared__ __attribute__((aligned(1024))) char tile[4][NBUF][KB + VB];
+__global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void attn_keys(AttnArgs p) {
+    constexpr int KT = 32, ES = KV8 ? 1 : 2, KROW = DK * ES, VROW = DV * ES;
+    constexpr int KB = KT * KROW, VB = KT * VROW, NK = KB / 1024, NV = VB / 1024;
+    constexpr int GROUP = 8;                   // tiles whose page numbers are held at once, twice
+    __shared__ __attribute__((aligned(1024))) char tile[4][KB + VB];
+    __shared__ int32_t page_of[4][2][GROUP * KT];
+    __shared__ uint64_t row_at[4][2][KT];      // where the next tile's key and value rows lie
     __shared__ float part_mc[4][32], part_l[4][32];
     __shared__ int part_odd[4];
 
@@ -163,86 +179,117 @@ __global__ __launch_bounds__(256, 1) void attn_keys(AttnArgs p) {
     const int kend = visible(p.m, u.s, (int)fdiv((uint32_t)last_row, p.m.fG));
     const int k0 = u.split * u.chunk, k1 = (int)min((int64_t)kend, (int64_t)k0 + u.chunk);
     if (u.split > 0 && k0 >= k1) return;
-    const int tiles = k1 > k0 ? (k1 - k0 + KT - 1) / KT : 0;
+    // the wave's tiles are its own quarter of the range, one after the other
+    const int all_tiles = k1 > k0 ? (k1 - k0 + KT - 1) / KT : 0;
+    const int quarter = (all_tiles + 3) / 4, first = min(wave * quarter, all_tiles);
+    const int tiles = min(quarter, all_tiles - first), base_key = k0 + first * KT;
 
     Rows<DK, DV, 1> w;
     const int row = min(row0 + r, last_row), token = (int)fdiv((uint32_t)row, p.m.fG);
-    const int vis = visible(p.m, u.s, token) - k0;
+    const int vis = visible(p.m, u.s, token) - base_key;
     const int vmin = __builtin_amdgcn_readlane(vis, 0);
     load_query<DK>(w.q[0], p.q + (int64_t)(u.s.first + token) * p.q_T +
                                (int64_t)(hk * p.m.G + row - token * p.m.G) * p.q_H, p.Dk, h);
     clear_rows(w);
     bool odd = false;
 
-    const int64_t koff = (int64_t)hk * p.k_H, voff = (int64_t)hk * p.v_H;
     const int32_t* table = p.m.table + (int64_t)u.b * p.m.t_B;
-    const uint32_t lds0 = lds_addr(&tile[wave][0][0]);
-    // lane j < 32 knows where key j of the tile lies
-    auto page_of = [&](int t) {
-        const int key = k0 + t * KT + r;
-        return t < tiles && key < k1 ? table[fdiv((uint32_t)key, p.m.fpage)] : -1;
-    };
-    u32x2 reg8[KV8 ? NK + NV : 1];
-    auto fetch = [&](int t, int page, uint32_t buf) -> uint32_t {
-        const uint32_t key = (uint32_t)(k0 + t * KT + r);
-        const uint32_t place = key - fdiv(key, p.m.fpage) * p.m.fpage.d;
-        const uint64_t ka = page_row(page, p.m, p.k, p.k_P, p.k_S, koff, place);
-        const uint64_t va = page_row(page, p.m, p.v, p.v_P, p.v_S, voff, place);
+    auto load_pages = [&](int group, int32_t (&x)[GROUP * KT / 64]) {
 #pragma unroll
-        for (int i = 0; i < NK + NV; ++i) {
-            const bool val = i >= NK;
-            const int ch = (val ? i - NK : i) * 64 + lane, cols = val ? VC : KC;
-            const int from = ch / cols, c = (ch % cols) ^ swz(from);
-            const uint64_t mine = val ? va : ka;
-            const uint64_t base = (uint64_t)(uint32_t)__shfl((int)(uint32_t)mine, from, 64) |
-                                  (uint64_t)(uint32_t)__shfl((int)(uint32_t)(mine >> 32), from, 64) << 32;
-            const uint64_t a = at_or_zeros(c * 8 < (val ? p.Dv : p.Dk), base + (uint64_t)(c * (KV8 ? 8 : 16)));
-            if constexpr (KV8) {
-                reg8[i] = *(const u32x2*)a;
-            } else {
-                dma16((const char*)a, __builtin_amdgcn_readfirstlane(buf + (uint32_t)((val ? KB : 0) + (val ? i - NK : i) * 1024)));
-            }
+        for (int k = 0; k < GROUP * KT / 64; ++k) {
+            const int key = base_key + group * GROUP * KT + k * 64 + lane;
+            x[k] = key < k1 ? table[fdiv((uint32_t)key, p.m.fpage)] : -1;
         }
+    };
+    auto keep_pages = [&](int group, const int32_t (&x)[GROUP * KT / 64]) {
+#pragma unroll
+        for (int k = 0; k < GROUP * KT / 64; ++k) page_of[wave][group & 1][k * 64 + lane] = x[k];
+    };
+    // lanes 0 .. 31 place the key rows of tile t, the others its value rows
+    const char* my_base = h == 0 ? p.k + (int64_t)hk * p.k_H : p.v + (int64_t)hk * p.v_H;
+    const int64_t my_P = h == 0 ? p.k_P : p.v_P, my_S = h == 0 ? p.k_S : p.v_S;
+    auto place_rows = [&](int t) {
+        const int page = page_of[wave][t / GROUP & 1][t % GROUP * KT + r];
+        const uint32_t key = (uint32_t)(base_key + t * KT + r);
+        const uint32_t place = key - fdiv(key, p.m.fpage) * p.m.fpage.d;
+        row_at[wave][h][r] = page_row(page, p.m, my_base, my_P, my_S, 0, place);
         return (uint32_t)__ballot(h == 0 && (uint32_t)page < (uint32_t)p.m.pages);
     };
-    auto widen = [&](uint32_t buf) {
-        if constexpr (KV8) {
+    const uint32_t kbuf = lds_addr(&tile[wave][0]), vbuf = kbuf + KB;
+    // a row's chunk c of 16 bytes lies at c ^ turn(row)
+    auto turn = [](int row) { return KV8 ? (DK * ES >= 128 ? row >> 1 & 7 : row >> 1 & 3) : swz(row); };
+    auto fetch = [&](bool val, uint32_t buf) {
+        constexpr int NMAX = NK > NV ? NK : NV;
+        const int cols = (val ? VROW : KROW) / 16, n = val ? NV : NK, width = (val ? p.Dv : p.Dk) * ES;
 #pragma unroll
-            for (int i = 0; i < NK + NV; ++i) {
-                const bool val = i >= NK;
-                lds_write16(buf + (uint32_t)((val ? KB : 0) + (val ? i - NK : i) * 1024 + lane * 16), widen8<E>(reg8[i]));
-            }
+        for (int i = 0; i < NMAX; ++i) {
+            if (i >= n) break;
+            const int ch = i * 64 + lane, from = ch / cols, c = (ch % cols) ^ turn(from);
+            const uint64_t a = at_or_zeros(c * 16 < width, row_at[wave][val][from] + (uint64_t)(c * 16));
+            dma16((const char*)a, __builtin_amdgcn_readfirstlane(buf + (uint32_t)(i * 1024)));
         }
     };
+
+    int32_t pages[GROUP * KT / 64];
     uint32_t there = 0;
-    int t = wave;
-    int page = page_of(t + 4);
-    if (t < tiles) {
-        there = fetch(t, page_of(t), lds0);
-        widen(lds0);
+    if (tiles > 0) {
+        load_pages(0, pages);
+        keep_pages(0, pages);
+        there = place_rows(0);
+        fetch(false, kbuf);
+        fetch(true, vbuf);
     }
-    int b = 0;
 #pragma unroll 1
-    for (; t < tiles; t += 4) {
-        const uint32_t cur = lds0 + (uint32_t)(b * (KB + VB)), nxt = lds0 + (uint32_t)((NBUF - 1 - b) * (KB + VB));
-        uint32_t there_next = 0;
-        if constexpr (!KV8) dma_wait();
-        if (NBUF == 2 || KV8) {
-            if (t + 4 < tiles) there_next = fetch(t + 4, page, nxt);
+    for (int t = 0; t < tiles; ++t) {
+        // keys of t are there; its values may still be on their way
+        asm volatile("s_waitcnt vmcnt(%0)" :: "n"(NV) : "memory");
+        f32x16 s[1][1];
+        uint32_t pr[1][1][8];
+        if constexpr (KV8) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[0][0][i] = 0.0f;
+#pragma unroll
+            for (int st = 0; st < DK / 16; ++st) {
+                const u32x2 x = *(const DCPA_LDS u32x2*)(uintptr_t)(kbuf + (uint32_t)(r * KROW + ((st ^ turn(r)) * 16) + h * 8));
+                s[0][0] = Mat<E>::mma(widen8<E>(x), w.q[0][st], s[0][0]);
+            }
+        } else {
+            scores<E, DK, 1, KT, KROW>(s, w.q, kbuf);
         }
-        const int page_next = page_of(t + 8);
+        const uint32_t now = there;
+        const bool next = t + 1 < tiles;
+        if (next) {
+            // (loads into LDS do not wait for this wave's reads)
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            there = place_rows(t + 1);
+            fetch(false, kbuf);
+        }
         const int lim[1] = {vis - t * KT};
-        const bool full = there == 0xffffffffu && vmin >= (t + 1) * KT;
-        odd |= attend<E, DK, DV, 1, KT, KROW, VROW>(w, cur, cur + KB, there, lim, full, p.c);
-        // this wave's LDS accesses stay in order, but loads into LDS do not wait for its reads
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if (NBUF == 1 && !KV8) {
-            if (t + 4 < tiles) there_next = fetch(t + 4, page, nxt);
+        const bool full = now == 0xffffffffu && vmin >= (t + 1) * KT;
+        weights<E>(w, s, pr, now, lim, full, p.c);
+        // values of t
+        if (next) asm volatile("s_waitcnt vmcnt(%0)" :: "n"(NK) : "memory");
+        else dma_wait();
+        if constexpr (KV8) {
+            const int g = (lane >> 4) & 1, li = lane & 15, j = li >> 1, key = 4 * h + (j & 3) + 8 * (j >> 2);
+            outputs<E, DK, DV, 1, KT>(w, pr, [&](int cb, int ks) {
+                const uint32_t a = vbuf + (uint32_t)((ks * 16 + key) * VROW + ((2 * cb + g) ^ turn(ks * 16 + key)) * 16 + (li & 1) * 8);
+                return widen8<E>(lds_read_tr8(a));
+            });
+        } else {
+            ValuePlace<VROW> vp;
+            vp.set(vbuf, lane);
+            outputs<E, DK, DV, 1, KT>(w, pr, [&](int cb, int ks) { return vp.read(cb, ks); });
         }
-        if (t + 4 < tiles) widen(nxt);
-        page = page_next;
-        there = there_next;
-        if (NBUF == 2) b ^= 1;
+        if (!full) odd |= odd_values<E, KV8>(vbuf, VB);
+        if (t % GROUP == 0 && t + GROUP < tiles) {
+            load_pages(t / GROUP + 1, pages);
+            keep_pages(t / GROUP + 1, pages);
+        }
+        if (next) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            fetch(true, vbuf);
+        }
     }
 
     // the four waves' sums and outputs on one scale, through LDS
@@ -265,25 +312,51 @@ __global__ __launch_bounds__(256, 1) void attn_keys(AttnArgs p) {
     for (int k = 0; k < 4; ++k) total += part_l[k][r] * exp2_fast(part_mc[k][r] - mc);
     // (mc +infinity, a row that met a score of +infinity: its sums are NaN already)
     const float f = w.mc[0] == mc ? 1.0f : exp2_fast(w.mc[0] - mc);
-    float* all = (float*)&tile[0][0][0];
-    static_assert(sizeof(tile) >= 4 * 32 * 32 * 4, "room for the parts of 32 columns");
+    // each wave adds up its quarter of the output registers
+    constexpr int PART = DV / 32 * 16 / 4;
+    float* all = (float*)&tile[0][0];
+    constexpr int ROUNDS = (4 * DV / 32 * 16 * 64 * 4 + (int)sizeof(tile) - 1) / (int)sizeof(tile);
+    constexpr int PER = PART / ROUNDS;         // registers of each quarter that one round exchanges
+    static_assert(PART % ROUNDS == 0, "rounds of equal size");
+    float mine[PART];
 #pragma unroll
-    for (int cb = 0; cb < DV / 32; ++cb) {
+    for (int round = 0; round < ROUNDS; ++round) {
         meet();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) all[(wave * 16 + i) * 64 + lane] = w.o[0][cb][i] * f;
-        meet();
-        if (wave == 0) {
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                w.o[0][cb][i] = (all[i * 64 + lane] + all[(16 + i) * 64 + lane]) +
-                                (all[(32 + i) * 64 + lane] + all[(48 + i) * 64 + lane]);
-        }
+            for (int i = 0; i < PER; ++i) {
+                const int at = k * PART + round * PER + i;
+                all[((k * 4 + wave) * PER + i) * 64 + lane] = w.o[0][at / 16][at % 16] * f;
+            }
+        meet();
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            mine[round * PER + i] = (all[((wave * 4 + 0) * PER + i) * 64 + lane] + all[((wave * 4 + 1) * PER + i) * 64 + lane]) +
+                                    (all[((wave * 4 + 2) * PER + i) * 64 + lane] + all[((wave * 4 + 3) * PER + i) * 64 + lane]);
     }
-    if (wave != 0) return;
-    w.mc[0] = mc;
-    w.l[0] = h == 0 ? total : 0.0f;
-    write_rows<E>(p, u, w, hk, unit, 32, row0, 0, nrows);
+    const int my_row = row0 + r;
+    if (my_row >= nrows) return;
+    float scale, lse2;
+    finish(total, mc, p.vs, scale, lse2);
+    const int head = hk * p.m.G + row - token * p.m.G;
+    const int64_t at = ((int64_t)hk * p.units + unit) * 32 + r;
+    const bool split = u.splits > 1;
+    if (h == 0 && wave == 0) {
+        if (split) p.ws_l[at] = lse2;
+        else if (p.lse != nullptr) p.lse[(int64_t)(u.s.first + token) * p.l_T + (int64_t)head * p.l_H] = lse2 * p.lmul;
+    }
+    char* o = p.out + (int64_t)(u.s.first + token) * p.o_T + (int64_t)head * p.o_H;
+#pragma unroll
+    for (int i = 0; i < PART; i += 4) {
+        const int reg = wave * PART + i, col = reg / 16 * 32 + (reg % 16) * 2 + h * 4;
+        if (col >= p.Dv) continue;
+        f32x4 x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = total == 0.0f ? 0.0f : mine[i + k] * scale;
+        if (split) *(f32x4*)(p.ws_o + at * p.Dv + col) = x;
+        else store4<E>(o + col * 2, x[0], x[1], x[2], x[3]);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -376,12 +449,12 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs p) {
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-AttnPlan plan_attn(const Batch& m, int Dk, int Dv) {
+AttnPlan plan_attn(const Batch& m, int Dk, int Dv, bool pieces) {
     AttnPlan pl;
     const int64_t rows = (int64_t)m.T * m.G;
     pl.latent = Dk > 256 || Dv > 256;
     // few rows a sequence: 32-row tiles whose waves share out the keys
-    pl.by_keys = !pl.latent && rows <= (int64_t)32 * m.B;
+    pl.by_keys = !pl.latent && pieces && rows <= (int64_t)32 * m.B;
     pl.rows = pl.by_keys ? 32 : 128;
     // row tiles, at most: a tile holds rows of one sequence
     const int64_t most = rows / pl.rows + m.B, each = (int64_t)m.T * ((m.G + pl.rows - 1) / pl.rows);

@@ -99,13 +99,19 @@ int check_batch(const dcpa_attn_args* a, Batch& m) {
     return DCP_OK;
 }
 
+AttnPlan plan_of(const dcpa_attn_args* a, const Batch& m) {
+    const bool pieces = a->cache_dtype != DCP_FP8_E4M3 ||
+                        (multiples({a->Dk, a->Dv, a->k_P, a->k_S, a->k_H}, 16) &&
+                         (!a->v || multiples({a->v_P, a->v_S, a->v_H}, 16)));
+    return plan_attn(m, (int)a->Dk, (int)a->Dv, pieces);
+}
+
 // Pointers and alignment of what both calls read.
 int check_inputs(const dcpa_attn_args* a) {
     if (!a->q || !a->cu_q || !a->kv_len || (a->max_pages > 0 && !a->block_table) || (a->num_pages > 0 && !a->k) ||
         (a->causal && a->N > 1 && !a->seq_len))
         return DCP_ERR_NULL;
-    const int ec = esize_of(a->cache_dtype);
-    if (!aligned(a->q, 16) || !multiples({a->q_T, a->q_H}, 8) || !aligned(a->k, 8 * ec) ||
+    if (!aligned(a->q, 16) || !multiples({a->q_T, a->q_H}, 8) || !aligned(a->k, 16) ||
         !multiples({a->k_P, a->k_S, a->k_H}, 8) || !aligned(a->block_table, 4) || !aligned(a->cu_q, 4) ||
         !aligned(a->kv_len, 4) || !aligned(a->seq_len, 4) || !aligned(a->lse, 4))
         return DCP_ERR_ALIGN;
@@ -122,7 +128,7 @@ int check_attn(const dcpa_attn_args* a, Batch& m) {
                  esize_of(a->cache_dtype)) ||
         !span_ok({{a->T, a->o_T}, {a->Hq, a->o_H}, {a->Dv, 1}}, 2))
         return DCP_ERR_STRIDE;
-    const AttnPlan pl = plan_attn(m, (int)a->Dk, (int)a->Dv);
+    const AttnPlan pl = plan_of(a, m);
     if ((int64_t)pl.units * m.Hkv > kMaxGrid || (pl.slots > 0 && a->T * a->Hq / 4 >= kMaxGrid)) return DCP_ERR_SHAPE;
     return DCP_OK;
 }
@@ -153,7 +159,7 @@ int64_t dcpa_paged_attn_workspace(const dcpa_attn_args* a) {
     Batch m;
     if (int st = check_attn(a, m)) return st;
     if (a->B == 0 || a->T == 0) return 0;
-    return plan_attn(m, (int)a->Dk, (int)a->Dv).ws_bytes;
+    return plan_of(a, m).ws_bytes;
 }
 
 int dcpa_paged_attn(const dcpa_attn_args* a, void* stream) {
@@ -164,10 +170,10 @@ int dcpa_paged_attn(const dcpa_attn_args* a, void* stream) {
     if (int st = check_inputs(a)) return st;
     if (!a->out) return DCP_ERR_NULL;
     const int ec = esize_of(a->cache_dtype);
-    if (!aligned(a->v, 8 * ec) || (a->v && !multiples({a->v_P, a->v_S, a->v_H}, 8)) || !aligned(a->out, 4) ||
+    if (!aligned(a->v, 16) || (a->v && !multiples({a->v_P, a->v_S, a->v_H}, 8)) || !aligned(a->out, 4) ||
         !multiples({a->o_T, a->o_H}, 2))
         return DCP_ERR_ALIGN;
-    const AttnPlan pl = plan_attn(k.m, (int)a->Dk, (int)a->Dv);
+    const AttnPlan pl = plan_of(a, k.m);
     if (pl.ws_bytes > 0 && (!a->workspace || a->workspace_bytes < pl.ws_bytes || !aligned(a->workspace, 16)))
         return DCPA_ERR_WORKSPACE;
     k.q = (const char*)a->q;

@@ -119,6 +119,13 @@ __device__ __forceinline__ void meet() {
     asm volatile("" ::: "memory");
 }
 
+// Sixteen 8-byte pieces of 16 lanes are eight rows of 16 bytes; lane i of the 16
+// gets column i of the eight rows.
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u32x2 lds_read_tr8(uint32_t a) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((DCPA_LDS i32x2*)(uintptr_t)a));
+}
+
 // What absent keys and columns are loaded from: a row of the widest cache.
 __device__ __attribute__((aligned(16))) const uint32_t kZeros[288] = {};
 

@@ -178,8 +178,8 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
         const uint32_t buf = buffer(t);
 #pragma unroll
         for (int i = 0; i < 5; ++i) {
-            const int ch = i * 64 + lane;
-            if (ch >= 8 * 36) continue;
+            // (all lanes take part in the exchange; the last round's upper half repeats a piece)
+            const int ch = min(i * 64 + lane, 8 * 36 - 1);
             const int row = ch / 36, c = ch % 36, in_tile = wave * 8 + row;
             u32x4 x = lds_read16(raw(t) + (uint32_t)(ch * 16));
             // rows that are only 8-byte aligned, and the half piece at a row's end
@@ -350,19 +350,7 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
             DCPA_PIN;
         });
         out_claim();
-        if (!full) {
-            // (a masked value that is not finite: see attend())
-            uint32_t hit = 0;
-#pragma unroll 1
-            for (int i = lane; i < KT * (DV / 8); i += 64) {
-                const u32x4 x = lds_read16(buf + (uint32_t)(i * 16));
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    hit |= (x[k] & Mat<E>::kExp & 0xffffu) == (Mat<E>::kExp & 0xffffu) ||
-                           (x[k] & Mat<E>::kExp & 0xffff0000u) == (Mat<E>::kExp & 0xffff0000u);
-            }
-            odd |= __ballot(hit != 0) != 0;
-        }
+        if (!full) odd |= odd_values<E, false>(buf, MAIN);
         if constexpr (NEXT) {
             settle(n);
             s = n;

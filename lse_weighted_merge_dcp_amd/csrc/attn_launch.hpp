@@ -58,7 +58,8 @@ struct AttnPlan {
     int32_t slots, tiles, units;
     int64_t ws_bytes;
 };
-AttnPlan plan_attn(const Batch& m, int Dk, int Dv);
+// pieces: the cache's rows and strides are whole pieces of 16 bytes.
+AttnPlan plan_attn(const Batch& m, int Dk, int Dv, bool pieces);
 hipError_t launch_attn(const AttnArgs& a, const AttnPlan& pl, bool bf16, bool kv8, hipStream_t stream);
 
 hipError_t launch_latent(const AttnArgs& a, dim3 grid, bool bf16, bool kv8, hipStream_t stream);

@@ -47,34 +47,60 @@ __device__ __forceinline__ void load_query(u32x4 (&q)[N], const char* row, int D
     }
 }
 
-// One tile of KT keys.  kbase / vbase: LDS addresses of the key and value
-// rows (KROW, VROW bytes apart).  `there`: bit j set where key j of the tile
-// exists.  vis[rb]: how many keys from the tile's first on the lane's row sees
-// (any value; compared with the key's place).  full: no masking needed.
-template <typename E, int DK, int DV, int RB, int KT, int KROW, int VROW>
-__device__ __forceinline__ bool attend(Rows<DK, DV, RB>& w, uint32_t kbase, uint32_t vbase, uint64_t there,
-                                       const int (&vis)[RB], bool full, float c) {
-    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
-    constexpr int NB = KT / 32;
-    f32x16 s[RB][NB];
+// Fragment addresses within a tile of 16-bit rows (see swz()).
+template <int KROW> struct KeyPlace {      // key r of 32, columns 16 st + 8 h .. + 7
+    uint32_t at[4];
+    __device__ __forceinline__ void set(uint32_t base, int r, int h) {
 #pragma unroll
-    for (int kb = 0; kb < NB; ++kb) {
+        for (int j = 0; j < 4; ++j) at[j] = base + (uint32_t)(r * KROW + ((2 * j + h) ^ swz(r)) * 16);
+    }
+    __device__ __forceinline__ u32x4 read(int st) const { return lds_read16(at[st & 3] + (uint32_t)((st >> 2) * 128)); }
+};
+template <int VROW> struct ValuePlace {    // 32 columns of block cb, the keys {0..3, 8..11} + 4 h of 16 ks ..
+    uint32_t at[2];
+    __device__ __forceinline__ void set(uint32_t base, int lane) {
+        // 16 lanes read four rows of 32 bytes, transposed
+        const int h = lane >> 5, g = (lane >> 4) & 1, li = lane & 15, row = 4 * h + li / 4;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            at[j] = base + (uint32_t)(row * VROW + (li & 1) * 8 + ((4 * j + 2 * g + (li & 3) / 2) ^ swz(row)) * 16);
+    }
+    __device__ __forceinline__ u32x4 read(int cb, int ks) const {
+        const uint32_t a = at[cb & 1] + (uint32_t)((cb >> 1) * 128 + ks * 16 * VROW);
+        const u32x2 x = lds_read_tr(a), y = lds_read_tr(a + 8 * VROW);
+        return u32x4{x.x, x.y, y.x, y.y};
+    }
+};
+
+// Scores of KT keys.
+template <typename E, int DK, int RB, int KT, int KROW>
+__device__ __forceinline__ void scores(f32x16 (&s)[RB][KT / 32], const u32x4 (&q)[RB][DK / 16], uint32_t kbase) {
+    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+#pragma unroll
+    for (int kb = 0; kb < KT / 32; ++kb) {
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[rb][kb][i] = 0.0f;
-        const uint32_t krow = kbase + (uint32_t)((kb * 32 + r) * KROW);
-        uint32_t at[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) at[j] = krow + (uint32_t)(((2 * j + h) ^ swz(r)) * 16);
+        KeyPlace<KROW> place;
+        place.set(kbase + (uint32_t)(kb * 32 * KROW), r, h);
 #pragma unroll
         for (int st = 0; st < DK / 16; ++st) {
-            const u32x4 a = lds_read16(at[st & 3] + (uint32_t)((st >> 2) * 128));
+            const u32x4 a = place.read(st);
 #pragma unroll
-            for (int rb = 0; rb < RB; ++rb) s[rb][kb] = Mat<E>::mma(a, w.q[rb][st], s[rb][kb]);
+            for (int rb = 0; rb < RB; ++rb) s[rb][kb] = Mat<E>::mma(a, q[rb][st], s[rb][kb]);
         }
     }
-    uint32_t p[RB][NB][8];
+}
+
+// Weights of a tile's scores, as B operands; updates maximum, sum and, where the
+// maximum moved, the outputs.  `there`: bit j set where key j of the tile
+// exists.  vis[rb]: how many keys from the tile's first on the lane's row sees
+// (any value; compared with the key's place).  full: no masking needed.
+template <typename E, int DK, int DV, int RB, int NB>
+__device__ __forceinline__ void weights(Rows<DK, DV, RB>& w, f32x16 (&s)[RB][NB], uint32_t (&p)[RB][NB][8],
+                                        uint64_t there, const int (&vis)[RB], bool full, float c) {
+    const int h = (threadIdx.x & 63) >> 5;
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
         if (!full) {
@@ -118,17 +144,11 @@ __device__ __forceinline__ bool attend(Rows<DK, DV, RB>& w, uint32_t kbase, uint
             }
         w.l[rb] += sum;
     }
-    // value fragments: 16 lanes read four rows of 32 bytes, transposed
-    const int g = (lane >> 4) & 1, li = lane & 15;
-    const uint32_t vrow = vbase + (uint32_t)((4 * h + li / 4) * VROW) + (uint32_t)((li & 1) * 8);
-    uint32_t va[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) va[j] = vrow + (uint32_t)(((4 * j + 2 * g + (li & 3) / 2) ^ swz(4 * h + li / 4)) * 16);
-    auto fragment = [&](int cb, int ks) {
-        const uint32_t a = va[cb & 1] + (uint32_t)((cb >> 1) * 128 + ks * 16 * VROW);
-        const u32x2 x = lds_read_tr(a), y = lds_read_tr(a + 8 * VROW);
-        return u32x4{x.x, x.y, y.x, y.y};
-    };
+}
+
+// Outputs += weights x values of KT keys; `fragment` as ValuePlace::read.
+template <typename E, int DK, int DV, int RB, int KT, typename F>
+__device__ __forceinline__ void outputs(Rows<DK, DV, RB>& w, const uint32_t (&p)[RB][KT / 32][8], F&& fragment) {
 #pragma unroll
     for (int cb = 0; cb < DV / 32; ++cb)
 #pragma unroll
@@ -140,15 +160,28 @@ __device__ __forceinline__ bool attend(Rows<DK, DV, RB>& w, uint32_t kbase, uint
                 w.o[rb][cb] = Mat<E>::mma(a, u32x4{pp[0], pp[1], pp[2], pp[3]}, w.o[rb][cb]);
             }
         }
-    if (full) return false;
+}
+
+// A value that one row sees and another does not must not reach the other as
+// 0 * infinity, which a matrix product cannot avoid.  Where a masked tile
+// holds anything not finite the wave's rows are computed again by slow_rows().
+// Whether the `bytes` bytes at `base` hold such a value; CODE: 8-bit NaN codes.
+template <typename E, bool CODE>
+__device__ __forceinline__ bool odd_values(uint32_t base, int bytes) {
     uint32_t hit = 0;
 #pragma unroll 1
-    for (int i = lane; i < KT * (DV / 8); i += 64) {
-        const u32x4 x = lds_read16(vbase + (uint32_t)((i / (DV / 8)) * VROW + (i % (DV / 8)) * 16));
+    for (int i = (threadIdx.x & 63) * 16; i < bytes; i += 1024) {
+        const u32x4 x = lds_read16(base + (uint32_t)i);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            hit |= (x[k] & Mat<E>::kExp & 0xffffu) == (Mat<E>::kExp & 0xffffu) ||
-                   (x[k] & Mat<E>::kExp & 0xffff0000u) == (Mat<E>::kExp & 0xffff0000u);
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (CODE) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) hit |= (x[k] >> (8 * j) & 0x7fu) == 0x7fu;
+            } else {
+                hit |= (x[k] & Mat<E>::kExp & 0xffffu) == (Mat<E>::kExp & 0xffffu) ||
+                       (x[k] & Mat<E>::kExp & 0xffff0000u) == (Mat<E>::kExp & 0xffff0000u);
+            }
+        }
     }
     return __ballot(hit != 0) != 0;
 }

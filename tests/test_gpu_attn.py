@@ -98,6 +98,17 @@ def test_8_bit_cache(dev, i, dtype):
     check(p, *call(p, dev))
 
 
+@pytest.mark.parametrize("Dk,Dv,Hkv", [(72, 72, 2), (64, 40, 1), (136, 128, 3), (24, 24, 1)])
+def test_8_bit_rows_of_half_pieces(dev, Dk, Dv, Hkv):
+    """8-bit rows that are not whole pieces of 16 bytes, in every kernel."""
+    p = Problem([(1, 70), (1, 33)], 4 * Hkv, Hkv, Dk, Dv, cache=F8, seed=56)
+    check(p, *call(p, dev))
+    p = Problem([(40, 70), (1, 33)], 2 * Hkv, Hkv, Dk, Dv, cache=F8, dtype=HF, seed=57)
+    check(p, *call(p, dev))
+    p = Problem([(2, 70), (1, 33)], 5, 1, 264 + Dk, Dv, cache=F8, shared=True, seed=58)
+    check(p, *call(p, dev))
+
+
 @pytest.mark.parametrize("N,rank,inter", [(2, 0, 1), (2, 1, 1), (3, 2, 4), (8, 7, 16), (16, 15, 1), (4, 1, 64)])
 @pytest.mark.parametrize("form", ["decode", "chunk", "latent"])
 def test_ranks(dev, N, rank, inter, form):
