@@ -360,6 +360,7 @@ int dcpa_cache_evict(const dcpa_evict_args* a, void* stream) {
     k.wide = rows(16);
     k.fpage = dcp::make_fastdiv((uint32_t)a->page_size);
     k.fHkv = dcp::make_fastdiv((uint32_t)a->Hkv);
+    k.fbudget = dcp::make_fastdiv((uint32_t)a->budget);
     return status(launch_evict(k, (hipStream_t)stream));
 }
 

@@ -119,7 +119,7 @@ struct EvictArgs {
     int32_t B, Hkv, k_bytes, v_bytes, pages, page_size, max_keys;
     int32_t budget, sink, recent;
     bool wide;               // rows and strides are 16-byte aligned (else 8)
-    FastDiv fpage, fHkv;
+    FastDiv fpage, fHkv, fbudget;
 };
 hipError_t launch_evict(const EvictArgs& a, hipStream_t stream);
 

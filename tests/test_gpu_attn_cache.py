@@ -326,6 +326,23 @@ def test_evict_ties_and_special_weights(dev):
     check_evict(dev, table, dst, kv, k, v, torch.zeros_like(mass), 300, 3, 5)
 
 
+def test_evict_long(dev):
+    """More keys than a workgroup holds in registers: 70000, with ties across the turns."""
+    L, budget, page = 70000, 40000, 64
+    table, dst, kv, k, v, mass = evict_problem([L], budget, 1, 8, 0, BF, page, 8)
+    mass = torch.randint(0, 50, mass.shape, generator=torch.Generator().manual_seed(1)).float()
+    md, kd = mass.to(dev), k.to(dev)
+    new, kept = attn.dcp_cache_evict(md, kd, None, table.to(dev), kv.to(dev), dst.to(dev), budget, n_sink=3, n_recent=9)
+    j = torch.arange(L)
+    w = mass[table[0].long()[j // page], j % page, 0].double()
+    w[:3] = w[L - 9:] = math.inf
+    want = torch.argsort(-w, stable=True)[:budget].sort().values
+    assert int(new[0]) == budget and torch.equal(kept[0, 0].cpu().long(), want)
+    i = torch.arange(budget)
+    got = kd.cpu()[dst[0].long()[i // page], i % page, 0]
+    assert torch.equal(got.view(torch.int16), k[table[0].long()[want // page], want % page, 0].view(torch.int16))
+
+
 def test_evict_bad_pages(dev):
     table, dst, kv, k, v, mass = evict_problem([300, 200], 64, 2, 16, 16, BF, 16, 7)
     table[0, 2], table[0, 3], table[1, 0] = -1, mass.shape[0], 1 << 30
