@@ -99,11 +99,14 @@ int check_batch(const dcpa_attn_args* a, Batch& m) {
     return DCP_OK;
 }
 
+// Whether key rows are whole pieces of 16 bytes.
+bool key_pieces(const dcpa_attn_args* a) {
+    return a->cache_dtype != DCP_FP8_E4M3 || multiples({a->Dk, a->k_P, a->k_S, a->k_H}, 16);
+}
 AttnPlan plan_of(const dcpa_attn_args* a, const Batch& m) {
-    const bool pieces = a->cache_dtype != DCP_FP8_E4M3 ||
-                        (multiples({a->Dk, a->Dv, a->k_P, a->k_S, a->k_H}, 16) &&
-                         (!a->v || multiples({a->v_P, a->v_S, a->v_H}, 16)));
-    return plan_attn(m, (int)a->Dk, (int)a->Dv, pieces);
+    const bool values = a->cache_dtype != DCP_FP8_E4M3 ||
+                        (a->Dv % 16 == 0 && (!a->v || multiples({a->v_P, a->v_S, a->v_H}, 16)));
+    return plan_attn(m, (int)a->Dk, (int)a->Dv, key_pieces(a) && values);
 }
 
 // Pointers and alignment of what both calls read.
@@ -205,7 +208,7 @@ int64_t dcpa_attn_mass_workspace(const dcpa_attn_args* a) {
     Batch m;
     if (int st = check_batch(a, m)) return st;
     if (a->B == 0 || a->T == 0) return 0;
-    return plan_mass(m).ws_bytes;
+    return plan_mass(m, (int)a->Dk, key_pieces(a)).ws_bytes;
 }
 
 int dcpa_attn_mass(const dcpa_attn_args* a, float* mass, int64_t m_P, int64_t m_S, int64_t m_H, void* stream) {
@@ -218,7 +221,7 @@ int dcpa_attn_mass(const dcpa_attn_args* a, float* mass, int64_t m_P, int64_t m_
     if (int st = check_inputs(a)) return st;
     if (!a->lse || (a->num_pages > 0 && !mass)) return DCP_ERR_NULL;
     if (!aligned(mass, 4)) return DCP_ERR_ALIGN;
-    const MassPlan pl = plan_mass(k.m);
+    const MassPlan pl = plan_mass(k.m, (int)a->Dk, key_pieces(a));
     if (pl.ws_bytes > 0 && (!a->workspace || a->workspace_bytes < pl.ws_bytes || !aligned(a->workspace, 16)))
         return DCPA_ERR_WORKSPACE;
     const int ec = esize_of(a->cache_dtype);
@@ -230,13 +233,13 @@ int dcpa_attn_mass(const dcpa_attn_args* a, float* mass, int64_t m_P, int64_t m_
     k.l_T = a->l_T; k.l_H = a->l_H;
     k.mass = mass;
     k.m_P = m_P; k.m_S = m_S; k.m_H = m_H;
-    k.ws = (float*)a->workspace;
+    k.ws = pl.ws_bytes > 0 ? (float*)a->workspace : nullptr;
     k.Dk = (int32_t)a->Dk;
-    k.target = pl.target;
+    k.slots = pl.slots;
     k.units = pl.units;
     k.c = (float)(a->scale * a->k_scale * 1.4426950408889634);
     k.lmul = a->lse_base == DCP_LSE_BASE_E ? kLog2e : 1.0f;
-    return status(launch_mass(k, a->dtype == DCP_BF16, a->cache_dtype == DCP_FP8_E4M3, (hipStream_t)stream));
+    return status(launch_mass(k, pl.few, a->dtype == DCP_BF16, a->cache_dtype == DCP_FP8_E4M3, (hipStream_t)stream));
 }
 
 int dcpa_qk_norm_rope_append(const dcpa_rope_args* a, void* stream) {

@@ -76,17 +76,18 @@ struct MassArgs {
     int64_t m_P, m_S, m_H;
     float* ws;
     int32_t Dk;
-    int32_t target;          // workgroups of one key head aimed at
+    int32_t slots;           // workgroups of one key head aimed at (0: one to a sequence)
     int32_t units;           // workgroups of one key head launched
     float c;
     float lmul;              // log2(e), or 1 for base 2
 };
 struct MassPlan {
-    int32_t target, units;
+    bool few;                // few rows to a sequence
+    int32_t slots, units;
     int64_t ws_bytes;
 };
-MassPlan plan_mass(const Batch& m);
-hipError_t launch_mass(const MassArgs& a, bool bf16, bool kv8, hipStream_t stream);
+MassPlan plan_mass(const Batch& m, int Dk, bool pieces);
+hipError_t launch_mass(const MassArgs& a, bool few, bool bf16, bool kv8, hipStream_t stream);
 
 struct RopeArgs {
     const char *q, *k, *v;

@@ -2,65 +2,89 @@
 //
 // For one key head and a key j, the sum over the rows that see it of
 // 2^(s_j c - g), g the row's merged log-sum-exp in powers of two.  Scores are
-// computed transposed as in attn_tile.hpp: a wave keeps the fragments of 32
-// keys in registers (A operand) and walks over the query rows (B operand, 32
-// at a time); each lane adds up the weights of its own query row, and one sum
-// over the 32 lanes at the end gives the keys' totals.  No two waves write the
-// same key, so there are no atomics; where rows are many and keys few, the
-// rows are split and mass_join adds the parts in order.
+// computed transposed as in attn_tile.hpp: a wave holds the fragments of its
+// keys in registers (A operand) and walks over the query rows, 32 at a time out
+// of LDS (B operand); each lane adds up the weights of its own query rows, and
+// one sum over the 32 lanes at the end gives the keys' totals.  No two waves
+// write the same key, so there are no atomics.
+//
+// Few rows (decode, mass_few) are bound by the bytes of the keys, which come
+// straight into LDS, the next tile of 32 while the present one is multiplied
+// (loaded into registers as fragments, 32 rows of 32 bytes to an instruction,
+// the same bytes took twice as long).  Many rows (mass_rows) are
+// bound by the exponentials (16 clocks for 64 scores, and as much again for
+// masks, scaling and sums, against 16 of matrix instructions at 128 columns):
+// 64 keys to a wave, so that a fragment of queries is read from LDS once for two
+// products.  Where the batch has fewer key steps than the chip has room for, the
+// rows are split, and mass_join adds the parts in order.
 #include "attn_device.hpp"
 
 namespace dcpa {
 
 namespace {
 
-constexpr int kKeys = 128;     // keys of a workgroup's step: 32 to a wave
+// A batch's layout over workgroups: each takes the keys [split chunk, (split +
+// 1) chunk) of a sequence, `keys` at a time, against part `part` of its rows.
+// Every wave works it out from the lengths on the device, as find_unit().  Rows
+// are only split where there is a workspace for the parts.
+struct Share {
+    Seq s;
+    int b, k0, k1, slot, part, parts;
+    bool ok;
+};
 
-// Key steps of all sequences, and the parts the rows are cut into so that
-// steps * parts comes near the target.
-__device__ __forceinline__ int row_parts(const Batch& m, int target) {
-    if (target <= 0) return 1;
+constexpr int kOneTile = 0x3fffffff;      // rows of a tile that holds any sequence
+
+template <int KEYS>
+__device__ __forceinline__ void share_out(const Batch& m, int slots, bool split_rows, int& chunk, int& parts) {
     const int lane = threadIdx.x & 63;
     int64_t steps = 0;
     int most = 0;
     for (int b0 = 0; b0 < m.B; b0 += 64)
         if (b0 + lane < m.B) {
             const Seq s = load_seq(m, b0 + lane);
-            if (s.n > 0) steps += (s.kv + kKeys - 1) / kKeys;
+            if (s.n > 0) steps += max(1, (s.kv + KEYS - 1) / KEYS);
             most = max(most, s.n);
         }
     steps = sum_wave(steps);
+    parts = 1;
+    chunk = KEYS;
+    if (steps >= slots) {
+        chunk = key_chunk<KEYS>(m, kOneTile, slots);
+        return;
+    }
+    if (!split_rows) return;
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) most = max(most, __shfl_xor(most, d, 64));
-    const int64_t tiles = ((int64_t)most * m.G + 31) / 32;
-    return (int)max((int64_t)1, min(min((int64_t)target / max((int64_t)1, steps), tiles), (int64_t)64));
+    // (at least four row tiles to a part)
+    const int64_t tiles = ((int64_t)most * m.G + 127) / 128;
+    parts = (int)max((int64_t)1, min(slots / max((int64_t)1, steps), tiles));
 }
 
-struct Step {
-    Seq s;
-    int b, step, slot;
-    bool ok;
-};
-__device__ __forceinline__ Step find_step(const Batch& m, int id) {
-    Step u;
+template <int KEYS> __device__ __forceinline__ Share find_share(const Batch& m, int slots, bool split_rows, int id) {
+    Share u;
     u.ok = false;
+    int chunk;
+    share_out<KEYS>(m, slots, split_rows, chunk, u.parts);
+    u.part = id % u.parts;
+    id /= u.parts;
+    u.slot = id;
     const int lane = threadIdx.x & 63;
     int base = 0;
     for (int b0 = 0; b0 < m.B; b0 += 64) {
-        int n = 0;
-        if (b0 + lane < m.B) {
-            const Seq s = load_seq(m, b0 + lane);
-            n = s.n > 0 ? (s.kv + kKeys - 1) / kKeys : 0;
-        }
+        int n = 0, kv;
+        tiles_of(m, b0 + lane, kOneTile, n, kv);
+        if (n > 0) n = max(1, (kv + chunk - 1) / chunk);
         const int incl = base + scan_incl(n, lane);
         const uint64_t past = __ballot(incl > id);
         if (past != 0) {
             const int at = __builtin_ctzll(past);
             u.b = b0 + at;
             u.s = load_seq(m, u.b);
-            u.step = id - (__builtin_amdgcn_readlane(incl, at) - __builtin_amdgcn_readlane(n, at));
-            u.slot = id;
-            u.ok = u.step >= 0;
+            const int split = id - (__builtin_amdgcn_readlane(incl, at) - __builtin_amdgcn_readlane(n, at));
+            u.k0 = split * chunk;
+            u.k1 = (int)min((int64_t)u.s.kv, (int64_t)u.k0 + chunk);
+            u.ok = split >= 0 && u.k0 < u.k1 && u.s.n > 0;
             return u;
         }
         base = __builtin_amdgcn_readlane(incl, 63);
@@ -75,134 +99,390 @@ __device__ __forceinline__ float* mass_at(const MassArgs& p, int b, int hk, int 
     return p.mass + (int64_t)id * p.m_P + (int64_t)(key - (int)(page * p.m.fpage.d)) * p.m_S + (int64_t)hk * p.m_H;
 }
 
-template <typename E, bool KV8, int DK>
-__global__ __launch_bounds__(256, 2) void mass_kernel(MassArgs p) {
+// KW keys to a wave.
+template <typename E, bool KV8, int DK, int KW>
+__global__ __launch_bounds__(256, 2) void mass_rows(MassArgs p) {
+    constexpr int KEYS = 4 * KW, NB = KW / 32, ST = DK / 16, KC = DK / 8, QROW = KC * 16, QB = 32 * QROW, NQ = 32 * KC / 256 + (32 * KC % 256 != 0);
+    constexpr int PAD = NQ * 256 * 16;         // whole rounds of the workgroup
+    __shared__ __attribute__((aligned(1024))) char qtile[2][PAD];
+    static_assert(QB <= PAD, "a tile of queries fits");
+    const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv);
+    const Share u = find_share<KEYS>(p.m, p.slots, p.ws != nullptr, (int)(blockIdx.x / (uint32_t)p.m.Hkv));
+    if (!u.ok) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = (int)dcp::wave_id(), r = lane & 31, h = lane >> 5;
-    const int parts = row_parts(p.m, p.target);
-    const uint32_t per = (uint32_t)(p.m.Hkv * parts);
-    // a fixed grid walks over the steps
-    for (uint32_t id = blockIdx.x;; id += gridDim.x) {
-        const Step u = find_step(p.m, (int)(id / per));
-        if (!u.ok) return;
-        const int hk = (int)(id % (uint32_t)p.m.Hkv), part = (int)(id / (uint32_t)p.m.Hkv % (uint32_t)parts);
-        const int key0 = u.step * kKeys + wave * 32, key = key0 + r;
-        // the wave's keys as A operand
-        u32x4 kf[DK / 16];
-        bool have = false;
-        const char* kr = nullptr;
-        if (key < u.s.kv) {
-            const uint32_t page = fdiv((uint32_t)key, p.m.fpage);
-            const int pid = p.m.table[(int64_t)u.b * p.m.t_B + page];
-            have = (uint32_t)pid < (uint32_t)p.m.pages;
-            if (have) kr = p.k + (int64_t)pid * p.k_P + (int64_t)(key - (int)(page * p.m.fpage.d)) * p.k_S + (int64_t)hk * p.k_H;
-        }
+    const int nrows = u.s.n * p.m.G, tiles = (nrows + 31) / 32, per_part = (tiles + u.parts - 1) / u.parts;
+    const int first_tile = u.part * per_part, end_tile = min(tiles, first_tile + per_part);
+    const int32_t* table = p.m.table + (int64_t)u.b * p.m.t_B;
+
+    // the wave's keys from k0 on as A operands; absent ones are zeros (and masked by their place)
+    auto load_keys = [&](int k0, u32x4 (&kf)[NB][ST], uint32_t (&there)[NB]) {
 #pragma unroll
-        for (int s = 0; s < DK / 16; ++s) {
-            const int c = 2 * s + h;
-            kf[s] = u32x4{0, 0, 0, 0};
-            if (have && c * 8 < p.Dk) {
-                if constexpr (KV8) kf[s] = widen8<E>(*(const u32x2*)(kr + c * 8));
-                else kf[s] = *(const u32x4*)(kr + c * 16);
+        for (int kb = 0; kb < NB; ++kb) {
+            const int key = k0 + wave * KW + kb * 32 + r;
+            const uint32_t page = fdiv((uint32_t)key, p.m.fpage);
+            const int id = key < u.k1 ? table[page] : -1;
+            const bool have = (uint32_t)id < (uint32_t)p.m.pages;
+            there[kb] = (uint32_t)__ballot(h == 0 && have);
+            const uint64_t row = have ? (uint64_t)(p.k + (int64_t)id * p.k_P +
+                                                   (int64_t)(key - (int)(page * p.m.fpage.d)) * p.k_S + (int64_t)hk * p.k_H)
+                                      : (uint64_t)kZeros;
+#pragma unroll
+            for (int s = 0; s < ST; ++s) {
+                const int c = 2 * s + h;
+                const uint64_t at = at_or_zeros(c * 8 < p.Dk, row + (uint64_t)(c * (KV8 ? 8 : 16)));
+                if constexpr (KV8) {
+                    const u32x2 x = *(const u32x2*)at;
+                    kf[kb][s].x = x.x;
+                    kf[kb][s].y = x.y;
+                } else {
+                    kf[kb][s] = *(const u32x4*)at;
+                }
             }
         }
+    };
+    const uint32_t lds0 = lds_addr(&qtile[0][0]);
+    auto row_place = [&](int row, int& token, int& head) {
+        row = min(row, nrows - 1);
+        token = (int)fdiv((uint32_t)row, p.m.fG);
+        head = hk * p.m.G + row - token * p.m.G;
+    };
+    // row tile t into buffer b
+    auto fetch = [&](int t, int b) {
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            const int ch = i * 256 + tid, row = min(ch / KC, 31), c = (ch % KC) ^ swz(row);
+            int token, head;
+            row_place(t * 32 + row, token, head);
+            const uint64_t at = (uint64_t)(p.q + (int64_t)(u.s.first + token) * p.q_T + (int64_t)head * p.q_H) + (uint64_t)(c * 16);
+            dma16((const char*)at_or_zeros(c * 8 < p.Dk, at),
+                  __builtin_amdgcn_readfirstlane(lds0 + (uint32_t)(b * PAD + (i * 256 + wave * 64) * 16)));
+        }
+    };
+    // what the lane's row of tile t sees, and its log-sum-exp in powers of two
+    auto row_of = [&](int t, int& vis, float& g) {
+        int token, head;
+        row_place(t * 32 + r, token, head);
+        vis = t * 32 + r < nrows ? visible(p.m, u.s, token) : 0;
+        g = p.lse[(int64_t)(u.s.first + token) * p.l_T + (int64_t)head * p.l_H];
+    };
+
+    // rows that see none of the range come first: skip their tiles
+    int lo = first_tile, hi = end_tile;
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2, last = min(mid * 32 + 31, nrows - 1);
+        if (visible(p.m, u.s, (int)fdiv((uint32_t)last, p.m.fG)) > u.k0) hi = mid;
+        else lo = mid + 1;
+    }
+    const int begin = lo;
+    const bool single = end_tile - begin <= 1;     // one tile of rows for all the keys: it stays in LDS
+    u32x4 kf[NB][ST];
+    uint32_t there[NB];
+    if (begin < end_tile) {
+        fetch(begin, 0);
+        load_keys(u.k0, kf, there);
+    }
+    int buf = 0, vis_next = 0;
+    float g_next = 0.0f;
+    if (begin < end_tile) row_of(begin, vis_next, g_next);
+#pragma unroll 1
+    for (int k0 = u.k0; k0 < u.k1; k0 += KEYS) {
+        float acc[NB][16];
+#pragma unroll
+        for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[kb][i] = 0.0f;
+        if constexpr (KV8) {
+#pragma unroll
+            for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+                for (int s = 0; s < ST; ++s) kf[kb][s] = widen8<E>(u32x2{kf[kb][s].x, kf[kb][s].y});
+        }
+#pragma unroll 1
+        for (int t = begin; t < end_tile; ++t) {
+            if (!single || k0 == u.k0) {
+                dma_wait();
+                meet();       // tile t is there, and the other buffer is free
+            }
+            const int vis = vis_next;
+            // (a row that saw nothing anywhere gives nothing)
+            const float g = g_next == -INFINITY ? INFINITY : g_next * p.lmul;
+            const int now = buf;
+            if (!single) {
+                const bool wrap = t + 1 == end_tile, more = !wrap || k0 + KEYS < u.k1;
+                if (more) {
+                    row_of(wrap ? begin : t + 1, vis_next, g_next);
+                    fetch(wrap ? begin : t + 1, buf ^ 1);
+                }
+                buf ^= 1;
+            }
+            const int key0 = k0 + wave * KW;
+            // rows are in the order of their tokens; those behind the last see nothing
+            if (__builtin_amdgcn_readlane(vis, min(31, nrows - 1 - t * 32)) <= key0) continue;
+            const bool all = t * 32 + 31 < nrows && __builtin_amdgcn_readlane(vis, 0) >= key0 + KW;
+            f32x16 s[NB];
+#pragma unroll
+            for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[kb][i] = 0.0f;
+            const uint32_t qrow = lds0 + (uint32_t)(now * PAD + r * QROW);
+#pragma unroll
+            for (int k = 0; k < ST; ++k) {
+                const u32x4 b = lds_read16(qrow + (uint32_t)(((2 * k + h) ^ swz(r)) * 16));
+#pragma unroll
+                for (int kb = 0; kb < NB; ++kb) s[kb] = Mat<E>::mma(kf[kb][k], b, s[kb]);
+            }
+#pragma unroll
+            for (int kb = 0; kb < NB; ++kb) {
+                if (all) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[kb][i] += exp2_fast(__builtin_fmaf(s[kb][i], p.c, -g));
+                } else {
+                    const int lim = vis - key0 - kb * 32 - 4 * h;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float x = exp2_fast(__builtin_fmaf(s[kb][i], p.c, -g));
+                        acc[kb][i] += 8 * (i / 4) + i % 4 < lim ? x : 0.0f;
+                    }
+                }
+            }
+        }
+        // totals over the 32 query lanes; lane i of each half takes register i
+#pragma unroll
+        for (int kb = 0; kb < NB; ++kb) {
+            float mine = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float x = acc[kb][i];
+                x += dcp::dpp_f<0x128>(x);
+                x += dcp::dpp_f<0x124>(x);
+                x += dcp::dpp_f<0x122>(x);
+                x += dcp::dpp_f<0x121>(x);
+                mine = (lane & 15) == i ? x : mine;
+            }
+            mine += __shfl_xor(mine, 16, 64);
+            if (r < 16) {
+                const int place = kb * 32 + 8 * (r / 4) + r % 4 + 4 * h, k = k0 + wave * KW + place;
+                if (u.parts > 1) {
+                    p.ws[(((int64_t)u.slot * p.m.Hkv + hk) * u.parts + u.part) * KEYS + wave * KW + place] = mine;
+                } else if (k < u.k1 && (there[kb] >> (place & 31) & 1u) != 0) {
+                    *mass_at(p, u.b, hk, k) += mine;
+                }
+            }
+        }
+        if (k0 + KEYS < u.k1 && begin < end_tile) load_keys(k0 + KEYS, kf, there);
+    }
+}
+
+// Few rows: a wave takes a quarter of the range, tile after tile (see attn_keys).
+template <typename E, bool KV8, int DK>
+__global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void mass_few(MassArgs p) {
+    constexpr int KT = 32, ES = KV8 ? 1 : 2, KROW = DK * ES, KB = KT * KROW, NK = KB / 1024, ST = DK / 16;
+    constexpr int GROUP = 8;                   // tiles whose page numbers and sums are held at once
+    __shared__ __attribute__((aligned(1024))) char tile[4][2][KB];
+    __shared__ int32_t page_of[4][2][GROUP * KT];
+    __shared__ uint64_t row_at[4][KT];
+    __shared__ float sum_of[4][GROUP * KT];
+    const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv);
+    const Share u = find_share<128>(p.m, p.slots, false, (int)(blockIdx.x / (uint32_t)p.m.Hkv));
+    if (!u.ok) return;
+    const int lane = threadIdx.x & 63, wave = (int)dcp::wave_id(), r = lane & 31, h = lane >> 5;
+    const int nrows = u.s.n * p.m.G, row_tiles = (nrows + 31) / 32;
+    const int all_tiles = (u.k1 - u.k0 + KT - 1) / KT, quarter = (all_tiles + 3) / 4, first = min(wave * quarter, all_tiles);
+    const int tiles = min(quarter, all_tiles - first), base_key = u.k0 + first * KT;
+    if (tiles <= 0) return;                    // (the waves of this kernel never meet)
+
+    const int32_t* table = p.m.table + (int64_t)u.b * p.m.t_B;
+    int32_t pages[GROUP * KT / 64];
+    auto load_pages = [&](int group) {
+#pragma unroll
+        for (int k = 0; k < GROUP * KT / 64; ++k) {
+            const int key = base_key + group * GROUP * KT + k * 64 + lane;
+            pages[k] = key < u.k1 ? table[fdiv((uint32_t)key, p.m.fpage)] : -1;
+        }
+    };
+    auto keep_pages = [&](int group) {
+#pragma unroll
+        for (int k = 0; k < GROUP * KT / 64; ++k) page_of[wave][group & 1][k * 64 + lane] = pages[k];
+    };
+    const uint32_t kbuf = lds_addr(&tile[wave][0][0]);
+    auto turn = [](int row) { return KV8 ? (KROW >= 128 ? row >> 1 & 7 : row >> 1 & 3) : swz(row); };
+    auto fetch = [&](int t) {
+        if (h == 0) {
+            const int page = page_of[wave][t / GROUP & 1][t % GROUP * KT + r];
+            const uint32_t key = (uint32_t)(base_key + t * KT + r);
+            const uint32_t place = key - fdiv(key, p.m.fpage) * p.m.fpage.d;
+            row_at[wave][r] = (uint32_t)page < (uint32_t)p.m.pages
+                                  ? (uint64_t)(p.k + (int64_t)page * p.k_P + (int64_t)place * p.k_S + (int64_t)hk * p.k_H)
+                                  : (uint64_t)kZeros;
+        }
+        constexpr int cols = KROW / 16;
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            const int ch = i * 64 + lane, from = ch / cols, c = (ch % cols) ^ turn(from);
+            dma16((const char*)at_or_zeros(c * 16 < p.Dk * ES, row_at[wave][from] + (uint64_t)(c * 16)),
+                  __builtin_amdgcn_readfirstlane(kbuf + (uint32_t)((t & 1) * KB + i * 1024)));
+        }
+    };
+    // the lane's query row of row tile rt
+    u32x4 q[ST];
+    int vis = 0;
+    float g = 0.0f;
+    auto load_rows = [&](int rt) {
+        const int row = min(rt * 32 + r, nrows - 1), token = (int)fdiv((uint32_t)row, p.m.fG), head = hk * p.m.G + row - token * p.m.G;
+        vis = rt * 32 + r < nrows ? visible(p.m, u.s, token) - base_key : 0;
+        const float x = p.lse[(int64_t)(u.s.first + token) * p.l_T + (int64_t)head * p.l_H];
+        g = x == -INFINITY ? INFINITY : x * p.lmul;      // (a row that saw nothing anywhere gives nothing)
+        const char* from = p.q + (int64_t)(u.s.first + token) * p.q_T + (int64_t)head * p.q_H;
+#pragma unroll
+        for (int s = 0; s < ST; ++s) {
+            const int c = 2 * s + h;
+            const u32x4 y = *(const u32x4*)(from + min(c, p.Dk / 8 - 1) * 16);
+            q[s] = c * 8 < p.Dk ? y : u32x4{0, 0, 0, 0};
+        }
+    };
+    load_pages(0);
+    load_rows(0);
+    keep_pages(0);
+    fetch(0);
+#pragma unroll 1
+    for (int t = 0; t < tiles; ++t) {
+        if (t % GROUP == 0 && t + GROUP < tiles) {
+            load_pages(t / GROUP + 1);
+            keep_pages(t / GROUP + 1);
+        }
+        if (t + 1 < tiles) {
+            fetch(t + 1);
+            asm volatile("s_waitcnt vmcnt(%0)" :: "n"(NK) : "memory");
+        } else {
+            dma_wait();
+        }
+        const uint32_t buf = kbuf + (uint32_t)((t & 1) * KB);
         float acc[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-        const int nrows = u.s.n * p.m.G, tiles = (nrows + 31) / 32;
-        const int per_part = (tiles + parts - 1) / parts;
-        const int first = part * per_part, end = min(tiles, first + per_part);
 #pragma unroll 1
-        for (int t = first; t < end; ++t) {
-            const int row = min(t * 32 + r, nrows - 1);
-            const int token = (int)fdiv((uint32_t)row, p.m.fG), head = hk * p.m.G + row - token * p.m.G;
-            const int lim = t * 32 + r < nrows ? visible(p.m, u.s, token) - key0 - 4 * h : 0;
-            if (__ballot(lim > 0) == 0) continue;
-            const char* q = p.q + (int64_t)(u.s.first + token) * p.q_T + (int64_t)head * p.q_H;
-            float g = p.lse[(int64_t)(u.s.first + token) * p.l_T + (int64_t)head * p.l_H] * p.lmul;
-            if (g == -INFINITY) g = INFINITY;      // a row that saw nothing anywhere gives nothing
+        for (int rt = 0; rt < row_tiles; ++rt) {
+            if (row_tiles > 1) load_rows(rt);
             f32x16 s;
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[i] = 0.0f;
 #pragma unroll
-            for (int k = 0; k < DK / 16; ++k) {
-                const int c = 2 * k + h;
-                u32x4 b = {0, 0, 0, 0};
-                if (c * 8 < p.Dk) b = *(const u32x4*)(q + c * 16);
-                s = Mat<E>::mma(kf[k], b, s);
+            for (int st = 0; st < ST; ++st) {
+                u32x4 a;
+                if constexpr (KV8)
+                    a = widen8<E>(*(const DCPA_LDS u32x2*)(uintptr_t)(buf + (uint32_t)(r * KROW + (st ^ turn(r)) * 16 + h * 8)));
+                else
+                    a = lds_read16(buf + (uint32_t)(r * KROW + ((2 * st + h) ^ turn(r)) * 16));
+                s = Mat<E>::mma(a, q[st], s);
             }
+            const int lim = vis - t * KT - 4 * h;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const float x = exp2_fast(__builtin_fmaf(s[i], p.c, -g));
                 acc[i] += 8 * (i / 4) + i % 4 < lim ? x : 0.0f;
             }
         }
-        // totals over the 32 query lanes; lane r = 0 of each half writes
+        // (the next load into this buffer does not wait for these reads)
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        // totals over the 32 query lanes; lane i of each half takes register i
+        float mine = 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) acc[i] += __shfl_xor(acc[i], d, 64);
+            float x = acc[i];
+            x += dcp::dpp_f<0x128>(x);
+            x += dcp::dpp_f<0x124>(x);
+            x += dcp::dpp_f<0x122>(x);
+            x += dcp::dpp_f<0x121>(x);
+            mine = (lane & 15) == i ? x : mine;
         }
-        float mine = acc[0];
+        mine += __shfl_xor(mine, 16, 64);
+        if (r < 16) sum_of[wave][t % GROUP * KT + 8 * (r / 4) + r % 4 + 4 * h] = mine;
+        if (t % GROUP == GROUP - 1 || t + 1 == tiles) {
+            // the sums of the group's keys join their weights
+            const int from = t / GROUP * GROUP * KT;
+            float* at[GROUP * KT / 64];
+            float old[GROUP * KT / 64];
 #pragma unroll
-        for (int i = 1; i < 16; ++i) mine = (r & 15) == i ? acc[i] : mine;
-        if (r < 16) {
-            const int place = 8 * (r / 4) + r % 4 + 4 * h, k = key0 + place;
-            if (parts > 1) {
-                p.ws[(((int64_t)u.slot * p.m.Hkv + hk) * parts + part) * kKeys + wave * 32 + place] = mine;
-            } else if (k < u.s.kv) {
-                float* m = mass_at(p, u.b, hk, k);
-                if (m != nullptr) *m += mine;
+            for (int k = 0; k < GROUP * KT / 64; ++k) {
+                const uint32_t key = (uint32_t)(base_key + from + k * 64 + lane);
+                const int page = from + k * 64 + lane < tiles * KT ? page_of[wave][t / GROUP & 1][k * 64 + lane] : -1;
+                const uint32_t place = key - fdiv(key, p.m.fpage) * p.m.fpage.d;
+                at[k] = (uint32_t)page < (uint32_t)p.m.pages
+                            ? p.mass + (int64_t)page * p.m_P + (int64_t)place * p.m_S + (int64_t)hk * p.m_H : nullptr;
+                old[k] = 0.0f;
+                if (at[k] != nullptr) old[k] = *at[k];
             }
+#pragma unroll
+            for (int k = 0; k < GROUP * KT / 64; ++k)
+                if (at[k] != nullptr) *at[k] = old[k] + sum_of[wave][k * 64 + lane];
         }
     }
 }
 
-__global__ __launch_bounds__(128) void mass_join(MassArgs p) {
-    const int parts = row_parts(p.m, p.target);
+// The parts of split rows, added in order: a thread to a key.
+template <int KEYS> __global__ __launch_bounds__(KEYS) void mass_join(MassArgs p) {
+    int chunk, parts;
+    share_out<KEYS>(p.m, p.slots, p.ws != nullptr, chunk, parts);
     if (parts == 1) return;
-    for (uint32_t id = blockIdx.x;; id += gridDim.x) {
-        const Step u = find_step(p.m, (int)(id / (uint32_t)p.m.Hkv));
-        if (!u.ok) return;
-        const int hk = (int)(id % (uint32_t)p.m.Hkv), key = u.step * kKeys + (int)threadIdx.x;
-        if (key >= u.s.kv) continue;
-        float* m = mass_at(p, u.b, hk, key);
-        if (m == nullptr) continue;
-        const float* w = p.ws + ((int64_t)u.slot * p.m.Hkv + hk) * parts * kKeys + threadIdx.x;
-        float sum = 0.0f;
-        for (int i = 0; i < parts; ++i) sum += w[(int64_t)i * kKeys];
-        *m += sum;
-    }
+    const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv);
+    const Share u = find_share<KEYS>(p.m, p.slots, p.ws != nullptr, (int)(blockIdx.x / (uint32_t)p.m.Hkv) * parts);
+    const int key = u.k0 + (int)threadIdx.x;
+    if (!u.ok || key >= u.k1) return;
+    float* m = mass_at(p, u.b, hk, key);
+    if (m == nullptr) return;
+    const float* w = p.ws + ((int64_t)u.slot * p.m.Hkv + hk) * parts * KEYS + threadIdx.x;
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) sum += w[(int64_t)i * KEYS];
+    *m += sum;
 }
+
+// Keys of a workgroup's step.
+int keys_of(bool few, int Dk) { return few || Dk > 128 ? 128 : 256; }
 
 }  // namespace
 
-MassPlan plan_mass(const Batch& m) {
+MassPlan plan_mass(const Batch& m, int Dk, bool pieces) {
     MassPlan pl;
     const int64_t rows = (int64_t)m.T * m.G;
-    // with few rows to a sequence the keys alone fill the chip, or nothing does
-    const int target = 1024 / m.Hkv;
-    pl.target = rows <= (int64_t)128 * m.B || target < 2 ? 0 : target;
-    pl.units = 2048;
-    // parts > 1 only while steps * parts <= target
-    pl.ws_bytes = pl.target == 0 ? 0 : (int64_t)pl.target * m.Hkv * kKeys * 4;
+    pl.few = pieces && Dk <= 256 && rows <= (int64_t)32 * m.B;
+    // two workgroups to a CU (four with few rows, whose ranges are then shorter); every sequence
+    // needs one at least
+    const int64_t want = pl.few ? 1024 : 512;
+    const int64_t seqs = m.T < m.B ? m.T : m.B;
+    pl.slots = (int32_t)((want + m.Hkv - 1) / m.Hkv);
+    // a sequence without keys or with one step takes a unit all the same
+    pl.units = (int32_t)(pl.slots > seqs ? pl.slots : 0);
+    if (pl.units == 0) {
+        // more sequences than that: each is one unit, whole
+        pl.slots = 0;
+        pl.units = (int32_t)seqs;
+    }
+    // parts > 1 only while steps * parts <= slots
+    pl.ws_bytes = pl.few ? 0 : (int64_t)pl.slots * m.Hkv * keys_of(pl.few, Dk) * 4;
     return pl;
 }
 
 namespace {
-template <typename E, bool KV8> hipError_t run(const MassArgs& a, hipStream_t stream) {
-    const dim3 grid((uint32_t)a.units), block(256);
-    const hipError_t e = a.Dk <= 64    ? launch(mass_kernel<E, KV8, 64>, grid, block, stream, a)
-                         : a.Dk <= 128 ? launch(mass_kernel<E, KV8, 128>, grid, block, stream, a)
-                         : a.Dk <= 256 ? launch(mass_kernel<E, KV8, 256>, grid, block, stream, a)
-                                       : launch(mass_kernel<E, KV8, 576>, grid, block, stream, a);
-    if (e != hipSuccess || a.target == 0) return e;
-    return launch(mass_join, dim3(1024), dim3(128), stream, a);
+template <typename E, bool KV8> hipError_t run(const MassArgs& a, bool few, hipStream_t stream) {
+    const dim3 grid((uint32_t)((int64_t)a.units * a.m.Hkv)), block(256);
+    if (few)
+        return a.Dk <= 64    ? launch(mass_few<E, KV8, 64>, grid, block, stream, a)
+               : a.Dk <= 128 ? launch(mass_few<E, KV8, 128>, grid, block, stream, a)
+                             : launch(mass_few<E, KV8, 256>, grid, block, stream, a);
+    const hipError_t e = a.Dk <= 64    ? launch(mass_rows<E, KV8, 64, 64>, grid, block, stream, a)
+                         : a.Dk <= 128 ? launch(mass_rows<E, KV8, 128, 64>, grid, block, stream, a)
+                         : a.Dk <= 256 ? launch(mass_rows<E, KV8, 256, 32>, grid, block, stream, a)
+                                       : launch(mass_rows<E, KV8, 576, 32>, grid, block, stream, a);
+    if (e != hipSuccess || a.slots == 0) return e;
+    return keys_of(false, a.Dk) == 128 ? launch(mass_join<128>, grid, dim3(128), stream, a)
+                                       : launch(mass_join<256>, grid, dim3(256), stream, a);
 }
 }  // namespace
 
-hipError_t launch_mass(const MassArgs& a, bool bf16, bool kv8, hipStream_t stream) {
-    if (bf16) return kv8 ? run<BF16T, true>(a, stream) : run<BF16T, false>(a, stream);
-    return kv8 ? run<F16T, true>(a, stream) : run<F16T, false>(a, stream);
+hipError_t launch_mass(const MassArgs& a, bool few, bool bf16, bool kv8, hipStream_t stream) {
+    if (bf16) return kv8 ? run<BF16T, true>(a, few, stream) : run<BF16T, false>(a, few, stream);
+    return kv8 ? run<F16T, true>(a, few, stream) : run<F16T, false>(a, few, stream);
 }
 
 }  // namespace dcpa

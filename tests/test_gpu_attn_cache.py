@@ -173,6 +173,11 @@ MASS = [
     dict(seqs=[(50, 60)], Hq=2, Hkv=2, Dk=576, cache=F8),
     dict(seqs=[(9, 9), (5, 5)], Hq=4, Hkv=2, Dk=64, causal=False, cross=[200, 0]),
     dict(seqs=[(60, 140)], Hq=4, Hkv=2, Dk=64, N=2, rank=0, cut=25),
+    dict(seqs=[(1, 90), (1, 700)], Hq=16, Hkv=2, Dk=128, cache=F8),
+    dict(seqs=[(1, 90), (1, 33)], Hq=4, Hkv=2, Dk=72, cache=F8),
+    dict(seqs=[(1, 90), (1, 33)], Hq=4, Hkv=1, Dk=192, dtype=HF, cache=F8, page=4),
+    dict(seqs=[(9, 90), (0, 3), (0, 40), (0, 7)], Hq=8, Hkv=1, Dk=64, page=4),   # many rows in one sequence of few
+    dict(seqs=[(1, 3000)], Hq=8, Hkv=1, Dk=64, page=16),
 ]
 
 
