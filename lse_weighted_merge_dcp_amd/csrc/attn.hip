@@ -84,7 +84,7 @@ __global__ __launch_bounds__(256, 2) void attn_rows(AttnArgs p) {
         for (int i = 0; i < NK + NV; ++i) {
             const bool val = i >= NK;
             const int ch = (val ? i - NK : i) * 256 + tid, cols = val ? VC : KC;
-            const int row = ch / cols, c = (ch % cols) ^ swz(row);
+            const int row = ch / cols, c = (ch % cols) ^ (val ? swz_v<VC>(row) : swz<KC>(row));
             const uint64_t base = val ? vrow_at[t & 1][row] : krow_at[t & 1][row];
             const uint64_t a = at_or_zeros(c * 8 < (val ? p.Dv : p.Dk), base + (uint64_t)(c * (KV8 ? 8 : 16)));
             if constexpr (KV8) {
@@ -217,14 +217,17 @@ __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void attn_keys(AttnArgs p) {
     };
     const uint32_t kbuf = lds_addr(&tile[wave][0]), vbuf = kbuf + KB;
     // a row's chunk c of 16 bytes lies at c ^ turn(row)
-    auto turn = [](int row) { return KV8 ? (DK * ES >= 128 ? row >> 1 & 7 : row >> 1 & 3) : swz(row); };
+    auto turn = [](bool val, int row) {
+        if constexpr (KV8) return DK >= 128 ? row >> 1 & 7 : row >> 1 & 3;
+        else return val ? swz_v<VROW / 16>(row) : swz<KROW / 16>(row);
+    };
     auto fetch = [&](bool val, uint32_t buf) {
         constexpr int NMAX = NK > NV ? NK : NV;
         const int cols = (val ? VROW : KROW) / 16, n = val ? NV : NK, width = (val ? p.Dv : p.Dk) * ES;
 #pragma unroll
         for (int i = 0; i < NMAX; ++i) {
             if (i >= n) break;
-            const int ch = i * 64 + lane, from = ch / cols, c = (ch % cols) ^ turn(from);
+            const int ch = i * 64 + lane, from = ch / cols, c = (ch % cols) ^ turn(val, from);
             const uint64_t a = at_or_zeros(c * 16 < width, row_at[wave][val][from] + (uint64_t)(c * 16));
             dma16((const char*)a, __builtin_amdgcn_readfirstlane(buf + (uint32_t)(i * 1024)));
         }
@@ -250,7 +253,7 @@ __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void attn_keys(AttnArgs p) {
             for (int i = 0; i < 16; ++i) s[0][0][i] = 0.0f;
 #pragma unroll
             for (int st = 0; st < DK / 16; ++st) {
-                const u32x2 x = *(const DCPA_LDS u32x2*)(uintptr_t)(kbuf + (uint32_t)(r * KROW + ((st ^ turn(r)) * 16) + h * 8));
+                const u32x2 x = *(const DCPA_LDS u32x2*)(uintptr_t)(kbuf + (uint32_t)(r * KROW + ((st ^ turn(false, r)) * 16) + h * 8));
                 s[0][0] = Mat<E>::mma(widen8<E>(x), w.q[0][st], s[0][0]);
             }
         } else {
@@ -273,7 +276,7 @@ __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void attn_keys(AttnArgs p) {
         if constexpr (KV8) {
             const int g = (lane >> 4) & 1, li = lane & 15, j = li >> 1, key = 4 * h + (j & 3) + 8 * (j >> 2);
             outputs<E, DK, DV, 1, KT>(w, pr, [&](int cb, int ks) {
-                const uint32_t a = vbuf + (uint32_t)((ks * 16 + key) * VROW + ((2 * cb + g) ^ turn(ks * 16 + key)) * 16 + (li & 1) * 8);
+                const uint32_t a = vbuf + (uint32_t)((ks * 16 + key) * VROW + ((2 * cb + g) ^ turn(true, ks * 16 + key)) * 16 + (li & 1) * 8);
                 return widen8<E>(lds_read_tr8(a));
             });
         } else {
@@ -389,11 +392,12 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs p) {
             continue;
         }
         const int at = __builtin_ctzll(found);
-        const int nt = __builtin_amdgcn_readlane(tiles, at), ns = __builtin_amdgcn_readlane(splits, at);
+        const int ns = __builtin_amdgcn_readlane(splits, at);
         if (ns == 1) return;                  // written whole
         const Seq s = load_seq(p.m, b0 + at);
         const int row = (t - s.first) * p.m.G + head, tile = row / p.rows, in_tile = row - tile * p.rows;
-        const int slot = __builtin_amdgcn_readlane(incl, at) - nt * ns + tile * ns;
+        // (a sequence's last tile comes first)
+        const int slot = __builtin_amdgcn_readlane(incl, at) - (tile + 1) * ns;
         if (slot < 0) return;
         // the ranges that the tile's last row has keys in
         const int last = min((tile + 1) * p.rows, s.n * p.m.G) - 1;

@@ -84,13 +84,20 @@ __device__ __forceinline__ float half_sum(float x) {
 }
 
 // --------------------------------------------------------------------------
-// A tile in LDS is [keys][chunks of 16 bytes]; chunk c of key r lies at place
-// c ^ swz(r) (the low three bits of c change).  Reads of one chunk column over
-// eight consecutive keys (the key fragments) then touch eight different
-// 16-byte places of 128 bytes, and transposing reads of 32 bytes of four
-// consecutive keys (the value fragments) four different 32-byte ones.
+// A tile in LDS is [rows][C chunks of 16 bytes]; chunk c of row r lies at place
+// c ^ swz(r).  LDS serves 64 banks, 256 bytes, a clock: a key fragment's read
+// takes one chunk column of 16 rows at a time, which then lie in 16 different
+// places of 256 bytes; a value fragment's transposing read 64 bytes of four
+// neighbouring rows, or 32 bytes of eight.  (Counters: no bank conflicts in
+// either; with the rows' low three bits alone both took twice the clocks.)
+// Rows of an odd number of 128 bytes already alternate between the halves.
 // --------------------------------------------------------------------------
-__device__ __forceinline__ int swz(int r) { return ((r & 3) << 1) | ((r >> 2) & 1); }
+template <int C> __device__ __forceinline__ int swz(int r) {
+    if constexpr (C % 16 == 0) return (r & 3) << 2 | (r >> 2 & 1) << 1 | (r >> 3 & 1);
+    else return (r >> 1 & 1) << 2 | (r >> 2 & 1) << 1 | (r >> 3 & 1);
+}
+// For values in a tile of their own: rows r and r + 8 at the same place.
+template <int C> __device__ __forceinline__ int swz_v(int r) { return swz<C>(r & 7); }
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
     return (uint32_t)(uintptr_t)(const DCPA_LDS char*)p;
@@ -278,8 +285,9 @@ __device__ __forceinline__ Unit find_unit(const Batch& m, int rows, int slots, i
             u.b = b0 + at;
             u.s = load_seq(m, u.b);
             u.splits = s;
-            u.tile = rest / s;
-            u.split = rest - u.tile * s;
+            // the last rows see most keys: they come first
+            u.split = rest % s;
+            u.tile = t - 1 - rest / s;
             u.slot = id - u.split;
             // (lengths that contradict each other could lead outside the tile)
             u.ok = rest >= 0 && (int64_t)u.tile * rows < (int64_t)u.s.n * m.G;

@@ -151,12 +151,12 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
         asm volatile("" : "+v"(ln));        // (keeps nine offsets from being held in registers)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int c = ln ^ swz(i);
+            const int c = ln ^ swz<64>(wave * 8 + i);
             const uint32_t to = buf + (uint32_t)((wave * 8 + i) * 1024);
             if constexpr (EXACT) dma16_from(lane64(row_at, 8 * i), (uint32_t)(c * 16), to);
             else dma16((const char*)at_or_zeros(c * 8 < p.Dk, lane64(row_at, 8 * i) + (uint64_t)(c * 16)), to);
         }
-        const int c = 64 + ((ln & 7) ^ swz(ln / 8));
+        const int c = 64 + ((ln & 7) ^ swz<8>(wave * 8 + ln / 8));
         dma16((const char*)at_or_zeros(EXACT || c * 8 < p.Dk, row_at + (uint64_t)(c * 16)),
               buf + (uint32_t)(MAIN + wave * 1024));
     };
@@ -194,8 +194,8 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int d = 2 * c + k;
-                const uint32_t to = d < 64 ? (uint32_t)(in_tile * 1024 + (d ^ swz(row)) * 16)
-                                           : (uint32_t)(MAIN + in_tile * 128 + ((d - 64) ^ swz(row)) * 16);
+                const uint32_t to = d < 64 ? (uint32_t)(in_tile * 1024 + (d ^ swz<64>(in_tile)) * 16)
+                                           : (uint32_t)(MAIN + in_tile * 128 + ((d - 64) ^ swz<8>(in_tile)) * 16);
                 lds_write16(buf + to, widen8<E>(k == 0 ? u32x2{x.x, x.y} : u32x2{x.z, x.w}));
             }
         }
@@ -226,21 +226,24 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
     float mc = kNoMax, l = 0.0f;
     bool odd = false;
 
-    // lane constants of the fragment reads (see attn_tile.hpp)
-    uint32_t ka[4], va[2];
+    // lane constants of the fragment reads (see attn_tile.hpp); values are read where the
+    // keys' places put them, so the second four rows of a fragment lie at the other chunk of a pair
+    uint32_t ka[8], va[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) ka[j] = (uint32_t)(r * 1024 + ((2 * j + h) ^ swz(r)) * 16);
+    for (int j = 0; j < 8; ++j) ka[j] = (uint32_t)(r * 1024 + ((2 * j + h) ^ swz<64>(r)) * 16);
     const int g = (lane >> 4) & 1, li = lane & 15;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 4; ++j)
         va[j] = (uint32_t)((4 * h + li / 4) * 1024 + (li & 1) * 8 +
-                           ((4 * j + 2 * g + (li & 3) / 2) ^ swz(4 * h + li / 4)) * 16);
+                           ((4 * j + 2 * g + (li & 3) / 2) ^ swz<64>(4 * h + li / 4)) * 16);
     auto key_fragment = [&](uint32_t buf, int st) {
-        return lds_read16(buf + ka[st & 3] + (st < 32 ? (uint32_t)((st >> 2) * 128) : (uint32_t)(MAIN - r * 896)));
+        if (st < 32) return lds_read16(buf + ka[st & 7] + (uint32_t)((st >> 3) * 256));
+        return lds_read16(buf + (uint32_t)(MAIN + r * 128 + ((2 * (st - 32) + h) ^ swz<8>(r)) * 16));
     };
     auto value_fragment = [&](uint32_t buf, int i) {          // i = 2 * block + half of the keys
-        const uint32_t a = buf + va[(i >> 1) & 1] + (uint32_t)((i >> 2) * 128 + (i & 1) * 16 * 1024);
-        const u32x2 x = lds_read_tr(a), y = lds_read_tr(a + 8 * 1024);
+        const uint32_t off = (uint32_t)((i >> 3) * 256 + (i & 1) * 16 * 1024);
+        const u32x2 x = lds_read_tr(buf + va[(i >> 1) & 3] + off);
+        const u32x2 y = lds_read_tr((buf + va[(i >> 1) & 3] ^ 16u) + off + 8 * 1024);
         return u32x4{x.x, x.y, y.x, y.y};
     };
     constexpr int AHEAD = 6, VAHEAD = 4;

@@ -150,7 +150,7 @@ __global__ __launch_bounds__(256, 2) void mass_rows(MassArgs p) {
     auto fetch = [&](int t, int b) {
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
-            const int ch = i * 256 + tid, row = min(ch / KC, 31), c = (ch % KC) ^ swz(row);
+            const int ch = i * 256 + tid, row = min(ch / KC, 31), c = (ch % KC) ^ swz<KC>(row);
             int token, head;
             row_place(t * 32 + row, token, head);
             const uint64_t at = (uint64_t)(p.q + (int64_t)(u.s.first + token) * p.q_T + (int64_t)head * p.q_H) + (uint64_t)(c * 16);
@@ -227,7 +227,7 @@ __global__ __launch_bounds__(256, 2) void mass_rows(MassArgs p) {
             const uint32_t qrow = lds0 + (uint32_t)(now * PAD + r * QROW);
 #pragma unroll
             for (int k = 0; k < ST; ++k) {
-                const u32x4 b = lds_read16(qrow + (uint32_t)(((2 * k + h) ^ swz(r)) * 16));
+                const u32x4 b = lds_read16(qrow + (uint32_t)(((2 * k + h) ^ swz<KC>(r)) * 16));
 #pragma unroll
                 for (int kb = 0; kb < NB; ++kb) s[kb] = Mat<E>::mma(kf[kb][k], b, s[kb]);
             }
@@ -305,7 +305,7 @@ __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void mass_few(MassArgs p) {
         for (int k = 0; k < GROUP * KT / 64; ++k) page_of[wave][group & 1][k * 64 + lane] = pages[k];
     };
     const uint32_t kbuf = lds_addr(&tile[wave][0][0]);
-    auto turn = [](int row) { return KV8 ? (KROW >= 128 ? row >> 1 & 7 : row >> 1 & 3) : swz(row); };
+    auto turn = [](int row) { return KV8 ? (KROW >= 128 ? row >> 1 & 7 : row >> 1 & 3) : swz<KROW / 16>(row); };
     auto fetch = [&](int t) {
         if (h == 0) {
             const int page = page_of[wave][t / GROUP & 1][t % GROUP * KT + r];

@@ -49,24 +49,26 @@ __device__ __forceinline__ void load_query(u32x4 (&q)[N], const char* row, int D
 
 // Fragment addresses within a tile of 16-bit rows (see swz()).
 template <int KROW> struct KeyPlace {      // key r of 32, columns 16 st + 8 h .. + 7
-    uint32_t at[4];
+    static constexpr int N = KROW % 256 == 0 ? 8 : 4;
+    uint32_t at[N];
     __device__ __forceinline__ void set(uint32_t base, int r, int h) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) at[j] = base + (uint32_t)(r * KROW + ((2 * j + h) ^ swz(r)) * 16);
+        for (int j = 0; j < N; ++j) at[j] = base + (uint32_t)(r * KROW + ((2 * j + h) ^ swz<KROW / 16>(r)) * 16);
     }
-    __device__ __forceinline__ u32x4 read(int st) const { return lds_read16(at[st & 3] + (uint32_t)((st >> 2) * 128)); }
+    __device__ __forceinline__ u32x4 read(int st) const { return lds_read16(at[st % N] + (uint32_t)(st / N * N * 32)); }
 };
 template <int VROW> struct ValuePlace {    // 32 columns of block cb, the keys {0..3, 8..11} + 4 h of 16 ks ..
-    uint32_t at[2];
+    static constexpr int N = VROW % 256 == 0 ? 4 : 2;
+    uint32_t at[N];
     __device__ __forceinline__ void set(uint32_t base, int lane) {
         // 16 lanes read four rows of 32 bytes, transposed
         const int h = lane >> 5, g = (lane >> 4) & 1, li = lane & 15, row = 4 * h + li / 4;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            at[j] = base + (uint32_t)(row * VROW + (li & 1) * 8 + ((4 * j + 2 * g + (li & 3) / 2) ^ swz(row)) * 16);
+        for (int j = 0; j < N; ++j)
+            at[j] = base + (uint32_t)(row * VROW + (li & 1) * 8 + ((4 * j + 2 * g + (li & 3) / 2) ^ swz_v<VROW / 16>(row)) * 16);
     }
     __device__ __forceinline__ u32x4 read(int cb, int ks) const {
-        const uint32_t a = at[cb & 1] + (uint32_t)((cb >> 1) * 128 + ks * 16 * VROW);
+        const uint32_t a = at[cb % N] + (uint32_t)(cb / N * N * 64 + ks * 16 * VROW);
         const u32x2 x = lds_read_tr(a), y = lds_read_tr(a + 8 * VROW);
         return u32x4{x.x, x.y, y.x, y.y};
     }
