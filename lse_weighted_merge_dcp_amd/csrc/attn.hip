@@ -143,7 +143,7 @@ __global__ __launch_bounds__(256, 2) void attn_rows(AttnArgs p) {
         if (t + 1 < tiles) widen(t + 1);
     }
     if (odd)
-        slow_rows<E, KV8, DK, DV>(p, u, hk, unit, R, row0, row0 + wave_row,
+        slow_rows<E, KV8, DK, DV>(late_args<AttnArgs>(), u, hk, unit, R, row0, row0 + wave_row,
                                   min(row0 + wave_row + 32 * RB, nrows), k0, k1);
     else
         write_rows<E>(p, u, w, hk, unit, R, row0, wave_row, nrows);
@@ -304,7 +304,7 @@ __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void attn_keys(AttnArgs p) {
     if (lane == 0) part_odd[wave] = odd;
     meet();
     if ((part_odd[0] | part_odd[1] | part_odd[2] | part_odd[3]) != 0) {
-        slow_rows<E, KV8, DK, DV>(p, u, hk, unit, 32, row0, row0 + wave * 8, min(row0 + wave * 8 + 8, nrows), k0, k1);
+        slow_rows<E, KV8, DK, DV>(late_args<AttnArgs>(), u, hk, unit, 32, row0, row0 + wave * 8, min(row0 + wave * 8 + 8, nrows), k0, k1);
         return;
     }
     float mc = kNoMax;

@@ -9,8 +9,8 @@ namespace dcpa {
 // where the table names no page.
 __device__ __forceinline__ uint64_t page_row(int page, const Batch& m, const char* base, int64_t P, int64_t S,
                                              int64_t off, uint32_t place) {
-    if ((uint32_t)page >= (uint32_t)m.pages) return (uint64_t)kZeros;
-    return (uint64_t)(base + (int64_t)page * P + (int64_t)place * S + off);
+    return at_or_zeros((uint32_t)page < (uint32_t)m.pages,
+                       (uint64_t)(base + off) + times64((uint32_t)page, P) + times64(place, S));
 }
 
 // Writes a wave's finished rows: to the outputs, or as a part for the join.

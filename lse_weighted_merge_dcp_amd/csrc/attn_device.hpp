@@ -136,6 +136,10 @@ __device__ __forceinline__ u32x2 lds_read_tr8(uint32_t a) {
 // What absent keys and columns are loaded from: a row of the widest cache.
 __device__ __attribute__((aligned(16))) const uint32_t kZeros[288] = {};
 
+// a * b, b >= 0, in the two products it takes.
+__device__ __forceinline__ uint64_t times64(uint32_t a, int64_t b) {
+    return (uint64_t)a * (uint32_t)b + ((uint64_t)(a * (uint32_t)((uint64_t)b >> 32)) << 32);
+}
 // at, or the row of zeros (in bit operations: written as a choice, the compiler
 // branches around the read of `at` for every piece).
 __device__ __forceinline__ uint64_t at_or_zeros(bool ok, uint64_t at) {
@@ -158,6 +162,15 @@ template <typename E> __device__ __forceinline__ u32x4 widen8(u32x2 x) {
         r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x.y, 1.0f, true));
     }
     return r;
+}
+
+// The kernel's arguments, read again where they are needed late: held from the
+// start they would take scalar registers through the whole main loop.
+template <typename T> __device__ __forceinline__ const T& late_args() {
+    typedef const __attribute__((address_space(4))) T* Ptr;
+    Ptr p = (Ptr)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const T*)p;
 }
 
 // --------------------------------------------------------------------------
@@ -183,6 +196,12 @@ __device__ __forceinline__ Seq load_seq(const Batch& m, int b) {
     s.kv = min(max(m.kv[b], 0), m.max_keys);
     s.len = m.seq != nullptr ? m.seq[b] : 0;
     return s;
+}
+
+// Lane `at`'s sequence, for the whole wave.
+__device__ __forceinline__ Seq seq_of(const Seq& s, int at) {
+    return Seq{__builtin_amdgcn_readlane(s.first, at), __builtin_amdgcn_readlane(s.n, at),
+               __builtin_amdgcn_readlane(s.kv, at), __builtin_amdgcn_readlane(s.len, at)};
 }
 
 // Keys that token i of the sequence sees.
@@ -273,8 +292,13 @@ __device__ __forceinline__ Unit find_unit(const Batch& m, int rows, int slots, i
     const int lane = threadIdx.x & 63;
     int base = 0;
     for (int b0 = 0; b0 < m.B; b0 += 64) {
-        int tiles, kv;
-        tiles_of(m, b0 + lane, rows, tiles, kv);
+        int tiles = 0, kv = 0;
+        Seq mine{};
+        if (b0 + lane < m.B) {
+            mine = load_seq(m, b0 + lane);
+            tiles = (mine.n * m.G + rows - 1) / rows;
+            kv = mine.kv;
+        }
         const int splits = max(1, (kv + u.chunk - 1) / u.chunk);
         const int incl = base + scan_incl(tiles * splits, lane);
         const uint64_t past = __ballot(incl > id);
@@ -283,7 +307,7 @@ __device__ __forceinline__ Unit find_unit(const Batch& m, int rows, int slots, i
             const int t = __builtin_amdgcn_readlane(tiles, at), s = __builtin_amdgcn_readlane(splits, at);
             const int rest = id - (__builtin_amdgcn_readlane(incl, at) - t * s);
             u.b = b0 + at;
-            u.s = load_seq(m, u.b);
+            u.s = seq_of(mine, at);
             u.splits = s;
             // the last rows see most keys: they come first
             u.split = rest % s;

@@ -24,9 +24,11 @@ namespace {
 
 // The scores' products, in ordinary registers.  The compiler does not see that
 // these are matrix instructions, so the waits it would add stand here: two
-// states in front, since a vector instruction may have written an operand just
-// before, and settle() between the last product and the first other use (an
-// 8-pass product's result may be read 11 states later).
+// states before the first of a row (a vector instruction may have written an
+// operand just before; between two products none writes an operand, which the
+// test of the compiled code checks too), and settle() between the last product
+// and the first other use (an 8-pass product's result may be read 11 states
+// later).
 template <typename E> __device__ __forceinline__ void mma_first(f32x16& d, u32x4 a, u32x4 b) {
     if constexpr (std::is_same_v<E, BF16T>)
         asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(d) : "v"(a), "v"(b));
@@ -35,19 +37,19 @@ template <typename E> __device__ __forceinline__ void mma_first(f32x16& d, u32x4
 }
 template <typename E> __device__ __forceinline__ void mma_next(f32x16& d, u32x4 a, u32x4 b) {
     if constexpr (std::is_same_v<E, BF16T>)
-        asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(d) : "v"(a), "v"(b));
+        asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(d) : "v"(a), "v"(b));
     else
-        asm("s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+v"(d) : "v"(a), "v"(b));
+        asm("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+v"(d) : "v"(a), "v"(b));
 }
 __device__ __forceinline__ void settle(f32x16& d) { asm volatile("s_nop 15\n\ts_nop 3" : "+v"(d)); }
 
 // Output block CB (32 columns) is a[16 CB .. 16 CB + 15].
 template <typename E, int CB> __device__ __forceinline__ void out_mma(u32x4 a, u32x4 b) {
     if constexpr (std::is_same_v<E, BF16T>)
-        asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 a[%2:%3], %0, %1, a[%2:%3]"
+        asm volatile("v_mfma_f32_32x32x16_bf16 a[%2:%3], %0, %1, a[%2:%3]"
                      :: "v"(a), "v"(b), "n"(16 * CB), "n"(16 * CB + 15));
     else
-        asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_f16 a[%2:%3], %0, %1, a[%2:%3]"
+        asm volatile("v_mfma_f32_32x32x16_f16 a[%2:%3], %0, %1, a[%2:%3]"
                      :: "v"(a), "v"(b), "n"(16 * CB), "n"(16 * CB + 15));
 }
 template <int I> __device__ __forceinline__ void out_scale4(float f) {
@@ -97,7 +99,7 @@ constexpr int MAIN = KT * 1024, KB = MAIN + KT * 128;
 // 16 bytes at base + off of every lane (base the same for the wave) to LDS.
 __device__ __forceinline__ void dma16_from(uint64_t base, uint32_t off, uint32_t to) {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-                 :: "v"(off), "s"(base), "s"(to) : "memory");
+                 :: "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(to)) : "memory");
 }
 __device__ __forceinline__ uint64_t lane64(uint64_t x, int lane) {
     return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, lane) |
@@ -113,9 +115,13 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
     constexpr int NBUF = KV8 ? 3 : 4, RAW = KV8 ? KT * DK : 0;
     __shared__ __attribute__((aligned(1024))) char tile[NBUF * KB + 2 * RAW];
     __shared__ uint8_t there_at[8][4];
-    // page numbers of the keys of 16 tiles, and of the next 16
-    constexpr int GROUP = 16;
+    // page numbers of the keys of 8 tiles, and of the next 8
+    constexpr int GROUP = 8;
+    static_assert(GROUP * KT == 256, "a key to a thread");
     __shared__ int32_t page_of[2][GROUP * KT];
+    // what the registers do not hold of the queries: the last QL fragments
+    constexpr int QL = 3, QR = STEPS - QL;
+    __shared__ u32x4 query_s[QL][256];
 
     const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv), unit = (int)(blockIdx.x / (uint32_t)p.m.Hkv);
     const Unit u = find_unit<KT>(p.m, R, p.slots, unit);
@@ -135,30 +141,35 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
     const uint32_t lds0 = lds_addr(&tile[0]);
     auto page_at = [&](int key) { return key < k1 ? table[fdiv((uint32_t)key, p.m.fpage)] : -1; };
     uint64_t row_at = 0;           // of the tile that is fetched next
-    auto place_rows = [&](int t) {
-        const int page = page_of[t / GROUP & 1][t % GROUP * KT + wave * 8 + lane / 8];
+    auto page_for = [&](int t) {
+        return t < tiles ? page_of[t / GROUP & 1][t % GROUP * KT + wave * 8 + lane / 8] : -1;
+    };
+    auto place_rows = [&](int t, int page) {
         const uint32_t key = (uint32_t)(my_key + t * KT);
         const uint32_t place = key - fdiv(key, p.m.fpage) * p.m.fpage.d;
         row_at = page_row(page, p.m, p.k, p.k_P, p.k_S, koff, place);
         // one bit for each of the 8 rows
         const uint64_t bits = __ballot((lane & 7) == 0 && (uint32_t)page < (uint32_t)p.m.pages);
-        if (lane == 0) there_at[t & 7][wave] = (uint8_t)(bits * 0x0102040810204080ull >> 56);
+        there_at[t & 7][wave] = (uint8_t)(bits * 0x0102040810204080ull >> 56);
     };
     auto buffer = [&](int t) { return lds0 + (uint32_t)(t % NBUF * KB); };
-    // the wave's rows of a tile: of each row the first 512 columns, then what is left of all eight
-    auto fetch_rows = [&](uint32_t buf) {
-        int ln = lane;
-        asm volatile("" : "+v"(ln));        // (keeps nine offsets from being held in registers)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = ln ^ swz<64>(wave * 8 + i);
+    // byte offsets of the lane's piece of a row: the wave's rows differ in known bits of swz()
+    const uint32_t my_off = (uint32_t)((lane ^ (wave & 1)) * 16);
+    const uint32_t my_rest = (uint32_t)((64 + ((lane & 7) ^ swz<8>(wave * 8 + lane / 8))) * 16);
+    // the wave's rows of a tile, in nine pieces: of each row the first 512 columns, then what is
+    // left of all eight
+    auto fetch_piece = [&](uint32_t buf, auto piece) {
+        constexpr int i = decltype(piece)::value;
+        if constexpr (i < 8) {
+            const uint32_t off = my_off ^ (uint32_t)(swz<64>(i) * 16);
             const uint32_t to = buf + (uint32_t)((wave * 8 + i) * 1024);
-            if constexpr (EXACT) dma16_from(lane64(row_at, 8 * i), (uint32_t)(c * 16), to);
-            else dma16((const char*)at_or_zeros(c * 8 < p.Dk, lane64(row_at, 8 * i) + (uint64_t)(c * 16)), to);
+            if constexpr (EXACT) dma16_from(lane64(row_at, 8 * i), off, to);
+            else dma16((const char*)at_or_zeros((int)off < p.Dk * 2, lane64(row_at, 8 * i) + off),
+                       __builtin_amdgcn_readfirstlane(to));
+        } else {
+            dma16((const char*)at_or_zeros(EXACT || (int)my_rest < p.Dk * 2, row_at + my_rest),
+                  __builtin_amdgcn_readfirstlane(buf + (uint32_t)(MAIN + wave * 1024)));
         }
-        const int c = 64 + ((ln & 7) ^ swz<8>(wave * 8 + ln / 8));
-        dma16((const char*)at_or_zeros(EXACT || c * 8 < p.Dk, row_at + (uint64_t)(c * 16)),
-              buf + (uint32_t)(MAIN + wave * 1024));
     };
     // 8-bit: rows as they are (576 bytes each) behind the tiles
     auto raw = [&](int t) { return lds0 + (uint32_t)(NBUF * KB + (t & 1) * RAW + wave * 8 * DK); };
@@ -203,67 +214,70 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
     // tile t asked for; its rows have been placed
     auto fetch = [&](int t) {
         if constexpr (KV8) fetch_raw(t);
-        else fetch_rows(buffer(t));
+        else times<9>([&](auto i) { fetch_piece(buffer(t), i); });
     };
-    auto load_pages = [&](int group, int32_t (&x)[2]) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) x[k] = page_at(k0 + group * GROUP * KT + k * 256 + tid);
+    auto load_pages = [&](int group, int32_t (&x)[1]) {
+        x[0] = page_at(k0 + group * GROUP * KT + tid);
     };
-    auto keep_pages = [&](int group, const int32_t (&x)[2]) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) page_of[group & 1][k * 256 + tid] = x[k];
+    auto keep_pages = [&](int group, const int32_t (&x)[1]) {
+        page_of[group & 1][tid] = x[0];
     };
 
     out_claim();
     times<DV / 8>([&](auto i) { out_zero4<i * 4>(); });
-    u32x4 q[STEPS];
+    u32x4 q[QR];
     const int my_row = min(row0 + wave_row + r, last_row), token = (int)fdiv((uint32_t)my_row, p.m.fG);
     const int vis = visible(p.m, u.s, token) - k0;
-    load_query<DK>(q, p.q + (int64_t)(u.s.first + token) * p.q_T +
-                          (int64_t)(hk * p.m.G + my_row - token * p.m.G) * p.q_H, p.Dk, h);
+    {
+        u32x4 all[STEPS];
+        load_query<DK>(all, p.q + (int64_t)(u.s.first + token) * p.q_T +
+                                (int64_t)(hk * p.m.G + my_row - token * p.m.G) * p.q_H, p.Dk, h);
+#pragma unroll
+        for (int i = 0; i < QR; ++i) q[i] = all[i];
+#pragma unroll
+        for (int i = 0; i < QL; ++i) query_s[i][tid] = all[QR + i];
+    }
+    auto query = [&](int st) { return st < QR ? q[min(st, QR - 1)] : query_s[max(st, QR) - QR][tid]; };
     const int vmin = __builtin_amdgcn_readlane(vis, 0), vmax = __builtin_amdgcn_readlane(vis, 31);
     const bool work = row0 + wave_row < nrows;          // (waves behind the last row only help to fetch)
     float mc = kNoMax, l = 0.0f;
     bool odd = false;
 
-    // lane constants of the fragment reads (see attn_tile.hpp); values are read where the
-    // keys' places put them, so the second four rows of a fragment lie at the other chunk of a pair
-    uint32_t ka[8], va[4];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ka[j] = (uint32_t)(r * 1024 + ((2 * j + h) ^ swz<64>(r)) * 16);
+    // Lane constants of the fragment reads (see attn_tile.hpp).  A step's chunk differs from the
+    // first one's in bits that the places are xored into anyway, so one address serves all; values
+    // are read where the keys' places put them, the second four rows of a fragment at the other
+    // chunk of a pair.
+    const uint32_t ka = (uint32_t)(r * 1024 + (h ^ swz<64>(r)) * 16);
+    const uint32_t kt = (uint32_t)(MAIN + r * 128 + (h ^ swz<8>(r)) * 16);
     const int g = (lane >> 4) & 1, li = lane & 15;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        va[j] = (uint32_t)((4 * h + li / 4) * 1024 + (li & 1) * 8 +
-                           ((4 * j + 2 * g + (li & 3) / 2) ^ swz<64>(4 * h + li / 4)) * 16);
+    const uint32_t va = (uint32_t)((4 * h + li / 4) * 1024 + (li & 1) * 8 +
+                                   ((2 * g + (li & 3) / 2) ^ swz<64>(4 * h + li / 4)) * 16);
     auto key_fragment = [&](uint32_t buf, int st) {
-        if (st < 32) return lds_read16(buf + ka[st & 7] + (uint32_t)((st >> 3) * 256));
-        return lds_read16(buf + (uint32_t)(MAIN + r * 128 + ((2 * (st - 32) + h) ^ swz<8>(r)) * 16));
+        if (st < 32) return lds_read16(((buf + ka) ^ (uint32_t)((st & 7) * 32)) + (uint32_t)((st >> 3) * 256));
+        return lds_read16((buf + kt) ^ (uint32_t)((st - 32) * 32));
     };
     auto value_fragment = [&](uint32_t buf, int i) {          // i = 2 * block + half of the keys
-        const uint32_t off = (uint32_t)((i >> 3) * 256 + (i & 1) * 16 * 1024);
-        const u32x2 x = lds_read_tr(buf + va[(i >> 1) & 3] + off);
-        const u32x2 y = lds_read_tr((buf + va[(i >> 1) & 3] ^ 16u) + off + 8 * 1024);
+        const uint32_t off = (uint32_t)((i >> 3) * 256 + (i & 1) * 16 * 1024), turn = (uint32_t)((i >> 1 & 3) * 64);
+        const u32x2 x = lds_read_tr(((buf + va) ^ turn) + off);
+        const u32x2 y = lds_read_tr(((buf + va) ^ (turn | 16u)) + off + 8 * 1024);
         return u32x4{x.x, x.y, y.x, y.y};
     };
-    constexpr int AHEAD = 6, VAHEAD = 4;
+    constexpr int AHEAD = 4, VAHEAD = 4;
 #define DCPA_PIN __builtin_amdgcn_sched_barrier(0)
 
     // what arrives first: tile 0, then 1 and 2
     f32x16 s;
     uint64_t rows1 = 0, rows2 = 0;     // 8-bit: of the two tiles that are still to be widened
     if (tiles > 0) {
-        int32_t x[2];
+        int32_t x[1];
         load_pages(0, x);
         keep_pages(0, x);
         meet();
 #pragma unroll
         for (int t = 0; t < 3; ++t) {
-            if (t < tiles) {
-                place_rows(t);
-                if (KV8 && t == 2) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                fetch(t);
-            }
+            place_rows(t, page_for(t));
+            if (KV8 && t == 2) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            fetch(t);
             if (KV8 && t == 0) {
                 dma_wait();
                 widen(0, row_at);
@@ -271,13 +285,14 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
             if (KV8 && t == 1) rows1 = row_at;
             if (KV8 && t == 2) rows2 = row_at;
         }
-        dma_wait();
+        // (tiles 1 and 2 may still be on their way)
+        if constexpr (!KV8) asm volatile("s_waitcnt vmcnt(18)" ::: "memory");
         meet();
         if (work && vmax > 0) {
             const uint32_t buf = buffer(0);
             times<STEPS>([&](auto st) {
-                if constexpr (st == 0) mma_first<E>(s, key_fragment(buf, st), q[0]);
-                else mma_next<E>(s, key_fragment(buf, st), q[st]);
+                if constexpr (st == 0) mma_first<E>(s, key_fragment(buf, st), query(st));
+                else mma_next<E>(s, key_fragment(buf, st), query(st));
             });
             settle(s);
         }
@@ -285,16 +300,18 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
     out_claim();
 
     // One tile's weights and outputs, with the next tile's scores between: the
-    // exponentials run in the shadow of its matrix instructions.
-    auto advance = [&](int t, auto next) {
+    // exponentials run in the shadow of its matrix instructions, one to two of them
+    // (an exponential takes half a product's time).  The nine pieces of tile t + 3
+    // are asked for all along, so that the four waves' requests do not queue up.
+    auto advance = [&](int t, uint32_t buf, uint32_t nbuf, uint32_t to, auto next) {
         constexpr bool NEXT = decltype(next)::value;
-        const uint32_t buf = buffer(t), nbuf = buffer(t + 1);
         u32x4 kf[AHEAD], vf[VAHEAD];
+        const uint32_t there = *(const uint32_t*)&there_at[t & 7][0];
+        const int page = page_for(t + 3);
         if constexpr (NEXT) {
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) kf[i] = key_fragment(nbuf, i);
         }
-        const uint32_t there = *(const uint32_t*)&there_at[t & 7][0];
         const bool full = there == 0xffffffffu && vmin >= (t + 1) * KT;
         if (!full) {
             const uint32_t bits = there >> (4 * h);
@@ -305,22 +322,9 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
                 s[i] = (bits >> j & 1u) != 0 && j < lim ? s[i] : -INFINITY;
             }
         }
-        f32x16 n;
-        auto product = [&](auto st) {
-            if constexpr (NEXT) {
-                if constexpr (st == 0) mma_first<E>(n, kf[0], q[0]);
-                else mma_next<E>(n, kf[st % AHEAD], q[st]);
-                DCPA_PIN;
-                if constexpr (st + AHEAD < STEPS) kf[st % AHEAD] = key_fragment(nbuf, st + AHEAD);
-            }
-        };
-        DCPA_PIN;
-        float top = -INFINITY;
-        times<8>([&](auto st) {
-            product(st);
-            top = fmaxf(top, fmaxf(s[2 * st], s[2 * st + 1]));
-            DCPA_PIN;
-        });
+        float top = fmaxf(s[0], -INFINITY);
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
         top = half_max(top) * p.c;
         if (__ballot(top > mc + Mat<E>::kTop + kLazy) != 0) {
             const float next_mc = top > mc + Mat<E>::kTop ? top - Mat<E>::kTop : mc;
@@ -332,25 +336,47 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
         }
         uint32_t pr[8];
         float sum = 0.0f;
+        f32x16 n;
+        u32x4 ql[QL];
+        place_rows(t + 3, page);
+        if constexpr (KV8) fetch(t + 3);
         DCPA_PIN;
-        times<28>([&](auto k) {
-            product(std::integral_constant<int, 8 + k>{});
-            if constexpr (k >= 2 && k < 18) {
-                constexpr int i = k - 2;
-                s[i] = exp2_fast(__builtin_fmaf(s[i], p.c, -mc));
-                sum += s[i];
-                if constexpr (i % 2 == 1) pr[i / 2] = Mat<E>::pack2(s[i - 1], s[i]);
+        times<STEPS>([&](auto st) {
+            if constexpr (NEXT) {
+                if constexpr (st == 0) mma_first<E>(n, kf[0], q[0]);
+                else if constexpr (st < QR) mma_next<E>(n, kf[st % AHEAD], q[st]);
+                else mma_next<E>(n, kf[st % AHEAD], ql[st - QR]);
+                DCPA_PIN;
+                if constexpr (st + AHEAD < STEPS) kf[st % AHEAD] = key_fragment(nbuf, st + AHEAD);
+                if constexpr (st + AHEAD >= QR && st + AHEAD < STEPS) ql[st + AHEAD - QR] = query_s[st + AHEAD - QR][tid];
             }
-            if constexpr (k >= 28 - VAHEAD) vf[k - (28 - VAHEAD)] = value_fragment(buf, k - (28 - VAHEAD));
+            if constexpr (st < 32 && st % 2 == 0) {
+                s[st / 2] = exp2_fast(__builtin_fmaf(s[st / 2], p.c, -mc));
+            } else if constexpr (st < 32) {
+                sum += s[st / 2];
+                if constexpr (st % 4 == 3) pr[st / 4] = Mat<E>::pack2(s[st / 2 - 1], s[st / 2]);
+            }
+            if constexpr (!KV8 && st % 7 == 5) fetch_piece(to, std::integral_constant<int, st / 7>{});
+            if constexpr (st >= STEPS - VAHEAD) vf[st - (STEPS - VAHEAD)] = value_fragment(buf, 2 * (st - (STEPS - VAHEAD)));
             DCPA_PIN;
         });
         l += sum;
+        // (kept from being computed later, between the products that need it)
+        asm volatile("" : "+v"(pr[0]), "+v"(pr[1]), "+v"(pr[2]), "+v"(pr[3]), "+v"(pr[4]), "+v"(pr[5]), "+v"(pr[6]), "+v"(pr[7]));
         const u32x4 p0 = {pr[0], pr[1], pr[2], pr[3]}, p1 = {pr[4], pr[5], pr[6], pr[7]};
         DCPA_PIN;
+        asm volatile("s_nop 1");      // (the weights were written just before)
         times<2 * CBS>([&](auto i) {
-            out_mma<E, i / 2>(vf[i % VAHEAD], i % 2 == 0 ? p0 : p1);
-            if constexpr (i + VAHEAD < 2 * CBS) vf[i % VAHEAD] = value_fragment(buf, i + VAHEAD);
+            // the two halves of the keys one after the other, so that a product does not wait for
+            // the one before it
+            constexpr int half = i / CBS, cb = i % CBS, m = i + VAHEAD;
+            out_mma<E, cb>(vf[i % VAHEAD], half == 0 ? p0 : p1);
+            if constexpr (m < 2 * CBS) vf[i % VAHEAD] = value_fragment(buf, m % CBS * 2 + m / CBS);
             DCPA_PIN;
+            if constexpr (!KV8 && i % 7 == 5 && 5 + i / 7 < 9) {
+                fetch_piece(to, std::integral_constant<int, 5 + i / 7>{});
+                DCPA_PIN;
+            }
         });
         out_claim();
         if (!full) odd |= odd_values<E, false>(buf, MAIN);
@@ -360,6 +386,7 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
         }
     };
 
+    uint32_t at0 = buffer(0), at1 = buffer(1), at2 = buffer(2), at3 = buffer(3);    // of tiles t .. t + 3
 #pragma unroll 1
     for (int t = 0; t < tiles; ++t) {
         out_claim();
@@ -373,57 +400,79 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
         }
         meet();               // tile t + 1 is there, and every wave is done with tile t - 1
         if (t % GROUP == 0 && t + GROUP < tiles) {
-            int32_t x[2];
+            int32_t x[1];
             load_pages(t / GROUP + 1, x);
             keep_pages(t / GROUP + 1, x);
         }
-        if (t + 3 < tiles) {
-            place_rows(t + 3);
-            fetch(t + 3);
-            if constexpr (KV8) rows2 = row_at;
-        } else {
-            dma_wait();       // (nothing follows that the count above could leave out)
-        }
-        out_claim();
+        // (behind the last tile the rows are the row of zeros: the count above stays the same)
         if (work && vmax > t * KT) {
-            if (t + 1 < tiles && vmax > (t + 1) * KT) advance(t, std::true_type{});
-            else advance(t, std::false_type{});
+            if (t + 1 < tiles && vmax > (t + 1) * KT) advance(t, at0, at1, at3, std::true_type{});
+            else advance(t, at0, at1, at3, std::false_type{});
+        } else {
+            place_rows(t + 3, page_for(t + 3));
+            fetch(t + 3);
         }
+        if constexpr (KV8) rows2 = row_at;
+        const uint32_t past = at0;
+        at0 = at1;
+        at1 = at2;
+        at2 = KV8 ? past : at3;
+        at3 = past;
     }
 #undef DCPA_PIN
+    dma_wait();               // nothing may arrive in LDS after the workgroup's end
 
     if (odd) {
-        slow_rows<E, KV8, DK, DV>(p, u, hk, unit, R, row0, row0 + wave_row, min(row0 + wave_row + 32, nrows), k0, k1);
+        meet();               // (the others meet once more before they write)
+        slow_rows<E, KV8, DK, DV>(late_args<AttnArgs>(), u, hk, unit, R, row0, row0 + wave_row, min(row0 + wave_row + 32, nrows), k0, k1);
         return;
     }
     asm volatile("s_nop 15\n\ts_nop 3");
     out_claim();
+    const AttnArgs& e = late_args<AttnArgs>();
     const float lsum = half_sum(l);
     float f, lse2;
-    finish(lsum, mc, p.vs, f, lse2);
-    const int in_tile = wave_row + r, row = row0 + in_tile;
-    if (row >= nrows) return;
-    if (u.splits > 1) {
-        const int64_t at = ((int64_t)hk * p.units + unit) * R + in_tile;
-        float* o = p.ws_o + at * p.Dv + h * 4;
-        if (h == 0) p.ws_l[at] = lse2;
-        times<DV / 8>([&](auto i) {
-            f32x4 x = out_read4<i * 4>();
-            const int col = i * 8;
-            if (lsum == 0.0f) x = f32x4{0, 0, 0, 0};
-            if (col + h * 4 < p.Dv) *(f32x4*)(o + col) = x * f;
-        });
-    } else {
-        const int head = hk * p.m.G + my_row - token * p.m.G;
-        char* o = p.out + (int64_t)(u.s.first + token) * p.o_T + (int64_t)head * p.o_H + h * 8;
-        if (h == 0 && p.lse != nullptr) p.lse[(int64_t)(u.s.first + token) * p.l_T + (int64_t)head * p.l_H] = lse2 * p.lmul;
-        times<DV / 8>([&](auto i) {
-            f32x4 x = out_read4<i * 4>();
-            const int col = i * 8;
-            if (lsum == 0.0f) x = f32x4{0, 0, 0, 0};
-            if (col + h * 4 < p.Dv) store4<E>(o + col * 2, x[0] * f, x[1] * f, x[2] * f, x[3] * f);
-        });
+    finish(lsum, mc, e.vs, f, lse2);
+    const int my = row0 + wave_row + r;
+    const int64_t part = ((int64_t)hk * e.units + unit) * R;
+    const bool split = u.splits > 1;
+    if (h == 0 && my < nrows) {
+        if (split) e.ws_l[part + wave_row + r] = lse2;
+        else if (e.lse != nullptr)
+            e.lse[(int64_t)(u.s.first + token) * e.l_T + (int64_t)(hk * e.m.G + my_row - token * e.m.G) * e.l_H] = lse2 * e.lmul;
     }
+    // The lanes hold columns of a row; through LDS, half the columns at a time, they become
+    // stretches of rows, which are written whole.  (Each wave its own 32 KB; chunk c of row r at c ^ r.)
+    const uint32_t mine = lds0 + (uint32_t)(wave * 32768);
+    int ln = lane;
+    asm volatile("" : "+v"(ln));             // (keeps the addresses below from being held all along)
+    const int er = ln & 31, eh = ln >> 5;
+    static_assert(sizeof(tile) >= 4 * 32768, "room for half the outputs");
+    meet();                   // (other waves may still have been reading tiles, or fallen out)
+    times<2>([&](auto part_of) {
+        constexpr int P = decltype(part_of)::value;
+        times<DV / 16>([&](auto i) {
+            f32x4 x = out_read4<P * (DV / 4) + i * 4>();
+            x = lsum == 0.0f ? f32x4{0, 0, 0, 0} : x * f;
+            lds_write16(mine + (uint32_t)(er * 1024 + ((2 * i + eh) ^ er) * 16), __builtin_bit_cast(u32x4, x));
+        });
+        // (this wave's LDS accesses stay in order)
+#pragma unroll 4
+        for (int k = 0; k < 32; ++k) {
+            const int row = row0 + wave_row + k;
+            if (row >= nrows) break;
+            const f32x4 x = __builtin_bit_cast(f32x4, lds_read16(mine + (uint32_t)(k * 1024 + (ln ^ k) * 16)));
+            const int col = P * (DV / 2) + ln * 4;
+            if (col >= e.Dv) continue;
+            if (split) {
+                *(f32x4*)(e.ws_o + (part + wave_row + k) * e.Dv + col) = x;
+            } else {
+                const int tok = (int)fdiv((uint32_t)row, e.m.fG);
+                store4<E>(e.out + (int64_t)(u.s.first + tok) * e.o_T + (int64_t)(hk * e.m.G + row - tok * e.m.G) * e.o_H + col * 2,
+                          x[0], x[1], x[2], x[3]);
+            }
+        }
+    });
 }
 
 }  // namespace
