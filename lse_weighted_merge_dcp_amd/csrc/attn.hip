@@ -385,7 +385,7 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs p) {
             const Seq s = load_seq(p.m, b);
             here = t >= s.first && t < s.first + s.n;
         }
-        const int incl = base + scan_incl(tiles * splits, lane);
+        const int incl = base + scan_incl(tiles * splits);
         const uint64_t found = __ballot(here);
         if (found == 0) {
             base = __builtin_amdgcn_readlane(incl, 63);

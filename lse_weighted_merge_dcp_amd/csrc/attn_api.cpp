@@ -96,6 +96,7 @@ int check_batch(const dcpa_attn_args* a, Batch& m) {
     m.fG = dcp::make_fastdiv((uint32_t)m.G);
     m.fpage = dcp::make_fastdiv((uint32_t)m.page_size);
     m.fHkv = dcp::make_fastdiv((uint32_t)m.Hkv);
+    m.fblock = dcp::make_fastdiv((uint32_t)(m.N * m.inter));
     return DCP_OK;
 }
 

@@ -178,8 +178,7 @@ template <typename T> __device__ __forceinline__ const T& late_args() {
 // --------------------------------------------------------------------------
 // Positions below x that lie on this rank.
 __device__ __forceinline__ int owned(const Batch& m, int x) {
-    const uint32_t block = (uint32_t)m.N * (uint32_t)m.inter, u = (uint32_t)max(x, 0);
-    const uint32_t full = u / block, rest = u - full * block;
+    const uint32_t u = (uint32_t)max(x, 0), full = fdiv(u, m.fblock), rest = u - full * m.fblock.d;
     return (int)(full * (uint32_t)m.inter) + min(max((int)rest - m.rank * m.inter, 0), m.inter);
 }
 
@@ -211,18 +210,31 @@ __device__ __forceinline__ int visible(const Batch& m, const Seq& s, int i) {
     return min(max(s.kv - hidden, 0), s.kv);
 }
 
-__device__ __forceinline__ int scan_incl(int x, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int y = __shfl_up(x, d, 64);
-        if (lane >= d) x += y;
-    }
+// Inclusive prefix sum over the wave: within rows of 16 lanes, then across them.
+__device__ __forceinline__ int scan_incl(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);    // row_shr 1, 2, 4, 8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);    // lane 15 to row 1, 47 to row 3
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);    // lane 31 to rows 2 and 3
     return x;
 }
-__device__ __forceinline__ int64_t sum_wave(int64_t x) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) x += __shfl_xor((long long)x, d, 64);
-    return x;
+// x plus the x of the lane that CTRL names, over the rows of lanes in ROWS (each half moved as 32 bits)
+template <int CTRL, int ROWS> __device__ __forceinline__ double add_from(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const int lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+    return x + __builtin_bit_cast(double, (uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
+}
+// Sum over the wave of whole numbers that add up to less than 2^53 (exact in a double, whose sum is one
+// instruction and needs no carry)
+__device__ __forceinline__ int64_t sum_wave(int64_t v) {
+    double x = add_from<0x118, 0xf>(add_from<0x114, 0xf>(add_from<0x112, 0xf>(add_from<0x111, 0xf>((double)v))));
+    x = add_from<0x143, 0xc>(add_from<0x142, 0xa>(x));
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    return (int64_t)__builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63) << 32 |
+                                                   (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63));
 }
 
 // The share of a batch that one workgroup takes: row tile `tile` of sequence
@@ -300,7 +312,7 @@ __device__ __forceinline__ Unit find_unit(const Batch& m, int rows, int slots, i
             kv = mine.kv;
         }
         const int splits = max(1, (kv + u.chunk - 1) / u.chunk);
-        const int incl = base + scan_incl(tiles * splits, lane);
+        const int incl = base + scan_incl(tiles * splits);
         const uint64_t past = __ballot(incl > id);
         if (past != 0) {
             const int at = __builtin_ctzll(past);

@@ -109,7 +109,7 @@ __global__ __launch_bounds__(kThreads) void evict_select(EvictArgs p) {
             __syncthreads();
             // thread t takes the two places 2047 - 2t and 2046 - 2t, the largest values first
             const int top = kBins - 1 - 2 * tid;
-            const int c0 = (int)bins[top], c1 = (int)bins[top - 1], incl = scan_incl(c0 + c1, lane);
+            const int c0 = (int)bins[top], c1 = (int)bins[top - 1], incl = scan_incl(c0 + c1);
             if (lane == 63) wave_s[wave] = incl;
             __syncthreads();
             int before = incl - c0 - c1;
@@ -138,7 +138,7 @@ __global__ __launch_bounds__(kThreads) void evict_select(EvictArgs p) {
         if (wave == 0) {
             int carry = 0;
             for (int e0 = 0; e0 < entries; e0 += 64) {
-                const int e = e0 + lane, c = e < entries ? flags_s[e] : 0, incl = scan_incl(c, lane);
+                const int e = e0 + lane, c = e < entries ? flags_s[e] : 0, incl = scan_incl(c);
                 if (e < entries) flags_s[e] = carry + incl - c;
                 carry += __builtin_amdgcn_readlane(incl, 63);
             }

@@ -448,6 +448,11 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
     asm volatile("" : "+v"(ln));             // (keeps the addresses below from being held all along)
     const int er = ln & 31, eh = ln >> 5;
     static_assert(sizeof(tile) >= 4 * 32768, "room for half the outputs");
+    const int Dv = e.Dv;
+    const FastDiv fG = e.m.fG;
+    const int64_t o_T = e.o_T, o_H = e.o_H;
+    char* out = e.out + (int64_t)u.s.first * o_T + (int64_t)hk * e.m.G * o_H;
+    float* parts = e.ws_o + (part + wave_row) * Dv;
     meet();                   // (other waves may still have been reading tiles, or fallen out)
     times<2>([&](auto part_of) {
         constexpr int P = decltype(part_of)::value;
@@ -457,19 +462,25 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
             lds_write16(mine + (uint32_t)(er * 1024 + ((2 * i + eh) ^ er) * 16), __builtin_bit_cast(u32x4, x));
         });
         // (this wave's LDS accesses stay in order)
-#pragma unroll 4
-        for (int k = 0; k < 32; ++k) {
-            const int row = row0 + wave_row + k;
-            if (row >= nrows) break;
-            const f32x4 x = __builtin_bit_cast(f32x4, lds_read16(mine + (uint32_t)(k * 1024 + (ln ^ k) * 16)));
-            const int col = P * (DV / 2) + ln * 4;
-            if (col >= e.Dv) continue;
-            if (split) {
-                *(f32x4*)(e.ws_o + (part + wave_row + k) * e.Dv + col) = x;
-            } else {
-                const int tok = (int)fdiv((uint32_t)row, e.m.fG);
-                store4<E>(e.out + (int64_t)(u.s.first + tok) * e.o_T + (int64_t)(hk * e.m.G + row - tok * e.m.G) * e.o_H + col * 2,
-                          x[0], x[1], x[2], x[3]);
+        const int col = P * (DV / 2) + ln * 4;
+#pragma unroll
+        for (int k0 = 0; k0 < 32; k0 += 8) {
+            f32x4 x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                x[k] = __builtin_bit_cast(f32x4, lds_read16(mine + (uint32_t)((k0 + k) * 1024 + (ln ^ (k0 + k)) * 16)));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int row = row0 + wave_row + k0 + k;
+                if (row < nrows && col < Dv) {
+                    if (split) {
+                        *(f32x4*)(parts + (int64_t)(k0 + k) * Dv + col) = x[k];
+                    } else {
+                        const int tok = (int)fdiv((uint32_t)row, fG);
+                        store4<E>(out + (int64_t)tok * o_T + (int64_t)(row - tok * (int)fG.d) * o_H + col * 2, x[k][0], x[k][1],
+                                  x[k][2], x[k][3]);
+                    }
+                }
             }
         }
     });

@@ -23,7 +23,7 @@ struct Batch {
     int32_t pages, page_size, max_keys;
     int32_t N, rank, inter;
     int32_t causal;
-    FastDiv fG, fpage, fHkv;
+    FastDiv fG, fpage, fHkv, fblock;     // fblock: N * inter
 };
 
 struct AttnArgs {

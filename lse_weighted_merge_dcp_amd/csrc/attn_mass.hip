@@ -75,7 +75,7 @@ template <int KEYS> __device__ __forceinline__ Share find_share(const Batch& m, 
         int n = 0, kv;
         tiles_of(m, b0 + lane, kOneTile, n, kv);
         if (n > 0) n = max(1, (kv + chunk - 1) / chunk);
-        const int incl = base + scan_incl(n, lane);
+        const int incl = base + scan_incl(n);
         const uint64_t past = __ballot(incl > id);
         if (past != 0) {
             const int at = __builtin_ctzll(past);
