@@ -19,8 +19,9 @@ template <int LPR> __device__ __forceinline__ float group_sum(float x) {
 
 // One row: x[s] holds elements 8 (s LPR + lane) .. + 7.
 template <typename E, int LPR, int SLOTS>
-__device__ __forceinline__ void norm_turn(float (&x)[SLOTS][8], int lane, const char* w, int nw, int D, float eps,
+__device__ __forceinline__ void norm_turn(float (&x)[SLOTS][8], int lane, const char* row, const char* w, int nw, float eps,
                                           const float* cs, int off, int rot, bool pairs) {
+    float f = 1.0f;
     if (nw > 0) {
         float sq = 0.0f;
 #pragma unroll
@@ -28,7 +29,7 @@ __device__ __forceinline__ void norm_turn(float (&x)[SLOTS][8], int lane, const 
             if (8 * (s * LPR + lane) < nw)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sq += x[s][i] * x[s][i];
-        const float f = 1.0f / __builtin_sqrtf(group_sum<LPR>(sq) / (float)nw + eps);
+        f = 1.0f / __builtin_sqrtf(group_sum<LPR>(sq) / (float)nw + eps);
 #pragma unroll
         for (int s = 0; s < SLOTS; ++s) {
             const int e0 = 8 * (s * LPR + lane);
@@ -63,14 +64,18 @@ __device__ __forceinline__ void norm_turn(float (&x)[SLOTS][8], int lane, const 
 #pragma unroll
         for (int s = 0; s < SLOTS; ++s) {
             const int chunk = s * LPR + lane, e0 = 8 * chunk - off;
-            const int from = e0 < half ? chunk + step : chunk - step;
+            const int partner = e0 < half ? chunk + step : chunk - step;
+            if constexpr (SLOTS == 1) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                y[s][i] = 0.0f;
+                for (int i = 0; i < 8; ++i) y[s][i] = __shfl(x[s][i], partner & (LPR - 1), LPR);
+            } else if (e0 >= 0 && e0 < rot) {
+                // (read again, out of the cache, and normed alike: which slot holds it differs from lane to lane)
+                dcp::Cvt<E, 16>::unpack(dcp::vload<16>(row + partner * 16), y[s]);
+                if (partner * 8 < nw) {
+                    float g[8];
+                    dcp::Cvt<E, 16>::unpack(dcp::vload<16>(w + partner * 16), g);
 #pragma unroll
-                for (int k = 0; k < SLOTS; ++k) {
-                    const float v = __shfl(x[k][i], from & (LPR - 1), LPR);
-                    if (SLOTS == 1 || from / LPR == k) y[s][i] = v;
+                    for (int i = 0; i < 8; ++i) y[s][i] = y[s][i] * f * g[i];
                 }
             }
         }
@@ -88,16 +93,14 @@ __device__ __forceinline__ void norm_turn(float (&x)[SLOTS][8], int lane, const 
             }
         }
     }
-    (void)D;
 }
 
 template <typename E, bool KV8, int LPR, int SLOTS>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
     constexpr int RPB = 256 / LPR;       // rows of a workgroup
     const int lane = (int)(threadIdx.x % LPR);
-    const int heads = p.Hq + p.Hkv * (p.v != nullptr ? 2 : 1);
-    const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
-    const int token = (int)(row / heads), which = (int)(row - (int64_t)token * heads);
+    const uint32_t row = blockIdx.x * RPB + threadIdx.x / LPR;
+    const int token = (int)fdiv(row, p.fheads), which = (int)(row - (uint32_t)token * p.fheads.d);
     if (token >= p.T) return;
     const int pos = min(max(p.pos[token], 0), p.positions - 1);
     const float* cs = p.cs + (int64_t)pos * p.cs_P;
@@ -131,7 +134,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
         if (e0 < D) dcp::Cvt<E, 16>::unpack(dcp::vload<16>(from + e0 * 2), x[s]);
     }
     if (!value)
-        norm_turn<E, LPR, SLOTS>(x, lane, query ? p.wq : p.wk, query ? p.nq : p.nk, D, p.eps, cs, p.off, p.rot, p.pairs != 0);
+        norm_turn<E, LPR, SLOTS>(x, lane, from, query ? p.wq : p.wk, query ? p.nq : p.nk, p.eps, cs, p.off, p.rot, p.pairs != 0);
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
         const int e0 = 8 * (s * LPR + lane);
@@ -153,9 +156,10 @@ template <typename E, bool KV8> hipError_t run(const RopeArgs& a, hipStream_t st
     const dim3 block(256);
     if (D <= 64) return launch(rope_kernel<E, KV8, 8, 1>, grid(8), block, stream, a);
     if (D <= 128) return launch(rope_kernel<E, KV8, 16, 1>, grid(16), block, stream, a);
-    if (D <= 256) return launch(rope_kernel<E, KV8, 32, 1>, grid(32), block, stream, a);
-    if (D <= 512) return launch(rope_kernel<E, KV8, 64, 1>, grid(64), block, stream, a);
-    return launch(rope_kernel<E, KV8, 64, 2>, grid(64), block, stream, a);
+    if (D <= 256) return launch(rope_kernel<E, KV8, 16, 2>, grid(16), block, stream, a);
+    if (D <= 512) return launch(rope_kernel<E, KV8, 16, 4>, grid(16), block, stream, a);
+    if (D <= 640) return launch(rope_kernel<E, KV8, 16, 5>, grid(16), block, stream, a);
+    return launch(rope_kernel<E, KV8, 16, 8>, grid(16), block, stream, a);
 }
 
 }  // namespace
