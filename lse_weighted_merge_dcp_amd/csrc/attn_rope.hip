@@ -3,8 +3,10 @@
 //
 // A stream: each row (one head of one token) is read once and written once.
 // A group of LPR lanes holds a row, eight elements (16 bytes) to a lane and
-// slot; the mean of squares is one reduction over the group, and the partner of
-// a rotated column in the "halves" layout comes from another lane of the group.
+// slot; the mean of squares is one reduction over the group.  Sixteen lanes to a
+// row of 576 (a 64-lane row left most of its second slot idle: 552 us for 8192 x
+// 129 rows against 433 with 16 lanes, 5.6 TB/s; with eight lanes and nine slots
+// the registers leave two waves to a SIMD: 651 us).
 #include "attn_device.hpp"
 
 namespace dcpa {
@@ -17,85 +19,19 @@ template <int LPR> __device__ __forceinline__ float group_sum(float x) {
     return x;
 }
 
-// One row: x[s] holds elements 8 (s LPR + lane) .. + 7.
-template <typename E, int LPR, int SLOTS>
-__device__ __forceinline__ void norm_turn(float (&x)[SLOTS][8], int lane, const char* row, const char* w, int nw, float eps,
-                                          const float* cs, int off, int rot, bool pairs) {
-    float f = 1.0f;
-    if (nw > 0) {
-        float sq = 0.0f;
+// Eight elements from column e0 on, times the row's factor and the weights.
+template <typename E>
+__device__ __forceinline__ void norm8(const dcp::Vec<16>& raw, int e0, const char* w, int nw, float f, float (&x)[8]) {
+    dcp::Cvt<E, 16>::unpack(raw, x);
+    if (e0 < nw) {
+        float g[8];
+        dcp::Cvt<E, 16>::unpack(dcp::vload<16>(w + e0 * 2), g);
 #pragma unroll
-        for (int s = 0; s < SLOTS; ++s)
-            if (8 * (s * LPR + lane) < nw)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sq += x[s][i] * x[s][i];
-        f = 1.0f / __builtin_sqrtf(group_sum<LPR>(sq) / (float)nw + eps);
-#pragma unroll
-        for (int s = 0; s < SLOTS; ++s) {
-            const int e0 = 8 * (s * LPR + lane);
-            if (e0 < nw) {
-                float g[8];
-                dcp::Cvt<E, 16>::unpack(dcp::vload<16>(w + e0 * 2), g);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[s][i] = x[s][i] * f * g[i];
-            }
-        }
-    }
-    if (rot == 0) return;
-    const int half = rot / 2;
-    if (pairs) {
-#pragma unroll
-        for (int s = 0; s < SLOTS; ++s) {
-            const int e0 = 8 * (s * LPR + lane) - off;
-            if (e0 >= 0 && e0 < rot) {
-                const f32x4 c = *(const f32x4*)(cs + e0 / 2), n = *(const f32x4*)(cs + half + e0 / 2);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a = x[s][2 * i], b = x[s][2 * i + 1];
-                    x[s][2 * i] = a * c[i] - b * n[i];
-                    x[s][2 * i + 1] = b * c[i] + a * n[i];
-                }
-            }
-        }
-    } else {
-        // the partner stands half a range away: the same place of another chunk
-        const int step = half / 8;
-        float y[SLOTS][8];
-#pragma unroll
-        for (int s = 0; s < SLOTS; ++s) {
-            const int chunk = s * LPR + lane, e0 = 8 * chunk - off;
-            const int partner = e0 < half ? chunk + step : chunk - step;
-            if constexpr (SLOTS == 1) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[s][i] = __shfl(x[s][i], partner & (LPR - 1), LPR);
-            } else if (e0 >= 0 && e0 < rot) {
-                // (read again, out of the cache, and normed alike: which slot holds it differs from lane to lane)
-                dcp::Cvt<E, 16>::unpack(dcp::vload<16>(row + partner * 16), y[s]);
-                if (partner * 8 < nw) {
-                    float g[8];
-                    dcp::Cvt<E, 16>::unpack(dcp::vload<16>(w + partner * 16), g);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) y[s][i] = y[s][i] * f * g[i];
-                }
-            }
-        }
-#pragma unroll
-        for (int s = 0; s < SLOTS; ++s) {
-            const int e0 = 8 * (s * LPR + lane) - off;
-            if (e0 >= 0 && e0 < rot) {
-                const bool low = e0 < half;
-                const int j = low ? e0 : e0 - half;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float c = cs[j + i], n = cs[half + j + i];
-                    x[s][i] = low ? x[s][i] * c - y[s][i] * n : x[s][i] * c + y[s][i] * n;
-                }
-            }
-        }
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * f * g[i];
     }
 }
 
-template <typename E, bool KV8, int LPR, int SLOTS>
+template <typename E, bool KV8, bool PAIRS, int LPR, int SLOTS>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
     constexpr int RPB = 256 / LPR;       // rows of a workgroup
     const int lane = (int)(threadIdx.x % LPR);
@@ -125,48 +61,107 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
         narrow = KV8;
         scale = value ? p.iv : p.ik;
     }
-    float x[SLOTS][8];
+    // the row as it was read; its pieces are widened one at a time, so that more rows are under way
+    dcp::Vec<16> raw[SLOTS];
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
         const int e0 = 8 * (s * LPR + lane);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[s][i] = 0.0f;
-        if (e0 < D) dcp::Cvt<E, 16>::unpack(dcp::vload<16>(from + e0 * 2), x[s]);
+        if (e0 < D) raw[s] = dcp::vload<16>(from + e0 * 2);
+        else raw[s].w[0] = raw[s].w[1] = raw[s].w[2] = raw[s].w[3] = 0;
     }
-    if (!value)
-        norm_turn<E, LPR, SLOTS>(x, lane, from, query ? p.wq : p.wk, query ? p.nq : p.nk, p.eps, cs, p.off, p.rot, p.pairs != 0);
+    const char* w = query ? p.wq : p.wk;
+    const int nw = value ? 0 : query ? p.nq : p.nk, rot = value ? 0 : p.rot, half = rot / 2;
+    // Where the partner stands half a range away it is the same place of another piece, in a slot that differs
+    // from lane to lane: it is read again, out of the cache, and before any store (the row may be written in place).
+    auto partner = [&](int s) { return 8 * (s * LPR + lane) + (8 * (s * LPR + lane) - p.off < half ? half : -half); };
+    dcp::Vec<16> other[SLOTS];
+    if constexpr (SLOTS > 1 && !PAIRS)
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+            const int at = 8 * (s * LPR + lane) - p.off;
+            if (at >= 0 && at < rot) other[s] = dcp::vload<16>(from + partner(s) * 2);
+        }
+    float f = 1.0f;
+    if (nw > 0) {
+        float sq = 0.0f;
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+            if (8 * (s * LPR + lane) < nw) {
+                float x[8];
+                dcp::Cvt<E, 16>::unpack(raw[s], x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sq += x[i] * x[i];
+            }
+        f = 1.0f / __builtin_sqrtf(group_sum<LPR>(sq) / (float)nw + p.eps);
+    }
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
-        const int e0 = 8 * (s * LPR + lane);
+        if constexpr (SLOTS > 1) asm volatile("" : "+v"(raw[s].w[0]), "+v"(raw[s].w[1]), "+v"(raw[s].w[2]), "+v"(raw[s].w[3]));
+        const int e0 = 8 * (s * LPR + lane), at = e0 - p.off;
+        float x[8];
+        norm8<E>(raw[s], e0, w, nw, f, x);
+        const bool turned = at >= 0 && at < rot;
+        if constexpr (PAIRS) {
+            if (turned) {
+                const f32x4 c = *(const f32x4*)(cs + at / 2), n = *(const f32x4*)(cs + half + at / 2);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float a = x[2 * i], b = x[2 * i + 1];
+                    x[2 * i] = a * c[i] - b * n[i];
+                    x[2 * i + 1] = b * c[i] + a * n[i];
+                }
+            }
+        } else {
+            const bool low = at < half;
+            float y[8];
+            if constexpr (SLOTS == 1) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = __shfl(x[i], partner(s) / 8 & (LPR - 1), LPR);
+            } else if (turned) {
+                norm8<E>(other[s], partner(s), w, nw, f, y);
+            }
+            if (turned) {
+                const int j = low ? at : at - half;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float c = cs[j + i], n = cs[half + j + i];
+                    x[i] = low ? x[i] * c - y[i] * n : x[i] * c + y[i] * n;
+                }
+            }
+        }
         if (e0 >= D) continue;
         if (KV8 && narrow) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[s][i] *= scale;
-            dcp::vstore<8>(to + e0, dcp::Cvt<dcp::FP8T, 8>::pack(x[s]));
+            for (int i = 0; i < 8; ++i) x[i] *= scale;
+            dcp::vstore<8>(to + e0, dcp::Cvt<dcp::FP8T, 8>::pack(x));
         } else {
-            dcp::vstore<16>(to + e0 * 2, dcp::Cvt<E, 16>::pack(x[s]));
+            dcp::vstore<16>(to + e0 * 2, dcp::Cvt<E, 16>::pack(x));
         }
     }
 }
 
-template <typename E, bool KV8> hipError_t run(const RopeArgs& a, hipStream_t stream) {
+template <typename E, bool KV8, bool PAIRS> hipError_t run(const RopeArgs& a, hipStream_t stream) {
     const int D = a.v != nullptr && a.Dv > a.D ? a.Dv : a.D;
     const int64_t rows = (int64_t)a.T * (a.Hq + a.Hkv * (a.v != nullptr ? 2 : 1));
     auto grid = [&](int lpr) { return dim3((uint32_t)((rows * lpr + 255) / 256)); };
     const dim3 block(256);
-    if (D <= 64) return launch(rope_kernel<E, KV8, 8, 1>, grid(8), block, stream, a);
-    if (D <= 128) return launch(rope_kernel<E, KV8, 16, 1>, grid(16), block, stream, a);
-    if (D <= 256) return launch(rope_kernel<E, KV8, 16, 2>, grid(16), block, stream, a);
-    if (D <= 512) return launch(rope_kernel<E, KV8, 16, 4>, grid(16), block, stream, a);
-    if (D <= 640) return launch(rope_kernel<E, KV8, 16, 5>, grid(16), block, stream, a);
-    return launch(rope_kernel<E, KV8, 16, 8>, grid(16), block, stream, a);
+    if (D <= 64) return launch(rope_kernel<E, KV8, PAIRS, 8, 1>, grid(8), block, stream, a);
+    if (D <= 128) return launch(rope_kernel<E, KV8, PAIRS, 16, 1>, grid(16), block, stream, a);
+    if (D <= 256) return launch(rope_kernel<E, KV8, PAIRS, 16, 2>, grid(16), block, stream, a);
+    if (D <= 512) return launch(rope_kernel<E, KV8, PAIRS, 16, 4>, grid(16), block, stream, a);
+    if (D <= 640) return launch(rope_kernel<E, KV8, PAIRS, 16, 5>, grid(16), block, stream, a);
+    return launch(rope_kernel<E, KV8, PAIRS, 16, 8>, grid(16), block, stream, a);
 }
 
 }  // namespace
 
 hipError_t launch_rope(const RopeArgs& a, bool bf16, bool kv8, hipStream_t stream) {
-    if (bf16) return kv8 ? run<BF16T, true>(a, stream) : run<BF16T, false>(a, stream);
-    return kv8 ? run<F16T, true>(a, stream) : run<F16T, false>(a, stream);
+    if (a.pairs != 0) {
+        if (bf16) return kv8 ? run<BF16T, true, true>(a, stream) : run<BF16T, false, true>(a, stream);
+        return kv8 ? run<F16T, true, true>(a, stream) : run<F16T, false, true>(a, stream);
+    }
+    if (bf16) return kv8 ? run<BF16T, true, false>(a, stream) : run<BF16T, false, false>(a, stream);
+    return kv8 ? run<F16T, true, false>(a, stream) : run<F16T, false, false>(a, stream);
 }
 
 }  // namespace dcpa

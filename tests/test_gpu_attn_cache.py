@@ -134,6 +134,24 @@ def test_norm_rope_in_place_strided_and_far_positions(dev):
     assert torch.equal(fd.cpu()[:, Hq * D:], fused[:, Hq * D:])
 
 
+@pytest.mark.parametrize("pairs", [False, True], ids=["halves", "pairs"])
+@pytest.mark.parametrize("D,off,rot", [(64, 0, 64), (256, 0, 256), (576, 64, 512), (1024, 0, 1024), (512, 480, 32)])
+def test_norm_rope_in_place_of_every_width(dev, D, off, rot, pairs):
+    """In place and into a tensor of its own give the same bits: no piece is read after it was turned."""
+    g = torch.Generator().manual_seed(D)
+    T, Hq = 300, 3
+    q, k = torch.randn(T, Hq, D, generator=g).to(BF), torch.randn(T, 1, D, generator=g).to(BF)
+    w = (1 + 0.2 * torch.randn(D, generator=g)).to(BF)
+    cs, pos = rope_table(64, rot), torch.randint(0, 64, (T,), generator=g).to(torch.int32)
+    d = lambda t: t.to(dev)  # noqa: E731
+    qd, kc, slots = d(q), torch.zeros(T, 1, 1, D, dtype=BF, device=dev), torch.arange(T, device=dev)
+    kw = dict(rope_offset=off, interleaved=pairs)
+    apart = attn.qk_norm_rope_append(qd, d(k), None, d(w), d(w), d(pos), d(cs), slots, kc, None, **kw)
+    near(apart.cpu(), oracle.norm_rope(q, w, 1e-6, cs, pos, off, pairs), BF)
+    attn.qk_norm_rope_append(qd, d(k), None, d(w), d(w), d(pos), d(cs), slots, kc, None, q_out=qd, **kw)
+    assert torch.equal(qd, apart)
+
+
 # ---------------------------------------------------------------------------
 # accumulated weights
 # ---------------------------------------------------------------------------
