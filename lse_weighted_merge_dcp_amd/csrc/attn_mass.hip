@@ -56,6 +56,7 @@ __device__ __forceinline__ void share_out(const Batch& m, int slots, bool split_
     if (!split_rows) return;
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) most = max(most, __shfl_xor(most, d, 64));
+    most = __builtin_amdgcn_readfirstlane(most);
     // (at least four row tiles to a part)
     const int64_t tiles = ((int64_t)most * m.G + 127) / 128;
     parts = (int)max((int64_t)1, min(slots / max((int64_t)1, steps), tiles));
@@ -99,11 +100,17 @@ __device__ __forceinline__ float* mass_at(const MassArgs& p, int b, int hk, int 
     return p.mass + (int64_t)id * p.m_P + (int64_t)(key - (int)(page * p.m.fpage.d)) * p.m_S + (int64_t)hk * p.m_H;
 }
 
-// KW keys to a wave.
+// KW keys to a wave.  The weights of one tile of rows are worked out between the
+// matrix instructions of the next, whose scores go to the other of two sets of
+// registers: alone, a SIMD takes 16 clocks for 64 weights (8 of them the power)
+// and 16 for the products of 64 scores at 128 columns; in turn, with a barrier
+// to a tile, two waves to a SIMD overlapped them by less than half (159 us for
+// 2 x 4096 rows against 2 x 8192 keys of 8 heads).
 template <typename E, bool KV8, int DK, int KW>
-__global__ __launch_bounds__(256, 2) void mass_rows(MassArgs p) {
+__global__ __launch_bounds__(256, DK > 256 ? 1 : 2) void mass_rows(MassArgs p) {
     constexpr int KEYS = 4 * KW, NB = KW / 32, ST = DK / 16, KC = DK / 8, QROW = KC * 16, QB = 32 * QROW, NQ = 32 * KC / 256 + (32 * KC % 256 != 0);
     constexpr int PAD = NQ * 256 * 16;         // whole rounds of the workgroup
+    constexpr int AHEAD = 3;                   // query fragments read ahead of their products
     __shared__ __attribute__((aligned(1024))) char qtile[2][PAD];
     static_assert(QB <= PAD, "a tile of queries fits");
     const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv);
@@ -116,20 +123,21 @@ __global__ __launch_bounds__(256, 2) void mass_rows(MassArgs p) {
 
     // the wave's keys from k0 on as A operands; absent ones are zeros (and masked by their place)
     auto load_keys = [&](int k0, u32x4 (&kf)[NB][ST], uint32_t (&there)[NB]) {
+        const MassArgs& e = late_args<MassArgs>();
 #pragma unroll
         for (int kb = 0; kb < NB; ++kb) {
             const int key = k0 + wave * KW + kb * 32 + r;
-            const uint32_t page = fdiv((uint32_t)key, p.m.fpage);
+            const uint32_t page = fdiv((uint32_t)key, e.m.fpage);
             const int id = key < u.k1 ? table[page] : -1;
-            const bool have = (uint32_t)id < (uint32_t)p.m.pages;
+            const bool have = (uint32_t)id < (uint32_t)e.m.pages;
             there[kb] = (uint32_t)__ballot(h == 0 && have);
-            const uint64_t row = have ? (uint64_t)(p.k + (int64_t)id * p.k_P +
-                                                   (int64_t)(key - (int)(page * p.m.fpage.d)) * p.k_S + (int64_t)hk * p.k_H)
+            const uint64_t row = have ? (uint64_t)(e.k + (int64_t)id * e.k_P +
+                                                   (int64_t)(key - (int)(page * e.m.fpage.d)) * e.k_S + (int64_t)hk * e.k_H)
                                       : (uint64_t)kZeros;
 #pragma unroll
             for (int s = 0; s < ST; ++s) {
                 const int c = 2 * s + h;
-                const uint64_t at = at_or_zeros(c * 8 < p.Dk, row + (uint64_t)(c * (KV8 ? 8 : 16)));
+                const uint64_t at = at_or_zeros(c * 8 < e.Dk, row + (uint64_t)(c * (KV8 ? 8 : 16)));
                 if constexpr (KV8) {
                     const u32x2 x = *(const u32x2*)at;
                     kf[kb][s].x = x.x;
@@ -141,29 +149,49 @@ __global__ __launch_bounds__(256, 2) void mass_rows(MassArgs p) {
         }
     };
     const uint32_t lds0 = lds_addr(&qtile[0][0]);
-    auto row_place = [&](int row, int& token, int& head) {
-        row = min(row, nrows - 1);
-        token = (int)fdiv((uint32_t)row, p.m.fG);
-        head = hk * p.m.G + row - token * p.m.G;
+    // Rows follow each other tile by tile, 32 on: their token and head are carried along, since the
+    // division and the products of an address take 16 clocks each.
+    struct Place {
+        int row, sub;       // of the sequence; head within the key head's
+        uint64_t at;
     };
-    // row tile t into buffer b
-    auto fetch = [&](int t, int b) {
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-            const int ch = i * 256 + tid, row = min(ch / KC, 31), c = (ch % KC) ^ swz<KC>(row);
-            int token, head;
-            row_place(t * 32 + row, token, head);
-            const uint64_t at = (uint64_t)(p.q + (int64_t)(u.s.first + token) * p.q_T + (int64_t)head * p.q_H) + (uint64_t)(c * 16);
-            dma16((const char*)at_or_zeros(c * 8 < p.Dk, at),
-                  __builtin_amdgcn_readfirstlane(lds0 + (uint32_t)(b * PAD + (i * 256 + wave * 64) * 16)));
+    const int G = p.m.G, next_t = (int)fdiv(32u, p.m.fG), next_g = 32 - next_t * G;
+    auto place_of = [&](int row, const void* base, int64_t s_T, int64_t s_H) {
+        const int token = (int)fdiv((uint32_t)row, p.m.fG), g = row - token * G;
+        return Place{row, g, (uint64_t)base + (uint64_t)((u.s.first + token) * s_T + (hk * G + g) * s_H)};
+    };
+    auto advance = [&](Place& x, int64_t s_T, int64_t s_H) {
+        const int64_t on = next_t * s_T + next_g * s_H, wrap = s_T - G * s_H;
+        x.row += 32;
+        x.sub += next_g;
+        x.at += (uint64_t)on;
+        if (x.sub >= G) {
+            x.sub -= G;
+            x.at += (uint64_t)wrap;
         }
     };
-    // what the lane's row of tile t sees, and its log-sum-exp in powers of two
-    auto row_of = [&](int t, int& vis, float& g) {
-        int token, head;
-        row_place(t * 32 + r, token, head);
-        vis = t * 32 + r < nrows ? visible(p.m, u.s, token) : 0;
-        g = p.lse[(int64_t)(u.s.first + token) * p.l_T + (int64_t)head * p.l_H];
+    // the pieces of the row tile that this lane brings, and the row that it weighs
+    Place piece[NQ], mine;
+    auto start_at = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            const int ch = i * 256 + tid, row = ch / KC;
+            piece[i] = place_of(t * 32 + row, p.q + ((ch % KC) ^ swz<KC>(row)) * 16, p.q_T, p.q_H);
+        }
+        mine = place_of(t * 32 + r, p.lse, p.l_T * 4, p.l_H * 4);
+    };
+    // the row tile that is due into buffer b, and this lane's log-sum-exp in powers of two (a row that saw
+    // nothing anywhere gives nothing)
+    auto fetch = [&](int b, float& g) {
+        g = mine.row < nrows ? *(const __attribute__((address_space(1))) float*)mine.at : 0.0f;
+        advance(mine, p.l_T * 4, p.l_H * 4);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            const int ch = i * 256 + tid, row = ch / KC;
+            dma16((const char*)at_or_zeros((((ch % KC) ^ swz<KC>(row)) * 8 < p.Dk) & (row < 32) & (piece[i].row < nrows), piece[i].at),
+                  __builtin_amdgcn_readfirstlane(lds0 + (uint32_t)(b * PAD + (i * 256 + wave * 64) * 16)));
+            advance(piece[i], p.q_T, p.q_H);
+        }
     };
 
     // rows that see none of the range come first: skip their tiles
@@ -177,79 +205,94 @@ __global__ __launch_bounds__(256, 2) void mass_rows(MassArgs p) {
     const bool single = end_tile - begin <= 1;     // one tile of rows for all the keys: it stays in LDS
     u32x4 kf[NB][ST];
     uint32_t there[NB];
+    int buf = 0;
+    float g_next = 0.0f;
     if (begin < end_tile) {
-        fetch(begin, 0);
+        start_at(begin);
+        fetch(0, g_next);
         load_keys(u.k0, kf, there);
     }
-    int buf = 0, vis_next = 0;
-    float g_next = 0.0f;
-    if (begin < end_tile) row_of(begin, vis_next, g_next);
 #pragma unroll 1
     for (int k0 = u.k0; k0 < u.k1; k0 += KEYS) {
+        const int key0 = k0 + wave * KW;
         float acc[NB][16];
+        f32x16 s0[NB], s1[NB];
 #pragma unroll
         for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[kb][i] = 0.0f;
+            for (int i = 0; i < 16; ++i) acc[kb][i] = s0[kb][i] = s1[kb][i] = 0.0f;
         if constexpr (KV8) {
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
                 for (int s = 0; s < ST; ++s) kf[kb][s] = widen8<E>(u32x2{kf[kb][s].x, kf[kb][s].y});
         }
-#pragma unroll 1
-        for (int t = begin; t < end_tile; ++t) {
+        float g_old = INFINITY;       // (the first time there is nothing to weigh)
+        auto weigh = [&](const f32x16 (&s)[NB], int j) {
+            acc[j / 16][j % 16] += exp2_fast(__builtin_fmaf(s[j / 16][j % 16], p.c, -g_old));
+            asm volatile("" : "+v"(acc[j / 16][j % 16]));     // (here, not where the sum is next used)
+        };
+        auto step = [&](int t, f32x16 (&now)[NB], const f32x16 (&old)[NB]) {
             if (!single || k0 == u.k0) {
                 dma_wait();
                 meet();       // tile t is there, and the other buffer is free
             }
-            const int vis = vis_next;
-            // (a row that saw nothing anywhere gives nothing)
-            const float g = g_next == -INFINITY ? INFINITY : g_next * p.lmul;
-            const int now = buf;
+            const float g = g_next;
+            const uint32_t qrow = lds0 + (uint32_t)(buf * PAD + r * QROW);
             if (!single) {
-                const bool wrap = t + 1 == end_tile, more = !wrap || k0 + KEYS < u.k1;
-                if (more) {
-                    row_of(wrap ? begin : t + 1, vis_next, g_next);
-                    fetch(wrap ? begin : t + 1, buf ^ 1);
-                }
+                const bool wrap = t + 1 == end_tile;
+                if (wrap) start_at(begin);
                 buf ^= 1;
+                if (!wrap || k0 + KEYS < u.k1) fetch(buf, g_next);
             }
-            const int key0 = k0 + wave * KW;
-            // rows are in the order of their tokens; those behind the last see nothing
-            if (__builtin_amdgcn_readlane(vis, min(31, nrows - 1 - t * 32)) <= key0) continue;
-            const bool all = t * 32 + 31 < nrows && __builtin_amdgcn_readlane(vis, 0) >= key0 + KW;
-            f32x16 s[NB];
+            u32x4 b[ST];
 #pragma unroll
-            for (int kb = 0; kb < NB; ++kb)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s[kb][i] = 0.0f;
-            const uint32_t qrow = lds0 + (uint32_t)(now * PAD + r * QROW);
+            for (int k = 0; k < AHEAD && k < ST; ++k) b[k] = lds_read16(qrow + (uint32_t)(((2 * k + h) ^ swz<KC>(r)) * 16));
 #pragma unroll
             for (int k = 0; k < ST; ++k) {
-                const u32x4 b = lds_read16(qrow + (uint32_t)(((2 * k + h) ^ swz<KC>(r)) * 16));
+                if (k + AHEAD < ST) b[k + AHEAD] = lds_read16(qrow + (uint32_t)(((2 * (k + AHEAD) + h) ^ swz<KC>(r)) * 16));
 #pragma unroll
-                for (int kb = 0; kb < NB; ++kb) s[kb] = Mat<E>::mma(kf[kb][k], b, s[kb]);
-            }
+                for (int kb = 0; kb < NB; ++kb) {
+                    now[kb] = k == 0 ? Mat<E>::mma(kf[kb][k], b[k], f32x16{}) : Mat<E>::mma(kf[kb][k], b[k], now[kb]);
+                    const int part = k * NB + kb, all = NB * 16;
 #pragma unroll
-            for (int kb = 0; kb < NB; ++kb) {
-                if (all) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[kb][i] += exp2_fast(__builtin_fmaf(s[kb][i], p.c, -g));
-                } else {
-                    const int lim = vis - key0 - kb * 32 - 4 * h;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float x = exp2_fast(__builtin_fmaf(s[kb][i], p.c, -g));
-                        acc[kb][i] += 8 * (i / 4) + i % 4 < lim ? x : 0.0f;
-                    }
+                    for (int j = part * all / (ST * NB); j < (part + 1) * all / (ST * NB); ++j) weigh(old, j);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
+            g_old = g == -INFINITY ? INFINITY : g * p.lmul;
+            // rows are in the order of their tokens: where the first sees all of the wave's keys, so do the
+            // others, but for those behind the last, which see nothing
+            if (t * 32 + 31 >= nrows || visible(p.m, u.s, (int)fdiv((uint32_t)(t * 32), p.m.fG)) < key0 + KW) {
+                const int row = t * 32 + r;
+                const int lim = row < nrows ? visible(p.m, u.s, (int)fdiv((uint32_t)row, p.m.fG)) - key0 - 4 * h : 0;
+                // (a row whose sum is NaN gives NaN to what it sees and nothing to the rest)
+                const bool bad = g_old != g_old;
+                if (bad) g_old = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NB * 16; ++j) {
+                    const float seen = bad ? NAN : now[j / 16][j % 16];
+                    now[j / 16][j % 16] = j / 16 * 32 + 8 * (j % 16 / 4) + j % 4 < lim ? seen : -INFINITY;
+                }
+            }
+        };
+        auto finish = [&](const f32x16 (&s)[NB]) {
+#pragma unroll
+            for (int j = 0; j < NB * 16; ++j) weigh(s, j);
+        };
+#pragma unroll 1
+        for (int t = begin; t < end_tile; t += 2) {
+            step(t, s0, s1);
+            if (t + 1 == end_tile) break;
+            step(t + 1, s1, s0);
         }
+        if ((end_tile - begin) % 2 != 0) finish(s0);
+        else finish(s1);
+        const MassArgs& e = late_args<MassArgs>();
         // totals over the 32 query lanes; lane i of each half takes register i
 #pragma unroll
         for (int kb = 0; kb < NB; ++kb) {
-            float mine = 0.0f;
+            float total = 0.0f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 float x = acc[kb][i];
@@ -257,15 +300,15 @@ __global__ __launch_bounds__(256, 2) void mass_rows(MassArgs p) {
                 x += dcp::dpp_f<0x124>(x);
                 x += dcp::dpp_f<0x122>(x);
                 x += dcp::dpp_f<0x121>(x);
-                mine = (lane & 15) == i ? x : mine;
+                total = (lane & 15) == i ? x : total;
             }
-            mine += __shfl_xor(mine, 16, 64);
+            total += __shfl_xor(total, 16, 64);
             if (r < 16) {
                 const int place = kb * 32 + 8 * (r / 4) + r % 4 + 4 * h, k = k0 + wave * KW + place;
                 if (u.parts > 1) {
-                    p.ws[(((int64_t)u.slot * p.m.Hkv + hk) * u.parts + u.part) * KEYS + wave * KW + place] = mine;
+                    e.ws[(((int64_t)u.slot * e.m.Hkv + hk) * u.parts + u.part) * KEYS + wave * KW + place] = total;
                 } else if (k < u.k1 && (there[kb] >> (place & 31) & 1u) != 0) {
-                    *mass_at(p, u.b, hk, k) += mine;
+                    *mass_at(e, u.b, hk, k) += total;
                 }
             }
         }
