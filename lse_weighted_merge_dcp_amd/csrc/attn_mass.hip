@@ -149,47 +149,46 @@ __global__ __launch_bounds__(256, DK > 256 ? 1 : 2) void mass_rows(MassArgs p) {
         }
     };
     const uint32_t lds0 = lds_addr(&qtile[0][0]);
-    // Rows follow each other tile by tile, 32 on: their token and head are carried along, since the
-    // division and the products of an address take 16 clocks each.
+    // Rows follow each other tile by tile, 32 on: their addresses are carried along, since the division and
+    // the products of an address take 16 clocks each.
     struct Place {
-        int row, sub;       // of the sequence; head within the key head's
+        int row, sub;       // of the tile; head within the key head's
         uint64_t at;
     };
     const int G = p.m.G, next_t = (int)fdiv(32u, p.m.fG), next_g = 32 - next_t * G;
-    auto place_of = [&](int row, const void* base, int64_t s_T, int64_t s_H) {
-        const int token = (int)fdiv((uint32_t)row, p.m.fG), g = row - token * G;
+    auto place_of = [&](int t, int row, const void* base, int64_t s_T, int64_t s_H) {
+        const int token = (int)fdiv((uint32_t)(t * 32 + row), p.m.fG), g = t * 32 + row - token * G;
         return Place{row, g, (uint64_t)base + (uint64_t)((u.s.first + token) * s_T + (hk * G + g) * s_H)};
     };
     auto advance = [&](Place& x, int64_t s_T, int64_t s_H) {
-        const int64_t on = next_t * s_T + next_g * s_H, wrap = s_T - G * s_H;
-        x.row += 32;
-        x.sub += next_g;
-        x.at += (uint64_t)on;
-        if (x.sub >= G) {
-            x.sub -= G;
-            x.at += (uint64_t)wrap;
+        x.at += (uint64_t)(next_t * s_T + next_g * s_H);
+        if (next_g != 0) {
+            x.sub += next_g;
+            const bool wrap = x.sub >= G;
+            x.sub -= wrap ? G : 0;
+            x.at += wrap ? (uint64_t)(s_T - G * s_H) : 0;
         }
     };
-    // the pieces of the row tile that this lane brings, and the row that it weighs
+    // the pieces of the row tile that this lane brings (columns that are not there: a row that never is), and
+    // the row that it weighs
     Place piece[NQ], mine;
     auto start_at = [&](int t) {
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
-            const int ch = i * 256 + tid, row = ch / KC;
-            piece[i] = place_of(t * 32 + row, p.q + ((ch % KC) ^ swz<KC>(row)) * 16, p.q_T, p.q_H);
+            const int ch = i * 256 + tid, row = min(ch / KC, 31), c = (ch % KC) ^ swz<KC>(row);
+            piece[i] = place_of(t, row, p.q + c * 16, p.q_T, p.q_H);
+            if (c * 8 >= p.Dk) piece[i].row = 32;
         }
-        mine = place_of(t * 32 + r, p.lse, p.l_T * 4, p.l_H * 4);
+        mine = place_of(t, r, p.lse, p.l_T * 4, p.l_H * 4);
     };
-    // the row tile that is due into buffer b, and this lane's log-sum-exp in powers of two (a row that saw
-    // nothing anywhere gives nothing)
-    auto fetch = [&](int b, float& g) {
-        g = mine.row < nrows ? *(const __attribute__((address_space(1))) float*)mine.at : 0.0f;
+    // row tile t, whose turn it is, into buffer b, and this lane's log-sum-exp in powers of two
+    auto fetch = [&](int t, int b, float& g) {
+        const int left = min(nrows - t * 32, 32);
+        g = *(const __attribute__((address_space(1))) float*)at_or_zeros(mine.row < left, mine.at);
         advance(mine, p.l_T * 4, p.l_H * 4);
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
-            const int ch = i * 256 + tid, row = ch / KC;
-            dma16((const char*)at_or_zeros((((ch % KC) ^ swz<KC>(row)) * 8 < p.Dk) & (row < 32) & (piece[i].row < nrows), piece[i].at),
-                  __builtin_amdgcn_readfirstlane(lds0 + (uint32_t)(b * PAD + (i * 256 + wave * 64) * 16)));
+            dma16((const char*)at_or_zeros(piece[i].row < left, piece[i].at), lds0 + (uint32_t)(b * PAD + (i * 256 + wave * 64) * 16));
             advance(piece[i], p.q_T, p.q_H);
         }
     };
@@ -205,15 +204,18 @@ __global__ __launch_bounds__(256, DK > 256 ? 1 : 2) void mass_rows(MassArgs p) {
     const bool single = end_tile - begin <= 1;     // one tile of rows for all the keys: it stays in LDS
     u32x4 kf[NB][ST];
     uint32_t there[NB];
-    int buf = 0;
     float g_next = 0.0f;
-    if (begin < end_tile) {
-        start_at(begin);
-        fetch(0, g_next);
-        load_keys(u.k0, kf, there);
-    }
 #pragma unroll 1
     for (int k0 = u.k0; k0 < u.k1; k0 += KEYS) {
+        const bool fresh = !single || k0 == u.k0;
+        if (begin < end_tile) {
+            if (fresh) {
+                meet();       // (other waves may still read the last keys' tiles)
+                start_at(begin);
+                fetch(begin, 0, g_next);
+            }
+            load_keys(k0, kf, there);
+        }
         const int key0 = k0 + wave * KW;
         float acc[NB][16];
         f32x16 s0[NB], s1[NB];
@@ -232,19 +234,14 @@ __global__ __launch_bounds__(256, DK > 256 ? 1 : 2) void mass_rows(MassArgs p) {
             acc[j / 16][j % 16] += exp2_fast(__builtin_fmaf(s[j / 16][j % 16], p.c, -g_old));
             asm volatile("" : "+v"(acc[j / 16][j % 16]));     // (here, not where the sum is next used)
         };
-        auto step = [&](int t, f32x16 (&now)[NB], const f32x16 (&old)[NB]) {
-            if (!single || k0 == u.k0) {
+        auto step = [&](int t, int buf, f32x16 (&now)[NB], const f32x16 (&old)[NB]) {
+            if (fresh) {
                 dma_wait();
                 meet();       // tile t is there, and the other buffer is free
             }
             const float g = g_next;
             const uint32_t qrow = lds0 + (uint32_t)(buf * PAD + r * QROW);
-            if (!single) {
-                const bool wrap = t + 1 == end_tile;
-                if (wrap) start_at(begin);
-                buf ^= 1;
-                if (!wrap || k0 + KEYS < u.k1) fetch(buf, g_next);
-            }
+            if (t + 1 < end_tile) fetch(t + 1, buf ^ 1, g_next);
             u32x4 b[ST];
 #pragma unroll
             for (int k = 0; k < AHEAD && k < ST; ++k) b[k] = lds_read16(qrow + (uint32_t)(((2 * k + h) ^ swz<KC>(r)) * 16));
@@ -282,9 +279,9 @@ __global__ __launch_bounds__(256, DK > 256 ? 1 : 2) void mass_rows(MassArgs p) {
         };
 #pragma unroll 1
         for (int t = begin; t < end_tile; t += 2) {
-            step(t, s0, s1);
+            step(t, 0, s0, s1);
             if (t + 1 == end_tile) break;
-            step(t + 1, s1, s0);
+            step(t + 1, 1, s1, s0);
         }
         if ((end_tile - begin) % 2 != 0) finish(s0);
         else finish(s1);
@@ -312,7 +309,6 @@ __global__ __launch_bounds__(256, DK > 256 ? 1 : 2) void mass_rows(MassArgs p) {
                 }
             }
         }
-        if (k0 + KEYS < u.k1 && begin < end_tile) load_keys(k0 + KEYS, kf, there);
     }
 }
 
