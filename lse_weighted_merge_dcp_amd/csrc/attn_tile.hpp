@@ -95,45 +95,58 @@ __device__ __forceinline__ void scores(f32x16 (&s)[RB][KT / 32], const u32x4 (&q
     }
 }
 
+// Masks a tile's scores.  `there`: bit j set where key j of the tile exists.
+// vis[rb]: how many keys from the tile's first on the lane's row sees (any
+// value; compared with the key's place).
+template <int RB, int NB>
+__device__ __forceinline__ void mask_scores(f32x16 (&s)[RB][NB], uint64_t there, const int (&vis)[RB]) {
+    const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int kb = 0; kb < NB; ++kb) {
+            const uint32_t bits = (uint32_t)(there >> (32 * kb)) >> (4 * h);
+            const int lim = vis[rb] - kb * 32 - 4 * h;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int j = 8 * (i / 4) + i % 4;
+                s[rb][kb][i] = (bits >> j & 1u) != 0 && j < lim ? s[rb][kb][i] : -INFINITY;
+            }
+        }
+}
+
+// The reference exponent for a tile whose scores reach `best` (of this half-wave's
+// keys); rescales sum and outputs where it moves.
+template <typename E, int DK, int DV, int RB>
+__device__ __forceinline__ void raise_top(Rows<DK, DV, RB>& w, float best, float c, int rb = 0) {
+    const float top = half_max(best) * c;
+    // (kTop: the scale on which the type's weights keep their precision)
+    if (__ballot(top > w.mc[rb] + Mat<E>::kTop + kLazy) != 0) {
+        const float next = top > w.mc[rb] + Mat<E>::kTop ? top - Mat<E>::kTop : w.mc[rb];
+        const float f = exp2_fast(w.mc[rb] - next);
+        w.mc[rb] = next;
+        w.l[rb] *= f;
+#pragma unroll
+        for (int cb = 0; cb < DV / 32; ++cb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w.o[rb][cb][i] *= f;
+    }
+}
+
 // Weights of a tile's scores, as B operands; updates maximum, sum and, where the
-// maximum moved, the outputs.  `there`: bit j set where key j of the tile
-// exists.  vis[rb]: how many keys from the tile's first on the lane's row sees
-// (any value; compared with the key's place).  full: no masking needed.
+// maximum moved, the outputs.  full: no masking needed.
 template <typename E, int DK, int DV, int RB, int NB>
 __device__ __forceinline__ void weights(Rows<DK, DV, RB>& w, f32x16 (&s)[RB][NB], uint32_t (&p)[RB][NB][8],
                                         uint64_t there, const int (&vis)[RB], bool full, float c) {
-    const int h = (threadIdx.x & 63) >> 5;
+    if (!full) mask_scores(s, there, vis);
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
-        if (!full) {
-#pragma unroll
-            for (int kb = 0; kb < NB; ++kb) {
-                const uint32_t bits = (uint32_t)(there >> (32 * kb)) >> (4 * h);
-                const int lim = vis[rb] - kb * 32 - 4 * h;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int j = 8 * (i / 4) + i % 4;
-                    s[rb][kb][i] = (bits >> j & 1u) != 0 && j < lim ? s[rb][kb][i] : -INFINITY;
-                }
-            }
-        }
         float top = -INFINITY;
 #pragma unroll
         for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[rb][kb][i]);
-        top = half_max(top) * c;
-        // (kTop: the scale on which the type's weights keep their precision)
-        if (__ballot(top > w.mc[rb] + Mat<E>::kTop + kLazy) != 0) {
-            const float next = top > w.mc[rb] + Mat<E>::kTop ? top - Mat<E>::kTop : w.mc[rb];
-            const float f = exp2_fast(w.mc[rb] - next);
-            w.mc[rb] = next;
-            w.l[rb] *= f;
-#pragma unroll
-            for (int cb = 0; cb < DV / 32; ++cb)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) w.o[rb][cb][i] *= f;
-        }
+        raise_top<E>(w, top, c, rb);
         float sum = 0.0f;
 #pragma unroll
         for (int kb = 0; kb < NB; ++kb)
