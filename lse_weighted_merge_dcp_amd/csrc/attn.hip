@@ -147,6 +147,9 @@ __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void attn_rows(AttnArgs p) {
 #pragma unroll
         for (int t = 0; t < 3; ++t) place_rows(t, page[t]);
     }
+    // (the query is there from here on: else the waits for it would stand in the loop, and wait for tiles)
+#pragma unroll
+    for (int st = 0; st < ST; ++st) asm volatile("" : "+v"(w.q[0][st]));
     meet();
     f32x16 s0[1][NB], s1[1][NB];
     float top = -INFINITY;
