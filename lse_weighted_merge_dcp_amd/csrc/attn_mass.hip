@@ -229,6 +229,11 @@ __global__ __launch_bounds__(256, DK > 256 ? 1 : 2) void mass_rows(MassArgs p) {
 #pragma unroll
                 for (int s = 0; s < ST; ++s) kf[kb][s] = widen8<E>(u32x2{kf[kb][s].x, kf[kb][s].y});
         }
+        // (the keys are there from here on: else the wait for them would stand in the loop, and wait for tiles)
+#pragma unroll
+        for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+            for (int s = 0; s < ST; ++s) asm volatile("" : "+v"(kf[kb][s]));
         float g_old = INFINITY;       // (the first time there is nothing to weigh)
         auto weigh = [&](const f32x16 (&s)[NB], int j) {
             acc[j / 16][j % 16] += exp2_fast(__builtin_fmaf(s[j / 16][j % 16], p.c, -g_old));
