@@ -263,6 +263,7 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
         return u32x4{x.x, x.y, y.x, y.y};
     };
     constexpr int AHEAD = 4, VAHEAD = 4;
+    constexpr int SETTLED = 5;         // products after which the result of the one before them is in its registers
 #define DCPA_PIN __builtin_amdgcn_sched_barrier(0)
 
     // what arrives first: tile 0, then 1 and 2
@@ -299,6 +300,28 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
     }
     out_claim();
 
+    // masks of tile t's scores, where there is something to mask
+    bool whole = true;
+    float best = -INFINITY;            // of the scores of this half-wave's keys
+    auto present = [&](int t) { return (uint32_t)__builtin_amdgcn_readfirstlane(*(const int*)&there_at[t & 7][0]); };
+    auto mask = [&](int t, uint32_t there, f32x16& x) {
+        whole = there == 0xffffffffu && vmin >= (t + 1) * KT;
+        if (whole) return;
+        settle(x);
+        const uint32_t bits = there >> (4 * h);
+        const int lim = vis - t * KT - 4 * h;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int j = 8 * (i / 4) + i % 4;
+            x[i] = (bits >> j & 1u) != 0 && j < lim ? x[i] : -INFINITY;
+        }
+    };
+    if (tiles > 0 && work && vmax > 0) {
+        mask(0, present(0), s);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) best = fmaxf(best, s[i]);
+    }
+
     // One tile's weights and outputs, with the next tile's scores between: the
     // exponentials run in the shadow of its matrix instructions, one to two of them
     // (an exponential takes half a product's time).  The nine pieces of tile t + 3
@@ -306,26 +329,14 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
     auto advance = [&](int t, uint32_t buf, uint32_t nbuf, uint32_t to, auto next) {
         constexpr bool NEXT = decltype(next)::value;
         u32x4 kf[AHEAD], vf[VAHEAD];
-        const uint32_t there = *(const uint32_t*)&there_at[t & 7][0];
         const int page = page_for(t + 3);
+        const uint32_t there = NEXT ? present(t + 1) : 0;      // (read early, ahead of the fragments)
         if constexpr (NEXT) {
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) kf[i] = key_fragment(nbuf, i);
         }
-        const bool full = there == 0xffffffffu && vmin >= (t + 1) * KT;
-        if (!full) {
-            const uint32_t bits = there >> (4 * h);
-            const int lim = vis - t * KT - 4 * h;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int j = 8 * (i / 4) + i % 4;
-                s[i] = (bits >> j & 1u) != 0 && j < lim ? s[i] : -INFINITY;
-            }
-        }
-        float top = fmaxf(s[0], -INFINITY);
-#pragma unroll
-        for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-        top = half_max(top) * p.c;
+        const bool full = whole;
+        const float top = half_max(best) * p.c;
         if (__ballot(top > mc + Mat<E>::kTop + kLazy) != 0) {
             const float next_mc = top > mc + Mat<E>::kTop ? top - Mat<E>::kTop : mc;
             const float f = exp2_fast(mc - next_mc);
@@ -338,8 +349,10 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
         float sum = 0.0f;
         f32x16 n;
         u32x4 ql[QL];
-        place_rows(t + 3, page);
-        if constexpr (KV8) fetch(t + 3);
+        if constexpr (KV8) {
+            place_rows(t + 3, page);
+            fetch(t + 3);
+        }
         DCPA_PIN;
         times<STEPS>([&](auto st) {
             if constexpr (NEXT) {
@@ -352,17 +365,24 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
             }
             if constexpr (st < 32 && st % 2 == 0) {
                 s[st / 2] = exp2_fast(__builtin_fmaf(s[st / 2], p.c, -mc));
+                if constexpr (st % 4 == 0) asm volatile("" : "+v"(s));
             } else if constexpr (st < 32) {
+                // (pinned here: the compiler would compute them later, between the products that need them)
                 sum += s[st / 2];
-                if constexpr (st % 4 == 3) pr[st / 4] = Mat<E>::pack2(s[st / 2 - 1], s[st / 2]);
+                asm volatile("" : "+v"(sum));
+                if constexpr (st % 4 == 3) {
+                    pr[st / 4] = Mat<E>::pack2(s[st / 2 - 1], s[st / 2]);
+                    asm volatile("" : "+v"(pr[st / 4]));
+                }
             }
+            if constexpr (!KV8 && st == 2) place_rows(t + 3, page);
             if constexpr (!KV8 && st % 7 == 5) fetch_piece(to, std::integral_constant<int, st / 7>{});
             if constexpr (st >= STEPS - VAHEAD) vf[st - (STEPS - VAHEAD)] = value_fragment(buf, 2 * (st - (STEPS - VAHEAD)));
             DCPA_PIN;
         });
         l += sum;
-        // (kept from being computed later, between the products that need it)
-        asm volatile("" : "+v"(pr[0]), "+v"(pr[1]), "+v"(pr[2]), "+v"(pr[3]), "+v"(pr[4]), "+v"(pr[5]), "+v"(pr[6]), "+v"(pr[7]));
+        if constexpr (NEXT) mask(t + 1, there, n);
+        best = -INFINITY;
         const u32x4 p0 = {pr[0], pr[1], pr[2], pr[3]}, p1 = {pr[4], pr[5], pr[6], pr[7]};
         DCPA_PIN;
         asm volatile("s_nop 1");      // (the weights were written just before)
@@ -373,6 +393,14 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
             out_mma<E, cb>(vf[i % VAHEAD], half == 0 ? p0 : p1);
             if constexpr (m < 2 * CBS) vf[i % VAHEAD] = value_fragment(buf, m % CBS * 2 + m / CBS);
             DCPA_PIN;
+            // the next tile's maximum; its last product was done four products ago
+            if constexpr (NEXT && i >= SETTLED && (i - SETTLED) % 3 == 0 && (i - SETTLED) / 3 < 8) {
+                constexpr int k = (i - SETTLED) / 3 * 2;
+                if constexpr (k == 0) asm volatile("" : "+v"(n));
+                best = fmaxf(best, fmaxf(n[k], n[k + 1]));
+                asm volatile("" : "+v"(best));
+                DCPA_PIN;
+            }
             if constexpr (!KV8 && i % 7 == 5 && 5 + i / 7 < 9) {
                 fetch_piece(to, std::integral_constant<int, 5 + i / 7>{});
                 DCPA_PIN;
@@ -380,10 +408,7 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
         });
         out_claim();
         if (!full) odd |= odd_values<E, false>(buf, MAIN);
-        if constexpr (NEXT) {
-            settle(n);
-            s = n;
-        }
+        if constexpr (NEXT) s = n;
     };
 
     uint32_t at0 = buffer(0), at1 = buffer(1), at2 = buffer(2), at3 = buffer(3);    // of tiles t .. t + 3
