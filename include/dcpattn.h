@@ -50,6 +50,13 @@
  *   owned(x) = number of positions below x that lie on this rank.
  * So a cache that dcpa_cache_evict has cut stays usable.  With causal = 0 every
  * token sees all kv_len[b] keys (an encoder's states, say).
+ *
+ * Limits (DCP_ERR_SHAPE beyond them): heads up to 2^16, sequences up to 2^20,
+ * T * Hq up to 2^30 (T * (Hq + 2 Hkv) in the first call), max_pages *
+ * page_size below 2^30, page_size up to 2^20, N * interleave up to 2^30; the
+ * attention and the weights up to 2^23 workgroups (row tiles of 128 rows, of 32
+ * where rows are few, times key heads, at least one to a sequence), the eviction
+ * up to B * Hkv = 2^22 and B * Hkv * budget = 2^25.
  */
 #ifndef DCPATTN_H
 #define DCPATTN_H

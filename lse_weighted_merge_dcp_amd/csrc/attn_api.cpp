@@ -137,6 +137,13 @@ int check_attn(const dcpa_attn_args* a, Batch& m) {
     return DCP_OK;
 }
 
+// The weights' plan; as check_attn, no more workgroups than a launch may have.
+int check_mass(const dcpa_attn_args* a, Batch& m, MassPlan& pl) {
+    if (int st = check_batch(a, m)) return st;
+    pl = plan_mass(m, (int)a->Dk, key_pieces(a));
+    return (int64_t)pl.units * m.Hkv > kMaxGrid ? DCP_ERR_SHAPE : DCP_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -207,22 +214,22 @@ int dcpa_paged_attn(const dcpa_attn_args* a, void* stream) {
 int64_t dcpa_attn_mass_workspace(const dcpa_attn_args* a) {
     if (a == nullptr) return DCP_ERR_NULL;
     Batch m;
-    if (int st = check_batch(a, m)) return st;
-    if (a->B == 0 || a->T == 0) return 0;
-    return plan_mass(m, (int)a->Dk, key_pieces(a)).ws_bytes;
+    MassPlan pl;
+    if (int st = check_mass(a, m, pl)) return st;
+    return a->B == 0 || a->T == 0 ? 0 : pl.ws_bytes;
 }
 
 int dcpa_attn_mass(const dcpa_attn_args* a, float* mass, int64_t m_P, int64_t m_S, int64_t m_H, void* stream) {
     if (a == nullptr) return DCP_ERR_NULL;
     MassArgs k;
-    if (int st = check_batch(a, k.m)) return st;
+    MassPlan pl;
+    if (int st = check_mass(a, k.m, pl)) return st;
     if (!strides_ok({m_P, m_S, m_H}) || !span_ok({{a->num_pages, m_P}, {a->page_size, m_S}, {a->Hkv, m_H}}, 4))
         return DCP_ERR_STRIDE;
     if (a->B == 0 || a->T == 0) return DCP_OK;
     if (int st = check_inputs(a)) return st;
     if (!a->lse || (a->num_pages > 0 && !mass)) return DCP_ERR_NULL;
     if (!aligned(mass, 4)) return DCP_ERR_ALIGN;
-    const MassPlan pl = plan_mass(k.m, (int)a->Dk, key_pieces(a));
     if (pl.ws_bytes > 0 && (!a->workspace || a->workspace_bytes < pl.ws_bytes || !aligned(a->workspace, 16)))
         return DCPA_ERR_WORKSPACE;
     const int ec = esize_of(a->cache_dtype);

@@ -142,15 +142,30 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
 
 template <typename E, bool KV8, bool PAIRS> hipError_t run(const RopeArgs& a, hipStream_t stream) {
     const int D = a.v != nullptr && a.Dv > a.D ? a.Dv : a.D;
-    const int64_t rows = (int64_t)a.T * (a.Hq + a.Hkv * (a.v != nullptr ? 2 : 1));
-    auto grid = [&](int lpr) { return dim3((uint32_t)((rows * lpr + 255) / 256)); };
-    const dim3 block(256);
-    if (D <= 64) return launch(rope_kernel<E, KV8, PAIRS, 8, 1>, grid(8), block, stream, a);
-    if (D <= 128) return launch(rope_kernel<E, KV8, PAIRS, 16, 1>, grid(16), block, stream, a);
-    if (D <= 256) return launch(rope_kernel<E, KV8, PAIRS, 16, 2>, grid(16), block, stream, a);
-    if (D <= 512) return launch(rope_kernel<E, KV8, PAIRS, 16, 4>, grid(16), block, stream, a);
-    if (D <= 640) return launch(rope_kernel<E, KV8, PAIRS, 16, 5>, grid(16), block, stream, a);
-    return launch(rope_kernel<E, KV8, PAIRS, 16, 8>, grid(16), block, stream, a);
+    const int64_t heads = a.Hq + a.Hkv * (a.v != nullptr ? 2 : 1);
+    // at most 2^23 workgroups to a launch: as many tokens at a time
+    auto go = [&](void (*kernel)(RopeArgs), int lpr) {
+        const int64_t rows = 256 / lpr, most = (rows << 23) / heads;
+        RopeArgs b = a;
+        for (int64_t t = 0; t < a.T; t += most) {
+            b.T = (int32_t)(a.T - t < most ? a.T - t : most);
+            b.q = a.q + t * a.q_T;
+            b.k = a.k + t * a.k_T;
+            if (a.v != nullptr) b.v = a.v + t * a.v_T;
+            b.qo = a.qo + t * a.qo_T;
+            if (a.pos != nullptr) b.pos = a.pos + t;
+            b.slots = a.slots + t;
+            const hipError_t e = launch(kernel, dim3((uint32_t)((b.T * heads + rows - 1) / rows)), dim3(256), stream, b);
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
+    };
+    if (D <= 64) return go(rope_kernel<E, KV8, PAIRS, 8, 1>, 8);
+    if (D <= 128) return go(rope_kernel<E, KV8, PAIRS, 16, 1>, 16);
+    if (D <= 256) return go(rope_kernel<E, KV8, PAIRS, 16, 2>, 16);
+    if (D <= 512) return go(rope_kernel<E, KV8, PAIRS, 16, 4>, 16);
+    if (D <= 640) return go(rope_kernel<E, KV8, PAIRS, 16, 5>, 16);
+    return go(rope_kernel<E, KV8, PAIRS, 16, 8>, 16);
 }
 
 }  // namespace

@@ -152,6 +152,24 @@ def test_norm_rope_in_place_of_every_width(dev, D, off, rot, pairs):
     assert torch.equal(qd, apart)
 
 
+def test_norm_rope_of_more_rows_than_a_launch(dev):
+    """2^23 workgroups of 32 rows of 8 columns: the tokens behind them go to a second launch."""
+    Hq, D = 512, 8
+    per = (32 << 23) // (Hq + 2)
+    T = per + 5
+    q = torch.randn(T, Hq, D, dtype=BF, device=dev)
+    k, v = torch.randn(T, 1, D, dtype=BF, device=dev), torch.randn(T, 1, D, dtype=BF, device=dev)
+    w = torch.full((D,), 1.5, dtype=BF, device=dev)
+    cs, pos = rope_table(4, 0).to(dev), torch.zeros(T, dtype=torch.int32, device=dev)
+    kc, vc = torch.zeros(T, 1, 1, D, dtype=BF, device=dev), torch.zeros(T, 1, 1, D, dtype=BF, device=dev)
+    slots = torch.arange(T, device=dev)
+    got = attn.qk_norm_rope_append(q, k, v, w, w, pos, cs, slots, kc, vc)
+    at = torch.tensor([0, 1, per - 1, per, per + 1, T - 1])
+    for x, y in ((q, got), (k, kc.view(T, 1, D))):
+        near(y[at.to(dev)].cpu(), oracle.norm_rope(x[at.to(dev)].cpu(), w.cpu(), 1e-6, cs.cpu(), pos[:6].cpu(), 0, False), BF)
+    assert torch.equal(vc.view(T, 1, D), v)
+
+
 # ---------------------------------------------------------------------------
 # accumulated weights
 # ---------------------------------------------------------------------------
