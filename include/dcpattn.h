@@ -99,7 +99,7 @@ const char* dcpa_status_str(int status);
  * turns by the nearest row of the table.
  *
  * dtype: DCP_F16 or DCP_BF16 (q, k, v, weights).  D, Dv multiples of 8 up to
- * 1024, rope_off a multiple of 8, rot a multiple of 16 (0: no rotation), rows
+ * 1024, rope_off a multiple of 8, rot a multiple of 8 (0: no rotation), rows
  * of q, k, v and q_out 16-byte aligned, rows of a cache 8-element aligned;
  * q_norm and k_norm are 0 or multiples of 8 up to D.
  */

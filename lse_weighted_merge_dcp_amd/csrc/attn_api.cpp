@@ -263,7 +263,7 @@ int dcpa_qk_norm_rope_append(const dcpa_rope_args* a, void* stream) {
     if (a->q_norm < 0 || a->q_norm % 8 != 0 || a->q_norm > a->D || a->k_norm < 0 || a->k_norm % 8 != 0 ||
         a->k_norm > a->D)
         return DCP_ERR_SHAPE;
-    if (a->rot < 0 || a->rot % 16 != 0 || a->rope_off < 0 || a->rope_off % 8 != 0 || a->rope_off > a->D ||
+    if (a->rot < 0 || a->rot % 8 != 0 || a->rope_off < 0 || a->rope_off % 8 != 0 || a->rope_off > a->D ||
         a->rot > a->D - a->rope_off)
         return DCP_ERR_SHAPE;
     if (a->positions_max < 1 || a->positions_max >= (int64_t(1) << 31) || !cache_shape_ok(a->num_pages, a->page_size, 0))

@@ -71,15 +71,26 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
     }
     const char* w = query ? p.wq : p.wk;
     const int nw = value ? 0 : query ? p.nq : p.nk, rot = value ? 0 : p.rot, half = rot / 2;
-    // Where the partner stands half a range away it is the same place of another piece, in a slot that differs
-    // from lane to lane: it is read again, out of the cache, and before any store (the row may be written in place).
-    auto partner = [&](int s) { return 8 * (s * LPR + lane) + (8 * (s * LPR + lane) - p.off < half ? half : -half); };
+    // Halves: the partner of a column stands half a range away.  Where that is whole pieces and a piece to a lane, it
+    // comes from another lane; else in fours (half a range is a multiple of four columns), read again, out of the
+    // cache, and before any store (the row may be written in place).
+    const bool from_lane = SLOTS == 1 && half % 8 == 0;
+    auto partner = [&](int s, int g) {
+        const int col = 8 * (s * LPR + lane) + 4 * g;
+        return col - p.off < half ? col + half : col - half;
+    };
     dcp::Vec<16> other[SLOTS];
-    if constexpr (SLOTS > 1 && !PAIRS)
+    if (!PAIRS && !from_lane)
 #pragma unroll
         for (int s = 0; s < SLOTS; ++s) {
             const int at = 8 * (s * LPR + lane) - p.off;
-            if (at >= 0 && at < rot) other[s] = dcp::vload<16>(from + partner(s) * 2);
+            if (at >= 0 && at < rot)
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const dcp::Vec<8> y = dcp::vload<8>(from + partner(s, g) * 2);
+                    other[s].w[2 * g] = y.w[0];
+                    other[s].w[2 * g + 1] = y.w[1];
+                }
         }
     float f = 1.0f;
     if (nw > 0) {
@@ -112,19 +123,27 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
                 }
             }
         } else {
-            const bool low = at < half;
             float y[8];
-            if constexpr (SLOTS == 1) {
+            if (from_lane) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = __shfl(x[i], partner(s) / 8 & (LPR - 1), LPR);
+                for (int i = 0; i < 8; ++i) y[i] = __shfl(x[i], partner(s, 0) / 8 & (LPR - 1), LPR);
             } else if (turned) {
-                norm8<E>(other[s], partner(s), w, nw, f, y);
+                dcp::Cvt<E, 16>::unpack(other[s], y);
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                    if (partner(s, g) < nw) {
+                        float t[4];
+                        dcp::Cvt<E, 8>::unpack(dcp::vload<8>(w + partner(s, g) * 2), t);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) y[4 * g + i] = y[4 * g + i] * f * t[i];
+                    }
             }
             if (turned) {
-                const int j = low ? at : at - half;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float c = cs[j + i], n = cs[half + j + i];
+                    const bool low = at + i / 4 * 4 < half;
+                    const int j = low ? at + i : at + i - half;
+                    const float c = cs[j], n = cs[half + j];
                     x[i] = low ? x[i] * c - y[i] * n : x[i] * c + y[i] * n;
                 }
             }

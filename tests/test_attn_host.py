@@ -178,7 +178,7 @@ def test_empty_calls_are_accepted():
 @pytest.mark.parametrize("over,want", [
     (dict(dtype=0), DTYPE), (dict(cache_dtype=1), DTYPE), (dict(T=-1), SHAPE), (dict(Hq=0), SHAPE), (dict(Hkv=0), SHAPE),
     (dict(D=4), SHAPE), (dict(D=1032), SHAPE), (dict(D=100), SHAPE), (dict(Dv=12), SHAPE), (dict(q_norm=136), SHAPE),
-    (dict(k_norm=4), SHAPE), (dict(rot=8), SHAPE), (dict(rot=-16), SHAPE), (dict(rope_off=4), SHAPE),
+    (dict(k_norm=4), SHAPE), (dict(rot=12), SHAPE), (dict(rot=-16), SHAPE), (dict(rope_off=4), SHAPE),
     (dict(rope_off=8), SHAPE), (dict(positions_max=0), SHAPE), (dict(page_size=0), SHAPE), (dict(eps=-1.0), VALUE),
     (dict(eps=float("nan")), VALUE), (dict(k_scale=0.0), VALUE), (dict(v_scale=float("inf")), VALUE),
     (dict(k_scale=1e-45), VALUE), (dict(q_T=-8), STRIDE), (dict(kc_P=1 << 57), STRIDE),

@@ -51,6 +51,13 @@ def near(got, want, dtype, fp32=2.0 ** -20):
     (6, 4, 2, 256, 8, 0, 0, 0, 0, False),
     (2, 2, 1, 192, 256, 64, 192, 64, 128, False),
     (3, 1, 1, 8, 24, 8, 8, 0, 0, True),
+    # half a range that is no whole piece of eight columns
+    (9, 5, 5, 80, 80, 80, 80, 0, 40, False),
+    (9, 5, 5, 80, 80, 80, 80, 0, 40, True),
+    (6, 3, 1, 64, 64, 64, 40, 8, 8, False),
+    (4, 2, 1, 96, 96, 0, 96, 16, 72, False),
+    (3, 2, 1, 576, 0, 576, 512, 24, 200, False),
+    (3, 2, 2, 8, 8, 8, 8, 0, 8, False),
 ])
 def test_norm_rope(dev, dtype, T, Hq, Hkv, D, Dv, nq, nk, off, rot, pairs):
     g = torch.Generator().manual_seed(T * D)
@@ -135,7 +142,8 @@ def test_norm_rope_in_place_strided_and_far_positions(dev):
 
 
 @pytest.mark.parametrize("pairs", [False, True], ids=["halves", "pairs"])
-@pytest.mark.parametrize("D,off,rot", [(64, 0, 64), (256, 0, 256), (576, 64, 512), (1024, 0, 1024), (512, 480, 32)])
+@pytest.mark.parametrize("D,off,rot", [(64, 0, 64), (256, 0, 256), (576, 64, 512), (1024, 0, 1024), (512, 480, 32), (80, 0, 40),
+                                       (576, 8, 520), (128, 0, 104)])
 def test_norm_rope_in_place_of_every_width(dev, D, off, rot, pairs):
     """In place and into a tensor of its own give the same bits: no piece is read after it was turned."""
     g = torch.Generator().manual_seed(D)
