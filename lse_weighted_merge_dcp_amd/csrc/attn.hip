@@ -23,7 +23,7 @@ namespace {
 // tile's keys are fetched one turn before its values.
 // ---------------------------------------------------------------------------
 template <typename E, bool KV8, bool EXACT, int DK, int DV, int KT>
-__global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void attn_rows(AttnArgs p) {
+__global__ __launch_bounds__(256, DK > 192 ? 1 : 2) void attn_rows(AttnArgs p) {
     constexpr int R = 128, KC = DK / 8, VC = DV / 8, NB = KT / 32, ST = DK / 16, CB = DV / 32, KS = KT / 16;
     constexpr int KROW = KC * 16, VROW = VC * 16;
     constexpr int KB = KT * KROW, VB = KT * VROW;
@@ -452,42 +452,55 @@ __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void attn_keys(AttnArgs p) {
 }
 
 // ---------------------------------------------------------------------------
-// attn_join: a wave to a row of a sequence whose keys were split; each lane
-// holds four columns (eight where the rows are wide)
+// attn_join: the rows of sequences whose keys were split; each lane holds four
+// columns (eight where the rows are wide).  Few rows have many parts: the four
+// waves of a workgroup share a row's (TOGETHER).  Many rows have few: a wave goes
+// from row to row, and works out the lengths once.
 // ---------------------------------------------------------------------------
-template <typename E, int STEP, int NC>
+template <typename E, int STEP, int NC, bool TOGETHER>
 __global__ __launch_bounds__(256) void attn_join(AttnArgs p) {
-    const int lane = threadIdx.x & 63;
-    const uint32_t id = blockIdx.x * 4 + dcp::wave_id();
-    const int hk = (int)(id % (uint32_t)p.m.Hkv), at_row = (int)(id / (uint32_t)p.m.Hkv);
-    const int t = (int)fdiv((uint32_t)at_row, p.m.fG), head = at_row - t * p.m.G;
-    if (t >= p.m.T) return;
+    constexpr int FLY = 8;                     // parts under way at once
+    __shared__ f32x4 share[TOGETHER ? 4 : 1][NC][64];
+    const int lane = threadIdx.x & 63, wave = (int)dcp::wave_id();
     const int chunk = key_chunk<STEP>(p.m, p.rows, p.slots);
-    int base = 0;
-    for (int b0 = 0; b0 < p.m.B; b0 += 64) {
-        const int b = b0 + lane;
-        int tiles, kv;
-        tiles_of(p.m, b, p.rows, tiles, kv);
-        const int splits = max(1, (kv + chunk - 1) / chunk);
-        bool here = false;
-        if (b < p.m.B) {
-            const Seq s = load_seq(p.m, b);
-            here = t >= s.first && t < s.first + s.n;
+    // lengths and units of sequences b0 .. b0 + 63, a lane to each
+    struct Line {
+        Seq s;
+        int splits, incl;
+    };
+    auto line_at = [&](int b0, int base) {
+        Line x{};
+        int tiles = 0;
+        if (b0 + lane < p.m.B) {
+            x.s = load_seq(p.m, b0 + lane);
+            tiles = (x.s.n * p.m.G + p.rows - 1) / p.rows;
         }
-        const int incl = base + scan_incl(tiles * splits);
-        const uint64_t found = __ballot(here);
-        if (found == 0) {
-            base = __builtin_amdgcn_readlane(incl, 63);
-            continue;
+        x.splits = max(1, (x.s.kv + chunk - 1) / chunk);
+        x.incl = base + scan_incl(tiles * x.splits);
+        return x;
+    };
+    const Line start = line_at(0, 0);
+    const int64_t all = (int64_t)p.m.T * p.m.G * p.m.Hkv;
+    const int64_t stride = TOGETHER ? gridDim.x : (int64_t)gridDim.x * 4;
+#pragma unroll 1
+    for (int64_t id = TOGETHER ? blockIdx.x : (int64_t)blockIdx.x * 4 + wave; id < all; id += stride) {
+        const uint32_t at_row = fdiv((uint32_t)id, p.m.fHkv);
+        const int hk = (int)((uint32_t)id - at_row * p.m.fHkv.d), t = (int)fdiv(at_row, p.m.fG), head = (int)at_row - t * p.m.G;
+        Line x = start;
+        uint64_t found = 0;
+        for (int b0 = 0;; b0 += 64, x = line_at(b0, __builtin_amdgcn_readlane(x.incl, 63))) {
+            found = __ballot(t >= x.s.first && t < x.s.first + x.s.n);
+            if (found != 0 || b0 + 64 >= p.m.B) break;
         }
+        if (found == 0) continue;
         const int at = __builtin_ctzll(found);
-        const int ns = __builtin_amdgcn_readlane(splits, at);
-        if (ns == 1) return;                  // written whole
-        const Seq s = load_seq(p.m, b0 + at);
+        const Seq s = seq_of(x.s, at);
+        const int ns = __builtin_amdgcn_readlane(x.splits, at);
+        if (ns == 1) continue;                // written whole
         const int row = (t - s.first) * p.m.G + head, tile = row / p.rows, in_tile = row - tile * p.rows;
         // (a sequence's last tile comes first)
-        const int slot = __builtin_amdgcn_readlane(incl, at) - (tile + 1) * ns;
-        if (slot < 0) return;
+        const int slot = __builtin_amdgcn_readlane(x.incl, at) - (tile + 1) * ns;
+        if (slot < 0) continue;
         // the ranges that the tile's last row has keys in
         const int last = min((tile + 1) * p.rows, s.n * p.m.G) - 1;
         const int kend = visible(p.m, s, (int)fdiv((uint32_t)last, p.m.fG));
@@ -496,32 +509,58 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs p) {
         float top = -INFINITY;
         bool bad = false;
         for (int k = lane; k < parts; k += 64) {
-            const float x = p.ws_l[first + (int64_t)k * p.rows];
-            bad |= x != x;
-            top = fmaxf(top, x);
+            const float y = p.ws_l[first + (int64_t)k * p.rows];
+            bad |= y != y;
+            top = fmaxf(top, y);
         }
 #pragma unroll
         for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-        bad = __ballot(bad) != 0;
         const float ref = top == -INFINITY ? 0.0f : top;
         float acc[NC * 4], sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < NC * 4; ++i) acc[i] = 0.0f;
-#pragma unroll 4
-        for (int k = 0; k < parts; ++k) {
-            const float f = exp2_fast(p.ws_l[first + (int64_t)k * p.rows] - ref);
+#pragma unroll 1
+        for (int k0 = 0; k0 < parts; k0 += 64) {
+            // a lane to a part's weight
+            const int here = min(64, parts - k0);
+            const float f = lane < here ? exp2_fast(p.ws_l[first + (int64_t)(k0 + lane) * p.rows] - ref) : 0.0f;
             sum += f;
+#pragma unroll 1
+            for (int k = TOGETHER ? wave * FLY : 0; k < here; k += TOGETHER ? 4 * FLY : FLY) {
+                f32x4 y[FLY][NC];
 #pragma unroll
-            for (int j = 0; j < NC; ++j) {
-                const int col = j * 256 + lane * 4;
-                if (col < p.Dv) {
-                    const f32x4 y = *(const f32x4*)(p.ws_o + (first + (int64_t)k * p.rows) * p.Dv + col);
+                for (int i = 0; i < FLY; ++i)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[j * 4 + i] += f * y[i];
+                    for (int j = 0; j < NC; ++j) {
+                        const int col = min(j * 256 + lane * 4, p.Dv - 4);
+                        y[i][j] = *(const f32x4*)(p.ws_o + (first + (int64_t)(k0 + min(k + i, here - 1)) * p.rows) * p.Dv + col);
+                    }
+#pragma unroll
+                for (int i = 0; i < FLY; ++i) {
+                    const float g = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), min(k + i, 63)));
+#pragma unroll
+                    for (int j = 0; j < NC; ++j)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) acc[j * 4 + c] += k + i < here ? g * y[i][j][c] : 0.0f;
                 }
             }
         }
-        if (bad) sum = NAN;
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 64);
+        if (__ballot(bad) != 0) sum = NAN;
+        if constexpr (TOGETHER) {
+#pragma unroll
+            for (int j = 0; j < NC; ++j) share[wave][j][lane] = f32x4{acc[j * 4], acc[j * 4 + 1], acc[j * 4 + 2], acc[j * 4 + 3]};
+            __syncthreads();
+            if (wave == 0)
+#pragma unroll
+                for (int j = 0; j < NC; ++j)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        acc[j * 4 + c] = share[0][j][lane][c] + share[1][j][lane][c] + share[2][j][lane][c] + share[3][j][lane][c];
+            __syncthreads();
+            if (wave != 0) continue;
+        }
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         char* o = p.out + (int64_t)t * p.o_T + (int64_t)(hk * p.m.G + head) * p.o_H;
 #pragma unroll
@@ -533,7 +572,6 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs p) {
         if (lane == 0 && p.lse != nullptr)
             p.lse[(int64_t)t * p.l_T + (int64_t)(hk * p.m.G + head) * p.l_H] =
                 (sum == 0.0f ? -INFINITY : ref + __builtin_amdgcn_logf(sum)) * p.lmul;
-        return;
     }
 }
 
@@ -567,9 +605,17 @@ namespace {
 
 template <typename E, int STEP>
 hipError_t run_join(const AttnArgs& a, hipStream_t stream) {
-    const dim3 grid((uint32_t)(((int64_t)a.m.T * a.m.G * a.m.Hkv + 3) / 4)), block(256);
-    return a.Dv <= 256 ? launch(attn_join<E, STEP, 1>, grid, block, stream, a)
-                       : launch(attn_join<E, STEP, 2>, grid, block, stream, a);
+    // a workgroup to a row up to what the chip holds at once, then a wave, and no more waves than that
+    const int64_t rows = (int64_t)a.m.T * a.m.G * a.m.Hkv;
+    const dim3 block(256);
+    if (rows <= 1024) {
+        const dim3 grid((uint32_t)rows);
+        return a.Dv <= 256 ? launch(attn_join<E, STEP, 1, true>, grid, block, stream, a)
+                           : launch(attn_join<E, STEP, 2, true>, grid, block, stream, a);
+    }
+    const dim3 grid((uint32_t)(rows < 8192 ? (rows + 3) / 4 : 2048));
+    return a.Dv <= 256 ? launch(attn_join<E, STEP, 1, false>, grid, block, stream, a)
+                       : launch(attn_join<E, STEP, 2, false>, grid, block, stream, a);
 }
 
 template <typename E, bool KV8>
@@ -597,7 +643,9 @@ hipError_t run(const AttnArgs& a, const AttnPlan& pl, hipStream_t stream) {
         e = a.Dk == 128 && a.Dv == 128 ? launch(attn_rows<E, KV8, true, 128, 128, 64>, grid, block, stream, a)
                                        : launch(attn_rows<E, KV8, false, 128, 128, 64>, grid, block, stream, a);
     else {
-        e = launch(attn_rows<E, KV8, false, 256, 256, 32>, grid, block, stream, a);
+        e = a.Dk <= 192 && a.Dv <= 128   ? launch(attn_rows<E, KV8, false, 192, 128, 32>, grid, block, stream, a)
+            : a.Dk <= 192 && a.Dv <= 192 ? launch(attn_rows<E, KV8, false, 192, 192, 32>, grid, block, stream, a)
+                                         : launch(attn_rows<E, KV8, false, 256, 256, 32>, grid, block, stream, a);
         if (e != hipSuccess || pl.slots == 0) return e;
         return run_join<E, 32>(a, stream);
     }
