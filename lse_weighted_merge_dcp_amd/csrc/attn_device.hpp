@@ -326,7 +326,7 @@ __device__ __forceinline__ Unit find_unit(const Batch& m, int rows, int slots, i
             u.tile = t - 1 - rest / s;
             u.slot = id - u.split;
             // (lengths that contradict each other could lead outside the tile)
-            u.ok = rest >= 0 && (int64_t)u.tile * rows < (int64_t)u.s.n * m.G;
+            u.ok = rest >= 0 && u.tile >= 0 && (int64_t)u.tile * rows < (int64_t)u.s.n * m.G;
             return u;
         }
         base = __builtin_amdgcn_readlane(incl, 63);

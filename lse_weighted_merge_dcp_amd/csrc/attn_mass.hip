@@ -205,7 +205,7 @@ __global__ __launch_bounds__(256, DK > 256 ? 1 : 2) void mass_rows(MassArgs p) {
     const int begin = lo;
     const bool single = end_tile - begin <= 1;     // one tile of rows for all the keys: it stays in LDS
     u32x4 kf[NB][ST];
-    uint32_t there[NB];
+    uint32_t there[NB] = {};
     float g_next = 0.0f;
 #pragma unroll 1
     for (int k0 = u.k0; k0 < u.k1; k0 += KEYS) {

@@ -38,7 +38,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
     const uint32_t row = blockIdx.x * RPB + threadIdx.x / LPR;
     const int token = (int)fdiv(row, p.fheads), which = (int)(row - (uint32_t)token * p.fheads.d);
     if (token >= p.T) return;
-    const int pos = min(max(p.pos[token], 0), p.positions - 1);
+    // (without rotation there may be no positions)
+    const int pos = p.rot > 0 ? min(max(p.pos[token], 0), p.positions - 1) : 0;
     const float* cs = p.cs + (int64_t)pos * p.cs_P;
     const bool query = which < p.Hq, value = which >= p.Hq + p.Hkv;
     char* to;

@@ -285,6 +285,37 @@ def test_many_sequences(dev):
     check(p, *call(p, dev))
 
 
+@pytest.mark.parametrize("form", ["decode", "chunk", "latent"])
+def test_sequences_without_tokens(dev, form):
+    """A padded batch: sequences of no new tokens, with and without a cache, among the others."""
+    seqs = [(0, 50), (1, 300), (0, 0), (3 if form == "decode" else 40, 340), (0, 9), (0, 0)]
+    p = Problem(seqs, 8, 1, *((576, 512) if form == "latent" else (128, 128)), shared=form == "latent", seed=120)
+    check(p, *call(p, dev))
+
+
+def test_long_sequences_behind_64_others(dev):
+    """Split keys of a sequence that is not among the first 64."""
+    p = Problem([(1, 20)] * 67 + [(1, 3000), (2, 90)] + [(1, 1)] * 3, 4, 2, 64, 64, seed=121)
+    check(p, *call(p, dev))
+    p = Problem([(1, 9)] * 66 + [(3, 900)], 48, 1, 128, 64, shared=True, seed=122)
+    check(p, *call(p, dev))
+
+
+def test_many_rows_of_split_keys(dev):
+    """More rows than the join has waves."""
+    p = Problem([(600, 900)], 16, 1, 64, 64, seed=123)
+    check(p, *call(p, dev))
+
+
+@pytest.mark.parametrize("cache", [BF, F8], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (192, 128), (192, 192), (160, 48), (256, 256), (64, 64), (72, 128)])
+def test_row_tiles_of_every_width(dev, Dk, Dv, cache):
+    """Several tiles of keys, whole ones and the diagonal's, pages that end inside them and one that is not there."""
+    p = Problem([(150, 420), (37, 37)], 2, 1, Dk, Dv, cache=cache, page=24, seed=124)
+    p.table[0, 3] = -1
+    check(p, *call(p, dev))
+
+
 def test_deterministic(dev):
     p = Problem([(1, 3000), (1, 900)], 16, 2, 128, 128, seed=78)
     a = call(p, dev)

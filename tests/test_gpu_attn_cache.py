@@ -160,6 +160,26 @@ def test_norm_rope_in_place_of_every_width(dev, D, off, rot, pairs):
     assert torch.equal(qd, apart)
 
 
+def test_norm_without_rotation_needs_no_positions(dev, monkeypatch):
+    """The C call with null positions and table."""
+    g = torch.Generator().manual_seed(9)
+    q, k = torch.randn(7, 2, 64, generator=g).to(BF), torch.randn(7, 1, 64, generator=g).to(BF)
+    w = (1 + 0.2 * torch.randn(64, generator=g)).to(BF)
+    cs, pos = torch.zeros(1, 0), torch.zeros(7, dtype=torch.int32)
+    d = lambda t: t.to(dev)  # noqa: E731
+    kc = torch.zeros(7, 1, 1, 64, dtype=BF, device=dev)
+
+    def without(fn, name, device, args):
+        fields = list(attn.ROPE_ARGS.unpack(args))
+        fields[11] = fields[12] = 0            # positions, cos_sin
+        assert fn(attn.ROPE_ARGS.pack(*fields), torch.cuda.current_stream().cuda_stream) == 0
+
+    monkeypatch.setattr(attn, "_call", without)
+    got = attn.qk_norm_rope_append(d(q), d(k), None, d(w), d(w), d(pos), d(cs), torch.arange(7, device=dev), kc, None)
+    near(got.cpu(), oracle.norm_rope(q, w, 1e-6, cs, pos, 0, False), BF)
+    near(kc.view(7, 1, 64).cpu(), oracle.norm_rope(k, w, 1e-6, cs, pos, 0, False), BF)
+
+
 def test_norm_rope_of_more_rows_than_a_launch(dev):
     """2^23 workgroups of 32 rows of 8 columns: the tokens behind them go to a second launch."""
     Hq, D = 512, 8
@@ -222,6 +242,9 @@ MASS = [
     dict(seqs=[(1, 90), (1, 33)], Hq=4, Hkv=1, Dk=192, dtype=HF, cache=F8, page=4),
     dict(seqs=[(9, 90), (0, 3), (0, 40), (0, 7)], Hq=8, Hkv=1, Dk=64, page=4),   # many rows in one sequence of few
     dict(seqs=[(1, 3000)], Hq=8, Hkv=1, Dk=64, page=16),
+    dict(seqs=[(1, 40)] * 66 + [(50, 600)], Hq=7, Hkv=1, Dk=128, page=16),
+    dict(seqs=[(300, 700), (33, 1400)], Hq=6, Hkv=2, Dk=128, N=2, rank=1, inter=16),
+    dict(seqs=[(97, 97)], Hq=5, Hkv=5, Dk=256, dtype=HF),
 ]
 
 
@@ -235,6 +258,18 @@ def test_mass(dev, i):
     lse += 0.1 * torch.randn(lse.shape, generator=g)
     lse[int(p.cu[0]), 0] = -math.inf        # this row saw nothing anywhere
     check_mass(p, lse, dev, i)
+
+
+@pytest.mark.parametrize("token", [0, 20, 39])
+def test_mass_of_a_row_without_a_sum(dev, token):
+    """A row whose log-sum-exp is NaN gives NaN to the keys that it sees and nothing to those that it does not."""
+    p = Problem([(40, 340)], 4, 1, 64, 8, seed=140)
+    lse = torch.full((p.T, p.Hq), 6.0)
+    lse[int(p.cu[0]) + token, 2] = math.nan
+    mass = torch.zeros(p.pages, p.page, 1, device=dev)
+    got = mass_call(p, lse, mass, dev).cpu()
+    page, place, _ = p.rows(0)
+    assert torch.equal(torch.isnan(got[page, place, 0]), torch.arange(340) <= 300 + token)
 
 
 def test_mass_sums_to_one_over_the_ranks(dev):
