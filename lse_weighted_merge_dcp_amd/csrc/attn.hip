@@ -467,7 +467,7 @@ __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void attn_keys(AttnArgs p) {
 // ---------------------------------------------------------------------------
 template <typename E, int STEP, int NC, bool TOGETHER>
 __global__ __launch_bounds__(256) void attn_join(AttnArgs p) {
-    constexpr int FLY = 8;                     // parts under way at once
+    constexpr int FLY = NC == 1 ? 8 : 4;       // parts under way at once
     __shared__ f32x4 share[TOGETHER ? 4 : 1][NC][64];
     const int lane = threadIdx.x & 63, wave = (int)dcp::wave_id();
     const int chunk = key_chunk<STEP>(p.m, p.rows, p.slots);
