@@ -277,7 +277,7 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
         load_pages(0, x);
         keep_pages(0, x);
         meet();
-#pragma unroll
+#pragma unroll 1
         for (int t = 0; t < 3; ++t) {
             place_rows(t, page_for(t));
             if (KV8 && t == 2) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
