@@ -265,7 +265,9 @@ __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void attn_keys(AttnArgs p) {
     __shared__ float part_mc[4][32], part_l[4][32];
     __shared__ int part_odd[4];
 
-    const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv), unit = (int)(blockIdx.x / (uint32_t)p.m.Hkv);
+    int hk, unit;
+    heads_together(p.m, hk, unit);
+    if (unit >= p.units) return;
     const Unit u = find_unit<128>(p.m, 32, p.slots, unit);
     if (!u.ok) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = (int)dcp::wave_id(), r = lane & 31, h = lane >> 5;
@@ -632,9 +634,10 @@ hipError_t run(const AttnArgs& a, const AttnPlan& pl, hipStream_t stream) {
     hipError_t e;
     const int d = a.Dk > a.Dv ? a.Dk : a.Dv;
     if (pl.by_keys) {
-        e = d <= 64    ? launch(attn_keys<E, KV8, 64, 64>, grid, block, stream, a)
-            : d <= 128 ? launch(attn_keys<E, KV8, 128, 128>, grid, block, stream, a)
-                       : launch(attn_keys<E, KV8, 256, 256>, grid, block, stream, a);
+        const dim3 near((uint32_t)((int64_t)(pl.units + 7) / 8 * 8 * a.m.Hkv));      // (see heads_together())
+        e = d <= 64    ? launch(attn_keys<E, KV8, 64, 64>, near, block, stream, a)
+            : d <= 128 ? launch(attn_keys<E, KV8, 128, 128>, near, block, stream, a)
+                       : launch(attn_keys<E, KV8, 256, 256>, near, block, stream, a);
         if (e != hipSuccess || pl.slots == 0) return e;
         return run_join<E, 128>(a, stream);
     }

@@ -133,7 +133,7 @@ int check_attn(const dcpa_attn_args* a, Batch& m) {
         !span_ok({{a->T, a->o_T}, {a->Hq, a->o_H}, {a->Dv, 1}}, 2))
         return DCP_ERR_STRIDE;
     const AttnPlan pl = plan_of(a, m);
-    if ((int64_t)pl.units * m.Hkv > kMaxGrid || (pl.slots > 0 && a->T * a->Hq / 4 >= kMaxGrid)) return DCP_ERR_SHAPE;
+    if (((int64_t)pl.units + 7) * m.Hkv > kMaxGrid || (pl.slots > 0 && a->T * a->Hq / 4 >= kMaxGrid)) return DCP_ERR_SHAPE;
     return DCP_OK;
 }
 
@@ -141,7 +141,7 @@ int check_attn(const dcpa_attn_args* a, Batch& m) {
 int check_mass(const dcpa_attn_args* a, Batch& m, MassPlan& pl) {
     if (int st = check_batch(a, m)) return st;
     pl = plan_mass(m, (int)a->Dk, key_pieces(a));
-    return (int64_t)pl.units * m.Hkv > kMaxGrid ? DCP_ERR_SHAPE : DCP_OK;
+    return ((int64_t)pl.units + 7) * m.Hkv > kMaxGrid ? DCP_ERR_SHAPE : DCP_OK;
 }
 
 }  // namespace

@@ -237,6 +237,15 @@ __device__ __forceinline__ int64_t sum_wave(int64_t v) {
                                                    (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63));
 }
 
+// Workgroups that read no key twice, of few rows: those of all key heads of a unit follow each other on one XCD
+// (workgroups go round the eight XCDs), since a cached token's heads lie next to each other, their weights in one
+// line even.
+__device__ __forceinline__ void heads_together(const Batch& m, int& hk, int& unit) {
+    const uint32_t id = blockIdx.x, turn = fdiv(id >> 3, m.fHkv);
+    hk = (int)((id >> 3) - turn * m.fHkv.d);
+    unit = (int)(turn * 8 + (id & 7));
+}
+
 // The share of a batch that one workgroup takes: row tile `tile` of sequence
 // b against the keys [split * chunk, (split + 1) * chunk).  Every wave works
 // it out by itself from the lengths on the device, so ragged batches are

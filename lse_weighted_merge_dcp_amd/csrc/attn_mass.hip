@@ -328,8 +328,10 @@ __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void mass_few(MassArgs p) {
     __shared__ int32_t page_of[4][2][GROUP * KT];
     __shared__ uint64_t row_at[4][KT];
     __shared__ float sum_of[4][GROUP * KT];
-    const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv);
-    const Share u = find_share<128>(p.m, p.slots, false, (int)(blockIdx.x / (uint32_t)p.m.Hkv));
+    int hk, unit;
+    heads_together(p.m, hk, unit);
+    if (unit >= p.units) return;
+    const Share u = find_share<128>(p.m, p.slots, false, unit);
     if (!u.ok) return;
     const int lane = threadIdx.x & 63, wave = (int)dcp::wave_id(), r = lane & 31, h = lane >> 5;
     const int nrows = u.s.n * p.m.G, row_tiles = (nrows + 31) / 32;
@@ -512,10 +514,12 @@ MassPlan plan_mass(const Batch& m, int Dk, bool pieces) {
 namespace {
 template <typename E, bool KV8> hipError_t run(const MassArgs& a, bool few, hipStream_t stream) {
     const dim3 grid((uint32_t)((int64_t)a.units * a.m.Hkv)), block(256);
-    if (few)
-        return a.Dk <= 64    ? launch(mass_few<E, KV8, 64>, grid, block, stream, a)
-               : a.Dk <= 128 ? launch(mass_few<E, KV8, 128>, grid, block, stream, a)
-                             : launch(mass_few<E, KV8, 256>, grid, block, stream, a);
+    if (few) {
+        const dim3 near((uint32_t)((int64_t)(a.units + 7) / 8 * 8 * a.m.Hkv));      // (see heads_together())
+        return a.Dk <= 64    ? launch(mass_few<E, KV8, 64>, near, block, stream, a)
+               : a.Dk <= 128 ? launch(mass_few<E, KV8, 128>, near, block, stream, a)
+                             : launch(mass_few<E, KV8, 256>, near, block, stream, a);
+    }
     const hipError_t e = a.Dk <= 64    ? launch(mass_rows<E, KV8, 64, 64>, grid, block, stream, a)
                          : a.Dk <= 128 ? launch(mass_rows<E, KV8, 128, 64>, grid, block, stream, a)
                          : a.Dk <= 256 ? launch(mass_rows<E, KV8, 256, 32>, grid, block, stream, a)
