@@ -251,7 +251,7 @@ __global__ __launch_bounds__(256, DK > 192 ? 1 : 2) void attn_rows(AttnArgs p) {
 // for the next values likewise, so one of the two is always on its way; the
 // other waves of the CU (two workgroups) fill the gaps.  8-bit rows lie in LDS
 // as in the cache and are widened as fragments: no two waves read the same.
-// 32 contexts of up to 32768 keys, 64 / 8 heads: 361 us, 5.2 TB/s; 64 8-bit ones of
+// 32 contexts of up to 32768 keys, 64 / 8 heads: 357 us, 5.3 TB/s; 64 8-bit ones of
 // up to 8192: 70 us, 3.8 TB/s (149 us when widened on the way into LDS).
 // ---------------------------------------------------------------------------
 template <typename E, bool KV8, int DK, int DV>

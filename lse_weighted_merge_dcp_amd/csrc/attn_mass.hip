@@ -12,7 +12,7 @@
 // straight into LDS, the next tile of 32 while the present one is multiplied
 // (loaded into registers as fragments, 32 rows of 32 bytes to an instruction,
 // the same bytes took twice as long): decode of 16 sequences of up to 16384 keys,
-// 8 key heads of 128, 65 us, 3.8 TB/s.  Many rows (mass_rows) are
+// 8 key heads of 128, 57 us, 4.4 TB/s (65 us with each head on an XCD of its own).  Many rows (mass_rows) are
 // bound by vector instructions (for 64 weights 8 clocks for the power, 4 to scale
 // and 4 to add, beside 16 of matrix instructions at 128 columns):
 // 64 keys to a wave, so that a fragment of queries is read from LDS once for two
