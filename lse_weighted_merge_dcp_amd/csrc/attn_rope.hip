@@ -141,11 +141,15 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
             }
             if (turned) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const bool low = at + i / 4 * 4 < half;
-                    const int j = low ? at + i : at + i - half;
-                    const float c = cs[j], n = cs[half + j];
-                    x[i] = low ? x[i] * c - y[i] * n : x[i] * c + y[i] * n;
+                for (int g = 0; g < 2; ++g) {
+                    const bool low = at + 4 * g < half;
+                    const int j = low ? at + 4 * g : at + 4 * g - half;
+                    const f32x4 c = *(const f32x4*)(cs + j), n = *(const f32x4*)(cs + half + j);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float& v = x[4 * g + i];
+                        v = low ? v * c[i] - y[4 * g + i] * n[i] : v * c[i] + y[4 * g + i] * n[i];
+                    }
                 }
             }
         }
