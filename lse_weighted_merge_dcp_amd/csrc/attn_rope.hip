@@ -5,8 +5,10 @@
 // A group of LPR lanes holds a row, eight elements (16 bytes) to a lane and
 // slot; the mean of squares is one reduction over the group.  Sixteen lanes to a
 // row of 576 (a 64-lane row left most of its second slot idle: 552 us for 8192 x
-// 129 rows against 433 with 16 lanes, 5.6 TB/s; with eight lanes and nine slots
-// the registers leave two waves to a SIMD: 651 us).
+// 129 rows against 420 with 16 lanes, 5.8 TB/s; with eight lanes and nine slots
+// the registers leave two waves to a SIMD: 651 us).  Rows turned by halves ask for
+// cosines and sines too, and for a partner: 4000 x 80 heads of 128 take 41 us, 35
+// turned by pairs, where HBM alone would take 24.
 #include "attn_device.hpp"
 
 namespace dcpa {
@@ -72,16 +74,15 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
     }
     const char* w = query ? p.wq : p.wk;
     const int nw = value ? 0 : query ? p.nq : p.nk, rot = value ? 0 : p.rot, half = rot / 2;
-    // Halves: the partner of a column stands half a range away.  Where that is whole pieces and a piece to a lane, it
-    // comes from another lane; else in fours (half a range is a multiple of four columns), read again, out of the
-    // cache, and before any store (the row may be written in place).
-    const bool from_lane = SLOTS == 1 && half % 8 == 0;
+    // Halves: the partners of four columns are the four that stand half a range (a multiple of four) away.  With a
+    // piece to a lane they come from another lane; else they are read again, out of the cache, and before any store
+    // (the row may be written in place).
     auto partner = [&](int s, int g) {
         const int col = 8 * (s * LPR + lane) + 4 * g;
         return col - p.off < half ? col + half : col - half;
     };
     dcp::Vec<16> other[SLOTS];
-    if (!PAIRS && !from_lane)
+    if constexpr (!PAIRS && SLOTS > 1)
 #pragma unroll
         for (int s = 0; s < SLOTS; ++s) {
             const int at = 8 * (s * LPR + lane) - p.off;
@@ -125,9 +126,13 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
             }
         } else {
             float y[8];
-            if (from_lane) {
+            if constexpr (SLOTS == 1) {
+                const bool other_four = half % 8 != 0;        // (of the piece)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = __shfl(x[i], partner(s, 0) / 8 & (LPR - 1), LPR);
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        y[4 * g + i] = __shfl(other_four ? x[4 * (1 - g) + i] : x[4 * g + i], partner(s, g) / 8 & (LPR - 1), LPR);
             } else if (turned) {
                 dcp::Cvt<E, 16>::unpack(other[s], y);
 #pragma unroll
