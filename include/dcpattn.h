@@ -134,7 +134,10 @@ int dcpa_qk_norm_rope_append(const dcpa_rope_args* a, void* stream);
  * whatever bits lie there.
  *
  * Scores, sums and outputs are accumulated in fp32; the weights are rounded
- * to `dtype` for the product with the values, the output once to `dtype`.
+ * to `dtype` for the product with the values, the output once to `dtype`.  Where
+ * rows are few (at most 32 to a sequence on average, rows of a token in one key
+ * head counted, Dk and Dv up to 256 and in 8 bits multiples of 16) what that
+ * rounding leaves of a weight goes through a second product.
  *
  * dtype: DCP_F16 or DCP_BF16 (q, out).  Hq a multiple of Hkv.  Dk, Dv
  * multiples of 8, at most 256, or in the latent layout (v == NULL) Dk <= 576,

@@ -250,9 +250,11 @@ __global__ __launch_bounds__(256, DK > 192 ? 1 : 2) void attn_rows(AttnArgs p) {
 // asks for the next keys as soon as its products have read the present ones,
 // for the next values likewise, so one of the two is always on its way; the
 // other waves of the CU (two workgroups) fill the gaps.  8-bit rows lie in LDS
-// as in the cache and are widened as fragments: no two waves read the same.
-// 32 contexts of up to 32768 keys, 64 / 8 heads: 357 us, 5.3 TB/s; 64 8-bit ones of
-// up to 8192: 70 us, 3.8 TB/s (149 us when widened on the way into LDS).
+// as in the cache and are widened as fragments: no two waves read the same.  The
+// matrix instructions have time to spare, so the weights take two products, their
+// remainders the second (see weights()).  32 contexts of up to 32768 keys, 64 / 8
+// heads: 369 us, 5.1 TB/s, with one product too; 64 8-bit ones of up to 8192: 72.9 us,
+// 3.6 TB/s, 71.5 with one (149 us when widened on the way into LDS).
 // ---------------------------------------------------------------------------
 template <typename E, bool KV8, int DK, int DV>
 __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void attn_keys(AttnArgs p) {
@@ -344,7 +346,7 @@ __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void attn_keys(AttnArgs p) {
         // keys of t are there; its values may still be on their way
         asm volatile("s_waitcnt vmcnt(%0)" :: "n"(NV) : "memory");
         f32x16 s[1][1];
-        uint32_t pr[1][1][8];
+        uint32_t pr[1][1][8], rest[1][1][8];
         if constexpr (KV8) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[0][0][i] = 0.0f;
@@ -366,20 +368,20 @@ __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void attn_keys(AttnArgs p) {
         }
         const int lim[1] = {vis - t * KT};
         const bool full = now == 0xffffffffu && vmin >= (t + 1) * KT;
-        weights<E>(w, s, pr, now, lim, full, p.c);
+        weights<E>(w, s, pr, rest, now, lim, full, p.c);
         // values of t
         if (next) asm volatile("s_waitcnt vmcnt(%0)" :: "n"(NK) : "memory");
         else dma_wait();
         if constexpr (KV8) {
             const int g = (lane >> 4) & 1, li = lane & 15, j = li >> 1, key = 4 * h + (j & 3) + 8 * (j >> 2);
-            outputs<E, DK, DV, 1, KT>(w, pr, [&](int cb, int ks) {
+            outputs<E, DK, DV, 1, KT>(w, pr, rest, [&](int cb, int ks) {
                 const uint32_t a = vbuf + (uint32_t)((ks * 16 + key) * VROW + ((2 * cb + g) ^ turn(true, ks * 16 + key)) * 16 + (li & 1) * 8);
                 return widen8<E>(lds_read_tr8(a));
             });
         } else {
             ValuePlace<VROW> vp;
             vp.set(vbuf, lane);
-            outputs<E, DK, DV, 1, KT>(w, pr, [&](int cb, int ks) { return vp.read(cb, ks); });
+            outputs<E, DK, DV, 1, KT>(w, pr, rest, [&](int cb, int ks) { return vp.read(cb, ks); });
         }
         if (!full) odd |= odd_values<E, KV8>(vbuf, VB);
         if (t % GROUP == 0 && t + GROUP < tiles) {

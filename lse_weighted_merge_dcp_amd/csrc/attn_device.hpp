@@ -42,6 +42,9 @@ template <> struct Mat<BF16T> {
         v.y = (__bf16)b;
         return __builtin_bit_cast(uint32_t, v);
     }
+    // the two halves of a pack2, widened
+    static __device__ __forceinline__ float low(uint32_t v) { return __uint_as_float(v << 16); }
+    static __device__ __forceinline__ float high(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
     static constexpr uint32_t kExp = 0x7f807f80u;   // exponent bits of the two halves
     // The weights' exponent is free: with the row maximum at 2^0 the smallest
     // bf16 is far below fp32's resolution of the sum.
@@ -58,6 +61,8 @@ template <> struct Mat<F16T> {
         v.y = (_Float16)b;
         return __builtin_bit_cast(uint32_t, v);
     }
+    static __device__ __forceinline__ float low(uint32_t v) { return (float)__builtin_bit_cast(f16x2, v).x; }
+    static __device__ __forceinline__ float high(uint32_t v) { return (float)__builtin_bit_cast(f16x2, v).y; }
     static constexpr uint32_t kExp = 0x7c007c00u;
     // fp16 loses relative precision below 2^-14: the row maximum stands at
     // 2^8, so that weights down to 2^-22 of the largest keep 11 bits.

@@ -133,11 +133,14 @@ __device__ __forceinline__ void raise_top(Rows<DK, DV, RB>& w, float best, float
     }
 }
 
-// Weights of a tile's scores, as B operands; updates maximum, sum and, where the
+// Weights of a tile's scores, as B operands: p, rounded to the payload type, and
+// in `rest` what the rounding left, so that the two together hold a weight to
+// 2^-17 (bf16) or 2^-22 (fp16) of itself.  Updates maximum, sum and, where the
 // maximum moved, the outputs.  full: no masking needed.
 template <typename E, int DK, int DV, int RB, int NB>
 __device__ __forceinline__ void weights(Rows<DK, DV, RB>& w, f32x16 (&s)[RB][NB], uint32_t (&p)[RB][NB][8],
-                                        uint64_t there, const int (&vis)[RB], bool full, float c) {
+                                        uint32_t (&rest)[RB][NB][8], uint64_t there, const int (&vis)[RB], bool full,
+                                        float c) {
     if (!full) mask_scores(s, there, vis);
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
@@ -156,14 +159,16 @@ __device__ __forceinline__ void weights(Rows<DK, DV, RB>& w, f32x16 (&s)[RB][NB]
                 const float y = exp2_fast(__builtin_fmaf(s[rb][kb][2 * i + 1], c, -w.mc[rb]));
                 sum += x + y;
                 p[rb][kb][i] = Mat<E>::pack2(x, y);
+                rest[rb][kb][i] = Mat<E>::pack2(x - Mat<E>::low(p[rb][kb][i]), y - Mat<E>::high(p[rb][kb][i]));
             }
         w.l[rb] += sum;
     }
 }
 
-// Outputs += weights x values of KT keys; `fragment` as ValuePlace::read.
+// Outputs += weights x values of KT keys, the weights in two products (see weights()); `fragment` as ValuePlace::read.
 template <typename E, int DK, int DV, int RB, int KT, typename F>
-__device__ __forceinline__ void outputs(Rows<DK, DV, RB>& w, const uint32_t (&p)[RB][KT / 32][8], F&& fragment) {
+__device__ __forceinline__ void outputs(Rows<DK, DV, RB>& w, const uint32_t (&p)[RB][KT / 32][8],
+                                        const uint32_t (&rest)[RB][KT / 32][8], F&& fragment) {
 #pragma unroll
     for (int cb = 0; cb < DV / 32; ++cb)
 #pragma unroll
@@ -171,8 +176,9 @@ __device__ __forceinline__ void outputs(Rows<DK, DV, RB>& w, const uint32_t (&p)
             const u32x4 a = fragment(cb, ks);
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb) {
-                const uint32_t* pp = &p[rb][ks / 2][(ks & 1) * 4];
+                const uint32_t *pp = &p[rb][ks / 2][(ks & 1) * 4], *pr = &rest[rb][ks / 2][(ks & 1) * 4];
                 w.o[rb][cb] = Mat<E>::mma(a, u32x4{pp[0], pp[1], pp[2], pp[3]}, w.o[rb][cb]);
+                w.o[rb][cb] = Mat<E>::mma(a, u32x4{pr[0], pr[1], pr[2], pr[3]}, w.o[rb][cb]);
             }
         }
 }
