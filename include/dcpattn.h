@@ -137,7 +137,10 @@ int dcpa_qk_norm_rope_append(const dcpa_rope_args* a, void* stream);
  * to `dtype` for the product with the values, the output once to `dtype`.  Where
  * rows are few (at most 32 to a sequence on average, rows of a token in one key
  * head counted, Dk and Dv up to 256 and in 8 bits multiples of 16) what that
- * rounding leaves of a weight goes through a second product.
+ * rounding leaves of a weight goes through a second product, so that a weight is
+ * held to 2^-16 (bf16) or 2^-22 (fp16) of itself.  wide_weights != 0 asks for the
+ * same in every other case, where matrix products bound the call and it takes
+ * 1.2 to 1.4 times as long.
  *
  * dtype: DCP_F16 or DCP_BF16 (q, out).  Hq a multiple of Hkv.  Dk, Dv
  * multiples of 8, at most 256, or in the latent layout (v == NULL) Dk <= 576,
@@ -161,7 +164,7 @@ typedef struct {
     float* lse;           int64_t l_T, l_H;   /* [T, Hq] words, nullable */
     void* workspace;      int64_t workspace_bytes;
     int64_t B, T, Hq, Hkv, Dk, Dv, num_pages, page_size, max_pages;
-    int64_t N, rank, interleave, causal, dtype, cache_dtype, lse_base;
+    int64_t N, rank, interleave, causal, dtype, cache_dtype, lse_base, wide_weights;
     double scale, k_scale, v_scale;
 } dcpa_attn_args;
 int dcpa_paged_attn(const dcpa_attn_args* a, void* stream);
@@ -175,7 +178,7 @@ int64_t dcpa_paged_attn_workspace(const dcpa_attn_args* a);
  * and lse the merged log-sum-exp over all ranks (so that the weights of one
  * row over all ranks sum to 1).  A row whose lse is -inf adds nothing.  The
  * call takes the fields of dcpa_attn_args it needs: v, Dv, v_scale (positive
- * all the same) and out are ignored, lse is read.  mass holds fp32 with strides
+ * all the same), out and wide_weights are ignored, lse is read.  mass holds fp32 with strides
  * m_P, m_S, m_H.  A page must not stand twice in the table rows of one call
  * (two sequences that share a page: two calls).  `workspace` holds the parts of
  * rows that are split over workgroups, dcpa_attn_mass_workspace gives its size.

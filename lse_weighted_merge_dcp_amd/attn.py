@@ -49,7 +49,7 @@ SIGNATURES = {
 }
 # The argument structs: every field 8 bytes, in the header's order.
 ROPE_ARGS = struct.Struct("=41q3d")
-ATTN_ARGS = struct.Struct("=40q3d")
+ATTN_ARGS = struct.Struct("=41q3d")
 EVICT_ARGS = struct.Struct("=33q")
 
 _DTYPE = {torch.float16: _lib.DCP_F16, torch.bfloat16: _lib.DCP_BF16}
@@ -183,7 +183,7 @@ def qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tens
 
 
 def _attn_args(q, k_cache, v_cache, block_table, cu_q, kv_len, seq_len, scale, Dv, rank, n_ranks, interleave, causal,
-               k_scale, v_scale, base_e, out, lse, ws, ws_bytes):
+               k_scale, v_scale, base_e, wide, out, lse, ws, ws_bytes):
     """The packed dcpa_attn_args of an attention or weight call."""
     T, Hq, Dk = q.shape
     pages, page_size, Hkv = k_cache.shape[0], k_cache.shape[1], k_cache.shape[2]
@@ -215,7 +215,7 @@ def _attn_args(q, k_cache, v_cache, block_table, cu_q, kv_len, seq_len, scale, D
         lse.data_ptr() if lse is not None else 0, ls[0], ls[1], ws, ws_bytes,
         B, T, Hq, Hkv, Dk, Dv, pages, page_size, block_table.shape[1],
         n_ranks, rank, interleave, 1 if causal else 0, dt, ct,
-        _lib.DCP_LSE_BASE_E if base_e else _lib.DCP_LSE_BASE_2, scale, k_scale, v_scale)
+        _lib.DCP_LSE_BASE_E if base_e else _lib.DCP_LSE_BASE_2, 1 if wide else 0, scale, k_scale, v_scale)
 
 
 _WS_AT = 22 * 8      # offset of workspace and workspace_bytes in the packed struct
@@ -241,8 +241,9 @@ def dcp_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional[tor
                    block_table: torch.Tensor, cu_q: torch.Tensor, kv_len: torch.Tensor, *,
                    seq_len: Optional[torch.Tensor] = None, scale: Optional[float] = None, v_dim: Optional[int] = None,
                    rank: int = 0, n_ranks: int = 1, interleave: int = 1, causal: bool = True, k_scale: float = 1.0,
-                   v_scale: float = 1.0, is_lse_base_on_e: bool = True, out: Optional[torch.Tensor] = None,
-                   out_lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+                   v_scale: float = 1.0, is_lse_base_on_e: bool = True, wide_weights: bool = False,
+                   out: Optional[torch.Tensor] = None, out_lse: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None):
     """Attention of the new tokens q [T,Hq,Dk] over this rank's paged cache:
     k_cache [pages,page_size,Hkv,Dk], v_cache [pages,page_size,Hkv,Dv], or None
     with v_dim = Dv: values are the first Dv columns of the keys.  Sequence b's
@@ -252,7 +253,10 @@ def dcp_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional[tor
     causal and n_ranks > 1).  Returns (out [T,Hq,Dv], lse [T,Hq] fp32), which
     ops.dcp_pack_a2a_send takes; a token that sees no key on this rank gets the
     neutral pair (0, -inf).  Rows outside the sequences are left as they were.
-    scale defaults to Dk ** -0.5."""
+    scale defaults to Dk ** -0.5.  The weights are rounded to q's type for the
+    product with the values; with wide_weights what the rounding leaves takes a
+    second product (1.2 to 1.4 times as long for many or latent rows; few rows
+    have it always)."""
     dev = _on_gpu(q, k_cache, v_cache, block_table, cu_q, kv_len, seq_len, out, out_lse, workspace)
     _rows(q, "q", 3)
     _rows(k_cache, "k_cache", 4)
@@ -277,7 +281,7 @@ def dcp_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional[tor
         raise ValueError("bad out_lse tensor")
     h = lib()
     args = _attn_args(q, k_cache, v_cache, block_table, cu_q, kv_len, seq_len, scale, Dv, rank, n_ranks, interleave,
-                      causal, k_scale, v_scale, is_lse_base_on_e, out, out_lse, 0, 0)
+                      causal, k_scale, v_scale, is_lse_base_on_e, wide_weights, out, out_lse, 0, 0)
     args, _keep = _with_workspace(args, h.dcpa_paged_attn_workspace, "dcpa_paged_attn", workspace, q)
     _call(h.dcpa_paged_attn, "dcpa_paged_attn", dev, args)
     return out, out_lse
@@ -304,7 +308,7 @@ def dcp_attn_mass(q: torch.Tensor, k_cache: torch.Tensor, lse: torch.Tensor, mas
         raise ValueError("mass must be float32 [pages,page_size,Hkv]")
     h = lib()
     args = _attn_args(q, k_cache, None, block_table, cu_q, kv_len, seq_len, scale, 8, rank, n_ranks, interleave,
-                      causal, k_scale, 1.0, is_lse_base_on_e, None, lse, 0, 0)
+                      causal, k_scale, 1.0, is_lse_base_on_e, False, None, lse, 0, 0)
     args, _keep = _with_workspace(args, h.dcpa_attn_mass_workspace, "dcpa_attn_mass", workspace, q)
     m = mass.stride()
     _call(h.dcpa_attn_mass, "dcpa_attn_mass", dev, args, mass.data_ptr(), m[0], m[1], m[2])

@@ -25,8 +25,12 @@ namespace {
 // PFLOP/s.)  Wider rows take 32 keys to a tile, and where the registers hold 192
 // columns two workgroups to a CU still fit: 1511 tokens of 192 / 128 columns take
 // 60 us, 133 us in tiles of 256.
+// The weights are rounded to the payload type for the product with the values,
+// whose error is then that of the output's own rounding once more.  WIDE: what the
+// rounding left takes a second product, half as many matrix instructions again:
+// the chunk above takes 631 us with it, 473 without.
 // ---------------------------------------------------------------------------
-template <typename E, bool KV8, bool EXACT, int DK, int DV, int KT>
+template <typename E, bool KV8, bool EXACT, int DK, int DV, int KT, bool WIDE>
 __global__ __launch_bounds__(256, DK > 192 ? 1 : 2) void attn_rows(AttnArgs p) {
     constexpr int R = 128, KC = DK / 8, VC = DV / 8, NB = KT / 32, ST = DK / 16, CB = DV / 32, KS = KT / 16;
     constexpr int KROW = KC * 16, VROW = VC * 16;
@@ -185,7 +189,7 @@ __global__ __launch_bounds__(256, DK > 192 ? 1 : 2) void attn_rows(AttnArgs p) {
         if (t < mine) {
             raise_top<E>(w, top, p.c);
             float mc = w.mc[0];
-            uint32_t pr[1][NB][8];
+            uint32_t pr[1][NB][8], rest[NB][8];
             float sum = 0.0f;
             // pairs of weights, as B operands
             auto power = [&](int j) {
@@ -194,6 +198,11 @@ __global__ __launch_bounds__(256, DK > 192 ? 1 : 2) void attn_rows(AttnArgs p) {
                 sum += x + y;
                 pr[0][j / 8][j % 8] = Mat<E>::pack2(x, y);
                 asm volatile("" : "+v"(pr[0][j / 8][j % 8]), "+v"(sum));     // (here, not where it is used)
+                if constexpr (WIDE) {
+                    uint32_t& left = rest[j / 8][j % 8];
+                    left = Mat<E>::pack2(x - Mat<E>::low(pr[0][j / 8][j % 8]), y - Mat<E>::high(pr[0][j / 8][j % 8]));
+                    asm volatile("" : "+v"(left));
+                }
             };
             const bool more = t + 1 < mine, all = full;
             if (more) {
@@ -219,6 +228,10 @@ __global__ __launch_bounds__(256, DK > 192 ? 1 : 2) void attn_rows(AttnArgs p) {
                 if (n + AHEAD < CB * KS) a[n + AHEAD] = vp.read((n + AHEAD) % CB, (n + AHEAD) / CB);
                 const uint32_t* pp = &pr[0][n / CB / 2][(n / CB & 1) * 4];
                 w.o[0][n % CB] = Mat<E>::mma(a[n], u32x4{pp[0], pp[1], pp[2], pp[3]}, w.o[0][n % CB]);
+                if constexpr (WIDE) {
+                    const uint32_t* pl = &rest[n / CB / 2][(n / CB & 1) * 4];
+                    w.o[0][n % CB] = Mat<E>::mma(a[n], u32x4{pl[0], pl[1], pl[2], pl[3]}, w.o[0][n % CB]);
+                }
 #pragma unroll
                 for (int j = n * 16 * NB / (CB * KS); j < (n + 1) * 16 * NB / (CB * KS); ++j)
                     top = fmaxf(top, next[0][j / 16][j % 16]);       // (of no use behind the last)
@@ -630,12 +643,34 @@ hipError_t run_join(const AttnArgs& a, hipStream_t stream) {
                        : launch(attn_join<E, STEP, 2, false>, grid, block, stream, a);
 }
 
+template <typename E, bool KV8, bool WIDE>
+hipError_t run_rows(const AttnArgs& a, const AttnPlan& pl, dim3 grid, dim3 block, hipStream_t stream) {
+    // (whole rows need no test of columns)
+    const int d = a.Dk > a.Dv ? a.Dk : a.Dv;
+    hipError_t e;
+    if (d <= 64)
+        e = a.Dk == 64 && a.Dv == 64 ? launch(attn_rows<E, KV8, true, 64, 64, 64, WIDE>, grid, block, stream, a)
+                                     : launch(attn_rows<E, KV8, false, 64, 64, 64, WIDE>, grid, block, stream, a);
+    else if (d <= 128)
+        e = a.Dk == 128 && a.Dv == 128 ? launch(attn_rows<E, KV8, true, 128, 128, 64, WIDE>, grid, block, stream, a)
+                                       : launch(attn_rows<E, KV8, false, 128, 128, 64, WIDE>, grid, block, stream, a);
+    else {
+        e = a.Dk <= 192 && a.Dv <= 128   ? launch(attn_rows<E, KV8, false, 192, 128, 32, WIDE>, grid, block, stream, a)
+            : a.Dk <= 192 && a.Dv <= 192 ? launch(attn_rows<E, KV8, false, 192, 192, 32, WIDE>, grid, block, stream, a)
+                                         : launch(attn_rows<E, KV8, false, 256, 256, 32, WIDE>, grid, block, stream, a);
+        if (e != hipSuccess || pl.slots == 0) return e;
+        return run_join<E, 32>(a, stream);
+    }
+    if (e != hipSuccess || pl.slots == 0) return e;
+    return run_join<E, 64>(a, stream);
+}
+
 template <typename E, bool KV8>
-hipError_t run(const AttnArgs& a, const AttnPlan& pl, hipStream_t stream) {
+hipError_t run(const AttnArgs& a, const AttnPlan& pl, bool wide, hipStream_t stream) {
     const dim3 grid((uint32_t)((int64_t)pl.units * a.m.Hkv)), block(256);
     hipError_t e;
-    const int d = a.Dk > a.Dv ? a.Dk : a.Dv;
     if (pl.by_keys) {
+        const int d = a.Dk > a.Dv ? a.Dk : a.Dv;
         const dim3 near((uint32_t)((int64_t)(pl.units + 7) / 8 * 8 * a.m.Hkv));      // (see heads_together())
         e = d <= 64    ? launch(attn_keys<E, KV8, 64, 64>, near, block, stream, a)
             : d <= 128 ? launch(attn_keys<E, KV8, 128, 128>, near, block, stream, a)
@@ -644,38 +679,23 @@ hipError_t run(const AttnArgs& a, const AttnPlan& pl, hipStream_t stream) {
         return run_join<E, 128>(a, stream);
     }
     if (pl.latent) {
-        e = launch_latent(a, grid, std::is_same_v<E, BF16T>, KV8, stream);
+        e = launch_latent(a, grid, std::is_same_v<E, BF16T>, KV8, wide, stream);
         if (e != hipSuccess || pl.slots == 0) return e;
         return run_join<E, 32>(a, stream);
     }
-    // (whole rows need no test of columns)
-    if (d <= 64)
-        e = a.Dk == 64 && a.Dv == 64 ? launch(attn_rows<E, KV8, true, 64, 64, 64>, grid, block, stream, a)
-                                     : launch(attn_rows<E, KV8, false, 64, 64, 64>, grid, block, stream, a);
-    else if (d <= 128)
-        e = a.Dk == 128 && a.Dv == 128 ? launch(attn_rows<E, KV8, true, 128, 128, 64>, grid, block, stream, a)
-                                       : launch(attn_rows<E, KV8, false, 128, 128, 64>, grid, block, stream, a);
-    else {
-        e = a.Dk <= 192 && a.Dv <= 128   ? launch(attn_rows<E, KV8, false, 192, 128, 32>, grid, block, stream, a)
-            : a.Dk <= 192 && a.Dv <= 192 ? launch(attn_rows<E, KV8, false, 192, 192, 32>, grid, block, stream, a)
-                                         : launch(attn_rows<E, KV8, false, 256, 256, 32>, grid, block, stream, a);
-        if (e != hipSuccess || pl.slots == 0) return e;
-        return run_join<E, 32>(a, stream);
-    }
-    if (e != hipSuccess || pl.slots == 0) return e;
-    return run_join<E, 64>(a, stream);
+    return wide ? run_rows<E, KV8, true>(a, pl, grid, block, stream) : run_rows<E, KV8, false>(a, pl, grid, block, stream);
 }
 
 }  // namespace
 
-hipError_t launch_attn(const AttnArgs& arg, const AttnPlan& pl, bool bf16, bool kv8, hipStream_t stream) {
+hipError_t launch_attn(const AttnArgs& arg, const AttnPlan& pl, bool bf16, bool kv8, bool wide, hipStream_t stream) {
     AttnArgs a = arg;
     if (!pl.latent && a.v == nullptr) {        // narrow rows: the values are read as columns of their own
         a.v = a.k;
         a.v_P = a.k_P; a.v_S = a.k_S; a.v_H = a.k_H;
     }
-    if (bf16) return kv8 ? run<BF16T, true>(a, pl, stream) : run<BF16T, false>(a, pl, stream);
-    return kv8 ? run<F16T, true>(a, pl, stream) : run<F16T, false>(a, pl, stream);
+    if (bf16) return kv8 ? run<BF16T, true>(a, pl, wide, stream) : run<BF16T, false>(a, pl, wide, stream);
+    return kv8 ? run<F16T, true>(a, pl, wide, stream) : run<F16T, false>(a, pl, wide, stream);
 }
 
 }  // namespace dcpa

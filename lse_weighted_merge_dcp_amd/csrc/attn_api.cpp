@@ -208,7 +208,8 @@ int dcpa_paged_attn(const dcpa_attn_args* a, void* stream) {
     // (in the latent layout the values are the keys' own columns)
     k.vs = (float)(a->v ? a->v_scale : a->k_scale);
     k.lmul = a->lse_base == DCP_LSE_BASE_E ? kLn2 : 1.0f;
-    return status(launch_attn(k, pl, a->dtype == DCP_BF16, a->cache_dtype == DCP_FP8_E4M3, (hipStream_t)stream));
+    return status(launch_attn(k, pl, a->dtype == DCP_BF16, a->cache_dtype == DCP_FP8_E4M3, a->wide_weights != 0,
+                              (hipStream_t)stream));
 }
 
 int64_t dcpa_attn_mass_workspace(const dcpa_attn_args* a) {

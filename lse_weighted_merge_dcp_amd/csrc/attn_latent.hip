@@ -12,7 +12,11 @@
 // their 68 matrix instructions take.  Between those instructions stand the powers
 // of the present tile, the maximum of the next, the addresses and the nine
 // requests of the one after that.  1024 tokens of 96 heads over 2048 keys a rank:
-// 416 us, 1.02 PFLOP/s; 64 sequences of one token, 128 heads: 181 us.
+// 416 us, 1.02 PFLOP/s; 64 sequences of one token, 128 heads: 180 us.
+// The weights are rounded to the payload type for the product with the values,
+// whose error is then that of the output's own rounding once more.  WIDE: what the
+// rounding left takes a second product, 100 matrix instructions to a tile for 68, and the
+// two calls above take 532 and 220 us.
 //
 // The compiler would move outputs between the two halves of the register file
 // around every use outside a product, and spill.  So the outputs live in a0 ..
@@ -110,8 +114,8 @@ __device__ __forceinline__ uint64_t lane64(uint64_t x, int lane) {
 }
 
 // EXACT: rows of all 576 columns (others are padded with zeros).
-template <typename E, bool KV8, bool EXACT>
-__global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
+template <typename E, bool KV8, bool EXACT, bool WIDE>
+__device__ __forceinline__ void latent_rows(const AttnArgs& p) {
     constexpr int R = 128, STEPS = DK / 16, CBS = DV / 32;
     // Tiles t and t + 1 are read while t + 2 and t + 3 arrive.  8-bit rows arrive as
     // they lie in the cache and are widened when their turn comes.
@@ -348,7 +352,7 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
             asm volatile("s_nop 15\n\ts_nop 3");
             times<DV / 8>([&](auto i) { out_scale4<i * 4>(f); });
         }
-        uint32_t pr[8];
+        uint32_t pr[8], rest[8];
         float sum = 0.0f;
         f32x16 n;
         u32x4 ql[QL];
@@ -376,6 +380,10 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
                 if constexpr (st % 4 == 3) {
                     pr[st / 4] = Mat<E>::pack2(s[st / 2 - 1], s[st / 2]);
                     asm volatile("" : "+v"(pr[st / 4]));
+                    if constexpr (WIDE) {
+                        rest[st / 4] = Mat<E>::pack2(s[st / 2 - 1] - Mat<E>::low(pr[st / 4]), s[st / 2] - Mat<E>::high(pr[st / 4]));
+                        asm volatile("" : "+v"(rest[st / 4]));
+                    }
                 }
             }
             if constexpr (!KV8 && st == 2) place_rows(t + 3, page);
@@ -394,6 +402,11 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
             // the one before it
             constexpr int half = i / CBS, cb = i % CBS, m = i + VAHEAD;
             out_mma<E, cb>(vf[i % VAHEAD], half == 0 ? p0 : p1);
+            if constexpr (WIDE) {
+                constexpr int at = half * 4;
+                DCPA_PIN;
+                out_mma<E, cb>(vf[i % VAHEAD], u32x4{rest[at], rest[at + 1], rest[at + 2], rest[at + 3]});
+            }
             if constexpr (m < 2 * CBS) vf[i % VAHEAD] = value_fragment(buf, m % CBS * 2 + m / CBS);
             DCPA_PIN;
             // the next tile's maximum; its last product was done four products ago
@@ -514,13 +527,23 @@ __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
     });
 }
 
+template <typename E, bool KV8, bool EXACT> __global__ __launch_bounds__(256, 1) void attn_latent(AttnArgs p) {
+    latent_rows<E, KV8, EXACT, false>(p);
+}
+template <typename E, bool KV8, bool EXACT> __global__ __launch_bounds__(256, 1) void latent_wide(AttnArgs p) {
+    latent_rows<E, KV8, EXACT, true>(p);
+}
+
 }  // namespace
 
-hipError_t launch_latent(const AttnArgs& a, dim3 grid, bool bf16, bool kv8, hipStream_t stream) {
+hipError_t launch_latent(const AttnArgs& a, dim3 grid, bool bf16, bool kv8, bool wide, hipStream_t stream) {
     const dim3 block(256);
     auto run = [&](auto e, auto k) {
         using E = decltype(e);
         constexpr bool K8 = decltype(k)::value;
+        if (wide)
+            return a.Dk == DK ? launch(latent_wide<E, K8, true>, grid, block, stream, a)
+                              : launch(latent_wide<E, K8, false>, grid, block, stream, a);
         return a.Dk == DK ? launch(attn_latent<E, K8, true>, grid, block, stream, a)
                           : launch(attn_latent<E, K8, false>, grid, block, stream, a);
     };

@@ -60,9 +60,10 @@ struct AttnPlan {
 };
 // pieces: the cache's rows and strides are whole pieces of 16 bytes.
 AttnPlan plan_attn(const Batch& m, int Dk, int Dv, bool pieces);
-hipError_t launch_attn(const AttnArgs& a, const AttnPlan& pl, bool bf16, bool kv8, hipStream_t stream);
+// wide: the weights' remainders take a second product where rows are many or latent too.
+hipError_t launch_attn(const AttnArgs& a, const AttnPlan& pl, bool bf16, bool kv8, bool wide, hipStream_t stream);
 
-hipError_t launch_latent(const AttnArgs& a, dim3 grid, bool bf16, bool kv8, hipStream_t stream);
+hipError_t launch_latent(const AttnArgs& a, dim3 grid, bool bf16, bool kv8, bool wide, hipStream_t stream);
 
 struct MassArgs {
     Batch m;

@@ -57,3 +57,36 @@ def test_few_rows(dev, D, cache, dtype):
 
 def test_few_rows_of_split_keys(dev):
     check(Problem([(1, 6000), (1, 3)], 8, 1, 128, 128, page=64, seed=2), dev)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("cache", [None, F8], ids=["16-bit", "fp8"])
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (40, 64), (128, 128), (72, 128), (192, 128), (192, 192), (256, 256)])
+def test_many_rows_on_request(dev, Dk, Dv, cache, dtype):
+    check(Problem([(70, 150), (33, 33)], 4, 2, Dk, Dv, dtype=dtype, cache=cache, page=24, seed=Dk + Dv), dev, wide_weights=True)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("cache", [None, F8], ids=["16-bit", "fp8"])
+@pytest.mark.parametrize("seqs,Hq,Dk,Dv", [([(1, 300), (1, 1)], 128, 576, 512), ([(9, 150)], 40, 576, 512), ([(3, 90)], 40, 320, 256),
+                                           ([(1, 2000)], 16, 576, 512)])
+def test_latent_rows_on_request(dev, seqs, Hq, Dk, Dv, cache, dtype):
+    check(Problem(seqs, Hq, 1, Dk, Dv, dtype=dtype, cache=cache, shared=True, seed=Hq), dev, wide_weights=True)
+
+
+@pytest.mark.parametrize("shared", [False, True], ids=["grouped", "latent"])
+def test_request_changes_nothing_but_the_rounding(dev, shared):
+    """Missing pages, rows without keys, several ranks and growing scores: as without it, within the looser bound."""
+    from test_gpu_attn import check as as_ever
+
+    shape = (20, 1, 576, 512) if shared else (4, 1, 128, 128)
+    p = Problem([(50, 50), (20, 300), (1, 7)], *shape, N=3, rank=2, shared=shared, seed=9)
+    p.table[1, 2] = -1
+    as_ever(p, *call(p, dev, wide_weights=True))
+    p = Problem([(40, 400)], *shape, shared=shared, seed=10)
+    for j in range(400):
+        page, at = p.place(0, j)
+        p.k[page, at] = 0.0
+        p.k[page, at, :, 0] = j / 4.0
+    p.q[:, :, 0] = 8.0
+    as_ever(p, *call(p, dev, wide_weights=True))
