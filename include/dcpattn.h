@@ -194,7 +194,8 @@ int64_t dcpa_attn_mass_workspace(const dcpa_attn_args* a);
  * of highest mass (NaN above all numbers, ties to the lowest index).  The kept
  * keys, in their old order, are copied to places 0 .. n-1 of the pages
  * dst_table[b, :], with their values (v nullable) and their mass.  kept[b, h,
- * i] is the old index of the i-th, -1 from n on; new_len[b] = n.
+ * i] is the old index of the i-th, -1 from n on; new_len[b] = n (new_len may be
+ * kv_len itself, else the two arrays must lie apart: DCPA_ERR_VALUE).
  *
  * Source pages are only read: destination pages must not be source pages of
  * any sequence of the call, nor appear twice.  A destination entry outside

@@ -325,8 +325,8 @@ def dcp_cache_evict(mass: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional
     and their mass are copied, in their old order, into the pages
     dst_table[b] (int32 [B, pages]) of the same pools; source pages are only
     read, and must not be among the destinations.  Returns (new_len [B] int32,
-    kept [B,Hkv,budget] int32: the old index of each kept key, -1 behind the
-    last)."""
+    which may be kv_len itself, kept [B,Hkv,budget] int32: the old index of each
+    kept key, -1 behind the last)."""
     dev = _on_gpu(mass, k_cache, v_cache, block_table, kv_len, dst_table, new_len, kept)
     _rows(k_cache, "k_cache", 4)
     pages, page_size, Hkv, Dk = k_cache.shape

@@ -355,6 +355,9 @@ int dcpa_cache_evict(const dcpa_evict_args* a, void* stream) {
     if (!rows(8) || !aligned(a->mass, 4) || !aligned(a->kv_len, 4) || !aligned(a->new_len, 4) || !aligned(a->kept, 4) ||
         !aligned(a->block_table, 4) || !aligned(a->dst_table, 4))
         return DCP_ERR_ALIGN;
+    // new lengths over the old ones of other sequences would be read for them
+    const uintptr_t l0 = (uintptr_t)a->kv_len, l1 = (uintptr_t)a->new_len, bytes = (uintptr_t)a->B * 4;
+    if (l0 != l1 && (l0 < l1 ? l1 - l0 : l0 - l1) < bytes) return DCPA_ERR_VALUE;
     EvictArgs k;
     k.mass = (char*)a->mass;
     k.m_P = a->m_P; k.m_S = a->m_S; k.m_H = a->m_H;

@@ -13,7 +13,8 @@
 // keys: 23 us, a chain of passes and barriers.
 // evict_gather: copies the kept rows and weights to their new places, a group
 // of lanes to a row.  Bound by the bytes of the rows: 64 x 4096 rows of 256 + 256
-// bytes in 54 us, 5.0 TB/s.
+// bytes in 54 us, 5.0 TB/s.  It writes the new lengths too: they
+// may lie where the old ones do, which all workgroups of evict_select read.
 #include "attn_device.hpp"
 
 namespace dcpa {
@@ -39,7 +40,6 @@ __global__ __launch_bounds__(kThreads) void evict_select(EvictArgs p) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int hk = (int)(blockIdx.x % (uint32_t)p.Hkv), b = (int)(blockIdx.x / (uint32_t)p.Hkv);
     const int L = min(max(p.kv[b], 0), p.max_keys), n = min(L, p.budget);
-    if (hk == 0 && tid == 0) p.new_len[b] = n;
     int32_t* kept = p.kept + (int64_t)b * p.kp_B + (int64_t)hk * p.kp_H;
     for (int i = n + tid; i < p.budget; i += kThreads) kept[i] = -1;
     if (L <= p.budget) {
@@ -252,6 +252,14 @@ __global__ __launch_bounds__(256) void evict_gather(EvictArgs p) {
 #pragma unroll
         for (int r = 0; r < ROWS; ++r)
             if (go[r]) *(float*)md[r] = have[r] ? *(const float*)ms[r] : -INFINITY;
+        // the lane of a sequence's first row writes its length (nobody else reads the old one here)
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const int64_t row = first + (int64_t)r * GROUPS;
+            const uint32_t at = (uint32_t)min(row, rows - 1), b = fdiv(fdiv(at, p.fHkv), p.fbudget);
+            if (row < rows && at == b * p.fbudget.d * p.fHkv.d)
+                p.new_len[b] = min(min(max(p.kv[b], 0), p.max_keys), p.budget);
+        }
     }
 }
 

@@ -207,7 +207,7 @@ class StackedAttention:
         new = -(-budget // self.page_size)
         for r in range(self.N):
             dst = [[self.free[r].pop() for _ in range(new)] for _ in self.lens]
-            attn.dcp_cache_evict(self.mass[r], self.k_cache[r], self.v_cache[r], self.table[r], self.kv_len[r].clone(),
+            attn.dcp_cache_evict(self.mass[r], self.k_cache[r], self.v_cache[r], self.table[r], self.kv_len[r],
                                  torch.tensor(dst, dtype=torch.int32, device=self.device), budget, n_sink=n_sink,
                                  n_recent=n_recent, new_len=self.kv_len[r])
             for b, pages in enumerate(dst):
