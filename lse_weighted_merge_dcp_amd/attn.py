@@ -370,15 +370,16 @@ def cache_slots(positions: torch.Tensor, sequence: torch.Tensor, block_table: to
     """The slots [T] (int64) that qk_norm_rope_append takes: token t of sequence
     sequence[t] at position positions[t] goes to place j % page_size of page
     block_table[sequence, j // page_size], j its index among this rank's
-    positions; -1 where another rank owns it or the table has no page.  Index
+    positions; -1 where another rank owns it or the table has no page, and for
+    padding (a negative position, or a sequence that the table has not).  Index
     arithmetic on small tensors (any device), for caches that have not been cut."""
     p, s = positions.long(), sequence.long()
     block = p // interleave
     j = block // n_ranks * interleave + p % interleave
     at = j // page_size
-    width = block_table.shape[1]
-    if width == 0:
+    rows, width = block_table.shape
+    if rows == 0 or width == 0:
         return torch.full_like(p, -1)
-    page = block_table[s, at.clamp(0, width - 1)].long()
-    mine = (block % n_ranks == rank) & (at < width) & (page >= 0)
+    page = block_table[s.clamp(0, rows - 1), at.clamp(0, width - 1)].long()
+    mine = (p >= 0) & (s >= 0) & (s < rows) & (block % n_ranks == rank) & (at < width) & (page >= 0)
     return torch.where(mine, page * page_size + j % page_size, -1)
