@@ -264,12 +264,13 @@ __global__ __launch_bounds__(256, DK > 256 ? 1 : 2) void mass_rows(MassArgs p) {
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
-            g_old = g == -INFINITY ? INFINITY : g * p.lmul;
+            const bool none = g == -INFINITY;     // the row saw nothing anywhere, whatever stands in it
+            g_old = none ? INFINITY : g * p.lmul;
             // rows are in the order of their tokens: where the first sees all of the wave's keys, so do the
-            // others, but for those behind the last, which see nothing
-            if (t * 32 + 31 >= nrows || visible(p.m, u.s, (int)fdiv((uint32_t)(t * 32), p.m.fG)) < key0 + KW) {
+            // others, but for those behind the last and those without a sum, which see nothing
+            if (t * 32 + 31 >= nrows || __ballot(none) != 0 || visible(p.m, u.s, (int)fdiv((uint32_t)(t * 32), p.m.fG)) < key0 + KW) {
                 const int row = t * 32 + r;
-                const int lim = row < nrows ? visible(p.m, u.s, (int)fdiv((uint32_t)row, p.m.fG)) - key0 - 4 * h : 0;
+                const int lim = row < nrows && !none ? visible(p.m, u.s, (int)fdiv((uint32_t)row, p.m.fG)) - key0 - 4 * h : 0;
                 // (a row whose sum is NaN gives NaN to what it sees and nothing to the rest)
                 const bool bad = g_old != g_old;
                 if (bad) g_old = 0.0f;
@@ -379,7 +380,7 @@ __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void mass_few(MassArgs p) {
         const int row = min(rt * 32 + r, nrows - 1), token = (int)fdiv((uint32_t)row, p.m.fG), head = hk * p.m.G + row - token * p.m.G;
         vis = rt * 32 + r < nrows ? visible(p.m, u.s, token) - base_key : 0;
         const float x = p.lse[(int64_t)(u.s.first + token) * p.l_T + (int64_t)head * p.l_H];
-        g = x == -INFINITY ? INFINITY : x * p.lmul;      // (a row that saw nothing anywhere gives nothing)
+        g = x == -INFINITY ? INFINITY : x * p.lmul;
         const char* from = p.q + (int64_t)(u.s.first + token) * p.q_T + (int64_t)head * p.q_H;
 #pragma unroll
         for (int s = 0; s < ST; ++s) {
@@ -423,7 +424,8 @@ __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void mass_few(MassArgs p) {
                     a = lds_read16(buf + (uint32_t)(r * KROW + ((2 * st + h) ^ turn(r)) * 16));
                 s = Mat<E>::mma(a, q[st], s);
             }
-            const int lim = vis - t * KT - 4 * h;
+            // (a row that saw nothing anywhere gives nothing, whatever stands in it)
+            const int lim = (g == INFINITY ? 0 : vis) - t * KT - 4 * h;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const float x = exp2_fast(__builtin_fmaf(s[i], p.c, -g));
