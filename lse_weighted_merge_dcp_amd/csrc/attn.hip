@@ -43,7 +43,7 @@ __global__ __launch_bounds__(256, DK > 192 ? 1 : 2) void attn_rows(AttnArgs p) {
     __shared__ uint64_t there_at[4];
 
     const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv), unit = (int)(blockIdx.x / (uint32_t)p.m.Hkv);
-    const Unit u = find_unit<KT>(p.m, R, p.slots, unit);
+    const Unit u = find_unit<KT>(p.m, R, p.slots, p.share, unit);
     if (!u.ok) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = (int)dcp::wave_id(), r = lane & 31, h = lane >> 5;
     const int nrows = u.s.n * p.m.G, row0 = u.tile * R, wave_row = wave * 32;
@@ -283,7 +283,7 @@ __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void attn_keys(AttnArgs p) {
     int hk, unit;
     heads_together(p.m, hk, unit);
     if (unit >= p.units) return;
-    const Unit u = find_unit<128>(p.m, 32, p.slots, unit);
+    const Unit u = find_unit<128>(p.m, 32, p.slots, p.share, unit);
     if (!u.ok) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = (int)dcp::wave_id(), r = lane & 31, h = lane >> 5;
     const int nrows = u.s.n * p.m.G, row0 = u.tile * 32;
@@ -487,7 +487,7 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs p) {
     constexpr int FLY = NC == 1 ? 8 : 4;       // parts under way at once
     __shared__ f32x4 share[TOGETHER ? 4 : 1][NC][64];
     const int lane = threadIdx.x & 63, wave = (int)dcp::wave_id();
-    const int chunk = key_chunk<STEP>(p.m, p.rows, p.slots);
+    const int chunk = key_chunk<STEP>(p.m, p.rows, p.slots, p.share);
     // lengths and units of sequences b0 .. b0 + 63, a lane to each
     struct Line {
         Seq s;
@@ -617,10 +617,12 @@ AttnPlan plan_attn(const Batch& m, int Dk, int Dv, bool pieces) {
     pl.tiles = (int32_t)(most < each ? most : each);
     // Workgroups that run at once: one latent workgroup to a CU, two of the others.  Fewer row
     // tiles than that: the keys are split so that the units fill the chip once; decode of ragged
-    // batches fills it several times over, so that long and short sequences even out.
+    // batches fills it several times over (see fill_slots()).
     const int64_t busy = (int64_t)pl.tiles * m.Hkv;
     const int64_t chip = pl.latent ? 256 : pl.by_keys ? 1024 : 512;
-    pl.slots = busy >= (pl.by_keys ? 4 * chip : chip) ? 0 : (int32_t)((chip + m.Hkv - 1) / m.Hkv);
+    pl.slots = pl.share = (int32_t)((chip + m.Hkv - 1) / m.Hkv);
+    if (pl.by_keys) fill_slots(pl.tiles, pl.slots, pl.share);
+    if (busy >= (pl.by_keys ? 4 * chip : chip)) pl.slots = 0;
     pl.units = pl.slots > pl.tiles ? pl.slots : pl.tiles;
     pl.ws_bytes = pl.slots == 0 ? 0 : (int64_t)pl.units * m.Hkv * pl.rows * (Dv + 1) * 4;
     return pl;

@@ -201,6 +201,7 @@ int dcpa_paged_attn(const dcpa_attn_args* a, void* stream) {
     k.Dv = (int32_t)a->Dv;
     k.rows = pl.rows;
     k.slots = pl.slots;
+    k.share = pl.share;
     k.units = pl.units;
     k.ws_o = (float*)a->workspace;
     k.ws_l = k.ws_o == nullptr ? nullptr : k.ws_o + (int64_t)pl.units * k.m.Hkv * pl.rows * a->Dv;
@@ -245,6 +246,7 @@ int dcpa_attn_mass(const dcpa_attn_args* a, float* mass, int64_t m_P, int64_t m_
     k.ws = pl.ws_bytes > 0 ? (float*)a->workspace : nullptr;
     k.Dk = (int32_t)a->Dk;
     k.slots = pl.slots;
+    k.share = pl.share;
     k.units = pl.units;
     k.c = (float)(a->scale * a->k_scale * 1.4426950408889634);
     k.lmul = a->lse_base == DCP_LSE_BASE_E ? kLog2e : 1.0f;

@@ -277,9 +277,10 @@ __device__ __forceinline__ void tiles_of(const Batch& m, int b, int rows, int& t
 
 // The length of a key range: the shortest multiple of STEP (to within an
 // eighth of the interval) with which the whole batch needs at most `slots`
-// units; kWhole where the tiles alone need that many.
+// units and none more than a `share`-th of its work; kWhole where the tiles
+// alone need that many.
 template <int STEP>
-__device__ __forceinline__ int key_chunk(const Batch& m, int rows, int slots) {
+__device__ __forceinline__ int key_chunk(const Batch& m, int rows, int slots, int share) {
     if (slots <= 0) return kWhole;
     const int lane = threadIdx.x & 63;
     int64_t work = 0;
@@ -294,7 +295,7 @@ __device__ __forceinline__ int key_chunk(const Batch& m, int rows, int slots) {
     if (all >= slots) return kWhole;
     // units <= work / chunk + tiles: `hi` is always enough, `lo` never too long
     auto steps = [](int64_t x) { return (int)min((int64_t)(kWhole / STEP), max((int64_t)2, (x + STEP - 1) / STEP)); };
-    int lo = steps((work + slots - 1) / slots), hi = max(lo, steps((work + slots - all - 1) / (slots - all)));
+    int lo = steps((work + share - 1) / share), hi = max(lo, steps((work + slots - all - 1) / (slots - all)));
 #pragma unroll 1
     for (int round = 0; round < 3 && lo < hi; ++round) {
         const int mid = lo + (hi - lo) / 2;
@@ -311,10 +312,10 @@ __device__ __forceinline__ int key_chunk(const Batch& m, int rows, int slots) {
 }
 
 template <int STEP>
-__device__ __forceinline__ Unit find_unit(const Batch& m, int rows, int slots, int id) {
+__device__ __forceinline__ Unit find_unit(const Batch& m, int rows, int slots, int share, int id) {
     Unit u;
     u.ok = false;
-    u.chunk = key_chunk<STEP>(m, rows, slots);
+    u.chunk = key_chunk<STEP>(m, rows, slots, share);
     const int lane = threadIdx.x & 63;
     int base = 0;
     for (int b0 = 0; b0 < m.B; b0 += 64) {

@@ -131,7 +131,7 @@ __device__ __forceinline__ void latent_rows(const AttnArgs& p) {
     __shared__ u32x4 query_s[QL][256];
 
     const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv), unit = (int)(blockIdx.x / (uint32_t)p.m.Hkv);
-    const Unit u = find_unit<KT>(p.m, R, p.slots, unit);
+    const Unit u = find_unit<KT>(p.m, R, p.slots, p.share, unit);
     if (!u.ok) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = (int)dcp::wave_id(), r = lane & 31, h = lane >> 5;
     const int nrows = u.s.n * p.m.G, row0 = u.tile * R, wave_row = wave * 32;

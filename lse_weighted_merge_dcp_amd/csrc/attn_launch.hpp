@@ -43,6 +43,7 @@ struct AttnArgs {
     int32_t Dk, Dv;
     int32_t rows;            // of a tile
     int32_t slots;           // units of one key head that the keys are split into (0: not split)
+    int32_t share;           // no key range longer than this share of the batch's keys needs
     int32_t units;           // (row tile, key range) pairs of one key head the launch covers
     float c;                 // scale * k_scale * log2(e): scores in powers of two
     float vs;                // v_scale
@@ -55,9 +56,20 @@ struct AttnPlan {
     int rows;                // rows of a tile
     bool latent;             // wide rows, the values are columns of the keys
     bool by_keys;            // the waves of a workgroup take different keys (few rows)
-    int32_t slots, tiles, units;
+    int32_t slots, share, tiles, units;
     int64_t ws_bytes;
 };
+// Few rows: the units that fill the chip, `slots`, leave no room to split a long sequence where the row
+// tiles alone are nearly as many.  From half as many tiles on half a chip's units are added to them, and a
+// sequence is split where it is longer than two units' equal shares, so that even batches stay whole.
+// (128 sequences of about 1000 keys, one of 131072, 8 key heads: 216 us, unsplit 1663; all of
+// about 1000: 120 us either way.)  Where they fill the chip four times over they stay whole: every
+// workgroup reads all lengths to split them, 500 sequences of 100 keys take 122 us and 512 unsplit 82.
+inline void fill_slots(int32_t tiles, int32_t& slots, int32_t& share) {
+    if (2 * (int64_t)tiles <= slots) return;
+    share = (slots + 1) / 2;
+    slots = tiles + share;
+}
 // pieces: the cache's rows and strides are whole pieces of 16 bytes.
 AttnPlan plan_attn(const Batch& m, int Dk, int Dv, bool pieces);
 // wide: the weights' remainders take a second product where rows are many or latent too.
@@ -77,14 +89,14 @@ struct MassArgs {
     int64_t m_P, m_S, m_H;
     float* ws;
     int32_t Dk;
-    int32_t slots;           // workgroups of one key head aimed at (0: one to a sequence)
+    int32_t slots, share;    // workgroups of one key head aimed at (0: one to a sequence); see AttnArgs
     int32_t units;           // workgroups of one key head launched
     float c;
     float lmul;              // log2(e), or 1 for base 2
 };
 struct MassPlan {
     bool few;                // few rows to a sequence
-    int32_t slots, units;
+    int32_t slots, share, units;
     int64_t ws_bytes;
 };
 MassPlan plan_mass(const Batch& m, int Dk, bool pieces);

@@ -37,7 +37,7 @@ struct Share {
 constexpr int kOneTile = 0x3fffffff;      // rows of a tile that holds any sequence
 
 template <int KEYS>
-__device__ __forceinline__ void share_out(const Batch& m, int slots, bool split_rows, int& chunk, int& parts) {
+__device__ __forceinline__ void share_out(const Batch& m, int slots, int share, bool split_rows, int& chunk, int& parts) {
     const int lane = threadIdx.x & 63;
     int64_t steps = 0;
     int most = 0;
@@ -51,7 +51,7 @@ __device__ __forceinline__ void share_out(const Batch& m, int slots, bool split_
     parts = 1;
     chunk = KEYS;
     if (steps >= slots) {
-        chunk = key_chunk<KEYS>(m, kOneTile, slots);
+        chunk = key_chunk<KEYS>(m, kOneTile, slots, share);
         return;
     }
     if (!split_rows) return;
@@ -63,11 +63,11 @@ __device__ __forceinline__ void share_out(const Batch& m, int slots, bool split_
     parts = (int)max((int64_t)1, min(slots / max((int64_t)1, steps), tiles));
 }
 
-template <int KEYS> __device__ __forceinline__ Share find_share(const Batch& m, int slots, bool split_rows, int id) {
+template <int KEYS> __device__ __forceinline__ Share find_share(const Batch& m, int slots, int share, bool split_rows, int id) {
     Share u;
     u.ok = false;
     int chunk;
-    share_out<KEYS>(m, slots, split_rows, chunk, u.parts);
+    share_out<KEYS>(m, slots, share, split_rows, chunk, u.parts);
     u.part = id % u.parts;
     id /= u.parts;
     u.slot = id;
@@ -116,7 +116,7 @@ __global__ __launch_bounds__(256, DK > 256 ? 1 : 2) void mass_rows(MassArgs p) {
     __shared__ __attribute__((aligned(1024))) char qtile[2][PAD];
     static_assert(QB <= PAD, "a tile of queries fits");
     const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv);
-    const Share u = find_share<KEYS>(p.m, p.slots, p.ws != nullptr, (int)(blockIdx.x / (uint32_t)p.m.Hkv));
+    const Share u = find_share<KEYS>(p.m, p.slots, p.share, p.ws != nullptr, (int)(blockIdx.x / (uint32_t)p.m.Hkv));
     if (!u.ok) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = (int)dcp::wave_id(), r = lane & 31, h = lane >> 5;
     const int nrows = u.s.n * p.m.G, tiles = (nrows + 31) / 32, per_part = (tiles + u.parts - 1) / u.parts;
@@ -332,7 +332,7 @@ __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void mass_few(MassArgs p) {
     int hk, unit;
     heads_together(p.m, hk, unit);
     if (unit >= p.units) return;
-    const Share u = find_share<128>(p.m, p.slots, false, unit);
+    const Share u = find_share<128>(p.m, p.slots, p.share, false, unit);
     if (!u.ok) return;
     const int lane = threadIdx.x & 63, wave = (int)dcp::wave_id(), r = lane & 31, h = lane >> 5;
     const int nrows = u.s.n * p.m.G, row_tiles = (nrows + 31) / 32;
@@ -472,10 +472,10 @@ __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void mass_few(MassArgs p) {
 // The parts of split rows, added in order: a thread to a key.
 template <int KEYS> __global__ __launch_bounds__(KEYS) void mass_join(MassArgs p) {
     int chunk, parts;
-    share_out<KEYS>(p.m, p.slots, p.ws != nullptr, chunk, parts);
+    share_out<KEYS>(p.m, p.slots, p.share, p.ws != nullptr, chunk, parts);
     if (parts == 1) return;
     const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv);
-    const Share u = find_share<KEYS>(p.m, p.slots, p.ws != nullptr, (int)(blockIdx.x / (uint32_t)p.m.Hkv) * parts);
+    const Share u = find_share<KEYS>(p.m, p.slots, p.share, p.ws != nullptr, (int)(blockIdx.x / (uint32_t)p.m.Hkv) * parts);
     const int key = u.k0 + (int)threadIdx.x;
     if (!u.ok || key >= u.k1) return;
     float* m = mass_at(p, u.b, hk, key);
@@ -500,16 +500,17 @@ MassPlan plan_mass(const Batch& m, int Dk, bool pieces) {
     // needs one at least
     const int64_t want = pl.few ? 1024 : 512;
     const int64_t seqs = m.T < m.B ? m.T : m.B;
-    pl.slots = (int32_t)((want + m.Hkv - 1) / m.Hkv);
+    pl.slots = pl.share = (int32_t)((want + m.Hkv - 1) / m.Hkv);
+    // rows are split only where sequences are few: parts > 1 only while steps * parts <= slots
+    pl.ws_bytes = pl.few || 2 * seqs > pl.slots ? 0 : (int64_t)pl.slots * m.Hkv * keys_of(pl.few, Dk) * 4;
+    fill_slots((int32_t)seqs, pl.slots, pl.share);
     // a sequence without keys or with one step takes a unit all the same
-    pl.units = (int32_t)(pl.slots > seqs ? pl.slots : 0);
-    if (pl.units == 0) {
+    pl.units = pl.slots;
+    if (seqs * m.Hkv >= 4 * want) {
         // more sequences than that: each is one unit, whole
         pl.slots = 0;
         pl.units = (int32_t)seqs;
     }
-    // parts > 1 only while steps * parts <= slots
-    pl.ws_bytes = pl.few ? 0 : (int64_t)pl.slots * m.Hkv * keys_of(pl.few, Dk) * 4;
     return pl;
 }
 
@@ -526,7 +527,7 @@ template <typename E, bool KV8> hipError_t run(const MassArgs& a, bool few, hipS
                          : a.Dk <= 128 ? launch(mass_rows<E, KV8, 128, 64>, grid, block, stream, a)
                          : a.Dk <= 256 ? launch(mass_rows<E, KV8, 256, 32>, grid, block, stream, a)
                                        : launch(mass_rows<E, KV8, 576, 32>, grid, block, stream, a);
-    if (e != hipSuccess || a.slots == 0) return e;
+    if (e != hipSuccess || a.ws == nullptr) return e;
     return keys_of(false, a.Dk) == 128 ? launch(mass_join<128>, grid, dim3(128), stream, a)
                                        : launch(mass_join<256>, grid, dim3(256), stream, a);
 }
