@@ -94,7 +94,9 @@ const char* dcpa_status_str(int status);
  * cache row slots[t] = page * page_size + place; v [T, Hkv, Dv] (nullable) goes
  * to the value cache unchanged but for its type.  A slot outside [0, num_pages
  * * page_size) is skipped: another rank owns that token.  Slots of one call
- * must differ.  An 8-bit cache stores x * (1 / scale) in fp32, rounded to
+ * must differ.  mass (nullable, strides m_P, m_S, m_H in words, laid out as
+ * dcpa_attn_mass takes it): the weight of every key that is written starts at 0.
+ * An 8-bit cache stores x * (1 / scale) in fp32, rounded to
  * nearest even and saturated at 448.  A position outside [0, positions_max)
  * turns by the nearest row of the table.
  *
@@ -114,6 +116,7 @@ typedef struct {
     void* q_out;          int64_t qo_T, qo_H;
     void* k_cache;        int64_t kc_P, kc_S, kc_H;
     void* v_cache;        int64_t vc_P, vc_S, vc_H;
+    float* mass;          int64_t m_P, m_S, m_H;
     int64_t T, Hq, Hkv, D, Dv, q_norm, k_norm, rope_off, rot, interleaved;
     int64_t positions_max, num_pages, page_size, dtype, cache_dtype;
     double eps, k_scale, v_scale;
@@ -179,7 +182,8 @@ int64_t dcpa_paged_attn_workspace(const dcpa_attn_args* a);
  * row over all ranks sum to 1).  A row whose lse is -inf adds nothing.  The
  * call takes the fields of dcpa_attn_args it needs: v, Dv, v_scale (positive
  * all the same), out and wide_weights are ignored, lse is read.  mass holds fp32 with strides
- * m_P, m_S, m_H.  A page must not stand twice in the table rows of one call
+ * m_P, m_S, m_H; a place's weight has to be 0 when a key is first written there,
+ * which dcpa_qk_norm_rope_append sees to if it is given mass.  A page must not stand twice in the table rows of one call
  * (two sequences that share a page: two calls).  `workspace` holds the parts of
  * rows that are split over workgroups, dcpa_attn_mass_workspace gives its size.
  */
@@ -197,6 +201,8 @@ int64_t dcpa_attn_mass_workspace(const dcpa_attn_args* a);
  * i] is the old index of the i-th, -1 from n on; new_len[b] = n (new_len may be
  * kv_len itself, else the two arrays must lie apart: DCPA_ERR_VALUE).
  *
+ * The other places of the destination pages keep what they hold, old weights too
+ * (see mass in dcpa_qk_norm_rope_append).
  * Source pages are only read: destination pages must not be source pages of
  * any sequence of the call, nor appear twice.  A destination entry outside
  * [0, num_pages) drops its rows; a missing source page's keys count as mass

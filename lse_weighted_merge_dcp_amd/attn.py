@@ -48,7 +48,7 @@ SIGNATURES = {
     "dcpa_cache_evict": ([_CP, _VP], ctypes.c_int),
 }
 # The argument structs: every field 8 bytes, in the header's order.
-ROPE_ARGS = struct.Struct("=41q3d")
+ROPE_ARGS = struct.Struct("=45q3d")
 ATTN_ARGS = struct.Struct("=41q3d")
 EVICT_ARGS = struct.Struct("=33q")
 
@@ -126,7 +126,8 @@ def qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tens
                         k_weight: Optional[torch.Tensor], positions: torch.Tensor, cos_sin: torch.Tensor,
                         slots: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional[torch.Tensor], *,
                         rope_offset: int = 0, interleaved: bool = False, eps: float = 1e-6, k_scale: float = 1.0,
-                        v_scale: float = 1.0, q_out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                        v_scale: float = 1.0, mass: Optional[torch.Tensor] = None,
+                        q_out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Norm and rotate new queries q [T,Hq,D] and keys k [T,Hkv,D], and write
     the keys and the values v [T,Hkv,Dv] (or None: the latent layout) into the
     cache rows slots [T] (int64: page * page_size + place; a slot outside the
@@ -135,8 +136,10 @@ def qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tens
     then the sines of each position, applied to the rot columns from
     rope_offset on, to columns (j, j + rot/2), or (2j, 2j+1) if interleaved.
     positions [T] is int32.  An 8-bit cache stores value / scale, rounded to
-    nearest even.  Returns q_out [T,Hq,D] (q itself may be given)."""
-    dev = _on_gpu(q, k, v, q_weight, k_weight, positions, cos_sin, slots, k_cache, v_cache, q_out)
+    nearest even.  mass [pages,page_size,Hkv] (fp32, of dcp_attn_mass): the weight
+    of every key that is written starts at 0, whatever an earlier key left there.
+    Returns q_out [T,Hq,D] (q itself may be given)."""
+    dev = _on_gpu(q, k, v, q_weight, k_weight, positions, cos_sin, slots, k_cache, v_cache, mass, q_out)
     for t, name, nd in ((q, "q", 3), (k, "k", 3), (k_cache, "k_cache", 4), (cos_sin, "cos_sin", 2)):
         _rows(t, name, nd)
     T, Hq, D = q.shape
@@ -160,6 +163,8 @@ def qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tens
             raise ValueError("%s must be a contiguous vector of the queries' dtype" % name)
     _ints(positions, "positions", (T,))
     _ints(slots, "slots", (T,), torch.int64)
+    if mass is not None and (mass.shape != k_cache.shape[:3] or mass.dtype != torch.float32):
+        raise ValueError("mass must be float32 [pages,page_size,Hkv]")
     if cos_sin.dtype != torch.float32:
         raise ValueError("cos_sin is float32 [positions, rot]")
     if q_out is None:
@@ -168,6 +173,7 @@ def qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tens
     if q_out.shape != (T, Hq, D) or q_out.dtype != q.dtype:
         raise ValueError("bad q_out tensor")
     qs, ks, os_, kcs = q.stride(), k.stride(), q_out.stride(), k_cache.stride()
+    ms = mass.stride() if mass is not None else (0, 0, 0)
     args = ROPE_ARGS.pack(
         q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
         v.data_ptr() if v is not None else 0, vs[0], vs[1],
@@ -175,6 +181,7 @@ def qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tens
         positions.data_ptr(), cos_sin.data_ptr(), cos_sin.stride(0), slots.data_ptr(),
         q_out.data_ptr(), os_[0], os_[1], k_cache.data_ptr(), kcs[0], kcs[1], kcs[2],
         v_cache.data_ptr() if v is not None else 0, vcs[0], vcs[1], vcs[2],
+        mass.data_ptr() if mass is not None else 0, ms[0], ms[1], ms[2],
         T, Hq, Hkv, D, Dv, q_weight.shape[0] if q_weight is not None else 0,
         k_weight.shape[0] if k_weight is not None else 0, rope_offset, cos_sin.shape[1], 1 if interleaved else 0,
         cos_sin.shape[0], pages, page_size, dt, ct, eps, k_scale, v_scale)
@@ -296,7 +303,8 @@ def dcp_attn_mass(q: torch.Tensor, k_cache: torch.Tensor, lse: torch.Tensor, mas
     new tokens q give each cached key of this rank: the sum over the tokens and
     the heads of the key's group of exp(s - lse), lse [T,Hq] fp32 the merged
     log-sum-exp of all ranks (ops.dcp_lse_combine; a rank that merged only its
-    own heads gathers the others' first).  The other arguments are those of
+    own heads gathers the others' first).  A new key's weight has to start at 0
+    (qk_norm_rope_append's mass).  The other arguments are those of
     dcp_paged_attn.  A page may stand only once in the block_table of a call.
     Returns mass."""
     dev = _on_gpu(q, k_cache, lse, mass, block_table, cu_q, kv_len, seq_len, workspace)
@@ -323,10 +331,11 @@ def dcp_cache_evict(mass: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional
     n_sink, the last n_recent and of the others those of highest mass
     [pages,page_size,Hkv] (ties to the oldest).  The kept keys, their values
     and their mass are copied, in their old order, into the pages
-    dst_table[b] (int32 [B, pages]) of the same pools; source pages are only
-    read, and must not be among the destinations.  Returns (new_len [B] int32,
-    which may be kv_len itself, kept [B,Hkv,budget] int32: the old index of each
-    kept key, -1 behind the last)."""
+    dst_table[b] (int32 [B, pages]) of the same pools, whose other places stay as
+    they are (give mass to qk_norm_rope_append); source pages are only read, and
+    must not be among the destinations.  Returns (new_len [B] int32, which may be
+    kv_len itself, kept [B,Hkv,budget] int32: the old index of each kept key, -1
+    behind the last)."""
     dev = _on_gpu(mass, k_cache, v_cache, block_table, kv_len, dst_table, new_len, kept)
     _rows(k_cache, "k_cache", 4)
     pages, page_size, Hkv, Dk = k_cache.shape

@@ -275,7 +275,7 @@ int dcpa_qk_norm_rope_append(const dcpa_rope_args* a, void* stream) {
         !positive(1.0 / a->k_scale) || !positive(1.0 / a->v_scale))
         return DCPA_ERR_VALUE;
     if (!strides_ok({a->q_T, a->q_H, a->k_T, a->k_H, a->v_T, a->v_H, a->cs_P, a->qo_T, a->qo_H, a->kc_P, a->kc_S,
-                     a->kc_H, a->vc_P, a->vc_S, a->vc_H}))
+                     a->kc_H, a->vc_P, a->vc_S, a->vc_H, a->m_P, a->m_S, a->m_H}))
         return DCP_ERR_STRIDE;
     const int ec = esize_of(a->cache_dtype);
     if (!span_ok({{a->T, a->q_T}, {a->Hq, a->q_H}, {a->D, 1}}, 2) ||
@@ -284,7 +284,8 @@ int dcpa_qk_norm_rope_append(const dcpa_rope_args* a, void* stream) {
         !span_ok({{a->T, a->v_T}, {a->Hkv, a->v_H}, {a->Dv, 1}}, 2) ||
         !span_ok({{a->num_pages, a->kc_P}, {a->page_size, a->kc_S}, {a->Hkv, a->kc_H}, {a->D, 1}}, ec) ||
         !span_ok({{a->num_pages, a->vc_P}, {a->page_size, a->vc_S}, {a->Hkv, a->vc_H}, {a->Dv, 1}}, ec) ||
-        !span_ok({{a->positions_max, a->cs_P}, {a->rot, 1}}, 4))
+        !span_ok({{a->positions_max, a->cs_P}, {a->rot, 1}}, 4) ||
+        !span_ok({{a->num_pages, a->m_P}, {a->page_size, a->m_S}, {a->Hkv, a->m_H}}, 4))
         return DCP_ERR_STRIDE;
     if (a->T == 0) return DCP_OK;
     if (!a->q || !a->k || !a->q_out || !a->slots || (a->rot > 0 && (!a->positions || !a->cos_sin)) ||
@@ -295,7 +296,7 @@ int dcpa_qk_norm_rope_append(const dcpa_rope_args* a, void* stream) {
         !aligned(a->q_weight, 16) || !aligned(a->k_weight, 16) || (a->rot > 0 && (!aligned(a->cos_sin, 16) || a->cs_P % 4 != 0)) ||
         !multiples({a->q_T, a->q_H, a->k_T, a->k_H, a->qo_T, a->qo_H, a->kc_P, a->kc_S, a->kc_H}, 8) ||
         (has_v && !multiples({a->v_T, a->v_H, a->vc_P, a->vc_S, a->vc_H}, 8)) || !aligned(a->k_cache, 8 * ec) ||
-        !aligned(a->v_cache, 8 * ec) || !aligned(a->positions, 4) || !aligned(a->slots, 8))
+        !aligned(a->v_cache, 8 * ec) || !aligned(a->mass, 4) || !aligned(a->positions, 4) || !aligned(a->slots, 8))
         return DCP_ERR_ALIGN;
     RopeArgs k;
     k.q = (const char*)a->q; k.k = (const char*)a->k; k.v = (const char*)a->v;
@@ -310,6 +311,8 @@ int dcpa_qk_norm_rope_append(const dcpa_rope_args* a, void* stream) {
     k.qo_T = a->qo_T * 2; k.qo_H = a->qo_H * 2;
     k.kc_P = a->kc_P * ec; k.kc_S = a->kc_S * ec; k.kc_H = a->kc_H * ec;
     k.vc_P = a->vc_P * ec; k.vc_S = a->vc_S * ec; k.vc_H = a->vc_H * ec;
+    k.mass = a->mass;
+    k.m_P = a->m_P; k.m_S = a->m_S; k.m_H = a->m_H;
     k.T = (int32_t)a->T; k.Hq = (int32_t)a->Hq; k.Hkv = (int32_t)a->Hkv; k.D = (int32_t)a->D; k.Dv = (int32_t)a->Dv;
     k.nq = (int32_t)a->q_norm; k.nk = (int32_t)a->k_norm; k.off = (int32_t)a->rope_off; k.rot = (int32_t)a->rot;
     k.pairs = a->interleaved != 0;

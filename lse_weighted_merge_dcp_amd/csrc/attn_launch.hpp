@@ -112,6 +112,8 @@ struct RopeArgs {
     const int64_t* slots;
     char *qo, *kc, *vc;
     int64_t qo_T, qo_H, kc_P, kc_S, kc_H, vc_P, vc_S, vc_H;
+    float* mass;             // nullable; strides in words
+    int64_t m_P, m_S, m_H;
     int32_t T, Hq, Hkv, D, Dv, nq, nk, off, rot, pairs;
     int32_t positions, page_size;
     int64_t slots_max;

@@ -61,6 +61,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
         to = value ? p.vc + page * p.vc_P + place * p.vc_S + (int64_t)hk * p.vc_H
                    : p.kc + page * p.kc_P + place * p.kc_S + (int64_t)hk * p.kc_H;
         if (value) D = p.Dv;
+        else if (p.mass != nullptr && lane == 0) p.mass[page * p.m_P + place * p.m_S + hk * p.m_H] = 0.0f;
         narrow = KV8;
         scale = value ? p.iv : p.ik;
     }

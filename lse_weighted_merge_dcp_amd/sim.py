@@ -187,7 +187,7 @@ class StackedAttention:
         qr = None
         for r in range(N):
             qr = attn.qk_norm_rope_append(q, k, v, q_weight, k_weight, pos, cos_sin, slots[r], self.k_cache[r],
-                                          self.v_cache[r], eps=eps, q_out=qr)
+                                          self.v_cache[r], eps=eps, mass=self.mass[r], q_out=qr)
             attn.dcp_paged_attn(qr, self.k_cache[r], self.v_cache[r], self.table[r], cu, self.kv_len[r],
                                 seq_len=seq_len, rank=r, n_ranks=N, interleave=self.interleave, out=out[r],
                                 out_lse=lse[r])
@@ -216,18 +216,3 @@ class StackedAttention:
                 self.held[r][b] = min(self.held[r][b], budget)
                 self.table[r, b] = -1
                 self.table[r, b, :new] = torch.tensor(pages, dtype=torch.int32)
-                # places behind the kept keys start without weight
-        self._clear_unused()
-
-    def _clear_unused(self) -> None:
-        """Weights of free places are zero, as a new key's are."""
-        for r in range(self.N):
-            for b, pages in enumerate(self.pages[r]):
-                full, rest = divmod(self.held[r][b], self.page_size)
-                for i, page in enumerate(pages):
-                    if i > full or (i == full and rest == 0):
-                        self.mass[r, page] = 0
-                    elif i == full:
-                        self.mass[r, page, rest:] = 0
-            if self.free[r]:
-                self.mass[r, self.free[r]] = 0

@@ -1,9 +1,27 @@
 """Further refusals of libdcpattn's host side (no GPU): see tests/test_attn_host.py."""
 import pytest
+import torch
 
-from test_attn_host import A, VALUE, evict_call
+from lse_weighted_merge_dcp_amd import attn
+from test_attn_host import A, ALIGN, OK, STRIDE, VALUE, evict_call, rope_call
 
 
 @pytest.mark.parametrize("shift", [-20, -4, 4, 20])
 def test_evict_refuses_lengths_that_overlap_in_part(shift):
     assert evict_call(B=6, kv_len=A, new_len=A + shift) == VALUE
+
+
+@pytest.mark.parametrize("over,want", [(dict(m_P=-1), STRIDE), (dict(m_S=1 << 57), STRIDE), (dict(T=1, mass=A + 2), ALIGN),
+                                       (dict(mass=A, m_P=64, m_S=4, m_H=1), OK)])
+def test_append_checks_the_weights(over, want):
+    assert rope_call(**over) == want
+
+
+def test_binding_checks_the_weights_of_an_append(monkeypatch):
+    monkeypatch.setattr(attn, "_on_gpu", lambda *ts: 0)
+    z = torch.zeros
+    q, k, kc = z(3, 8, 64, dtype=torch.bfloat16), z(3, 2, 64, dtype=torch.bfloat16), z(4, 16, 2, 64, dtype=torch.bfloat16)
+    for mass in (z(4, 16, 3), z(4, 16), z(4, 16, 2, dtype=torch.float64)):
+        with pytest.raises(ValueError, match="mass"):
+            attn.qk_norm_rope_append(q, k, None, None, None, z(3, dtype=torch.int32), z(1, 0), z(3, dtype=torch.int64), kc, None,
+                                     mass=mass)
