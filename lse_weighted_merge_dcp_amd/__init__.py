@@ -12,9 +12,9 @@ include/dcpattn.h): norm, rotation and cache append of new tokens, attention
 over the rank's paged cache, accumulated attention weights, and eviction.
 """
 from ._lib import DcpError, DcpLaunchError
-from .attn import AttnError, cache_slots, dcp_attn_mass, dcp_cache_evict, dcp_paged_attn, qk_norm_rope_append
+from .attn import AttnError, cache_slots, dcp_attn_mass, dcp_cache_evict, dcp_paged_attn, owned_positions, qk_norm_rope_append
 from .ops import cp_lse_combine_inplace, dcp_lse_combine, dcp_pack_a2a_send, interleaved_views, lse_pack_dim
 
 __all__ = ["AttnError", "DcpError", "DcpLaunchError", "cache_slots", "cp_lse_combine_inplace", "dcp_attn_mass",
            "dcp_cache_evict", "dcp_lse_combine", "dcp_pack_a2a_send", "dcp_paged_attn", "interleaved_views",
-           "lse_pack_dim", "qk_norm_rope_append"]
+           "lse_pack_dim", "owned_positions", "qk_norm_rope_append"]

@@ -15,6 +15,7 @@ PyTorch fallback.
                         from the LSE that ops.dcp_lse_combine returns
   dcp_cache_evict       keep the keys of highest accumulated weight
   cache_slots           where this rank caches new tokens
+  owned_positions       how many positions of a sequence lie on this rank
 
 Under DCP the token at position p lies on rank (p // interleave) % n_ranks: the
 round-robin length formula of sglang PR #33926 report, 实现拆解 item 2, in
@@ -374,21 +375,39 @@ def dcp_cache_evict(mass: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional
     return new_len, kept
 
 
+def owned_positions(length, rank: int = 0, n_ranks: int = 1, interleave: int = 1):
+    """How many of the positions 0 .. length-1 lie on this rank (length: an int
+    or an integer tensor): the cached length of a sequence that has not been cut,
+    and by its growth what a step adds to any."""
+    block = n_ranks * interleave
+    rest = length % block - rank * interleave
+    rest = rest.clamp(0, interleave) if isinstance(rest, torch.Tensor) else min(max(rest, 0), interleave)
+    return length // block * interleave + rest
+
+
 def cache_slots(positions: torch.Tensor, sequence: torch.Tensor, block_table: torch.Tensor, page_size: int,
-                rank: int = 0, n_ranks: int = 1, interleave: int = 1) -> torch.Tensor:
+                rank: int = 0, n_ranks: int = 1, interleave: int = 1, *, kv_len: Optional[torch.Tensor] = None,
+                seq_len: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The slots [T] (int64) that qk_norm_rope_append takes: token t of sequence
     sequence[t] at position positions[t] goes to place j % page_size of page
     block_table[sequence, j // page_size], j its index among this rank's
     positions; -1 where another rank owns it or the table has no page, and for
-    padding (a negative position, or a sequence that the table has not).  Index
-    arithmetic on small tensors (any device), for caches that have not been cut."""
+    padding (a negative position, or a sequence that the table has not).  Where
+    caches have been cut (dcp_cache_evict), kv_len and seq_len [B] give the rank's
+    cached length and the whole length of every sequence at one moment since then,
+    before this step or after it alike: places count on from what is cached.
+    Index arithmetic on small tensors (any device)."""
+    if (kv_len is None) != (seq_len is None):
+        raise ValueError("kv_len and seq_len go together")
     p, s = positions.long(), sequence.long()
-    block = p // interleave
-    j = block // n_ranks * interleave + p % interleave
-    at = j // page_size
     rows, width = block_table.shape
     if rows == 0 or width == 0:
         return torch.full_like(p, -1)
-    page = block_table[s.clamp(0, rows - 1), at.clamp(0, width - 1)].long()
-    mine = (p >= 0) & (s >= 0) & (s < rows) & (block % n_ranks == rank) & (at < width) & (page >= 0)
+    at_row = s.clamp(0, rows - 1)
+    j = owned_positions(p, rank, n_ranks, interleave)
+    if kv_len is not None:
+        j = j + (kv_len.long() - owned_positions(seq_len.long(), rank, n_ranks, interleave))[at_row]
+    at = j // page_size
+    page = block_table[at_row, at.clamp(0, width - 1)].long()
+    mine = (p >= 0) & (s >= 0) & (s < rows) & (p // interleave % n_ranks == rank) & (j >= 0) & (at < width) & (page >= 0)
     return torch.where(mine, page * page_size + j % page_size, -1)

@@ -26,3 +26,48 @@ def test_sequences_outside_the_table_get_no_slot():
     assert attn.cache_slots(pos, seq, table, 16).tolist() == [-1, -1, -1, 7 * 16 + 1]
     assert attn.cache_slots(pos, seq, table[:0], 16).tolist() == [-1] * 4
     assert attn.cache_slots(pos, seq, table[:, :0], 16).tolist() == [-1] * 4
+
+
+@pytest.mark.parametrize("N,inter", [(1, 1), (2, 1), (3, 4), (8, 16)])
+def test_owned_positions(N, inter):
+    for r in range(N):
+        count = [sum(p // inter % N == r for p in range(n)) for n in range(200)]
+        assert [attn.owned_positions(n, r, N, inter) for n in range(200)] == count
+        assert attn.owned_positions(torch.arange(200), r, N, inter).tolist() == count
+
+
+@pytest.mark.parametrize("N,inter", [(1, 1), (2, 1), (3, 4)])
+def test_slots_count_on_in_a_cut_cache(N, inter):
+    """Steps and cuts in turn: a token takes the place behind what its rank holds, by the lengths before the step and
+    by those after it; a position from before the cut has no place."""
+    page, B = 4, 2
+    table = torch.arange(2 * 9 * N, dtype=torch.int32).view(N, B, 9).flip(2)
+    lens, held = [0] * B, [[0] * B for _ in range(N)]
+    for new, budget in (([30, 5], 6), ([1, 1], 8), ([9, 22], 3), ([0, 1], 4)):
+        pos = torch.tensor([m + i for m, n in zip(lens, new) for i in range(n)])
+        seq = torch.tensor([b for b, n in enumerate(new) for _ in range(n)])
+        want = torch.full((N, len(pos)), -1)
+        before = [(torch.tensor(held[r]), torch.tensor(lens)) for r in range(N)]
+        for t, (p, b) in enumerate(zip(pos.tolist(), seq.tolist())):
+            r = p // inter % N
+            j = held[r][b]
+            held[r][b] += 1
+            want[r, t] = int(table[r, b, j // page]) * page + j % page if j // page < 9 else -1
+        lens = [m + n for m, n in zip(lens, new)]
+        for r in range(N):
+            for kv, whole in (before[r], (torch.tensor(held[r], dtype=torch.int32), torch.tensor(lens, dtype=torch.int32))):
+                got = attn.cache_slots(pos, seq, table[r], page, r, N, inter, kv_len=kv, seq_len=whole)
+                assert torch.equal(got, want[r])
+            grown = before[r][0] + attn.owned_positions(torch.tensor(lens), r, N, inter) - attn.owned_positions(before[r][1], r, N, inter)
+            assert grown.tolist() == held[r]
+            held[r] = [min(h, budget) for h in held[r]]
+            old = attn.cache_slots(torch.zeros(B, dtype=torch.long), torch.arange(B), table[r], page, r, N, inter,
+                                   kv_len=torch.zeros(B, dtype=torch.int32), seq_len=torch.tensor(lens))
+            assert old.tolist() == [-1] * B
+
+
+def test_cut_lengths_go_together():
+    t = torch.zeros(1, dtype=torch.long)
+    for kw in (dict(kv_len=t), dict(seq_len=t)):
+        with pytest.raises(ValueError):
+            attn.cache_slots(t, t, torch.zeros(1, 1, dtype=torch.int32), 4, **kw)

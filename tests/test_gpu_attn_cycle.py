@@ -1,9 +1,10 @@
-"""A cache's life across calls: lengths updated in place by the eviction."""
+"""A cache's life across calls: lengths updated in place by the eviction, weights
+of new keys, and appends, attention, weights and cuts in turn."""
 import pytest
 import torch
 
 import attn_oracle as oracle
-from lse_weighted_merge_dcp_amd import attn
+from lse_weighted_merge_dcp_amd import attn, ops
 from test_gpu_attn_cache import check_evict, evict_problem
 
 pytestmark = pytest.mark.gpu
@@ -52,3 +53,69 @@ def test_a_new_key_starts_without_weight(dev, D, pairs):
         assert torch.equal(torch.nan_to_num(mass.cpu(), 99.0).reshape(-1, Hkv), torch.nan_to_num(want, 99.0))
         assert bool((store[:, :, 0] == 7.0).all()) and bool((store[:, :, 1 + page:] == 7.0).all())
         mass.copy_(old)
+
+
+def test_append_attend_weigh_cut_and_on(dev):
+    """Three rounds of a cache through the public calls alone: slots, append, attention, merge, weights and cut, each
+    against what is cached (64 bits), with pages handed out again without being cleared."""
+    N, Hq, Hkv, D, page, budget, inter, B = 2, 4, 2, 64, 4, 8, 2, 2
+    g = torch.Generator().manual_seed(11)
+    width, pages = 12, 2 * 2 * 12 + 1
+    kc, vc = (torch.randn(N, pages, page, Hkv, D, generator=g).to(BF).to(dev) for _ in range(2))
+    mass = torch.full((N, pages, page, Hkv), 55.0, device=dev)     # old weights everywhere
+    half = torch.arange(B * width, dtype=torch.int32, device=dev).view(B, width)
+    tables = [half, half + B * width]                              # in turn, one cut's destination the next one's source
+    kv = torch.zeros(N, B, dtype=torch.int32, device=dev)
+    seq = torch.zeros(B, dtype=torch.int32, device=dev)
+    still = torch.zeros(1, 0, device=dev)
+    for turn, new in enumerate(([40, 23], [1, 3], [5, 30])):
+        T = sum(new)
+        q, k, v = (torch.randn(T, h, D, generator=g).to(BF).to(dev) for h in (Hq, Hkv, Hkv))
+        n = torch.tensor(new, dtype=torch.int32, device=dev)
+        cu = torch.tensor([0, new[0], T], dtype=torch.int32, device=dev)
+        of = torch.repeat_interleave(torch.arange(B, device=dev), n.long())
+        pos = (seq[of] + torch.arange(T, device=dev) - cu[of]).int()
+        table = tables[turn % 2]
+        parts, before = [], mass.clone()
+        grown = torch.zeros_like(kv)
+        for r in range(N):
+            slots = attn.cache_slots(pos, of, table, page, r, N, inter, kv_len=kv[r], seq_len=seq)
+            grown[r] = kv[r] + attn.owned_positions(seq + n, r, N, inter) - attn.owned_positions(seq, r, N, inter)
+            attn.qk_norm_rope_append(q, k, v, None, None, pos, still, slots, kc[r], vc[r], mass=mass[r])
+            before[r].view(-1, Hkv)[slots[slots >= 0]] = 0.0
+        kv, seq = grown, seq + n
+        for r in range(N):
+            parts.append(attn.dcp_paged_attn(q, kc[r], vc[r], table, cu, kv[r], seq_len=seq, rank=r, n_ranks=N, interleave=inter))
+        out, lse = ops.dcp_lse_combine(torch.stack([o for o, _ in parts]), torch.stack([x for _, x in parts]))
+        for r in range(N):
+            attn.dcp_attn_mass(q, kc[r], lse, mass[r], table, cu, kv[r], seq_len=seq, rank=r, n_ranks=N, interleave=inter)
+        u = 2.0 ** -8
+        for b in range(B):
+            for h in range(Hq):
+                kd, vd, at = [], [], []
+                for r in range(N):
+                    j = torch.arange(int(kv[r, b]))
+                    place = (table[b].cpu().long()[j // page], j % page)
+                    kd.append(kc[r].cpu().double()[place[0], place[1], h // 2])
+                    vd.append(vc[r].cpu().double()[place[0], place[1], h // 2])
+                for i in range(new[b]):
+                    # a token sees of each rank all but the keys of the tokens behind it
+                    later = [int(attn.owned_positions(int(seq[b]), r, N, inter) -
+                                 attn.owned_positions(int(seq[b]) - new[b] + i + 1, r, N, inter)) for r in range(N)]
+                    K = torch.cat([x[:len(x) - m] for x, m in zip(kd, later)])
+                    V = torch.cat([x[:len(x) - m] for x, m in zip(vd, later)])
+                    row = int(cu[b]) + i
+                    x = q[row, h].cpu().double()
+                    s = (K @ x) * D ** -0.5
+                    w = torch.softmax(s, 0)
+                    ds = float((u * 2.0 ** -8 + (D + 4) * 2.0 ** -24) * D ** -0.5 * (K.abs() @ x.abs()).max())
+                    # weights, partials and the merge are rounded once each
+                    assert bool(((out[row, h].cpu().double() - w @ V).abs() <= (4 * u + 2 * ds) * (w @ V.abs())).all())
+                    assert abs(float(lse[row, h]) - float(torch.logsumexp(s, 0))) <= ds + 1e-5
+        # every row gave the keys of all ranks a weight of 1, on top of what was there
+        assert bool(((mass - before).double().sum((0, 1, 2)).cpu() - T * 2).abs().max() <= T * 2 * 2.0 ** -12)
+        for r in range(N):
+            want_new, want_kept = oracle.evict(mass[r].cpu(), table.cpu(), kv[r].cpu(), budget, 1, 2, pages)
+            _, kept = attn.dcp_cache_evict(mass[r], kc[r], vc[r], table, kv[r], tables[(turn + 1) % 2], budget, n_sink=1,
+                                           n_recent=2, new_len=kv[r])
+            assert torch.equal(kv[r].cpu(), want_new) and torch.equal(kept.cpu(), want_kept)
