@@ -56,7 +56,7 @@
  * page_size below 2^30, page_size up to 2^20, N * interleave up to 2^30; the
  * attention and the weights up to 2^23 workgroups (row tiles of 128 rows, of 32
  * where rows are few, times key heads, at least one to a sequence), the eviction
- * up to B * Hkv = 2^22 and B * Hkv * budget = 2^25.
+ * up to B * Hkv = 2^21 and B * Hkv * budget = 2^28.
  */
 #ifndef DCPATTN_H
 #define DCPATTN_H

@@ -330,7 +330,7 @@ int dcpa_qk_norm_rope_append(const dcpa_rope_args* a, void* stream) {
 int dcpa_cache_evict(const dcpa_evict_args* a, void* stream) {
     if (a == nullptr) return DCP_ERR_NULL;
     if (a->esize != 1 && a->esize != 2 && a->esize != 4) return DCP_ERR_DTYPE;
-    if (a->B < 0 || a->Hkv < 1 || a->Hkv > (1 << 16) || a->B > (int64_t(1) << 20) || a->B * a->Hkv > (int64_t(1) << 22) ||
+    if (a->B < 0 || a->Hkv < 1 || a->Hkv > (1 << 16) || a->B > (int64_t(1) << 20) || a->B * a->Hkv > (int64_t(1) << 21) ||
         a->Dk < 1 || a->Dk > 4096 || (a->v && (a->Dv < 1 || a->Dv > 4096)) ||
         !cache_shape_ok(a->num_pages, a->page_size, a->max_pages) ||
         !cache_shape_ok(a->num_pages, a->page_size, a->dst_pages))
@@ -338,7 +338,8 @@ int dcpa_cache_evict(const dcpa_evict_args* a, void* stream) {
     if (a->budget < 1 || a->n_sink < 0 || a->n_recent < 0 || a->n_sink > a->budget ||
         a->n_recent > a->budget - a->n_sink || a->budget > a->dst_pages * a->page_size)
         return DCPA_ERR_VALUE;
-    if (a->B * a->Hkv * a->budget > 4 * kMaxGrid) return DCP_ERR_SHAPE;
+    // 2^31 work-items of a launch: 1024 to a sequence and head above, up to 32 to a row here
+    if (a->B * a->Hkv * a->budget > kMaxGrid * 32) return DCP_ERR_SHAPE;
     if (!strides_ok({a->m_P, a->m_S, a->m_H, a->k_P, a->k_S, a->k_H, a->v_P, a->v_S, a->v_H, a->t_B, a->d_B, a->kp_B,
                      a->kp_H}))
         return DCP_ERR_STRIDE;

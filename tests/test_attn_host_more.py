@@ -3,7 +3,7 @@ import pytest
 import torch
 
 from lse_weighted_merge_dcp_amd import attn
-from test_attn_host import A, ALIGN, OK, STRIDE, VALUE, evict_call, rope_call
+from test_attn_host import A, ALIGN, NULL, OK, SHAPE, STRIDE, VALUE, evict_call, rope_call
 
 
 @pytest.mark.parametrize("shift", [-20, -4, 4, 20])
@@ -25,3 +25,14 @@ def test_binding_checks_the_weights_of_an_append(monkeypatch):
         with pytest.raises(ValueError, match="mass"):
             attn.qk_norm_rope_append(q, k, None, None, None, z(3, dtype=torch.int32), z(1, 0), z(3, dtype=torch.int64), kc, None,
                                      mass=mass)
+
+
+@pytest.mark.parametrize("over,want", [
+    (dict(B=64, Hkv=8, budget=131072, dst_pages=8192), NULL), (dict(B=1 << 10, Hkv=1 << 10, budget=256, dst_pages=16), NULL),
+    (dict(B=1 << 10, Hkv=1 << 10, budget=257, dst_pages=17), SHAPE), (dict(B=1 << 20, Hkv=4, budget=12, dst_pages=1), SHAPE),
+    (dict(B=1 << 20, Hkv=3, budget=12, dst_pages=1), SHAPE), (dict(B=1 << 20, Hkv=2, budget=12, dst_pages=1), NULL), (dict(B=1, budget=(1 << 28) + 1, dst_pages=1 << 25), SHAPE),
+])
+def test_size_of_an_eviction(over, want):
+    """2^31 work-items to a launch: rows take at most 32 and go four at a time, 2^28 of them, and 2^21 workgroups of
+    1024, one to a sequence and head.  NULL: past the limits, and then refused for a pointer."""
+    assert evict_call(**dict(dict(mass=0, kp_H=0, kp_B=0), **over)) == want

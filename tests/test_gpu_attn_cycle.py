@@ -119,3 +119,20 @@ def test_append_attend_weigh_cut_and_on(dev):
             _, kept = attn.dcp_cache_evict(mass[r], kc[r], vc[r], table, kv[r], tables[(turn + 1) % 2], budget, n_sink=1,
                                            n_recent=2, new_len=kv[r])
             assert torch.equal(kv[r].cpu(), want_new) and torch.equal(kept.cpu(), want_kept)
+
+
+def test_a_large_budget(dev):
+    """64 sequences of 8 heads with room for 131072 keys each, 2^26 rows of the list, most of them empty."""
+    lens, budget, page = [100 + b for b in range(64)], 131072, 256
+    table, dst, kv, k, v, mass = evict_problem(lens, page, 8, 4, 4, torch.float32, page, 12)
+    wide = torch.full((64, budget // page), -1, dtype=torch.int32)
+    wide[:, :1] = dst
+    d = lambda t: t.to(dev)  # noqa: E731
+    kd, vd, md = d(k), d(v), d(mass)
+    new, kept = attn.dcp_cache_evict(md, kd, vd, d(table), d(kv), d(wide), budget)
+    assert torch.equal(new.cpu(), kv)
+    for b in (0, 31, 63):
+        n = lens[b]
+        assert torch.equal(kept[b, :, :n].cpu(), torch.arange(n, dtype=torch.int32).expand(8, n)) and bool((kept[b, :, n:] == -1).all())
+        for x, y in ((k, kd), (v, vd), (mass, md)):
+            assert torch.equal(y[int(dst[b, 0]), :n].cpu(), x[int(table[b, 0]), :n])
