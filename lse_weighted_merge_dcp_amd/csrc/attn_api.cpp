@@ -319,7 +319,6 @@ int dcpa_qk_norm_rope_append(const dcpa_rope_args* a, void* stream) {
     k.positions = (int32_t)a->positions_max;
     k.page_size = (int32_t)a->page_size;
     k.slots_max = a->num_pages * a->page_size;
-    k.fpage = dcp::make_fastdiv((uint32_t)a->page_size);
     k.fheads = dcp::make_fastdiv((uint32_t)(a->Hq + a->Hkv * (has_v ? 2 : 1)));
     k.eps = (float)a->eps;
     k.ik = (float)(1.0 / a->k_scale);

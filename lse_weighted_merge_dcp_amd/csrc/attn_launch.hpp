@@ -117,7 +117,7 @@ struct RopeArgs {
     int32_t T, Hq, Hkv, D, Dv, nq, nk, off, rot, pairs;
     int32_t positions, page_size;
     int64_t slots_max;
-    FastDiv fpage, fheads;   // fheads: heads of a token, queries, keys and values together
+    FastDiv fheads;          // heads of a token, queries, keys and values together
     float eps, ik, iv;       // eps, 1 / k_scale, 1 / v_scale
 };
 hipError_t launch_rope(const RopeArgs& a, bool bf16, bool kv8, hipStream_t stream);

@@ -55,6 +55,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs p) {
     } else {
         const int64_t slot = p.slots[token];
         if (slot < 0 || slot >= p.slots_max) return;
+        // (slots may be past 32 bits)
         const int64_t page = slot / p.page_size, place = slot - page * p.page_size;
         const int hk = which - p.Hq - (value ? p.Hkv : 0);
         from = value ? p.v + (int64_t)token * p.v_T + (int64_t)hk * p.v_H : p.k + (int64_t)token * p.k_T + (int64_t)hk * p.k_H;
