@@ -136,3 +136,55 @@ def test_a_large_budget(dev):
         assert torch.equal(kept[b, :, :n].cpu(), torch.arange(n, dtype=torch.int32).expand(8, n)) and bool((kept[b, :, n:] == -1).all())
         for x, y in ((k, kd), (v, vd), (mass, md)):
             assert torch.equal(y[int(dst[b, 0]), :n].cpu(), x[int(table[b, 0]), :n])
+
+
+@pytest.mark.parametrize("wide", [False, True], ids=["", "wide"])
+@pytest.mark.parametrize("latent", [False, True], ids=["grouped", "latent"])
+def test_a_captured_step(dev, latent, wide):
+    """Slots, append, attention, weights and a cut in one graph: replayed on new inputs and lengths, with eager work
+    between, it does what the eager calls do, bit for bit."""
+    g = torch.Generator().manual_seed(5)
+    B, page, pages, budget = 3, 16, 60, 40
+    Hq, Hkv, D, Dv = (20, 1, 576, 512) if latent else (8, 2, 128, 128)
+    T = 9
+    d = lambda *s: torch.randn(*s, generator=g).to(BF).to(dev)  # noqa: E731
+    still = torch.zeros(1, 0, device=dev)
+    table = torch.randperm(pages, generator=g)[:B * 15].to(torch.int32).view(B, 15).to(dev)
+    dst = torch.tensor([i for i in range(pages) if i not in table.cpu().flatten().tolist()][:3 * B], dtype=torch.int32, device=dev).view(B, 3)
+    st = dict(q=d(T, Hq, D), k=d(T, Hkv, D), v=None if latent else d(T, Hkv, Dv), kc=d(pages, page, Hkv, D),
+              vc=None if latent else d(pages, page, Hkv, Dv), mass=torch.rand(pages, page, Hkv, generator=g).to(dev),
+              cu=torch.tensor([0, 1, 6, 8], dtype=torch.int32, device=dev), kv=torch.tensor([200, 17, 90], dtype=torch.int32, device=dev),
+              pos=torch.tensor([199, 12, 13, 14, 15, 16, 88, 89, -1], dtype=torch.int32, device=dev),
+              of=torch.tensor([0, 1, 1, 1, 1, 1, 2, 2, -1], device=dev))
+
+    def step(s):
+        slots = attn.cache_slots(s["pos"], s["of"], table, page)
+        q = attn.qk_norm_rope_append(s["q"], s["k"], s["v"], None, None, s["pos"], still, slots, s["kc"], s["vc"], mass=s["mass"])
+        out, lse = torch.zeros(T, Hq, Dv, dtype=BF, device=dev), torch.zeros(T, Hq, device=dev)
+        attn.dcp_paged_attn(q, s["kc"], s["vc"], table, s["cu"], s["kv"], v_dim=Dv, wide_weights=wide, out=out, out_lse=lse)
+        attn.dcp_attn_mass(q, s["kc"], lse, s["mass"], table, s["cu"], s["kv"])
+        new, kept = attn.dcp_cache_evict(s["mass"], s["kc"], s["vc"], table, s["kv"], dst, budget, n_sink=1, n_recent=2, new_len=s["kv"])
+        return [out, lse, kept, new] + [t for t in (s["kc"], s["vc"], s["mass"]) if t is not None]
+
+    copy = lambda: {k: None if t is None else t.clone() for k, t in st.items()}  # noqa: E731
+    step(copy())
+    torch.cuda.synchronize()
+    held = copy()
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(stream), torch.cuda.graph(graph, stream=stream):
+        got = step(held)
+    for turn in range(4):
+        for k in ("q", "k", "v", "kc", "vc"):
+            if st[k] is not None:
+                st[k].copy_(d(*st[k].shape))
+        st["mass"].uniform_()
+        st["kv"].copy_(torch.tensor([200 - 50 * turn, 17, 90 + turn], dtype=torch.int32))
+        st["pos"][0] = 199 - 50 * turn
+        for k, t in st.items():
+            if t is not None:
+                held[k].copy_(t)
+        graph.replay()
+        want = step(copy())
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y), turn
