@@ -12,9 +12,11 @@
 // straight into LDS, the next tile of 32 while the present one is multiplied
 // (loaded into registers as fragments, 32 rows of 32 bytes to an instruction,
 // the same bytes took twice as long): decode of 16 sequences of up to 16384 keys,
-// 8 key heads of 128, 57 us, 4.4 TB/s (65 us with each head on an XCD of its own).  Many rows (mass_rows) are
-// bound by vector instructions (for 64 weights 8 clocks for the power, 4 to scale
-// and 4 to add, beside 16 of matrix instructions at 128 columns):
+// 8 key heads of 128, 59 us, 4.3 TB/s (65 us with each head on an XCD of its own).  Many rows (mass_rows) are
+// bound by the instructions of a weight (for 64 of them 8 clocks for the power, 4 to
+// scale and 4 to add, beside 16 of matrix instructions at 128 columns; the two
+// interleaved take 1.3 times the products alone) and by a barrier with a full wait
+// for every 32 rows:
 // 64 keys to a wave, so that a fragment of queries is read from LDS once for two
 // products.  Where the batch has fewer key steps than the chip has room for, the
 // rows are split, and mass_join adds the parts in order.
@@ -106,7 +108,7 @@ __device__ __forceinline__ float* mass_at(const MassArgs& p, int b, int hk, int 
 // registers: alone, a SIMD takes 16 clocks for 64 weights (8 of them the power)
 // and 16 for the products of 64 scores at 128 columns; in turn, with a barrier
 // to a tile, two waves to a SIMD overlapped them by less than half (159 us for
-// 2 x 4096 rows against 2 x 8192 keys of 8 heads; now 125 us, 0.7 PFLOP/s).  A
+// 2 x 4096 rows against 2 x 8192 keys of 8 heads; now 127 us, 0.7 PFLOP/s).  A
 // deeper ring of tiles took more scalar registers than there are (144 us).
 template <typename E, bool KV8, int DK, int KW>
 __global__ __launch_bounds__(256, DK > 256 ? 1 : 2) void mass_rows(MassArgs p) {

@@ -5,10 +5,10 @@
 // A group of LPR lanes holds a row, eight elements (16 bytes) to a lane and
 // slot; the mean of squares is one reduction over the group.  Sixteen lanes to a
 // row of 576 (a 64-lane row left most of its second slot idle: 552 us for 8192 x
-// 129 rows against 420 with 16 lanes, 5.8 TB/s; with eight lanes and nine slots
+// 129 rows against 424 with 16 lanes, 5.7 TB/s; with eight lanes and nine slots
 // the registers leave two waves to a SIMD: 651 us).  Rows turned by halves ask for
-// cosines and sines too, and for a partner: 4000 x 80 heads of 128 take 41 us, 35
-// turned by pairs, where HBM alone would take 24.
+// cosines and sines too, and for a partner: 4000 x (64 + 8 + 8) heads of 128, all
+// cached, take 56 us, 49 turned by pairs, where HBM alone would take 27.
 #include "attn_device.hpp"
 
 namespace dcpa {
