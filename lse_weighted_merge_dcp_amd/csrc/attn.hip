@@ -487,7 +487,9 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs p) {
     constexpr int FLY = NC == 1 ? 8 : 4;       // parts under way at once
     __shared__ f32x4 share[TOGETHER ? 4 : 1][NC][64];
     const int lane = threadIdx.x & 63, wave = (int)dcp::wave_id();
-    const int chunk = key_chunk<STEP>(p.m, p.rows, p.slots, p.share);
+    int longest;
+    const int chunk = key_chunk<STEP>(p.m, p.rows, p.slots, p.share, longest);
+    if (__ballot(longest > chunk) == 0) return;       // nothing was split
     // lengths and units of sequences b0 .. b0 + 63, a lane to each
     struct Line {
         Seq s;
@@ -617,12 +619,14 @@ AttnPlan plan_attn(const Batch& m, int Dk, int Dv, bool pieces) {
     pl.tiles = (int32_t)(most < each ? most : each);
     // Workgroups that run at once: one latent workgroup to a CU, two of the others.  Fewer row
     // tiles than that: the keys are split so that the units fill the chip once; decode of ragged
-    // batches fills it several times over (see fill_slots()).
+    // batches (few rows, a few tokens to a sequence of latent ones) up to four times over (see
+    // fill_slots()).
     const int64_t busy = (int64_t)pl.tiles * m.Hkv;
     const int64_t chip = pl.latent ? 256 : pl.by_keys ? 1024 : 512;
     pl.slots = pl.share = (int32_t)((chip + m.Hkv - 1) / m.Hkv);
-    if (pl.by_keys) fill_slots(pl.tiles, pl.slots, pl.share);
-    if (busy >= (pl.by_keys ? 4 * chip : chip)) pl.slots = 0;
+    const bool decode = pl.by_keys || (pl.latent && m.T <= (int64_t)8 * m.B);
+    if (decode) fill_slots(pl.tiles, pl.slots, pl.share);
+    if (busy >= (decode ? 4 * chip : chip)) pl.slots = 0;
     pl.units = pl.slots > pl.tiles ? pl.slots : pl.tiles;
     pl.ws_bytes = pl.slots == 0 ? 0 : (int64_t)pl.units * m.Hkv * pl.rows * (Dv + 1) * 4;
     return pl;

@@ -278,9 +278,10 @@ __device__ __forceinline__ void tiles_of(const Batch& m, int b, int rows, int& t
 // The length of a key range: the shortest multiple of STEP (to within an
 // eighth of the interval) with which the whole batch needs at most `slots`
 // units and none more than a `share`-th of its work; kWhole where the tiles
-// alone need that many.
+// alone need that many.  `longest`: the most keys that the lane met.
 template <int STEP>
-__device__ __forceinline__ int key_chunk(const Batch& m, int rows, int slots, int share) {
+__device__ __forceinline__ int key_chunk(const Batch& m, int rows, int slots, int share, int& longest) {
+    longest = 0;
     if (slots <= 0) return kWhole;
     const int lane = threadIdx.x & 63;
     int64_t work = 0;
@@ -289,6 +290,7 @@ __device__ __forceinline__ int key_chunk(const Batch& m, int rows, int slots, in
         tiles_of(m, b0 + lane, rows, tiles, kv);
         work += (int64_t)tiles * kv;
         all += tiles;
+        longest = max(longest, kv);
     }
     work = sum_wave(work);
     all = (int)sum_wave((int64_t)all);
@@ -309,6 +311,12 @@ __device__ __forceinline__ int key_chunk(const Batch& m, int rows, int slots, in
         else lo = mid + 1;
     }
     return hi * STEP;
+}
+
+template <int STEP>
+__device__ __forceinline__ int key_chunk(const Batch& m, int rows, int slots, int share) {
+    int longest;
+    return key_chunk<STEP>(m, rows, slots, share, longest);
 }
 
 template <int STEP>

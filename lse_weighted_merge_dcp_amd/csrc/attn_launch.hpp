@@ -59,12 +59,13 @@ struct AttnPlan {
     int32_t slots, share, tiles, units;
     int64_t ws_bytes;
 };
-// Few rows: the units that fill the chip, `slots`, leave no room to split a long sequence where the row
+// Decode: the units that fill the chip, `slots`, leave no room to split a long sequence where the row
 // tiles alone are nearly as many.  From half as many tiles on half a chip's units are added to them, and a
 // sequence is split where it is longer than two units' equal shares, so that even batches stay whole.
 // (128 sequences of about 1000 keys, one of 131072, 8 key heads: 216 us, unsplit 1663; all of
-// about 1000: 120 us either way.)  Where they fill the chip four times over they stay whole: every
-// workgroup reads all lengths to split them, 500 sequences of 100 keys take 122 us and 512 unsplit 82.
+// about 1000: 120 us either way.  256 latent ones of 128 heads: 214 and 6291 us; 126 and 118 us.)  Where
+// they fill the chip four times over they stay whole: every workgroup reads all lengths to split them, 500
+// sequences of 100 keys take 105 us and 512 unsplit 81.
 inline void fill_slots(int32_t tiles, int32_t& slots, int32_t& share) {
     if (2 * (int64_t)tiles <= slots) return;
     share = (slots + 1) / 2;

@@ -45,3 +45,23 @@ def test_many_rows_of_many_sequences(dev):
     want, tol = p.mass(lse, before)
     got = mass_call(p, lse, before.to(dev), dev, workspace=torch.empty(0, device=dev)).cpu().double()
     assert bool(((got - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("B,at,n", [(135, 134, 1), (255, 0, 1), (270, 100, 1), (140, 70, 3)])
+def test_one_long_latent_sequence(dev, B, at, n):
+    """The same for latent rows, where a sequence's tokens fill row tiles of their own; shared rows of few heads."""
+    seqs = [(1, 1 + i * 7 % 40) for i in range(B)]
+    seqs[at] = (n, 1500)
+    p = Problem(seqs, 3, 1, 576, 512, shared=True, seed=B)
+    ws = torch.full((1 << 25,), math.nan, device=dev)
+    strict(p, call(p, dev, workspace=ws))
+    assert not bool(torch.isnan(ws).all()), "no range was split"
+
+
+def test_even_batches_need_no_join(dev):
+    """Nothing is split: every row is written whole, and the workspace stays as it was."""
+    for kw in (dict(Hq=8, Hkv=8, Dk=32, Dv=32), dict(Hq=3, Hkv=1, Dk=576, Dv=512, shared=True)):
+        p = Problem([(1, 30 + i % 7) for i in range(200)], seed=3, **kw)
+        ws = torch.full((1 << 25,), math.nan, device=dev)
+        strict(p, call(p, dev, workspace=ws))
+        assert bool(torch.isnan(ws).all())
