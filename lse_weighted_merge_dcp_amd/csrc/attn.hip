@@ -480,7 +480,8 @@ __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void attn_keys(AttnArgs p) {
 // waves of a workgroup share a row's (TOGETHER).  Many rows have few: a wave goes
 // from row to row, and works out the lengths once.  Bound by latency: eight parts
 // under way at once (7 rows of 155 parts: 9 us, 54 us one part after the other by
-// one wave; 2048 rows by a wave each 8 us, by a workgroup each 14 us).
+// one wave; 2048 rows by a wave each 8 us, by a workgroup each 14 us).  Where the
+// lengths turn out even nothing was split, and nothing is joined.
 // ---------------------------------------------------------------------------
 template <typename E, int STEP, int NC, bool TOGETHER>
 __global__ __launch_bounds__(256) void attn_join(AttnArgs p) {
