@@ -399,8 +399,12 @@ def cache_slots(positions: torch.Tensor, sequence: torch.Tensor, block_table: to
     Index arithmetic on small tensors (any device)."""
     if (kv_len is None) != (seq_len is None):
         raise ValueError("kv_len and seq_len go together")
-    p, s = positions.long(), sequence.long()
+    _require(page_size >= 1 and n_ranks >= 1 and interleave >= 1 and 0 <= rank < n_ranks,
+             "page_size, n_ranks and interleave are positive, rank below n_ranks")
     rows, width = block_table.shape
+    if positions.shape != sequence.shape or kv_len is not None and not kv_len.shape == seq_len.shape == (rows,):
+        raise ValueError("expected positions and sequence of one shape, kv_len and seq_len [B]")
+    p, s = positions.long(), sequence.long()
     if rows == 0 or width == 0:
         return torch.full_like(p, -1)
     at_row = s.clamp(0, rows - 1)

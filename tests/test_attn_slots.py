@@ -71,3 +71,16 @@ def test_cut_lengths_go_together():
     for kw in (dict(kv_len=t), dict(seq_len=t)):
         with pytest.raises(ValueError):
             attn.cache_slots(t, t, torch.zeros(1, 1, dtype=torch.int32), 4, **kw)
+
+
+def test_lengths_of_every_sequence():
+    """One length to a row of the table, or indexing would leave the arrays."""
+    t, table = torch.zeros(3, dtype=torch.long), torch.zeros(3, 2, dtype=torch.int32)
+    for kv, seq in ((t[:2], t), (t, t[:2]), (t[:, None], t)):
+        with pytest.raises(ValueError):
+            attn.cache_slots(t, t, table, 4, kv_len=kv, seq_len=seq)
+    with pytest.raises(ValueError):
+        attn.cache_slots(t, t[:2], table, 4)
+    for kw in (dict(page_size=0), dict(n_ranks=0), dict(interleave=0), dict(n_ranks=2, rank=2), dict(rank=-1)):
+        with pytest.raises(ValueError):
+            attn.cache_slots(t, t, table, **dict(dict(page_size=4), **kw))
