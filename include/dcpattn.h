@@ -89,7 +89,7 @@ const char* dcpa_status_str(int status);
  * where (u, v) are columns (j, j + rot/2) of the range, or (2j, 2j+1) if
  * interleaved != 0.  Each result is rounded once.
  *
- * q [T, Hq, D] -> q_out [T, Hq, D] (may be q itself, same strides), normed by
+ * q [T, Hq, D] -> q_out [T, Hq, D] (may be q itself, with the same strides), normed by
  * q_weight [q_norm].  k [T, Hkv, D], normed by k_weight [k_norm], goes to the
  * cache row slots[t] = page * page_size + place; v [T, Hkv, Dv] (nullable) goes
  * to the value cache unchanged but for its type.  A slot outside [0, num_pages

@@ -288,6 +288,7 @@ int dcpa_qk_norm_rope_append(const dcpa_rope_args* a, void* stream) {
         !span_ok({{a->num_pages, a->m_P}, {a->page_size, a->m_S}, {a->Hkv, a->m_H}}, 4))
         return DCP_ERR_STRIDE;
     if (a->T == 0) return DCP_OK;
+    if (a->q_out == a->q && ((a->T > 1 && a->qo_T != a->q_T) || (a->Hq > 1 && a->qo_H != a->q_H))) return DCP_ERR_STRIDE;
     if (!a->q || !a->k || !a->q_out || !a->slots || (a->rot > 0 && (!a->positions || !a->cos_sin)) ||
         (a->q_norm > 0 && !a->q_weight) || (a->k_norm > 0 && !a->k_weight) ||
         (a->num_pages > 0 && (!a->k_cache || (has_v && !a->v_cache))))

@@ -36,3 +36,11 @@ def test_size_of_an_eviction(over, want):
     """2^31 work-items to a launch: rows take at most 32 and go four at a time, 2^28 of them, and 2^21 workgroups of
     1024, one to a sequence and head.  NULL: past the limits, and then refused for a pointer."""
     assert evict_call(**dict(dict(mass=0, kp_H=0, kp_B=0), **over)) == want
+
+
+@pytest.mark.parametrize("over,want", [(dict(q_out=A, qo_T=2048), STRIDE), (dict(q_out=A, qo_H=256), STRIDE),
+                                       (dict(q_out=A, qo_T=2048, T=1), NULL), (dict(q_out=A, qo_H=256, Hq=1, Hkv=1), NULL),
+                                       (dict(q_out=A), NULL), (dict(q_out=2 * A, qo_T=2048), NULL)])
+def test_append_in_place_needs_the_same_strides(over, want):
+    """q_out = q of other strides would be written over queries that are still to be read.  (NULL: past this check.)"""
+    assert rope_call(**dict(dict(T=3, slots=0), **over)) == want
