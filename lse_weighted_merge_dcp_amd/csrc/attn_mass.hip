@@ -249,6 +249,7 @@ __global__ __launch_bounds__(256, DK > 256 ? 1 : 2) void mass_rows(MassArgs p) {
                 meet();       // tile t is there, and the other buffer is free
             }
             const float g = g_next;
+            const bool some = __ballot(g == -INFINITY) != 0;     // rows that saw nothing anywhere, whatever stands in them
             const uint32_t qrow = lds0 + (uint32_t)(buf * PAD + r * QROW);
             if (t + 1 < end_tile) fetch(t + 1, buf ^ 1, g_next);
             u32x4 b[ST];
@@ -266,11 +267,11 @@ __global__ __launch_bounds__(256, DK > 256 ? 1 : 2) void mass_rows(MassArgs p) {
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
-            const bool none = g == -INFINITY;     // the row saw nothing anywhere, whatever stands in it
+            const bool none = g == -INFINITY;
             g_old = none ? INFINITY : g * p.lmul;
             // rows are in the order of their tokens: where the first sees all of the wave's keys, so do the
             // others, but for those behind the last and those without a sum, which see nothing
-            if (t * 32 + 31 >= nrows || __ballot(none) != 0 || visible(p.m, u.s, (int)fdiv((uint32_t)(t * 32), p.m.fG)) < key0 + KW) {
+            if (t * 32 + 31 >= nrows || some || visible(p.m, u.s, (int)fdiv((uint32_t)(t * 32), p.m.fG)) < key0 + KW) {
                 const int row = t * 32 + r;
                 const int lim = row < nrows && !none ? visible(p.m, u.s, (int)fdiv((uint32_t)row, p.m.fG)) - key0 - 4 * h : 0;
                 // (a row whose sum is NaN gives NaN to what it sees and nothing to the rest)
