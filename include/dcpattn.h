@@ -224,6 +224,57 @@ typedef struct {
 } dcpa_evict_args;
 int dcpa_cache_evict(const dcpa_evict_args* a, void* stream);
 
+/*
+ * dcpa_batch_plan
+ *
+ * What a step of the calls above needs of its batch, from the number of new
+ * tokens of each sequence.  seq_len and kv_len hold the lengths before the step
+ * (over all ranks; cached on this rank).  For a sequence that goes on, new_len =
+ * n >= 0:
+ *   seq_out = seq_len + n,  kv_out = kv_len + owned(seq_len + n) - owned(seq_len),
+ *   block_table[b, i] for ceil(kv_len / page_size) <= i < ceil(kv_out / page_size)
+ *     (and i < max_pages): pages from the end of the free list, in the order of
+ *     sequences and places, -1 once it is empty,
+ * and its rows are cu_q[b] .. cu_q[b+1]-1 with, for row t, position seq_len + t -
+ * cu_q[b], sequence b, and the slot that dcpa_qk_norm_rope_append takes: -1 where
+ * another rank owns the position or the table has no page.  The rows from cu_q[B]
+ * to T-1 get -1 in all three.  Tokens beyond row T-1, or beyond a length of 2^30 -
+ * 1, are not taken: cu_q and the lengths count those that are.
+ * new_len < 0: the sequence has ended.  Its lengths become 0, and its pages
+ * block_table[b, i] >= 0, keep_pages[b] <= i < ceil(kv_len / page_size), go onto
+ * the end of the list, ahead of any page that this call takes (keep_pages NULL:
+ * 0; pages in front that others use, or that stay).  Its table row keeps its
+ * entries, which no length counts any more.
+ * free_pages [free_max] holds free_count[0] pages (clamped to [0, free_max];
+ * pages given back beyond free_max are lost); free_count_out is what is left,
+ * or, negative, minus the number of pages that were missing.
+ *
+ * Where caches were cut, kv_len counts what is cached, as in the other calls.
+ * seq_out, kv_out and free_count_out may be the inputs themselves; other
+ * overlaps of outputs with inputs or each other are not allowed (partial ones of
+ * the lengths: DCPA_ERR_VALUE).  T up to 2^30 rows, free_max below 2^31; B = 0
+ * and T = 0 are no special cases (cu_q[0], the rows' padding and the count are
+ * written).
+ */
+typedef struct {
+    const int32_t* new_len;                /* [B] */
+    const int32_t* seq_len;                /* [B] */
+    const int32_t* kv_len;                 /* [B] */
+    const int32_t* keep_pages;             /* [B], nullable */
+    int32_t* block_table; int64_t t_B;     /* [B, max_pages] */
+    int32_t* free_pages;                   /* [free_max] */
+    const int32_t* free_count;             /* [1] */
+    int32_t* free_count_out;               /* [1] */
+    int32_t* seq_out;                      /* [B] */
+    int32_t* kv_out;                       /* [B] */
+    int32_t* cu_q;                         /* [B + 1] */
+    int32_t* positions;                    /* [T] */
+    int32_t* sequence;                     /* [T] */
+    int64_t* slots;                        /* [T] */
+    int64_t B, T, max_pages, page_size, free_max, N, rank, interleave;
+} dcpa_plan_args;
+int dcpa_batch_plan(const dcpa_plan_args* a, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -14,6 +14,8 @@ PyTorch fallback.
   dcp_attn_mass         accumulate the attention weight of every cached key
                         from the LSE that ops.dcp_lse_combine returns
   dcp_cache_evict       keep the keys of highest accumulated weight
+  dcp_batch_plan        a step's lengths, page tables, positions and cache slots
+                        from the numbers of new tokens, on the GPU
   cache_slots           where this rank caches new tokens
   owned_positions       how many positions of a sequence lie on this rank
 
@@ -26,7 +28,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -47,11 +49,13 @@ SIGNATURES = {
     "dcpa_attn_mass": ([_CP, _VP, _I64, _I64, _I64, _VP], ctypes.c_int),
     "dcpa_attn_mass_workspace": ([_CP], _I64),
     "dcpa_cache_evict": ([_CP, _VP], ctypes.c_int),
+    "dcpa_batch_plan": ([_CP, _VP], ctypes.c_int),
 }
 # The argument structs: every field 8 bytes, in the header's order.
 ROPE_ARGS = struct.Struct("=45q3d")
 ATTN_ARGS = struct.Struct("=41q3d")
 EVICT_ARGS = struct.Struct("=33q")
+PLAN_ARGS = struct.Struct("=23q")
 
 _DTYPE = {torch.float16: _lib.DCP_F16, torch.bfloat16: _lib.DCP_BF16}
 _CACHE = {torch.float16: _lib.DCP_F16, torch.bfloat16: _lib.DCP_BF16, torch.float8_e4m3fn: _lib.DCP_FP8_E4M3}
@@ -373,6 +377,70 @@ def dcp_cache_evict(mass: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional
         budget, n_sink, n_recent)
     _call(lib().dcpa_cache_evict, "dcpa_cache_evict", dev, args)
     return new_len, kept
+
+
+class BatchPlan(NamedTuple):
+    """What dcp_batch_plan gives a step: int32 but for slots (int64)."""
+    cu_q: torch.Tensor          # [B + 1]
+    seq_len: torch.Tensor       # [B], after the step
+    kv_len: torch.Tensor        # [B], after the step
+    free_count: torch.Tensor    # [1]
+    positions: torch.Tensor     # [T]
+    sequence: torch.Tensor      # [T]
+    slots: torch.Tensor         # [T]
+
+
+def dcp_batch_plan(new_len: torch.Tensor, seq_len: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor,
+                   free_pages: torch.Tensor, free_count: torch.Tensor, max_tokens: int, page_size: int, *,
+                   rank: int = 0, n_ranks: int = 1, interleave: int = 1, keep_pages: Optional[torch.Tensor] = None,
+                   out: Optional[BatchPlan] = None) -> BatchPlan:
+    """Plan a step with new_len[b] new tokens of sequence b (int32 [B]; negative:
+    the sequence has ended), whose lengths before it are seq_len (over all ranks)
+    and kv_len (cached on this rank).  Sequences that grow past their last page
+    get pages from the end of free_pages (int32, of which the first
+    free_count[0] are free; -1 once there are none), written into
+    block_table (int32 [B, pages]); ended ones first give theirs back, but for
+    the first keep_pages[b].  Returns the plan of max_tokens rows: cu_q,
+    lengths after the step and pages left (negative: so many were missing), and
+    for every row its position, its sequence and its slot for
+    qk_norm_rope_append, -1 behind the last token (slots also where another
+    rank owns the position, or no page is there).  Tokens beyond the last row
+    are not taken.  out: the tensors to write; its seq_len, kv_len and free_count
+    may be the inputs themselves."""
+    _require(max_tokens >= 0 and page_size >= 1, "max_tokens is not negative, page_size positive")
+    if new_len.dim() != 1 or block_table.dim() != 2:
+        raise ValueError("new_len must be int32 [B], block_table int32 [B, pages of a sequence]")
+    B, T = new_len.shape[0], max_tokens
+    if out is None:
+        # (one allocation: seven would take longer than the kernel)
+        words = torch.empty(2 * T + (3 * B + 3) // 2, dtype=torch.int64, device=new_len.device)
+        slots, rest = words.split([T, words.shape[0] - T])
+        cu, seq, kv, left, pos, sid, _ = rest.view(torch.int32).split([B + 1, B, B, 1, T, T, 2 * rest.shape[0] - 3 * B - 2 - 2 * T])
+        out = BatchPlan(cu, seq, kv, left, pos, sid, slots)
+        dev = _on_gpu(new_len, seq_len, kv_len, block_table, free_pages, free_count, keep_pages)
+    else:
+        dev = _on_gpu(new_len, seq_len, kv_len, block_table, free_pages, free_count, keep_pages, *out)
+        for t, name, n in ((out.cu_q, "out.cu_q", B + 1), (out.seq_len, "out.seq_len", B), (out.kv_len, "out.kv_len", B),
+                           (out.free_count, "out.free_count", 1), (out.positions, "out.positions", T),
+                           (out.sequence, "out.sequence", T)):
+            _ints(t, name, (n,))
+        _ints(out.slots, "out.slots", (T,), torch.int64)
+    _ints(new_len, "new_len", (B,))
+    _ints(seq_len, "seq_len", (B,))
+    _ints(kv_len, "kv_len", (B,))
+    if keep_pages is not None:
+        _ints(keep_pages, "keep_pages", (B,))
+    _ints(block_table, "block_table", (B, block_table.shape[1]))
+    _ints(free_pages, "free_pages", (free_pages.numel(),))
+    _ints(free_count, "free_count", (1,))
+    args = PLAN_ARGS.pack(
+        new_len.data_ptr(), seq_len.data_ptr(), kv_len.data_ptr(), keep_pages.data_ptr() if keep_pages is not None else 0,
+        block_table.data_ptr(), block_table.stride(0) if B > 1 else block_table.shape[1], free_pages.data_ptr(),
+        free_count.data_ptr(), out.free_count.data_ptr(), out.seq_len.data_ptr(), out.kv_len.data_ptr(),
+        out.cu_q.data_ptr(), out.positions.data_ptr(), out.sequence.data_ptr(), out.slots.data_ptr(),
+        B, max_tokens, block_table.shape[1], page_size, free_pages.numel(), n_ranks, rank, interleave)
+    _call(lib().dcpa_batch_plan, "dcpa_batch_plan", dev, args)
+    return out
 
 
 def owned_positions(length, rank: int = 0, n_ranks: int = 1, interleave: int = 1):

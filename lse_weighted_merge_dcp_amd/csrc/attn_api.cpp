@@ -53,6 +53,12 @@ bool cache_shape_ok(int64_t pages, int64_t page_size, int64_t max_pages) {
            max_pages >= 0 && max_pages < (int64_t(1) << 31) && max_pages * page_size < (int64_t(1) << 30);
 }
 
+bool ranks_ok(int64_t N, int64_t rank, int64_t inter) {
+    return N >= 1 && N <= (1 << 20) && rank >= 0 && rank < N && inter >= 1 && inter <= (1 << 20) &&
+           N * inter <= (int64_t(1) << 30);
+}
+uintptr_t apart(uintptr_t x, uintptr_t y) { return x < y ? y - x : x - y; }
+
 // The checks that the attention and the weights share; fills `m`.
 int check_batch(const dcpa_attn_args* a, Batch& m) {
     if (a->dtype != DCP_F16 && a->dtype != DCP_BF16) return DCP_ERR_DTYPE;
@@ -64,9 +70,7 @@ int check_batch(const dcpa_attn_args* a, Batch& m) {
     if (a->Hq % a->Hkv != 0) return DCP_ERR_HEADS_NOT_DIVISIBLE;
     if (a->Dk < 8 || a->Dk % 8 != 0 || a->Dk > 576) return DCP_ERR_SHAPE;
     if (!cache_shape_ok(a->num_pages, a->page_size, a->max_pages)) return DCP_ERR_SHAPE;
-    if (a->N < 1 || a->N > (1 << 20) || a->rank < 0 || a->rank >= a->N || a->interleave < 1 ||
-        a->interleave > (1 << 20) || a->N * a->interleave > (int64_t(1) << 30))
-        return DCP_ERR_SHAPE;
+    if (!ranks_ok(a->N, a->rank, a->interleave)) return DCP_ERR_SHAPE;
     if (!positive(a->scale) || !positive(a->k_scale) || !positive(a->v_scale) ||
         !positive(a->scale * a->k_scale * 1.4426950408889634))
         return DCPA_ERR_VALUE;
@@ -384,6 +388,47 @@ int dcpa_cache_evict(const dcpa_evict_args* a, void* stream) {
     k.fHkv = dcp::make_fastdiv((uint32_t)a->Hkv);
     k.fbudget = dcp::make_fastdiv((uint32_t)a->budget);
     return status(launch_evict(k, (hipStream_t)stream));
+}
+
+int dcpa_batch_plan(const dcpa_plan_args* a, void* stream) {
+    if (a == nullptr) return DCP_ERR_NULL;
+    if (a->B < 0 || a->B > (int64_t(1) << 20) || a->T < 0 || a->T > kMaxRows || a->free_max < 0 ||
+        a->free_max >= (int64_t(1) << 31) || !cache_shape_ok(0, a->page_size, a->max_pages) ||
+        !ranks_ok(a->N, a->rank, a->interleave))
+        return DCP_ERR_SHAPE;
+    if (!strides_ok({a->t_B}) || !span_ok({{a->B, a->t_B}, {a->max_pages, 1}}, 4)) return DCP_ERR_STRIDE;
+    // (rows of the table that overlap would be written by two sequences)
+    if (a->B > 1 && a->t_B < a->max_pages) return DCP_ERR_STRIDE;
+    if (!a->free_count || !a->free_count_out || !a->cu_q || (a->free_max > 0 && !a->free_pages) ||
+        (a->B > 0 && (!a->new_len || !a->seq_len || !a->kv_len || !a->seq_out || !a->kv_out ||
+                      (a->max_pages > 0 && !a->block_table))) ||
+        (a->T > 0 && (!a->positions || !a->sequence || !a->slots)))
+        return DCP_ERR_NULL;
+    for (const void* x : {(const void*)a->new_len, (const void*)a->seq_len, (const void*)a->kv_len,
+                          (const void*)a->keep_pages, (const void*)a->block_table, (const void*)a->free_pages,
+                          (const void*)a->free_count, (const void*)a->free_count_out, (const void*)a->seq_out,
+                          (const void*)a->kv_out, (const void*)a->cu_q, (const void*)a->positions, (const void*)a->sequence})
+        if (!aligned(x, 4)) return DCP_ERR_ALIGN;
+    if (!aligned(a->slots, 8)) return DCP_ERR_ALIGN;
+    // a length written over another sequence's that is still to be read
+    for (const int32_t* out : {a->seq_out, a->kv_out})
+        for (const int32_t* in : {a->new_len, a->seq_len, a->kv_len, a->keep_pages})
+            if (in && in != out && apart((uintptr_t)in, (uintptr_t)out) < (uintptr_t)a->B * 4) return DCPA_ERR_VALUE;
+    if (a->B > 0 && apart((uintptr_t)a->seq_out, (uintptr_t)a->kv_out) < (uintptr_t)a->B * 4) return DCPA_ERR_VALUE;
+    PlanArgs k;
+    k.new_len = a->new_len; k.seq = a->seq_len; k.kv = a->kv_len; k.keep = a->keep_pages;
+    k.table = a->block_table;
+    k.t_B = a->t_B;
+    k.free = a->free_pages; k.count = a->free_count;
+    k.count_out = a->free_count_out; k.seq_out = a->seq_out; k.kv_out = a->kv_out; k.cu = a->cu_q;
+    k.positions = a->positions; k.sequence = a->sequence;
+    k.slots = a->slots;
+    k.B = (int32_t)a->B; k.T = (int32_t)a->T; k.width = (int32_t)a->max_pages;
+    k.page_size = (int32_t)a->page_size; k.free_max = (int32_t)a->free_max;
+    k.N = (int32_t)a->N; k.rank = (int32_t)a->rank; k.inter = (int32_t)a->interleave;
+    k.fpage = dcp::make_fastdiv((uint32_t)k.page_size);
+    k.fblock = dcp::make_fastdiv((uint32_t)(k.N * k.inter));
+    return status(launch_plan(k, (hipStream_t)stream));
 }
 
 }  // extern "C"

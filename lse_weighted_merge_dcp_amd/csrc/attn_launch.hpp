@@ -140,6 +140,20 @@ struct EvictArgs {
 };
 hipError_t launch_evict(const EvictArgs& a, hipStream_t stream);
 
+struct PlanArgs {
+    const int32_t *new_len, *seq, *kv, *keep;   // keep: nullable
+    int32_t* table;
+    int64_t t_B;
+    int32_t* free;
+    const int32_t* count;
+    int32_t *count_out, *seq_out, *kv_out, *cu, *positions, *sequence;
+    int64_t* slots;
+    int32_t B, T, width, page_size, free_max, N, rank, inter;
+    int32_t rows_here;       // up to as many token rows are done by the kernel of the lengths
+    FastDiv fpage, fblock;
+};
+hipError_t launch_plan(const PlanArgs& a, hipStream_t stream);
+
 // Launch kernel(arg) and return that launch's own status.
 template <typename Arg>
 inline hipError_t launch(void (*kernel)(Arg), dim3 grid, dim3 block, hipStream_t stream, const Arg& arg) {
