@@ -275,6 +275,66 @@ typedef struct {
 } dcpa_plan_args;
 int dcpa_batch_plan(const dcpa_plan_args* a, void* stream);
 
+/*
+ * dcpa_project
+ *
+ * The projections on both sides of latent attention, head by head:
+ *   y[t, h, n] = sum_{k < K} x[t, h, k] w[h, n, k]      n < N
+ *   y[t, h, N + c] = x[t, h, K + c]                      c < copy
+ * Queries [nope | rope] into latent space: w the heads' key weights [Dn, Dc] with
+ * K = Dn, N = Dc, copy = Dr.  Latent outputs to values: w the value weights
+ * [Dv, Dc] with K = Dc, N = Dv, copy = 0.  Sums in fp32, each result rounded
+ * once; the copied columns keep their bits.
+ *
+ * dtype: DCP_F16 or DCP_BF16 (x, w, y).  N and K multiples of 8 up to 1024,
+ * copy a multiple of 8 up to 1024, H up to 2^16, T * H up to 2^30.  One of w_N
+ * and w_K is 1, the other a multiple of 8; the other strides are multiples of
+ * 8, x, w and y 16-byte aligned.  y overlaps neither x nor w.
+ */
+typedef struct {
+    const void* x;        int64_t x_T, x_H;
+    const void* w;        int64_t w_H, w_N, w_K;
+    void* y;              int64_t y_T, y_H;
+    int64_t T, H, N, K, copy, dtype;
+} dcpa_project_args;
+int dcpa_project(const dcpa_project_args* a, void* stream);
+
+/*
+ * dcpa_latent_expand
+ *
+ * Keys and values of every head from cached latent rows c = [latent Dc | rope Dr]
+ * (the cache of the latent layout, one key head): for cached key j < kv_len[b]
+ *   k[b, j, h] = k_scale [ sum_c w_k[h, n, c] c_j[c]  (n < Dn) | c_j[Dc ..] (Dr) ]
+ *   v[b, j, h] = k_scale sum_c w_v[h, n, c] c_j[c]             (n < Dv)
+ * Sums in fp32, each result rounded once to dtype: attention over them reads
+ * keys of that type, as if they had been cached.  kv_len is clamped to max_keys
+ * and to max_pages * page_size.  Rows behind kv_len, and keys whose page is
+ * missing, are left as they were.
+ *
+ * places [B, max_keys] (nullable) gets b * max_keys + j for every such key, -1
+ * where its page is missing: the block_table with which dcpa_paged_attn reads k and
+ * v as caches of B * max_keys pages of one key (where they are contiguous over b).
+ *
+ * dtype: DCP_F16 or DCP_BF16 (w_k, w_v, k, v); cache_dtype dtype or
+ * DCP_FP8_E4M3.  Dn, Dv multiples of 8 up to 512, Dr a multiple of 8 (0: none),
+ * Dc a multiple of 8, Dc + Dr <= 576.  Weight rows are contiguous over Dc, all
+ * strides multiples of 8, all buffers 16-byte aligned, B * max_keys below 2^30.
+ * The outputs overlap neither each other nor the inputs.
+ */
+typedef struct {
+    const void* cache;    int64_t c_P, c_S;       /* [num_pages, page_size, Dc + Dr] */
+    const int32_t* block_table; int64_t t_B;
+    const int32_t* kv_len;                        /* [B] */
+    const void* w_k;      int64_t wk_H, wk_N;     /* [H, Dn, Dc] */
+    const void* w_v;      int64_t wv_H, wv_N;     /* [H, Dv, Dc] */
+    void* k;              int64_t k_B, k_S, k_H;  /* [B, max_keys, H, Dn + Dr] */
+    void* v;              int64_t v_B, v_S, v_H;  /* [B, max_keys, H, Dv] */
+    int32_t* places;      int64_t p_B;
+    int64_t B, H, Dn, Dr, Dv, Dc, max_keys, num_pages, page_size, max_pages, dtype, cache_dtype;
+    double k_scale;
+} dcpa_expand_args;
+int dcpa_latent_expand(const dcpa_expand_args* a, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

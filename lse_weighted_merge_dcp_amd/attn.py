@@ -14,6 +14,11 @@ PyTorch fallback.
   dcp_attn_mass         accumulate the attention weight of every cached key
                         from the LSE that ops.dcp_lse_combine returns
   dcp_cache_evict       keep the keys of highest accumulated weight
+  latent_queries        queries into latent space, in front of attention over
+                        latent rows
+  latent_values         its latent outputs to values
+  latent_expand         keys and values of every head from cached latent rows
+  dcp_latent_attn       attention over them: latent attention in the expanded form
   dcp_batch_plan        a step's lengths, page tables, positions and cache slots
                         from the numbers of new tokens, on the GPU
   cache_slots           where this rank caches new tokens
@@ -50,12 +55,16 @@ SIGNATURES = {
     "dcpa_attn_mass_workspace": ([_CP], _I64),
     "dcpa_cache_evict": ([_CP, _VP], ctypes.c_int),
     "dcpa_batch_plan": ([_CP, _VP], ctypes.c_int),
+    "dcpa_project": ([_CP, _VP], ctypes.c_int),
+    "dcpa_latent_expand": ([_CP, _VP], ctypes.c_int),
 }
 # The argument structs: every field 8 bytes, in the header's order.
 ROPE_ARGS = struct.Struct("=45q3d")
 ATTN_ARGS = struct.Struct("=41q3d")
 EVICT_ARGS = struct.Struct("=33q")
 PLAN_ARGS = struct.Struct("=23q")
+PROJECT_ARGS = struct.Struct("=16q")
+EXPAND_ARGS = struct.Struct("=34q1d")
 
 _DTYPE = {torch.float16: _lib.DCP_F16, torch.bfloat16: _lib.DCP_BF16}
 _CACHE = {torch.float16: _lib.DCP_F16, torch.bfloat16: _lib.DCP_BF16, torch.float8_e4m3fn: _lib.DCP_FP8_E4M3}
@@ -377,6 +386,129 @@ def dcp_cache_evict(mass: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional
         budget, n_sink, n_recent)
     _call(lib().dcpa_cache_evict, "dcpa_cache_evict", dev, args)
     return new_len, kept
+
+
+def _project(x, w, turned, N, K, copy, out, name):
+    """One dcpa_project call: w [H, ., .] with its rows as columns of the result (turned: as sums)."""
+    dev = _on_gpu(x, w, out)
+    _rows(x, "x", 3)
+    T, H = x.shape[0], x.shape[1]
+    if x.dtype not in _DTYPE or w.dtype != x.dtype:
+        raise ValueError("%s: float16 or bfloat16 rows and weights of one dtype" % name)
+    if out is None:
+        out = torch.empty((T, H, N + copy), dtype=x.dtype, device=x.device)
+    _rows(out, "out", 3)
+    if out.shape != (T, H, N + copy) or out.dtype != x.dtype:
+        raise ValueError("bad out tensor")
+    xs, ws, ys = x.stride(), w.stride(), out.stride()
+    w_N, w_K = (ws[2], ws[1]) if turned else (ws[1], ws[2])
+    args = PROJECT_ARGS.pack(x.data_ptr(), xs[0], xs[1], w.data_ptr(), ws[0], w_N, w_K, out.data_ptr(), ys[0], ys[1],
+                             T, H, N, K, copy, _DTYPE[x.dtype])
+    _call(lib().dcpa_project, "dcpa_project", dev, args)
+    return out
+
+
+def latent_queries(q: torch.Tensor, w_uk: torch.Tensor, *, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Queries q [T,H,Dn+Dr] into latent space: [q[..., :Dn] @ w_uk[h] | q[...,
+    Dn:]], [T,H,Dc+Dr], with the key weights w_uk [H,Dn,Dc] of a latent layer.
+    The result is what qk_norm_rope_append (rope_offset = Dc) and dcp_paged_attn
+    take against latent rows.  w_uk may be a view of the whole projection
+    [H,Dn+Dv,Dc], or of a transposed one (one of its last two dimensions
+    contiguous)."""
+    if w_uk.dim() != 3 or q.dim() != 3 or w_uk.shape[0] != q.shape[1] or q.shape[2] < w_uk.shape[1]:
+        raise ValueError("expected q [T,H,Dn+Dr] and w_uk [H,Dn,Dc]")
+    Dn, Dc = w_uk.shape[1], w_uk.shape[2]
+    return _project(q, w_uk, True, Dc, Dn, q.shape[2] - Dn, out, "latent_queries")
+
+
+def latent_values(o: torch.Tensor, w_uv: torch.Tensor, *, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Values [T,H,Dv] from (merged) latent outputs o [T,H,Dc]: o[t, h] @
+    w_uv[h].T, with the value weights w_uv [H,Dv,Dc] of a latent layer (one of
+    the last two dimensions contiguous)."""
+    if w_uv.dim() != 3 or o.dim() != 3 or w_uv.shape[0] != o.shape[1] or o.shape[2] != w_uv.shape[2]:
+        raise ValueError("expected o [T,H,Dc] and w_uv [H,Dv,Dc]")
+    return _project(o, w_uv, False, w_uv.shape[1], w_uv.shape[2], 0, out, "latent_values")
+
+
+def latent_expand(kv_cache: torch.Tensor, w_uk: torch.Tensor, w_uv: torch.Tensor, block_table: torch.Tensor,
+                  kv_len: torch.Tensor, max_keys: int, *, k_scale: float = 1.0, k_out: Optional[torch.Tensor] = None,
+                  v_out: Optional[torch.Tensor] = None, places: Optional[torch.Tensor] = None):
+    """Keys and values of every head from cached latent rows kv_cache
+    [pages,page_size,1,Dc+Dr]: for the first kv_len[b] cached keys of each
+    sequence (at most max_keys), k [B,max_keys,H,Dn+Dr] = [w_uk[h] c | rope] and
+    v [B,max_keys,H,Dv] = w_uv[h] c, with w_uk [H,Dn,Dc] and w_uv [H,Dv,Dc]
+    (contiguous over Dc), rounded to the weights' type.  Rows behind kv_len and
+    keys without a page are left as they were.  places (int32 [B,max_keys]) gets
+    the block_table for caches of one key to a page, as which dcp_paged_attn
+    takes the two (dcp_latent_attn does it all).  Returns (k, v)."""
+    dev = _on_gpu(kv_cache, w_uk, w_uv, block_table, kv_len, k_out, v_out, places)
+    for t, name, nd in ((kv_cache, "kv_cache", 4), (w_uk, "w_uk", 3), (w_uv, "w_uv", 3)):
+        _rows(t, name, nd)
+    H, Dn, Dc = w_uk.shape
+    Dv, Dr = w_uv.shape[1], kv_cache.shape[3] - Dc
+    if w_uv.shape != (H, Dv, Dc) or w_uv.dtype != w_uk.dtype or kv_cache.shape[2] != 1 or Dr < 0:
+        raise ValueError("expected kv_cache [pages,page_size,1,Dc+Dr], w_uk [H,Dn,Dc] and w_uv [H,Dv,Dc] of one dtype")
+    dt, ct = _cache_types(w_uk.dtype, kv_cache)
+    B = kv_len.shape[0]
+    _ints(kv_len, "kv_len", (B,))
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [B, pages of a sequence]")
+    _ints(block_table, "block_table", (B, block_table.shape[1]))
+    _require(max_keys >= 0, "max_keys must not be negative")
+    if k_out is None:
+        k_out = torch.empty((B, max_keys, H, Dn + Dr), dtype=w_uk.dtype, device=w_uk.device)
+    if v_out is None:
+        v_out = torch.empty((B, max_keys, H, Dv), dtype=w_uk.dtype, device=w_uk.device)
+    _rows(k_out, "k_out", 4)
+    _rows(v_out, "v_out", 4)
+    if (k_out.shape != (B, max_keys, H, Dn + Dr) or v_out.shape != (B, max_keys, H, Dv) or k_out.dtype != w_uk.dtype or
+            v_out.dtype != w_uk.dtype):
+        raise ValueError("bad k_out or v_out tensor")
+    if places is not None:
+        _ints(places, "places", (B, max_keys))
+    cs, wk, wv, ks, vs = kv_cache.stride(), w_uk.stride(), w_uv.stride(), k_out.stride(), v_out.stride()
+    args = EXPAND_ARGS.pack(
+        kv_cache.data_ptr(), cs[0], cs[1], block_table.data_ptr(), block_table.stride(0), kv_len.data_ptr(),
+        w_uk.data_ptr(), wk[0], wk[1], w_uv.data_ptr(), wv[0], wv[1], k_out.data_ptr(), ks[0], ks[1], ks[2],
+        v_out.data_ptr(), vs[0], vs[1], vs[2], places.data_ptr() if places is not None else 0,
+        places.stride(0) if places is not None else 0, B, H, Dn, Dr, Dv, Dc, max_keys, kv_cache.shape[0],
+        kv_cache.shape[1], block_table.shape[1], dt, ct, k_scale)
+    _call(lib().dcpa_latent_expand, "dcpa_latent_expand", dev, args)
+    return k_out, v_out
+
+
+def dcp_latent_attn(q: torch.Tensor, kv_cache: torch.Tensor, w_uk: torch.Tensor, w_uv: torch.Tensor,
+                    block_table: torch.Tensor, cu_q: torch.Tensor, kv_len: torch.Tensor, max_keys: int, *,
+                    seq_len: Optional[torch.Tensor] = None, scale: Optional[float] = None, rank: int = 0,
+                    n_ranks: int = 1, interleave: int = 1, causal: bool = True, k_scale: float = 1.0,
+                    is_lse_base_on_e: bool = True, wide_weights: bool = False, out: Optional[torch.Tensor] = None,
+                    out_lse: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                    v_out: Optional[torch.Tensor] = None, places: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None):
+    """Latent attention in the expanded form: keys and values of every head are
+    made from the rank's cached latent rows (latent_expand), and the new tokens'
+    queries q [T,H,Dn+Dr], as the model has them (rotated, not taken into latent
+    space), attend to those.  For prompt chunks: a pair of query and key costs
+    Dn + Dr + Dv products instead of the latent form's 2 Dc + Dr, a key H (Dn + Dv)
+    Dc more.  max_keys: as many keys as a sequence may have cached here at most;
+    kv_len is clamped to it.  k_out, v_out (contiguous) and places are buffers to keep
+    them in, fresh ones if not given.  The other arguments are those of
+    dcp_paged_attn.  Returns (out [T,H,Dv], lse [T,H])."""
+    B, (H, Dn, _), Dv = kv_len.shape[0], w_uk.shape, w_uv.shape[1]
+    Dk = Dn + kv_cache.shape[3] - w_uk.shape[2]
+    for t, name in ((k_out, "k_out"), (v_out, "v_out"), (places, "places")):
+        if t is not None and not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+    if q.dim() != 3 or q.shape[1:] != (H, Dk) or q.dtype != w_uk.dtype:
+        raise ValueError("expected q [T,H,Dn+Dr] of the weights' dtype")
+    if places is None:
+        places = torch.empty((B, max_keys), dtype=torch.int32, device=q.device)
+    k, v = latent_expand(kv_cache, w_uk, w_uv, block_table, kv_len, max_keys, k_scale=k_scale, k_out=k_out, v_out=v_out,
+                         places=places)
+    return dcp_paged_attn(q, k.view(B * max_keys, 1, H, Dk), v.view(B * max_keys, 1, H, Dv), places, cu_q, kv_len,
+                          seq_len=seq_len, scale=scale, rank=rank, n_ranks=n_ranks, interleave=interleave, causal=causal,
+                          is_lse_base_on_e=is_lse_base_on_e, wide_weights=wide_weights, out=out, out_lse=out_lse,
+                          workspace=workspace)
 
 
 class BatchPlan(NamedTuple):

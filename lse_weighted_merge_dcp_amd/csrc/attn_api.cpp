@@ -431,4 +431,84 @@ int dcpa_batch_plan(const dcpa_plan_args* a, void* stream) {
     return status(launch_plan(k, (hipStream_t)stream));
 }
 
+int dcpa_project(const dcpa_project_args* a, void* stream) {
+    if (a == nullptr) return DCP_ERR_NULL;
+    if (a->dtype != DCP_F16 && a->dtype != DCP_BF16) return DCP_ERR_DTYPE;
+    auto cols = [](int64_t d) { return d >= 8 && d % 8 == 0 && d <= 1024; };
+    if (a->T < 0 || a->T > kMaxRows || a->H < 1 || a->H > (1 << 16) || a->T * a->H > kMaxRows || !cols(a->N) ||
+        !cols(a->K) || (a->copy != 0 && !cols(a->copy)) || project_workgroups(a->T, a->H, a->N) > kMaxGrid)
+        return DCP_ERR_SHAPE;
+    const bool turned = a->w_N == 1;
+    if (!strides_ok({a->x_T, a->x_H, a->w_H, a->w_N, a->w_K, a->y_T, a->y_H}) || (!turned && a->w_K != 1) ||
+        !span_ok({{a->T, a->x_T}, {a->H, a->x_H}, {a->K + a->copy, 1}}, 2) ||
+        !span_ok({{a->T, a->y_T}, {a->H, a->y_H}, {a->N + a->copy, 1}}, 2) ||
+        !span_ok({{a->H, a->w_H}, {a->N, a->w_N}, {a->K, a->w_K}}, 2))
+        return DCP_ERR_STRIDE;
+    if (a->T == 0) return DCP_OK;
+    if (!a->x || !a->w || !a->y) return DCP_ERR_NULL;
+    if (!aligned(a->x, 16) || !aligned(a->w, 16) || !aligned(a->y, 16) ||
+        !multiples({a->x_T, a->x_H, a->w_H, turned ? a->w_K : a->w_N, a->y_T, a->y_H}, 8))
+        return DCP_ERR_ALIGN;
+    ProjectArgs k;
+    k.x = (const char*)a->x; k.w = (const char*)a->w; k.y = (char*)a->y;
+    k.x_T = a->x_T * 2; k.x_H = a->x_H * 2;
+    k.w_H = a->w_H * 2; k.w_N = a->w_N * 2; k.w_K = a->w_K * 2;
+    k.y_T = a->y_T * 2; k.y_H = a->y_H * 2;
+    k.T = (int32_t)a->T; k.H = (int32_t)a->H; k.N = (int32_t)a->N; k.K = (int32_t)a->K; k.copy = (int32_t)a->copy;
+    k.fH = dcp::make_fastdiv((uint32_t)a->H);
+    return status(launch_project(k, turned, a->dtype == DCP_BF16, (hipStream_t)stream));
+}
+
+int dcpa_latent_expand(const dcpa_expand_args* a, void* stream) {
+    if (a == nullptr) return DCP_ERR_NULL;
+    if (a->dtype != DCP_F16 && a->dtype != DCP_BF16) return DCP_ERR_DTYPE;
+    if (a->cache_dtype != a->dtype && a->cache_dtype != DCP_FP8_E4M3) return DCP_ERR_DTYPE;
+    auto cols = [](int64_t d) { return d >= 8 && d % 8 == 0 && d <= 512; };
+    if (a->B < 0 || a->B > (int64_t(1) << 20) || a->H < 1 || a->H > (1 << 16) || !cols(a->Dn) || !cols(a->Dv) ||
+        a->Dr < 0 || a->Dr % 8 != 0 || a->Dc < 8 || a->Dc % 8 != 0 || a->Dr > 576 || a->Dc > 576 || a->Dc + a->Dr > 576 ||
+        a->max_keys < 0 || a->max_keys >= kMaxRows || a->B * a->max_keys >= kMaxRows ||
+        !cache_shape_ok(a->num_pages, a->page_size, a->max_pages))
+        return DCP_ERR_SHAPE;
+    const int64_t named = a->max_pages * a->page_size, keys = a->max_keys < named ? a->max_keys : named;
+    if (expand_workgroups(a->B, a->max_keys, a->H, a->Dn + a->Dv) > kMaxGrid / 2) return DCP_ERR_SHAPE;
+    if (!positive(a->k_scale)) return DCPA_ERR_VALUE;
+    const int ec = esize_of(a->cache_dtype);
+    if (!strides_ok({a->c_P, a->c_S, a->t_B, a->wk_H, a->wk_N, a->wv_H, a->wv_N, a->k_B, a->k_S, a->k_H, a->v_B, a->v_S,
+                     a->v_H, a->p_B}) ||
+        !span_ok({{a->num_pages, a->c_P}, {a->page_size, a->c_S}, {a->Dc + a->Dr, 1}}, ec) ||
+        !span_ok({{a->B, a->t_B}, {a->max_pages, 1}}, 4) || !span_ok({{a->B, a->p_B}, {a->max_keys, 1}}, 4) ||
+        !span_ok({{a->H, a->wk_H}, {a->Dn, a->wk_N}, {a->Dc, 1}}, 2) ||
+        !span_ok({{a->H, a->wv_H}, {a->Dv, a->wv_N}, {a->Dc, 1}}, 2) ||
+        !span_ok({{a->B, a->k_B}, {a->max_keys, a->k_S}, {a->H, a->k_H}, {a->Dn + a->Dr, 1}}, 2) ||
+        !span_ok({{a->B, a->v_B}, {a->max_keys, a->v_S}, {a->H, a->v_H}, {a->Dv, 1}}, 2))
+        return DCP_ERR_STRIDE;
+    if (a->B == 0 || a->max_keys == 0) return DCP_OK;
+    if ((a->max_pages > 0 && !a->block_table) || !a->kv_len || !a->w_k || !a->w_v || !a->k || !a->v || (a->num_pages > 0 && !a->cache))
+        return DCP_ERR_NULL;
+    for (const void* x : {a->cache, a->w_k, a->w_v, (const void*)a->k, (const void*)a->v})
+        if (!aligned(x, 16)) return DCP_ERR_ALIGN;
+    if (!multiples({a->c_P, a->c_S, a->wk_H, a->wk_N, a->wv_H, a->wv_N, a->k_B, a->k_S, a->k_H, a->v_B, a->v_S, a->v_H}, 8) ||
+        !aligned(a->block_table, 4) || !aligned(a->kv_len, 4) || !aligned(a->places, 4))
+        return DCP_ERR_ALIGN;
+    ExpandArgs k;
+    k.cache = (const char*)a->cache;
+    k.c_P = a->c_P * ec; k.c_S = a->c_S * ec;
+    k.table = a->block_table; k.kv = a->kv_len;
+    k.t_B = a->t_B;
+    k.wk = (const char*)a->w_k; k.wv = (const char*)a->w_v;
+    k.wk_H = a->wk_H * 2; k.wk_N = a->wk_N * 2; k.wv_H = a->wv_H * 2; k.wv_N = a->wv_N * 2;
+    k.ko = (char*)a->k; k.vo = (char*)a->v;
+    k.ko_B = a->k_B * 2; k.ko_S = a->k_S * 2; k.ko_H = a->k_H * 2;
+    k.vo_B = a->v_B * 2; k.vo_S = a->v_S * 2; k.vo_H = a->v_H * 2;
+    k.places = a->places;
+    k.pl_B = a->p_B;
+    k.B = (int32_t)a->B; k.H = (int32_t)a->H;
+    k.Dn = (int32_t)a->Dn; k.Dr = (int32_t)a->Dr; k.Dv = (int32_t)a->Dv; k.Dc = (int32_t)a->Dc;
+    k.most = (int32_t)a->max_keys; k.keys = (int32_t)keys; k.pages = (int32_t)a->num_pages;
+    k.fpage = dcp::make_fastdiv((uint32_t)a->page_size);
+    k.fper = dcp::make_fastdiv((uint32_t)(a->Dn + a->Dv));
+    k.ks = (float)a->k_scale;
+    return status(launch_expand(k, a->dtype == DCP_BF16, a->cache_dtype == DCP_FP8_E4M3, (hipStream_t)stream));
+}
+
 }  // extern "C"

@@ -154,6 +154,40 @@ struct PlanArgs {
 };
 hipError_t launch_plan(const PlanArgs& a, hipStream_t stream);
 
+// y[t, h] = x[t, h] W[h], and columns that are copied.
+struct ProjectArgs {
+    const char *x, *w;
+    char* y;
+    int64_t x_T, x_H, w_H, w_N, w_K, y_T, y_H;
+    int32_t T, H, N, K, copy;
+    int32_t mt;              // row tiles
+    FastDiv fH, fnt;         // fnt: column tiles
+};
+// turned: the weights of a head lie as [K][N] (else as [N][K]).
+hipError_t launch_project(const ProjectArgs& a, bool turned, bool bf16, hipStream_t stream);
+int64_t project_workgroups(int64_t T, int64_t H, int64_t N);
+
+struct ExpandArgs {
+    const char* cache;
+    int64_t c_P, c_S;
+    const int32_t* table;
+    int64_t t_B;
+    const int32_t* kv;
+    const char *wk, *wv;
+    int64_t wk_H, wk_N, wv_H, wv_N;
+    char *ko, *vo;
+    int64_t ko_B, ko_S, ko_H, vo_B, vo_S, vo_H;
+    int32_t* places;         // nullable
+    int64_t pl_B;
+    int32_t B, H, Dn, Dr, Dv, Dc;
+    int32_t most, keys;      // rows of the outputs; of these, what the page table can name
+    int32_t pages, mt, nt;   // row and column tiles
+    FastDiv fpage, fper;     // fper: Dn + Dv
+    float ks;
+};
+hipError_t launch_expand(const ExpandArgs& a, bool bf16, bool x8, hipStream_t stream);
+int64_t expand_workgroups(int64_t B, int64_t most, int64_t H, int64_t per);
+
 // Launch kernel(arg) and return that launch's own status.
 template <typename Arg>
 inline hipError_t launch(void (*kernel)(Arg), dim3 grid, dim3 block, hipStream_t stream, const Arg& arg) {
