@@ -11,6 +11,8 @@ PyTorch fallback.
                         keys and values into its paged cache
   dcp_paged_attn        attention of new tokens over the rank's cache: the
                         partial output and LSE that ops.dcp_pack_a2a_send takes
+  dcp_prefix_attn       the same for a batch whose sequences share the first keys
+                        of their caches, which are read once for a group
   dcp_attn_mass         accumulate the attention weight of every cached key
                         from the LSE that ops.dcp_lse_combine returns
   dcp_cache_evict       keep the keys of highest accumulated weight
@@ -55,6 +57,8 @@ SIGNATURES = {
     "dcpa_attn_mass_workspace": ([_CP], _I64),
     "dcpa_cache_evict": ([_CP, _VP], ctypes.c_int),
     "dcpa_batch_plan": ([_CP, _VP], ctypes.c_int),
+    "dcpa_prefix_attn": ([_CP, _VP, _VP, _I64, _VP], ctypes.c_int),
+    "dcpa_prefix_attn_workspace": ([_CP, _I64], _I64),
     "dcpa_project": ([_CP, _VP], ctypes.c_int),
     "dcpa_latent_expand": ([_CP, _VP], ctypes.c_int),
 }
@@ -258,27 +262,8 @@ def _with_workspace(args: bytes, query, name: str, workspace: Optional[torch.Ten
     return args[:_WS_AT] + w + args[_WS_AT + 16:], workspace
 
 
-def dcp_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional[torch.Tensor],
-                   block_table: torch.Tensor, cu_q: torch.Tensor, kv_len: torch.Tensor, *,
-                   seq_len: Optional[torch.Tensor] = None, scale: Optional[float] = None, v_dim: Optional[int] = None,
-                   rank: int = 0, n_ranks: int = 1, interleave: int = 1, causal: bool = True, k_scale: float = 1.0,
-                   v_scale: float = 1.0, is_lse_base_on_e: bool = True, wide_weights: bool = False,
-                   out: Optional[torch.Tensor] = None, out_lse: Optional[torch.Tensor] = None,
-                   workspace: Optional[torch.Tensor] = None):
-    """Attention of the new tokens q [T,Hq,Dk] over this rank's paged cache:
-    k_cache [pages,page_size,Hkv,Dk], v_cache [pages,page_size,Hkv,Dv], or None
-    with v_dim = Dv: values are the first Dv columns of the keys.  Sequence b's
-    tokens are rows cu_q[b]..cu_q[b+1]-1 (int32 [B+1]), its cached keys the
-    first kv_len[b] places of the pages block_table[b] (int32), this step's own
-    keys among them; seq_len[b] is its whole length over all ranks (needed if
-    causal and n_ranks > 1).  Returns (out [T,Hq,Dv], lse [T,Hq] fp32), which
-    ops.dcp_pack_a2a_send takes; a token that sees no key on this rank gets the
-    neutral pair (0, -inf).  Rows outside the sequences are left as they were.
-    scale defaults to Dk ** -0.5.  The weights are rounded to q's type for the
-    product with the values; with wide_weights what the rounding leaves takes a
-    second product (1.2 to 1.4 times as long for many or latent rows; few rows
-    have it always)."""
-    dev = _on_gpu(q, k_cache, v_cache, block_table, cu_q, kv_len, seq_len, out, out_lse, workspace)
+def _attn_outputs(q, k_cache, v_cache, v_dim, out, out_lse):
+    """The checked shapes of an attention call: (Dv, out, out_lse), allocated where they are not given."""
     _rows(q, "q", 3)
     _rows(k_cache, "k_cache", 4)
     T, Hq, Dk = q.shape
@@ -300,11 +285,64 @@ def dcp_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional[tor
         raise ValueError("bad out tensor")
     if out_lse.shape != (T, Hq) or out_lse.dtype != torch.float32:
         raise ValueError("bad out_lse tensor")
+    return Dv, out, out_lse
+
+
+def dcp_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional[torch.Tensor],
+                   block_table: torch.Tensor, cu_q: torch.Tensor, kv_len: torch.Tensor, *,
+                   seq_len: Optional[torch.Tensor] = None, scale: Optional[float] = None, v_dim: Optional[int] = None,
+                   rank: int = 0, n_ranks: int = 1, interleave: int = 1, causal: bool = True, k_scale: float = 1.0,
+                   v_scale: float = 1.0, is_lse_base_on_e: bool = True, wide_weights: bool = False,
+                   out: Optional[torch.Tensor] = None, out_lse: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None):
+    """Attention of the new tokens q [T,Hq,Dk] over this rank's paged cache:
+    k_cache [pages,page_size,Hkv,Dk], v_cache [pages,page_size,Hkv,Dv], or None
+    with v_dim = Dv: values are the first Dv columns of the keys.  Sequence b's
+    tokens are rows cu_q[b]..cu_q[b+1]-1 (int32 [B+1]), its cached keys the
+    first kv_len[b] places of the pages block_table[b] (int32), this step's own
+    keys among them; seq_len[b] is its whole length over all ranks (needed if
+    causal and n_ranks > 1).  Returns (out [T,Hq,Dv], lse [T,Hq] fp32), which
+    ops.dcp_pack_a2a_send takes; a token that sees no key on this rank gets the
+    neutral pair (0, -inf).  Rows outside the sequences are left as they were.
+    scale defaults to Dk ** -0.5.  The weights are rounded to q's type for the
+    product with the values; with wide_weights what the rounding leaves takes a
+    second product (1.2 to 1.4 times as long for many or latent rows; few rows
+    have it always)."""
+    dev = _on_gpu(q, k_cache, v_cache, block_table, cu_q, kv_len, seq_len, out, out_lse, workspace)
+    Dv, out, out_lse = _attn_outputs(q, k_cache, v_cache, v_dim, out, out_lse)
     h = lib()
     args = _attn_args(q, k_cache, v_cache, block_table, cu_q, kv_len, seq_len, scale, Dv, rank, n_ranks, interleave,
                       causal, k_scale, v_scale, is_lse_base_on_e, wide_weights, out, out_lse, 0, 0)
     args, _keep = _with_workspace(args, h.dcpa_paged_attn_workspace, "dcpa_paged_attn", workspace, q)
     _call(h.dcpa_paged_attn, "dcpa_paged_attn", dev, args)
+    return out, out_lse
+
+
+def dcp_prefix_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional[torch.Tensor],
+                    block_table: torch.Tensor, cu_q: torch.Tensor, kv_len: torch.Tensor, cu_group: torch.Tensor,
+                    shared_len: torch.Tensor, *, seq_len: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                    v_dim: Optional[int] = None, rank: int = 0, n_ranks: int = 1, interleave: int = 1,
+                    causal: bool = True, k_scale: float = 1.0, v_scale: float = 1.0, is_lse_base_on_e: bool = True,
+                    wide_weights: bool = False, out: Optional[torch.Tensor] = None,
+                    out_lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """dcp_paged_attn for a batch whose sequences share the first keys of their
+    caches (a common system prompt or document): the same result, with the shared
+    keys read once for all rows of a group.  Group g is the sequences
+    cu_group[g]..cu_group[g+1]-1 (int32 [groups+1]); the first shared_len[g]
+    (int32 [groups]) cached keys of each of them on this rank are the same: whole
+    pages that stand in all their rows of block_table.  Sequences outside the
+    groups share nothing.  Returns (out [T,Hq,Dv], lse [T,Hq] fp32).  The weights
+    are rounded to q's type for the product with the values, unless wide_weights."""
+    dev = _on_gpu(q, k_cache, v_cache, block_table, cu_q, kv_len, seq_len, cu_group, shared_len, out, out_lse, workspace)
+    Dv, out, out_lse = _attn_outputs(q, k_cache, v_cache, v_dim, out, out_lse)
+    groups = shared_len.shape[0] if shared_len.dim() == 1 else -1
+    _ints(shared_len, "shared_len", (groups,))
+    _ints(cu_group, "cu_group", (groups + 1,))
+    h = lib()
+    args = _attn_args(q, k_cache, v_cache, block_table, cu_q, kv_len, seq_len, scale, Dv, rank, n_ranks, interleave,
+                      causal, k_scale, v_scale, is_lse_base_on_e, wide_weights, out, out_lse, 0, 0)
+    args, _keep = _with_workspace(args, lambda a: h.dcpa_prefix_attn_workspace(a, groups), "dcpa_prefix_attn", workspace, q)
+    _call(h.dcpa_prefix_attn, "dcpa_prefix_attn", dev, args, cu_group.data_ptr(), shared_len.data_ptr(), groups)
     return out, out_lse
 
 

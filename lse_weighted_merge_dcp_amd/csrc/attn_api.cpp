@@ -126,7 +126,7 @@ int check_inputs(const dcpa_attn_args* a) {
     return DCP_OK;
 }
 
-int check_attn(const dcpa_attn_args* a, Batch& m) {
+int check_shapes(const dcpa_attn_args* a, Batch& m) {
     if (int st = check_batch(a, m)) return st;
     const bool shared = a->v == nullptr;
     if (a->Dv < 8 || a->Dv % 8 != 0 || a->Dv > 512) return DCP_ERR_SHAPE;
@@ -136,8 +136,58 @@ int check_attn(const dcpa_attn_args* a, Batch& m) {
                  esize_of(a->cache_dtype)) ||
         !span_ok({{a->T, a->o_T}, {a->Hq, a->o_H}, {a->Dv, 1}}, 2))
         return DCP_ERR_STRIDE;
-    const AttnPlan pl = plan_of(a, m);
-    if (((int64_t)pl.units + 7) * m.Hkv > kMaxGrid || (pl.slots > 0 && a->T * a->Hq / 4 >= kMaxGrid)) return DCP_ERR_SHAPE;
+    return DCP_OK;
+}
+// No more workgroups than a launch may have, those that join rows among them.
+bool grid_ok(const dcpa_attn_args* a, const AttnPlan& pl, const Batch& m) {
+    return ((int64_t)pl.units + 7) * m.Hkv <= kMaxGrid && (pl.slots == 0 || a->T * a->Hq / 4 < kMaxGrid);
+}
+int check_attn(const dcpa_attn_args* a, Batch& m) {
+    if (int st = check_shapes(a, m)) return st;
+    return grid_ok(a, plan_of(a, m), m) ? DCP_OK : DCP_ERR_SHAPE;
+}
+int check_prefix(const dcpa_attn_args* a, int64_t groups, Batch& m, AttnPlan& pl) {
+    if (int st = check_shapes(a, m)) return st;
+    if (groups < 0 || groups > (int64_t(1) << 20)) return DCP_ERR_SHAPE;
+    pl = plan_prefix(m, groups, (int)a->Dk, (int)a->Dv);
+    return grid_ok(a, pl, m) ? DCP_OK : DCP_ERR_SHAPE;
+}
+
+// Alignment of what the attention calls write, and of the values.
+int check_outputs(const dcpa_attn_args* a) {
+    if (!a->out) return DCP_ERR_NULL;
+    if (!aligned(a->v, 16) || (a->v && !multiples({a->v_P, a->v_S, a->v_H}, 8)) || !aligned(a->out, 4) ||
+        !multiples({a->o_T, a->o_H}, 2))
+        return DCP_ERR_ALIGN;
+    return DCP_OK;
+}
+// The arguments of the attention kernels (m is there already).
+int fill_attn(const dcpa_attn_args* a, const AttnPlan& pl, AttnArgs& k) {
+    const int ec = esize_of(a->cache_dtype);
+    if (pl.ws_bytes > 0 && (!a->workspace || a->workspace_bytes < pl.ws_bytes || !aligned(a->workspace, 16)))
+        return DCPA_ERR_WORKSPACE;
+    k.q = (const char*)a->q;
+    k.q_T = a->q_T * 2; k.q_H = a->q_H * 2;
+    k.k = (const char*)a->k;
+    k.k_P = a->k_P * ec; k.k_S = a->k_S * ec; k.k_H = a->k_H * ec;
+    k.v = (const char*)a->v;
+    k.v_P = a->v_P * ec; k.v_S = a->v_S * ec; k.v_H = a->v_H * ec;
+    k.out = (char*)a->out;
+    k.o_T = a->o_T * 2; k.o_H = a->o_H * 2;
+    k.lse = a->lse;
+    k.l_T = a->l_T; k.l_H = a->l_H;
+    k.Dk = (int32_t)a->Dk;
+    k.Dv = (int32_t)a->Dv;
+    k.rows = pl.rows;
+    k.slots = pl.slots;
+    k.share = pl.share;
+    k.units = pl.units;
+    k.ws_o = (float*)a->workspace;
+    k.ws_l = k.ws_o == nullptr ? nullptr : k.ws_o + (int64_t)pl.units * k.m.Hkv * pl.rows * a->Dv;
+    k.c = (float)(a->scale * a->k_scale * 1.4426950408889634);
+    // (in the latent layout the values are the keys' own columns)
+    k.vs = (float)(a->v ? a->v_scale : a->k_scale);
+    k.lmul = a->lse_base == DCP_LSE_BASE_E ? kLn2 : 1.0f;
     return DCP_OK;
 }
 
@@ -183,38 +233,38 @@ int dcpa_paged_attn(const dcpa_attn_args* a, void* stream) {
     if (int st = check_attn(a, k.m)) return st;
     if (a->B == 0 || a->T == 0) return DCP_OK;
     if (int st = check_inputs(a)) return st;
-    if (!a->out) return DCP_ERR_NULL;
-    const int ec = esize_of(a->cache_dtype);
-    if (!aligned(a->v, 16) || (a->v && !multiples({a->v_P, a->v_S, a->v_H}, 8)) || !aligned(a->out, 4) ||
-        !multiples({a->o_T, a->o_H}, 2))
-        return DCP_ERR_ALIGN;
+    if (int st = check_outputs(a)) return st;
     const AttnPlan pl = plan_of(a, k.m);
-    if (pl.ws_bytes > 0 && (!a->workspace || a->workspace_bytes < pl.ws_bytes || !aligned(a->workspace, 16)))
-        return DCPA_ERR_WORKSPACE;
-    k.q = (const char*)a->q;
-    k.q_T = a->q_T * 2; k.q_H = a->q_H * 2;
-    k.k = (const char*)a->k;
-    k.k_P = a->k_P * ec; k.k_S = a->k_S * ec; k.k_H = a->k_H * ec;
-    k.v = (const char*)a->v;
-    k.v_P = a->v_P * ec; k.v_S = a->v_S * ec; k.v_H = a->v_H * ec;
-    k.out = (char*)a->out;
-    k.o_T = a->o_T * 2; k.o_H = a->o_H * 2;
-    k.lse = a->lse;
-    k.l_T = a->l_T; k.l_H = a->l_H;
-    k.Dk = (int32_t)a->Dk;
-    k.Dv = (int32_t)a->Dv;
-    k.rows = pl.rows;
-    k.slots = pl.slots;
-    k.share = pl.share;
-    k.units = pl.units;
-    k.ws_o = (float*)a->workspace;
-    k.ws_l = k.ws_o == nullptr ? nullptr : k.ws_o + (int64_t)pl.units * k.m.Hkv * pl.rows * a->Dv;
-    k.c = (float)(a->scale * a->k_scale * 1.4426950408889634);
-    // (in the latent layout the values are the keys' own columns)
-    k.vs = (float)(a->v ? a->v_scale : a->k_scale);
-    k.lmul = a->lse_base == DCP_LSE_BASE_E ? kLn2 : 1.0f;
+    if (int st = fill_attn(a, pl, k)) return st;
     return status(launch_attn(k, pl, a->dtype == DCP_BF16, a->cache_dtype == DCP_FP8_E4M3, a->wide_weights != 0,
                               (hipStream_t)stream));
+}
+
+int64_t dcpa_prefix_attn_workspace(const dcpa_attn_args* a, int64_t n_groups) {
+    if (a == nullptr) return DCP_ERR_NULL;
+    Batch m;
+    AttnPlan pl;
+    if (int st = check_prefix(a, n_groups, m, pl)) return st;
+    return a->B == 0 || a->T == 0 ? 0 : pl.ws_bytes;
+}
+
+int dcpa_prefix_attn(const dcpa_attn_args* a, const int32_t* cu_group, const int32_t* shared_len, int64_t n_groups,
+                     void* stream) {
+    if (a == nullptr) return DCP_ERR_NULL;
+    GroupArgs k;
+    AttnPlan pl;
+    if (int st = check_prefix(a, n_groups, k.m, pl)) return st;
+    if (a->B == 0 || a->T == 0) return DCP_OK;
+    if (int st = check_inputs(a)) return st;
+    if (n_groups > 0 && (!cu_group || !shared_len)) return DCP_ERR_NULL;
+    if (!aligned(cu_group, 4) || !aligned(shared_len, 4)) return DCP_ERR_ALIGN;
+    if (int st = check_outputs(a)) return st;
+    if (int st = fill_attn(a, pl, k)) return st;
+    k.cug = cu_group;
+    k.same = shared_len;
+    k.groups = (int32_t)n_groups;
+    return status(launch_prefix(k, pl.latent, a->dtype == DCP_BF16, a->cache_dtype == DCP_FP8_E4M3, a->wide_weights != 0,
+                                (hipStream_t)stream));
 }
 
 int64_t dcpa_attn_mass_workspace(const dcpa_attn_args* a) {

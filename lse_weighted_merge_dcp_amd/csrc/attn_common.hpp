@@ -68,8 +68,8 @@ __device__ __forceinline__ void write_rows(const AttnArgs& p, const Unit& u, con
 // it (values that are not finite in a masked tile).  A call of its own, with
 // its own copies of the arguments: a reference to the kernel's would move them
 // from scalar registers to memory for the whole kernel.
-template <typename E, bool KV8, int DK, int DV>
-__device__ __noinline__ void slow_rows(AttnArgs p, Unit u, int hk, int unit, int tile_rows, int row0,
+template <typename E, bool KV8, int DK, int DV, typename A, typename U>
+__device__ __noinline__ void slow_rows(A p, U u, int hk, int unit, int tile_rows, int row0,
                                        int first, int end, int k0, int k1) {
     const int lane = threadIdx.x & 63;
     constexpr int NQ = (DK + 63) / 64, NO = (DV + 63) / 64, ES = KV8 ? 1 : 2;
@@ -84,7 +84,7 @@ __device__ __noinline__ void slow_rows(AttnArgs p, Unit u, int hk, int unit, int
 #pragma unroll 1
     for (int row = first; row < end; ++row) {
         const int token = (int)fdiv((uint32_t)row, p.m.fG), head = hk * p.m.G + row - token * p.m.G;
-        const int stop = min(k1, visible(p.m, u.s, token));
+        const int stop = min(k1, sees(p, u, token));
         const char* q = p.q + (int64_t)(u.s.first + token) * p.q_T + (int64_t)head * p.q_H;
         float x[NQ], acc[NO], mc = kNoMax, l = 0.0f;
 #pragma unroll

@@ -357,4 +357,20 @@ __device__ __forceinline__ Unit find_unit(const Batch& m, int rows, int slots, i
     return u;
 }
 
+// How a workgroup finds its share, and what its rows see, by the arguments of the
+// kernel (attn_prefix.hpp has them for sequences that share keys).
+template <int STEP> __device__ __forceinline__ Unit unit_of(const AttnArgs& p, int rows, int id) {
+    return find_unit<STEP>(p.m, rows, p.slots, p.share, id);
+}
+__device__ __forceinline__ int first_key(const Unit&) { return 0; }
+// one behind the last key that a row of the tile sees; last_row: the tile's last
+__device__ __forceinline__ int last_key(const AttnArgs& p, const Unit& u, int last_row) {
+    return visible(p.m, u.s, (int)fdiv((uint32_t)last_row, p.m.fG));
+}
+__device__ __forceinline__ int sees(const AttnArgs& p, const Unit& u, int token) { return visible(p.m, u.s, token); }
+// The least and the most of the lanes' `vis` (32 rows, twice): rows are in the order of their tokens, the
+// first sees least, the last most.
+__device__ __forceinline__ int least_seen(const Unit&, int vis) { return __builtin_amdgcn_readlane(vis, 0); }
+__device__ __forceinline__ int most_seen(const Unit&, int vis) { return __builtin_amdgcn_readlane(vis, 31); }
+
 }  // namespace dcpa

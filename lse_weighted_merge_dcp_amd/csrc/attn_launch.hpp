@@ -78,6 +78,15 @@ hipError_t launch_attn(const AttnArgs& a, const AttnPlan& pl, bool bf16, bool kv
 
 hipError_t launch_latent(const AttnArgs& a, dim3 grid, bool bf16, bool kv8, bool wide, hipStream_t stream);
 
+// Attention of sequences that share their first keys, group by group.
+struct GroupArgs : AttnArgs {
+    const int32_t* cug;      // [groups + 1]: sequences
+    const int32_t* same;     // [groups]: shared keys
+    int32_t groups;
+};
+AttnPlan plan_prefix(const Batch& m, int64_t groups, int Dk, int Dv);
+hipError_t launch_prefix(const GroupArgs& a, bool latent, bool bf16, bool kv8, bool wide, hipStream_t stream);
+
 struct MassArgs {
     Batch m;
     const char* q;
