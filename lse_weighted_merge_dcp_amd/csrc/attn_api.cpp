@@ -108,11 +108,11 @@ int check_batch(const dcpa_attn_args* a, Batch& m) {
 bool key_pieces(const dcpa_attn_args* a) {
     return a->cache_dtype != DCP_FP8_E4M3 || multiples({a->Dk, a->k_P, a->k_S, a->k_H}, 16);
 }
-AttnPlan plan_of(const dcpa_attn_args* a, const Batch& m) {
-    const bool values = a->cache_dtype != DCP_FP8_E4M3 ||
-                        (a->Dv % 16 == 0 && (!a->v || multiples({a->v_P, a->v_S, a->v_H}, 16)));
-    return plan_attn(m, (int)a->Dk, (int)a->Dv, key_pieces(a) && values);
+bool cache_pieces(const dcpa_attn_args* a) {
+    return key_pieces(a) && (a->cache_dtype != DCP_FP8_E4M3 ||
+                             (a->Dv % 16 == 0 && (!a->v || multiples({a->v_P, a->v_S, a->v_H}, 16))));
 }
+AttnPlan plan_of(const dcpa_attn_args* a, const Batch& m) { return plan_attn(m, (int)a->Dk, (int)a->Dv, cache_pieces(a)); }
 
 // Pointers and alignment of what both calls read.
 int check_inputs(const dcpa_attn_args* a) {
@@ -149,7 +149,7 @@ int check_attn(const dcpa_attn_args* a, Batch& m) {
 int check_prefix(const dcpa_attn_args* a, int64_t groups, Batch& m, AttnPlan& pl) {
     if (int st = check_shapes(a, m)) return st;
     if (groups < 0 || groups > (int64_t(1) << 20)) return DCP_ERR_SHAPE;
-    pl = plan_prefix(m, groups, (int)a->Dk, (int)a->Dv);
+    pl = plan_prefix(m, groups, (int)a->Dk, (int)a->Dv, cache_pieces(a));
     return grid_ok(a, pl, m) ? DCP_OK : DCP_ERR_SHAPE;
 }
 
@@ -161,8 +161,8 @@ int check_outputs(const dcpa_attn_args* a) {
         return DCP_ERR_ALIGN;
     return DCP_OK;
 }
-// The arguments of the attention kernels (m is there already).
-int fill_attn(const dcpa_attn_args* a, const AttnPlan& pl, AttnArgs& k) {
+// The arguments of the attention kernels (m is there already); lists: bytes of the workspace in front of the parts.
+int fill_attn(const dcpa_attn_args* a, const AttnPlan& pl, AttnArgs& k, int64_t lists = 0) {
     const int ec = esize_of(a->cache_dtype);
     if (pl.ws_bytes > 0 && (!a->workspace || a->workspace_bytes < pl.ws_bytes || !aligned(a->workspace, 16)))
         return DCPA_ERR_WORKSPACE;
@@ -182,8 +182,8 @@ int fill_attn(const dcpa_attn_args* a, const AttnPlan& pl, AttnArgs& k) {
     k.slots = pl.slots;
     k.share = pl.share;
     k.units = pl.units;
-    k.ws_o = (float*)a->workspace;
-    k.ws_l = k.ws_o == nullptr ? nullptr : k.ws_o + (int64_t)pl.units * k.m.Hkv * pl.rows * a->Dv;
+    k.ws_o = (float*)((char*)a->workspace + lists);
+    k.ws_l = a->workspace == nullptr ? nullptr : k.ws_o + (int64_t)pl.units * k.m.Hkv * pl.rows * a->Dv;
     k.c = (float)(a->scale * a->k_scale * 1.4426950408889634);
     // (in the latent layout the values are the keys' own columns)
     k.vs = (float)(a->v ? a->v_scale : a->k_scale);
@@ -259,10 +259,13 @@ int dcpa_prefix_attn(const dcpa_attn_args* a, const int32_t* cu_group, const int
     if (n_groups > 0 && (!cu_group || !shared_len)) return DCP_ERR_NULL;
     if (!aligned(cu_group, 4) || !aligned(shared_len, 4)) return DCP_ERR_ALIGN;
     if (int st = check_outputs(a)) return st;
-    if (int st = fill_attn(a, pl, k)) return st;
+    if (int st = fill_attn(a, pl, k, prefix_list_bytes(pl.units, n_groups + a->B))) return st;
+    k.list = (PrefixUnit*)a->workspace;
+    k.entries = (PrefixEntry*)(k.list + pl.units);
     k.cug = cu_group;
     k.same = shared_len;
     k.groups = (int32_t)n_groups;
+    k.own_rows = pl.by_keys ? 32 : pl.rows;
     return status(launch_prefix(k, pl.latent, a->dtype == DCP_BF16, a->cache_dtype == DCP_FP8_E4M3, a->wide_weights != 0,
                                 (hipStream_t)stream));
 }

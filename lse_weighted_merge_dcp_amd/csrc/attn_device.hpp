@@ -225,6 +225,20 @@ __device__ __forceinline__ int scan_incl(int x) {
     x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);    // lane 31 to rows 2 and 3
     return x;
 }
+// Sums that stop at `most` (<= 2^30): what a lane adds never passes 2^31.
+__device__ __forceinline__ int add_to(int a, int b, int most) { return (int)min((uint32_t)a + (uint32_t)b, (uint32_t)most); }
+template <int CTRL, int ROWS> __device__ __forceinline__ int scan_step(int x, int most) {
+    return add_to(x, __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, false), most);
+}
+// scan_incl() of such sums.
+__device__ __forceinline__ int scan_upto(int x, int most) {
+    x = scan_step<0x111, 0xf>(x, most);
+    x = scan_step<0x112, 0xf>(x, most);
+    x = scan_step<0x114, 0xf>(x, most);
+    x = scan_step<0x118, 0xf>(x, most);
+    x = scan_step<0x142, 0xa>(x, most);
+    return scan_step<0x143, 0xc>(x, most);
+}
 // x plus the x of the lane that CTRL names, over the rows of lanes in ROWS (each half moved as 32 bits)
 template <int CTRL, int ROWS> __device__ __forceinline__ double add_from(double x) {
     const uint64_t u = __builtin_bit_cast(uint64_t, x);

@@ -78,13 +78,31 @@ hipError_t launch_attn(const AttnArgs& a, const AttnPlan& pl, bool bf16, bool kv
 
 hipError_t launch_latent(const AttnArgs& a, dim3 grid, bool bf16, bool kv8, bool wide, hipStream_t stream);
 
-// Attention of sequences that share their first keys, group by group.
+// Attention of sequences that share their first keys, group by group.  Lists that
+// its first kernel leaves in the workspace: units of work, and where the units of
+// each group and then each sequence stand.
+struct PrefixUnit {
+    int32_t b;                           // table row
+    int32_t first, n, kv, len;           // rows and lengths (of the group: first row, rows, shared keys)
+    int32_t begin, end;                  // keys
+    int32_t tile, split, splits, chunk;
+    int32_t b0, b1;                      // sequences of a group (else none)
+    int32_t even;                        // all rows see all shared keys
+    int32_t unused[2];
+};
+struct PrefixEntry {
+    int32_t first, n, slot, splits, begin, kv, len, chunk;
+};
 struct GroupArgs : AttnArgs {
     const int32_t* cug;      // [groups + 1]: sequences
     const int32_t* same;     // [groups]: shared keys
-    int32_t groups;
+    PrefixUnit* list;        // [units]
+    PrefixEntry* entries;    // [groups + B]
+    int32_t groups, step;    // step: keys of a tile
+    int32_t own_rows;        // rows of a tile of a sequence against its own keys (`rows`, or 32 where they are few)
 };
-AttnPlan plan_prefix(const Batch& m, int64_t groups, int Dk, int Dv);
+int64_t prefix_list_bytes(int64_t units, int64_t entries);
+AttnPlan plan_prefix(const Batch& m, int64_t groups, int Dk, int Dv, bool pieces);
 hipError_t launch_prefix(const GroupArgs& a, bool latent, bool bf16, bool kv8, bool wide, hipStream_t stream);
 
 struct MassArgs {

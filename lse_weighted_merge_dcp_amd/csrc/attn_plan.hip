@@ -27,19 +27,9 @@ __device__ __forceinline__ int pages_for(const PlanArgs& p, int keys) {
     return (int)min(fdiv((uint32_t)keys + (uint32_t)p.page_size - 1u, p.fpage), (uint32_t)p.width);
 }
 
-// Sums that stop at `most` (<= 2^30): what a lane adds never passes 2^31.
-__device__ __forceinline__ int add_to(int a, int b, int most) { return (int)min((uint32_t)a + (uint32_t)b, (uint32_t)most); }
-template <int CTRL, int ROWS> __device__ __forceinline__ int scan_step(int x, int most) {
-    return add_to(x, __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, false), most);
-}
 // Inclusive sum over the workgroup; every thread gets the whole in `all`.
 __device__ __forceinline__ int scan_block(int x, int most, int& all, int (&wave_s)[kWaves]) {
-    x = scan_step<0x111, 0xf>(x, most);
-    x = scan_step<0x112, 0xf>(x, most);
-    x = scan_step<0x114, 0xf>(x, most);
-    x = scan_step<0x118, 0xf>(x, most);
-    x = scan_step<0x142, 0xa>(x, most);
-    x = scan_step<0x143, 0xc>(x, most);
+    x = scan_upto(x, most);
     const int wave = threadIdx.x >> 6;
     __syncthreads();                    // (the last call's sums have been read)
     if ((threadIdx.x & 63) == 63) wave_s[wave] = x;

@@ -4,9 +4,12 @@
 // The rows of all sequences of a group stand together, so against the shared
 // keys they are one long sequence: its row tiles take the shared keys once for
 // 128 rows of whichever sequences, and every sequence's own tiles take the keys
-// behind them.  Both are units of one launch of the kernels for many rows
-// (attn_rows.hpp, attn_latent.hpp), which differ only in how a workgroup finds
-// its share and in what a row sees; a row's parts are joined by a second kernel.
+// behind them.  Both are units of one launch, of the code that single sequences
+// run (attn_rows.hpp, attn_latent.hpp, attn_keys.hpp for a sequence's own keys where
+// rows are few), which differs only in how a workgroup finds its share and in what
+// a row sees: a list that a kernel of one workgroup has made.  A row's parts are
+// joined by a third kernel.
+#include "attn_keys.hpp"
 #include "attn_latent.hpp"
 #include "attn_rows.hpp"
 
@@ -20,132 +23,22 @@ struct GroupUnit : Unit {
     int b0, b1;     // the group's sequences (none: a sequence's own keys)
     bool even;      // every row of the group sees all shared keys
 };
-
-// Sequences of group g, and how many keys they share.
-struct Group {
-    int b0, b1, keys;
-};
-__device__ __forceinline__ Group load_group(const GroupArgs& p, int g) {
-    Group x;
-    x.b0 = min(max(p.cug[g], 0), p.m.B);
-    x.b1 = min(max(p.cug[g + 1], x.b0), p.m.B);
-    x.keys = x.b1 > x.b0 ? min(max(p.same[g], 0), p.m.max_keys) : 0;
-    return x;
-}
-// Keys that sequence b shares with its group.
-__device__ __forceinline__ int shared_of(const GroupArgs& p, int b) {
-    // the last group that starts at b or before it
-    int lo = 0, hi = p.groups - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.cug[mid] <= b) lo = mid;
-        else hi = mid - 1;
-    }
-    if (p.groups == 0) return 0;
-    const Group x = load_group(p, lo);
-    return b >= x.b0 && b < x.b1 ? x.keys : 0;
-}
-
-// Entry v of the list of groups and then sequences: rows, first key, keys from there on.
-struct Entry {
-    Seq s;
-    int begin, keys, tiles;
-};
-__device__ __forceinline__ Entry load_entry(const GroupArgs& p, int v, int rows) {
-    Entry x{};
-    if (v < p.groups) {
-        const Group y = load_group(p, v);
-        if (y.keys > 0) {
-            x.s.first = min(max(p.m.cu[y.b0], 0), p.m.T);
-            x.s.n = min(max(p.m.cu[y.b1], x.s.first), p.m.T) - x.s.first;
-            x.keys = x.s.kv = y.keys;
-        }
-    } else if (v < p.groups + p.m.B) {
-        x.s = load_seq(p.m, v - p.groups);
-        x.begin = shared_of(p, v - p.groups);
-        x.keys = max(x.s.kv - x.begin, 0);
-    }
-    x.tiles = (x.s.n * p.m.G + rows - 1) / rows;
-    return x;
-}
-
-// As key_chunk() and find_unit(), over that list.
-template <int STEP> __device__ __forceinline__ int group_chunk(const GroupArgs& p, int rows) {
-    if (p.slots <= 0) return kWhole;
-    const int lane = threadIdx.x & 63, all = p.groups + p.m.B;
-    int64_t work = 0;
-    int tiles = 0;
-    Entry x;
-    for (int v0 = 0; v0 < all; v0 += 64) {
-        x = load_entry(p, v0 + lane, rows);
-        work += (int64_t)x.tiles * x.keys;
-        tiles += x.tiles;
-    }
-    work = sum_wave(work);
-    tiles = (int)sum_wave((int64_t)tiles);
-    if (tiles >= p.slots) return kWhole;
-    auto steps = [](int64_t x) { return (int)min((int64_t)(kWhole / STEP), max((int64_t)2, (x + STEP - 1) / STEP)); };
-    int lo = steps((work + p.share - 1) / p.share), hi = max(lo, steps((work + p.slots - tiles - 1) / (p.slots - tiles)));
-#pragma unroll 1
-    for (int round = 0; round < 3 && lo < hi; ++round) {
-        const int mid = lo + (hi - lo) / 2;
-        int64_t units = 0;
-        for (int v0 = 0; v0 < all; v0 += 64) {
-            if (all > 64) x = load_entry(p, v0 + lane, rows);
-            units += (int64_t)x.tiles * max(1, (x.keys + mid * STEP - 1) / (mid * STEP));
-        }
-        units = sum_wave(units);
-        if (units <= p.slots) hi = mid;
-        else lo = mid + 1;
-    }
-    return hi * STEP;
-}
-
-template <int STEP> __device__ __forceinline__ GroupUnit unit_of(const GroupArgs& p, int rows, int id) {
+template <int STEP> __device__ __forceinline__ GroupUnit unit_of(const GroupArgs& p, int, int id) {
+    const PrefixUnit x = p.list[id];
     GroupUnit u;
-    u.ok = false;
-    u.chunk = group_chunk<STEP>(p, rows);
-    const int lane = threadIdx.x & 63;
-    int base = 0;
-    for (int v0 = 0; v0 < p.groups + p.m.B; v0 += 64) {
-        const Entry x = load_entry(p, v0 + lane, rows);
-        const int splits = max(1, (x.keys + u.chunk - 1) / u.chunk);
-        const int incl = base + scan_incl(x.tiles * splits);
-        const uint64_t past = __ballot(incl > id);
-        if (past != 0) {
-            const int at = __builtin_ctzll(past), v = v0 + at;
-            const int t = __builtin_amdgcn_readlane(x.tiles, at), s = __builtin_amdgcn_readlane(splits, at);
-            const int rest = id - (__builtin_amdgcn_readlane(incl, at) - t * s);
-            u.s = seq_of(x.s, at);
-            u.begin = __builtin_amdgcn_readlane(x.begin, at);
-            u.end = u.begin + __builtin_amdgcn_readlane(x.keys, at);
-            u.split = rest % s;
-            u.tile = t - 1 - rest / s;
-            u.slot = id - u.split;
-            u.ok = rest >= 0 && u.tile >= 0 && (int64_t)u.tile * rows < (int64_t)u.s.n * p.m.G;
-            u.b0 = u.b1 = 0;
-            u.even = true;
-            u.b = v - p.groups;
-            // (a row of a sequence that shares no keys and was not split has one part: it is written whole)
-            u.splits = u.begin > 0 ? max(s, 2) : s;
-            if (v < p.groups) {
-                const Group y = load_group(p, v);
-                u.b = u.b0 = y.b0;
-                u.b1 = y.b1;
-                u.splits = max(s, 2);
-                for (int b = y.b0; b < y.b1; b += 64) {
-                    bool all = true;
-                    if (b + lane < y.b1) {
-                        const Seq q = load_seq(p.m, b + lane);
-                        all = q.n == 0 || visible(p.m, q, 0) >= u.end;
-                    }
-                    if (__ballot(!all) != 0) u.even = false;
-                }
-            }
-            return u;
-        }
-        base = __builtin_amdgcn_readlane(incl, 63);
-    }
+    u.s = Seq{x.first, x.n, x.kv, x.len};
+    u.b = x.b;
+    u.tile = x.tile;
+    u.split = x.split;
+    u.splits = x.splits;
+    u.chunk = x.chunk;
+    u.slot = id - x.split;
+    u.ok = x.n > 0;
+    u.begin = x.begin;
+    u.end = x.end;
+    u.b0 = x.b0;
+    u.b1 = x.b1;
+    u.even = x.even != 0;
     return u;
 }
 __device__ __forceinline__ int first_key(const GroupUnit& u) { return u.begin; }
@@ -180,9 +73,240 @@ __device__ __forceinline__ int most_seen(const GroupUnit&, int vis) {
 
 namespace {
 
+// ---------------------------------------------------------------------------
+// prefix_list: the units of a call, by one workgroup: a thread to an entry (group
+// or sequence), then a thread to a unit.
+//
+// The key ranges' length is chosen among 64 that cut the longest entry evenly:
+// with U units of which the longest takes c keys, `slots` of them at once and a
+// price of kPrice keys to a unit (its start and its part), either all run at once
+// and take c + kPrice, or their mean load and one unit more.
+// ---------------------------------------------------------------------------
+constexpr int kThreads = 1024, kWaves = kThreads / 64, kTries = 64, kPrice = 128;
+constexpr int kMost = 1 << 30;
+// in how many ranges: each number about an eighth above the last
+struct Ways {
+    uint16_t n[kTries];
+};
+constexpr Ways make_ways() {
+    Ways w{};
+    int n = 1;
+    for (int k = 0; k < kTries; ++k) {
+        w.n[k] = (uint16_t)n;
+        n += n < 8 ? 1 : n / 8;
+    }
+    return w;
+}
+__device__ const Ways kWays = make_ways();
+
+// Sequences of group g, and how many keys they share.
+struct Group {
+    int b0, b1, keys;
+};
+__device__ __forceinline__ Group load_group(const GroupArgs& p, int g) {
+    Group x;
+    x.b0 = min(max(p.cug[g], 0), p.m.B);
+    x.b1 = min(max(p.cug[g + 1], x.b0), p.m.B);
+    x.keys = x.b1 > x.b0 ? min(max(p.same[g], 0), p.m.max_keys) : 0;
+    return x;
+}
+// Keys that sequence b shares with its group.
+__device__ __forceinline__ int shared_of(const GroupArgs& p, int b) {
+    if (p.groups == 0) return 0;
+    // the last group that starts at b or before it
+    int lo = 0, hi = p.groups - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.cug[mid] <= b) lo = mid;
+        else hi = mid - 1;
+    }
+    const Group x = load_group(p, lo);
+    return b >= x.b0 && b < x.b1 ? x.keys : 0;
+}
+
+// Entry v of the list of groups and then sequences: rows, first key, keys from there on.
+struct Entry {
+    Seq s;
+    int begin, keys, tiles;
+    int b0, b1;     // (group) its sequences
+    bool even;      // (sequence) its first token sees all that is shared
+};
+// (128 or 32 rows to a tile)
+__device__ __forceinline__ int tiles_for(int each, int rows) { return (rows + each - 1) >> (each == 128 ? 7 : 5); }
+__device__ __forceinline__ Entry load_entry(const GroupArgs& p, int v) {
+    Entry x{};
+    x.even = true;
+    if (v < p.groups) {
+        const Group y = load_group(p, v);
+        x.s.first = min(max(p.m.cu[y.b0], 0), p.m.T);
+        x.s.n = min(max(p.m.cu[y.b1], x.s.first), p.m.T) - x.s.first;
+        x.keys = x.s.kv = y.keys;
+        x.tiles = y.keys > 0 ? tiles_for(p.rows, x.s.n * p.m.G) : 0;
+        x.b0 = y.b0;
+        x.b1 = y.b1;
+    } else if (v < p.groups + p.m.B) {
+        x.s = load_seq(p.m, v - p.groups);
+        x.begin = shared_of(p, v - p.groups);
+        x.keys = max(x.s.kv - x.begin, 0);
+        x.tiles = tiles_for(p.own_rows, x.s.n * p.m.G);
+        x.even = x.s.n == 0 || visible(p.m, x.s, 0) >= x.begin;
+    }
+    return x;
+}
+
+__global__ __launch_bounds__(kThreads) void prefix_list(GroupArgs p) {
+    __shared__ int64_t work_s[kWaves], units_s[kTries];
+    __shared__ Entry entry_s[kThreads];
+    __shared__ int ends_s[kThreads], odd_s[kThreads], splits_s[kThreads], length_s[kTries];
+    __shared__ int scan_s[2][kWaves], longest_s[kWaves], chunk_s;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, all = p.groups + p.m.B;
+    // work and the longest entry; the first 1024 entries stay in LDS
+    Entry x{};
+    int64_t work = 0;
+    int longest = 0;
+    for (int v0 = 0; v0 < all; v0 += kThreads) {
+        const Entry y = load_entry(p, v0 + tid);
+        work += (int64_t)y.tiles * y.keys;
+        if (y.tiles > 0) longest = max(longest, y.keys);
+        if (v0 == 0) x = y;
+    }
+    entry_s[tid] = x;
+    work = sum_wave(work);
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) longest = max(longest, __shfl_xor(longest, d, 64));
+    if (lane == 0) {
+        work_s[wave] = work;
+        longest_s[wave] = longest;
+    }
+    __syncthreads();
+    work = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        work += work_s[w];
+        longest = max(longest, longest_s[w]);
+    }
+    // the ranges' lengths that are tried, and the units that each of them makes
+    const int ways = kWays.n[lane];
+    const int c = max(2, ((longest + ways - 1) / ways + p.step - 1) / p.step) * p.step;
+    if (wave == 0) length_s[lane] = c;
+    for (int k = wave; k < kTries; k += kWaves) {
+        const int len = __builtin_amdgcn_readlane(c, k);
+        int64_t n = 0;
+        for (int v0 = 0; v0 < all; v0 += 64) {
+            const int v = v0 + lane;
+            int t, keys;
+            if (v < kThreads) {
+                t = entry_s[v].tiles;
+                keys = entry_s[v].keys;
+            } else {
+                const Entry y = load_entry(p, v);
+                t = y.tiles;
+                keys = y.keys;
+            }
+            n += (int64_t)t * max(1, (int)(((uint32_t)keys + (uint32_t)len - 1u) / (uint32_t)len));
+        }
+        n = sum_wave(n);
+        if (lane == 0) units_s[k] = n;
+    }
+    __syncthreads();
+    if (wave == 0) {
+        const int64_t n = units_s[lane];
+        const float most = (float)min(c, max(longest, 1)), load = ((float)work + (float)n * kPrice) / (float)p.share;
+        float price = n <= p.share ? most + kPrice : load + most;
+        if (n > p.units && lane > 0) price = 3.0e38f;       // (whole entries always fit)
+        float best = price;
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) best = fminf(best, __shfl_xor(best, d, 64));
+        if (lane == 0) chunk_s = length_s[0];
+        const uint64_t at = __ballot(price == best);
+        if (at != 0 && lane == __builtin_ctzll(at)) chunk_s = c;
+    }
+    __syncthreads();
+    const int chunk = chunk_s;
+
+    int base = 0;
+    for (int v0 = 0; v0 < all; v0 += kThreads) {
+        if (v0 > 0) {
+            x = load_entry(p, v0 + tid);
+            entry_s[tid] = x;
+        }
+        const int v = v0 + tid, splits = max(1, (int)(((uint32_t)x.keys + (uint32_t)chunk - 1u) / (uint32_t)chunk));
+        // units and sequences that see less than is shared, counted up to each entry
+        // (lengths that contradict each other may add up to anything: no sum passes kMost)
+        const int mine = (int)min((int64_t)x.tiles * splits, (int64_t)kMost);
+        int ends = scan_upto(mine, kMost), odd = scan_incl(x.even ? 0 : 1);
+        if (lane == 63) {
+            scan_s[0][wave] = ends;
+            scan_s[1][wave] = odd;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+            if (w < wave) {
+                ends = add_to(ends, scan_s[0][w], kMost);
+                odd += scan_s[1][w];
+            }
+        ends = add_to(base, ends, kMost);
+        ends_s[tid] = ends;
+        odd_s[tid] = odd;
+        splits_s[tid] = splits;
+        if (v < all) p.entries[v] = PrefixEntry{x.s.first, x.s.n, ends - mine, splits, x.begin, x.s.kv, x.s.len, chunk};
+        __syncthreads();
+        const int top = ends_s[kThreads - 1];
+        for (int id = base + tid; id < min(top, p.units); id += kThreads) {
+            int lo = 0, hi = kThreads - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (ends_s[mid] > id) hi = mid;
+                else lo = mid + 1;
+            }
+            const int e = v0 + lo, s = splits_s[lo], rest = id - (lo > 0 ? ends_s[lo - 1] : base);
+            const Entry y = entry_s[lo];
+            const int back = (int)((uint32_t)rest / (uint32_t)s);
+            PrefixUnit u{};
+            u.first = y.s.first; u.n = y.s.n; u.kv = y.s.kv; u.len = y.s.len;
+            u.begin = y.begin; u.end = y.begin + y.keys;
+            u.split = rest - back * s;
+            u.tile = y.tiles - 1 - back;          // the last rows see most keys: they come first
+            u.chunk = chunk;
+            u.even = 1;
+            u.b = e - p.groups;
+            // (a row of a sequence that shares no keys and was not split has one part: it is written whole)
+            u.splits = y.begin > 0 ? max(s, 2) : s;
+            if (e < p.groups) {
+                u.b = u.b0 = y.b0;
+                u.b1 = y.b1;
+                u.splits = max(s, 2);
+                // (where the list is longer than the workgroup every row finds its sequence)
+                u.even = all <= kThreads && odd_s[p.groups + y.b1 - 1] == odd_s[p.groups + y.b0 - 1];
+            }
+            // (nor do they lead outside the rows)
+            if (u.tile < 0 || (int64_t)u.tile * (e < p.groups ? p.rows : p.own_rows) >= (int64_t)u.n * p.m.G) u.n = 0;
+            p.list[id] = u;
+        }
+        base = top;
+        __syncthreads();
+    }
+    for (int id = base + tid; id < p.units; id += kThreads) p.list[id].n = 0;
+}
+
 template <typename E, bool KV8, bool EXACT, int DK, int DV, int KT, bool WIDE>
 __global__ __launch_bounds__(256, DK > 192 ? 1 : 2) void prefix_rows(GroupArgs p) {
-    rows_of<E, KV8, EXACT, DK, DV, KT, WIDE>(p);
+    __shared__ RowsLds<DK, DV, KT> lds;
+    rows_of<E, KV8, EXACT, DK, DV, KT, WIDE>(p, lds);
+}
+// The same where rows are few: a sequence's own keys shared out over the waves, which keeps more loads under
+// way.
+template <typename E, bool KV8, bool EXACT, int DK, int DV, int KT, int DO, bool WIDE>
+__global__ __launch_bounds__(256, DO > 128 ? 1 : 2) void prefix_few(GroupArgs p) {
+    __shared__ union Lds {
+        RowsLds<DK, DV, KT> rows;
+        KeysLds<KV8, DO, DO> keys;
+    } lds;
+    const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv), unit = (int)(blockIdx.x / (uint32_t)p.m.Hkv);
+    const GroupUnit u = unit_of<KT>(p, p.rows, unit);
+    if (u.b1 > u.b0) rows_of<E, KV8, EXACT, DK, DV, KT, WIDE>(p, lds.rows);
+    else keys_of<E, KV8, DO, DO>(p, lds.keys, u, hk, unit);
 }
 template <typename E, bool KV8, bool EXACT, bool WIDE> __global__ __launch_bounds__(256, 1) void prefix_latent(GroupArgs p) {
     latent_rows<E, KV8, EXACT, WIDE>(p);
@@ -192,47 +316,49 @@ template <typename E, bool KV8, bool EXACT, bool WIDE> __global__ __launch_bound
 // prefix_join: a row's parts, those against the shared keys and those against its
 // sequence's own, on one scale (as attn_join).
 // ---------------------------------------------------------------------------
-template <typename E, int STEP, int NC, bool TOGETHER>
+template <typename E, int NC, bool TOGETHER>
 __global__ __launch_bounds__(256) void prefix_join(GroupArgs p) {
     constexpr int FLY = NC == 1 ? 8 : 4;       // parts under way at once
     __shared__ f32x4 share[TOGETHER ? 4 : 1][NC][64];
     const int lane = threadIdx.x & 63, wave = (int)dcp::wave_id();
-    const int chunk = group_chunk<STEP>(p, p.rows);
     const int64_t all = (int64_t)p.m.T * p.m.G * p.m.Hkv;
     const int64_t stride = TOGETHER ? gridDim.x : (int64_t)gridDim.x * 4;
+    // the last of n entries from `at` on whose rows start at t or before it: 64 at a time
+    auto find = [&](int at, int n, int t) {
+        int lo = 0, count = n;
+        while (count > 1) {
+            const int step = (count + 63) / 64, i = lo + lane * step;
+            const uint64_t before = __ballot(lane * step < count && p.entries[at + min(i, n - 1)].first <= t);
+            const int k = max(0, 63 - __builtin_clzll(before | 1));
+            count = min(step, count - k * step);
+            lo += k * step;
+        }
+        return at + lo;
+    };
 #pragma unroll 1
     for (int64_t id = TOGETHER ? blockIdx.x : (int64_t)blockIdx.x * 4 + wave; id < all; id += stride) {
         const uint32_t at_row = fdiv((uint32_t)id, p.m.fHkv);
         const int hk = (int)((uint32_t)id - at_row * p.m.fHkv.d), t = (int)fdiv(at_row, p.m.fG), head = (int)at_row - t * p.m.G;
         // the row's group and its sequence: first slots and numbers of parts
         int slot[2] = {0, 0}, parts[2] = {0, 0}, in_tile[2] = {0, 0};
-        bool whole = false, found_seq = false;
-        int base = 0;
-        for (int v0 = 0; v0 < p.groups + p.m.B && !found_seq; v0 += 64) {
-            const Entry x = load_entry(p, v0 + lane, p.rows);
-            const int splits = max(1, (x.keys + chunk - 1) / chunk);
-            const int incl = base + scan_incl(x.tiles * splits);
-            base = __builtin_amdgcn_readlane(incl, 63);
-#pragma unroll
-            for (int kind = 0; kind < 2; ++kind) {
-                const bool mine = (v0 + lane < p.groups) == (kind == 0) && t >= x.s.first && t < x.s.first + x.s.n;
-                const uint64_t found = __ballot(mine);
-                if (found == 0) continue;
-                const int at = __builtin_ctzll(found);
-                const Seq s = seq_of(x.s, at);
-                const int ns = __builtin_amdgcn_readlane(splits, at), begin = __builtin_amdgcn_readlane(x.begin, at);
-                const int row = (t - s.first) * p.m.G + head, tile = row / p.rows;
-                in_tile[kind] = row - tile * p.rows;
-                // (the last tile comes first)
-                slot[kind] = __builtin_amdgcn_readlane(incl, at) - (tile + 1) * ns;
-                parts[kind] = ns;
-                if (kind == 1) {
-                    found_seq = true;
-                    whole = ns == 1 && begin == 0;
-                    // the ranges that the tile's last row has keys in
-                    const int last = min((tile + 1) * p.rows, s.n * p.m.G) - 1;
-                    const int kend = visible(p.m, s, (int)fdiv((uint32_t)last, p.m.fG)) - begin;
-                    parts[1] = min(ns, max(1, (kend + chunk - 1) / chunk));
+        const PrefixEntry y = p.entries[find(p.groups, p.m.B, t)];
+        const bool found_seq = t >= y.first && t < y.first + y.n;
+        const bool whole = y.splits == 1 && y.begin == 0;
+        if (found_seq && !whole) {
+            const int row = (t - y.first) * p.m.G + head, tile = row / p.own_rows;
+            in_tile[1] = row - tile * p.own_rows;
+            slot[1] = y.slot + (tiles_for(p.own_rows, y.n * p.m.G) - 1 - tile) * y.splits;     // (the last tile comes first)
+            // the ranges that the tile's last row has keys in
+            const int last = min((tile + 1) * p.own_rows, y.n * p.m.G) - 1;
+            const int kend = visible(p.m, Seq{y.first, y.n, y.kv, y.len}, (int)fdiv((uint32_t)last, p.m.fG)) - y.begin;
+            parts[1] = min(y.splits, max(1, (kend + y.chunk - 1) / y.chunk));
+            if (y.begin > 0) {
+                const PrefixEntry g = p.entries[find(0, p.groups, t)];
+                if (t >= g.first && t < g.first + g.n && g.kv > 0) {
+                    const int grow = (t - g.first) * p.m.G + head, gtile = grow / p.rows;
+                    in_tile[0] = grow - gtile * p.rows;
+                    slot[0] = g.slot + (tiles_for(p.rows, g.n * p.m.G) - 1 - gtile) * g.splits;
+                    parts[0] = g.splits;
                 }
             }
         }
@@ -315,64 +441,76 @@ __global__ __launch_bounds__(256) void prefix_join(GroupArgs p) {
     }
 }
 
-template <typename E, int STEP>
+template <typename E>
 hipError_t run_join(const GroupArgs& a, hipStream_t stream) {
     const int64_t rows = (int64_t)a.m.T * a.m.G * a.m.Hkv;
     const dim3 block(256);
     if (rows <= 1024) {
         const dim3 grid((uint32_t)rows);
-        return a.Dv <= 256 ? launch(prefix_join<E, STEP, 1, true>, grid, block, stream, a)
-                           : launch(prefix_join<E, STEP, 2, true>, grid, block, stream, a);
+        return a.Dv <= 256 ? launch(prefix_join<E, 1, true>, grid, block, stream, a)
+                           : launch(prefix_join<E, 2, true>, grid, block, stream, a);
     }
     const dim3 grid((uint32_t)(rows < 8192 ? (rows + 3) / 4 : 2048));
-    return a.Dv <= 256 ? launch(prefix_join<E, STEP, 1, false>, grid, block, stream, a)
-                       : launch(prefix_join<E, STEP, 2, false>, grid, block, stream, a);
+    return a.Dv <= 256 ? launch(prefix_join<E, 1, false>, grid, block, stream, a)
+                       : launch(prefix_join<E, 2, false>, grid, block, stream, a);
 }
 
 template <typename E, bool KV8, bool WIDE>
 hipError_t run(const GroupArgs& a, bool latent, hipStream_t stream) {
     const dim3 grid((uint32_t)((int64_t)a.units * a.m.Hkv)), block(256);
-    hipError_t e;
+    hipError_t e = launch(prefix_list, dim3(1), dim3(kThreads), stream, a);
+    if (e != hipSuccess) return e;
     if (latent) {
         e = a.Dk == latent::DK ? launch(prefix_latent<E, KV8, true, WIDE>, grid, block, stream, a)
                                : launch(prefix_latent<E, KV8, false, WIDE>, grid, block, stream, a);
-        return e != hipSuccess ? e : run_join<E, 32>(a, stream);
+        return e != hipSuccess ? e : run_join<E>(a, stream);
     }
     const int d = a.Dk > a.Dv ? a.Dk : a.Dv;
-    if (d <= 64) {
-        e = launch(prefix_rows<E, KV8, false, 64, 64, 64, WIDE>, grid, block, stream, a);
-        return e != hipSuccess ? e : run_join<E, 64>(a, stream);
-    }
-    if (d <= 128) {
-        e = a.Dk == 128 && a.Dv == 128 ? launch(prefix_rows<E, KV8, true, 128, 128, 64, WIDE>, grid, block, stream, a)
-                                       : launch(prefix_rows<E, KV8, false, 128, 128, 64, WIDE>, grid, block, stream, a);
-        return e != hipSuccess ? e : run_join<E, 64>(a, stream);
-    }
-    e = a.Dk <= 192 && a.Dv <= 128 ? launch(prefix_rows<E, KV8, false, 192, 128, 32, WIDE>, grid, block, stream, a)
-                                   : launch(prefix_rows<E, KV8, false, 256, 256, 32, WIDE>, grid, block, stream, a);
-    return e != hipSuccess ? e : run_join<E, 32>(a, stream);
+    const bool few = a.own_rows == 32;
+    auto rows = [&](auto exact, auto dk, auto dv, auto kt, auto own) {
+        constexpr bool X = decltype(exact)::value;
+        constexpr int K = decltype(dk)::value, V = decltype(dv)::value, T = decltype(kt)::value, O = decltype(own)::value;
+        return few ? launch(prefix_few<E, KV8, X, K, V, T, O, WIDE>, grid, block, stream, a)
+                   : launch(prefix_rows<E, KV8, X, K, V, T, WIDE>, grid, block, stream, a);
+    };
+    constexpr std::integral_constant<int, 32> n32{};
+    constexpr std::integral_constant<int, 64> n64{};
+    constexpr std::integral_constant<int, 128> n128{};
+    constexpr std::integral_constant<int, 192> n192{};
+    constexpr std::integral_constant<int, 256> n256{};
+    if (d <= 64) e = rows(std::false_type{}, n64, n64, n64, n64);
+    else if (d <= 128) e = a.Dk == 128 && a.Dv == 128 ? rows(std::true_type{}, n128, n128, n64, n128) : rows(std::false_type{}, n128, n128, n64, n128);
+    else e = a.Dk <= 192 && a.Dv <= 128 ? rows(std::false_type{}, n192, n128, n32, n256) : rows(std::false_type{}, n256, n256, n32, n256);
+    return e != hipSuccess ? e : run_join<E>(a, stream);
 }
 
 }  // namespace
 
-AttnPlan plan_prefix(const Batch& m, int64_t groups, int Dk, int Dv) {
+int64_t prefix_list_bytes(int64_t units, int64_t entries) {
+    return units * (int64_t)sizeof(PrefixUnit) + entries * (int64_t)sizeof(PrefixEntry);
+}
+
+AttnPlan plan_prefix(const Batch& m, int64_t groups, int Dk, int Dv, bool pieces) {
     AttnPlan pl;
     const int64_t rows = (int64_t)m.T * m.G;
     pl.latent = Dk > 256 || Dv > 256;
-    pl.by_keys = false;
+    // few rows a sequence: its own keys by 32 rows, as in plan_attn()
+    pl.by_keys = !pl.latent && pieces && rows <= (int64_t)32 * m.B;
     pl.rows = 128;
     // row tiles, at most: of sequences, and once more of groups
-    pl.tiles = (int32_t)(2 * (rows / pl.rows) + m.B + groups);
+    pl.tiles = (int32_t)(rows / (pl.by_keys ? 32 : 128) + m.B + rows / 128 + groups);
+    // workgroups of a key head that run at once; up to twice as many key ranges beside the tiles
     const int64_t chip = pl.latent ? 256 : 512;
     pl.share = (int32_t)((chip + m.Hkv - 1) / m.Hkv);
-    pl.slots = pl.tiles + pl.share;
+    pl.slots = pl.tiles + 2 * pl.share;
     pl.units = pl.slots;
-    pl.ws_bytes = (int64_t)pl.units * m.Hkv * pl.rows * (Dv + 1) * 4;
+    pl.ws_bytes = prefix_list_bytes(pl.units, groups + m.B) + (int64_t)pl.units * m.Hkv * pl.rows * (Dv + 1) * 4;
     return pl;
 }
 
 hipError_t launch_prefix(const GroupArgs& arg, bool latent, bool bf16, bool kv8, bool wide, hipStream_t stream) {
     GroupArgs a = arg;
+    a.step = latent || a.Dk > 128 || a.Dv > 128 ? 32 : 64;      // keys of a tile
     if (!latent && a.v == nullptr) {           // narrow rows: the values are read as columns of their own
         a.v = a.k;
         a.v_P = a.k_P; a.v_S = a.k_S; a.v_H = a.k_H;

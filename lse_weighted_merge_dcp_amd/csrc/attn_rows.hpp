@@ -26,17 +26,23 @@ namespace dcpa {
 // rounding left takes a second product, half as many matrix instructions again:
 // the chunk above takes 631 us with it, 473 without.
 // ---------------------------------------------------------------------------
+template <int DK, int DV, int KT> struct RowsLds {
+    __attribute__((aligned(1024))) char ktile[2][KT * DK * 2], vtile[2][KT * DV * 2];
+    uint64_t krow_at[4][KT], vrow_at[4][KT];     // of tile t at t % 4
+    uint64_t there_at[4];
+};
+
 template <typename E, bool KV8, bool EXACT, int DK, int DV, int KT, bool WIDE, typename A>
-__device__ __forceinline__ void rows_of(const A& p) {
+__device__ __forceinline__ void rows_of(const A& p, RowsLds<DK, DV, KT>& lds) {
     constexpr int R = 128, KC = DK / 8, VC = DV / 8, NB = KT / 32, ST = DK / 16, CB = DV / 32, KS = KT / 16;
     constexpr int KROW = KC * 16, VROW = VC * 16;
     constexpr int KB = KT * KROW, VB = KT * VROW;
     constexpr int NK = KT * KC / 256, NV = KT * VC / 256;   // 16-byte chunks of a thread
     constexpr int AHEAD = 2;                                // fragments read ahead of their products
     static_assert(KT * KC % 256 == 0 && KT * VC % 256 == 0, "a tile is whole rounds of the workgroup");
-    __shared__ __attribute__((aligned(1024))) char ktile[2][KB], vtile[2][VB];
-    __shared__ uint64_t krow_at[4][KT], vrow_at[4][KT];     // of tile t at t % 4
-    __shared__ uint64_t there_at[4];
+    auto& krow_at = lds.krow_at;
+    auto& vrow_at = lds.vrow_at;
+    auto& there_at = lds.there_at;
 
     const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv), unit = (int)(blockIdx.x / (uint32_t)p.m.Hkv);
     const auto u = unit_of<KT>(p, R, unit);
@@ -61,7 +67,8 @@ __device__ __forceinline__ void rows_of(const A& p) {
                                    (int64_t)(hk * p.m.G + row - token * p.m.G) * p.q_H, Dk, h);
     }
     const int vmin = least_seen(u, vis);
-    const int mine = max(0, min(tiles, (most_seen(u, vis) + KT - 1) / KT));
+    // (waves behind the last row only help to fetch)
+    const int mine = row0 + wave_row < nrows ? max(0, min(tiles, (most_seen(u, vis) + KT - 1) / KT)) : 0;
     clear_rows(w);
     bool odd = false;
 
@@ -83,7 +90,7 @@ __device__ __forceinline__ void rows_of(const A& p) {
         const uint64_t bits = __ballot(lane < KT && (uint32_t)page < (uint32_t)p.m.pages);
         if (lane == 0) there_at[t & 3] = bits;
     };
-    const uint32_t kbuf = lds_addr(&ktile[0][0]), vbuf = lds_addr(&vtile[0][0]);
+    const uint32_t kbuf = lds_addr(&lds.ktile[0][0]), vbuf = lds_addr(&lds.vtile[0][0]);
     u32x2 reg8[KV8 ? NK + NV : 1];
     // the keys or values of tile t: straight into LDS, or into registers to be widened
     auto fetch = [&](auto val, int t) {
