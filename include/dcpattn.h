@@ -197,6 +197,22 @@ int dcpa_prefix_attn(const dcpa_attn_args* a, const int32_t* cu_group, const int
 int64_t dcpa_prefix_attn_workspace(const dcpa_attn_args* a, int64_t n_groups);
 
 /*
+ * dcpa_pair_attn
+ *
+ * dcpa_paged_attn over keys and values in two 16-bit parts: a key is k plus, in
+ * its first Dr columns, k_rest [num_pages, page_size, Hkv, Dr]; a value is v plus
+ * v_rest [num_pages, page_size, Hkv, Dv].  Products of both parts go into the same
+ * fp32 sums, so scores and outputs are those of the sums of the parts; the
+ * weights are rounded as there (wide_weights: not the values' second part's).
+ * cache_dtype is dtype, v not NULL, Dk and Dv at most 256, Dr a multiple of 8 up to
+ * Dk; the rests' strides are multiples of 8, 16-byte aligned.  A query that is not
+ * finite gives NaN.  The workspace query is dcpa_pair_attn_workspace.
+ */
+int dcpa_pair_attn(const dcpa_attn_args* a, const void* k_rest, int64_t kr_P, int64_t kr_S, int64_t kr_H, int64_t Dr,
+                   const void* v_rest, int64_t vr_P, int64_t vr_S, int64_t vr_H, void* stream);
+int64_t dcpa_pair_attn_workspace(const dcpa_attn_args* a);
+
+/*
  * dcpa_attn_mass
  *
  * mass[page, place, hk] += sum over the rows (t, h) of the sequence with key
@@ -329,9 +345,11 @@ int dcpa_project(const dcpa_project_args* a, void* stream);
  * (the cache of the latent layout, one key head): for cached key j < kv_len[b]
  *   k[b, j, h] = k_scale [ sum_c w_k[h, n, c] c_j[c]  (n < Dn) | c_j[Dc ..] (Dr) ]
  *   v[b, j, h] = k_scale sum_c w_v[h, n, c] c_j[c]             (n < Dv)
- * Sums in fp32, each result rounded once to dtype: attention over them reads
- * keys of that type, as if they had been cached.  kv_len is clamped to max_keys
- * and to max_pages * page_size.  Rows behind kv_len, and keys whose page is
+ * Sums in fp32, each result rounded once to dtype.  k_rest and v_rest (both or
+ * neither) get what that rounding left of the sums, rounded once more, so that
+ * the two together hold a result to 2^-16 (bf16) or 2^-22 (fp16, or 2^-25) of itself: keys
+ * and values for dcpa_pair_attn.  (The columns of the rope have none: with k_scale =
+ * 1 they are exact.)  kv_len is clamped to max_keys and to max_pages * page_size.  Rows behind kv_len, and keys whose page is
  * missing, are left as they were.
  *
  * places [B, max_keys] (nullable) gets b * max_keys + j for every such key, -1
@@ -352,6 +370,8 @@ typedef struct {
     const void* w_v;      int64_t wv_H, wv_N;     /* [H, Dv, Dc] */
     void* k;              int64_t k_B, k_S, k_H;  /* [B, max_keys, H, Dn + Dr] */
     void* v;              int64_t v_B, v_S, v_H;  /* [B, max_keys, H, Dv] */
+    void* k_rest;         int64_t kr_B, kr_S, kr_H; /* [B, max_keys, H, Dn], nullable */
+    void* v_rest;         int64_t vr_B, vr_S, vr_H; /* [B, max_keys, H, Dv], nullable */
     int32_t* places;      int64_t p_B;
     int64_t B, H, Dn, Dr, Dv, Dc, max_keys, num_pages, page_size, max_pages, dtype, cache_dtype;
     double k_scale;

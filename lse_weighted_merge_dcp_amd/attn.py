@@ -59,6 +59,8 @@ SIGNATURES = {
     "dcpa_batch_plan": ([_CP, _VP], ctypes.c_int),
     "dcpa_prefix_attn": ([_CP, _VP, _VP, _I64, _VP], ctypes.c_int),
     "dcpa_prefix_attn_workspace": ([_CP, _I64], _I64),
+    "dcpa_pair_attn": ([_CP] + [_VP, _I64, _I64, _I64, _I64] + [_VP, _I64, _I64, _I64] + [_VP], ctypes.c_int),
+    "dcpa_pair_attn_workspace": ([_CP], _I64),
     "dcpa_project": ([_CP, _VP], ctypes.c_int),
     "dcpa_latent_expand": ([_CP, _VP], ctypes.c_int),
 }
@@ -68,7 +70,7 @@ ATTN_ARGS = struct.Struct("=41q3d")
 EVICT_ARGS = struct.Struct("=33q")
 PLAN_ARGS = struct.Struct("=23q")
 PROJECT_ARGS = struct.Struct("=16q")
-EXPAND_ARGS = struct.Struct("=34q1d")
+EXPAND_ARGS = struct.Struct("=42q1d")
 
 _DTYPE = {torch.float16: _lib.DCP_F16, torch.bfloat16: _lib.DCP_BF16}
 _CACHE = {torch.float16: _lib.DCP_F16, torch.bfloat16: _lib.DCP_BF16, torch.float8_e4m3fn: _lib.DCP_FP8_E4M3}
@@ -470,16 +472,19 @@ def latent_values(o: torch.Tensor, w_uv: torch.Tensor, *, out: Optional[torch.Te
 
 def latent_expand(kv_cache: torch.Tensor, w_uk: torch.Tensor, w_uv: torch.Tensor, block_table: torch.Tensor,
                   kv_len: torch.Tensor, max_keys: int, *, k_scale: float = 1.0, k_out: Optional[torch.Tensor] = None,
-                  v_out: Optional[torch.Tensor] = None, places: Optional[torch.Tensor] = None):
+                  v_out: Optional[torch.Tensor] = None, k_rest: Optional[torch.Tensor] = None,
+                  v_rest: Optional[torch.Tensor] = None, places: Optional[torch.Tensor] = None):
     """Keys and values of every head from cached latent rows kv_cache
     [pages,page_size,1,Dc+Dr]: for the first kv_len[b] cached keys of each
     sequence (at most max_keys), k [B,max_keys,H,Dn+Dr] = [w_uk[h] c | rope] and
     v [B,max_keys,H,Dv] = w_uv[h] c, with w_uk [H,Dn,Dc] and w_uv [H,Dv,Dc]
-    (contiguous over Dc), rounded to the weights' type.  Rows behind kv_len and
-    keys without a page are left as they were.  places (int32 [B,max_keys]) gets
-    the block_table for caches of one key to a page, as which dcp_paged_attn
-    takes the two (dcp_latent_attn does it all).  Returns (k, v)."""
-    dev = _on_gpu(kv_cache, w_uk, w_uv, block_table, kv_len, k_out, v_out, places)
+    (contiguous over Dc), rounded to the weights' type.  k_rest [B,max_keys,H,Dn]
+    and v_rest [B,max_keys,H,Dv] (both or neither) get what the rounding leaves, in
+    the same type.  Rows behind kv_len and keys without a page are left as they
+    were.  places (int32 [B,max_keys]) gets the block_table for caches of one key to a
+    page, as which dcp_paged_attn takes k and v (dcp_latent_attn does it all).
+    Returns (k, v)."""
+    dev = _on_gpu(kv_cache, w_uk, w_uv, block_table, kv_len, k_out, v_out, k_rest, v_rest, places)
     for t, name, nd in ((kv_cache, "kv_cache", 4), (w_uk, "w_uk", 3), (w_uv, "w_uv", 3)):
         _rows(t, name, nd)
     H, Dn, Dc = w_uk.shape
@@ -493,24 +498,29 @@ def latent_expand(kv_cache: torch.Tensor, w_uk: torch.Tensor, w_uv: torch.Tensor
         raise ValueError("block_table must be int32 [B, pages of a sequence]")
     _ints(block_table, "block_table", (B, block_table.shape[1]))
     _require(max_keys >= 0, "max_keys must not be negative")
+    if (k_rest is None) != (v_rest is None):
+        raise ValueError("k_rest and v_rest go together")
     if k_out is None:
         k_out = torch.empty((B, max_keys, H, Dn + Dr), dtype=w_uk.dtype, device=w_uk.device)
     if v_out is None:
         v_out = torch.empty((B, max_keys, H, Dv), dtype=w_uk.dtype, device=w_uk.device)
-    _rows(k_out, "k_out", 4)
-    _rows(v_out, "v_out", 4)
-    if (k_out.shape != (B, max_keys, H, Dn + Dr) or v_out.shape != (B, max_keys, H, Dv) or k_out.dtype != w_uk.dtype or
-            v_out.dtype != w_uk.dtype):
-        raise ValueError("bad k_out or v_out tensor")
+    strides = []
+    for t, name, d in ((k_out, "k_out", Dn + Dr), (v_out, "v_out", Dv), (k_rest, "k_rest", Dn), (v_rest, "v_rest", Dv)):
+        if t is None:
+            strides += [0, 0, 0, 0]
+            continue
+        _rows(t, name, 4)
+        if t.shape != (B, max_keys, H, d) or t.dtype != w_uk.dtype:
+            raise ValueError("%s must be [B,max_keys,H,%d] of the weights' dtype" % (name, d))
+        strides += [t.data_ptr(), *t.stride()[:3]]
     if places is not None:
         _ints(places, "places", (B, max_keys))
-    cs, wk, wv, ks, vs = kv_cache.stride(), w_uk.stride(), w_uv.stride(), k_out.stride(), v_out.stride()
+    cs, wk, wv = kv_cache.stride(), w_uk.stride(), w_uv.stride()
     args = EXPAND_ARGS.pack(
         kv_cache.data_ptr(), cs[0], cs[1], block_table.data_ptr(), block_table.stride(0), kv_len.data_ptr(),
-        w_uk.data_ptr(), wk[0], wk[1], w_uv.data_ptr(), wv[0], wv[1], k_out.data_ptr(), ks[0], ks[1], ks[2],
-        v_out.data_ptr(), vs[0], vs[1], vs[2], places.data_ptr() if places is not None else 0,
-        places.stride(0) if places is not None else 0, B, H, Dn, Dr, Dv, Dc, max_keys, kv_cache.shape[0],
-        kv_cache.shape[1], block_table.shape[1], dt, ct, k_scale)
+        w_uk.data_ptr(), wk[0], wk[1], w_uv.data_ptr(), wv[0], wv[1], *strides,
+        places.data_ptr() if places is not None else 0, places.stride(0) if places is not None else 0,
+        B, H, Dn, Dr, Dv, Dc, max_keys, kv_cache.shape[0], kv_cache.shape[1], block_table.shape[1], dt, ct, k_scale)
     _call(lib().dcpa_latent_expand, "dcpa_latent_expand", dev, args)
     return k_out, v_out
 
@@ -519,34 +529,57 @@ def dcp_latent_attn(q: torch.Tensor, kv_cache: torch.Tensor, w_uk: torch.Tensor,
                     block_table: torch.Tensor, cu_q: torch.Tensor, kv_len: torch.Tensor, max_keys: int, *,
                     seq_len: Optional[torch.Tensor] = None, scale: Optional[float] = None, rank: int = 0,
                     n_ranks: int = 1, interleave: int = 1, causal: bool = True, k_scale: float = 1.0,
-                    is_lse_base_on_e: bool = True, wide_weights: bool = False, out: Optional[torch.Tensor] = None,
-                    out_lse: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
-                    v_out: Optional[torch.Tensor] = None, places: Optional[torch.Tensor] = None,
-                    workspace: Optional[torch.Tensor] = None):
+                    is_lse_base_on_e: bool = True, wide_weights: bool = False, rounded: bool = False,
+                    out: Optional[torch.Tensor] = None, out_lse: Optional[torch.Tensor] = None,
+                    k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+                    k_rest: Optional[torch.Tensor] = None, v_rest: Optional[torch.Tensor] = None,
+                    places: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
     """Latent attention in the expanded form: keys and values of every head are
     made from the rank's cached latent rows (latent_expand), and the new tokens'
     queries q [T,H,Dn+Dr], as the model has them (rotated, not taken into latent
     space), attend to those.  For prompt chunks: a pair of query and key costs
-    Dn + Dr + Dv products instead of the latent form's 2 Dc + Dr, a key H (Dn + Dv)
-    Dc more.  max_keys: as many keys as a sequence may have cached here at most;
-    kv_len is clamped to it.  k_out, v_out (contiguous) and places are buffers to keep
-    them in, fresh ones if not given.  The other arguments are those of
-    dcp_paged_attn.  Returns (out [T,H,Dv], lse [T,H])."""
+    Dn + Dr + Dv products (here 2 Dn + Dr + 2 Dv) instead of the latent form's 2 Dc +
+    Dr, a key H (Dn + Dv) Dc more.  Keys and values are kept in two parts, so that
+    they are not rounded to 16 bits on the way; rounded=True does round them, once,
+    as a cache would hold them, and is faster.  max_keys: as many keys as a sequence
+    may have cached here at most; kv_len is clamped to it.  k_out, v_out, k_rest,
+    v_rest (contiguous, as latent_expand has them) and places are buffers to keep
+    them in, fresh ones if not given; they hold keys without k_scale.  The other
+    arguments are those of dcp_paged_attn.  Returns (out [T,H,Dv], lse [T,H])."""
     B, (H, Dn, _), Dv = kv_len.shape[0], w_uk.shape, w_uv.shape[1]
     Dk = Dn + kv_cache.shape[3] - w_uk.shape[2]
-    for t, name in ((k_out, "k_out"), (v_out, "v_out"), (places, "places")):
+    for t, name in ((k_out, "k_out"), (v_out, "v_out"), (k_rest, "k_rest"), (v_rest, "v_rest"), (places, "places")):
         if t is not None and not t.is_contiguous():
             raise ValueError("%s must be contiguous" % name)
     if q.dim() != 3 or q.shape[1:] != (H, Dk) or q.dtype != w_uk.dtype:
         raise ValueError("expected q [T,H,Dn+Dr] of the weights' dtype")
+    if rounded and (k_rest is not None or v_rest is not None):
+        raise ValueError("rounded keys and values have no rest")
     if places is None:
         places = torch.empty((B, max_keys), dtype=torch.int32, device=q.device)
-    k, v = latent_expand(kv_cache, w_uk, w_uv, block_table, kv_len, max_keys, k_scale=k_scale, k_out=k_out, v_out=v_out,
-                         places=places)
-    return dcp_paged_attn(q, k.view(B * max_keys, 1, H, Dk), v.view(B * max_keys, 1, H, Dv), places, cu_q, kv_len,
-                          seq_len=seq_len, scale=scale, rank=rank, n_ranks=n_ranks, interleave=interleave, causal=causal,
-                          is_lse_base_on_e=is_lse_base_on_e, wide_weights=wide_weights, out=out, out_lse=out_lse,
-                          workspace=workspace)
+    if not rounded:
+        if k_rest is None:
+            k_rest = torch.empty((B, max_keys, H, Dn), dtype=q.dtype, device=q.device)
+        if v_rest is None:
+            v_rest = torch.empty((B, max_keys, H, Dv), dtype=q.dtype, device=q.device)
+    # (the scale goes to the scores and the outputs, so that the columns of the rope stay exact)
+    k, v = latent_expand(kv_cache, w_uk, w_uv, block_table, kv_len, max_keys, k_out=k_out, v_out=v_out, k_rest=k_rest,
+                         v_rest=v_rest, places=places)
+    k, v = k.view(B * max_keys, 1, H, Dk), v.view(B * max_keys, 1, H, Dv)
+    if rounded:
+        return dcp_paged_attn(q, k, v, places, cu_q, kv_len, seq_len=seq_len, scale=scale, rank=rank, n_ranks=n_ranks,
+                              interleave=interleave, causal=causal, k_scale=k_scale, v_scale=k_scale,
+                              is_lse_base_on_e=is_lse_base_on_e, wide_weights=wide_weights, out=out, out_lse=out_lse,
+                              workspace=workspace)
+    dev = _on_gpu(q, cu_q, seq_len, out, out_lse, workspace)
+    Dv, out, out_lse = _attn_outputs(q, k, v, None, out, out_lse)
+    h = lib()
+    args = _attn_args(q, k, v, places, cu_q, kv_len, seq_len, scale, Dv, rank, n_ranks, interleave, causal, k_scale,
+                      k_scale, is_lse_base_on_e, wide_weights, out, out_lse, 0, 0)
+    args, _keep = _with_workspace(args, h.dcpa_pair_attn_workspace, "dcpa_pair_attn", workspace, q)
+    _call(h.dcpa_pair_attn, "dcpa_pair_attn", dev, args, k_rest.data_ptr(), H * Dn, H * Dn, Dn, Dn, v_rest.data_ptr(),
+          H * Dv, H * Dv, Dv)
+    return out, out_lse
 
 
 class BatchPlan(NamedTuple):

@@ -248,6 +248,11 @@ hipError_t run(const AttnArgs& a, const AttnPlan& pl, bool wide, hipStream_t str
 
 }  // namespace
 
+hipError_t join_rows(const AttnArgs& a, int step, bool bf16, hipStream_t stream) {
+    if (step == 32) return bf16 ? run_join<BF16T, 32>(a, stream) : run_join<F16T, 32>(a, stream);
+    return bf16 ? run_join<BF16T, 64>(a, stream) : run_join<F16T, 64>(a, stream);
+}
+
 hipError_t launch_attn(const AttnArgs& arg, const AttnPlan& pl, bool bf16, bool kv8, bool wide, hipStream_t stream) {
     AttnArgs a = arg;
     if (!pl.latent && a.v == nullptr) {        // narrow rows: the values are read as columns of their own

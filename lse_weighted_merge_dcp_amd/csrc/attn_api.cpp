@@ -153,6 +153,15 @@ int check_prefix(const dcpa_attn_args* a, int64_t groups, Batch& m, AttnPlan& pl
     return grid_ok(a, pl, m) ? DCP_OK : DCP_ERR_SHAPE;
 }
 
+int check_pairs(const dcpa_attn_args* a, Batch& m, AttnPlan& pl) {
+    if (int st = check_shapes(a, m)) return st;
+    if (a->cache_dtype != a->dtype) return DCP_ERR_DTYPE;
+    if (a->v == nullptr && a->num_pages > 0) return DCP_ERR_NULL;
+    if (a->Dk > 256 || a->Dv > 256) return DCP_ERR_SHAPE;
+    pl = plan_pairs(m, (int)a->Dv);
+    return grid_ok(a, pl, m) ? DCP_OK : DCP_ERR_SHAPE;
+}
+
 // Alignment of what the attention calls write, and of the values.
 int check_outputs(const dcpa_attn_args* a) {
     if (!a->out) return DCP_ERR_NULL;
@@ -268,6 +277,39 @@ int dcpa_prefix_attn(const dcpa_attn_args* a, const int32_t* cu_group, const int
     k.own_rows = pl.by_keys ? 32 : pl.rows;
     return status(launch_prefix(k, pl.latent, a->dtype == DCP_BF16, a->cache_dtype == DCP_FP8_E4M3, a->wide_weights != 0,
                                 (hipStream_t)stream));
+}
+
+int64_t dcpa_pair_attn_workspace(const dcpa_attn_args* a) {
+    if (a == nullptr) return DCP_ERR_NULL;
+    Batch m;
+    AttnPlan pl;
+    if (int st = check_pairs(a, m, pl)) return st;
+    return a->B == 0 || a->T == 0 ? 0 : pl.ws_bytes;
+}
+
+int dcpa_pair_attn(const dcpa_attn_args* a, const void* k_rest, int64_t kr_P, int64_t kr_S, int64_t kr_H, int64_t Dr,
+                   const void* v_rest, int64_t vr_P, int64_t vr_S, int64_t vr_H, void* stream) {
+    if (a == nullptr) return DCP_ERR_NULL;
+    PairArgs k;
+    AttnPlan pl;
+    if (int st = check_pairs(a, k.m, pl)) return st;
+    if (Dr < 8 || Dr % 8 != 0 || Dr > a->Dk) return DCP_ERR_SHAPE;
+    if (!strides_ok({kr_P, kr_S, kr_H, vr_P, vr_S, vr_H}) ||
+        !span_ok({{a->num_pages, kr_P}, {a->page_size, kr_S}, {a->Hkv, kr_H}, {Dr, 1}}, 2) ||
+        !span_ok({{a->num_pages, vr_P}, {a->page_size, vr_S}, {a->Hkv, vr_H}, {a->Dv, 1}}, 2))
+        return DCP_ERR_STRIDE;
+    if (a->B == 0 || a->T == 0) return DCP_OK;
+    if (int st = check_inputs(a)) return st;
+    if (a->num_pages > 0 && (!k_rest || !v_rest)) return DCP_ERR_NULL;
+    if (int st = check_outputs(a)) return st;
+    if (!aligned(k_rest, 16) || !aligned(v_rest, 16) || !multiples({kr_P, kr_S, kr_H, vr_P, vr_S, vr_H}, 8)) return DCP_ERR_ALIGN;
+    if (int st = fill_attn(a, pl, k)) return st;
+    k.kr = (const char*)k_rest;
+    k.kr_P = kr_P * 2; k.kr_S = kr_S * 2; k.kr_H = kr_H * 2;
+    k.vr = (const char*)v_rest;
+    k.vr_P = vr_P * 2; k.vr_S = vr_S * 2; k.vr_H = vr_H * 2;
+    k.Dr = (int32_t)Dr;
+    return status(launch_pairs(k, pl, a->dtype == DCP_BF16, a->wide_weights != 0, (hipStream_t)stream));
 }
 
 int64_t dcpa_attn_mass_workspace(const dcpa_attn_args* a) {
@@ -527,7 +569,9 @@ int dcpa_latent_expand(const dcpa_expand_args* a, void* stream) {
     if (!positive(a->k_scale)) return DCPA_ERR_VALUE;
     const int ec = esize_of(a->cache_dtype);
     if (!strides_ok({a->c_P, a->c_S, a->t_B, a->wk_H, a->wk_N, a->wv_H, a->wv_N, a->k_B, a->k_S, a->k_H, a->v_B, a->v_S,
-                     a->v_H, a->p_B}) ||
+                     a->v_H, a->kr_B, a->kr_S, a->kr_H, a->vr_B, a->vr_S, a->vr_H, a->p_B}) ||
+        !span_ok({{a->B, a->kr_B}, {a->max_keys, a->kr_S}, {a->H, a->kr_H}, {a->Dn, 1}}, 2) ||
+        !span_ok({{a->B, a->vr_B}, {a->max_keys, a->vr_S}, {a->H, a->vr_H}, {a->Dv, 1}}, 2) ||
         !span_ok({{a->num_pages, a->c_P}, {a->page_size, a->c_S}, {a->Dc + a->Dr, 1}}, ec) ||
         !span_ok({{a->B, a->t_B}, {a->max_pages, 1}}, 4) || !span_ok({{a->B, a->p_B}, {a->max_keys, 1}}, 4) ||
         !span_ok({{a->H, a->wk_H}, {a->Dn, a->wk_N}, {a->Dc, 1}}, 2) ||
@@ -536,11 +580,12 @@ int dcpa_latent_expand(const dcpa_expand_args* a, void* stream) {
         !span_ok({{a->B, a->v_B}, {a->max_keys, a->v_S}, {a->H, a->v_H}, {a->Dv, 1}}, 2))
         return DCP_ERR_STRIDE;
     if (a->B == 0 || a->max_keys == 0) return DCP_OK;
-    if ((a->max_pages > 0 && !a->block_table) || !a->kv_len || !a->w_k || !a->w_v || !a->k || !a->v || (a->num_pages > 0 && !a->cache))
+    if ((a->max_pages > 0 && !a->block_table) || !a->kv_len || !a->w_k || !a->w_v || !a->k || !a->v || (a->num_pages > 0 && !a->cache) || !a->k_rest != !a->v_rest)
         return DCP_ERR_NULL;
-    for (const void* x : {a->cache, a->w_k, a->w_v, (const void*)a->k, (const void*)a->v})
+    for (const void* x : {a->cache, a->w_k, a->w_v, (const void*)a->k, (const void*)a->v, (const void*)a->k_rest, (const void*)a->v_rest})
         if (!aligned(x, 16)) return DCP_ERR_ALIGN;
-    if (!multiples({a->c_P, a->c_S, a->wk_H, a->wk_N, a->wv_H, a->wv_N, a->k_B, a->k_S, a->k_H, a->v_B, a->v_S, a->v_H}, 8) ||
+    if (!multiples({a->c_P, a->c_S, a->wk_H, a->wk_N, a->wv_H, a->wv_N, a->k_B, a->k_S, a->k_H, a->v_B, a->v_S, a->v_H,
+                    a->kr_B, a->kr_S, a->kr_H, a->vr_B, a->vr_S, a->vr_H}, 8) ||
         !aligned(a->block_table, 4) || !aligned(a->kv_len, 4) || !aligned(a->places, 4))
         return DCP_ERR_ALIGN;
     ExpandArgs k;
@@ -553,6 +598,9 @@ int dcpa_latent_expand(const dcpa_expand_args* a, void* stream) {
     k.ko = (char*)a->k; k.vo = (char*)a->v;
     k.ko_B = a->k_B * 2; k.ko_S = a->k_S * 2; k.ko_H = a->k_H * 2;
     k.vo_B = a->v_B * 2; k.vo_S = a->v_S * 2; k.vo_H = a->v_H * 2;
+    k.kr = (char*)a->k_rest; k.vr = (char*)a->v_rest;
+    k.kr_B = a->kr_B * 2; k.kr_S = a->kr_S * 2; k.kr_H = a->kr_H * 2;
+    k.vr_B = a->vr_B * 2; k.vr_S = a->vr_S * 2; k.vr_H = a->vr_H * 2;
     k.places = a->places;
     k.pl_B = a->p_B;
     k.B = (int32_t)a->B; k.H = (int32_t)a->H;

@@ -106,6 +106,14 @@ __device__ __noinline__ void slow_rows(A p, U u, int hk, int unit, int tile_rows
 #pragma unroll
             for (int i = 0; i < NQ; ++i)
                 if (lane + 64 * i < p.Dk) s += x[i] * one(kr + (lane + 64 * i) * ES);
+            const char* rest = nullptr;
+            if constexpr (std::is_same_v<A, PairArgs>) {
+                const char* more = p.kr + (int64_t)id * p.kr_P + place * p.kr_S + (int64_t)hk * p.kr_H;
+                rest = p.vr + (int64_t)id * p.vr_P + place * p.vr_S + (int64_t)hk * p.vr_H;
+#pragma unroll
+                for (int i = 0; i < NQ; ++i)
+                    if (lane + 64 * i < p.Dr) s += x[i] * one(more + (lane + 64 * i) * ES);
+            }
 #pragma unroll
             for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d, 64);
             s *= p.c;
@@ -114,7 +122,8 @@ __device__ __noinline__ void slow_rows(A p, U u, int hk, int unit, int tile_rows
             l = l * f + w;
 #pragma unroll
             for (int i = 0; i < NO; ++i)
-                if (lane + 64 * i < p.Dv) acc[i] = acc[i] * f + w * one(vr + (lane + 64 * i) * ES);
+                if (lane + 64 * i < p.Dv)
+                    acc[i] = acc[i] * f + w * (one(vr + (lane + 64 * i) * ES) + (rest != nullptr ? one(rest + (lane + 64 * i) * ES) : 0.0f));
         }
         float f, lse2;
         finish(l, mc, p.vs, f, lse2);

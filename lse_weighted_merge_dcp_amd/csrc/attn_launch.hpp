@@ -78,6 +78,19 @@ hipError_t launch_attn(const AttnArgs& a, const AttnPlan& pl, bool bf16, bool kv
 
 hipError_t launch_latent(const AttnArgs& a, dim3 grid, bool bf16, bool kv8, bool wide, hipStream_t stream);
 
+// Attention over keys and values in two parts, the second what the rounding of the first left.
+struct PairArgs : AttnArgs {
+    const char* kr;          // the first Dr columns of the keys
+    int64_t kr_P, kr_S, kr_H;
+    const char* vr;
+    int64_t vr_P, vr_S, vr_H;
+    int32_t Dr;
+};
+AttnPlan plan_pairs(const Batch& m, int Dv);
+hipError_t launch_pairs(const PairArgs& a, const AttnPlan& pl, bool bf16, bool wide, hipStream_t stream);
+// Joins the split rows of launch_attn() (step: keys of a tile).
+hipError_t join_rows(const AttnArgs& a, int step, bool bf16, hipStream_t stream);
+
 // Attention of sequences that share their first keys, group by group.  Lists that
 // its first kernel leaves in the workspace: units of work, and where the units of
 // each group and then each sequence stand.
@@ -204,6 +217,8 @@ struct ExpandArgs {
     int64_t wk_H, wk_N, wv_H, wv_N;
     char *ko, *vo;
     int64_t ko_B, ko_S, ko_H, vo_B, vo_S, vo_H;
+    char *kr, *vr;           // what the rounding leaves; null: not asked for
+    int64_t kr_B, kr_S, kr_H, vr_B, vr_S, vr_H;
     int32_t* places;         // nullable
     int64_t pl_B;
     int32_t B, H, Dn, Dr, Dv, Dc;

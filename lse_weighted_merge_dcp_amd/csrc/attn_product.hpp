@@ -130,27 +130,38 @@ template <typename E, int MT_, int NT_, int WM, int WN, int ST, bool TURNED, boo
         }
     }
     // The wave's results times `scale`, rounded, in pieces of eight columns: put(row of the tile, column of the
-    // tile, piece).
-    template <typename F> __device__ __forceinline__ void store(float scale, F&& put) {
+    // tile, piece, what the rounding left where REST).
+    template <bool REST, typename F> __device__ __forceinline__ void store(float scale, F&& put) {
         const int r = lane & 31, h = lane >> 5;
+        // (the upper half-wave's part of the first group of four against the lower one's of the second)
+        auto join = [](const uint32_t (&v)[2][2]) {
+            const auto x = __builtin_amdgcn_permlane32_swap(v[0][0], v[1][0], false, false);
+            const auto y = __builtin_amdgcn_permlane32_swap(v[0][1], v[1][1], false, false);
+            return u32x4{x[0], y[0], x[1], y[1]};
+        };
 #pragma unroll
         for (int j = 0; j < BM; ++j)
 #pragma unroll
             for (int i = 0; i < BN; ++i)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    uint32_t v[2][2];
+                    uint32_t v[2][2], rest[2][2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
                         for (int d = 0; d < 2; ++d) {
                             const int k = q * 8 + e * 4 + d * 2;
-                            v[e][d] = Mat<E>::pack2(acc[i][j][k] * scale, acc[i][j][k + 1] * scale);
+                            float x = acc[i][j][k] * scale, y = acc[i][j][k + 1] * scale;
+                            // (one value each: the compiler would take the product into the conversion, which then
+                            // rounds it once, and round it twice for the rest)
+                            if constexpr (REST) asm("" : "+v"(x), "+v"(y));
+                            v[e][d] = Mat<E>::pack2(x, y);
+                            if constexpr (REST) rest[e][d] = Mat<E>::pack2(x - Mat<E>::low(v[e][d]), y - Mat<E>::high(v[e][d]));
                         }
-                    // (the upper half-wave's part of the first group against the lower one's of the second)
-                    const auto x = __builtin_amdgcn_permlane32_swap(v[0][0], v[1][0], false, false);
-                    const auto y = __builtin_amdgcn_permlane32_swap(v[0][1], v[1][1], false, false);
-                    put((wm * BM + j) * 32 + r, (wn * BN + i) * 32 + q * 16 + h * 8, u32x4{x[0], y[0], x[1], y[1]});
+                    const u32x4 whole = join(v);
+                    u32x4 left = {};
+                    if constexpr (REST) left = join(rest);
+                    put((wm * BM + j) * 32 + r, (wn * BN + i) * 32 + q * 16 + h * 8, whole, left);
                 }
     }
 };

@@ -42,7 +42,7 @@ __global__ __launch_bounds__(256, 2) void project_rows(ProjectArgs p) {
     }
     t.run(p.K, p.w_K, n_here);
     char* y = p.y + (int64_t)head * p.y_H;
-    t.store(1.0f, [&](int row, int col, u32x4 v) {
+    t.template store<false>(1.0f, [&](int row, int col, u32x4 v, u32x4) {
         if (row0 + row < p.T && col0 + col < p.N)
             *(u32x4*)(y + (int64_t)(row0 + row) * p.y_T + (col0 + col) * 2) = v;
     });
@@ -60,7 +60,7 @@ __global__ __launch_bounds__(256, 2) void project_rows(ProjectArgs p) {
 // expand_rows: a workgroup takes 256 keys of a sequence and 256 of the H (Dn + Dv)
 // weight rows.
 // ---------------------------------------------------------------------------
-template <typename E, bool X8> __global__ __launch_bounds__(512, 2) void expand_rows(ExpandArgs p) {
+template <typename E, bool X8, bool REST> __global__ __launch_bounds__(512, 2) void expand_rows(ExpandArgs p) {
     using P = Product<E, 256, 256, 2, 4, 2, false, X8>;
     __shared__ __attribute__((aligned(1024))) char lds[P::LDS];
     const int nt = (int)(blockIdx.x % (uint32_t)p.nt), rest = (int)(blockIdx.x / (uint32_t)p.nt);
@@ -113,7 +113,7 @@ template <typename E, bool X8> __global__ __launch_bounds__(512, 2) void expand_
     meet();
     char* ko = p.ko + (int64_t)b * p.ko_B;
     char* vo = p.vo + (int64_t)b * p.vo_B;
-    t.store(p.ks, [&](int row, int col, u32x4 v) {
+    auto put = [&](int row, int col, u32x4 v, u32x4 rest) {
         const int j = row0 + row;
         const uint32_t n = (uint32_t)(col0 + col), h = fdiv(n, p.fper);
         const int d = (int)(n - h * (uint32_t)per);
@@ -121,7 +121,13 @@ template <typename E, bool X8> __global__ __launch_bounds__(512, 2) void expand_
         char* at = d < p.Dn ? ko + (int64_t)j * p.ko_S + (int64_t)h * p.ko_H + d * 2
                             : vo + (int64_t)j * p.vo_S + (int64_t)h * p.vo_H + (d - p.Dn) * 2;
         *(u32x4*)at = v;
-    });
+        if constexpr (REST) {
+            at = d < p.Dn ? p.kr + (int64_t)b * p.kr_B + (int64_t)j * p.kr_S + (int64_t)h * p.kr_H + d * 2
+                          : p.vr + (int64_t)b * p.vr_B + (int64_t)j * p.vr_S + (int64_t)h * p.vr_H + (d - p.Dn) * 2;
+            *(u32x4*)at = rest;
+        }
+    };
+    t.template store<REST>(p.ks, put);
     // the columns that all heads share, for the heads whose first weight row is this tile's
     if (p.Dr > 0) {
         const int h0 = (col0 + per - 1) / per, h1 = min((min(col0 + 256, cols) + per - 1) / per, p.H), pieces = p.Dr / 8;
@@ -192,7 +198,9 @@ hipError_t launch_expand(const ExpandArgs& arg, bool bf16, bool x8, hipStream_t 
     const dim3 grid((uint32_t)((int64_t)a.B * a.mt * a.nt)), block(512);
     auto run = [&](auto e) {
         using E = decltype(e);
-        return x8 ? launch(expand_rows<E, true>, grid, block, stream, a) : launch(expand_rows<E, false>, grid, block, stream, a);
+        if (a.kr != nullptr)
+            return x8 ? launch(expand_rows<E, true, true>, grid, block, stream, a) : launch(expand_rows<E, false, true>, grid, block, stream, a);
+        return x8 ? launch(expand_rows<E, true, false>, grid, block, stream, a) : launch(expand_rows<E, false, false>, grid, block, stream, a);
     };
     return bf16 ? run(BF16T{}) : run(F16T{});
 }

@@ -31,9 +31,17 @@ template <int DK, int DV, int KT> struct RowsLds {
     uint64_t krow_at[4][KT], vrow_at[4][KT];     // of tile t at t % 4
     uint64_t there_at[4];
 };
+// Keys and values in two parts, the second what the rounding of the first left (DR columns of a key have one).
+template <int DK, int DV, int KT, int DR> struct PairLds : RowsLds<DK, DV, KT> {
+    __attribute__((aligned(1024))) char krest[2][KT * DR * 2], vrest[2][KT * DV * 2];
+    uint64_t krest_at[4][KT], vrest_at[4][KT];
+};
 
-template <typename E, bool KV8, bool EXACT, int DK, int DV, int KT, bool WIDE, typename A>
-__device__ __forceinline__ void rows_of(const A& p, RowsLds<DK, DV, KT>& lds) {
+template <typename E, bool KV8, bool EXACT, int DK, int DV, int KT, bool WIDE, int DR = 0, typename A, typename L>
+__device__ __forceinline__ void rows_of(const A& p, L& lds) {
+    constexpr bool PAIRS = DR > 0;
+    constexpr int RC = DR / 8, SR = DR / 16, RROW = DR * 2, RB = KT * RROW, NR = KT * RC / 256;
+    static_assert(!(PAIRS && KV8) && KT * RC % 256 == 0 && DR <= DK, "parts of 16 bits");
     constexpr int R = 128, KC = DK / 8, VC = DV / 8, NB = KT / 32, ST = DK / 16, CB = DV / 32, KS = KT / 16;
     constexpr int KROW = KC * 16, VROW = VC * 16;
     constexpr int KB = KT * KROW, VB = KT * VROW;
@@ -86,6 +94,10 @@ __device__ __forceinline__ void rows_of(const A& p, RowsLds<DK, DV, KT>& lds) {
         if (lane < KT) {
             krow_at[t & 3][lane] = ka;
             vrow_at[t & 3][lane] = page_row(page, p.m, p.v, p.v_P, p.v_S, voff, place);
+            if constexpr (PAIRS) {
+                lds.krest_at[t & 3][lane] = page_row(page, p.m, p.kr, p.kr_P, p.kr_S, (int64_t)hk * p.kr_H, place);
+                lds.vrest_at[t & 3][lane] = page_row(page, p.m, p.vr, p.vr_P, p.vr_S, (int64_t)hk * p.vr_H, place);
+            }
         }
         const uint64_t bits = __ballot(lane < KT && (uint32_t)page < (uint32_t)p.m.pages);
         if (lane == 0) there_at[t & 3] = bits;
@@ -108,6 +120,18 @@ __device__ __forceinline__ void rows_of(const A& p, RowsLds<DK, DV, KT>& lds) {
                 dma16((const char*)at, (V ? vbuf + (uint32_t)((t & 1) * VB) : kbuf + (uint32_t)((t & 1) * KB)) +
                                            (uint32_t)((i * 256 + wave * 64) * 16));
         }
+        if constexpr (PAIRS) {
+            constexpr int rcols = V ? VC : RC;
+#pragma unroll
+            for (int i = 0; i < (V ? NV : NR); ++i) {
+                const int ch = i * 256 + tid, row = ch / rcols, c = (ch % rcols) ^ (V ? swz_v<VC>(row) : swz<RC>(row));
+                uint64_t at = (V ? lds.vrest_at[t & 3][row] : lds.krest_at[t & 3][row]) + (uint64_t)(c * 16);
+                if constexpr (!EXACT) at = at_or_zeros(c * 8 < (V ? Dv : p.Dr), at);
+                dma16((const char*)at, (V ? lds_addr(&lds.vrest[0][0]) + (uint32_t)((t & 1) * VB)
+                                          : lds_addr(&lds.krest[0][0]) + (uint32_t)((t & 1) * RB)) +
+                                           (uint32_t)((i * 256 + wave * 64) * 16));
+            }
+        }
     };
     auto widen = [&](auto val, int t) {
         constexpr bool V = decltype(val)::value;
@@ -120,19 +144,25 @@ __device__ __forceinline__ void rows_of(const A& p, RowsLds<DK, DV, KT>& lds) {
     constexpr std::true_type values{};
     constexpr std::false_type keys{};
 
-    // scores of tile t; `beside(n)`: what is done beside matrix instruction n of NB ST
+    // scores of tile t; `beside(n)`: what is done beside matrix instruction n of NB (ST + SR)
     auto multiply_keys = [&](int t, f32x16 (&s)[1][NB], auto beside) {
+        constexpr int N = ST * NB, ALL = N + SR * NB;
         KeyPlace<KROW> place;
         place.set(kbuf + (uint32_t)((t & 1) * KB), r, h);
-        u32x4 a[ST * NB];
-        auto read = [&](int n) { a[n] = lds_read16(place.at[n / NB % place.N] + (uint32_t)(n / NB / place.N * place.N * 32 + n % NB * 32 * KROW)); };
+        KeyPlace<PAIRS ? RROW : KROW> more;
+        if constexpr (PAIRS) more.set(lds_addr(&lds.krest[0][0]) + (uint32_t)((t & 1) * RB), r, h);
+        u32x4 a[ALL];
+        auto read = [&](int n) {
+            if (n < N) a[n] = lds_read16(place.at[n / NB % place.N] + (uint32_t)(n / NB / place.N * place.N * 32 + n % NB * 32 * KROW));
+            else a[n] = lds_read16(more.at[(n - N) / NB % more.N] + (uint32_t)((n - N) / NB / more.N * more.N * 32 + n % NB * 32 * RROW));
+        };
 #pragma unroll
-        for (int n = 0; n < AHEAD && n < ST * NB; ++n) read(n);
+        for (int n = 0; n < AHEAD && n < ALL; ++n) read(n);
 #pragma unroll
-        for (int n = 0; n < ST * NB; ++n) {
-            if (n + AHEAD < ST * NB) read(n + AHEAD);
+        for (int n = 0; n < ALL; ++n) {
+            if (n + AHEAD < ALL) read(n + AHEAD);
             f32x16& x = s[0][n % NB];
-            x = n < NB ? Mat<E>::mma(a[n], w.q[0][n / NB], f32x16{}) : Mat<E>::mma(a[n], w.q[0][n / NB], x);
+            x = n < NB ? Mat<E>::mma(a[n], w.q[0][n / NB], f32x16{}) : Mat<E>::mma(a[n], w.q[0][(n < N ? n : n - N) / NB], x);
             beside(n);
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -210,7 +240,7 @@ __device__ __forceinline__ void rows_of(const A& p, RowsLds<DK, DV, KT>& lds) {
             if (more) {
                 multiply_keys(t + 1, next, [&](int n) {
 #pragma unroll
-                    for (int j = n * 8 / ST; j < (n + 1) * 8 / ST; ++j) power(j);
+                    for (int j = n * 8 / (ST + SR); j < (n + 1) * 8 / (ST + SR); ++j) power(j);
                 });
                 full = mask(t + 1, next);
             } else {
@@ -220,27 +250,36 @@ __device__ __forceinline__ void rows_of(const A& p, RowsLds<DK, DV, KT>& lds) {
             }
             w.l[0] += sum;
             top = -INFINITY;
-            ValuePlace<VROW> vp;
+            ValuePlace<VROW> vp, vq;
             vp.set(vbuf + (uint32_t)((t & 1) * VB), lane);
-            u32x4 a[CB * KS];
+            if constexpr (PAIRS) vq.set(lds_addr(&lds.vrest[0][0]) + (uint32_t)((t & 1) * VB), lane);
+            constexpr int N = CB * KS, P = PAIRS ? 2 : 1;         // products of a fragment and of its rest
+            u32x4 a[N * P];
+            auto read = [&](int n) { a[n] = n % P == 0 ? vp.read(n / P % CB, n / P / CB) : vq.read(n / P % CB, n / P / CB); };
 #pragma unroll
-            for (int n = 0; n < AHEAD && n < CB * KS; ++n) a[n] = vp.read(n % CB, n / CB);
+            for (int n = 0; n < AHEAD && n < N * P; ++n) read(n);
 #pragma unroll
-            for (int n = 0; n < CB * KS; ++n) {
-                if (n + AHEAD < CB * KS) a[n + AHEAD] = vp.read((n + AHEAD) % CB, (n + AHEAD) / CB);
-                const uint32_t* pp = &pr[0][n / CB / 2][(n / CB & 1) * 4];
-                w.o[0][n % CB] = Mat<E>::mma(a[n], u32x4{pp[0], pp[1], pp[2], pp[3]}, w.o[0][n % CB]);
+            for (int n = 0; n < N; ++n) {
+#pragma unroll
+                for (int q = 0; q < P; ++q) {
+                    if (n * P + q + AHEAD < N * P) read(n * P + q + AHEAD);
+                    const uint32_t* pp = &pr[0][n / CB / 2][(n / CB & 1) * 4];
+                    w.o[0][n % CB] = Mat<E>::mma(a[n * P + q], u32x4{pp[0], pp[1], pp[2], pp[3]}, w.o[0][n % CB]);
+                }
                 if constexpr (WIDE) {
                     const uint32_t* pl = &rest[n / CB / 2][(n / CB & 1) * 4];
-                    w.o[0][n % CB] = Mat<E>::mma(a[n], u32x4{pl[0], pl[1], pl[2], pl[3]}, w.o[0][n % CB]);
+                    w.o[0][n % CB] = Mat<E>::mma(a[n * P], u32x4{pl[0], pl[1], pl[2], pl[3]}, w.o[0][n % CB]);
                 }
 #pragma unroll
-                for (int j = n * 16 * NB / (CB * KS); j < (n + 1) * 16 * NB / (CB * KS); ++j)
+                for (int j = n * 16 * NB / N; j < (n + 1) * 16 * NB / N; ++j)
                     top = fmaxf(top, next[0][j / 16][j % 16]);       // (of no use behind the last)
                 asm volatile("" : "+v"(top));
                 __builtin_amdgcn_sched_barrier(0);
             }
-            if (!all) odd |= odd_values<E, false>(vbuf + (uint32_t)((t & 1) * VB), VB);
+            if (!all) {
+                odd |= odd_values<E, false>(vbuf + (uint32_t)((t & 1) * VB), VB);
+                if constexpr (PAIRS) odd |= odd_values<E, false>(lds_addr(&lds.vrest[0][0]) + (uint32_t)((t & 1) * VB), VB);
+            }
         }
         if (wave == 0 && t + 3 < tiles) place_rows(t + 3, page);
         if (t + 2 < tiles) widen(keys, t + 2);

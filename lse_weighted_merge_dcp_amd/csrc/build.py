@@ -24,7 +24,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 PKG = os.path.dirname(HERE)
 ROOT = os.path.dirname(PKG)
-SOURCES = ["attn.hip", "attn_latent.hip", "attn_mass.hip", "attn_rope.hip", "attn_evict.hip", "attn_plan.hip", "attn_project.hip", "attn_prefix.hip",
+SOURCES = ["attn.hip", "attn_latent.hip", "attn_mass.hip", "attn_rope.hip", "attn_evict.hip", "attn_plan.hip", "attn_project.hip", "attn_prefix.hip", "attn_pairs.hip",
            "attn_api.cpp",
            "api.cpp", "pack.hip", "combine.hip", "inplace.hip", "bench_api.cpp"]
 LIB = os.path.join(PKG, "libdcpmerge.so")
@@ -36,13 +36,14 @@ EXPORTS = {
     BENCH_LIB: ["dcpb_pack", "dcpb_unpack_combine", "dcpb_lse_combine_inplace", "dcpb_empty_kernel"],
     ATTN_LIB: ["dcpa_status_str", "dcpa_qk_norm_rope_append", "dcpa_paged_attn", "dcpa_paged_attn_workspace",
                "dcpa_attn_mass", "dcpa_attn_mass_workspace", "dcpa_cache_evict", "dcpa_batch_plan",
-               "dcpa_project", "dcpa_latent_expand", "dcpa_prefix_attn", "dcpa_prefix_attn_workspace"],
+               "dcpa_project", "dcpa_latent_expand", "dcpa_prefix_attn", "dcpa_prefix_attn_workspace",
+               "dcpa_pair_attn", "dcpa_pair_attn_workspace"],
 }
 OBJECTS = {
     LIB: ["api", "pack", "combine", "inplace"],
     BENCH_LIB: ["bench_api", "api", "pack", "combine", "inplace"],
     ATTN_LIB: ["attn_api", "attn", "attn_latent", "attn_mass", "attn_rope", "attn_evict", "attn_plan", "attn_project",
-               "attn_prefix"],
+               "attn_prefix", "attn_pairs"],
 }
 ARCH = "gfx950"
 

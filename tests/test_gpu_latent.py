@@ -2,9 +2,10 @@
 
 Tolerances.  A product sum of K terms in fp32, in any order: (K + 2) 2^-24 sum |x w|.  The result rounded once to the
 payload type: u |y|, u = eps / 2, and half the smallest subnormal.  An 8-bit cache's values are exact in 16 bits; the
-scale is one more fp32 rounding.  Attention over expanded rows is checked against attention over the rows as they were
-rounded (its own tolerances, attn_oracle), and against the exact definition with what those roundings can do: keys off
-by u |k| move a score by dS = u scale sum |q k|, values by u |v|."""
+scale is one more fp32 rounding.  A result in two parts is off by u^2 |y| (the rest of at most u |y| is rounded once more)
+and half the smallest subnormal.  Attention over expanded rows is checked against the exact definition with what the keys'
+and values' rounding r can do (r = u^2 in two parts, u rounded): keys off by r |k| move a score by dS = r scale sum |q k|,
+values by r |v|."""
 import math
 
 import pytest
@@ -170,6 +171,15 @@ def test_expand(kv, page, dims, dtype, cache):
     m = there[:, :, None, None]
     close(k, torch.where(m, ek, 9.0), torch.where(m, tk, 0.0))
     close(v, torch.where(m, ev, 9.0), torch.where(m, tv, 0.0))
+    # in two parts
+    k2, v2 = torch.full_like(k, 9.0), torch.full_like(v, 9.0)
+    kr, vr = torch.full_like(k[..., :dims[1]], 9.0).contiguous(), torch.full_like(v, 9.0)
+    attn.latent_expand(*p.gpu(), most, k_scale=p.ks, k_out=k2, v_out=v2, k_rest=kr, v_rest=vr)
+    assert torch.equal(k2, k) and torch.equal(v2, v)
+    for whole, rest, want, tol, c in ((k[..., :dims[1]], kr, ek[..., :dims[1]], tk[..., :dims[1]], dims[1]), (v, vr, ev, tv, dims[3])):
+        both = whole.cpu().double() + rest.cpu().double()
+        fine = tol - U[dtype] * want.abs() + U[dtype] ** 2 * want.abs()
+        close(both, torch.where(m, want, 18.0), torch.where(m, fine, 0.0))
     at = torch.arange(len(kv) * most).view(len(kv), most)
     want = torch.where(there, at, -1)
     counted = torch.arange(most)[None] < p.len[:, None]
@@ -223,9 +233,12 @@ def test_one_key_does_not_reach_another():
 
 @pytest.mark.parametrize("dtype,cache", [(torch.bfloat16, None), (torch.float16, torch.float8_e4m3fn)])
 @pytest.mark.parametrize("N,rank,inter", [(1, 0, 1), (4, 2, 1), (2, 1, 16)])
-def test_latent_attention(N, rank, inter, dtype, cache):
+@pytest.mark.parametrize("mode", ["parts", "wide", "rounded"])
+@pytest.mark.parametrize("dims", [(64, 16, 48, 128), (128, 64, 128, 64), (96, 32, 128, 72), (160, 64, 200, 64), (8, 0, 8, 16)])
+def test_latent_attention(N, rank, inter, mode, dims, dtype, cache):
     """The expanded form against the definition, and against the absorbed form over the same cache."""
-    H, Dn, Dr, Dv, Dc = 6, 64, 16, 48, 128
+    Dn, Dr, Dv, Dc = dims
+    H = 3
     seqs = [(40, 300), (1, 90), (7, 7), (0, 50)]
     lat = Problem(seqs, H, 1, Dc + Dr, Dc, dtype=dtype, cache=cache, page=16, N=N, rank=rank, inter=inter, shared=True, seed=3)
     if N == 1:
@@ -238,9 +251,11 @@ def test_latent_attention(N, rank, inter, dtype, cache):
     scale = (Dn + Dr) ** -0.5
     args = dict(seq_len=lat.seq.to(DEV), scale=scale, rank=rank, n_ranks=N, interleave=inter)
     cache_g, table, cu, kv = lat.k.to(DEV), lat.table.to(DEV), lat.cu.to(DEV), lat.kv.to(DEV)
-    out, lse = attn.dcp_latent_attn(q.to(DEV), cache_g, wg[:, :Dn], wg[:, Dn:], table, cu, kv, most, k_scale=lat.ks, **args)
+    out, lse = attn.dcp_latent_attn(q.to(DEV), cache_g, wg[:, :Dn], wg[:, Dn:], table, cu, kv, most, k_scale=lat.ks,
+                                    rounded=mode == "rounded", wide_weights=mode == "wide", **args)
     out, lse = out.cpu().double(), lse.cpu().double()
     u = U[dtype]
+    ur = u if mode == "rounded" else u * u
     for b, (n, _) in enumerate(seqs):
         m = lat.seen(b)
         row = lat.keys(b, 0)
@@ -256,12 +271,12 @@ def test_latent_attention(N, rank, inter, dtype, cache):
                     assert bool((out[r, h] == 0).all()) and float(lse[r, h]) == -math.inf
                     continue
                 s = scale * (key[m[i]] @ qd)
-                ds = float((scale * ((u * key[m[i]].abs() + kmag[m[i]]) @ qd.abs() +
-                                     (Dn + Dr + 4) * 2.0 ** -24 * (key[m[i]].abs() @ qd.abs()))).max())
+                ds = float((scale * ((ur * key[m[i]].abs() + kmag[m[i]] + FLOOR[dtype]) @ qd.abs() +
+                                     (2 * Dn + Dr + 4) * 2.0 ** -24 * (key[m[i]].abs() @ qd.abs()))).max())
                 p = torch.softmax(s, 0)
                 o, M = p @ val[m[i]], p @ val[m[i]].abs()
-                # the output's and a weight's rounding, the values' rounding and sums, the scores'
-                tol = u * o.abs() + 2 * u * M + p @ mag[m[i]] + (2 * ds * (1 + 2 * ds) + 2.0 ** -20) * M * (1 + 2 * u) + FLOOR[dtype]
+                # the output's and a weight's rounding (a wide weight's rest, 2^-16 or less), the values' and their sums', the scores'
+                tol = u * o.abs() + ((u * u if mode == "wide" and ur == u * u else u) + ur) * M + p @ mag[m[i]] + FLOOR[dtype] + (2 * ds * (1 + 2 * ds) + 2.0 ** -20) * M * (1 + 2 * u) + FLOOR[dtype]
                 assert bool(((out[r, h] - o).abs() <= tol).all())
                 assert abs(float(lse[r, h] - torch.logsumexp(s, 0))) <= ds + 2.0 ** -20 + 2.0 ** -22 * abs(float(lse[r, h]))
     # the absorbed form: other roundings (the latent queries' and outputs'), the same attention
@@ -273,6 +288,30 @@ def test_latent_attention(N, rank, inter, dtype, cache):
     seen = torch.isfinite(lse)
     assert torch.equal(seen, torch.isfinite(lse2.cpu()))
     assert float((got - out)[seen].abs().max()) <= tol and float((lse2.cpu().double() - lse)[seen].abs().max()) <= tol
+
+
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+@pytest.mark.parametrize("dims", [(64, 64, 64), (128, 64, 128), (192, 64, 200)])
+def test_latent_rows_that_are_masked_reach_no_token(dims, what):
+    """Not finite: a latent row that the first tokens of a chunk do not see, one behind the length, and buffers that hold
+    anything before the call."""
+    Dn, Dr, Dv, Dc, H = *dims, 96, 2
+    p = Rows([100], H, Dn, Dr, Dv, Dc, page=16, seed=7)
+    p.cache[int(p.table[0, 6]), 3] = what                       # key 99: seen by the last token alone
+    p.cache[int(p.table[0, 6]), 4:] = what
+    g = torch.Generator().manual_seed(8)
+    q = rand(g, 40, H, Dn + Dr).to(DEV)
+    cu = torch.tensor([0, 40], dtype=torch.int32, device=DEV)
+    full = lambda d: torch.full((1, 128, H, d), what, dtype=torch.bfloat16, device=DEV)       # noqa: E731
+    for rounded in (False, True):
+        more = {} if rounded else dict(k_rest=full(Dn), v_rest=full(Dv))
+        out, lse = attn.dcp_latent_attn(q, *p.gpu()[:4], cu, p.len.to(DEV), 128, rounded=rounded, k_out=full(Dn + Dr),
+                                        v_out=full(Dv), **more)
+        ref, rl = attn.dcp_latent_attn(q[:39], *p.gpu()[:4], torch.tensor([0, 39], dtype=torch.int32, device=DEV),
+                                       p.len.to(DEV) - 1, 128, rounded=rounded)
+        assert bool(torch.isfinite(out[:39]).all()) and bool(torch.isfinite(lse[:39]).all())
+        assert float((out[:39].float() - ref.float()).abs().max()) <= 2.0 ** -6 and float((lse[:39] - rl).abs().max()) <= 2.0 ** -14
+        assert not bool(torch.isfinite(out[39]).all())
 
 
 def test_layer_captured_and_replayed():
@@ -297,6 +336,7 @@ def test_layer_captured_and_replayed():
     qe = torch.empty(B, H, Dn + Dr, dtype=torch.bfloat16, device=DEV)
     lse2 = torch.empty_like(lse)
     ke, ve = (torch.zeros(B, 80, H, d, dtype=torch.bfloat16, device=DEV) for d in (Dn + Dr, Dv))
+    kr, vr = (torch.zeros(B, 80, H, d, dtype=torch.bfloat16, device=DEV) for d in (Dn, Dv))
     places = torch.empty(B, 80, dtype=torch.int32, device=DEV)
     ws = torch.empty(1 << 27, dtype=torch.uint8, device=DEV)
 
@@ -308,7 +348,7 @@ def test_layer_captured_and_replayed():
         qe[..., :Dn].copy_(q[..., :Dn])
         qe[..., Dn:].copy_(rot[..., Dc:])
         attn.dcp_latent_attn(qe, cache, w[:, :Dn], w[:, Dn:], table, cu, kv, 80, scale=0.1, out=y2, out_lse=lse2, k_out=ke,
-                             v_out=ve, places=places, workspace=ws)
+                             v_out=ve, k_rest=kr, v_rest=vr, places=places, workspace=ws)
 
     layer()
     graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
