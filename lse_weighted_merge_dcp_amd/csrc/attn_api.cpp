@@ -531,7 +531,7 @@ int dcpa_project(const dcpa_project_args* a, void* stream) {
     if (a->dtype != DCP_F16 && a->dtype != DCP_BF16) return DCP_ERR_DTYPE;
     auto cols = [](int64_t d) { return d >= 8 && d % 8 == 0 && d <= 1024; };
     if (a->T < 0 || a->T > kMaxRows || a->H < 1 || a->H > (1 << 16) || a->T * a->H > kMaxRows || !cols(a->N) ||
-        !cols(a->K) || (a->copy != 0 && !cols(a->copy)) || project_workgroups(a->T, a->H, a->N) > kMaxGrid)
+        !cols(a->K) || (a->copy != 0 && !cols(a->copy)) || project_tiles(a->T, a->H, a->N) >= kMaxRows)
         return DCP_ERR_SHAPE;
     const bool turned = a->w_N == 1;
     if (!strides_ok({a->x_T, a->x_H, a->w_H, a->w_N, a->w_K, a->y_T, a->y_H}) || (!turned && a->w_K != 1) ||

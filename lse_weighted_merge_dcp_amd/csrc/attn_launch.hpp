@@ -200,12 +200,12 @@ struct ProjectArgs {
     char* y;
     int64_t x_T, x_H, w_H, w_N, w_K, y_T, y_H;
     int32_t T, H, N, K, copy;
-    int32_t mt;              // row tiles
+    int32_t tiles, each;     // each: tiles of a workgroup
     FastDiv fH, fnt;         // fnt: column tiles
 };
 // turned: the weights of a head lie as [K][N] (else as [N][K]).
 hipError_t launch_project(const ProjectArgs& a, bool turned, bool bf16, hipStream_t stream);
-int64_t project_workgroups(int64_t T, int64_t H, int64_t N);
+int64_t project_tiles(int64_t T, int64_t H, int64_t N);
 
 struct ExpandArgs {
     const char* cache;
@@ -223,7 +223,8 @@ struct ExpandArgs {
     int64_t pl_B;
     int32_t B, H, Dn, Dr, Dv, Dc;
     int32_t most, keys;      // rows of the outputs; of these, what the page table can name
-    int32_t pages, mt, nt;   // row and column tiles
+    int32_t pages, mt, nt;   // row tiles of a sequence, column tiles
+    int32_t each;            // column tiles of a workgroup
     FastDiv fpage, fper;     // fper: Dn + Dv
     float ks;
 };

@@ -13,189 +13,260 @@ namespace dcpa {
 namespace {
 
 // ---------------------------------------------------------------------------
-// project_rows
+// project_rows: a workgroup takes p.each tiles in the order (rows, head, columns).
 // ---------------------------------------------------------------------------
+#ifndef PKT
+#define PKT 64
+#define POCC 2
+#define PMT 128
+#define PNT 128
+#define PST 2
+#endif
 template <typename E, int MT, int NT, int ST, bool TURNED>
-__global__ __launch_bounds__(256, 2) void project_rows(ProjectArgs p) {
-    using P = Product<E, MT, NT, 2, 2, ST, TURNED, false>;
+__global__ __launch_bounds__(256, POCC) void project_rows(ProjectArgs p) {
+    using P = Product<E, MT, NT, PKT, 2, 2, ST, TURNED, false>;
     __shared__ __attribute__((aligned(1024))) char lds[P::LDS];
-    // the column tiles of a unit (one head's row tile) follow each other on one XCD, which the heads keep
-    const uint32_t id = blockIdx.x, turn = fdiv(id >> 3, p.fnt);
-    const int nt = (int)((id >> 3) - turn * p.fnt.d);
-    const int64_t unit = (int64_t)turn * 8 + (id & 7);
-    if (unit >= (int64_t)p.mt * p.H) return;
-    const int m = (int)fdiv((uint32_t)unit, p.fH), head = (int)((uint32_t)unit - (uint32_t)m * p.fH.d);
-    const int row0 = m * MT, col0 = nt * NT;
-    P t(lds);
-    const char* x = p.x + (int64_t)head * p.x_H;
-    const char* w = p.w + (int64_t)head * p.w_H;
+    P c(lds);
+    const int first = (int)blockIdx.x * p.each, tiles = min(p.each, p.tiles - first);
+    if (tiles <= 0) return;
+    struct Tile {
+        int row0, head, col0;
+    };
+    auto tile = [&](int t) {
+        const uint32_t id = (uint32_t)(first + t), unit = fdiv(id, p.fnt), m = fdiv(unit, p.fH);
+        return Tile{(int)m * MT, (int)(unit - m * p.fH.d), (int)(id - unit * p.fnt.d) * NT};
+    };
+    auto aim = [&](int t) {
+        const Tile a = tile(t);
+        const char* x = p.x + (int64_t)a.head * p.x_H;
+        const char* w = p.w + (int64_t)a.head * p.w_H;
 #pragma unroll
-    for (int i = 0; i < P::NX; ++i) t.xat[i] = (uint64_t)(x + (int64_t)min(row0 + t.x_row(i), p.T - 1) * p.x_T);
-    bool n_here = true;
-    if constexpr (TURNED) {
-        n_here = col0 + t.wc * 8 < p.N;
+        for (int i = 0; i < P::NX; ++i) c.xat[i] = (uint64_t)(x + (int64_t)min(a.row0 + c.x_row(i), p.T - 1) * p.x_T);
+        if constexpr (TURNED) {
+            c.n_here = a.col0 + c.wc * 8 < p.N;
 #pragma unroll
-        for (int i = 0; i < P::NW; ++i) t.wat[i] = (uint64_t)(w + (int64_t)t.w_row(i) * p.w_K + (col0 + t.wc * 8) * 2);
-    } else {
+            for (int i = 0; i < P::NW; ++i) c.wat[i] = (uint64_t)(w + (int64_t)c.w_row(i) * p.w_K + (a.col0 + c.wc * 8) * 2);
+        } else {
 #pragma unroll
-        for (int i = 0; i < P::NW; ++i) t.wat[i] = (uint64_t)(w + (int64_t)min(col0 + t.w_row(i), p.N - 1) * p.w_N);
-    }
-    t.run(p.K, p.w_K, n_here);
-    char* y = p.y + (int64_t)head * p.y_H;
-    t.template store<false>(1.0f, [&](int row, int col, u32x4 v, u32x4) {
-        if (row0 + row < p.T && col0 + col < p.N)
-            *(u32x4*)(y + (int64_t)(row0 + row) * p.y_T + (col0 + col) * 2) = v;
-    });
-    if (nt == 0 && p.copy > 0) {
-        const int pieces = p.copy / 8;
-        for (int i = threadIdx.x; i < MT * pieces; i += 256) {
-            const int row = row0 + i / pieces, c = i % pieces;
-            if (row < p.T)
-                *(u32x4*)(y + (int64_t)row * p.y_T + (p.N + c * 8) * 2) = *(const u32x4*)(x + (int64_t)row * p.x_T + (p.K + c * 8) * 2);
+            for (int i = 0; i < P::NW; ++i) c.wat[i] = (uint64_t)(w + (int64_t)min(a.col0 + c.w_row(i), p.N - 1) * p.w_N);
         }
-    }
+    };
+    c.template run<P::STORES>(tiles, p.K, p.w_K, aim, [&](int t) {
+        const Tile a = tile(t);
+        const int col = a.col0 + c.out_col();
+        char* y = p.y + (int64_t)a.head * p.y_H;
+        char* to = y + (int64_t)a.row0 * p.y_T + col * 2;
+        const bool whole = a.row0 + MT <= p.T && a.col0 + NT <= p.N;
+        if (whole) c.template store<false>(1.0f, to, p.y_T, nullptr, 0, [](int) { return true; });
+        else c.template store<false>(1.0f, to, p.y_T, nullptr, 0, [&](int row) { return a.row0 + row < p.T && col < p.N; });
+        const bool copies = p.copy > 0 && a.col0 == 0;
+        if (copies) {
+            const char* x = p.x + (int64_t)a.head * p.x_H;
+            const int pieces = p.copy / 8;
+            for (int i = threadIdx.x; i < MT * pieces; i += 256) {
+                const int row = a.row0 + i / pieces, k = i % pieces;
+                if (row < p.T)
+                    *(u32x4*)(y + (int64_t)row * p.y_T + (p.N + k * 8) * 2) = *(const u32x4*)(x + (int64_t)row * p.x_T + (p.K + k * 8) * 2);
+            }
+        }
+        return whole && !copies;
+    });
 }
 
 // ---------------------------------------------------------------------------
-// expand_rows: a workgroup takes 256 keys of a sequence and 256 of the H (Dn + Dv)
-// weight rows.
+// expand_rows: a workgroup takes 256 keys of a sequence and p.each tiles of 256 of
+// the H (Dn + Dv) weight rows.
 // ---------------------------------------------------------------------------
+constexpr int MT = 256, NT = 256;
 template <typename E, bool X8, bool REST> __global__ __launch_bounds__(512, 2) void expand_rows(ExpandArgs p) {
-    using P = Product<E, 256, 256, 2, 4, 2, false, X8>;
+    using P = Product<E, MT, NT, 64, 2, 4, 2, false, X8>;
+    constexpr int ES = X8 ? 1 : 2, NR = 4;      // NR: the thread's pieces of the columns that all heads share, at most
     __shared__ __attribute__((aligned(1024))) char lds[P::LDS];
-    const int nt = (int)(blockIdx.x % (uint32_t)p.nt), rest = (int)(blockIdx.x / (uint32_t)p.nt);
-    const int b = rest / p.mt, row0 = (rest - b * p.mt) * 256, col0 = nt * 256;
+    // 8 row tiles by 4 ranges of columns at a time on one XCD (32 CUs), so that its L2 serves most of what they read
+    const uint32_t local = blockIdx.x >> 3, id = local % 32, super = local / 32 * 8 + (blockIdx.x & 7);
+    const uint32_t across = (uint32_t)(p.mt * p.B + 7) / 8;
+    const int mb = (int)(super % across * 8 + (id & 7)), nt0 = (int)(super / across * 4 + (id >> 3)) * p.each;
+    if (mb >= p.mt * p.B || nt0 >= p.nt) return;
+    const int b = mb / p.mt, row0 = (mb - b * p.mt) * MT, tiles = min(p.each, p.nt - nt0);
     // (a length may be more than the table has pages for: those keys are not there)
     const int counted = min(max(p.kv[b], 0), p.most), kv = min(counted, p.keys);
-    auto place_of = [&](int j, bool there) {
-        if (nt == 0 && p.places != nullptr && j < counted) p.places[(int64_t)b * p.pl_B + j] = there ? b * p.most + j : -1;
+    auto name = [&](int j, bool there) {
+        if (nt0 == 0 && p.places != nullptr && j < counted) p.places[(int64_t)b * p.pl_B + j] = there ? b * p.most + j : -1;
     };
     if (row0 >= kv) {
-        if (threadIdx.x < 256) place_of(row0 + (int)threadIdx.x, false);
+        if (threadIdx.x < MT) name(row0 + (int)threadIdx.x, false);
         return;
     }
-    constexpr int ES = X8 ? 1 : 2;
     const int per = p.Dn + p.Dv, cols = per * p.H;
     const int32_t* table = p.table + (int64_t)b * p.t_B;
-    P t(lds);
-    auto page_of = [&](int j, int& place) {
-        const uint32_t at = fdiv((uint32_t)j, p.fpage);
-        place = j - (int)(at * p.fpage.d);
-        return table[at];
+    P c(lds);
+    const char* base = p.cache;
+    // where cached row j lies (an address of zeros where its page is missing; the row of zeros is as long as the
+    // widest cached row)
+    auto row_at = [&](int j, bool& there) {
+        const uint32_t at = fdiv((uint32_t)j, p.fpage), place = (uint32_t)j - at * p.fpage.d;
+        const int page = table[at];
+        there = (uint32_t)page < (uint32_t)p.pages;
+        return at_or_zeros(there, (uint64_t)base + times64((uint32_t)page, p.c_P) + times64(place, p.c_S));
     };
 #pragma unroll
     for (int i = 0; i < P::NX; ++i) {
-        int place;
-        const int page = page_of(min(row0 + t.x_row(i), kv - 1), place);
-        const bool there = (uint32_t)page < (uint32_t)p.pages;
-        // (the row of zeros is as long as the widest cached row)
-        t.xat[i] = at_or_zeros(there, (uint64_t)p.cache + times64((uint32_t)page, p.c_P) + times64((uint32_t)place, p.c_S));
+        bool there;
+        c.xat[i] = row_at(min(row0 + c.x_row(i), kv - 1), there);
     }
+    // which rows of the tile are there: bit r of here[r / 64]
+    uint64_t here[MT / 64];
+    bool all_here = true;
 #pragma unroll
-    for (int i = 0; i < P::NW; ++i) {
-        const uint32_t n = (uint32_t)min(col0 + t.w_row(i), cols - 1), h = fdiv(n, p.fper);
-        const int d = (int)(n - h * (uint32_t)per);
-        t.wat[i] = d < p.Dn ? (uint64_t)(p.wk + (int64_t)h * p.wk_H + (int64_t)d * p.wk_N)
-                            : (uint64_t)(p.wv + (int64_t)h * p.wv_H + (int64_t)(d - p.Dn) * p.wv_N);
-    }
-    t.run(p.Dc, 0, true);
-    meet();
-    // which of the tile's keys are there
-    uint8_t* there_s = (uint8_t*)lds;
-    if (threadIdx.x < 256) {
-        const int j = row0 + (int)threadIdx.x;
-        int place;
+    for (int i = 0; i < MT / 64; ++i) {
+        const int j = row0 + i * 64 + c.lane;
         bool there = false;
-        if (j < kv) there = (uint32_t)page_of(j, place) < (uint32_t)p.pages;
-        there_s[threadIdx.x] = there;
-        place_of(j, there);
+        if (j < kv) row_at(j, there);
+        here[i] = __ballot(there);
+        all_here &= here[i] == ~0ull;
+        if (c.wave == 0) name(j, there);
     }
-    meet();
-    char* ko = p.ko + (int64_t)b * p.ko_B;
-    char* vo = p.vo + (int64_t)b * p.vo_B;
-    auto put = [&](int row, int col, u32x4 v, u32x4 rest) {
-        const int j = row0 + row;
-        const uint32_t n = (uint32_t)(col0 + col), h = fdiv(n, p.fper);
-        const int d = (int)(n - h * (uint32_t)per);
-        if ((int)n >= cols || !there_s[row]) return;
-        char* at = d < p.Dn ? ko + (int64_t)j * p.ko_S + (int64_t)h * p.ko_H + d * 2
-                            : vo + (int64_t)j * p.vo_S + (int64_t)h * p.vo_H + (d - p.Dn) * 2;
-        *(u32x4*)at = v;
-        if constexpr (REST) {
-            at = d < p.Dn ? p.kr + (int64_t)b * p.kr_B + (int64_t)j * p.kr_S + (int64_t)h * p.kr_H + d * 2
-                          : p.vr + (int64_t)b * p.vr_B + (int64_t)j * p.vr_S + (int64_t)h * p.vr_H + (d - p.Dn) * 2;
-            *(u32x4*)at = rest;
+    auto is_here = [&](int row) { return (here[row >> 6] >> (row & 63) & 1) != 0; };
+    // the columns that all heads share, held for all of them where they are few
+    const int pieces = p.Dr / 8;
+    const bool held = pieces <= NR * 512 / MT;
+    u32x4 rope[NR];
+    auto shared_piece = [&](int row, int k) {
+        bool there;
+        const char* from = (const char*)row_at(row0 + row, there) + (p.Dc + k * 8) * ES;
+        u32x4 v;
+        if constexpr (X8) v = widen8<E>(*(const u32x2*)from);
+        else v = *(const u32x4*)from;
+        if (p.ks != 1.0f) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = Mat<E>::pack2(Mat<E>::low(v[e]) * p.ks, Mat<E>::high(v[e]) * p.ks);
+        }
+        return v;
+    };
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const int n = i * 512 + c.tid;
+        rope[i] = u32x4{0, 0, 0, 0};
+        if (held && n < MT * pieces && is_here(n / pieces)) rope[i] = shared_piece(n / pieces, n % pieces);
+    }
+    // (a whole tile of one head makes as many stores in every wave)
+    const bool plain = all_here && per == NT && pieces == NR * 512 / MT;
+    auto aim = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < P::NW; ++i) {
+            const uint32_t n = (uint32_t)min((nt0 + t) * NT + c.w_row(i), cols - 1), h = fdiv(n, p.fper);
+            const int d = (int)(n - h * (uint32_t)per);
+            c.wat[i] = d < p.Dn ? (uint64_t)(p.wk + (int64_t)h * p.wk_H + (int64_t)d * p.wk_N)
+                                : (uint64_t)(p.wv + (int64_t)h * p.wv_H + (int64_t)(d - p.Dn) * p.wv_N);
         }
     };
-    t.template store<REST>(p.ks, put);
-    // the columns that all heads share, for the heads whose first weight row is this tile's
-    if (p.Dr > 0) {
-        const int h0 = (col0 + per - 1) / per, h1 = min((min(col0 + 256, cols) + per - 1) / per, p.H), pieces = p.Dr / 8;
-        for (int i = threadIdx.x; i < 256 * pieces; i += 512) {
-            const int row = i / pieces, c = i % pieces, j = row0 + row;
-            if (!there_s[row]) continue;
-            int place;
-            const int page = page_of(j, place);
-            const char* from = p.cache + (int64_t)page * p.c_P + (int64_t)place * p.c_S + (p.Dc + c * 8) * ES;
-            u32x4 v;
-            if constexpr (X8) {
-                v = widen8<E>(*(const u32x2*)from);
-                uint32_t s[4];
+    c.template run<P::STORES * (REST ? 2 : 1) + NR>(tiles, p.Dc, 0, aim, [&](int t) {
+        const int col0 = (nt0 + t) * NT;
+        const uint32_t n = (uint32_t)(col0 + c.out_col()), h = fdiv(n, p.fper);
+        const int d = (int)(n - h * (uint32_t)per);
+        const bool key = d < p.Dn, in = (int)n < cols;
+        char* to = key ? p.ko + (int64_t)b * p.ko_B + (int64_t)row0 * p.ko_S + (int64_t)h * p.ko_H + d * 2
+                       : p.vo + (int64_t)b * p.vo_B + (int64_t)row0 * p.vo_S + (int64_t)h * p.vo_H + (d - p.Dn) * 2;
+        char* rest = to;
+        if constexpr (REST)
+            rest = key ? p.kr + (int64_t)b * p.kr_B + (int64_t)row0 * p.kr_S + (int64_t)h * p.kr_H + d * 2
+                       : p.vr + (int64_t)b * p.vr_B + (int64_t)row0 * p.vr_S + (int64_t)h * p.vr_H + (d - p.Dn) * 2;
+        const int64_t to_S = key ? p.ko_S : p.vo_S, rest_S = key ? p.kr_S : p.vr_S;
+        char* ko = p.ko + (int64_t)b * p.ko_B + (int64_t)row0 * p.ko_S + p.Dn * 2;
+        if (plain) {
+            c.template store<REST>(p.ks, to, to_S, rest, rest_S, [](int) { return true; });
 #pragma unroll
-                for (int k = 0; k < 4; ++k) s[k] = Mat<E>::pack2(Mat<E>::low(v[k]) * p.ks, Mat<E>::high(v[k]) * p.ks);
-                v = u32x4{s[0], s[1], s[2], s[3]};
-            } else {
-                v = *(const u32x4*)from;
-                if (p.ks != 1.0f) {
-                    uint32_t s[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) s[k] = Mat<E>::pack2(Mat<E>::low(v[k]) * p.ks, Mat<E>::high(v[k]) * p.ks);
-                    v = u32x4{s[0], s[1], s[2], s[3]};
-                }
-            }
-            for (int h = h0; h < h1; ++h)
-                *(u32x4*)(ko + (int64_t)j * p.ko_S + (int64_t)h * p.ko_H + (p.Dn + c * 8) * 2) = v;
+            for (int i = 0; i < NR; ++i) *(u32x4*)(ko + (i * 64 + c.tid / 8) * p.ko_S + (int64_t)(nt0 + t) * p.ko_H + c.tid % 8 * 16) = rope[i];
+            return true;
         }
-    }
+        c.template store<REST>(p.ks, to, to_S, rest, rest_S, [&](int row) { return in && is_here(row); });
+        // the shared columns, of the heads whose first weight row is this tile's
+        const int h0 = (col0 + per - 1) / per, h1 = min((min(col0 + NT, cols) + per - 1) / per, p.H);
+        if (held) {
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const int n = i * 512 + c.tid;
+                if (n < MT * pieces && is_here(n / pieces))
+                    for (int e = h0; e < h1; ++e) *(u32x4*)(ko + n / pieces * p.ko_S + (int64_t)e * p.ko_H + n % pieces * 16) = rope[i];
+            }
+        } else {
+            for (int i = c.tid; i < MT * pieces; i += 512) {
+                const int row = i / pieces, k = i - row * pieces;
+                if (!is_here(row)) continue;
+                const u32x4 v = shared_piece(row, k);
+                for (int e = h0; e < h1; ++e) *(u32x4*)(ko + row * p.ko_S + (int64_t)e * p.ko_H + k * 16) = v;
+            }
+        }
+        return false;
+    });
 }
 
-template <typename E, int MT, int NT, int ST> hipError_t project(const ProjectArgs& arg, bool turned, hipStream_t stream) {
-    ProjectArgs a = arg;
-    a.mt = (a.T + MT - 1) / MT;
-    const int nt = (a.N + NT - 1) / NT;
-    a.fnt = dcp::make_fastdiv((uint32_t)nt);
-    const dim3 grid((uint32_t)(((int64_t)a.mt * a.H + 7) / 8 * 8 * nt)), block(256);
-    return turned ? launch(project_rows<E, MT, NT, ST, true>, grid, block, stream, a)
-                  : launch(project_rows<E, MT, NT, ST, false>, grid, block, stream, a);
+int64_t tiles_of(int64_t n, int64_t each) { return (n + each - 1) / each; }
+
+// How many of `all` tiles a workgroup takes where `slots` run at once: the rounds of the longest, each with a tile's
+// worth of start and end.
+int64_t share_of(int64_t all, int64_t slots) {
+    int64_t best = 1, price = tiles_of(all, slots) * 2;
+    for (int64_t rounds = 1; rounds <= 4; ++rounds) {
+        const int64_t each = tiles_of(all, slots * rounds), now = tiles_of(tiles_of(all, each), slots) * (each + 1);
+        if (now < price) {
+            price = now;
+            best = each;
+        }
+    }
+    return best;
 }
 
 // Rows of a tile.
 bool few_rows(int64_t T) { return T <= 128; }
-int64_t tiles_of(int64_t n, int64_t each) { return (n + each - 1) / each; }
+
+template <typename E, int MT, int NT, int ST> hipError_t project(const ProjectArgs& arg, bool turned, hipStream_t stream) {
+    ProjectArgs a = arg;
+    const int64_t nt = tiles_of(a.N, NT), all = tiles_of(a.T, MT) * a.H * nt;
+    a.fnt = dcp::make_fastdiv((uint32_t)nt);
+    a.tiles = (int32_t)all;
+    a.each = (int32_t)share_of(all, 512);
+    const dim3 grid((uint32_t)tiles_of(all, a.each)), block(256);
+    return turned ? launch(project_rows<E, MT, NT, ST, true>, grid, block, stream, a)
+                  : launch(project_rows<E, MT, NT, ST, false>, grid, block, stream, a);
+}
+
+// Weight tiles of a workgroup of expand_rows.
+int64_t expand_each(int64_t rows, int64_t nt) {
+    const int64_t ranges = 256 / rows;             // of columns, so that the workgroups fill the chip once
+    return ranges < 1 ? nt : tiles_of(nt, ranges);
+}
+int64_t expand_grid(int64_t rows, int64_t nt, int64_t each) {
+    // whole super tiles, a multiple of 8 of them
+    return tiles_of(tiles_of(rows, 8) * tiles_of(tiles_of(nt, each), 4), 8) * 8 * 32;
+}
 
 }  // namespace
 
-int64_t project_workgroups(int64_t T, int64_t H, int64_t N) {
+int64_t project_tiles(int64_t T, int64_t H, int64_t N) {
     const int64_t each = few_rows(T) ? 64 : 128;
-    return (tiles_of(T, each) * H + 7) / 8 * 8 * tiles_of(N, each);
+    return tiles_of(T, each) * H * tiles_of(N, each);
 }
 int64_t expand_workgroups(int64_t B, int64_t most, int64_t H, int64_t per) {
-    return B * tiles_of(most, 256) * tiles_of(H * per, 256);
+    const int64_t rows = B * tiles_of(most, MT), nt = tiles_of(H * per, NT);
+    return expand_grid(rows, nt, rows > 0 ? expand_each(rows, nt) : 1);
 }
 
 hipError_t launch_project(const ProjectArgs& a, bool turned, bool bf16, hipStream_t stream) {
     auto run = [&](auto e) {
         using E = decltype(e);
-        return few_rows(a.T) ? project<E, 64, 64, 4>(a, turned, stream) : project<E, 128, 128, 2>(a, turned, stream);
+        return few_rows(a.T) ? project<E, 64, 64, 4>(a, turned, stream) : project<E, PMT, PNT, PST>(a, turned, stream);
     };
     return bf16 ? run(BF16T{}) : run(F16T{});
 }
 
 hipError_t launch_expand(const ExpandArgs& arg, bool bf16, bool x8, hipStream_t stream) {
     ExpandArgs a = arg;
-    a.mt = (a.most + 255) / 256;
-    a.nt = (int32_t)(((int64_t)a.H * (a.Dn + a.Dv) + 255) / 256);
-    const dim3 grid((uint32_t)((int64_t)a.B * a.mt * a.nt)), block(512);
+    a.mt = (int32_t)tiles_of(a.most, MT);
+    a.nt = (int32_t)tiles_of((int64_t)a.H * (a.Dn + a.Dv), NT);
+    const int64_t rows = (int64_t)a.B * a.mt;
+    a.each = (int32_t)expand_each(rows, a.nt);
+    const dim3 grid((uint32_t)expand_grid(rows, a.nt, a.each)), block(512);
     auto run = [&](auto e) {
         using E = decltype(e);
         if (a.kr != nullptr)
