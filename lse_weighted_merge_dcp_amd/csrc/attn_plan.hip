@@ -55,31 +55,36 @@ template <typename F> __device__ __forceinline__ int find_end(int n, int at, F&&
     return lo;
 }
 
-// Row t of the step: sequence b, whose rows are [first, end); b == B: padding.
-__device__ __forceinline__ void write_token(const PlanArgs& p, int t, int b, int first, int end) {
-    int pos = -1, seq = -1;
-    int64_t slot = -1;
-    if (b < p.B) {
-        const int n = end - first, L = p.seq_out[b] - n, base = owned(p, L);
-        const int before = p.kv_out[b] - (owned(p, L + n) - base);
-        pos = L + t - first;
-        seq = b;
-        const uint32_t full = fdiv((uint32_t)pos, p.fblock);
-        const int rest = (int)((uint32_t)pos - full * p.fblock.d) - p.rank * p.inter;
-        if (rest >= 0 && rest < p.inter) {
-            const uint32_t j = (uint32_t)(before + (int)(full * (uint32_t)p.inter) + rest - base), at = fdiv(j, p.fpage);
-            if (at < (uint32_t)p.width) {
-                const int page = p.table[(int64_t)b * p.t_B + at];
-                if (page >= 0) slot = (int64_t)page * p.page_size + (int)(j - at * p.fpage.d);
-            }
-        }
-    }
+// The slot of position pos of a sequence that had L positions, `before` of its keys cached here, or -1.
+// page_at(i): entry i of its table row.
+template <typename F> __device__ __forceinline__ int64_t slot_of(const PlanArgs& p, int pos, int L, int before, F&& page_at) {
+    const uint32_t full = fdiv((uint32_t)pos, p.fblock);
+    const int rest = (int)((uint32_t)pos - full * p.fblock.d) - p.rank * p.inter;
+    if (rest < 0 || rest >= p.inter) return -1;
+    const uint32_t j = (uint32_t)(before + (int)(full * (uint32_t)p.inter) + rest - owned(p, L)), at = fdiv(j, p.fpage);
+    if (at >= (uint32_t)p.width) return -1;
+    const int page = page_at((int)at);
+    return page < 0 ? -1 : (int64_t)page * p.page_size + (int)(j - at * p.fpage.d);
+}
+__device__ __forceinline__ void write_row(const PlanArgs& p, int t, int pos, int seq, int64_t slot) {
     p.positions[t] = pos;
     p.sequence[t] = seq;
     p.slots[t] = slot;
 }
+// Row t of the step: sequence b, whose rows are [first, end); b == B: padding.
+__device__ __forceinline__ void write_token(const PlanArgs& p, int t, int b, int first, int end) {
+    if (b >= p.B) {
+        write_row(p, t, -1, -1, -1);
+        return;
+    }
+    const int n = end - first, L = p.seq_out[b] - n, before = p.kv_out[b] - (owned(p, L + n) - owned(p, L)), pos = L + t - first;
+    const int32_t* row = p.table + (int64_t)b * p.t_B;
+    write_row(p, t, pos, b, slot_of(p, pos, L, before, [&](int i) { return row[i]; }));
+}
 
 __global__ __launch_bounds__(kThreads) void plan_lengths(PlanArgs p) {
+    constexpr int EACH = 8;             // pages of a thread that are given back at a time
+    constexpr int FEW = 4;              // new tokens and pages up to which a sequence's thread writes them itself
     __shared__ int wave_s[kWaves];
     __shared__ int ends_s[kThreads], first_s[kThreads], rows_s[kThreads];
     const int tid = threadIdx.x;
@@ -100,9 +105,16 @@ __global__ __launch_bounds__(kThreads) void plan_lengths(PlanArgs p) {
     };
     auto sequence_of = [&](int k) { return find_end(kThreads, k, [&](int i) { return ends_s[i]; }); };
     load(0);
-    bool any = false;
-    for (int b = tid; b < p.B; b += kThreads) any |= (b == tid ? ended : p.new_len[b] < 0);
+    bool any = ended;
+    for (int b = tid + kThreads; b < p.B; b += kThreads) any |= p.new_len[b] < 0;
     int count = min(max(p.count[0], 0), p.free_max);
+    // the page that the sequence's first new key goes to, if it has it already (few sequences: asked for ahead of all else)
+    const bool one = p.B <= kThreads && p.T <= p.rows_here;
+    int last = -1;
+    if (one && n > 0) {
+        const uint32_t at = fdiv((uint32_t)m, p.fpage);
+        if (at < (uint32_t)p.width && at * p.fpage.d < (uint32_t)m) last = p.table[(int64_t)tid * p.t_B + at];
+    }
 
     // pages of ended sequences, in the order of sequences and pages, onto the list
     if (__syncthreads_or(any) != 0) {
@@ -114,17 +126,31 @@ __global__ __launch_bounds__(kThreads) void plan_lengths(PlanArgs p) {
             ends_s[tid] = incl;
             first_s[tid] = keep;
             __syncthreads();
-            for (int k0 = 0; k0 < total; k0 += kThreads) {
-                const int k = k0 + tid;
-                int page = -1;
-                if (k < total) {
-                    const int i = sequence_of(k);
-                    page = p.table[(int64_t)(b0 + i) * p.t_B + first_s[i] + (k - (i > 0 ? ends_s[i - 1] : 0))];
+            for (int k0 = 0; k0 < total; k0 += kThreads * EACH) {
+                int page[EACH];
+                bool gap = false;
+#pragma unroll
+                for (int e = 0; e < EACH; ++e) {
+                    const int k = k0 + e * kThreads + tid;
+                    page[e] = -1;
+                    if (k < total) {
+                        const int i = sequence_of(k);
+                        page[e] = p.table[(int64_t)(b0 + i) * p.t_B + first_s[i] + (k - (i > 0 ? ends_s[i - 1] : 0))];
+                        gap |= page[e] < 0;
+                    }
                 }
-                int pushed;
-                const int at = count + scan_block(page >= 0 ? 1 : 0, kMost, pushed, wave_s) - 1;
-                if (page >= 0 && at < p.free_max) p.free[at] = page;
-                count = min(count + pushed, p.free_max);
+                // (entries without a page leave no gaps in the list)
+                const bool gaps = __syncthreads_or(gap) != 0;
+#pragma unroll 1
+                for (int e = 0; e < EACH; ++e) {
+                    int pg = -1;
+#pragma unroll
+                    for (int i = 0; i < EACH; ++i) pg = i == e ? page[i] : pg;
+                    int at = count + tid, pushed = min(max(total - k0 - e * kThreads, 0), kThreads);
+                    if (gaps) at = count + scan_block(pg >= 0 ? 1 : 0, kMost, pushed, wave_s) - 1;
+                    if (pg >= 0 && at < p.free_max) p.free[at] = pg;
+                    count = min(count + pushed, p.free_max);
+                }
             }
             __syncthreads();
         }
@@ -132,6 +158,7 @@ __global__ __launch_bounds__(kThreads) void plan_lengths(PlanArgs p) {
     }
 
     int rows = 0, taken = 0;
+    bool done = false;                   // the token rows are written
     if (tid == 0) p.cu[0] = 0;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
         if (b0 > 0) load(b0);
@@ -140,27 +167,57 @@ __global__ __launch_bounds__(kThreads) void plan_lengths(PlanArgs p) {
         const int end = add_to(rows, scan_block(n, p.T, all, wave_s), p.T);
         rows_s[tid] = end;
         __syncthreads();
-        n = end - (tid > 0 ? rows_s[tid - 1] : rows);
+        const int first = tid > 0 ? rows_s[tid - 1] : rows;
+        n = end - first;
         rows = add_to(rows, all, p.T);
         const int kv = m + owned(p, L + n) - owned(p, L), held = pages_for(p, m);
-        ends_s[tid] = scan_block(ended || b0 + tid >= p.B ? 0 : max(pages_for(p, kv) - held, 0), kMost, pages, wave_s);
-        first_s[tid] = held;
+        const int need = ended || b0 + tid >= p.B ? 0 : max(pages_for(p, kv) - held, 0);
+        const int incl = scan_block(need, kMost, pages, wave_s);
         if (b0 + tid < p.B) {
             p.cu[b0 + tid + 1] = end;
             p.seq_out[b0 + tid] = ended ? 0 : L + n;
             p.kv_out[b0 + tid] = ended ? 0 : kv;
         }
-        __syncthreads();
-        for (int k = tid; k < pages; k += kThreads) {
-            const int i = sequence_of(k);
-            const int from = count - 1 - add_to(taken, k, kMost);
-            p.table[(int64_t)(b0 + i) * p.t_B + first_s[i] + (k - (i > 0 ? ends_s[i - 1] : 0))] = from >= 0 ? p.free[from] : -1;
+        // (the barriers of the scan stand between what was given back and what is taken)
+        if (one && __syncthreads_or(n > FEW || need > FEW) == 0) {
+            int got[FEW];
+            int32_t* row = p.table + (int64_t)tid * p.t_B;
+#pragma unroll
+            for (int i = 0; i < FEW; ++i) {
+                const int from = count - 1 - (incl - need + i);
+                got[i] = i < need && from >= 0 ? p.free[from] : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < FEW; ++i)
+                if (i < need) row[held + i] = got[i];
+#pragma unroll
+            for (int i = 0; i < FEW; ++i)
+                if (i < n)
+                    write_row(p, first + i, L + i, tid, slot_of(p, L + i, L, m, [&](int at) {
+                                  int page = last;
+#pragma unroll
+                                  for (int e = 0; e < FEW; ++e) page = at == held + e ? got[e] : page;
+                                  return page;
+                              }));
+            for (int t = rows + tid; t < p.T; t += kThreads) write_row(p, t, -1, -1, -1);
+            done = true;
+        } else {
+            ends_s[tid] = incl;
+            first_s[tid] = held;
+            __syncthreads();
+            for (int k = tid; k < pages; k += kThreads) {
+                const int i = sequence_of(k);
+                const int from = count - 1 - add_to(taken, k, kMost);
+                p.table[(int64_t)(b0 + i) * p.t_B + first_s[i] + (k - (i > 0 ? ends_s[i - 1] : 0))] = from >= 0 ? p.free[from] : -1;
+            }
         }
         taken = add_to(taken, pages, kMost);
         __syncthreads();
     }
     if (tid == 0) p.count_out[0] = count - taken;
-    if (p.T > p.rows_here) return;
+    if (p.B == 0)
+        for (int t = tid; t < p.T; t += kThreads) write_row(p, t, -1, -1, -1);
+    if (done || p.B == 0 || p.T > p.rows_here) return;
     __syncthreads();
     for (int t = tid; t < p.T; t += kThreads) {
         const int b = p.B <= kThreads ? find_end(p.B, t, [&](int i) { return rows_s[i]; })

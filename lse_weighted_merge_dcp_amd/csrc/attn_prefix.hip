@@ -77,14 +77,14 @@ namespace {
 // prefix_list: the units of a call, by one workgroup: a thread to an entry (group
 // or sequence), then a thread to a unit.
 //
-// The key ranges' length is chosen among 64 that cut the longest entry evenly:
+// The key ranges' length is chosen among 32 that cut the longest entry evenly:
 // with U units of which the longest takes c keys, `slots` of them at once and a
 // price of kPrice keys to a unit (its start and its part), either all run at once
 // and take c + kPrice, or their mean load and one unit more.
 // ---------------------------------------------------------------------------
-constexpr int kThreads = 1024, kWaves = kThreads / 64, kTries = 64, kPrice = 128;
+constexpr int kThreads = 1024, kWaves = kThreads / 64, kTries = 32, kPrice = 128;
 constexpr int kMost = 1 << 30;
-// in how many ranges: each number about an eighth above the last
+// in how many ranges: each number about a quarter above the last
 struct Ways {
     uint16_t n[kTries];
 };
@@ -93,7 +93,7 @@ constexpr Ways make_ways() {
     int n = 1;
     for (int k = 0; k < kTries; ++k) {
         w.n[k] = (uint16_t)n;
-        n += n < 8 ? 1 : n / 8;
+        n += n < 4 ? 1 : n / 4;
     }
     return w;
 }
@@ -155,23 +155,28 @@ __device__ __forceinline__ Entry load_entry(const GroupArgs& p, int v) {
 }
 
 __global__ __launch_bounds__(kThreads) void prefix_list(GroupArgs p) {
-    __shared__ int64_t work_s[kWaves], units_s[kTries];
+    __shared__ float work_s[kWaves], units_s[kTries];
     __shared__ Entry entry_s[kThreads];
     __shared__ int ends_s[kThreads], odd_s[kThreads], splits_s[kThreads], length_s[kTries];
     __shared__ int scan_s[2][kWaves], longest_s[kWaves], chunk_s;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, all = p.groups + p.m.B;
     // work and the longest entry; the first 1024 entries stay in LDS
     Entry x{};
-    int64_t work = 0;
+    float work = 0.0f;
     int longest = 0;
     for (int v0 = 0; v0 < all; v0 += kThreads) {
         const Entry y = load_entry(p, v0 + tid);
-        work += (int64_t)y.tiles * y.keys;
+        work += (float)y.tiles * (float)y.keys;
         if (y.tiles > 0) longest = max(longest, y.keys);
         if (v0 == 0) x = y;
     }
     entry_s[tid] = x;
-    work = sum_wave(work);
+    auto add_all = [](float y) {
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) y += __shfl_xor(y, d, 64);
+        return y;
+    };
+    work = add_all(work);
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) longest = max(longest, __shfl_xor(longest, d, 64));
     if (lane == 0) {
@@ -179,19 +184,20 @@ __global__ __launch_bounds__(kThreads) void prefix_list(GroupArgs p) {
         longest_s[wave] = longest;
     }
     __syncthreads();
-    work = 0;
+    work = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
         work += work_s[w];
         longest = max(longest, longest_s[w]);
     }
     // the ranges' lengths that are tried, and the units that each of them makes
-    const int ways = kWays.n[lane];
+    const int ways = kWays.n[lane % kTries];
     const int c = max(2, ((longest + ways - 1) / ways + p.step - 1) / p.step) * p.step;
-    if (wave == 0) length_s[lane] = c;
+    if (wave == 0 && lane < kTries) length_s[lane] = c;
     for (int k = wave; k < kTries; k += kWaves) {
         const int len = __builtin_amdgcn_readlane(c, k);
-        int64_t n = 0;
+        const float inv = 1.0f / (float)len;
+        float n = 0.0f;              // (exact up to 2^24, more than a launch may have)
         for (int v0 = 0; v0 < all; v0 += 64) {
             const int v = v0 + lane;
             int t, keys;
@@ -203,17 +209,18 @@ __global__ __launch_bounds__(kThreads) void prefix_list(GroupArgs p) {
                 t = y.tiles;
                 keys = y.keys;
             }
-            n += (int64_t)t * max(1, (int)(((uint32_t)keys + (uint32_t)len - 1u) / (uint32_t)len));
+            const int q = (int)((float)keys * inv), rest = keys - q * len;      // (q off by one at most)
+            n += (float)t * (float)max(1, q + (rest > 0 ? 1 : 0) + (rest > len ? 1 : 0));
         }
-        n = sum_wave(n);
+        n = add_all(n);
         if (lane == 0) units_s[k] = n;
     }
     __syncthreads();
     if (wave == 0) {
-        const int64_t n = units_s[lane];
-        const float most = (float)min(c, max(longest, 1)), load = ((float)work + (float)n * kPrice) / (float)p.share;
-        float price = n <= p.share ? most + kPrice : load + most;
-        if (n > p.units && lane > 0) price = 3.0e38f;       // (whole entries always fit)
+        const float n = units_s[lane % kTries];
+        const float most = (float)min(c, max(longest, 1)), load = (work + n * kPrice) / (float)p.share;
+        float price = n <= (float)p.share ? most + kPrice : load + most;
+        if (n > (float)p.units && lane > 0) price = 3.0e38f;       // (whole entries always fit)
         float best = price;
 #pragma unroll
         for (int d = 32; d > 0; d >>= 1) best = fminf(best, __shfl_xor(best, d, 64));
