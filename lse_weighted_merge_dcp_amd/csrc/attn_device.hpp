@@ -239,6 +239,22 @@ __device__ __forceinline__ int scan_upto(int x, int most) {
     x = scan_step<0x142, 0xa>(x, most);
     return scan_step<0x143, 0xc>(x, most);
 }
+// The wave's sum, largest or smallest value, for every lane: OP(a, b) over rows of 16 lanes, then across them
+// (exchanges within the vector unit: a shuffle through LDS takes a hundred clocks).  `none`: OP's neutral value.
+template <int CTRL, int ROWS, typename T, typename F> __device__ __forceinline__ T fold_step(T x, T none, F&& op) {
+    static_assert(sizeof(T) == 4, "one register");
+    const int y = __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, x), CTRL, ROWS, 0xf, false);
+    return op(x, __builtin_bit_cast(T, y));
+}
+template <typename T, typename F> __device__ __forceinline__ T fold_wave(T x, T none, F&& op) {
+    x = fold_step<0x111, 0xf>(x, none, op);
+    x = fold_step<0x112, 0xf>(x, none, op);
+    x = fold_step<0x114, 0xf>(x, none, op);
+    x = fold_step<0x118, 0xf>(x, none, op);
+    x = fold_step<0x142, 0xa>(x, none, op);
+    x = fold_step<0x143, 0xc>(x, none, op);
+    return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63));
+}
 // x plus the x of the lane that CTRL names, over the rows of lanes in ROWS (each half moved as 32 bits)
 template <int CTRL, int ROWS> __device__ __forceinline__ double add_from(double x) {
     const uint64_t u = __builtin_bit_cast(uint64_t, x);

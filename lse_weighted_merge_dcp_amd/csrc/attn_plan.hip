@@ -30,18 +30,14 @@ __device__ __forceinline__ int pages_for(const PlanArgs& p, int keys) {
 // Inclusive sum over the workgroup; every thread gets the whole in `all`.
 __device__ __forceinline__ int scan_block(int x, int most, int& all, int (&wave_s)[kWaves]) {
     x = scan_upto(x, most);
-    const int wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = (int)dcp::wave_id();
     __syncthreads();                    // (the last call's sums have been read)
-    if ((threadIdx.x & 63) == 63) wave_s[wave] = x;
+    if (lane == 63) wave_s[wave] = x;
     __syncthreads();
-    all = 0;
-    int before = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        if (w == wave) before = all;
-        all = add_to(all, wave_s[w], most);
-    }
-    return add_to(before, x, most);
+    // (a lane to a wave: a loop over them all is five times the code, and code that is run once waits to be fetched)
+    const int to = scan_upto(lane < kWaves ? wave_s[lane] : 0, most);
+    all = __builtin_amdgcn_readlane(to, kWaves - 1);
+    return wave > 0 ? add_to(__builtin_amdgcn_readlane(to, wave - 1), x, most) : x;
 }
 
 // The first i in [0, n) with ends(i) > at (n if there is none; ends do not fall).
@@ -103,7 +99,7 @@ __global__ __launch_bounds__(kThreads) void plan_lengths(PlanArgs p) {
         ended = n < 0;
         n = min(max(n, 0), kMost - 1 - L);
     };
-    auto sequence_of = [&](int k) { return find_end(kThreads, k, [&](int i) { return ends_s[i]; }); };
+    auto sequence_of = [&](int k) { return find_end(min(p.B, kThreads), k, [&](int i) { return ends_s[i]; }); };
     load(0);
     bool any = ended;
     for (int b = tid + kThreads; b < p.B; b += kThreads) any |= p.new_len[b] < 0;

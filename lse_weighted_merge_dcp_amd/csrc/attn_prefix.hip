@@ -99,6 +99,12 @@ constexpr Ways make_ways() {
 }
 __device__ const Ways kWays = make_ways();
 
+// In how many ranges of `len` keys `keys` are cut, one at least; inv: 1 / len.
+__device__ __forceinline__ int ranges_of(int keys, int len, float inv) {
+    const int q = (int)((float)keys * inv), rest = keys - q * len;      // (q off by one at most: keys / len < 2^14)
+    return max(1, q + (rest > 0 ? 1 : 0) + (rest > len ? 1 : 0));
+}
+
 // Sequences of group g, and how many keys they share.
 struct Group {
     int b0, b1, keys;
@@ -133,17 +139,22 @@ struct Entry {
 };
 // (128 or 32 rows to a tile)
 __device__ __forceinline__ int tiles_for(int each, int rows) { return (rows + each - 1) >> (each == 128 ? 7 : 5); }
-__device__ __forceinline__ Entry load_entry(const GroupArgs& p, int v) {
+// The rows of a group.
+__device__ __forceinline__ void group_rows(const GroupArgs& p, Entry& x, int first, int end) {
+    x.s.first = first;
+    x.s.n = max(end - first, 0);
+    x.tiles = x.keys > 0 ? tiles_for(p.rows, x.s.n * p.m.G) : 0;
+}
+// rows: also those of a group, which take one more load after the others.
+__device__ __forceinline__ Entry load_entry(const GroupArgs& p, int v, bool rows) {
     Entry x{};
     x.even = true;
     if (v < p.groups) {
         const Group y = load_group(p, v);
-        x.s.first = min(max(p.m.cu[y.b0], 0), p.m.T);
-        x.s.n = min(max(p.m.cu[y.b1], x.s.first), p.m.T) - x.s.first;
         x.keys = x.s.kv = y.keys;
-        x.tiles = y.keys > 0 ? tiles_for(p.rows, x.s.n * p.m.G) : 0;
         x.b0 = y.b0;
         x.b1 = y.b1;
+        if (rows) group_rows(p, x, min(max(p.m.cu[y.b0], 0), p.m.T), min(max(p.m.cu[y.b1], 0), p.m.T));
     } else if (v < p.groups + p.m.B) {
         x.s = load_seq(p.m, v - p.groups);
         x.begin = shared_of(p, v - p.groups);
@@ -159,37 +170,46 @@ __global__ __launch_bounds__(kThreads) void prefix_list(GroupArgs p) {
     __shared__ Entry entry_s[kThreads];
     __shared__ int ends_s[kThreads], odd_s[kThreads], splits_s[kThreads], length_s[kTries];
     __shared__ int scan_s[2][kWaves], longest_s[kWaves], chunk_s;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, all = p.groups + p.m.B;
+    const int tid = threadIdx.x, lane = tid & 63, wave = (int)dcp::wave_id(), all = p.groups + p.m.B;
     // work and the longest entry; the first 1024 entries stay in LDS
     Entry x{};
     float work = 0.0f;
     int longest = 0;
-    for (int v0 = 0; v0 < all; v0 += kThreads) {
-        const Entry y = load_entry(p, v0 + tid);
+    const bool held = all <= kThreads;       // all of them
+    auto count = [&](const Entry& y) {
         work += (float)y.tiles * (float)y.keys;
         if (y.tiles > 0) longest = max(longest, y.keys);
-        if (v0 == 0) x = y;
-    }
-    entry_s[tid] = x;
-    auto add_all = [](float y) {
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) y += __shfl_xor(y, d, 64);
-        return y;
     };
-    work = add_all(work);
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) longest = max(longest, __shfl_xor(longest, d, 64));
+    x = load_entry(p, tid, !held);
+    entry_s[tid] = x;
+    if (held) {
+        __syncthreads();
+        if (tid < p.groups) {
+            // (row b's place is the end of row b - 1; an empty group stands in its place among the others)
+            auto place = [&](int b) {
+                if (b == 0) return entry_s[p.groups].s.first;
+                const Seq y = entry_s[p.groups + b - 1].s;
+                return y.first + y.n;
+            };
+            group_rows(p, x, place(x.b0), place(x.b1));
+        }
+        __syncthreads();
+        if (tid < p.groups) entry_s[tid] = x;
+    }
+    count(x);
+    for (int v0 = kThreads; v0 < all; v0 += kThreads) count(load_entry(p, v0 + tid, true));
+    auto add = [](float a, float b) { return a + b; };
+    work = fold_wave(work, 0.0f, add);
+    auto most_of = [](int a, int b) { return max(a, b); };
+    longest = fold_wave(longest, 0, most_of);
     if (lane == 0) {
         work_s[wave] = work;
         longest_s[wave] = longest;
     }
     __syncthreads();
-    work = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        work += work_s[w];
-        longest = max(longest, longest_s[w]);
-    }
+    // (a lane to a wave: a loop over them all is five times the code, and code that is run once waits to be fetched)
+    work = fold_wave(lane < kWaves ? work_s[lane] : 0.0f, 0.0f, add);
+    longest = fold_wave(lane < kWaves ? longest_s[lane] : 0, 0, most_of);
     // the ranges' lengths that are tried, and the units that each of them makes
     const int ways = kWays.n[lane % kTries];
     const int c = max(2, ((longest + ways - 1) / ways + p.step - 1) / p.step) * p.step;
@@ -205,14 +225,13 @@ __global__ __launch_bounds__(kThreads) void prefix_list(GroupArgs p) {
                 t = entry_s[v].tiles;
                 keys = entry_s[v].keys;
             } else {
-                const Entry y = load_entry(p, v);
+                const Entry y = load_entry(p, v, true);
                 t = y.tiles;
                 keys = y.keys;
             }
-            const int q = (int)((float)keys * inv), rest = keys - q * len;      // (q off by one at most)
-            n += (float)t * (float)max(1, q + (rest > 0 ? 1 : 0) + (rest > len ? 1 : 0));
+            n += (float)t * (float)ranges_of(keys, len, inv);
         }
-        n = add_all(n);
+        n = fold_wave(n, 0.0f, add);
         if (lane == 0) units_s[k] = n;
     }
     __syncthreads();
@@ -221,9 +240,7 @@ __global__ __launch_bounds__(kThreads) void prefix_list(GroupArgs p) {
         const float most = (float)min(c, max(longest, 1)), load = (work + n * kPrice) / (float)p.share;
         float price = n <= (float)p.share ? most + kPrice : load + most;
         if (n > (float)p.units && lane > 0) price = 3.0e38f;       // (whole entries always fit)
-        float best = price;
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) best = fminf(best, __shfl_xor(best, d, 64));
+        const float best = fold_wave(price, 3.0e38f, [](float a, float b) { return fminf(a, b); });
         if (lane == 0) chunk_s = length_s[0];
         const uint64_t at = __ballot(price == best);
         if (at != 0 && lane == __builtin_ctzll(at)) chunk_s = c;
@@ -234,10 +251,10 @@ __global__ __launch_bounds__(kThreads) void prefix_list(GroupArgs p) {
     int base = 0;
     for (int v0 = 0; v0 < all; v0 += kThreads) {
         if (v0 > 0) {
-            x = load_entry(p, v0 + tid);
+            x = load_entry(p, v0 + tid, true);
             entry_s[tid] = x;
         }
-        const int v = v0 + tid, splits = max(1, (int)(((uint32_t)x.keys + (uint32_t)chunk - 1u) / (uint32_t)chunk));
+        const int v = v0 + tid, splits = ranges_of(x.keys, chunk, 1.0f / (float)chunk);
         // units and sequences that see less than is shared, counted up to each entry
         // (lengths that contradict each other may add up to anything: no sum passes kMost)
         const int mine = (int)min((int64_t)x.tiles * splits, (int64_t)kMost);
@@ -247,12 +264,11 @@ __global__ __launch_bounds__(kThreads) void prefix_list(GroupArgs p) {
             scan_s[1][wave] = odd;
         }
         __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w)
-            if (w < wave) {
-                ends = add_to(ends, scan_s[0][w], kMost);
-                odd += scan_s[1][w];
-            }
+        const int e_to = scan_upto(lane < kWaves ? scan_s[0][lane] : 0, kMost), o_to = scan_incl(lane < kWaves ? scan_s[1][lane] : 0);
+        if (wave > 0) {
+            ends = add_to(ends, __builtin_amdgcn_readlane(e_to, wave - 1), kMost);
+            odd += __builtin_amdgcn_readlane(o_to, wave - 1);
+        }
         ends = add_to(base, ends, kMost);
         ends_s[tid] = ends;
         odd_s[tid] = odd;
@@ -261,7 +277,7 @@ __global__ __launch_bounds__(kThreads) void prefix_list(GroupArgs p) {
         __syncthreads();
         const int top = ends_s[kThreads - 1];
         for (int id = base + tid; id < min(top, p.units); id += kThreads) {
-            int lo = 0, hi = kThreads - 1;
+            int lo = 0, hi = min(all - v0, kThreads) - 1;
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
                 if (ends_s[mid] > id) hi = mid;
@@ -269,7 +285,8 @@ __global__ __launch_bounds__(kThreads) void prefix_list(GroupArgs p) {
             }
             const int e = v0 + lo, s = splits_s[lo], rest = id - (lo > 0 ? ends_s[lo - 1] : base);
             const Entry y = entry_s[lo];
-            const int back = (int)((uint32_t)rest / (uint32_t)s);
+            int back = (int)((float)rest / (float)s);          // (off by one at most)
+            back += back * s > rest ? -1 : (back + 1) * s <= rest ? 1 : 0;
             PrefixUnit u{};
             u.first = y.s.first; u.n = y.s.n; u.kv = y.s.kv; u.len = y.s.len;
             u.begin = y.begin; u.end = y.begin + y.keys;
