@@ -171,9 +171,9 @@ template <typename E, int MT_, int NT_, int KT_, int WM, int WN, int ST, bool TU
     }
     // The wave's results times `scale`, rounded, to the rows of the tile, `at` being where the columns out_col() .. + 7
     // of its first row lie and `bytes` a row's distance from the next; ok(row): whether they are written.  REST:
-    // what the rounding left as well, likewise.
+    // what the rounding left as well, likewise.  FAR: results that no cache will hold until they are read.
     __device__ __forceinline__ int out_col() const { return wn * BN * 32 + lane % OC * 8; }
-    template <bool REST, typename F>
+    template <bool REST, bool FAR, typename F>
     __device__ __forceinline__ void store(float scale, char* at, int64_t bytes, char* rest, int64_t rest_bytes, F&& ok) {
         at += (wm * BM * 32 + lane / OC) * bytes;
         rest += (wm * BM * 32 + lane / OC) * rest_bytes;
@@ -213,7 +213,11 @@ template <typename E, int MT_, int NT_, int KT_, int WM, int WN, int ST, bool TU
                 for (int k = 0; k < OC / 2; ++k) {
                     const int row = k * (64 / OC) + lane / OC;
                     const u32x4 v = lds_read16(os + place(row, lane % OC));
-                    if (ok((wm * BM + j) * 32 + row)) *(u32x4*)(pass == 0 ? at : rest) = v;
+                    if (ok((wm * BM + j) * 32 + row)) {
+                        u32x4* to = (u32x4*)(pass == 0 ? at : rest);
+                        if constexpr (FAR) __builtin_nontemporal_store(v, to);
+                        else *to = v;
+                    }
                     // (from one row to the next, not all the addresses at once)
                     if (pass == 0) {
                         at += 64 / OC * bytes;

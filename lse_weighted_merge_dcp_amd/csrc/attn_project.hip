@@ -22,7 +22,7 @@ namespace {
 #define PNT 128
 #define PST 2
 #endif
-template <typename E, int MT, int NT, int ST, bool TURNED>
+template <typename E, int MT, int NT, int ST, bool TURNED, bool FAR>
 __global__ __launch_bounds__(256, POCC) void project_rows(ProjectArgs p) {
     using P = Product<E, MT, NT, PKT, 2, 2, ST, TURNED, false>;
     __shared__ __attribute__((aligned(1024))) char lds[P::LDS];
@@ -57,8 +57,8 @@ __global__ __launch_bounds__(256, POCC) void project_rows(ProjectArgs p) {
         char* y = p.y + (int64_t)a.head * p.y_H;
         char* to = y + (int64_t)a.row0 * p.y_T + col * 2;
         const bool whole = a.row0 + MT <= p.T && a.col0 + NT <= p.N;
-        if (whole) c.template store<false>(1.0f, to, p.y_T, nullptr, 0, [](int) { return true; });
-        else c.template store<false>(1.0f, to, p.y_T, nullptr, 0, [&](int row) { return a.row0 + row < p.T && col < p.N; });
+        if (whole) c.template store<false, FAR>(1.0f, to, p.y_T, nullptr, 0, [](int) { return true; });
+        else c.template store<false, FAR>(1.0f, to, p.y_T, nullptr, 0, [&](int row) { return a.row0 + row < p.T && col < p.N; });
         const bool copies = p.copy > 0 && a.col0 == 0;
         if (copies) {
             const char* x = p.x + (int64_t)a.head * p.x_H;
@@ -78,7 +78,7 @@ __global__ __launch_bounds__(256, POCC) void project_rows(ProjectArgs p) {
 // the H (Dn + Dv) weight rows.
 // ---------------------------------------------------------------------------
 constexpr int MT = 256, NT = 256;
-template <typename E, bool X8, bool REST> __global__ __launch_bounds__(512, 2) void expand_rows(ExpandArgs p) {
+template <typename E, bool X8, bool REST, bool FAR> __global__ __launch_bounds__(512, 2) void expand_rows(ExpandArgs p) {
     using P = Product<E, MT, NT, 64, 2, 4, 2, false, X8>;
     constexpr int ES = X8 ? 1 : 2, NR = 4;      // NR: the thread's pieces of the columns that all heads share, at most
     __shared__ __attribute__((aligned(1024))) char lds[P::LDS];
@@ -174,12 +174,12 @@ template <typename E, bool X8, bool REST> __global__ __launch_bounds__(512, 2) v
         const int64_t to_S = key ? p.ko_S : p.vo_S, rest_S = key ? p.kr_S : p.vr_S;
         char* ko = p.ko + (int64_t)b * p.ko_B + (int64_t)row0 * p.ko_S + p.Dn * 2;
         if (plain) {
-            c.template store<REST>(p.ks, to, to_S, rest, rest_S, [](int) { return true; });
+            c.template store<REST, FAR>(p.ks, to, to_S, rest, rest_S, [](int) { return true; });
 #pragma unroll
             for (int i = 0; i < NR; ++i) *(u32x4*)(ko + (i * 64 + c.tid / 8) * p.ko_S + (int64_t)(nt0 + t) * p.ko_H + c.tid % 8 * 16) = rope[i];
             return true;
         }
-        c.template store<REST>(p.ks, to, to_S, rest, rest_S, [&](int row) { return in && is_here(row); });
+        c.template store<REST, FAR>(p.ks, to, to_S, rest, rest_S, [&](int row) { return in && is_here(row); });
         // the shared columns, of the heads whose first weight row is this tile's
         const int h0 = (col0 + per - 1) / per, h1 = min((min(col0 + NT, cols) + per - 1) / per, p.H);
         if (held) {
@@ -217,6 +217,9 @@ int64_t share_of(int64_t all, int64_t slots) {
     return best;
 }
 
+// Results of an eighth of the Infinity Cache and more go out with the nontemporal hint.
+bool far_out(int64_t bytes) { return bytes >= (int64_t(1) << 25); }
+
 // Rows of a tile.
 bool few_rows(int64_t T) { return T <= 128; }
 
@@ -227,8 +230,12 @@ template <typename E, int MT, int NT, int ST> hipError_t project(const ProjectAr
     a.tiles = (int32_t)all;
     a.each = (int32_t)share_of(all, 512);
     const dim3 grid((uint32_t)tiles_of(all, a.each)), block(256);
-    return turned ? launch(project_rows<E, MT, NT, ST, true>, grid, block, stream, a)
-                  : launch(project_rows<E, MT, NT, ST, false>, grid, block, stream, a);
+    const bool far = far_out((int64_t)a.T * a.H * a.N * 2);
+    if (turned)
+        return far ? launch(project_rows<E, MT, NT, ST, true, true>, grid, block, stream, a)
+                   : launch(project_rows<E, MT, NT, ST, true, false>, grid, block, stream, a);
+    return far ? launch(project_rows<E, MT, NT, ST, false, true>, grid, block, stream, a)
+               : launch(project_rows<E, MT, NT, ST, false, false>, grid, block, stream, a);
 }
 
 // Weight tiles of a workgroup of expand_rows.
@@ -269,9 +276,15 @@ hipError_t launch_expand(const ExpandArgs& arg, bool bf16, bool x8, hipStream_t 
     const dim3 grid((uint32_t)expand_grid(rows, a.nt, a.each)), block(512);
     auto run = [&](auto e) {
         using E = decltype(e);
-        if (a.kr != nullptr)
-            return x8 ? launch(expand_rows<E, true, true>, grid, block, stream, a) : launch(expand_rows<E, false, true>, grid, block, stream, a);
-        return x8 ? launch(expand_rows<E, true, false>, grid, block, stream, a) : launch(expand_rows<E, false, false>, grid, block, stream, a);
+        auto with = [&](auto k8, auto far) {
+            constexpr bool X8 = decltype(k8)::value, FAR = decltype(far)::value;
+            return a.kr != nullptr ? launch(expand_rows<E, X8, true, FAR>, grid, block, stream, a)
+                                   : launch(expand_rows<E, X8, false, FAR>, grid, block, stream, a);
+        };
+        constexpr std::true_type yes{};
+        constexpr std::false_type no{};
+        if (far_out((int64_t)a.B * a.most * a.H * (a.Dn + a.Dr + a.Dv) * 2)) return x8 ? with(yes, yes) : with(no, yes);
+        return x8 ? with(yes, no) : with(no, no);
     };
     return bf16 ? run(BF16T{}) : run(F16T{});
 }
