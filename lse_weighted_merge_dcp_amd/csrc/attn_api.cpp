@@ -565,7 +565,7 @@ int dcpa_latent_expand(const dcpa_expand_args* a, void* stream) {
         !cache_shape_ok(a->num_pages, a->page_size, a->max_pages))
         return DCP_ERR_SHAPE;
     const int64_t named = a->max_pages * a->page_size, keys = a->max_keys < named ? a->max_keys : named;
-    if (expand_workgroups(a->B, a->max_keys, a->H, a->Dn + a->Dv) > kMaxGrid / 2) return DCP_ERR_SHAPE;
+    if (expand_workgroups(a->B, a->max_keys, a->k_rest != nullptr) > kMaxGrid / 2) return DCP_ERR_SHAPE;
     if (!positive(a->k_scale)) return DCPA_ERR_VALUE;
     const int ec = esize_of(a->cache_dtype);
     if (!strides_ok({a->c_P, a->c_S, a->t_B, a->wk_H, a->wk_N, a->wv_H, a->wv_N, a->k_B, a->k_S, a->k_H, a->v_B, a->v_S,

@@ -114,6 +114,8 @@ struct GroupArgs : AttnArgs {
     int32_t groups, step;    // step: keys of a tile
     int32_t own_rows;        // rows of a tile of a sequence against its own keys (`rows`, or 32 where they are few)
 };
+hipError_t launch_prefix_bf16(const GroupArgs& a, bool kv8, bool wide, hipStream_t stream);
+hipError_t launch_prefix_f16(const GroupArgs& a, bool kv8, bool wide, hipStream_t stream);
 int64_t prefix_list_bytes(int64_t units, int64_t entries);
 AttnPlan plan_prefix(const Batch& m, int64_t groups, int Dk, int Dv, bool pieces);
 hipError_t launch_prefix(const GroupArgs& a, bool latent, bool bf16, bool kv8, bool wide, hipStream_t stream);
@@ -223,13 +225,12 @@ struct ExpandArgs {
     int64_t pl_B;
     int32_t B, H, Dn, Dr, Dv, Dc;
     int32_t most, keys;      // rows of the outputs; of these, what the page table can name
-    int32_t pages, mt, nt;   // row tiles of a sequence, column tiles
-    int32_t each;            // column tiles of a workgroup
+    int32_t pages, nt;       // nt: column tiles
     FastDiv fpage, fper;     // fper: Dn + Dv
     float ks;
 };
 hipError_t launch_expand(const ExpandArgs& a, bool bf16, bool x8, hipStream_t stream);
-int64_t expand_workgroups(int64_t B, int64_t most, int64_t H, int64_t per);
+int64_t expand_workgroups(int64_t B, int64_t most, bool rest);
 
 // Launch kernel(arg) and return that launch's own status.
 template <typename Arg>

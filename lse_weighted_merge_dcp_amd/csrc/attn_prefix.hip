@@ -1,75 +1,9 @@
-// attn_prefix.hip -- attention of a batch whose sequences share the first keys
-// of their caches, group by group.
-//
-// The rows of all sequences of a group stand together, so against the shared
-// keys they are one long sequence: its row tiles take the shared keys once for
-// 128 rows of whichever sequences, and every sequence's own tiles take the keys
-// behind them.  Both are units of one launch, of the code that single sequences
-// run (attn_rows.hpp, attn_latent.hpp, attn_keys.hpp for a sequence's own keys where
-// rows are few), which differs only in how a workgroup finds its share and in what
-// a row sees: a list that a kernel of one workgroup has made.  A row's parts are
-// joined by a third kernel.
-#include "attn_keys.hpp"
+// attn_prefix.hip -- attention behind shared prefixes (attn_prefix.hpp): the list of
+// units, the kernels of the latent layout, the join, and the calls' layout.
 #include "attn_latent.hpp"
-#include "attn_rows.hpp"
+#include "attn_prefix.hpp"
 
 namespace dcpa {
-
-// A workgroup's share: rows of one sequence against its own keys, or rows of a
-// group against the keys that its sequences share.
-struct GroupUnit : Unit {
-    int begin;      // first key
-    int end;        // one behind the last shared key (group)
-    int b0, b1;     // the group's sequences (none: a sequence's own keys)
-    bool even;      // every row of the group sees all shared keys
-};
-template <int STEP> __device__ __forceinline__ GroupUnit unit_of(const GroupArgs& p, int, int id) {
-    const PrefixUnit x = p.list[id];
-    GroupUnit u;
-    u.s = Seq{x.first, x.n, x.kv, x.len};
-    u.b = x.b;
-    u.tile = x.tile;
-    u.split = x.split;
-    u.splits = x.splits;
-    u.chunk = x.chunk;
-    u.slot = id - x.split;
-    u.ok = x.n > 0;
-    u.begin = x.begin;
-    u.end = x.end;
-    u.b0 = x.b0;
-    u.b1 = x.b1;
-    u.even = x.even != 0;
-    return u;
-}
-__device__ __forceinline__ int first_key(const GroupUnit& u) { return u.begin; }
-__device__ __forceinline__ int last_key(const GroupArgs& p, const GroupUnit& u, int last_row) {
-    return u.b1 > u.b0 ? u.end : visible(p.m, u.s, (int)fdiv((uint32_t)last_row, p.m.fG));
-}
-__device__ __forceinline__ int sees(const GroupArgs& p, const GroupUnit& u, int token) {
-    if (u.b1 == u.b0) return visible(p.m, u.s, token);
-    if (u.even) return u.end;
-    // the last sequence that starts at the token's row or before it
-    const int t = u.s.first + token;
-    int lo = u.b0, hi = u.b1 - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (min(max(p.m.cu[mid], 0), p.m.T) <= t) lo = mid;
-        else hi = mid - 1;
-    }
-    const Seq s = load_seq(p.m, lo);
-    return min(visible(p.m, s, t - s.first), u.end);
-}
-// (rows of several sequences are in no order)
-__device__ __forceinline__ int least_seen(const GroupUnit&, int vis) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) vis = min(vis, __shfl_xor(vis, d, 64));
-    return __builtin_amdgcn_readfirstlane(vis);
-}
-__device__ __forceinline__ int most_seen(const GroupUnit&, int vis) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) vis = max(vis, __shfl_xor(vis, d, 64));
-    return __builtin_amdgcn_readfirstlane(vis);
-}
 
 namespace {
 
@@ -82,7 +16,7 @@ namespace {
 // price of kPrice keys to a unit (its start and its part), either all run at once
 // and take c + kPrice, or their mean load and one unit more.
 // ---------------------------------------------------------------------------
-constexpr int kThreads = 1024, kWaves = kThreads / 64, kTries = 32, kPrice = 128;
+constexpr int kThreads = 1024, kWaves = kThreads / 64, kTries = 32, kPrice = 1024;
 constexpr int kMost = 1 << 30;
 // in how many ranges: each number about a quarter above the last
 struct Ways {
@@ -314,24 +248,6 @@ __global__ __launch_bounds__(kThreads) void prefix_list(GroupArgs p) {
     for (int id = base + tid; id < p.units; id += kThreads) p.list[id].n = 0;
 }
 
-template <typename E, bool KV8, bool EXACT, int DK, int DV, int KT, bool WIDE>
-__global__ __launch_bounds__(256, DK > 192 ? 1 : 2) void prefix_rows(GroupArgs p) {
-    __shared__ RowsLds<DK, DV, KT> lds;
-    rows_of<E, KV8, EXACT, DK, DV, KT, WIDE>(p, lds);
-}
-// The same where rows are few: a sequence's own keys shared out over the waves, which keeps more loads under
-// way.
-template <typename E, bool KV8, bool EXACT, int DK, int DV, int KT, int DO, bool WIDE>
-__global__ __launch_bounds__(256, DO > 128 ? 1 : 2) void prefix_few(GroupArgs p) {
-    __shared__ union Lds {
-        RowsLds<DK, DV, KT> rows;
-        KeysLds<KV8, DO, DO> keys;
-    } lds;
-    const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv), unit = (int)(blockIdx.x / (uint32_t)p.m.Hkv);
-    const GroupUnit u = unit_of<KT>(p, p.rows, unit);
-    if (u.b1 > u.b0) rows_of<E, KV8, EXACT, DK, DV, KT, WIDE>(p, lds.rows);
-    else keys_of<E, KV8, DO, DO>(p, lds.keys, u, hk, unit);
-}
 template <typename E, bool KV8, bool EXACT, bool WIDE> __global__ __launch_bounds__(256, 1) void prefix_latent(GroupArgs p) {
     latent_rows<E, KV8, EXACT, WIDE>(p);
 }
@@ -479,33 +395,10 @@ hipError_t run_join(const GroupArgs& a, hipStream_t stream) {
                        : launch(prefix_join<E, 2, false>, grid, block, stream, a);
 }
 
-template <typename E, bool KV8, bool WIDE>
-hipError_t run(const GroupArgs& a, bool latent, hipStream_t stream) {
+template <typename E, bool KV8, bool WIDE> hipError_t run_latent(const GroupArgs& a, hipStream_t stream) {
     const dim3 grid((uint32_t)((int64_t)a.units * a.m.Hkv)), block(256);
-    hipError_t e = launch(prefix_list, dim3(1), dim3(kThreads), stream, a);
-    if (e != hipSuccess) return e;
-    if (latent) {
-        e = a.Dk == latent::DK ? launch(prefix_latent<E, KV8, true, WIDE>, grid, block, stream, a)
-                               : launch(prefix_latent<E, KV8, false, WIDE>, grid, block, stream, a);
-        return e != hipSuccess ? e : run_join<E>(a, stream);
-    }
-    const int d = a.Dk > a.Dv ? a.Dk : a.Dv;
-    const bool few = a.own_rows == 32;
-    auto rows = [&](auto exact, auto dk, auto dv, auto kt, auto own) {
-        constexpr bool X = decltype(exact)::value;
-        constexpr int K = decltype(dk)::value, V = decltype(dv)::value, T = decltype(kt)::value, O = decltype(own)::value;
-        return few ? launch(prefix_few<E, KV8, X, K, V, T, O, WIDE>, grid, block, stream, a)
-                   : launch(prefix_rows<E, KV8, X, K, V, T, WIDE>, grid, block, stream, a);
-    };
-    constexpr std::integral_constant<int, 32> n32{};
-    constexpr std::integral_constant<int, 64> n64{};
-    constexpr std::integral_constant<int, 128> n128{};
-    constexpr std::integral_constant<int, 192> n192{};
-    constexpr std::integral_constant<int, 256> n256{};
-    if (d <= 64) e = rows(std::false_type{}, n64, n64, n64, n64);
-    else if (d <= 128) e = a.Dk == 128 && a.Dv == 128 ? rows(std::true_type{}, n128, n128, n64, n128) : rows(std::false_type{}, n128, n128, n64, n128);
-    else e = a.Dk <= 192 && a.Dv <= 128 ? rows(std::false_type{}, n192, n128, n32, n256) : rows(std::false_type{}, n256, n256, n32, n256);
-    return e != hipSuccess ? e : run_join<E>(a, stream);
+    return a.Dk == latent::DK ? launch(prefix_latent<E, KV8, true, WIDE>, grid, block, stream, a)
+                              : launch(prefix_latent<E, KV8, false, WIDE>, grid, block, stream, a);
 }
 
 }  // namespace
@@ -539,13 +432,20 @@ hipError_t launch_prefix(const GroupArgs& arg, bool latent, bool bf16, bool kv8,
         a.v = a.k;
         a.v_P = a.k_P; a.v_S = a.k_S; a.v_H = a.k_H;
     }
-    auto with = [&](auto e, auto k) {
-        using E = decltype(e);
-        constexpr bool K8 = decltype(k)::value;
-        return wide ? run<E, K8, true>(a, latent, stream) : run<E, K8, false>(a, latent, stream);
-    };
-    if (bf16) return kv8 ? with(BF16T{}, std::true_type{}) : with(BF16T{}, std::false_type{});
-    return kv8 ? with(F16T{}, std::true_type{}) : with(F16T{}, std::false_type{});
+    hipError_t e = launch(prefix_list, dim3(1), dim3(kThreads), stream, a);
+    if (e != hipSuccess) return e;
+    if (!latent) e = bf16 ? launch_prefix_bf16(a, kv8, wide, stream) : launch_prefix_f16(a, kv8, wide, stream);
+    else {
+        auto with = [&](auto type, auto k) {
+            using E = decltype(type);
+            constexpr bool K8 = decltype(k)::value;
+            return wide ? run_latent<E, K8, true>(a, stream) : run_latent<E, K8, false>(a, stream);
+        };
+        e = bf16 ? (kv8 ? with(BF16T{}, std::true_type{}) : with(BF16T{}, std::false_type{}))
+                 : (kv8 ? with(F16T{}, std::true_type{}) : with(F16T{}, std::false_type{}));
+    }
+    if (e != hipSuccess) return e;
+    return bf16 ? run_join<BF16T>(a, stream) : run_join<F16T>(a, stream);
 }
 
 }  // namespace dcpa

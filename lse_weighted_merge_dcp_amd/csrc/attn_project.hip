@@ -74,32 +74,63 @@ __global__ __launch_bounds__(256, POCC) void project_rows(ProjectArgs p) {
 }
 
 // ---------------------------------------------------------------------------
-// expand_rows: a workgroup takes 256 keys of a sequence and p.each tiles of 256 of
+// expand_rows: a workgroup takes 256 or 128 keys of a sequence and p.each tiles of 256 of
 // the H (Dn + Dv) weight rows.
 // ---------------------------------------------------------------------------
-constexpr int MT = 256, NT = 256;
+// (128 keys where the roundings' rests are written too: their way out takes the registers of the other 128)
+constexpr int NT = 256;
+constexpr int expand_rows_of(bool rest) { return rest ? 128 : 256; }
+constexpr int kChip = 256, kMostRounds = 4;     // workgroups that run at once; rounds of them, at most, where columns are cut
 template <typename E, bool X8, bool REST, bool FAR> __global__ __launch_bounds__(512, 2) void expand_rows(ExpandArgs p) {
+    constexpr int MT = expand_rows_of(REST);
     using P = Product<E, MT, NT, 64, 2, 4, 2, false, X8>;
-    constexpr int ES = X8 ? 1 : 2, NR = 4;      // NR: the thread's pieces of the columns that all heads share, at most
+    constexpr int ES = X8 ? 1 : 2, NR = MT * 8 / 512;      // NR: the thread's pieces of the columns that all heads share, at most
     __shared__ __attribute__((aligned(1024))) char lds[P::LDS];
-    // 8 row tiles by 4 ranges of columns at a time on one XCD (32 CUs), so that its L2 serves most of what they read
-    const uint32_t local = blockIdx.x >> 3, id = local % 32, super = local / 32 * 8 + (blockIdx.x & 7);
-    const uint32_t across = (uint32_t)(p.mt * p.B + 7) / 8;
-    const int mb = (int)(super % across * 8 + (id & 7)), nt0 = (int)(super / across * 4 + (id >> 3)) * p.each;
-    if (mb >= p.mt * p.B || nt0 >= p.nt) return;
-    const int b = mb / p.mt, row0 = (mb - b * p.mt) * MT, tiles = min(p.each, p.nt - nt0);
+    P c(lds);
+    // Row tiles that there are keys for, and into how many ranges the columns are cut for each: of 64 numbers the one
+    // with which the longest workgroup (rounds of the chip times its tiles, and a third of one to start) ends first.
+    // Row tiles 8 apart go to one XCD with all their ranges, so that its L2 serves most of what they read.
+    int rows = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 64)
+        rows += b0 + c.lane < p.B ? (min(max(p.kv[b0 + c.lane], 0), p.most) + MT - 1) / MT : 0;
+    rows = fold_wave(rows, 0, [](int x, int y) { return x + y; });
+    const int apart = rows >= 8 ? (rows + 7) / 8 * 8 : max(rows, 1);
+    int ranges;
+    {
+        const int r = c.lane + 1, each = (p.nt + r - 1) / r, rounds = (apart * r + kChip - 1) / kChip;
+        const bool fits = r == 1 || (r <= p.nt && apart * r <= kMostRounds * kChip);
+        const int price = fits ? (int)min((int64_t)rounds * (3 * each + 1), (int64_t)1 << 24) * 64 + c.lane : 0x7fffffff;
+        ranges = (fold_wave(price, 0x7fffffff, [](int x, int y) { return min(x, y); }) & 63) + 1;
+    }
+    const int range = (int)blockIdx.x / apart, m = (int)blockIdx.x - range * apart;
+    if (m >= rows || range >= ranges) return;
+    const int each = (p.nt + ranges - 1) / ranges, nt0 = range * each, tiles = min(each, p.nt - nt0);
+    if (tiles <= 0) return;
+    int b = 0, mt = m;
+    for (int b0 = 0, base = 0; b0 < p.B; b0 += 64) {
+        const int mine = b0 + c.lane < p.B ? (min(max(p.kv[b0 + c.lane], 0), p.most) + MT - 1) / MT : 0;
+        const int ends = base + scan_incl(mine);
+        const uint64_t past = __ballot(ends > m);
+        if (past != 0) {
+            const int at = __builtin_ctzll(past);
+            b = b0 + at;
+            mt = m - (__builtin_amdgcn_readlane(ends, at) - __builtin_amdgcn_readlane(mine, at));
+            break;
+        }
+        base = __builtin_amdgcn_readlane(ends, 63);
+    }
+    const int row0 = mt * MT;
     // (a length may be more than the table has pages for: those keys are not there)
     const int counted = min(max(p.kv[b], 0), p.most), kv = min(counted, p.keys);
     auto name = [&](int j, bool there) {
         if (nt0 == 0 && p.places != nullptr && j < counted) p.places[(int64_t)b * p.pl_B + j] = there ? b * p.most + j : -1;
     };
     if (row0 >= kv) {
-        if (threadIdx.x < MT) name(row0 + (int)threadIdx.x, false);
+        if ((int)threadIdx.x < MT) name(row0 + (int)threadIdx.x, false);
         return;
     }
     const int per = p.Dn + p.Dv, cols = per * p.H;
     const int32_t* table = p.table + (int64_t)b * p.t_B;
-    P c(lds);
     const char* base = p.cache;
     // where cached row j lies (an address of zeros where its page is missing; the row of zeros is as long as the
     // widest cached row)
@@ -238,25 +269,16 @@ template <typename E, int MT, int NT, int ST> hipError_t project(const ProjectAr
                : launch(project_rows<E, MT, NT, ST, false, false>, grid, block, stream, a);
 }
 
-// Weight tiles of a workgroup of expand_rows.
-int64_t expand_each(int64_t rows, int64_t nt) {
-    const int64_t ranges = 256 / rows;             // of columns, so that the workgroups fill the chip once
-    return ranges < 1 ? nt : tiles_of(nt, ranges);
-}
-int64_t expand_grid(int64_t rows, int64_t nt, int64_t each) {
-    // whole super tiles, a multiple of 8 of them
-    return tiles_of(tiles_of(rows, 8) * tiles_of(tiles_of(nt, each), 4), 8) * 8 * 32;
-}
-
 }  // namespace
 
 int64_t project_tiles(int64_t T, int64_t H, int64_t N) {
     const int64_t each = few_rows(T) ? 64 : 128;
     return tiles_of(T, each) * H * tiles_of(N, each);
 }
-int64_t expand_workgroups(int64_t B, int64_t most, int64_t H, int64_t per) {
-    const int64_t rows = B * tiles_of(most, MT), nt = tiles_of(H * per, NT);
-    return expand_grid(rows, nt, rows > 0 ? expand_each(rows, nt) : 1);
+int64_t expand_workgroups(int64_t B, int64_t most, bool rest) {
+    // (row tiles 8 apart, or as many workgroups as columns are cut for; the kernel finds how many there are)
+    const int64_t rows = (B * tiles_of(most, expand_rows_of(rest)) + 7) / 8 * 8;
+    return rows > kMostRounds * kChip ? rows : kMostRounds * kChip;
 }
 
 hipError_t launch_project(const ProjectArgs& a, bool turned, bool bf16, hipStream_t stream) {
@@ -269,11 +291,8 @@ hipError_t launch_project(const ProjectArgs& a, bool turned, bool bf16, hipStrea
 
 hipError_t launch_expand(const ExpandArgs& arg, bool bf16, bool x8, hipStream_t stream) {
     ExpandArgs a = arg;
-    a.mt = (int32_t)tiles_of(a.most, MT);
     a.nt = (int32_t)tiles_of((int64_t)a.H * (a.Dn + a.Dv), NT);
-    const int64_t rows = (int64_t)a.B * a.mt;
-    a.each = (int32_t)expand_each(rows, a.nt);
-    const dim3 grid((uint32_t)expand_grid(rows, a.nt, a.each)), block(512);
+    const dim3 grid((uint32_t)expand_workgroups(a.B, a.most, a.kr != nullptr)), block(512);
     auto run = [&](auto e) {
         using E = decltype(e);
         auto with = [&](auto k8, auto far) {

@@ -24,7 +24,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 PKG = os.path.dirname(HERE)
 ROOT = os.path.dirname(PKG)
-SOURCES = ["attn.hip", "attn_latent.hip", "attn_mass.hip", "attn_rope.hip", "attn_evict.hip", "attn_plan.hip", "attn_project.hip", "attn_prefix.hip", "attn_pairs.hip",
+SOURCES = ["attn.hip", "attn_latent.hip", "attn_mass.hip", "attn_rope.hip", "attn_evict.hip", "attn_plan.hip", "attn_project.hip", "attn_prefix.hip",
+           "attn_prefix_bf16.hip", "attn_prefix_f16.hip", "attn_pairs.hip",
            "attn_api.cpp",
            "api.cpp", "pack.hip", "combine.hip", "inplace.hip", "bench_api.cpp"]
 LIB = os.path.join(PKG, "libdcpmerge.so")
@@ -43,7 +44,7 @@ OBJECTS = {
     LIB: ["api", "pack", "combine", "inplace"],
     BENCH_LIB: ["bench_api", "api", "pack", "combine", "inplace"],
     ATTN_LIB: ["attn_api", "attn", "attn_latent", "attn_mass", "attn_rope", "attn_evict", "attn_plan", "attn_project",
-               "attn_prefix", "attn_pairs"],
+               "attn_prefix", "attn_prefix_bf16", "attn_prefix_f16", "attn_pairs"],
 }
 ARCH = "gfx950"
 
