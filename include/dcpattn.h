@@ -181,15 +181,16 @@ int64_t dcpa_paged_attn_workspace(const dcpa_attn_args* a);
  * for all rows of a group.  Group g is the sequences cu_group[g] ..
  * cu_group[g+1]-1; the first shared_len[g] cached keys of all of them are the
  * same (whole pages that stand in all their table rows), and are read through the
- * table row of the group's first sequence.  shared_len[g] is clamped to [0,
- * max_pages * page_size]; a sequence sees of the shared keys what it would see of
- * its own (none where its kv_len is 0).  Sequences outside the groups share nothing.
+ * table row of the first of them whose kv_len is shared_len[g] or more (of the
+ * first, if there is none).  shared_len[g] is clamped to [0, max_pages *
+ * page_size]; a sequence sees of the shared keys what it would see of its own (none
+ * where its kv_len is 0).  Sequences outside the groups share nothing.
  * cu_group has to be non-decreasing (as cu_q, other contents give wrong numbers
  * but no access outside the buffers).
  *
  * Parts of every row live in `workspace`, whose size dcpa_prefix_attn_workspace
- * gives.  Weights are rounded to `dtype` for the product with the values, also
- * where rows are few; wide_weights as in dcpa_paged_attn.  Up to 2^20 groups; the
+ * gives.  Weights of shared keys are rounded to `dtype` for the product with the
+ * values, also where rows are few; wide_weights as in dcpa_paged_attn.  Up to 2^20 groups; the
  * limit of 2^23 workgroups counts the row tiles of sequences and of groups.
  */
 int dcpa_prefix_attn(const dcpa_attn_args* a, const int32_t* cu_group, const int32_t* shared_len, int64_t n_groups,

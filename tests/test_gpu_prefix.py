@@ -115,6 +115,37 @@ def test_cut_caches_and_missing_pages(form):
     check(p, *call(p, cu, same))
 
 
+@pytest.mark.parametrize("form", FORMS)
+def test_padding_in_front_of_a_group(form):
+    """The group's first sequences hold nothing, or less than is shared, and their table rows name no pages."""
+    Hq, Hkv, Dk, Dv, latent = FORMS[form]
+    p = Problem([(1, 90), (1, 40), (2, 120), (1, 100)], Hq, Hkv, Dk, Dv, page=16, shared=latent, seed=42)
+    cu, same = share(p, [(0, 4, 96)])
+    p.kv[0] = 0
+    p.table[0] = -1
+    p.table[1, 3:] = -1
+    check(p, *call(p, cu, same))
+
+
+def test_more_groups_and_sequences_than_a_workgroup_has_threads():
+    """Lists of more than 1024 entries, with groups across the border of what one pass holds, and padding among them."""
+    r = random.Random(43)
+    seqs, groups, b = [], [], 0
+    while b < 1100:
+        n = min(r.choice([1, 3, 40, 200]), 1100 - b)
+        keys = 16 * r.randint(0, 3)
+        groups.append((b, b + n, keys))
+        seqs += [(r.choice([0, 1, 1]), keys + 2 + r.randint(0, 20)) for _ in range(n)]
+        b += n
+    p = Problem(seqs, 1, 1, 16, 16, page=16, seed=43)
+    cu, same = share(p, groups)
+    for g0, g1, keys in groups:
+        if g1 - g0 > 2:
+            p.kv[g0] = 0
+            p.table[g0] = -1
+    check(p, *call(p, cu, same))
+
+
 @pytest.mark.parametrize("what", [math.nan, math.inf])
 @pytest.mark.parametrize("form", FORMS)
 def test_masked_places_never_reach_a_row(form, what):
