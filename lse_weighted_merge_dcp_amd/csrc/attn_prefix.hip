@@ -289,7 +289,9 @@ __global__ __launch_bounds__(256) void prefix_join(GroupArgs p) {
         const int hk = (int)((uint32_t)id - at_row * p.m.fHkv.d), t = (int)fdiv(at_row, p.m.fG), head = (int)at_row - t * p.m.G;
         // the row's group and its sequence: first slots and numbers of parts
         int slot[2] = {0, 0}, parts[2] = {0, 0}, in_tile[2] = {0, 0};
-        const PrefixEntry y = p.entries[find(p.groups, p.m.B, t)];
+        // (both asked for before either is looked at)
+        const int own = find(p.groups, p.m.B, t), group = find(0, p.groups, t);
+        const PrefixEntry y = p.entries[own], g = p.entries[group];
         const bool found_seq = t >= y.first && t < y.first + y.n;
         const bool whole = y.splits == 1 && y.begin == 0;
         if (found_seq && !whole) {
@@ -301,7 +303,6 @@ __global__ __launch_bounds__(256) void prefix_join(GroupArgs p) {
             const int kend = visible(p.m, Seq{y.first, y.n, y.kv, y.len}, (int)fdiv((uint32_t)last, p.m.fG)) - y.begin;
             parts[1] = min(y.splits, max(1, (kend + y.chunk - 1) / y.chunk));
             if (y.begin > 0) {
-                const PrefixEntry g = p.entries[find(0, p.groups, t)];
                 if (t >= g.first && t < g.first + g.n && g.kv > 0) {
                     const int grow = (t - g.first) * p.m.G + head, gtile = grow / p.rows;
                     in_tile[0] = grow - gtile * p.rows;

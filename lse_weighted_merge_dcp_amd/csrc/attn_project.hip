@@ -1,11 +1,19 @@
 // attn_project.hip -- the projections on both sides of latent attention, head
 // by head, and the keys and values of all heads from cached latent rows.
 //
-// project_rows: y[t, h] = x[t, h] W[h], rows of tokens against one head's
-// weights.  Bound by the weights' bytes where tokens are few, by the rows' where
-// they are many (a weight of 128 x 512 makes 512 outputs of 128 inputs: 205
-// operations a byte, and the matrix instructions do 220).
-// expand_rows: cached rows against the weights of all heads side by side.
+// project_rows: y[t, h] = x[t, h] W[h], rows of tokens against one head's weights.
+// Bound by bytes: the weights' where tokens are few (64 tokens, 128 heads of 128 x
+// 512: 8 us for queries, 7.2 for values, of which the 27 MB take 4.5 and a launch the
+// rest), the rows' where they are many (a weight of 128 x 512 makes 512 outputs of
+// 128 inputs: 205 operations a byte, and the matrix instructions do 220).  4096
+// tokens' queries take 229 us, 3.6 TB/s; without their stores 117, so stores and the
+// rest still come one after the other; 2001 tokens' values of 96 heads 43 us, 6.0 TB/s.
+// expand_rows: cached rows against the weights of all heads side by side.  Bound by
+// the LDS: a step of 256 x 256 x 64 takes 2048 clocks of matrix instructions, and as
+// many of LDS accesses for the fragments (1536) and the next operands (512).  16384
+// rows, 128 heads of 128 + 64 / 128 columns: 720 us, 0.76 PFLOP/s (390 us without loads
+// and stores, 515 without stores; tiles of 128 x 256 by two workgroups to a CU 860 us,
+// steps of 32 columns 827, one workgroup to a tile 814).
 #include "attn_product.hpp"
 
 namespace dcpa {
@@ -15,16 +23,9 @@ namespace {
 // ---------------------------------------------------------------------------
 // project_rows: a workgroup takes p.each tiles in the order (rows, head, columns).
 // ---------------------------------------------------------------------------
-#ifndef PKT
-#define PKT 64
-#define POCC 2
-#define PMT 128
-#define PNT 128
-#define PST 2
-#endif
 template <typename E, int MT, int NT, int ST, bool TURNED, bool FAR>
-__global__ __launch_bounds__(256, POCC) void project_rows(ProjectArgs p) {
-    using P = Product<E, MT, NT, PKT, 2, 2, ST, TURNED, false>;
+__global__ __launch_bounds__(256, 2) void project_rows(ProjectArgs p) {
+    using P = Product<E, MT, NT, 64, 2, 2, ST, TURNED, false>;
     __shared__ __attribute__((aligned(1024))) char lds[P::LDS];
     P c(lds);
     const int first = (int)blockIdx.x * p.each, tiles = min(p.each, p.tiles - first);
@@ -251,8 +252,10 @@ int64_t share_of(int64_t all, int64_t slots) {
 // Results of an eighth of the Infinity Cache and more go out with the nontemporal hint.
 bool far_out(int64_t bytes) { return bytes >= (int64_t(1) << 25); }
 
-// Rows of a tile.
-bool few_rows(int64_t T) { return T <= 128; }
+// Tiles of 64 x 64 for few tokens, and where those of 128 x 128 leave half the chip without one; larger ones read
+// rows and weights half as often.  (Values of 64 tokens, 128 heads 7.2 us in small tiles, 8.4 in large ones; of 128
+// tokens 10.3 and 9.0, queries of 256 17.4 and 14.1; values of 256 and 512 tokens of 16 heads 7.0 and 8.4.)
+bool few_rows(int64_t T, int64_t H, int64_t N) { return T <= 64 || tiles_of(T, 128) * H * tiles_of(N, 128) < 128; }
 
 template <typename E, int MT, int NT, int ST> hipError_t project(const ProjectArgs& arg, bool turned, hipStream_t stream) {
     ProjectArgs a = arg;
@@ -272,7 +275,7 @@ template <typename E, int MT, int NT, int ST> hipError_t project(const ProjectAr
 }  // namespace
 
 int64_t project_tiles(int64_t T, int64_t H, int64_t N) {
-    const int64_t each = few_rows(T) ? 64 : 128;
+    const int64_t each = few_rows(T, H, N) ? 64 : 128;
     return tiles_of(T, each) * H * tiles_of(N, each);
 }
 int64_t expand_workgroups(int64_t B, int64_t most, bool rest) {
@@ -284,7 +287,7 @@ int64_t expand_workgroups(int64_t B, int64_t most, bool rest) {
 hipError_t launch_project(const ProjectArgs& a, bool turned, bool bf16, hipStream_t stream) {
     auto run = [&](auto e) {
         using E = decltype(e);
-        return few_rows(a.T) ? project<E, 64, 64, 4>(a, turned, stream) : project<E, PMT, PNT, PST>(a, turned, stream);
+        return few_rows(a.T, a.H, a.N) ? project<E, 64, 64, 4>(a, turned, stream) : project<E, 128, 128, 2>(a, turned, stream);
     };
     return bf16 ? run(BF16T{}) : run(F16T{});
 }
