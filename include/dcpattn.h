@@ -4,13 +4,20 @@
  *
  * Under DCP a sequence's keys and values are dealt out over N ranks in blocks
  * of `interleave` positions: position p lies on rank (p / interleave) % N.
- * Each rank keeps its share in a paged cache.  The four calls here are what a
- * layer does around the merge of dcpmerge.h:
+ * Each rank keeps its share in a paged cache.  The calls here are what a step and
+ * its layers do around the merge of dcpmerge.h:
  *
+ *   dcpa_batch_plan           a step's lengths, page tables, positions and slots
  *   dcpa_qk_norm_rope_append  norm and rotate new queries and keys, write the
  *                             keys and values this rank owns into its cache
  *   dcpa_paged_attn           attention of new tokens over the rank's cache:
  *                             the partial output and LSE that dcp_pack takes
+ *   dcpa_prefix_attn          the same for sequences that share their first keys,
+ *                             which are read once for all of a group
+ *   dcpa_project              the projections on both sides of latent attention
+ *   dcpa_latent_expand        keys and values of all heads from latent rows
+ *   dcpa_pair_attn            attention over keys and values in two 16-bit parts,
+ *                             as the expansion makes them
  *   dcpa_attn_mass            accumulate the attention weight of each cached
  *                             key from the merged LSE of dcp_unpack_combine
  *   dcpa_cache_evict          keep the keys of highest accumulated weight:

@@ -6,6 +6,9 @@
 // far more than fp32 sums and powers do.  The two parts together hold them to
 // 2^-16 (bf16) or 2^-22 (fp16), for 8 more matrix instructions beside 12 in the
 // scores of 128 + 64 columns and twice as many in the values.
+// Bound by matrix instructions, as rows_of().  A chunk of 3 ragged sequences to 1500
+// tokens over 4500 keys, 32 heads of 192 / 128 columns: 535 to 585 us; keys and
+// values rounded once 343, with results that are off by more than their own rounding.
 #include "attn_rows.hpp"
 
 namespace dcpa {

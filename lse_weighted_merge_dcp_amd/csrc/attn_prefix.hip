@@ -12,9 +12,15 @@ namespace {
 // or sequence), then a thread to a unit.
 //
 // The key ranges' length is chosen among 32 that cut the longest entry evenly:
-// with U units of which the longest takes c keys, `slots` of them at once and a
-// price of kPrice keys to a unit (its start and its part), either all run at once
-// and take c + kPrice, or their mean load and one unit more.
+// with U units of which the longest takes c keys, `share` of them at once and a
+// price of kPrice keys to a unit (its start, and a part of 128 rows written and read
+// again), either all run at once and take c + kPrice, or their mean load and one
+// unit more.  (64 sequences behind 32768 keys on four ranks: 68 us a call in ranges of
+// 1024 keys, 75 of 704, 82 of 384.)
+// Every workgroup finding its own unit from the lengths, as those of single
+// sequences do, took 112 us there, a dozen dependent loads in front of 8 key tiles;
+// this kernel takes 8.5 and the rest 60.  Most of that is waiting: for the lengths (two
+// loads one after the other) and for code that is run once.
 // ---------------------------------------------------------------------------
 constexpr int kThreads = 1024, kWaves = kThreads / 64, kTries = 32, kPrice = 1024;
 constexpr int kMost = 1 << 30;
@@ -262,7 +268,8 @@ template <typename E, bool KV8, bool EXACT, bool WIDE> __global__ __launch_bound
 
 // ---------------------------------------------------------------------------
 // prefix_join: a row's parts, those against the shared keys and those against its
-// sequence's own, on one scale (as attn_join).
+// sequence's own, on one scale (as attn_join).  Bound by latency: the row's place, its
+// entry, its parts' sums, its parts (4096 rows of 9 to 10 parts: 10 us).
 // ---------------------------------------------------------------------------
 template <typename E, int NC, bool TOGETHER>
 __global__ __launch_bounds__(256) void prefix_join(GroupArgs p) {

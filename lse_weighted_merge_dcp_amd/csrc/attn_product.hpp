@@ -3,13 +3,13 @@
 // instructions.
 //
 // The steps of all tiles make one row, so that the first operands of a tile are on
-// their way while the last one's products are taken and its results go out: of
-// tiles of 128 x 128 x 128 by a workgroup each, two thirds of the time went by in
-// starts and ends.  The product is computed transposed (A = weights, B = rows), so
-// that a lane holds, of one row m, four neighbouring columns n in a register group;
-// an exchange between the half-waves makes them eight, and through 4 KB of LDS of
-// its own a wave turns them into whole lines of 128 bytes of a row.  (Stored from the
-// registers in pieces of 32 bytes, lines left the L2 half written: 1.9 GB for 1.3.)
+// their way while the last one's products are taken and its results go out (4096
+// tokens' queries by a workgroup to each tile of 128 x 128: 349 us, 229 so).  The
+// product is computed transposed (A = weights, B = rows), so that a lane holds, of
+// one row m, four neighbouring columns n in a register group; an exchange between
+// the half-waves makes them eight, and through 4 KB of LDS of its own a wave turns
+// them into whole lines of 128 bytes of a row.  (Stored from the registers in pieces
+// of 32 bytes, lines left the L2 half written: 1.9 GB for 1.3.)
 #pragma once
 #include "attn_device.hpp"
 
