@@ -572,7 +572,7 @@ def dcp_latent_attn(q: torch.Tensor, kv_cache: torch.Tensor, w_uk: torch.Tensor,
                               interleave=interleave, causal=causal, k_scale=k_scale, v_scale=k_scale,
                               is_lse_base_on_e=is_lse_base_on_e, wide_weights=wide_weights, out=out, out_lse=out_lse,
                               workspace=workspace)
-    dev = _on_gpu(q, cu_q, seq_len, out, out_lse, workspace)
+    dev = _on_gpu(q, k, v, k_rest, v_rest, places, cu_q, kv_len, seq_len, out, out_lse, workspace)
     Dv, out, out_lse = _attn_outputs(q, k, v, None, out, out_lse)
     h = lib()
     args = _attn_args(q, k, v, places, cu_q, kv_len, seq_len, scale, Dv, rank, n_ranks, interleave, causal, k_scale,

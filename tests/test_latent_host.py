@@ -137,3 +137,29 @@ def test_binding_checks():
         attn.dcp_latent_attn(b(3, 4, 128), b(9, 16, 1, 576), b(4, 128, 512), b(4, 128, 512), i(2, 4), i(3), i(2), 64)
     with pytest.raises(ValueError, match="device tensors"):
         attn.dcp_prefix_attn(b(3, 4, 64), b(9, 16, 1, 64), b(9, 16, 1, 64), i(2, 4), i(3), i(2), i(2), i(1))
+
+
+def test_all_tensors_of_the_expanded_form_are_on_one_device(monkeypatch):
+    b = lambda *s: torch.zeros(s, dtype=torch.bfloat16)        # noqa: E731
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)           # noqa: E731
+    seen = []
+
+    class Seen(Exception):
+        pass
+
+    def on_gpu(*ts):
+        seen.extend(ts)
+        raise Seen
+
+    k, v = b(2, 64, 4, 192), b(2, 64, 4, 128)
+    rests, places, cu, kv, seq = (b(2, 64, 4, 128), b(2, 64, 4, 128)), i(2, 64), i(3), i(2), i(2)
+    q, work = b(3, 4, 192), torch.zeros(64, dtype=torch.uint8)
+    out, lse = b(3, 4, 128), torch.zeros(3, 4)
+    monkeypatch.setattr(attn, "latent_expand", lambda *a, **kw: (k, v))     # (which checks its own)
+    monkeypatch.setattr(attn, "_on_gpu", on_gpu)
+    with pytest.raises(Seen):
+        attn.dcp_latent_attn(q, b(9, 16, 1, 576), b(4, 128, 512), b(4, 128, 512), i(2, 4), cu, kv, 64, seq_len=seq, k_out=k,
+                             v_out=v, k_rest=rests[0], v_rest=rests[1], places=places, out=out, out_lse=lse, workspace=work)
+    at = {t.data_ptr() for t in seen if t is not None}
+    for t in (q, k, v, *rests, places, cu, kv, seq, out, lse, work):
+        assert t.data_ptr() in at
