@@ -146,10 +146,12 @@ __global__ __launch_bounds__(kThreads) void plan_lengths(PlanArgs p) {
                     int pg = -1;
 #pragma unroll
                     for (int i = 0; i < EACH; ++i) pg = i == e ? page[i] : pg;
-                    int at = count + tid, pushed = min(max(total - k0 - e * kThreads, 0), kThreads);
-                    if (gaps) at = count + scan_block(pg >= 0 ? 1 : 0, kMost, pushed, wave_s) - 1;
-                    if (pg >= 0 && at < p.free_max) p.free[at] = pg;
-                    count = min(count + pushed, p.free_max);
+                    // (unsigned: places behind a full list of nearly 2^31 pages pass 2^31)
+                    uint32_t at = (uint32_t)count + (uint32_t)tid;
+                    int pushed = min(max(total - k0 - e * kThreads, 0), kThreads);
+                    if (gaps) at = (uint32_t)count + (uint32_t)(scan_block(pg >= 0 ? 1 : 0, kMost, pushed, wave_s) - 1);
+                    if (pg >= 0 && at < (uint32_t)p.free_max) p.free[at] = pg;
+                    count = add_to(count, pushed, p.free_max);
                 }
             }
             __syncthreads();
