@@ -18,6 +18,7 @@
  *   dcpa_latent_expand        keys and values of all heads from latent rows
  *   dcpa_pair_attn            attention over keys and values in two 16-bit parts,
  *                             as the expansion makes them
+ *   dcpa_latent_attn          the two in one call: latent attention in its expanded form
  *   dcpa_attn_mass            accumulate the attention weight of each cached
  *                             key from the merged LSE of dcp_unpack_combine
  *   dcpa_cache_evict          keep the keys of highest accumulated weight:
@@ -385,6 +386,23 @@ typedef struct {
     double k_scale;
 } dcpa_expand_args;
 int dcpa_latent_expand(const dcpa_expand_args* a, void* stream);
+
+/*
+ * dcpa_latent_attn
+ *
+ * dcpa_latent_expand and then attention over what it made, by dcpa_pair_attn where
+ * k_rest and v_rest are given, else by dcpa_paged_attn.  The checks of both are made
+ * before either is enqueued: on an error k, v, the rests and places are as they were.
+ * `a` has q, cu_q, seq_len, out, lse, workspace, T, Hq, the ranks, causal, dtype (e's),
+ * lse_base, wide_weights and scale; B is that of e.  Its other fields are ignored: keys,
+ * values, lengths, heads, columns and the scale (of both keys and values) are those of
+ * e, whose places are needed and whose k, v and rests are contiguous over b (k_B =
+ * max_keys * k_S; so for each).  The keys and values that are written are those without
+ * k_scale, which goes to the scores and the outputs.  The workspace query takes
+ * the same arguments (k_rest NULL or not; other pointers may be NULL).
+ */
+int dcpa_latent_attn(const dcpa_expand_args* e, const dcpa_attn_args* a, void* stream);
+int64_t dcpa_latent_attn_workspace(const dcpa_expand_args* e, const dcpa_attn_args* a);
 
 #ifdef __cplusplus
 }

@@ -63,6 +63,8 @@ SIGNATURES = {
     "dcpa_pair_attn_workspace": ([_CP], _I64),
     "dcpa_project": ([_CP, _VP], ctypes.c_int),
     "dcpa_latent_expand": ([_CP, _VP], ctypes.c_int),
+    "dcpa_latent_attn": ([_CP, _CP, _VP], ctypes.c_int),
+    "dcpa_latent_attn_workspace": ([_CP, _CP], _I64),
 }
 # The argument structs: every field 8 bytes, in the header's order.
 ROPE_ARGS = struct.Struct("=45q3d")
@@ -471,21 +473,8 @@ def latent_values(o: torch.Tensor, w_uv: torch.Tensor, *, out: Optional[torch.Te
     return _project(o, w_uv, False, w_uv.shape[1], w_uv.shape[2], 0, out, "latent_values")
 
 
-def latent_expand(kv_cache: torch.Tensor, w_uk: torch.Tensor, w_uv: torch.Tensor, block_table: torch.Tensor,
-                  kv_len: torch.Tensor, max_keys: int, *, k_scale: float = 1.0, k_out: Optional[torch.Tensor] = None,
-                  v_out: Optional[torch.Tensor] = None, k_rest: Optional[torch.Tensor] = None,
-                  v_rest: Optional[torch.Tensor] = None, places: Optional[torch.Tensor] = None):
-    """Keys and values of every head from cached latent rows kv_cache
-    [pages,page_size,1,Dc+Dr]: for the first kv_len[b] cached keys of each
-    sequence (at most max_keys), k [B,max_keys,H,Dn+Dr] = [w_uk[h] c | rope] and
-    v [B,max_keys,H,Dv] = w_uv[h] c, with w_uk [H,Dn,Dc] and w_uv [H,Dv,Dc]
-    (contiguous over Dc), rounded to the weights' type.  k_rest [B,max_keys,H,Dn]
-    and v_rest [B,max_keys,H,Dv] (both or neither) get what the rounding leaves, in
-    the same type.  Rows behind kv_len and keys without a page are left as they
-    were.  places (int32 [B,max_keys]) gets the block_table for caches of one key to a
-    page, as which dcp_paged_attn takes k and v (dcp_latent_attn does it all).
-    Returns (k, v)."""
-    dev = _on_gpu(kv_cache, w_uk, w_uv, block_table, kv_len, k_out, v_out, k_rest, v_rest, places)
+def _expand_args(kv_cache, w_uk, w_uv, block_table, kv_len, max_keys, k_scale, k_out, v_out, k_rest, v_rest, places):
+    """The packed dcpa_expand_args of an expansion, and its outputs, allocated where they are not given."""
     for t, name, nd in ((kv_cache, "kv_cache", 4), (w_uk, "w_uk", 3), (w_uv, "w_uv", 3)):
         _rows(t, name, nd)
     H, Dn, Dc = w_uk.shape
@@ -517,11 +506,30 @@ def latent_expand(kv_cache: torch.Tensor, w_uk: torch.Tensor, w_uv: torch.Tensor
     if places is not None:
         _ints(places, "places", (B, max_keys))
     cs, wk, wv = kv_cache.stride(), w_uk.stride(), w_uv.stride()
-    args = EXPAND_ARGS.pack(
+    return EXPAND_ARGS.pack(
         kv_cache.data_ptr(), cs[0], cs[1], block_table.data_ptr(), block_table.stride(0), kv_len.data_ptr(),
         w_uk.data_ptr(), wk[0], wk[1], w_uv.data_ptr(), wv[0], wv[1], *strides,
         places.data_ptr() if places is not None else 0, places.stride(0) if places is not None else 0,
-        B, H, Dn, Dr, Dv, Dc, max_keys, kv_cache.shape[0], kv_cache.shape[1], block_table.shape[1], dt, ct, k_scale)
+        B, H, Dn, Dr, Dv, Dc, max_keys, kv_cache.shape[0], kv_cache.shape[1], block_table.shape[1], dt, ct, k_scale), k_out, v_out
+
+
+def latent_expand(kv_cache: torch.Tensor, w_uk: torch.Tensor, w_uv: torch.Tensor, block_table: torch.Tensor,
+                  kv_len: torch.Tensor, max_keys: int, *, k_scale: float = 1.0, k_out: Optional[torch.Tensor] = None,
+                  v_out: Optional[torch.Tensor] = None, k_rest: Optional[torch.Tensor] = None,
+                  v_rest: Optional[torch.Tensor] = None, places: Optional[torch.Tensor] = None):
+    """Keys and values of every head from cached latent rows kv_cache
+    [pages,page_size,1,Dc+Dr]: for the first kv_len[b] cached keys of each
+    sequence (at most max_keys), k [B,max_keys,H,Dn+Dr] = [w_uk[h] c | rope] and
+    v [B,max_keys,H,Dv] = w_uv[h] c, with w_uk [H,Dn,Dc] and w_uv [H,Dv,Dc]
+    (contiguous over Dc), rounded to the weights' type.  k_rest [B,max_keys,H,Dn]
+    and v_rest [B,max_keys,H,Dv] (both or neither) get what the rounding leaves, in
+    the same type.  Rows behind kv_len and keys without a page are left as they
+    were.  places (int32 [B,max_keys]) gets the block_table for caches of one key to a
+    page, as which dcp_paged_attn takes k and v (dcp_latent_attn does it all).
+    Returns (k, v)."""
+    dev = _on_gpu(kv_cache, w_uk, w_uv, block_table, kv_len, k_out, v_out, k_rest, v_rest, places)
+    args, k_out, v_out = _expand_args(kv_cache, w_uk, w_uv, block_table, kv_len, max_keys, k_scale, k_out, v_out, k_rest,
+                                      v_rest, places)
     _call(lib().dcpa_latent_expand, "dcpa_latent_expand", dev, args)
     return k_out, v_out
 
@@ -556,6 +564,10 @@ def dcp_latent_attn(q: torch.Tensor, kv_cache: torch.Tensor, w_uk: torch.Tensor,
         raise ValueError("expected q [T,H,Dn+Dr] of the weights' dtype")
     if rounded and (k_rest is not None or v_rest is not None):
         raise ValueError("rounded keys and values have no rest")
+    # (one call, whose checks are all made before it writes anything)
+    dev = _on_gpu(q, kv_cache, w_uk, w_uv, block_table, cu_q, kv_len, seq_len, k_out, v_out, k_rest, v_rest, places, out,
+                  out_lse, workspace)
+    _require(max_keys >= 0, "max_keys must not be negative")
     if places is None:
         places = torch.empty((B, max_keys), dtype=torch.int32, device=q.device)
     if not rounded:
@@ -563,23 +575,15 @@ def dcp_latent_attn(q: torch.Tensor, kv_cache: torch.Tensor, w_uk: torch.Tensor,
             k_rest = torch.empty((B, max_keys, H, Dn), dtype=q.dtype, device=q.device)
         if v_rest is None:
             v_rest = torch.empty((B, max_keys, H, Dv), dtype=q.dtype, device=q.device)
-    # (the scale goes to the scores and the outputs, so that the columns of the rope stay exact)
-    k, v = latent_expand(kv_cache, w_uk, w_uv, block_table, kv_len, max_keys, k_out=k_out, v_out=v_out, k_rest=k_rest,
-                         v_rest=v_rest, places=places)
+    make, k, v = _expand_args(kv_cache, w_uk, w_uv, block_table, kv_len, max_keys, k_scale, k_out, v_out, k_rest, v_rest,
+                              places)
     k, v = k.view(B * max_keys, 1, H, Dk), v.view(B * max_keys, 1, H, Dv)
-    if rounded:
-        return dcp_paged_attn(q, k, v, places, cu_q, kv_len, seq_len=seq_len, scale=scale, rank=rank, n_ranks=n_ranks,
-                              interleave=interleave, causal=causal, k_scale=k_scale, v_scale=k_scale,
-                              is_lse_base_on_e=is_lse_base_on_e, wide_weights=wide_weights, out=out, out_lse=out_lse,
-                              workspace=workspace)
-    dev = _on_gpu(q, k, v, k_rest, v_rest, places, cu_q, kv_len, seq_len, out, out_lse, workspace)
     Dv, out, out_lse = _attn_outputs(q, k, v, None, out, out_lse)
     h = lib()
     args = _attn_args(q, k, v, places, cu_q, kv_len, seq_len, scale, Dv, rank, n_ranks, interleave, causal, k_scale,
                       k_scale, is_lse_base_on_e, wide_weights, out, out_lse, 0, 0)
-    args, _keep = _with_workspace(args, h.dcpa_pair_attn_workspace, "dcpa_pair_attn", workspace, q)
-    _call(h.dcpa_pair_attn, "dcpa_pair_attn", dev, args, k_rest.data_ptr(), H * Dn, H * Dn, Dn, Dn, v_rest.data_ptr(),
-          H * Dv, H * Dv, Dv)
+    args, _keep = _with_workspace(args, lambda a: h.dcpa_latent_attn_workspace(make, a), "dcpa_latent_attn", workspace, q)
+    _call(h.dcpa_latent_attn, "dcpa_latent_attn", dev, make, args)
     return out, out_lse
 
 

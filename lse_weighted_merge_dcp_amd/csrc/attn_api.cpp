@@ -200,6 +200,163 @@ int fill_attn(const dcpa_attn_args* a, const AttnPlan& pl, AttnArgs& k, int64_t 
     return DCP_OK;
 }
 
+// The checks of an attention call and its arguments; any: there are rows.
+int prepare_attn(const dcpa_attn_args* a, AttnArgs& k, AttnPlan& pl, bool& any) {
+    any = false;
+    if (int st = check_attn(a, k.m)) return st;
+    if (a->B == 0 || a->T == 0) return DCP_OK;
+    any = true;
+    if (int st = check_inputs(a)) return st;
+    if (int st = check_outputs(a)) return st;
+    pl = plan_of(a, k.m);
+    return fill_attn(a, pl, k);
+}
+int run_attn(const dcpa_attn_args* a, const AttnArgs& k, const AttnPlan& pl, void* stream) {
+    return status(launch_attn(k, pl, a->dtype == DCP_BF16, a->cache_dtype == DCP_FP8_E4M3, a->wide_weights != 0,
+                              (hipStream_t)stream));
+}
+
+// The second part of keys or values.
+struct Rest {
+    const void* at;
+    int64_t P, S, H;
+};
+int prepare_pairs(const dcpa_attn_args* a, const Rest& kr, int64_t Dr, const Rest& vr, PairArgs& k, AttnPlan& pl, bool& any) {
+    any = false;
+    if (int st = check_pairs(a, k.m, pl)) return st;
+    if (Dr < 8 || Dr % 8 != 0 || Dr > a->Dk) return DCP_ERR_SHAPE;
+    if (!strides_ok({kr.P, kr.S, kr.H, vr.P, vr.S, vr.H}) ||
+        !span_ok({{a->num_pages, kr.P}, {a->page_size, kr.S}, {a->Hkv, kr.H}, {Dr, 1}}, 2) ||
+        !span_ok({{a->num_pages, vr.P}, {a->page_size, vr.S}, {a->Hkv, vr.H}, {a->Dv, 1}}, 2))
+        return DCP_ERR_STRIDE;
+    if (a->B == 0 || a->T == 0) return DCP_OK;
+    any = true;
+    if (int st = check_inputs(a)) return st;
+    if (a->num_pages > 0 && (!kr.at || !vr.at)) return DCP_ERR_NULL;
+    if (int st = check_outputs(a)) return st;
+    if (!aligned(kr.at, 16) || !aligned(vr.at, 16) || !multiples({kr.P, kr.S, kr.H, vr.P, vr.S, vr.H}, 8)) return DCP_ERR_ALIGN;
+    if (int st = fill_attn(a, pl, k)) return st;
+    k.kr = (const char*)kr.at;
+    k.kr_P = kr.P * 2; k.kr_S = kr.S * 2; k.kr_H = kr.H * 2;
+    k.vr = (const char*)vr.at;
+    k.vr_P = vr.P * 2; k.vr_S = vr.S * 2; k.vr_H = vr.H * 2;
+    k.Dr = (int32_t)Dr;
+    return DCP_OK;
+}
+int run_pairs(const dcpa_attn_args* a, const PairArgs& k, const AttnPlan& pl, void* stream) {
+    return status(launch_pairs(k, pl, a->dtype == DCP_BF16, a->wide_weights != 0, (hipStream_t)stream));
+}
+
+// What the expansion takes, without its pointers.
+int check_expand(const dcpa_expand_args* a) {
+    if (a->dtype != DCP_F16 && a->dtype != DCP_BF16) return DCP_ERR_DTYPE;
+    if (a->cache_dtype != a->dtype && a->cache_dtype != DCP_FP8_E4M3) return DCP_ERR_DTYPE;
+    auto cols = [](int64_t d) { return d >= 8 && d % 8 == 0 && d <= 512; };
+    if (a->B < 0 || a->B > (int64_t(1) << 20) || a->H < 1 || a->H > (1 << 16) || !cols(a->Dn) || !cols(a->Dv) ||
+        a->Dr < 0 || a->Dr % 8 != 0 || a->Dc < 8 || a->Dc % 8 != 0 || a->Dr > 576 || a->Dc > 576 || a->Dc + a->Dr > 576 ||
+        a->max_keys < 0 || a->max_keys >= kMaxRows || a->B * a->max_keys >= kMaxRows ||
+        !cache_shape_ok(a->num_pages, a->page_size, a->max_pages))
+        return DCP_ERR_SHAPE;
+    if (expand_workgroups(a->B, a->max_keys, a->k_rest != nullptr) > kMaxGrid / 2) return DCP_ERR_SHAPE;
+    if (!positive(a->k_scale)) return DCPA_ERR_VALUE;
+    const int ec = esize_of(a->cache_dtype);
+    if (!strides_ok({a->c_P, a->c_S, a->t_B, a->wk_H, a->wk_N, a->wv_H, a->wv_N, a->k_B, a->k_S, a->k_H, a->v_B, a->v_S,
+                     a->v_H, a->kr_B, a->kr_S, a->kr_H, a->vr_B, a->vr_S, a->vr_H, a->p_B}) ||
+        !span_ok({{a->B, a->kr_B}, {a->max_keys, a->kr_S}, {a->H, a->kr_H}, {a->Dn, 1}}, 2) ||
+        !span_ok({{a->B, a->vr_B}, {a->max_keys, a->vr_S}, {a->H, a->vr_H}, {a->Dv, 1}}, 2) ||
+        !span_ok({{a->num_pages, a->c_P}, {a->page_size, a->c_S}, {a->Dc + a->Dr, 1}}, ec) ||
+        !span_ok({{a->B, a->t_B}, {a->max_pages, 1}}, 4) || !span_ok({{a->B, a->p_B}, {a->max_keys, 1}}, 4) ||
+        !span_ok({{a->H, a->wk_H}, {a->Dn, a->wk_N}, {a->Dc, 1}}, 2) ||
+        !span_ok({{a->H, a->wv_H}, {a->Dv, a->wv_N}, {a->Dc, 1}}, 2) ||
+        !span_ok({{a->B, a->k_B}, {a->max_keys, a->k_S}, {a->H, a->k_H}, {a->Dn + a->Dr, 1}}, 2) ||
+        !span_ok({{a->B, a->v_B}, {a->max_keys, a->v_S}, {a->H, a->v_H}, {a->Dv, 1}}, 2))
+        return DCP_ERR_STRIDE;
+    return DCP_OK;
+}
+// Its checks and arguments; any: there is something to expand.
+int prepare_expand(const dcpa_expand_args* a, ExpandArgs& k, bool& any) {
+    any = false;
+    if (int st = check_expand(a)) return st;
+    if (a->B == 0 || a->max_keys == 0) return DCP_OK;
+    any = true;
+    if ((a->max_pages > 0 && !a->block_table) || !a->kv_len || !a->w_k || !a->w_v || !a->k || !a->v || (a->num_pages > 0 && !a->cache) || !a->k_rest != !a->v_rest)
+        return DCP_ERR_NULL;
+    for (const void* x : {a->cache, a->w_k, a->w_v, (const void*)a->k, (const void*)a->v, (const void*)a->k_rest, (const void*)a->v_rest})
+        if (!aligned(x, 16)) return DCP_ERR_ALIGN;
+    if (!multiples({a->c_P, a->c_S, a->wk_H, a->wk_N, a->wv_H, a->wv_N, a->k_B, a->k_S, a->k_H, a->v_B, a->v_S, a->v_H,
+                    a->kr_B, a->kr_S, a->kr_H, a->vr_B, a->vr_S, a->vr_H}, 8) ||
+        !aligned(a->block_table, 4) || !aligned(a->kv_len, 4) || !aligned(a->places, 4))
+        return DCP_ERR_ALIGN;
+    const int ec = esize_of(a->cache_dtype);
+    const int64_t named = a->max_pages * a->page_size, keys = a->max_keys < named ? a->max_keys : named;
+    k.cache = (const char*)a->cache;
+    k.c_P = a->c_P * ec; k.c_S = a->c_S * ec;
+    k.table = a->block_table; k.kv = a->kv_len;
+    k.t_B = a->t_B;
+    k.wk = (const char*)a->w_k; k.wv = (const char*)a->w_v;
+    k.wk_H = a->wk_H * 2; k.wk_N = a->wk_N * 2; k.wv_H = a->wv_H * 2; k.wv_N = a->wv_N * 2;
+    k.ko = (char*)a->k; k.vo = (char*)a->v;
+    k.ko_B = a->k_B * 2; k.ko_S = a->k_S * 2; k.ko_H = a->k_H * 2;
+    k.vo_B = a->v_B * 2; k.vo_S = a->v_S * 2; k.vo_H = a->v_H * 2;
+    k.kr = (char*)a->k_rest; k.vr = (char*)a->v_rest;
+    k.kr_B = a->kr_B * 2; k.kr_S = a->kr_S * 2; k.kr_H = a->kr_H * 2;
+    k.vr_B = a->vr_B * 2; k.vr_S = a->vr_S * 2; k.vr_H = a->vr_H * 2;
+    k.places = a->places;
+    k.pl_B = a->p_B;
+    k.B = (int32_t)a->B; k.H = (int32_t)a->H;
+    k.Dn = (int32_t)a->Dn; k.Dr = (int32_t)a->Dr; k.Dv = (int32_t)a->Dv; k.Dc = (int32_t)a->Dc;
+    k.most = (int32_t)a->max_keys; k.keys = (int32_t)keys; k.pages = (int32_t)a->num_pages;
+    k.fpage = dcp::make_fastdiv((uint32_t)a->page_size);
+    k.fper = dcp::make_fastdiv((uint32_t)(a->Dn + a->Dv));
+    k.ks = (float)a->k_scale;
+    return DCP_OK;
+}
+int run_expand(const dcpa_expand_args* a, const ExpandArgs& k, void* stream) {
+    return status(launch_expand(k, a->dtype == DCP_BF16, a->cache_dtype == DCP_FP8_E4M3, (hipStream_t)stream));
+}
+
+// The two calls that attention in the expanded form consists of: `make` without the scale, which goes to the scores and
+// the outputs, so that the columns of the rope stay exact, and attention over caches of one key to a page.
+int expanded_form(const dcpa_expand_args* e, const dcpa_attn_args* a, dcpa_expand_args& make, dcpa_attn_args& over, Rest& kr,
+                  Rest& vr) {
+    if (int st = check_expand(e)) return st;
+    if (a->dtype != e->dtype) return DCP_ERR_DTYPE;
+    if (a->B != e->B) return DCP_ERR_SHAPE;
+    const int64_t n = e->max_keys;
+    // from a key to the next, over all sequences
+    if (e->B > 1 && n > 1 && (e->k_B != n * e->k_S || e->v_B != n * e->v_S ||
+                              (e->k_rest && (e->kr_B != n * e->kr_S || e->vr_B != n * e->vr_S))))
+        return DCP_ERR_STRIDE;
+    auto apart = [&](int64_t b, int64_t s) { return n > 1 ? s : b; };
+    kr = Rest{e->k_rest, apart(e->kr_B, e->kr_S), 0, e->kr_H};
+    vr = Rest{e->v_rest, apart(e->vr_B, e->vr_S), 0, e->vr_H};
+    make = *e;
+    make.k_scale = 1.0;
+    over = *a;
+    over.k = e->k;
+    over.k_P = apart(e->k_B, e->k_S);
+    over.k_S = 0;
+    over.k_H = e->k_H;
+    // (no values at all, an empty buffer or a size query: NULL would say that they lie within the keys)
+    static const char none alignas(16) = 0;
+    over.v = e->v ? e->v : &none;
+    over.v_P = apart(e->v_B, e->v_S);
+    over.v_S = 0;
+    over.v_H = e->v_H;
+    over.block_table = e->places;
+    over.t_B = e->p_B;
+    over.kv_len = e->kv_len;
+    over.Hkv = e->H;
+    over.Dk = e->Dn + e->Dr;
+    over.Dv = e->Dv;
+    over.num_pages = e->B * n;
+    over.page_size = 1;
+    over.max_pages = n;
+    over.cache_dtype = e->dtype;
+    over.k_scale = over.v_scale = e->k_scale;
+    return DCP_OK;
+}
+
 // The weights' plan; as check_attn, no more workgroups than a launch may have.
 int check_mass(const dcpa_attn_args* a, Batch& m, MassPlan& pl) {
     if (int st = check_batch(a, m)) return st;
@@ -239,14 +396,10 @@ int64_t dcpa_paged_attn_workspace(const dcpa_attn_args* a) {
 int dcpa_paged_attn(const dcpa_attn_args* a, void* stream) {
     if (a == nullptr) return DCP_ERR_NULL;
     AttnArgs k;
-    if (int st = check_attn(a, k.m)) return st;
-    if (a->B == 0 || a->T == 0) return DCP_OK;
-    if (int st = check_inputs(a)) return st;
-    if (int st = check_outputs(a)) return st;
-    const AttnPlan pl = plan_of(a, k.m);
-    if (int st = fill_attn(a, pl, k)) return st;
-    return status(launch_attn(k, pl, a->dtype == DCP_BF16, a->cache_dtype == DCP_FP8_E4M3, a->wide_weights != 0,
-                              (hipStream_t)stream));
+    AttnPlan pl;
+    bool any;
+    if (int st = prepare_attn(a, k, pl, any)) return st;
+    return any ? run_attn(a, k, pl, stream) : DCP_OK;
 }
 
 int64_t dcpa_prefix_attn_workspace(const dcpa_attn_args* a, int64_t n_groups) {
@@ -292,24 +445,9 @@ int dcpa_pair_attn(const dcpa_attn_args* a, const void* k_rest, int64_t kr_P, in
     if (a == nullptr) return DCP_ERR_NULL;
     PairArgs k;
     AttnPlan pl;
-    if (int st = check_pairs(a, k.m, pl)) return st;
-    if (Dr < 8 || Dr % 8 != 0 || Dr > a->Dk) return DCP_ERR_SHAPE;
-    if (!strides_ok({kr_P, kr_S, kr_H, vr_P, vr_S, vr_H}) ||
-        !span_ok({{a->num_pages, kr_P}, {a->page_size, kr_S}, {a->Hkv, kr_H}, {Dr, 1}}, 2) ||
-        !span_ok({{a->num_pages, vr_P}, {a->page_size, vr_S}, {a->Hkv, vr_H}, {a->Dv, 1}}, 2))
-        return DCP_ERR_STRIDE;
-    if (a->B == 0 || a->T == 0) return DCP_OK;
-    if (int st = check_inputs(a)) return st;
-    if (a->num_pages > 0 && (!k_rest || !v_rest)) return DCP_ERR_NULL;
-    if (int st = check_outputs(a)) return st;
-    if (!aligned(k_rest, 16) || !aligned(v_rest, 16) || !multiples({kr_P, kr_S, kr_H, vr_P, vr_S, vr_H}, 8)) return DCP_ERR_ALIGN;
-    if (int st = fill_attn(a, pl, k)) return st;
-    k.kr = (const char*)k_rest;
-    k.kr_P = kr_P * 2; k.kr_S = kr_S * 2; k.kr_H = kr_H * 2;
-    k.vr = (const char*)v_rest;
-    k.vr_P = vr_P * 2; k.vr_S = vr_S * 2; k.vr_H = vr_H * 2;
-    k.Dr = (int32_t)Dr;
-    return status(launch_pairs(k, pl, a->dtype == DCP_BF16, a->wide_weights != 0, (hipStream_t)stream));
+    bool any;
+    if (int st = prepare_pairs(a, Rest{k_rest, kr_P, kr_S, kr_H}, Dr, Rest{v_rest, vr_P, vr_S, vr_H}, k, pl, any)) return st;
+    return any ? run_pairs(a, k, pl, stream) : DCP_OK;
 }
 
 int64_t dcpa_attn_mass_workspace(const dcpa_attn_args* a) {
@@ -556,60 +694,40 @@ int dcpa_project(const dcpa_project_args* a, void* stream) {
 
 int dcpa_latent_expand(const dcpa_expand_args* a, void* stream) {
     if (a == nullptr) return DCP_ERR_NULL;
-    if (a->dtype != DCP_F16 && a->dtype != DCP_BF16) return DCP_ERR_DTYPE;
-    if (a->cache_dtype != a->dtype && a->cache_dtype != DCP_FP8_E4M3) return DCP_ERR_DTYPE;
-    auto cols = [](int64_t d) { return d >= 8 && d % 8 == 0 && d <= 512; };
-    if (a->B < 0 || a->B > (int64_t(1) << 20) || a->H < 1 || a->H > (1 << 16) || !cols(a->Dn) || !cols(a->Dv) ||
-        a->Dr < 0 || a->Dr % 8 != 0 || a->Dc < 8 || a->Dc % 8 != 0 || a->Dr > 576 || a->Dc > 576 || a->Dc + a->Dr > 576 ||
-        a->max_keys < 0 || a->max_keys >= kMaxRows || a->B * a->max_keys >= kMaxRows ||
-        !cache_shape_ok(a->num_pages, a->page_size, a->max_pages))
-        return DCP_ERR_SHAPE;
-    const int64_t named = a->max_pages * a->page_size, keys = a->max_keys < named ? a->max_keys : named;
-    if (expand_workgroups(a->B, a->max_keys, a->k_rest != nullptr) > kMaxGrid / 2) return DCP_ERR_SHAPE;
-    if (!positive(a->k_scale)) return DCPA_ERR_VALUE;
-    const int ec = esize_of(a->cache_dtype);
-    if (!strides_ok({a->c_P, a->c_S, a->t_B, a->wk_H, a->wk_N, a->wv_H, a->wv_N, a->k_B, a->k_S, a->k_H, a->v_B, a->v_S,
-                     a->v_H, a->kr_B, a->kr_S, a->kr_H, a->vr_B, a->vr_S, a->vr_H, a->p_B}) ||
-        !span_ok({{a->B, a->kr_B}, {a->max_keys, a->kr_S}, {a->H, a->kr_H}, {a->Dn, 1}}, 2) ||
-        !span_ok({{a->B, a->vr_B}, {a->max_keys, a->vr_S}, {a->H, a->vr_H}, {a->Dv, 1}}, 2) ||
-        !span_ok({{a->num_pages, a->c_P}, {a->page_size, a->c_S}, {a->Dc + a->Dr, 1}}, ec) ||
-        !span_ok({{a->B, a->t_B}, {a->max_pages, 1}}, 4) || !span_ok({{a->B, a->p_B}, {a->max_keys, 1}}, 4) ||
-        !span_ok({{a->H, a->wk_H}, {a->Dn, a->wk_N}, {a->Dc, 1}}, 2) ||
-        !span_ok({{a->H, a->wv_H}, {a->Dv, a->wv_N}, {a->Dc, 1}}, 2) ||
-        !span_ok({{a->B, a->k_B}, {a->max_keys, a->k_S}, {a->H, a->k_H}, {a->Dn + a->Dr, 1}}, 2) ||
-        !span_ok({{a->B, a->v_B}, {a->max_keys, a->v_S}, {a->H, a->v_H}, {a->Dv, 1}}, 2))
-        return DCP_ERR_STRIDE;
-    if (a->B == 0 || a->max_keys == 0) return DCP_OK;
-    if ((a->max_pages > 0 && !a->block_table) || !a->kv_len || !a->w_k || !a->w_v || !a->k || !a->v || (a->num_pages > 0 && !a->cache) || !a->k_rest != !a->v_rest)
-        return DCP_ERR_NULL;
-    for (const void* x : {a->cache, a->w_k, a->w_v, (const void*)a->k, (const void*)a->v, (const void*)a->k_rest, (const void*)a->v_rest})
-        if (!aligned(x, 16)) return DCP_ERR_ALIGN;
-    if (!multiples({a->c_P, a->c_S, a->wk_H, a->wk_N, a->wv_H, a->wv_N, a->k_B, a->k_S, a->k_H, a->v_B, a->v_S, a->v_H,
-                    a->kr_B, a->kr_S, a->kr_H, a->vr_B, a->vr_S, a->vr_H}, 8) ||
-        !aligned(a->block_table, 4) || !aligned(a->kv_len, 4) || !aligned(a->places, 4))
-        return DCP_ERR_ALIGN;
     ExpandArgs k;
-    k.cache = (const char*)a->cache;
-    k.c_P = a->c_P * ec; k.c_S = a->c_S * ec;
-    k.table = a->block_table; k.kv = a->kv_len;
-    k.t_B = a->t_B;
-    k.wk = (const char*)a->w_k; k.wv = (const char*)a->w_v;
-    k.wk_H = a->wk_H * 2; k.wk_N = a->wk_N * 2; k.wv_H = a->wv_H * 2; k.wv_N = a->wv_N * 2;
-    k.ko = (char*)a->k; k.vo = (char*)a->v;
-    k.ko_B = a->k_B * 2; k.ko_S = a->k_S * 2; k.ko_H = a->k_H * 2;
-    k.vo_B = a->v_B * 2; k.vo_S = a->v_S * 2; k.vo_H = a->v_H * 2;
-    k.kr = (char*)a->k_rest; k.vr = (char*)a->v_rest;
-    k.kr_B = a->kr_B * 2; k.kr_S = a->kr_S * 2; k.kr_H = a->kr_H * 2;
-    k.vr_B = a->vr_B * 2; k.vr_S = a->vr_S * 2; k.vr_H = a->vr_H * 2;
-    k.places = a->places;
-    k.pl_B = a->p_B;
-    k.B = (int32_t)a->B; k.H = (int32_t)a->H;
-    k.Dn = (int32_t)a->Dn; k.Dr = (int32_t)a->Dr; k.Dv = (int32_t)a->Dv; k.Dc = (int32_t)a->Dc;
-    k.most = (int32_t)a->max_keys; k.keys = (int32_t)keys; k.pages = (int32_t)a->num_pages;
-    k.fpage = dcp::make_fastdiv((uint32_t)a->page_size);
-    k.fper = dcp::make_fastdiv((uint32_t)(a->Dn + a->Dv));
-    k.ks = (float)a->k_scale;
-    return status(launch_expand(k, a->dtype == DCP_BF16, a->cache_dtype == DCP_FP8_E4M3, (hipStream_t)stream));
+    bool any;
+    if (int st = prepare_expand(a, k, any)) return st;
+    return any ? run_expand(a, k, stream) : DCP_OK;
+}
+
+int64_t dcpa_latent_attn_workspace(const dcpa_expand_args* e, const dcpa_attn_args* a) {
+    if (e == nullptr || a == nullptr) return DCP_ERR_NULL;
+    dcpa_expand_args make;
+    dcpa_attn_args over;
+    Rest kr, vr;
+    if (int st = expanded_form(e, a, make, over, kr, vr)) return st;
+    return e->k_rest ? dcpa_pair_attn_workspace(&over) : dcpa_paged_attn_workspace(&over);
+}
+
+int dcpa_latent_attn(const dcpa_expand_args* e, const dcpa_attn_args* a, void* stream) {
+    if (e == nullptr || a == nullptr) return DCP_ERR_NULL;
+    dcpa_expand_args make;
+    dcpa_attn_args over;
+    Rest kr, vr;
+    if (int st = expanded_form(e, a, make, over, kr, vr)) return st;
+    ExpandArgs x;
+    PairArgs k;
+    AttnPlan pl;
+    bool keys, rows;
+    if (int st = prepare_expand(&make, x, keys)) return st;
+    if (keys && !e->places) return DCP_ERR_NULL;
+    const bool parts = e->k_rest != nullptr;
+    if (int st = parts ? prepare_pairs(&over, kr, e->Dn, vr, k, pl, rows) : prepare_attn(&over, k, pl, rows)) return st;
+    // (every check is made: from here on work is enqueued)
+    if (keys)
+        if (int st = run_expand(&make, x, stream)) return st;
+    if (!rows) return DCP_OK;
+    return parts ? run_pairs(&over, k, pl, stream) : run_attn(&over, k, pl, stream);
 }
 
 }  // extern "C"

@@ -38,7 +38,7 @@ EXPORTS = {
     ATTN_LIB: ["dcpa_status_str", "dcpa_qk_norm_rope_append", "dcpa_paged_attn", "dcpa_paged_attn_workspace",
                "dcpa_attn_mass", "dcpa_attn_mass_workspace", "dcpa_cache_evict", "dcpa_batch_plan",
                "dcpa_project", "dcpa_latent_expand", "dcpa_prefix_attn", "dcpa_prefix_attn_workspace",
-               "dcpa_pair_attn", "dcpa_pair_attn_workspace"],
+               "dcpa_pair_attn", "dcpa_pair_attn_workspace", "dcpa_latent_attn", "dcpa_latent_attn_workspace"],
 }
 OBJECTS = {
     LIB: ["api", "pack", "combine", "inplace"],
