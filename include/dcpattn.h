@@ -397,9 +397,12 @@ int dcpa_latent_expand(const dcpa_expand_args* a, void* stream);
  * lse_base, wide_weights and scale; B is that of e.  Its other fields are ignored: keys,
  * values, lengths, heads, columns and the scale (of both keys and values) are those of
  * e, whose places are needed and whose k, v and rests are contiguous over b (k_B =
- * max_keys * k_S; so for each).  The keys and values that are written are those without
- * k_scale, which goes to the scores and the outputs.  The workspace query takes
- * the same arguments (k_rest NULL or not; other pointers may be NULL).
+ * max_keys * k_S; so for each).  k_scale = f 2^p with the power of two p that makes 1
+ * <= f < 2, held to [-15, 7] (a 16-bit cache: [-15, 0]): the keys and values that
+ * are written are those divided by f, which goes to the scores and the outputs.  The
+ * columns of the rope are exact in them (but for an fp16 cache with k_scale < 1,
+ * where they are off by up to 2^-25).  The workspace query takes the same
+ * arguments (k_rest NULL or not; other pointers may be NULL).
  */
 int dcpa_latent_attn(const dcpa_expand_args* e, const dcpa_attn_args* a, void* stream);
 int64_t dcpa_latent_attn_workspace(const dcpa_expand_args* e, const dcpa_attn_args* a);

@@ -553,8 +553,10 @@ def dcp_latent_attn(q: torch.Tensor, kv_cache: torch.Tensor, w_uk: torch.Tensor,
     as a cache would hold them, and is faster.  max_keys: as many keys as a sequence
     may have cached here at most; kv_len is clamped to it.  k_out, v_out, k_rest,
     v_rest (contiguous, as latent_expand has them) and places are buffers to keep
-    them in, fresh ones if not given; they hold keys without k_scale.  The other
-    arguments are those of dcp_paged_attn.  Returns (out [T,H,Dv], lse [T,H])."""
+    them in, fresh ones if not given; they hold keys and values divided by what is left
+    of k_scale without a power of two (dcpa_latent_attn in the header), so that they
+    are in the type's range where the keys themselves are.  The other arguments are
+    those of dcp_paged_attn.  Returns (out [T,H,Dv], lse [T,H])."""
     B, (H, Dn, _), Dv = kv_len.shape[0], w_uk.shape, w_uv.shape[1]
     Dk = Dn + kv_cache.shape[3] - w_uk.shape[2]
     for t, name in ((k_out, "k_out"), (v_out, "v_out"), (k_rest, "k_rest"), (v_rest, "v_rest"), (places, "places")):

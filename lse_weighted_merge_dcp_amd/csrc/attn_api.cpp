@@ -315,8 +315,14 @@ int run_expand(const dcpa_expand_args* a, const ExpandArgs& k, void* stream) {
     return status(launch_expand(k, a->dtype == DCP_BF16, a->cache_dtype == DCP_FP8_E4M3, (hipStream_t)stream));
 }
 
-// The two calls that attention in the expanded form consists of: `make` without the scale, which goes to the scores and
-// the outputs, so that the columns of the rope stay exact, and attention over caches of one key to a page.
+// The two calls that attention in the expanded form consists of: the expansion `make`, and attention over caches of one
+// key to a page.
+// The scale k_scale = f 2^e, 1 <= f < 2, is shared out: 2^e into the expansion, f to the scores and the outputs.  So what is
+// written is within a factor of 2 of the keys and values themselves, however small or large the scale of a cache, and
+// stays within fp16 where they do (a cache of rows near 448 with a scale of 2^-10 holds keys whose products with
+// the weights pass 65504 by themselves); and the columns of the rope, which have no second part, stay exact: an 8-bit
+// number, a multiple of 2^-9 up to 448, times 2^-15 to 2^7 is an fp16 one (16-bit ones lose what lies below 2^-24
+// times 1 / f; they are not made larger).
 int expanded_form(const dcpa_expand_args* e, const dcpa_attn_args* a, dcpa_expand_args& make, dcpa_attn_args& over, Rest& kr,
                   Rest& vr) {
     if (int st = check_expand(e)) return st;
@@ -331,7 +337,10 @@ int expanded_form(const dcpa_expand_args* e, const dcpa_attn_args* a, dcpa_expan
     kr = Rest{e->k_rest, apart(e->kr_B, e->kr_S), 0, e->kr_H};
     vr = Rest{e->v_rest, apart(e->vr_B, e->vr_S), 0, e->vr_H};
     make = *e;
-    make.k_scale = 1.0;
+    int power;
+    frexp(e->k_scale, &power);
+    const int least = -15, most = e->cache_dtype == DCP_FP8_E4M3 ? 7 : 0;
+    make.k_scale = ldexp(1.0, power - 1 < least ? least : power - 1 > most ? most : power - 1);
     over = *a;
     over.k = e->k;
     over.k_P = apart(e->k_B, e->k_S);
@@ -353,7 +362,7 @@ int expanded_form(const dcpa_expand_args* e, const dcpa_attn_args* a, dcpa_expan
     over.page_size = 1;
     over.max_pages = n;
     over.cache_dtype = e->dtype;
-    over.k_scale = over.v_scale = e->k_scale;
+    over.k_scale = over.v_scale = e->k_scale / make.k_scale;
     return DCP_OK;
 }
 
