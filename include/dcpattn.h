@@ -197,9 +197,9 @@ int64_t dcpa_paged_attn_workspace(const dcpa_attn_args* a);
  * but no access outside the buffers).
  *
  * Parts of every row live in `workspace`, whose size dcpa_prefix_attn_workspace
- * gives.  Weights of shared keys are rounded to `dtype` for the product with the
- * values, also where rows are few; wide_weights as in dcpa_paged_attn.  Up to 2^20 groups; the
- * limit of 2^23 workgroups counts the row tiles of sequences and of groups.
+ * gives.  The weights are held as in dcpa_paged_attn: with what their rounding leaves
+ * where rows are few (those of a sequence, not of a group) or wide_weights is
+ * given, else rounded to `dtype`.  Up to 2^20 groups; the limit of 2^23 workgroups counts the row tiles of sequences and of groups.
  */
 int dcpa_prefix_attn(const dcpa_attn_args* a, const int32_t* cu_group, const int32_t* shared_len, int64_t n_groups,
                      void* stream);

@@ -15,8 +15,10 @@ __global__ __launch_bounds__(256, DK > 192 ? 1 : 2) void prefix_rows(GroupArgs p
     rows_of<E, KV8, EXACT, DK, DV, KT, WIDE>(p, lds);
 }
 // The same where rows are few: a sequence's own keys shared out over the waves, which keeps more loads under
-// way.
-template <typename E, bool KV8, bool EXACT, int DK, int DV, int KT, int DO, bool WIDE>
+// way.  keys_of() holds every weight in two products, and so do the shared keys here (as attention of each sequence by
+// itself would): 64 sequences behind 32768 keys, 64 / 8 heads, 73 us, with one product for the shared keys 69; 48 of four
+// tokens over an 8-bit cache 54 and 46.
+template <typename E, bool KV8, bool EXACT, int DK, int DV, int KT, int DO>
 __global__ __launch_bounds__(256, DO > 128 ? 1 : 2) void prefix_few(GroupArgs p) {
     __shared__ union Lds {
         RowsLds<DK, DV, KT> rows;
@@ -24,7 +26,7 @@ __global__ __launch_bounds__(256, DO > 128 ? 1 : 2) void prefix_few(GroupArgs p)
     } lds;
     const int hk = (int)(blockIdx.x % (uint32_t)p.m.Hkv), unit = (int)(blockIdx.x / (uint32_t)p.m.Hkv);
     const GroupUnit u = unit_of<KT>(p, p.rows, unit);
-    if (u.b1 > u.b0) rows_of<E, KV8, EXACT, DK, DV, KT, WIDE>(p, lds.rows);
+    if (u.b1 > u.b0) rows_of<E, KV8, EXACT, DK, DV, KT, true>(p, lds.rows);
     else keys_of<E, KV8, DO, DO>(p, lds.keys, u, hk, unit);
 }
 template <typename E, bool KV8, bool WIDE> hipError_t run(const GroupArgs& a, hipStream_t stream) {
@@ -35,7 +37,9 @@ template <typename E, bool KV8, bool WIDE> hipError_t run(const GroupArgs& a, hi
     auto rows = [&](auto exact, auto dk, auto dv, auto kt, auto own) {
         constexpr bool X = decltype(exact)::value;
         constexpr int K = decltype(dk)::value, V = decltype(dv)::value, T = decltype(kt)::value, O = decltype(own)::value;
-        return few ? launch(prefix_few<E, KV8, X, K, V, T, O, WIDE>, grid, block, stream, a)
+        // (8-bit rows of 128 columns wait in registers to be widened: with 64 keys to a tile the loop would spill)
+        constexpr int TF = KV8 && K == 128 ? 32 : T;
+        return few ? launch(prefix_few<E, KV8, X, K, V, TF, O>, grid, block, stream, a)
                    : launch(prefix_rows<E, KV8, X, K, V, T, WIDE>, grid, block, stream, a);
     };
     constexpr std::integral_constant<int, 32> n32{};
