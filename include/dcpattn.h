@@ -199,7 +199,8 @@ int64_t dcpa_paged_attn_workspace(const dcpa_attn_args* a);
  * Parts of every row live in `workspace`, whose size dcpa_prefix_attn_workspace
  * gives.  The weights are held as in dcpa_paged_attn: with what their rounding leaves
  * where rows are few (those of a sequence, not of a group) or wide_weights is
- * given, else rounded to `dtype`.  Up to 2^20 groups; the limit of 2^23 workgroups counts the row tiles of sequences and of groups.
+ * given, else rounded to `dtype`.  Up to 2^20 groups; the limit of 2^23 workgroups
+ * counts the row tiles of sequences and of groups.
  */
 int dcpa_prefix_attn(const dcpa_attn_args* a, const int32_t* cu_group, const int32_t* shared_len, int64_t n_groups,
                      void* stream);
@@ -212,10 +213,11 @@ int64_t dcpa_prefix_attn_workspace(const dcpa_attn_args* a, int64_t n_groups);
  * its first Dr columns, k_rest [num_pages, page_size, Hkv, Dr]; a value is v plus
  * v_rest [num_pages, page_size, Hkv, Dv].  Products of both parts go into the same
  * fp32 sums, so scores and outputs are those of the sums of the parts; the
- * weights are rounded as there (wide_weights: not the values' second part's).
- * cache_dtype is dtype, v not NULL, Dk and Dv at most 256, Dr a multiple of 8 up to
- * Dk; the rests' strides are multiples of 8, 16-byte aligned.  A query that is not
- * finite gives NaN.  The workspace query is dcpa_pair_attn_workspace.
+ * weights are held as there, with what their rounding leaves where rows are few (at
+ * most 32 to a sequence on average) or wide_weights is given (in the product with the
+ * values' first part, not their second).  cache_dtype is dtype, v not NULL, Dk and
+ * Dv at most 256, Dr a multiple of 8 up to Dk; the rests' strides are multiples of 8,
+ * 16-byte aligned.  A query that is not finite gives NaN.  The workspace query is dcpa_pair_attn_workspace.
  */
 int dcpa_pair_attn(const dcpa_attn_args* a, const void* k_rest, int64_t kr_P, int64_t kr_S, int64_t kr_H, int64_t Dr,
                    const void* v_rest, int64_t vr_P, int64_t vr_S, int64_t vr_H, void* stream);

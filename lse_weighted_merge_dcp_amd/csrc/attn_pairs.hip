@@ -47,7 +47,9 @@ AttnPlan plan_pairs(const Batch& m, int Dv) {
     return pl;
 }
 
-hipError_t launch_pairs(const PairArgs& a, const AttnPlan& pl, bool bf16, bool wide, hipStream_t stream) {
+hipError_t launch_pairs(const PairArgs& a, const AttnPlan& pl, bool bf16, bool asked, hipStream_t stream) {
+    // few rows to a sequence: weights in two products, as where their keys are shared out over the waves (attn_keys.hpp)
+    const bool wide = asked || (int64_t)a.m.T * a.m.G <= (int64_t)32 * a.m.B;
     const hipError_t e = bf16 ? (wide ? run<BF16T, true>(a, pl, stream) : run<BF16T, false>(a, pl, stream))
                               : (wide ? run<F16T, true>(a, pl, stream) : run<F16T, false>(a, pl, stream));
     if (e != hipSuccess || pl.slots == 0) return e;
