@@ -196,10 +196,15 @@ int64_t dcpa_paged_attn_workspace(const dcpa_attn_args* a);
  * cu_group has to be non-decreasing (as cu_q, other contents give wrong numbers
  * but no access outside the buffers).
  *
- * Parts of every row live in `workspace`, whose size dcpa_prefix_attn_workspace
- * gives.  The weights are held as in dcpa_paged_attn: with what their rounding leaves
- * where rows are few (those of a sequence, not of a group) or wide_weights is
- * given, else rounded to `dtype`.  Up to 2^20 groups; the limit of 2^23 workgroups
+ * Sequences of many rows (128 and more of a key head to each on average) gain nothing
+ * from it, and neither does a batch without groups: these run as dcpa_paged_attn, every
+ * sequence by its own table row.  Else the parts of every row live in `workspace`, whose
+ * size dcpa_prefix_attn_workspace gives: about 512 (Dv + 1) bytes for each of
+ * Hkv (B + n_groups + R / S + R / 128 + 1024 / Hkv) units, R = T Hq / Hkv, S = 32 where
+ * rows are few, else 128 (256 sequences of one token, 64 / 8 heads of 128: 250 MB).  The
+ * weights are held as in dcpa_paged_attn: with what their rounding leaves where rows are
+ * few (those of a sequence, not of a group) or wide_weights is given, else rounded to
+ * `dtype`.  Up to 2^20 groups; the limit of 2^23 workgroups
  * counts the row tiles of sequences and of groups.
  */
 int dcpa_prefix_attn(const dcpa_attn_args* a, const int32_t* cu_group, const int32_t* shared_len, int64_t n_groups,

@@ -149,7 +149,7 @@ int check_attn(const dcpa_attn_args* a, Batch& m) {
 int check_prefix(const dcpa_attn_args* a, int64_t groups, Batch& m, AttnPlan& pl) {
     if (int st = check_shapes(a, m)) return st;
     if (groups < 0 || groups > (int64_t(1) << 20)) return DCP_ERR_SHAPE;
-    pl = plan_prefix(m, groups, (int)a->Dk, (int)a->Dv, cache_pieces(a));
+    pl = sharing_pays(m, groups) ? plan_prefix(m, groups, (int)a->Dk, (int)a->Dv, cache_pieces(a)) : plan_of(a, m);
     return grid_ok(a, pl, m) ? DCP_OK : DCP_ERR_SHAPE;
 }
 
@@ -430,6 +430,10 @@ int dcpa_prefix_attn(const dcpa_attn_args* a, const int32_t* cu_group, const int
     if (n_groups > 0 && (!cu_group || !shared_len)) return DCP_ERR_NULL;
     if (!aligned(cu_group, 4) || !aligned(shared_len, 4)) return DCP_ERR_ALIGN;
     if (int st = check_outputs(a)) return st;
+    if (!sharing_pays(k.m, n_groups)) {
+        if (int st = fill_attn(a, pl, k)) return st;
+        return run_attn(a, k, pl, stream);
+    }
     if (int st = fill_attn(a, pl, k, prefix_list_bytes(pl.units, n_groups + a->B))) return st;
     k.list = (PrefixUnit*)a->workspace;
     k.entries = (PrefixEntry*)(k.list + pl.units);

@@ -117,6 +117,13 @@ struct GroupArgs : AttnArgs {
 hipError_t launch_prefix_bf16(const GroupArgs& a, bool kv8, bool wide, hipStream_t stream);
 hipError_t launch_prefix_f16(const GroupArgs& a, bool kv8, bool wide, hipStream_t stream);
 int64_t prefix_list_bytes(int64_t units, int64_t entries);
+// Whether the keys that groups share are read for all their rows at once, or by each sequence for itself
+// (launch_attn()).  From whole tiles of rows to a sequence on (128 rows of a key head, on average) a tile that holds
+// rows of several sequences saves no matrix instruction, but every row's parts go through memory: 24 chunks to 2048
+// tokens behind 8192 keys (2048 here), 64 / 8 heads, took 5150 us and 2.0 GB of workspace, 2230 us and none by
+// themselves; 64 sequences of 16 tokens behind 8192 keys here 386 and 295 us, of 8 tokens 218 and 238.  (8-bit rows lose
+// up to a tenth so: 64 of 16 tokens 410 and 441 us, behind 1024 keys 157 and 85.)
+inline bool sharing_pays(const Batch& m, int64_t groups) { return groups > 0 && (int64_t)m.T * m.G < (int64_t)128 * m.B; }
 AttnPlan plan_prefix(const Batch& m, int64_t groups, int Dk, int Dv, bool pieces);
 hipError_t launch_prefix(const GroupArgs& a, bool latent, bool bf16, bool kv8, bool wide, hipStream_t stream);
 
