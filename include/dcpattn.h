@@ -190,7 +190,7 @@ int64_t dcpa_paged_attn_workspace(const dcpa_attn_args* a);
  * cu_group[g+1]-1; the first shared_len[g] cached keys of all of them are the
  * same (whole pages that stand in all their table rows), and are read through the
  * table row of the first of them whose kv_len is shared_len[g] or more (of the
- * first, if there is none).  shared_len[g] is clamped to [0, max_pages *
+ * longest, if there is none).  shared_len[g] is clamped to [0, max_pages *
  * page_size]; a sequence sees of the shared keys what it would see of its own (none
  * where its kv_len is 0).  Sequences outside the groups share nothing.
  * cu_group has to be non-decreasing (as cu_q, other contents give wrong numbers
@@ -204,8 +204,8 @@ int64_t dcpa_paged_attn_workspace(const dcpa_attn_args* a);
  * rows are few, else 128 (256 sequences of one token, 64 / 8 heads of 128: 250 MB).  The
  * weights are held as in dcpa_paged_attn: with what their rounding leaves where rows are
  * few (those of a sequence, not of a group) or wide_weights is given, else rounded to
- * `dtype`.  Up to 2^20 groups; the limit of 2^23 workgroups
- * counts the row tiles of sequences and of groups.
+ * `dtype`.  Up to 2^20 groups; the limit of 2^23 workgroups counts the row tiles of
+ * sequences and of groups.
  */
 int dcpa_prefix_attn(const dcpa_attn_args* a, const int32_t* cu_group, const int32_t* shared_len, int64_t n_groups,
                      void* stream);

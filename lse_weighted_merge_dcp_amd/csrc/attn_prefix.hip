@@ -238,14 +238,16 @@ __global__ __launch_bounds__(kThreads) void prefix_list(GroupArgs p) {
             // (a row of a sequence that shares no keys and was not split has one part: it is written whole)
             u.splits = y.begin > 0 ? max(s, 2) : s;
             if (e < p.groups) {
-                // the shared keys by the table row of the first sequence whose cache holds them all (padding may stand first)
-                u.b = u.b0 = y.b0;
+                // the shared keys by the table row of the first sequence whose cache holds them all (padding may stand
+                // first), of the longest where none does
+                u.b0 = y.b0;
                 u.b1 = y.b1;
-                for (int b = y.b0; b < y.b1; ++b) {
+                int most = -1;
+                for (int b = y.b0; b < y.b1 && most < y.keys; ++b) {
                     const int kv = held ? entry_s[p.groups + b].s.kv : min(max(p.m.kv[b], 0), p.m.max_keys);
-                    if (kv >= y.keys) {
+                    if (kv > most) {
+                        most = kv;
                         u.b = b;
-                        break;
                     }
                 }
                 u.splits = max(s, 2);
