@@ -364,7 +364,8 @@ int dcpa_project(const dcpa_project_args* a, void* stream);
  * Sums in fp32, each result rounded once to dtype.  k_rest and v_rest (both or
  * neither) get what that rounding left of the sums, rounded once more, so that
  * the two together hold a result to 2^-16 (bf16) or 2^-22 (fp16, or 2^-25) of itself: keys
- * and values for dcpa_pair_attn.  (The columns of the rope have none: with k_scale =
+ * and values for dcpa_pair_attn.  A result beyond the type's largest number is infinite,
+ * with a rest of 0.  (The columns of the rope have none: with k_scale =
  * 1 they are exact.)  kv_len is clamped to max_keys and to max_pages * page_size.  Rows behind kv_len, and keys whose page is
  * missing, are left as they were.
  *

@@ -181,6 +181,8 @@ template <typename E, int MT_, int NT_, int KT_, int WM, int WN, int ST, bool TU
         // (rows of 128 bytes: two of them share 256)
         auto place = [](int row, int c) { return (uint32_t)(row * OC * 16 + (c ^ (OC == 8 ? row >> 1 & 7 : row >> 2 & 3)) * 16); };
         static_assert(OC == 4 || OC == 8, "rows of one or two blocks");
+        // (a result that the type cannot hold is infinite and leaves nothing: their difference would make its row NaN)
+        auto left = [](float x, float rounded) { return __builtin_isinf(rounded) ? 0.0f : x - rounded; };
 #pragma unroll
         for (int j = 0; j < BM; ++j)
 #pragma unroll
@@ -200,7 +202,7 @@ template <typename E, int MT_, int NT_, int KT_, int WM, int WN, int ST, bool TU
                                 // then rounds it once, and round it twice for the rest)
                                 if constexpr (REST) asm("" : "+v"(x), "+v"(y));
                                 v[e][d] = Mat<E>::pack2(x, y);
-                                if (pass == 1) v[e][d] = Mat<E>::pack2(x - Mat<E>::low(v[e][d]), y - Mat<E>::high(v[e][d]));
+                                if (pass == 1) v[e][d] = Mat<E>::pack2(left(x, Mat<E>::low(v[e][d])), left(y, Mat<E>::high(v[e][d])));
                             }
                         // (the upper half-wave's part of the first group of four against the lower one's of the second)
                         const auto x = __builtin_amdgcn_permlane32_swap(v[0][0], v[1][0], false, false);
