@@ -211,6 +211,11 @@ def qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tens
     return q_out
 
 
+# The address of a value cache without pages, never followed (torch has none for it; NULL says that values lie within the
+# keys, which have other limits).
+_NO_PAGES = 16
+
+
 def _attn_args(q, k_cache, v_cache, block_table, cu_q, kv_len, seq_len, scale, Dv, rank, n_ranks, interleave, causal,
                k_scale, v_scale, base_e, wide, out, lse, ws, ws_bytes):
     """The packed dcpa_attn_args of an attention or weight call."""
@@ -237,7 +242,7 @@ def _attn_args(q, k_cache, v_cache, block_table, cu_q, kv_len, seq_len, scale, D
         scale = Dk ** -0.5
     return ATTN_ARGS.pack(
         q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), ks[0], ks[1], ks[2],
-        v_cache.data_ptr() if v_cache is not None else 0, vs[0], vs[1], vs[2],
+        (v_cache.data_ptr() or _NO_PAGES) if v_cache is not None else 0, vs[0], vs[1], vs[2],
         block_table.data_ptr(), block_table.stride(0), cu_q.data_ptr(), kv_len.data_ptr(),
         seq_len.data_ptr() if seq_len is not None else 0,
         out.data_ptr() if out is not None else 0, os_[0], os_[1],
