@@ -21,7 +21,7 @@ namespace dcpa {
 template <typename E, int MT_, int NT_, int KT_, int WM, int WN, int ST, bool TURNED, bool X8> struct Product {
     static constexpr int MT = MT_, NT = NT_, KT = KT_, THREADS = WM * WN * 64;
     static constexpr int BM = MT / WM / 32, BN = NT / WN / 32;
-    static constexpr int ROW = KT * 2, KC = KT / 8;                    // bytes and pieces of a row of KT columns
+    static constexpr int ROW = KT * 2, KC = KT / 8;                    // bytes and pieces of a row of KT columns (see swz())
     static constexpr int XB = MT * ROW, WB = NT * ROW;                 // bytes of a step
     static constexpr int NX = XB / 16 / THREADS, NW = WB / 16 / THREADS;
     static constexpr int WC = TURNED ? NT / 8 : KC;                    // 16-byte pieces of a row of weights in LDS
@@ -49,14 +49,9 @@ template <typename E, int MT_, int NT_, int KT_, int WM, int WN, int ST, bool TU
         xs = lds_addr(lds);
         ws = xs + ST * XB;
         os = ws + ST * WB + (uint32_t)(wave * OB);
-        xc = (tid % KC) ^ turn<KC>(tid / KC);
-        wc = (tid % WC) ^ turn<WC>(tid / WC);
+        xc = (tid % KC) ^ swz<KC>(tid / KC);
+        wc = (tid % WC) ^ swz<WC>(tid / WC);
         n_here = true;
-    }
-    // where a row's pieces lie (see swz(); rows of 64 bytes: four of them share 256 bytes)
-    template <int C> static __device__ __forceinline__ int turn(int r) {
-        if constexpr (C == 4) return r >> 2 & 3;
-        else return swz<C>(r);
     }
     // row of the tile that piece i of this thread belongs to (a row of k where the weights are turned)
     __device__ __forceinline__ int x_row(int i) const { return i * (THREADS / KC) + tid / KC; }
@@ -96,14 +91,14 @@ template <typename E, int MT_, int NT_, int KT_, int WM, int WN, int ST, bool TU
 #pragma unroll
         for (int st = 0; st < KT / 16; ++st) {
             u32x4 a[BN], b[BM];
-            const uint32_t at = (uint32_t)(r * ROW + ((2 * st + h) ^ turn<KC>(r)) * 16);
+            const uint32_t at = (uint32_t)(r * ROW + ((2 * st + h) ^ swz<KC>(r)) * 16);
 #pragma unroll
             for (int i = 0; i < BN; ++i) {
                 const int nb = wn * BN + i;                  // block of 32 columns
                 if constexpr (TURNED) {
                     const int k = st * 16 + 8 * h + li / 4, c = nb * 4 + 2 * g + (li & 3) / 2;
-                    const u32x2 lo = lds_read_tr(wb + (uint32_t)(k * NT * 2 + (c ^ turn<WC>(k)) * 16 + (li & 1) * 8));
-                    const u32x2 hi = lds_read_tr(wb + (uint32_t)((k + 4) * NT * 2 + (c ^ turn<WC>(k + 4)) * 16 + (li & 1) * 8));
+                    const u32x2 lo = lds_read_tr(wb + (uint32_t)(k * NT * 2 + (c ^ swz<WC>(k)) * 16 + (li & 1) * 8));
+                    const u32x2 hi = lds_read_tr(wb + (uint32_t)((k + 4) * NT * 2 + (c ^ swz<WC>(k + 4)) * 16 + (li & 1) * 8));
                     a[i] = u32x4{lo.x, lo.y, hi.x, hi.y};
                 } else {
                     a[i] = lds_read16(wb + (uint32_t)(nb * 32 * ROW) + at);
