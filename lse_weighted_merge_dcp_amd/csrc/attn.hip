@@ -5,6 +5,7 @@
 // attn_keys: up to 32 rows, the keys shared out over the waves (attn_keys.hpp).
 // attn_join: joins the key ranges of one row tile that went to different
 // workgroups.
+#include "attn_join.hpp"
 #include "attn_keys.hpp"
 #include "attn_rows.hpp"
 
@@ -38,7 +39,6 @@ __global__ __launch_bounds__(256, DK > 128 ? 1 : 2) void attn_keys(AttnArgs p) {
 // ---------------------------------------------------------------------------
 template <typename E, int STEP, int NC, bool TOGETHER>
 __global__ __launch_bounds__(256) void attn_join(AttnArgs p) {
-    constexpr int FLY = NC == 1 ? 8 : 4;       // parts under way at once
     __shared__ f32x4 share[TOGETHER ? 4 : 1][NC][64];
     const int lane = threadIdx.x & 63, wave = (int)dcp::wave_id();
     int longest;
@@ -87,72 +87,7 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs p) {
         const int kend = visible(p.m, s, (int)fdiv((uint32_t)last, p.m.fG));
         const int parts = min(max(1, (kend + chunk - 1) / chunk), p.units - slot);
         const int64_t first = ((int64_t)hk * p.units + slot) * p.rows + in_tile;
-        float top = -INFINITY;
-        bool bad = false;
-        for (int k = lane; k < parts; k += 64) {
-            const float y = p.ws_l[first + (int64_t)k * p.rows];
-            bad |= y != y;
-            top = fmaxf(top, y);
-        }
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-        const float ref = top == -INFINITY ? 0.0f : top;
-        float acc[NC * 4], sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NC * 4; ++i) acc[i] = 0.0f;
-#pragma unroll 1
-        for (int k0 = 0; k0 < parts; k0 += 64) {
-            // a lane to a part's weight
-            const int here = min(64, parts - k0);
-            const float f = lane < here ? exp2_fast(p.ws_l[first + (int64_t)(k0 + lane) * p.rows] - ref) : 0.0f;
-            sum += f;
-#pragma unroll 1
-            for (int k = TOGETHER ? wave * FLY : 0; k < here; k += TOGETHER ? 4 * FLY : FLY) {
-                f32x4 y[FLY][NC];
-#pragma unroll
-                for (int i = 0; i < FLY; ++i)
-#pragma unroll
-                    for (int j = 0; j < NC; ++j) {
-                        const int col = min(j * 256 + lane * 4, p.Dv - 4);
-                        y[i][j] = *(const f32x4*)(p.ws_o + (first + (int64_t)(k0 + min(k + i, here - 1)) * p.rows) * p.Dv + col);
-                    }
-#pragma unroll
-                for (int i = 0; i < FLY; ++i) {
-                    const float g = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), min(k + i, 63)));
-#pragma unroll
-                    for (int j = 0; j < NC; ++j)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[j * 4 + c] += k + i < here ? g * y[i][j][c] : 0.0f;
-                }
-            }
-        }
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 64);
-        if (__ballot(bad) != 0) sum = NAN;
-        if constexpr (TOGETHER) {
-#pragma unroll
-            for (int j = 0; j < NC; ++j) share[wave][j][lane] = f32x4{acc[j * 4], acc[j * 4 + 1], acc[j * 4 + 2], acc[j * 4 + 3]};
-            __syncthreads();
-            if (wave == 0)
-#pragma unroll
-                for (int j = 0; j < NC; ++j)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        acc[j * 4 + c] = share[0][j][lane][c] + share[1][j][lane][c] + share[2][j][lane][c] + share[3][j][lane][c];
-            __syncthreads();
-            if (wave != 0) continue;
-        }
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        char* o = p.out + (int64_t)t * p.o_T + (int64_t)(hk * p.m.G + head) * p.o_H;
-#pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            const int col = j * 256 + lane * 4;
-            if (col < p.Dv)
-                store4<E>(o + col * 2, acc[j * 4] * inv, acc[j * 4 + 1] * inv, acc[j * 4 + 2] * inv, acc[j * 4 + 3] * inv);
-        }
-        if (lane == 0 && p.lse != nullptr)
-            p.lse[(int64_t)t * p.l_T + (int64_t)(hk * p.m.G + head) * p.l_H] =
-                (sum == 0.0f ? -INFINITY : ref + __builtin_amdgcn_logf(sum)) * p.lmul;
+        join_parts<E, NC, TOGETHER>(p, share, t, hk * p.m.G + head, parts, [&](int k) { return first + (int64_t)k * p.rows; });
     }
 }
 

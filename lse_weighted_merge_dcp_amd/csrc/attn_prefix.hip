@@ -1,5 +1,6 @@
 // attn_prefix.hip -- attention behind shared prefixes (attn_prefix.hpp): the list of
 // units, the kernels of the latent layout, the join, and the calls' layout.
+#include "attn_join.hpp"
 #include "attn_latent.hpp"
 #include "attn_prefix.hpp"
 
@@ -275,7 +276,6 @@ template <typename E, bool KV8, bool EXACT, bool WIDE> __global__ __launch_bound
 // ---------------------------------------------------------------------------
 template <typename E, int NC, bool TOGETHER>
 __global__ __launch_bounds__(256) void prefix_join(GroupArgs p) {
-    constexpr int FLY = NC == 1 ? 8 : 4;       // parts under way at once
     __shared__ f32x4 share[TOGETHER ? 4 : 1][NC][64];
     const int lane = threadIdx.x & 63, wave = (int)dcp::wave_id();
     const int64_t all = (int64_t)p.m.T * p.m.G * p.m.Hkv;
@@ -330,72 +330,7 @@ __global__ __launch_bounds__(256) void prefix_join(GroupArgs p) {
         const int64_t first0 = ((int64_t)hk * p.units + slot[0]) * p.rows + in_tile[0];
         const int64_t first1 = ((int64_t)hk * p.units + slot[1]) * p.rows + in_tile[1];
         auto part = [&](int k) { return k < parts[0] ? first0 + (int64_t)k * p.rows : first1 + (int64_t)(k - parts[0]) * p.rows; };
-        float top = -INFINITY;
-        bool bad = false;
-        for (int k = lane; k < n; k += 64) {
-            const float y = p.ws_l[part(k)];
-            bad |= y != y;
-            top = fmaxf(top, y);
-        }
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-        const float ref = top == -INFINITY ? 0.0f : top;
-        float acc[NC * 4], sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NC * 4; ++i) acc[i] = 0.0f;
-#pragma unroll 1
-        for (int k0 = 0; k0 < n; k0 += 64) {
-            // a lane to a part's weight
-            const int here = min(64, n - k0);
-            const float f = lane < here ? exp2_fast(p.ws_l[part(k0 + lane)] - ref) : 0.0f;
-            sum += f;
-#pragma unroll 1
-            for (int k = TOGETHER ? wave * FLY : 0; k < here; k += TOGETHER ? 4 * FLY : FLY) {
-                f32x4 y[FLY][NC];
-#pragma unroll
-                for (int i = 0; i < FLY; ++i)
-#pragma unroll
-                    for (int j = 0; j < NC; ++j) {
-                        const int col = min(j * 256 + lane * 4, p.Dv - 4);
-                        y[i][j] = *(const f32x4*)(p.ws_o + part(k0 + min(k + i, here - 1)) * p.Dv + col);
-                    }
-#pragma unroll
-                for (int i = 0; i < FLY; ++i) {
-                    const float g = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), min(k + i, 63)));
-#pragma unroll
-                    for (int j = 0; j < NC; ++j)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[j * 4 + c] += k + i < here ? g * y[i][j][c] : 0.0f;
-                }
-            }
-        }
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 64);
-        if (__ballot(bad) != 0) sum = NAN;
-        if constexpr (TOGETHER) {
-#pragma unroll
-            for (int j = 0; j < NC; ++j) share[wave][j][lane] = f32x4{acc[j * 4], acc[j * 4 + 1], acc[j * 4 + 2], acc[j * 4 + 3]};
-            __syncthreads();
-            if (wave == 0)
-#pragma unroll
-                for (int j = 0; j < NC; ++j)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        acc[j * 4 + c] = share[0][j][lane][c] + share[1][j][lane][c] + share[2][j][lane][c] + share[3][j][lane][c];
-            __syncthreads();
-            if (wave != 0) continue;
-        }
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        char* o = p.out + (int64_t)t * p.o_T + (int64_t)(hk * p.m.G + head) * p.o_H;
-#pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            const int col = j * 256 + lane * 4;
-            if (col < p.Dv)
-                store4<E>(o + col * 2, acc[j * 4] * inv, acc[j * 4 + 1] * inv, acc[j * 4 + 2] * inv, acc[j * 4 + 3] * inv);
-        }
-        if (lane == 0 && p.lse != nullptr)
-            p.lse[(int64_t)t * p.l_T + (int64_t)(hk * p.m.G + head) * p.l_H] =
-                (sum == 0.0f ? -INFINITY : ref + __builtin_amdgcn_logf(sum)) * p.lmul;
+        join_parts<E, NC, TOGETHER>(p, share, t, hk * p.m.G + head, n, part);
     }
 }
 
