@@ -448,6 +448,8 @@ def _project(x, w, turned, N, K, copy, out, name):
     _rows(out, "out", 3)
     if out.shape != (T, H, N + copy) or out.dtype != x.dtype:
         raise ValueError("bad out tensor")
+    if out.numel() > 0 and out.data_ptr() in (x.data_ptr(), w.data_ptr()):
+        raise ValueError("%s: out must not lie over its inputs" % name)
     xs, ws, ys = x.stride(), w.stride(), out.stride()
     w_N, w_K = (ws[2], ws[1]) if turned else (ws[1], ws[2])
     args = PROJECT_ARGS.pack(x.data_ptr(), xs[0], xs[1], w.data_ptr(), ws[0], w_N, w_K, out.data_ptr(), ys[0], ys[1],
@@ -462,7 +464,7 @@ def latent_queries(q: torch.Tensor, w_uk: torch.Tensor, *, out: Optional[torch.T
     The result is what qk_norm_rope_append (rope_offset = Dc) and dcp_paged_attn
     take against latent rows.  w_uk may be a view of the whole projection
     [H,Dn+Dv,Dc], or of a transposed one (one of its last two dimensions
-    contiguous)."""
+    contiguous).  out must not lie over q or w_uk."""
     if w_uk.dim() != 3 or q.dim() != 3 or w_uk.shape[0] != q.shape[1] or q.shape[2] < w_uk.shape[1]:
         raise ValueError("expected q [T,H,Dn+Dr] and w_uk [H,Dn,Dc]")
     Dn, Dc = w_uk.shape[1], w_uk.shape[2]
@@ -472,7 +474,7 @@ def latent_queries(q: torch.Tensor, w_uk: torch.Tensor, *, out: Optional[torch.T
 def latent_values(o: torch.Tensor, w_uv: torch.Tensor, *, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Values [T,H,Dv] from (merged) latent outputs o [T,H,Dc]: o[t, h] @
     w_uv[h].T, with the value weights w_uv [H,Dv,Dc] of a latent layer (one of
-    the last two dimensions contiguous)."""
+    the last two dimensions contiguous).  out must not lie over o or w_uv."""
     if w_uv.dim() != 3 or o.dim() != 3 or w_uv.shape[0] != o.shape[1] or o.shape[2] != w_uv.shape[2]:
         raise ValueError("expected o [T,H,Dc] and w_uv [H,Dv,Dc]")
     return _project(o, w_uv, False, w_uv.shape[1], w_uv.shape[2], 0, out, "latent_values")
