@@ -7,7 +7,7 @@
 // 2^-16 (bf16) or 2^-22 (fp16), for 8 more matrix instructions beside 12 in the
 // scores of 128 + 64 columns and twice as many in the values.
 // Bound by matrix instructions, as rows_of().  A chunk of 3 ragged sequences to 1500
-// tokens over 4500 keys, 32 heads of 192 / 128 columns: 535 to 585 us; keys and
+// tokens over 4500 keys, 32 heads of 192 / 128 columns: 535 to 580 us; keys and
 // values rounded once 343, with results that are off by more than their own rounding.
 #include "attn_rows.hpp"
 

@@ -16,12 +16,15 @@ namespace {
 // with U units of which the longest takes c keys, `share` of them at once and a
 // price of kPrice keys to a unit (its start, and a part of 128 rows written and read
 // again), either all run at once and take c + kPrice, or their mean load and one
-// unit more.  (64 sequences behind 32768 keys on four ranks: 68 us a call in ranges of
-// 1024 keys, 75 of 704, 82 of 384.)
+// unit more.  (64 sequences behind 32768 keys on four ranks, with one product for the
+// shared keys' weights: 68 us a call in ranges of 1024 keys, 75 of 704, 82 of 384.)
 // Every workgroup finding its own unit from the lengths, as those of single
 // sequences do, took 112 us there, a dozen dependent loads in front of 8 key tiles;
-// this kernel takes 8.5 and the rest 60.  Most of that is waiting: for the lengths (two
+// this kernel took 8.5 and the rest 60.  Most of its time is waiting: for the lengths (two
 // loads one after the other) and for code that is run once.
+// More than kThreads entries do not stay in LDS and are loaded again for every length that
+// is tried: 1100 sequences of one token in 4 groups take 65 us a call, 2000 in 8 115, by
+// themselves 81 and 164.
 // ---------------------------------------------------------------------------
 constexpr int kThreads = 1024, kWaves = kThreads / 64, kTries = 32, kPrice = 1024;
 constexpr int kMost = 1 << 30;

@@ -3,17 +3,19 @@
 //
 // project_rows: y[t, h] = x[t, h] W[h], rows of tokens against one head's weights.
 // Bound by bytes: the weights' where tokens are few (64 tokens, 128 heads of 128 x
-// 512: 8 us for queries, 7.2 for values, of which the 27 MB take 4.5 and a launch the
+// 512: 9.2 us for queries, 7.5 for values, of which the 27 MB take 4.5 and a launch the
 // rest), the rows' where they are many (a weight of 128 x 512 makes 512 outputs of
 // 128 inputs: 205 operations a byte, and the matrix instructions do 220).  4096
-// tokens' queries take 229 us, 3.6 TB/s; without their stores 117, so stores and the
-// rest still come one after the other; 2001 tokens' values of 96 heads 43 us, 6.0 TB/s.
+// tokens' queries take 223 us, 3.7 TB/s; without their stores 117, so stores and the
+// rest still come one after the other; 2001 tokens' values of 96 heads 55 us, 4.7 TB/s
+// (42 over the same rows again and again: the Infinity Cache holds part of them).
 // expand_rows: cached rows against the weights of all heads side by side.  Bound by
-// the LDS: a step of 256 x 256 x 64 takes 2048 clocks of matrix instructions, and as
-// many of LDS accesses for the fragments (1536) and the next operands (512).  16384
-// rows, 128 heads of 128 + 64 / 128 columns: 720 us, 0.76 PFLOP/s (390 us without loads
-// and stores, 515 without stores; tiles of 128 x 256 by two workgroups to a CU 860 us,
-// steps of 32 columns 827, one workgroup to a tile 814).
+// products and stores, which come one after the other as the waves of a CU's one
+// workgroup go in step.  In the products a step of 256 x 256 x 64 takes 2048 clocks of
+// matrix instructions, and as many of LDS accesses for the fragments (1536) and the next
+// operands (512).  16384 rows, 128 heads of 128 + 64 / 128 columns: 731 to 746 us, 0.74
+// PFLOP/s (390 us without loads and stores, 515 without stores; tiles of 128 x 256 by two
+// workgroups to a CU 860 us, steps of 32 columns 827, one workgroup to a tile 814).
 #include "attn_product.hpp"
 
 namespace dcpa {
@@ -249,7 +251,9 @@ int64_t share_of(int64_t all, int64_t slots) {
     return best;
 }
 
-// Results of an eighth of the Infinity Cache and more go out with the nontemporal hint.
+// Results of an eighth of the Infinity Cache and more go out with the nontemporal hint.  In the expansion the size is
+// that of the buffers (without the rests), since the host knows no lengths: a few keys in large ones take as long with
+// the hint as without (300 keys of 128 heads 30 and 34 us, attention over them 66 and 69).
 bool far_out(int64_t bytes) { return bytes >= (int64_t(1) << 25); }
 
 // Tiles of 64 x 64 for few tokens, and where those of 128 x 128 leave half the chip without one; larger ones read
