@@ -112,7 +112,7 @@ __device__ __forceinline__ Entry load_entry(const GroupArgs& p, int v, bool rows
 __global__ __launch_bounds__(kThreads) void prefix_list(GroupArgs p) {
     __shared__ float work_s[kWaves], units_s[kTries];
     __shared__ Entry entry_s[kThreads];
-    __shared__ int ends_s[kThreads], odd_s[kThreads], splits_s[kThreads], length_s[kTries];
+    __shared__ int ends_s[kThreads], odd_s[kThreads], splits_s[kThreads], owner_s[kThreads], length_s[kTries];
     __shared__ int scan_s[2][kWaves], longest_s[kWaves], chunk_s;
     const int tid = threadIdx.x, lane = tid & 63, wave = (int)dcp::wave_id(), all = p.groups + p.m.B;
     // work and the longest entry; the first 1024 entries stay in LDS
@@ -199,6 +199,25 @@ __global__ __launch_bounds__(kThreads) void prefix_list(GroupArgs p) {
             entry_s[tid] = x;
         }
         const int v = v0 + tid, splits = ranges_of(x.keys, chunk, 1.0f / (float)chunk);
+        // The shared keys are read by the table row of the first sequence of the group whose cache holds them all, of
+        // the longest where none does: mostly the first one; else (padding may stand first) the wave looks for it, 64
+        // sequences at a time.
+        auto cached = [&](int b) { return held ? entry_s[p.groups + b].s.kv : min(max(p.m.kv[b], 0), p.m.max_keys); };
+        int owner = x.b0;
+        for (uint64_t todo = __ballot(x.b1 > x.b0 && x.tiles > 0 && cached(x.b0) < x.keys); todo != 0; todo &= todo - 1) {
+            const int at = __builtin_ctzll(todo), keys = __builtin_amdgcn_readlane(x.keys, at);
+            const int b0 = __builtin_amdgcn_readlane(x.b0, at), b1 = __builtin_amdgcn_readlane(x.b1, at);
+            int found = b0, most = -1;
+            for (int b = b0; b < b1 && most < keys; b += 64) {
+                const int kv = b + lane < b1 ? min(cached(b + lane), keys) : -1, top = fold_wave(kv, -1, most_of);
+                if (top > most) {
+                    most = top;
+                    found = b + __builtin_ctzll(__ballot(kv == top));
+                }
+            }
+            if (lane == at) owner = found;
+        }
+        owner_s[tid] = owner;
         // units and sequences that see less than is shared, counted up to each entry
         // (lengths that contradict each other may add up to anything: no sum passes kMost)
         const int mine = (int)min((int64_t)x.tiles * splits, (int64_t)kMost);
@@ -242,18 +261,9 @@ __global__ __launch_bounds__(kThreads) void prefix_list(GroupArgs p) {
             // (a row of a sequence that shares no keys and was not split has one part: it is written whole)
             u.splits = y.begin > 0 ? max(s, 2) : s;
             if (e < p.groups) {
-                // the shared keys by the table row of the first sequence whose cache holds them all (padding may stand
-                // first), of the longest where none does
+                u.b = owner_s[lo];
                 u.b0 = y.b0;
                 u.b1 = y.b1;
-                int most = -1;
-                for (int b = y.b0; b < y.b1 && most < y.keys; ++b) {
-                    const int kv = held ? entry_s[p.groups + b].s.kv : min(max(p.m.kv[b], 0), p.m.max_keys);
-                    if (kv > most) {
-                        most = kv;
-                        u.b = b;
-                    }
-                }
                 u.splits = max(s, 2);
                 // (where the list is longer than the workgroup every row finds its sequence)
                 u.even = all <= kThreads && odd_s[p.groups + y.b1 - 1] == odd_s[p.groups + y.b0 - 1];
