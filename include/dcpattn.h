@@ -222,7 +222,8 @@ int64_t dcpa_prefix_attn_workspace(const dcpa_attn_args* a, int64_t n_groups);
  * most 32 to a sequence on average) or wide_weights is given (in the product with the
  * values' first part, not their second).  cache_dtype is dtype, v not NULL, Dk and
  * Dv at most 256, Dr a multiple of 8 up to Dk; the rests' strides are multiples of 8,
- * 16-byte aligned.  A query that is not finite gives NaN.  The workspace query is dcpa_pair_attn_workspace.
+ * 16-byte aligned.  A query that is not finite gives NaN.  The workspace query is
+ * dcpa_pair_attn_workspace.
  */
 int dcpa_pair_attn(const dcpa_attn_args* a, const void* k_rest, int64_t kr_P, int64_t kr_S, int64_t kr_H, int64_t Dr,
                    const void* v_rest, int64_t vr_P, int64_t vr_S, int64_t vr_H, void* stream);
@@ -365,9 +366,9 @@ int dcpa_project(const dcpa_project_args* a, void* stream);
  * neither) get what that rounding left of the sums, rounded once more, so that
  * the two together hold a result to 2^-16 (bf16) or 2^-22 (fp16, or 2^-25) of itself: keys
  * and values for dcpa_pair_attn.  A result beyond the type's largest number is infinite,
- * with a rest of 0.  (The columns of the rope have none: with k_scale =
- * 1 they are exact.)  kv_len is clamped to max_keys and to max_pages * page_size.  Rows behind kv_len, and keys whose page is
- * missing, are left as they were.
+ * with a rest of 0.  (The columns of the rope have none: with k_scale = 1 they are
+ * exact.)  kv_len is clamped to max_keys and to max_pages * page_size.  Rows behind
+ * kv_len, and keys whose page is missing, are left as they were.
  *
  * places [B, max_keys] (nullable) gets b * max_keys + j for every such key, -1
  * where its page is missing: the block_table with which dcpa_paged_attn reads k and

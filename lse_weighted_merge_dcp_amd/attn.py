@@ -341,8 +341,9 @@ def dcp_prefix_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional[to
     (int32 [groups]) cached keys of each of them on this rank are the same: whole
     pages that stand in all their rows of block_table.  Sequences outside the
     groups share nothing.  For one or a few new tokens to a sequence; prompt chunks
-    (128 rows of a key head and more to a sequence) run as in dcp_paged_attn.  Returns (out [T,Hq,Dv], lse [T,Hq] fp32).  Weights are
-    rounded or not as in dcp_paged_attn (wide_weights)."""
+    (128 rows of a key head and more to a sequence) run as in dcp_paged_attn.  Returns
+    (out [T,Hq,Dv], lse [T,Hq] fp32).  Weights are rounded or not as in dcp_paged_attn
+    (wide_weights)."""
     dev = _on_gpu(q, k_cache, v_cache, block_table, cu_q, kv_len, seq_len, cu_group, shared_len, out, out_lse, workspace)
     Dv, out, out_lse = _attn_outputs(q, k_cache, v_cache, v_dim, out, out_lse)
     groups = shared_len.shape[0] if shared_len.dim() == 1 else -1
