@@ -13,7 +13,7 @@
 // The shared keys are bound by matrix instructions as soon as a group has more than
 // some 64 rows of a key head, the sequences' own keys by their bytes, so the two fill
 // each other's gaps.  64 sequences behind 32768 keys (8192 on this rank), 64 / 8 heads
-// of 128: 73 to 77 us, 56 of them the units (floor 24: 148 MB), the rest the list and
+// of 128: 73 to 78 us, 56 of them the units (floor 24: 148 MB), the rest the list and
 // the join; 215 where each sequence reads all of its keys.  Few shared keys do not pay
 // for the list: 4 sequences behind 1000 (250 here) take 22 us, by themselves 16; nor do
 // sequences of many rows for their parts (sharing_pays()).

@@ -13,7 +13,7 @@
 // products and stores, which come one after the other as the waves of a CU's one
 // workgroup go in step.  In the products a step of 256 x 256 x 64 takes 2048 clocks of
 // matrix instructions, and as many of LDS accesses for the fragments (1536) and the next
-// operands (512).  16384 rows, 128 heads of 128 + 64 / 128 columns: 731 to 746 us, 0.74
+// operands (512).  16384 rows, 128 heads of 128 + 64 / 128 columns: 731 to 755 us, 0.74
 // PFLOP/s (390 us without loads and stores, 515 without stores; tiles of 128 x 256 by two
 // workgroups to a CU 860 us, steps of 32 columns 827, one workgroup to a tile 814).
 #include "attn_product.hpp"
